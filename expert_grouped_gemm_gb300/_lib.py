@@ -28,11 +28,15 @@ MOE_BF16 = 0
 MOE_F32 = 1
 MOE_FROZEN = 1
 MOE_RECOMPUTE = 2
+MOE_NORM_KINDS = {"layer": 0, "rms": 1}
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 EXPORTED = ["moe_workspace_size", "moe_fwd", "moe_select_retained", "moe_bwd", "moe_read_status",
             "moe_last_error", "moe_workspace_entry", "moe_kernel_launches", "moe_timing_enable",
             "moe_timing_read", "moe_route_noalloc", "moe_plan_quota", "moe_selftest_wait", "moe_fwd_decode",
-            "moe_selftest_decode_wait"]
+            "moe_selftest_decode_wait", "moe_norm_workspace_size", "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd",
+            "moe_gate_bwd", "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd"]
 
 
 class MoeError(RuntimeError):
@@ -45,6 +49,23 @@ class Dims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("F", ctypes.c_int64), ("E", ctypes.c_int64),
                 ("k", ctypes.c_int64), ("F_shared", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class GateDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("n_group", ctypes.c_int64),
+                ("topk_group", ctypes.c_int64), ("group_take", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("out_f32", ctypes.c_int32)]
 
 
 _lib = None
@@ -81,6 +102,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moe_kernel_launches.restype = ctypes.c_int64
     lib.moe_timing_enable.argtypes = [ctypes.c_int]
     lib.moe_timing_read.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
+    ND, GD, LD = ctypes.POINTER(NormDims), ctypes.POINTER(GateDims), ctypes.POINTER(LinearDims)
+    sz = ctypes.c_size_t
+    lib.moe_norm_workspace_size.argtypes = [ND, ctypes.POINTER(sz)]
+    lib.moe_norm_fwd.argtypes = [ND] + [vp] * 9
+    lib.moe_norm_bwd.argtypes = [ND, vp, sz] + [vp] * 10
+    lib.moe_gate_fwd.argtypes = [GD] + [vp] * 6
+    lib.moe_gate_bwd.argtypes = [GD] + [vp] * 5
+    lib.moe_linear_workspace_size.argtypes = [LD, ctypes.POINTER(sz)]
+    lib.moe_linear_fwd.argtypes = [LD, vp, sz] + [vp] * 7
+    lib.moe_linear_bwd.argtypes = [LD, vp, sz] + [vp] * 8
+    for name in ["moe_norm_workspace_size", "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd",
+                 "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd"]:
+        getattr(lib, name).restype = ctypes.c_int
     for name in ["moe_workspace_size", "moe_fwd", "moe_fwd_decode", "moe_selftest_decode_wait", "moe_select_retained",
                  "moe_bwd", "moe_read_status",
                  "moe_workspace_entry", "moe_timing_enable", "moe_timing_read"]:
@@ -226,6 +260,133 @@ def moe_selftest_wait(arrive: bool, limit_us: int, device_status, stream=None):
     rc = load().moe_selftest_wait(_stream(stream), 1 if arrive else 0, int(limit_us),
                                   _ptr(device_status, "device_status", torch.int32))
     _check(rc)
+
+
+# ---------------------------------------------------------------- around the experts
+def _dt(dtype) -> int:
+    if dtype not in ("bf16", "f32"):
+        raise ValueError(f"dtype must be 'bf16' or 'f32', got {dtype!r}")
+    return MOE_BF16 if dtype == "bf16" else MOE_F32
+
+
+def _named(table: dict, value, what: str) -> int:
+    if value not in table:
+        raise ValueError(f"{what} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _tensor(t, name, dtype, shape, required=True):
+    """The pointer of a contiguous CUDA tensor of this dtype and shape (None stays None when not required)."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def make_norm_dims(T, H, dtype="bf16", kind="layer", eps=1e-5) -> NormDims:
+    return NormDims(T, H, _dt(dtype), _named(MOE_NORM_KINDS, kind, "kind"), eps)
+
+
+def alloc_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_norm_workspace_size(ctypes.byref(dims), ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def moe_norm_fwd(dims: NormDims, x, residual, weight, bias, y, sum=None, mean=None, rstd=None, stream=None):
+    """y = norm(x + residual) * weight + bias; sum receives x + residual, mean and rstd the statistics."""
+    io, f32 = _io_dtype(dims), torch.float32
+    th, h, t = (dims.T, dims.H), (dims.H,), (dims.T,)
+    args = (
+        _tensor(x, "x", io, th), _tensor(residual, "residual", io, th, False),
+        _tensor(weight, "weight", io, h), _tensor(bias, "bias", io, h, False), _tensor(y, "y", io, th),
+        _tensor(sum, "sum", io, th, False), _tensor(mean, "mean", f32, t, False), _tensor(rstd, "rstd", f32, t, False))
+    _check(load().moe_norm_fwd(dims, _stream(stream), *args))
+
+
+def moe_norm_bwd(dims: NormDims, ws, dy, dsum, x, weight, mean, rstd, dx, dweight, dbias=None, stream=None):
+    """Gradients of moe_norm_fwd; x is the tensor that was normalised, dsum what reaches it past the norm."""
+    io, f32 = _io_dtype(dims), torch.float32
+    th, h, t = (dims.T, dims.H), (dims.H,), (dims.T,)
+    _check(load().moe_norm_bwd(
+        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, th),
+        _tensor(dsum, "dsum", io, th, False), _tensor(x, "x", io, th), _tensor(weight, "weight", io, h),
+        _tensor(mean, "mean", f32, t, False), _tensor(rstd, "rstd", f32, t), _tensor(dx, "dx", io, th),
+        _tensor(dweight, "dweight", io, h), _tensor(dbias, "dbias", io, h, False)))
+
+
+def make_gate_dims(T, E, k, score="softmax", renorm=True, scale=1.0, n_group=1, topk_group=1, group_take=1,
+                   dtype="f32", grad_dtype="f32") -> GateDims:
+    return GateDims(T, E, k, n_group, topk_group, group_take, _named(MOE_SCORES, score, "score"), 1 if renorm else 0,
+                    _dt(dtype), _dt(grad_dtype), scale)
+
+
+def moe_gate_fwd(dims: GateDims, logits, bias, topk_idx, topk_w, expert_count=None, stream=None):
+    """Experts and weights of every token from its router logits; bias takes part in the selection only."""
+    tk = (dims.T, dims.k)
+    args = (
+        _tensor(logits, "logits", _io_dtype(dims), (dims.T, dims.E)),
+        _tensor(bias, "bias", torch.float32, (dims.E,), False), _tensor(topk_idx, "topk_idx", torch.int32, tk),
+        _tensor(topk_w, "topk_w", torch.float32, tk),
+        _tensor(expert_count, "expert_count", torch.int32, (dims.E,), False))
+    _check(load().moe_gate_fwd(dims, _stream(stream), *args))
+
+
+def moe_gate_bwd(dims: GateDims, logits, topk_idx, dtopk_w, dlogits, stream=None):
+    """Gradient of the weights of moe_gate_fwd to the logits, the selection held fixed."""
+    tk, te = (dims.T, dims.k), (dims.T, dims.E)
+    grad = torch.bfloat16 if dims.grad_dtype == MOE_BF16 else torch.float32
+    args = (
+        _tensor(logits, "logits", _io_dtype(dims), te),
+        _tensor(topk_idx, "topk_idx", torch.int32, tk), _tensor(dtopk_w, "dtopk_w", torch.float32, tk),
+        _tensor(dlogits, "dlogits", grad, te))
+    _check(load().moe_gate_bwd(dims, _stream(stream), *args))
+
+
+def make_linear_dims(M, K, N, dtype="bf16", act="none", out_f32=False) -> LinearDims:
+    return LinearDims(M, K, N, _dt(dtype), _named(MOE_ACTS, act, "act"), 1 if out_f32 else 0)
+
+
+def alloc_linear_workspace(dims: LinearDims, device="cuda") -> torch.Tensor:
+    """A workspace of moe_linear_workspace_size bytes, its first 4096 bytes zero as the library wants them."""
+    n = ctypes.c_size_t(0)
+    _check(load().moe_linear_workspace_size(ctypes.byref(dims), ctypes.byref(n)))
+    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+    ws[:4096].zero_()
+    return ws
+
+
+def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stream=None):
+    """y = act(x w + bias) + residual; pre receives x w + bias."""
+    io = _io_dtype(dims)
+    mn = (dims.M, dims.N)
+    _check(load().moe_linear_fwd(
+        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(x, "x", io, (dims.M, dims.K)),
+        _tensor(w, "w", io, (dims.K, dims.N)), _tensor(bias, "bias", io, (dims.N,), False),
+        _tensor(residual, "residual", io, mn, False), _tensor(y, "y", torch.float32 if dims.out_f32 else io, mn),
+        _tensor(pre, "pre", io, mn, False)))
+
+
+def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=None, stream=None):
+    """Gradients of moe_linear_fwd; pre is needed when the activation is not 'none'."""
+    io = _io_dtype(dims)
+    mn, mk, kn = (dims.M, dims.N), (dims.M, dims.K), (dims.K, dims.N)
+    _check(load().moe_linear_bwd(
+        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, mn),
+        _tensor(x, "x", io, mk), _tensor(w, "w", io, kn), _tensor(pre, "pre", io, mn, False),
+        _tensor(dx, "dx", io, mk, False), _tensor(dw, "dw", io, kn, False),
+        _tensor(dbias, "dbias", io, (dims.N,), False)))
 
 
 def moe_read_status(ws: torch.Tensor, stream=None) -> int:

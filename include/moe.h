@@ -252,6 +252,152 @@ MOE_API int moe_route_noalloc(const moe_dims* dims, void* stream, const void* x,
 MOE_API int moe_plan_quota(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, int64_t rho_num,
                            int64_t rho_den, const int32_t* budget, int32_t* quota);
 
+/* ------------------------------------------------------------------------
+ * Around the experts: the norm, linear and gate operators of the transformer
+ * layer the MoE block sits in, each forward and backward, and the block's
+ * forward and backward on a caller's routing. The conventions above hold for
+ * them too (device pointers to contiguous row-major buffers, 16-byte aligned
+ * tensors, work only enqueued on `stream`, MOE_OK or a negative moe_status).
+ * The pages this library follows describe the experts only; these operators
+ * are the usual ones of such layers and have no counterpart there.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+
+typedef struct moe_norm_dims {
+  int64_t T;      /* rows (tokens), >= 1 */
+  int64_t H;      /* row length, 1 <= H <= 65536; any value */
+  int32_t dtype;  /* moe_dtype of x, residual, weight, bias, y, sum and every gradient */
+  int32_t kind;   /* moe_norm_kind */
+  float eps;      /* added to the variance (mean square); finite, >= 0 */
+} moe_norm_dims;
+
+/* moe_norm_workspace_size -- bytes of workspace moe_norm_bwd needs (the forward needs
+ * none). Host-only; validates dims. */
+MOE_API int moe_norm_workspace_size(const moe_norm_dims* dims, size_t* bytes);
+
+/*
+ * moe_norm_fwd -- layer norm or RMS norm of each row, a residual added on the way:
+ *   h = x + residual;  mean = sum_i h_i / H (0 for MOE_NORM_RMS);
+ *   rstd = 1 / sqrt(sum_i (h_i - mean)^2 / H + eps);
+ *   y_i = (h_i - mean) rstd weight_i + bias_i.
+ * h, the statistics and y are computed in fp32; sum and y are rounded once when stored
+ * (the statistics are those of the unrounded h).
+ * Inputs:  x[T,H], residual[T,H] (nullable = 0), weight[H], bias[H] (nullable = 0).
+ * Outputs: y[T,H]; sum[T,H] = h (nullable; needs residual); mean[T], rstd[T] float
+ *          (nullable; mean must be null for MOE_NORM_RMS).
+ * y or sum may be the buffer of x or residual (in place); y and sum must differ.
+ */
+MOE_API int moe_norm_fwd(const moe_norm_dims* dims, void* stream, const void* x, const void* residual,
+                         const void* weight, const void* bias, void* y, void* sum, float* mean, float* rstd);
+
+/*
+ * moe_norm_bwd -- gradients of moe_norm_fwd. With xh = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - mean_i(g) - xh mean_i(g xh)) + dsum   (mean_i(g) term: layer norm only)
+ *   dweight_i = sum_t dy xh,  dbias_i = sum_t dy.
+ * dx is the gradient of both x and residual of the forward.
+ * Inputs:  dy[T,H], dsum[T,H] (nullable: the gradient that reaches `sum` past the norm),
+ *          x[T,H] (what was normalised: the forward's `sum`, or its x without a residual),
+ *          weight[H], mean[T] (null for MOE_NORM_RMS), rstd[T] float.
+ * Outputs: dx[T,H] (may be the buffer of dy or dsum), dweight[H], dbias[H] (nullable);
+ *          the weight gradients are overwritten and summed in a fixed order.
+ */
+MOE_API int moe_norm_bwd(const moe_norm_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy,
+                         const void* dsum, const void* x, const void* weight, const float* mean, const float* rstd,
+                         void* dx, void* dweight, void* dbias);
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct moe_gate_dims {
+  int64_t T;           /* tokens, >= 1 */
+  int64_t E;           /* experts, <= 1024 */
+  int64_t k;           /* experts per token, 1 <= k <= min(32, topk_group * E / n_group) */
+  int64_t n_group;     /* groups of E / n_group consecutive experts; divides E, <= 32; 1 = no groups */
+  int64_t topk_group;  /* groups a token may use, 1 <= topk_group <= n_group */
+  int32_t group_take;  /* a group's score is the sum of its 1 or 2 largest choice scores */
+  int32_t score;       /* moe_score */
+  int32_t renorm;      /* nonzero: the k weights are divided by their sum */
+  int32_t dtype;       /* moe_dtype of logits */
+  int32_t grad_dtype;  /* moe_dtype of dlogits */
+  float scale;         /* factor on the weights (finite) */
+} moe_gate_dims;
+
+/*
+ * moe_gate_fwd -- routing from router logits: which experts a token uses and how much.
+ *   s = softmax(logits_t) or sigmoid(logits_t);  c = s + bias (choice scores: the balance
+ *   bias takes part in the selection only); the topk_group groups with the largest group
+ *   scores stay; the k experts with the largest c among them, in descending order of c,
+ *   ties to the lower group and expert; topk_w = scale * s / (renorm ? sum of the k s : 1).
+ * A logit of -inf (or NaN) masks its expert: s = 0, and it is chosen only where fewer than
+ * k experts are left, after every unmasked one of the kept groups; a group without an
+ * unmasked expert is kept last, and group scores sum unmasked experts only. When all k
+ * chosen s are zero the weights are zero. A +inf logit is the limit: softmax shares 1 among
+ * the +inf logits.
+ * Scores are fp32. Inputs: logits[T,E] (dims.dtype), bias[E] float (nullable).
+ * Outputs: topk_idx[T,k] int32, topk_w[T,k] float, expert_count[E] int32 (nullable: tokens
+ * that chose each expert, what a balance-bias update reads).
+ */
+MOE_API int moe_gate_fwd(const moe_gate_dims* dims, void* stream, const void* logits, const float* bias,
+                         int32_t* topk_idx, float* topk_w, int32_t* expert_count);
+
+/*
+ * moe_gate_bwd -- gradient of topk_w to the logits, the selection held fixed. With the k
+ * chosen scores s_j, S their sum and dw the gradient of topk_w:
+ *   ds_j = scale (dw_j - sum_i dw_i s_i / S) / S   with renorm, else scale dw_j;
+ *   softmax: dlogits_e = s_e (ds_e - sum_j ds_j s_j);  sigmoid: dlogits_e = ds_e s_e (1 - s_e)
+ *   with ds_e = 0 for experts that were not chosen. Masked logits get 0.
+ * Inputs:  logits[T,E] as in the forward, topk_idx[T,k] (an index outside [0, E) is skipped),
+ *          dtopk_w[T,k] float. Output: dlogits[T,E] (dims.grad_dtype), every element written.
+ */
+MOE_API int moe_gate_bwd(const moe_gate_dims* dims, void* stream, const void* logits, const int32_t* topk_idx,
+                         const float* dtopk_w, void* dlogits);
+
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,      /* z Phi(z) */
+  MOE_ACT_GELU_TANH = 3, /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4       /* z sigmoid(z) */
+} moe_act;
+
+typedef struct moe_linear_dims {
+  int64_t M;        /* rows (tokens), 1 <= M < 2^31 */
+  int64_t K;        /* input features, 1 <= K < 2^24; any value */
+  int64_t N;        /* output features, 1 <= N < 2^24; any value */
+  int32_t dtype;    /* moe_dtype of x, w, bias, residual, pre and every gradient */
+  int32_t act;      /* moe_act */
+  int32_t out_f32;  /* nonzero: y is float whatever dtype is (router logits) */
+} moe_linear_dims;
+
+/*
+ * moe_linear_workspace_size -- bytes of workspace of moe_linear_fwd and moe_linear_bwd for
+ * these dims (256-byte aligned). The caller sets its first 4096 bytes to zero once, when it
+ * allocates the workspace; they hold the status word (moe_read_status) and counters that
+ * every call leaves at zero. Host-only; validates dims.
+ */
+MOE_API int moe_linear_workspace_size(const moe_linear_dims* dims, size_t* bytes);
+
+/*
+ * moe_linear_fwd -- matrix product with bias, activation and residual in its epilogue:
+ *   z = x w + bias;  y = act(z) + residual.   (fp32 accumulation, each output rounded once)
+ * Inputs:  x[M,K], w[K,N], bias[N] (nullable), residual[M,N] (nullable).
+ * Outputs: y[M,N] (dims.dtype, or float with out_f32; may be the buffer of residual when
+ *          both have one type); pre[M,N] = z (nullable; what the backward needs when act is
+ *          not MOE_ACT_NONE).
+ */
+MOE_API int moe_linear_fwd(const moe_linear_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x,
+                           const void* w, const void* bias, const void* residual, void* y, void* pre);
+
+/*
+ * moe_linear_bwd -- gradients of moe_linear_fwd (the residual's is dy itself):
+ *   dz = dy act'(pre);  dx = dz w^T;  dw = x^T dz;  dbias_n = sum_m dz.
+ * In bf16 dz is rounded to bf16 for the two products; dbias sums the unrounded dz.
+ * Inputs:  dy[M,N] (dims.dtype), x[M,K], w[K,N], pre[M,N] (null when act is MOE_ACT_NONE).
+ * Outputs: dx[M,K], dw[K,N], dbias[N], each nullable; overwritten, summed in a fixed order.
+ */
+MOE_API int moe_linear_bwd(const moe_linear_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy,
+                           const void* x, const void* w, const void* pre, void* dx, void* dw, void* dbias);
+
 /*
  * moe_selftest_wait -- checks, on the GPU, the bounded barrier wait that every
  * pipelined kernel of the library uses. A one-thread kernel waits on an
