@@ -6,6 +6,7 @@
 #include "act.cuh"
 #include "block.h"
 #include "common.cuh"
+#include "linear_tc.h"
 
 namespace moe {
 namespace {
@@ -133,16 +134,25 @@ cudaError_t run_simt(const SimtGemm& g, cudaStream_t st, int* launches) {
   return cudaSuccess;
 }
 
+// The tensor-core kernel needs bf16 rows of a multiple of 16 bytes.
+bool tc_shape(const moe_linear_dims& d) { return d.dtype == MOE_BF16 && d.K % 8 == 0 && d.N % 8 == 0; }
+
 template <typename T>
-cudaError_t fwd(const moe_linear_dims& d, const void* x, const void* w, const void* bias, const void* residual,
-                void* y, void* pre, cudaStream_t st, int* launches) {
+cudaError_t fwd(const moe_linear_dims& d, void* ws, const void* x, const void* w, const void* bias,
+                const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
+  if (tc_shape(d)) {
+    LinearGemm g = {(int)d.M, (int)d.N, (int)d.K, x, w, d.K, d.N, 0, 1, bias, residual, y, pre, d.act, d.out_f32,
+                    static_cast<int*>(ws)};
+    *launches += 1;
+    return launch_linear_tc(g, sms, st);
+  }
   SimtGemm g = {x, w, d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, bias, residual, y, pre, d.act, d.out_f32};
   return run_simt<T>(g, st, launches);
 }
 
 template <typename T>
 cudaError_t bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w, const void* pre,
-                void* dx, void* dw, void* dbias, cudaStream_t st, int* launches) {
+                void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
   const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
   const bool has_act = d.act != MOE_ACT_NONE;
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + kLinearHeader);
@@ -160,6 +170,20 @@ cudaError_t bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* 
     }
   }
   cudaError_t e = cudaSuccess;
+  if (tc_shape(d)) {
+    int* status = static_cast<int*>(ws);
+    if (dx) {
+      LinearGemm g = {M, K, N, dz, w, N, N, 0, 0, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0, status};
+      *launches += 1;
+      if ((e = launch_linear_tc(g, sms, st)) != cudaSuccess) return e;
+    }
+    if (dw) {
+      LinearGemm g = {K, N, M, x, dz, K, N, 1, 1, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0, status};
+      *launches += 1;
+      e = launch_linear_tc(g, sms, st);
+    }
+    return e;
+  }
   if (dx) {
     SimtGemm g = {dz, w, N, 1, 1, N, M, N, K, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0};
     if ((e = run_simt<T>(g, st, launches)) != cudaSuccess) return e;
@@ -181,15 +205,15 @@ size_t linear_workspace_bytes(const moe_linear_dims& d) {
 
 cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x, const void* w, const void* bias,
                               const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
-  return d.dtype == MOE_BF16 ? fwd<__nv_bfloat16>(d, x, w, bias, residual, y, pre, st, launches)
-                             : fwd<float>(d, x, w, bias, residual, y, pre, st, launches);
+  return d.dtype == MOE_BF16 ? fwd<__nv_bfloat16>(d, ws, x, w, bias, residual, y, pre, sms, st, launches)
+                             : fwd<float>(d, ws, x, w, bias, residual, y, pre, sms, st, launches);
 }
 
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,
                               const void* pre, void* dx, void* dw, void* dbias, int sms, cudaStream_t st,
                               int* launches) {
-  return d.dtype == MOE_BF16 ? bwd<__nv_bfloat16>(d, ws, dy, x, w, pre, dx, dw, dbias, st, launches)
-                             : bwd<float>(d, ws, dy, x, w, pre, dx, dw, dbias, st, launches);
+  return d.dtype == MOE_BF16 ? bwd<__nv_bfloat16>(d, ws, dy, x, w, pre, dx, dw, dbias, sms, st, launches)
+                             : bwd<float>(d, ws, dy, x, w, pre, dx, dw, dbias, sms, st, launches);
 }
 
 }  // namespace moe

@@ -1,0 +1,416 @@
+// linear_tc.cu -- the products of the linear operator on the 5th-generation tensor cores.
+//
+// k_linear_tc: persistent, one CTA per SM or a pair of CTAs (cta_group::2) per 256-row tile.
+//   warp 0     TMA producer: k-blocks of 64 into a ring of 128-byte-swizzled tiles
+//   warp 1     MMA issuer: tcgen05.mma into one of two tensor-memory accumulators
+//   warps 2-9  epilogue, two warps per tensor-memory lane quarter: bias, activation, residual,
+//              staged through shared memory and out with TMA stores, while the next tile's
+//              products run
+// A pair shares its B columns: a k-block costs each CTA 16 KB of A and 16 KB of B for a
+// 256 x 256 tile, 64 bytes per clock at the full MMA rate where a single CTA's 128 x 256
+// tile needs 96. Ragged sizes need no padding in memory: TMA reads zeros past the end of a
+// matrix and drops what is stored there. Every wait is bounded; one that runs out raises the
+// status word, and the CTA lets its own copies and MMAs finish, frees its tensor memory and
+// returns.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "linear_tc.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 64;                  // k-block: one 128-byte swizzle row of bf16
+constexpr int kChunkBytes = 64 * 128;    // an MN-major 64 (k) x 64 chunk
+constexpr int kStage = 32 * 128;         // one warp's 32 x 64 staging tile
+constexpr int kEpiWarps = 8;
+
+template <int CTAS, int BN>
+struct Cfg {
+  static constexpr int THREADS = 64 + 32 * kEpiWarps;
+  static constexpr int TILE_M = 128 * CTAS;
+  static constexpr int BCOLS = BN / CTAS;  // B columns this CTA loads
+  static constexpr int A_BYTES = 128 * kBK * 2;
+  static constexpr int B_BYTES = BCOLS * kBK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = (196608 / STAGE_BYTES) < 8 ? (196608 / STAGE_BYTES) : 8;
+  static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFF = EPI_OFF + kEpiWarps * kStage;
+  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+};
+
+struct TcArgs {
+  LinearGemm g;
+  int kblocks, mt, nt;
+};
+
+// byte offset of 16-byte piece j of row r in a 128-byte-swizzled staging tile
+__device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+
+// Tiles run down eight row blocks before they move to the next columns, so the tiles in
+// flight share a few row and column blocks in L2.
+__device__ __forceinline__ void tile_at(const TcArgs& a, int t, int* m, int* n) {
+  constexpr int G = 8;
+  const int grp = t / (G * a.nt), r = t - grp * (G * a.nt);
+  const int rows = min(G, a.mt - grp * G);
+  *n = r / rows;
+  *m = grp * G + (r - *n * rows);
+}
+
+template <int CTAS, int BN>
+__global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
+    k_linear_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmP, const TcArgs args) {
+  using C = Cfg<CTAS, BN>;
+  constexpr bool PAIR = CTAS == 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const LinearGemm& g = args.g;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int unit = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int units = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);   // the leader's producer arms it for both CTAs' bytes
+      mbar_init(&empty[s], 1);  // one MMA commit (multicast to both CTAs of a pair)
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], kEpiWarps * CTAS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    if constexpr (PAIR) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+    else tmem_alloc(tmem_slot, C::TMEM_COLS);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers exist before any remote arrive
+  tc_fence_after();
+  pdl_wait();  // the set-up above touched no global memory; everything below may read the previous kernel's outputs
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+  const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
+  const int total = args.mt * args.nt;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued[C::STAGES];
+#pragma unroll
+    for (int s = 0; s < C::STAGES; ++s) issued[s] = -1;
+    bool ok = true;
+    for (int t = unit; t < total && ok; t += units) {
+      int mt, nt;
+      tile_at(args, t, &mt, &nt);
+      const int m0 = mt * C::TILE_M + (int)rank * 128;
+      const int n0 = nt * BN + (int)rank * C::BCOLS;
+      for (int kb = 0; kb < args.kblocks; ++kb) {
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES), sb = sa + C::A_BYTES;
+        const uint32_t fb = full0 + stage * 8;
+        if (leader) mbar_arrive_expect_tx(&full[stage], CTAS * C::STAGE_BYTES);
+        issued[stage] = (int)phase;
+        auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+          if constexpr (PAIR) tma_load_2d_pair(dst, map, fb, c0, c1);
+          else tma_load_2d(dst, map, fb, c0, c1);
+        };
+        if (g.a_mn) {
+          load(sa, &tmA, m0, kb * kBK);
+          load(sa + kChunkBytes, &tmA, m0 + 64, kb * kBK);
+        } else {
+          load(sa, &tmA, kb * kBK, m0);
+        }
+        if (g.b_mn) {
+#pragma unroll
+          for (int c = 0; c < C::BCOLS / 64; ++c) load(sb + c * kChunkBytes, &tmB, n0 + c * 64, kb * kBK);
+        } else {
+          load(sb, &tmB, kb * kBK, n0);
+        }
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // no copy of ours may still be landing when the CTA leaves
+    if (leader)
+      for (int s = 0; s < C::STAGES; ++s)
+        if (issued[s] >= 0) mbar_wait_timed(&full[s], (uint32_t)issued[s], 200000000ull);
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = idesc_bf16(C::TILE_M, BN, g.a_mn, g.b_mn);
+    const uint32_t sa0 = smem_u32(smem);
+    const uint64_t ad0 = g.a_mn ? sdesc_sw128(sa0, kChunkBytes, 1024) : sdesc_sw128(sa0, 16, 1024);
+    const uint64_t bd0 =
+        g.b_mn ? sdesc_sw128(sa0 + C::A_BYTES, kChunkBytes, 1024) : sdesc_sw128(sa0 + C::A_BYTES, 16, 1024);
+    const uint64_t as = g.a_mn ? 2048 >> 4 : 32 >> 4, bs = g.b_mn ? 2048 >> 4 : 32 >> 4;
+    auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+      if constexpr (PAIR) tc_mma_bf16_pair(d, a, b, idesc, acc);
+      else tc_mma_bf16(d, a, b, idesc, acc);
+    };
+    int stage = 0, acc_i = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = unit; t < total && ok; t += units) {
+      const int acc = acc_i & 1;
+      const uint32_t par = (uint32_t)((acc_i >> 1) & 1);
+      const bool free_acc = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], par ^ 1u, abort_flag)
+                                 : mbar_wait_bounded(&tempty[acc], par ^ 1u, abort_flag);
+      if (!free_acc) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+      for (int kb = 0; kb < args.kblocks; ++kb) {
+        if (!mbar_wait_bounded(&full[stage], phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = ad0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+        const uint64_t bd = bd0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+        mma(d, ad, bd, kb != 0 ? 1u : 0u);
+        mma(d, ad + as, bd + bs, 1u);
+        mma(d, ad + 2 * as, bd + 2 * bs, 1u);
+        mma(d, ad + 3 * as, bd + 3 * bs, 1u);
+        if constexpr (PAIR) tc_commit_pair_mc(&empty[stage]);
+        else tc_commit(&empty[stage]);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if constexpr (PAIR) tc_commit_pair_mc(&tfull[acc]);
+      else tc_commit(&tfull[acc]);
+      ++acc_i;
+    }
+    if constexpr (PAIR) tc_commit_pair(drain);
+    else tc_commit(drain);
+    mbar_wait_timed(drain, 0, 200000000ull);
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;    // the tensor-memory lane quarter this warp may read
+    const int ew = warp - 2;
+    const uint32_t tile = smem_u32(smem + C::EPI_OFF + ew * kStage);
+    constexpr int CW = BN / 64 / 2;  // 64-column chunks of this warp
+    const int c0 = (ew / 4) * CW;
+    const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
+    const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
+    int acc_i = 0;
+    for (int t = unit; t < total; t += units) {
+      int mt, nt;
+      tile_at(args, t, &mt, &nt);
+      const int64_t row0 = (int64_t)mt * C::TILE_M + (int)rank * 128 + q * 32;  // this warp's first row
+      const int rows = (int)min((int64_t)32, (int64_t)g.M - row0);              // rows of it that exist
+      const int acc = acc_i & 1;
+      if (!mbar_wait_bounded(&tfull[acc], (uint32_t)((acc_i >> 1) & 1), abort_flag)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
+      for (int c = c0; c < c0 + CW; ++c) {
+        const int n0 = nt * BN + c * 64;
+        if (rows <= 0 || n0 >= g.N) continue;  // the same for the whole warp
+        const int cols = min(64, g.N - n0);    // a multiple of 8
+        // the staging tile is free once the stores that used it have read it
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        if (res) {  // eight lanes a row, 16 bytes each
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (lane >> 3) + 4 * i, j = lane & 7;
+            if (r < rows && 8 * j < cols) cp_async16(tile + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
+          }
+          cp_async_commit();
+        }
+        uint32_t v[2][32];
+        tmem_ld32_async(taddr + c * 64, v[0]);
+        tmem_ld32_async(taddr + c * 64 + 32, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_order(v[1]);
+        if (res) {
+          cp_async_wait<0>();
+          __syncwarp();
+        }
+        uint4 ypk[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float z[8], y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[j >> 2][(j & 3) * 8 + i]);
+          if (bias && 8 * j < cols) {
+            float b[8];
+            bf16x8_to_f(__ldg(reinterpret_cast<const uint4*>(bias + n0 + 8 * j)), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] += b[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = z[i];
+          if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = act_fwd<true>(g.act, z[i]);
+          }
+          if (res) {
+            float b[8];
+            bf16x8_to_f(ld_shared_v4(tile + piece(lane, j)), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += b[i];
+          }
+          if (g.out_f32) {
+            if (lane < rows && 8 * j < cols) {
+              float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0 + 8 * j);
+              o[0] = make_float4(y[0], y[1], y[2], y[3]);
+              o[1] = make_float4(y[4], y[5], y[6], y[7]);
+            }
+          } else {
+            ypk[j] = f_to_bf16x8(y);
+          }
+          // each lane overwrites only the residual pieces it has just read
+          if (g.pre) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z));
+          else if (!g.out_f32) st_shared_v4(tile + piece(lane, j), ypk[j]);
+        }
+        if (g.out_f32 && !g.pre) continue;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(g.pre ? &tmP : &tmY, tile, n0, (int)row0);
+          bulk_commit();
+        }
+        if (g.pre && !g.out_f32) {  // y follows through the same tile
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile + piece(lane, j), ypk[j]);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmY, tile, n0, (int)row0);
+            bulk_commit();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(tempty0 + acc * 8);
+        else mbar_arrive(&tempty[acc]);
+      }
+      ++acc_i;
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // no CTA of the pair leaves while the other still uses it
+  tc_fence_after();
+  if (threadIdx.x == 0 && *abort_flag) set_status(g.status, MOE_ERR_TIMEOUT);
+  if (warp == 2) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// bf16 [rows, cols], row stride ld elements, box 64 columns x box_rows, 128-byte swizzle
+bool make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CTAS, int BN>
+cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
+  using C = Cfg<CTAS, BN>;
+  static_assert(C::SMEM <= 232448, "shared memory budget");
+  auto kern = k_linear_tc<CTAS, BN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mA, mB, mY, mP;
+  bool ok = g.a_mn ? make_map(&mA, g.A, g.K, g.M, g.lda, kBK) : make_map(&mA, g.A, g.M, g.K, g.lda, 128);
+  ok = ok && (g.b_mn ? make_map(&mB, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mB, g.B, g.N, g.K, g.ldb, C::BCOLS));
+  mY = mP = mA;  // where unused
+  if (!g.out_f32) ok = ok && make_map(&mY, g.y, g.M, g.N, g.N, 32);
+  if (g.pre) ok = ok && make_map(&mP, g.pre, g.M, g.N, g.N, 32);
+  if (!ok) return cudaErrorInvalidValue;
+  TcArgs a;
+  a.g = g;
+  a.kblocks = (g.K + kBK - 1) / kBK;
+  a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
+  a.nt = (g.N + BN - 1) / BN;
+  const int64_t total = (int64_t)a.mt * a.nt;
+  if (total >= (1ll << 31)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (MOE_PDL) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (CTAS == 2) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = 2;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  cfg.gridDim = dim3((unsigned)(CTAS * std::min<int64_t>(total, sms / CTAS)));
+  return cudaLaunchKernelEx(&cfg, kern, mA, mB, mY, mP, a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
+  const int64_t t256 = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
+  if (g.M > 128 && t256 * 2 >= sms) return launch_tile<2, 256>(g, sms, st);
+  return launch_tile<1, 128>(g, sms, st);
+}
+
+}  // namespace moe
