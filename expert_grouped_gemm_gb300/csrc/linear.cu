@@ -85,7 +85,10 @@ __global__ void __launch_bounds__(256) k_linear_simt(const SimtGemm g) {
       if (m >= g.M || n >= g.N) continue;
       const int64_t o = (int64_t)m * g.N + n;
       const float z = acc[i][j] + (g.bias ? io<T>::to_f(reinterpret_cast<const T*>(g.bias)[n]) : 0.0f);
-      float y = act_fwd<sizeof(T) == 2>(g.act, z);
+      const float zz[1] = {z};
+      float yy[1];
+      act_fwd<sizeof(T) == 2, 1>(g.act, zz, yy);
+      float y = yy[0];
       if (g.residual) y += io<T>::to_f(reinterpret_cast<const T*>(g.residual)[o]);
       if (g.pre) reinterpret_cast<T*>(g.pre)[o] = io<T>::cvt(z);
       if (g.out_f32) reinterpret_cast<float*>(g.out)[o] = y;
@@ -108,7 +111,12 @@ __global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T*
   for (int m = m0; m < m1; ++m) {
     const int64_t o = (int64_t)m * N + n;
     float v = io<T>::to_f(dy[o]);
-    if (pre) v *= act_grad<sizeof(T) == 2>(act, io<T>::to_f(pre[o]));
+    if (pre) {
+      const float z[1] = {io<T>::to_f(pre[o])};
+      float d[1] = {v};
+      act_grad_mul<sizeof(T) == 2, 1>(act, z, d);
+      v = d[0];
+    }
     if (dz) dz[o] = io<T>::cvt(v);
     s += v;
   }

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kBK = 64;                  // k-block: one 128-byte swizzle row of bf16
 constexpr int kChunkBytes = 64 * 128;    // an MN-major 64 (k) x 64 chunk
-constexpr int kStage = 32 * 128;         // one warp's 32 x 64 staging tile
+constexpr int kStage = 32 * 128;         // one 32 x 64 staging tile; a warp has two
 constexpr int kEpiWarps = 8;
 
 template <int CTAS, int BN>
@@ -37,9 +37,9 @@ struct Cfg {
   static constexpr int A_BYTES = 128 * kBK * 2;
   static constexpr int B_BYTES = BCOLS * kBK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = (196608 / STAGE_BYTES) < 8 ? (196608 / STAGE_BYTES) : 8;
+  static constexpr int STAGES = 163840 / STAGE_BYTES;
   static constexpr int EPI_OFF = STAGES * STAGE_BYTES;
-  static constexpr int BAR_OFF = EPI_OFF + kEpiWarps * kStage;
+  static constexpr int BAR_OFF = EPI_OFF + kEpiWarps * 2 * kStage;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
 };
@@ -216,12 +216,13 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;    // the tensor-memory lane quarter this warp may read
     const int ew = warp - 2;
-    const uint32_t tile = smem_u32(smem + C::EPI_OFF + ew * kStage);
+    const uint32_t tile = smem_u32(smem + C::EPI_OFF + ew * 2 * kStage);
     constexpr int CW = BN / 64 / 2;  // 64-column chunks of this warp
     const int c0 = (ew / 4) * CW;
     const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
     const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
     int acc_i = 0;
+    int sc = 0;  // chunks stored so far
     for (int t = unit; t < total; t += units) {
       int mt, nt;
       tile_at(args, t, &mt, &nt);
@@ -235,14 +236,20 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         const int n0 = nt * BN + c * 64;
         if (rows <= 0 || n0 >= g.N) continue;  // the same for the whole warp
         const int cols = min(64, g.N - n0);    // a multiple of 8
-        // the staging tile is free once the stores that used it have read it
-        if (lane == 0) bulk_wait_read_all();
+        // With a second output z takes one tile and y the other; else y alternates between the
+        // two, and the stores of the chunk before may still be reading.
+        const uint32_t ty = tile + (g.pre ? kStage : (sc & 1) * kStage);
+        ++sc;
+        if (lane == 0) {
+          if (g.pre) bulk_wait_read_all();
+          else bulk_wait_read_but1();
+        }
         __syncwarp();
         if (res) {  // eight lanes a row, 16 bytes each
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = (lane >> 3) + 4 * i, j = lane & 7;
-            if (r < rows && 8 * j < cols) cp_async16(tile + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
+            if (r < rows && 8 * j < cols) cp_async16(ty + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
           }
           cp_async_commit();
         }
@@ -255,7 +262,6 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           cp_async_wait<0>();
           __syncwarp();
         }
-        uint4 ypk[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float z[8], y[8];
@@ -267,49 +273,28 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[i] += b[i];
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = z[i];
-          if (g.act != MOE_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = act_fwd<true>(g.act, z[i]);
-          }
+          act_fwd<true, 8>(g.act, z, y);
           if (res) {
             float b[8];
-            bf16x8_to_f(ld_shared_v4(tile + piece(lane, j)), b);
+            bf16x8_to_f(ld_shared_v4(ty + piece(lane, j)), b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] += b[i];
           }
-          if (g.out_f32) {
-            if (lane < rows && 8 * j < cols) {
-              float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0 + 8 * j);
-              o[0] = make_float4(y[0], y[1], y[2], y[3]);
-              o[1] = make_float4(y[4], y[5], y[6], y[7]);
-            }
-          } else {
-            ypk[j] = f_to_bf16x8(y);
-          }
-          // each lane overwrites only the residual pieces it has just read
           if (g.pre) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z));
-          else if (!g.out_f32) st_shared_v4(tile + piece(lane, j), ypk[j]);
+          if (!g.out_f32) {  // over the residual piece this lane has just read
+            st_shared_v4(ty + piece(lane, j), f_to_bf16x8(y));
+          } else if (lane < rows && 8 * j < cols) {
+            float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0 + 8 * j);
+            o[0] = make_float4(y[0], y[1], y[2], y[3]);
+            o[1] = make_float4(y[4], y[5], y[6], y[7]);
+          }
         }
-        if (g.out_f32 && !g.pre) continue;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(g.pre ? &tmP : &tmY, tile, n0, (int)row0);
+          if (!g.out_f32) tma_store_2d(&tmY, ty, n0, (int)row0);
+          if (g.pre) tma_store_2d(&tmP, tile, n0, (int)row0);
           bulk_commit();
-        }
-        if (g.pre && !g.out_f32) {  // y follows through the same tile
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile + piece(lane, j), ypk[j]);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tmY, tile, n0, (int)row0);
-            bulk_commit();
-          }
         }
       }
       tc_fence_before();
