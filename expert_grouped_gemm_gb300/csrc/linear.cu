@@ -96,41 +96,130 @@ __global__ void __launch_bounds__(256) k_linear_simt(const SimtGemm g) {
     }
 }
 
-constexpr int kColChunks = 64;  // row chunks of the bias gradient's partial sums
+// ---------------------------------------------------------------- dz and the bias gradient
+// dz = dy act'(pre), row stride ldz (stored when dz is given), and the column sums of dz (when
+// part is given). Bound by HBM: dy and pre are read once, dz written once. A block of 64 x 4
+// threads owns 64 vectors of VEC columns and a chunk of rows, four rows of it at a time, with
+// the loads of eight steps in flight; it adds its columns in registers, then over its four
+// row lanes in order.
+constexpr int kDzCols = 64, kDzRows = 4;
+constexpr int kDzSlots = 1216;  // blocks to aim for: 8 for each of 152 SMs
 
-// dz = dy act'(pre) (stored when dz is given) and, when part is given, the column sums of one
-// chunk of rows.
-template <typename T>
-__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T* dz, float* part, int M, int N, int act,
-                                                   int per) {
-  pdl_wait();  // the previous kernel has completed and its writes are visible
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= N) return;
-  const int m0 = blockIdx.y * per, m1 = min(M, m0 + per);
-  float s = 0.0f;
-  for (int m = m0; m < m1; ++m) {
-    const int64_t o = (int64_t)m * N + n;
-    float v = io<T>::to_f(dy[o]);
-    if (pre) {
-      const float z[1] = {io<T>::to_f(pre[o])};
-      float d[1] = {v};
-      act_grad_mul<sizeof(T) == 2, 1>(act, z, d);
-      v = d[0];
-    }
-    if (dz) dz[o] = io<T>::cvt(v);
-    s += v;
-  }
-  if (part) part[(int64_t)blockIdx.y * N + n] = s;
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[VEC]) {
+  struct alignas(sizeof(T) * VEC) A {
+    T v[VEC];
+  };
+  const A a = *reinterpret_cast<const A*>(p);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = io<T>::to_f(a.v[i]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
+  struct alignas(sizeof(T) * VEC) A {
+    T v[VEC];
+  };
+  A a;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) a.v[i] = io<T>::cvt(f[i]);
+  *reinterpret_cast<A*>(p) = a;
 }
 
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T* dz, float* part, int M, int N,
+                                                   int64_t ldz, int act, int per) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ float red[kDzRows][kDzCols * VEC];
+  const int cx = threadIdx.x % kDzCols, ry = threadIdx.x / kDzCols;
+  const int n = (blockIdx.x * kDzCols + cx) * VEC;
+  const int m1 = min(M, ((int)blockIdx.y + 1) * per);
+  float sum[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+  if (n < N) {
+    constexpr int U = 4;  // rows in flight
+    for (int m = blockIdx.y * per + ry; m < m1; m += U * kDzRows) {
+      float d[U][VEC], z[U][VEC];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (m + u * kDzRows < m1) {
+          const int64_t o = (int64_t)(m + u * kDzRows) * N + n;
+          load_vec<T, VEC>(dy + o, d[u]);
+          if (pre) load_vec<T, VEC>(pre + o, z[u]);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (m + u * kDzRows < m1) {
+          if (pre) act_grad_mul<sizeof(T) == 2, VEC>(act, z[u], d[u]);
+          if (dz) store_vec<T, VEC>(dz + (int64_t)(m + u * kDzRows) * ldz + n, d[u]);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) sum[i] += d[u][i];
+        }
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) red[ry][cx * VEC + i] = sum[i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < kDzCols * VEC; c += blockDim.x) {
+    const int col = blockIdx.x * kDzCols * VEC + c;
+    if (col >= N) break;
+    float s = red[0][c];
+#pragma unroll
+    for (int r = 1; r < kDzRows; ++r) s += red[r][c];
+    part[(int64_t)blockIdx.y * N + col] = s;
+  }
+}
+
+// The chunks' column sums added: eight lanes of chunks per column, then those in order.
 template <typename T>
 __global__ void __launch_bounds__(256) k_linear_dbias(const float* part, int chunks, int N, T* db) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  const int n = blockIdx.x * blockDim.x + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float red[8][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int n = blockIdx.x * 32 + cx;
   float s = 0.0f;
-  for (int c = 0; c < chunks; ++c) s += part[(int64_t)c * N + n];
-  db[n] = io<T>::cvt(s);
+  if (n < N) {
+#pragma unroll 8
+    for (int c = ry; c < chunks; c += 8) s += part[(int64_t)c * N + n];
+  }
+  red[ry][cx] = s;
+  __syncthreads();
+  if (ry == 0 && n < N) {
+#pragma unroll
+    for (int r = 1; r < 8; ++r) s += red[r][cx];
+    db[n] = io<T>::cvt(s);
+  }
+}
+
+// Row chunks of the column sums: enough blocks for two rounds on every SM, at least 16 rows each.
+int dz_chunks(int64_t M, int64_t N, int vec) {
+  const int64_t cb = (N + kDzCols * vec - 1) / (kDzCols * vec);
+  const int64_t want = std::max<int64_t>(1, (int64_t)kDzSlots / cb);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, (M + 15) / 16));
+}
+
+// A matrix with odd rows copied to rows of a multiple of 16 bytes, for the tensor-core products
+// (TMA reads rows at 16-byte strides). The columns past C of dst are never read.
+__global__ void __launch_bounds__(256) k_pack_rows(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t R, int C,
+                                                   int64_t ld) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  constexpr int U = 8;
+  const int64_t total = R * C;
+  for (int64_t base = (int64_t)blockIdx.x * 256 * U + threadIdx.x; base < total; base += (int64_t)gridDim.x * 256 * U) {
+    __nv_bfloat16 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (base + u * 256 < total) v[u] = src[base + u * 256];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = base + u * 256;
+      if (i < total) {
+        const int64_t r = i / C;
+        dst[r * ld + (i - r * C)] = v[u];
+      }
+    }
+  }
 }
 
 template <typename T>
@@ -142,86 +231,148 @@ cudaError_t run_simt(const SimtGemm& g, cudaStream_t st, int* launches) {
   return cudaSuccess;
 }
 
-// The tensor-core kernel needs bf16 rows of a multiple of 16 bytes.
-bool tc_shape(const moe_linear_dims& d) { return d.dtype == MOE_BF16 && d.K % 8 == 0 && d.N % 8 == 0; }
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <typename T>
-cudaError_t fwd(const moe_linear_dims& d, void* ws, const void* x, const void* w, const void* bias,
-                const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
-  if (tc_shape(d)) {
-    LinearGemm g = {(int)d.M, (int)d.N, (int)d.K, x, w, d.K, d.N, 0, 1, bias, residual, y, pre, d.act, d.out_f32,
-                    static_cast<int*>(ws)};
-    *launches += 1;
-    return launch_linear_tc(g, sms, st);
-  }
-  SimtGemm g = {x, w, d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, bias, residual, y, pre, d.act, d.out_f32};
-  return run_simt<T>(g, st, launches);
+// Workspace: header, column sums, dz, and copies of x and w with rows of a multiple of 16 bytes
+// where the caller's are not.
+struct LinearWs {
+  size_t part, dz, xp, wp, total;
+};
+LinearWs layout(const moe_linear_dims& d) {
+  const bool bf = d.dtype == MOE_BF16;
+  const size_t es = bf ? 2 : 4;
+  LinearWs L;
+  size_t o = kLinearHeader;
+  L.part = o;
+  o += up256((size_t)dz_chunks(d.M, d.N, d.N % (16 / (int64_t)es) ? 1 : 16 / (int)es) * d.N * sizeof(float));
+  L.dz = o;
+  o += up256((size_t)d.M * (bf ? up8(d.N) : d.N) * es);
+  L.xp = o;
+  if (bf && d.K % 8) o += up256((size_t)d.M * up8(d.K) * es);
+  L.wp = o;
+  if (bf && d.N % 8) o += up256((size_t)d.K * up8(d.N) * es);
+  L.total = o;
+  return L;
+}
+
+// p itself when its rows are multiples of 16 bytes, else a packed copy at `copy`
+cudaError_t packed(const void** p, void* copy, int64_t R, int64_t C, int sms, cudaStream_t st, int* launches) {
+  if (C % 8 == 0) return cudaSuccess;
+  const int64_t blocks = (R * C + 2047) / 2048;
+  *launches += 1;
+  MOE_LAUNCH(k_pack_rows, (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), 256, 0, st,
+             static_cast<const __nv_bfloat16*>(*p), static_cast<__nv_bfloat16*>(copy), R, (int)C, up8(C));
+  *p = copy;
+  return cudaSuccess;
 }
 
 template <typename T>
-cudaError_t bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w, const void* pre,
-                void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
+cudaError_t run_dz(const moe_linear_dims& d, const void* dy, const void* pre, void* dz, int64_t ldz, float* part,
+                   cudaStream_t st, int* launches) {
+  constexpr int V = 16 / sizeof(T);
+  const int M = (int)d.M, N = (int)d.N;
+  const int vec = N % V ? 1 : V;
+  const int cb = (N + kDzCols * vec - 1) / (kDzCols * vec);
+  const int want = dz_chunks(M, N, vec), per = (M + want - 1) / want, chunks = (M + per - 1) / per;
+  *launches += 1;
+  if (vec == V)
+    MOE_LAUNCH((k_linear_dz<T, V>), dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)pre, (T*)dz, part, M, N, ldz,
+               d.act, per);
+  else
+    MOE_LAUNCH((k_linear_dz<T, 1>), dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)pre, (T*)dz, part, M, N, ldz,
+               d.act, per);
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t run_dbias(const moe_linear_dims& d, const float* part, void* db, cudaStream_t st, int* launches) {
+  constexpr int V = 16 / sizeof(T);
+  const int M = (int)d.M, N = (int)d.N;
+  const int want = dz_chunks(M, N, N % V ? 1 : V), per = (M + want - 1) / want, chunks = (M + per - 1) / per;
+  *launches += 1;
+  MOE_LAUNCH(k_linear_dbias<T>, (N + 31) / 32, 256, 0, st, part, chunks, N, (T*)db);
+  return cudaSuccess;
+}
+
+cudaError_t fwd_bf16(const moe_linear_dims& d, char* ws, const void* x, const void* w, const void* bias,
+                     const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
+  const LinearWs L = layout(d);
+  cudaError_t e;
+  if ((e = packed(&x, ws + L.xp, d.M, d.K, sms, st, launches)) != cudaSuccess) return e;
+  if ((e = packed(&w, ws + L.wp, d.K, d.N, sms, st, launches)) != cudaSuccess) return e;
+  LinearGemm g = {(int)d.M, (int)d.N, (int)d.K, x,   w,     up8(d.K),  up8(d.N), 0, 1, bias, residual,
+                  y,        pre,      d.act,    d.out_f32, reinterpret_cast<int*>(ws)};
+  *launches += 1;
+  return launch_linear_tc(g, sms, st);
+}
+
+cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const void* x, const void* w, const void* pre,
+                     void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
+  const LinearWs L = layout(d);
   const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
-  const bool has_act = d.act != MOE_ACT_NONE;
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + kLinearHeader);
-  T* dzb = reinterpret_cast<T*>(static_cast<char*>(ws) + kLinearHeader +
-                                ((size_t)kColChunks * N * sizeof(float) + 255) / 256 * 256);
-  const void* dz = has_act ? dzb : dy;
-  if (has_act || dbias) {
-    const int per = (M + kColChunks - 1) / kColChunks, chunks = (M + per - 1) / per;
-    *launches += 1;
-    MOE_LAUNCH(k_linear_dz<T>, dim3((N + 255) / 256, chunks), 256, 0, st, (const T*)dy, (const T*)pre,
-               has_act ? dzb : nullptr, dbias ? part : nullptr, M, N, d.act, per);
-    if (dbias) {
-      *launches += 1;
-      MOE_LAUNCH(k_linear_dbias<T>, (N + 255) / 256, 256, 0, st, (const float*)part, chunks, N, (T*)dbias);
-    }
-  }
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  int* status = reinterpret_cast<int*>(ws);
+  // dz is dy itself without an activation, unless the products need it with wider rows
+  const bool store = (dx || dw) && (d.act != MOE_ACT_NONE || N % 8);
+  const void* dz = store ? ws + L.dz : dy;
   cudaError_t e = cudaSuccess;
-  if (tc_shape(d)) {
-    int* status = static_cast<int*>(ws);
-    if (dx) {
-      LinearGemm g = {M, K, N, dz, w, N, N, 0, 0, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0, status};
-      *launches += 1;
-      if ((e = launch_linear_tc(g, sms, st)) != cudaSuccess) return e;
-    }
-    if (dw) {
-      LinearGemm g = {K, N, M, x, dz, K, N, 1, 1, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0, status};
-      *launches += 1;
-      e = launch_linear_tc(g, sms, st);
-    }
-    return e;
+  if (store || dbias)
+    e = run_dz<__nv_bfloat16>(d, dy, pre, store ? ws + L.dz : nullptr, up8(N), dbias ? part : nullptr, st, launches);
+  if (e == cudaSuccess && dbias) e = run_dbias<__nv_bfloat16>(d, part, dbias, st, launches);
+  if (e == cudaSuccess && dx) {
+    if ((e = packed(&w, ws + L.wp, K, N, sms, st, launches)) != cudaSuccess) return e;
+    LinearGemm g = {M, K, N, dz, w, up8(N), up8(N), 0, 0, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0, status};
+    *launches += 1;
+    e = launch_linear_tc(g, sms, st);
   }
-  if (dx) {
+  if (e == cudaSuccess && dw) {
+    if ((e = packed(&x, ws + L.xp, M, K, sms, st, launches)) != cudaSuccess) return e;
+    LinearGemm g = {K, N, M, x, dz, up8(K), up8(N), 1, 1, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0, status};
+    *launches += 1;
+    e = launch_linear_tc(g, sms, st);
+  }
+  return e;
+}
+
+cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const void* x, const void* w, const void* pre,
+                    void* dx, void* dw, void* dbias, cudaStream_t st, int* launches) {
+  const LinearWs L = layout(d);
+  const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  const bool store = (dx || dw) && d.act != MOE_ACT_NONE;
+  const void* dz = store ? ws + L.dz : dy;
+  cudaError_t e = cudaSuccess;
+  if (store || dbias) e = run_dz<float>(d, dy, pre, store ? ws + L.dz : nullptr, N, dbias ? part : nullptr, st, launches);
+  if (e == cudaSuccess && dbias) e = run_dbias<float>(d, part, dbias, st, launches);
+  if (e == cudaSuccess && dx) {
     SimtGemm g = {dz, w, N, 1, 1, N, M, N, K, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0};
-    if ((e = run_simt<T>(g, st, launches)) != cudaSuccess) return e;
+    e = run_simt<float>(g, st, launches);
   }
-  if (dw) {
+  if (e == cudaSuccess && dw) {
     SimtGemm g = {x, dz, 1, K, N, 1, K, M, N, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0};
-    e = run_simt<T>(g, st, launches);
+    e = run_simt<float>(g, st, launches);
   }
   return e;
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(const moe_linear_dims& d) {
-  const size_t es = d.dtype == MOE_BF16 ? 2 : 4;
-  return kLinearHeader + ((size_t)kColChunks * d.N * sizeof(float) + 255) / 256 * 256 +
-         ((size_t)d.M * d.N * es + 255) / 256 * 256;
-}
+size_t linear_workspace_bytes(const moe_linear_dims& d) { return layout(d).total; }
 
 cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x, const void* w, const void* bias,
                               const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
-  return d.dtype == MOE_BF16 ? fwd<__nv_bfloat16>(d, ws, x, w, bias, residual, y, pre, sms, st, launches)
-                             : fwd<float>(d, ws, x, w, bias, residual, y, pre, sms, st, launches);
+  if (d.dtype == MOE_BF16)
+    return fwd_bf16(d, static_cast<char*>(ws), x, w, bias, residual, y, pre, sms, st, launches);
+  SimtGemm g = {x, w, d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, bias, residual, y, pre, d.act, d.out_f32};
+  return run_simt<float>(g, st, launches);
 }
 
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,
                               const void* pre, void* dx, void* dw, void* dbias, int sms, cudaStream_t st,
                               int* launches) {
-  return d.dtype == MOE_BF16 ? bwd<__nv_bfloat16>(d, ws, dy, x, w, pre, dx, dw, dbias, sms, st, launches)
-                             : bwd<float>(d, ws, dy, x, w, pre, dx, dw, dbias, sms, st, launches);
+  return d.dtype == MOE_BF16 ? bwd_bf16(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, sms, st, launches)
+                             : bwd_f32(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, st, launches);
 }
 
 }  // namespace moe

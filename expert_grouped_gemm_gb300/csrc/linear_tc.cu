@@ -12,6 +12,12 @@
 // matrix and drops what is stored there. Every wait is bounded; one that runs out raises the
 // status word, and the CTA lets its own copies and MMAs finish, frees its tensor memory and
 // returns.
+//
+// k_linear_split: for products with too few 128-row tiles to fill the GPU (decoding batches, a
+// narrow output). The wide matrix (the weight) takes the MMA's 128 rows and the tokens its
+// columns, so a product with a handful of tokens multiplies 16 of them, not 128; a cluster of
+// up to eight CTAs shares one output tile, each with a part of K, and adds the parts in rank
+// order through distributed shared memory, so the result does not depend on timing.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -52,6 +58,28 @@ struct TcArgs {
 // byte offset of 16-byte piece j of row r in a 128-byte-swizzled staging tile
 __device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
+// A warp's 32 x 64 piece of a row-major bf16 matrix into a staging tile and back, two columns a lane.
+__device__ __forceinline__ void rows_in(uint32_t tile, const __nv_bfloat16* src, int64_t ld, int rows, int cols,
+                                        int lane) {
+  for (int r = 0; r < rows; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = lane + 32 * h;
+      const uint16_t v = c < cols ? *reinterpret_cast<const uint16_t*>(src + r * ld + c) : (uint16_t)0;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + piece(r, c >> 3) + (c & 7) * 2), "h"(v) : "memory");
+    }
+}
+__device__ __forceinline__ void rows_out(__nv_bfloat16* dst, int64_t ld, uint32_t tile, int rows, int cols, int lane) {
+  for (int r = 0; r < rows; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = lane + 32 * h;
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(tile + piece(r, c >> 3) + (c & 7) * 2) : "memory");
+      if (c < cols) *reinterpret_cast<uint16_t*>(dst + r * ld + c) = v;
+    }
+}
+
 // Tiles run down eight row blocks before they move to the next columns, so the tiles in
 // flight share a few row and column blocks in L2.
 __device__ __forceinline__ void tile_at(const TcArgs& a, int t, int* m, int* n) {
@@ -62,7 +90,9 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int t, int* m, int* n) 
   *m = grp * G + (r - *n * rows);
 }
 
-template <int CTAS, int BN>
+// VEC: the rows of y, pre and the residual are multiples of 16 bytes (N % 8 == 0); else they are
+// read and written element by element, still a whole row of the tile per instruction.
+template <int CTAS, int BN, bool VEC>
 __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmP, const TcArgs args) {
@@ -235,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       for (int c = c0; c < c0 + CW; ++c) {
         const int n0 = nt * BN + c * 64;
         if (rows <= 0 || n0 >= g.N) continue;  // the same for the whole warp
-        const int cols = min(64, g.N - n0);    // a multiple of 8
+        const int cols = min(64, g.N - n0);    // with VEC a multiple of 8
         // With a second output z takes one tile and y the other; else y alternates between the
         // two, and the stores of the chunk before may still be reading.
         const uint32_t ty = tile + (g.pre ? kStage : (sc & 1) * kStage);
@@ -245,13 +275,17 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           else bulk_wait_read_but1();
         }
         __syncwarp();
-        if (res) {  // eight lanes a row, 16 bytes each
+        if (res) {
+          if constexpr (VEC) {  // eight lanes a row, 16 bytes each
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (lane >> 3) + 4 * i, j = lane & 7;
-            if (r < rows && 8 * j < cols) cp_async16(ty + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
+            for (int i = 0; i < 8; ++i) {
+              const int r = (lane >> 3) + 4 * i, j = lane & 7;
+              if (r < rows && 8 * j < cols) cp_async16(ty + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
+            }
+            cp_async_commit();
+          } else {
+            rows_in(ty, res + row0 * g.N + n0, g.N, rows, cols, lane);
           }
-          cp_async_commit();
         }
         uint32_t v[2][32];
         tmem_ld32_async(taddr + c * 64, v[0]);
@@ -259,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         tmem_ld_wait(v[0]);
         tmem_ld_order(v[1]);
         if (res) {
-          cp_async_wait<0>();
+          if constexpr (VEC) cp_async_wait<0>();
           __syncwarp();
         }
 #pragma unroll
@@ -269,7 +303,12 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[j >> 2][(j & 3) * 8 + i]);
           if (bias && 8 * j < cols) {
             float b[8];
-            bf16x8_to_f(__ldg(reinterpret_cast<const uint4*>(bias + n0 + 8 * j)), b);
+            if constexpr (VEC) {
+              bf16x8_to_f(__ldg(reinterpret_cast<const uint4*>(bias + n0 + 8 * j)), b);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) b[i] = 8 * j + i < cols ? __bfloat162float(bias[n0 + 8 * j + i]) : 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[i] += b[i];
           }
@@ -284,10 +323,25 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           if (!g.out_f32) {  // over the residual piece this lane has just read
             st_shared_v4(ty + piece(lane, j), f_to_bf16x8(y));
           } else if (lane < rows && 8 * j < cols) {
-            float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0 + 8 * j);
-            o[0] = make_float4(y[0], y[1], y[2], y[3]);
-            o[1] = make_float4(y[4], y[5], y[6], y[7]);
+            float* of = reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0 + 8 * j;
+            if constexpr (VEC) {
+              float4* o = reinterpret_cast<float4*>(of);
+              o[0] = make_float4(y[0], y[1], y[2], y[3]);
+              o[1] = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (8 * j + i < cols) of[i] = y[i];
+            }
           }
+        }
+        if constexpr (!VEC) {
+          __syncwarp();
+          const int64_t o = row0 * g.N + n0;
+          if (!g.out_f32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + o, g.N, ty, rows, cols, lane);
+          if (g.pre) rows_out(reinterpret_cast<__nv_bfloat16*>(g.pre) + o, g.N, tile, rows, cols, lane);
+          __syncwarp();
+          continue;
         }
         fence_async_smem();
         __syncwarp();
@@ -320,6 +374,186 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
   }
 }
 
+// ---------------------------------------------------------------- few tiles: K split over a cluster
+template <int NB>
+struct SplitCfg {
+  static constexpr int THREADS = 192;  // producer, MMA issuer, four epilogue warps
+  static constexpr int A_BYTES = 128 * kBK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + NB * kBK * 2;
+  // up to 64 tokens two CTAs share an SM
+  static constexpr int STAGES = (NB <= 64 ? 110592 : 196608) / STAGE_BYTES;
+  static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static constexpr uint32_t TMEM_COLS = NB < 32 ? 32 : NB;
+  static_assert(NB * 128 * 4 <= BAR_OFF, "the partial sums reuse the ring");
+};
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// z -> y, pre of one element
+__device__ __forceinline__ void emit(const LinearGemm& g, int64_t t, int n, float z) {
+  const int64_t o = t * g.N + n;
+  const float zz[1] = {z};
+  float y[1];
+  act_fwd<true, 1>(g.act, zz, y);
+  if (g.residual) y[0] += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g.residual)[o]);
+  if (g.pre) reinterpret_cast<__nv_bfloat16*>(g.pre)[o] = __float2bfloat16_rn(z);
+  if (g.out_f32) reinterpret_cast<float*>(g.y)[o] = y[0];
+  else reinterpret_cast<__nv_bfloat16*>(g.y)[o] = __float2bfloat16_rn(y[0]);
+}
+
+// Block (feature tile of 128, token tile of NB, part of K); the cluster holds the parts of one tile.
+template <int NB>
+__global__ void __launch_bounds__(SplitCfg<NB>::THREADS)
+    k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const TcArgs args, int S) {
+  using C = SplitCfg<NB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* done = empty + C::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const LinearGemm& g = args.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
+  const int f0 = (tile % args.nt) * 128, t0 = (tile / args.nt) * NB;
+  const int kb0 = (int)((int64_t)args.kblocks * part / S), kb1 = (int)((int64_t)args.kblocks * (part + 1) / S);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();  // the set-up above touched no global memory; everything below may read the previous kernel's outputs
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+      if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) break;
+      const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES), sb = sa + C::A_BYTES;
+      const uint32_t fb = smem_u32(&full[stage]);
+      mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+      if (g.b_mn) {
+        tma_load_2d(sa, &tmW, fb, f0, kb * kBK);
+        tma_load_2d(sa + kChunkBytes, &tmW, fb, f0 + 64, kb * kBK);
+      } else {
+        tma_load_2d(sa, &tmW, fb, kb * kBK, f0);
+      }
+      if (g.a_mn) {
+#pragma unroll
+        for (int c = 0; c < NB / 64; ++c) tma_load_2d(sb + c * kChunkBytes, &tmX, fb, t0 + c * 64, kb * kBK);
+      } else {
+        tma_load_2d(sb, &tmX, fb, kb * kBK, t0);
+      }
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    // no copy of ours may still be landing when the CTA leaves
+    for (int s = 0; s < min(C::STAGES, issued); ++s)
+      mbar_wait_timed(&full[s], s < stage ? phase : phase ^ 1u, 200000000ull);
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = idesc_bf16(128, NB, g.b_mn, g.a_mn);
+    const uint32_t sa0 = smem_u32(smem);
+    const uint64_t ad0 = g.b_mn ? sdesc_sw128(sa0, kChunkBytes, 1024) : sdesc_sw128(sa0, 16, 1024);
+    const uint64_t bd0 =
+        g.a_mn ? sdesc_sw128(sa0 + C::A_BYTES, kChunkBytes, 1024) : sdesc_sw128(sa0 + C::A_BYTES, 16, 1024);
+    const uint64_t as = g.b_mn ? 2048 >> 4 : 32 >> 4, bs = g.a_mn ? 2048 >> 4 : 32 >> 4;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_bounded(&full[stage], phase, abort_flag)) break;
+      tc_fence_after();
+      const uint64_t ad = ad0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+      const uint64_t bd = bd0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+      tc_mma_bf16(tmem_base, ad, bd, idesc, kb != kb0 ? 1u : 0u);
+      tc_mma_bf16(tmem_base, ad + as, bd + bs, idesc, 1u);
+      tc_mma_bf16(tmem_base, ad + 2 * as, bd + 2 * bs, idesc, 1u);
+      tc_mma_bf16(tmem_base, ad + 3 * as, bd + 3 * bs, idesc, 1u);
+      tc_commit(&empty[stage]);
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    tc_commit(done);
+    mbar_wait_timed(done, 0, 200000000ull);
+  }
+  __syncwarp();
+
+  // ------------------------------------------------------------ epilogue
+  const int ntok = min(NB, g.M - t0);
+  const int f = (warp & 3) * 32 + lane;  // this thread's feature of the tile
+  const int n = f0 + f;
+  float* sums = reinterpret_cast<float*>(smem);  // [token][128], over the ring once every MMA has read it
+  bool ok = true;
+  if (warp >= 2) {
+    ok = mbar_wait_bounded(done, 0, abort_flag);
+    tc_fence_after();
+    const float b = ok && g.bias && n < g.N ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g.bias)[n]) : 0.0f;
+    if (ok) {
+#pragma unroll 1
+      for (int c = 0; c < (NB + 31) / 32; ++c) {
+        if (c * 32 >= ntok) break;
+        float v[32];
+        tmem_ld32(tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(c * 32), v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int t = c * 32 + i;
+          if (t < ntok) {
+            if (S > 1) sums[t * 128 + f] = v[i];
+            else if (n < g.N) emit(g, t0 + t, n, v[i] + b);
+          }
+        }
+      }
+    }
+  }
+  if (S > 1) {
+    cluster_sync_all();  // every part is in its CTA's shared memory
+    if (warp >= 2 && ok && n < g.N) {
+      const int a = ntok * part / S, e = ntok * (part + 1) / S;  // the tokens this CTA finishes
+      const float b = g.bias ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g.bias)[n]) : 0.0f;
+      for (int t = a; t < e; ++t) {
+        const uint32_t addr = smem_u32(sums + t * 128 + f);
+        float v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = r < S ? ld_cluster_f32(mapa_shared(addr, r)) : 0.0f;
+        float z = v[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < S) z += v[r];
+        emit(g, t0 + t, n, z + b);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another still reads its sums
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && *abort_flag) set_status(g.status, MOE_ERR_TIMEOUT);
+  if (warp == 2) tmem_dealloc(tmem_base, C::TMEM_COLS);
+}
+
 // ---------------------------------------------------------------- host side
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -334,6 +568,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// launch attributes shared by the kernels of this file: stream order, and clusters of `cluster` CTAs
+struct LaunchCfg {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  LaunchCfg(dim3 grid, int threads, int smem, cudaStream_t st, int cluster) {
+    int n = 0;
+    if (MOE_PDL) {
+      at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+      at[n].id = cudaLaunchAttributeClusterDimension;
+      at[n].val.clusterDim.x = (unsigned)cluster;
+      at[n].val.clusterDim.y = 1;
+      at[n++].val.clusterDim.z = 1;
+    }
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = (unsigned)n;
+  }
+  LaunchCfg(const LaunchCfg&) = delete;
+};
+
 // bf16 [rows, cols], row stride ld elements, box 64 columns x box_rows, 128-byte swizzle
 bool make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
   auto fn = encode_fn();
@@ -347,19 +607,19 @@ bool make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CTAS, int BN>
+template <int CTAS, int BN, bool VEC>
 cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   using C = Cfg<CTAS, BN>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
-  auto kern = k_linear_tc<CTAS, BN>;
+  auto kern = k_linear_tc<CTAS, BN, VEC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   CUtensorMap mA, mB, mY, mP;
   bool ok = g.a_mn ? make_map(&mA, g.A, g.K, g.M, g.lda, kBK) : make_map(&mA, g.A, g.M, g.K, g.lda, 128);
   ok = ok && (g.b_mn ? make_map(&mB, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mB, g.B, g.N, g.K, g.ldb, C::BCOLS));
   mY = mP = mA;  // where unused
-  if (!g.out_f32) ok = ok && make_map(&mY, g.y, g.M, g.N, g.N, 32);
-  if (g.pre) ok = ok && make_map(&mP, g.pre, g.M, g.N, g.N, 32);
+  if (VEC && !g.out_f32) ok = ok && make_map(&mY, g.y, g.M, g.N, g.N, 32);
+  if (VEC && g.pre) ok = ok && make_map(&mP, g.pre, g.M, g.N, g.N, 32);
   if (!ok) return cudaErrorInvalidValue;
   TcArgs a;
   a.g = g;
@@ -367,35 +627,63 @@ cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
   a.nt = (g.N + BN - 1) / BN;
   const int64_t total = (int64_t)a.mt * a.nt;
+  if (total >= (1ll << 30)) return cudaErrorInvalidValue;
+  LaunchCfg l(dim3((unsigned)(CTAS * std::min<int64_t>(total, sms / CTAS))), C::THREADS, C::SMEM, st, CTAS);
+  return cudaLaunchKernelEx(&l.cfg, kern, mA, mB, mY, mP, a);
+}
+
+template <int NB>
+cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
+  using C = SplitCfg<NB>;
+  static_assert(C::SMEM <= 232448, "shared memory budget");
+  if (g.a_mn && NB < 64) return cudaErrorInvalidValue;
+  auto kern = k_linear_split<NB>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mW, mX;
+  bool ok = g.b_mn ? make_map(&mW, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mW, g.B, g.N, g.K, g.ldb, 128);
+  ok = ok && (g.a_mn ? make_map(&mX, g.A, g.K, g.M, g.lda, kBK) : make_map(&mX, g.A, g.M, g.K, g.lda, NB));
+  if (!ok) return cudaErrorInvalidValue;
+  TcArgs a;
+  a.g = g;
+  a.kblocks = (g.K + kBK - 1) / kBK;
+  a.mt = (g.M + NB - 1) / NB;
+  a.nt = (g.N + 127) / 128;
+  const int64_t total = (int64_t)a.mt * a.nt * S;
   if (total >= (1ll << 31)) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[2];
-  int n = 0;
-  if (MOE_PDL) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  LaunchCfg l(dim3((unsigned)total), C::THREADS, C::SMEM, st, S);
+  return cudaLaunchKernelEx(&l.cfg, kern, mW, mX, a, S);
+}
+
+cudaError_t launch_split(const LinearGemm& g, int nb, int S, cudaStream_t st) {
+  switch (nb) {
+    case 16: return launch_split_nb<16>(g, S, st);
+    case 32: return launch_split_nb<32>(g, S, st);
+    case 64: return launch_split_nb<64>(g, S, st);
+    case 128: return launch_split_nb<128>(g, S, st);
+    default: return launch_split_nb<256>(g, S, st);
   }
-  if (CTAS == 2) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = 2;
-    at[n].val.clusterDim.y = 1;
-    at[n++].val.clusterDim.z = 1;
-  }
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  cfg.gridDim = dim3((unsigned)(CTAS * std::min<int64_t>(total, sms / CTAS)));
-  return cudaLaunchKernelEx(&cfg, kern, mA, mB, mY, mP, a);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
+  const int kblocks = (g.K + kBK - 1) / kBK;
   const int64_t t256 = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
-  if (g.M > 128 && t256 * 2 >= sms) return launch_tile<2, 256>(g, sms, st);
-  return launch_tile<1, 128>(g, sms, st);
+  const int64_t t128 = (int64_t)((g.M + 127) / 128) * ((g.N + 127) / 128);
+  const bool vec = g.N % 8 == 0;
+  if (t128 * 2 <= sms || g.M <= 64) {
+    int nb = 16;
+    while (nb < 256 && nb < g.M) nb *= 2;
+    if (g.a_mn && nb < 64) nb = 64;
+    const int64_t tiles = (int64_t)((g.M + nb - 1) / nb) * ((g.N + 127) / 128);
+    const int slots = sms * (nb <= 64 ? 2 : 1);
+    int S = 1;
+    while (S < 8 && 2 * S <= kblocks && tiles * 2 * S <= slots) S *= 2;
+    return launch_split(g, nb, S, st);
+  }
+  if (g.M > 128 && t256 * 2 >= sms) return vec ? launch_tile<2, 256, true>(g, sms, st) : launch_tile<2, 256, false>(g, sms, st);
+  return vec ? launch_tile<1, 128, true>(g, sms, st) : launch_tile<1, 128, false>(g, sms, st);
 }
 
 }  // namespace moe
