@@ -4,11 +4,52 @@
 // the mean of the squared deviations, taken in a second pass over the row (the one-pass
 // form sum(h^2) - mean^2 loses every digit when the mean is large against the spread).
 // Both directions are bound by HBM: each tensor is read or written once.
+#include <algorithm>
+
 #include "block.h"
 #include "common.cuh"
 
 namespace moe {
 namespace {
+
+// VEC consecutive elements as one 16-byte (or, VEC = 1, one-element) access.
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Vec {
+  T v[VEC];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Vec<T, VEC>& a, float (&f)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = io<T>::to_f(a.v[i]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> pack(const float (&f)[VEC]) {
+  Vec<T, VEC> a;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) a.v[i] = io<T>::cvt(f[i]);
+  return a;
+}
+
+// Sums of two values over a group of G threads (a warp, or G / 32 warps that meet at barrier
+// `id`); every thread gets both. `slots` is the group's own, two sets of G / 32 entries used in
+// turn, so one barrier a call is enough. Fixed tree: the same result on every run.
+template <int G>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2* slots, int* turn, int id) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (G > 32) {
+    constexpr int W = G / 32;
+    float2* s = slots + *turn * W;
+    *turn ^= 1;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x % G) >> 5;
+    if (lane == 0) s[w] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(G) : "memory");
+    const float2 v = lane < W ? s[lane] : make_float2(0.0f, 0.0f);
+    a = warp_sum(v.x);
+    b = warp_sum(v.y);
+  }
+  return make_float2(a, b);
+}
 
 // Block-wide sums of two values; every thread gets both (fixed tree: same result each run).
 __device__ __forceinline__ float2 block_sum2(float a, float b) {
@@ -25,9 +66,10 @@ __device__ __forceinline__ float2 block_sum2(float a, float b) {
   return v;
 }
 
-// Block per row, three passes over it.
+// Rows too long for a block's registers (16384 elements; backward 8192 in fp32 or
+// without 16-byte alignment): block per row, three passes over it.
 template <typename T>
-__global__ void __launch_bounds__(256) k_norm_fwd(const T* x, const T* res, const T* w, const T* b, T* y, T* sum,
+__global__ void __launch_bounds__(256) k_norm_fwd_long(const T* x, const T* res, const T* w, const T* b, T* y, T* sum,
                                                   float* mean, float* rstd, int rows, int H, int rms, float eps) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   for (int t = blockIdx.x; t < rows; t += gridDim.x) {
@@ -55,9 +97,9 @@ __global__ void __launch_bounds__(256) k_norm_fwd(const T* x, const T* res, cons
   }
 }
 
-// dx, block per row.
+// dx of such rows, block per row.
 template <typename T>
-__global__ void __launch_bounds__(256) k_norm_dx(const T* dy, const T* dsum, const T* x, const T* w, const float* mean,
+__global__ void __launch_bounds__(256) k_norm_dx_long(const T* dy, const T* dsum, const T* x, const T* w, const float* mean,
                                                  const float* rstd, T* dx, int rows, int H) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   for (int t = blockIdx.x; t < rows; t += gridDim.x) {
@@ -84,7 +126,7 @@ constexpr int kNormChunks = 128;  // row chunks of the weight-gradient partial s
 
 // Partial sums over one chunk of rows: part[c][0][i] = sum dy xh, part[c][1][i] = sum dy.
 template <typename T>
-__global__ void __launch_bounds__(256) k_norm_dw(const T* dy, const T* x, const float* mean, const float* rstd,
+__global__ void __launch_bounds__(256) k_norm_dw_long(const T* dy, const T* x, const float* mean, const float* rstd,
                                                  float* part, int rows, int H, int per) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
@@ -101,28 +143,503 @@ __global__ void __launch_bounds__(256) k_norm_dw(const T* dy, const T* x, const 
   part[((int64_t)blockIdx.y * 2 + 1) * H + i] = ab;
 }
 
-// The chunks' partial sums added in chunk order.
+// The chunks' partial sums added: eight chunk lanes a column, each in chunk order, then the lanes.
 template <typename T>
 __global__ void __launch_bounds__(256) k_norm_dw_sum(const float* part, int chunks, int H, T* dw, T* db) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= H) return;
+  __shared__ float red[2][8][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + cx;
   float aw = 0.0f, ab = 0.0f;
-  for (int c = 0; c < chunks; ++c) {
-    aw += part[((int64_t)c * 2) * H + i];
-    ab += part[((int64_t)c * 2 + 1) * H + i];
+  if (i < H) {
+#pragma unroll 8
+    for (int c = ry; c < chunks; c += 8) {
+      aw += part[((int64_t)c * 2) * H + i];
+      if (db) ab += part[((int64_t)c * 2 + 1) * H + i];
+    }
   }
-  dw[i] = io<T>::cvt(aw);
-  if (db) db[i] = io<T>::cvt(ab);
+  red[0][ry][cx] = aw;
+  red[1][ry][cx] = ab;
+  __syncthreads();
+  if (ry == 0 && i < H) {
+#pragma unroll
+    for (int r = 1; r < 8; ++r) {
+      aw += red[0][r][cx];
+      ab += red[1][r][cx];
+    }
+    dw[i] = io<T>::cvt(aw);
+    if (db) db[i] = io<T>::cvt(ab);
+  }
+}
+
+
+// ---------------------------------------------------------------- rows held in registers
+template <int G>
+constexpr int kFwdThreads = G < 256 ? 256 : G;
+
+struct FwdArgs {
+  const void *x, *res, *w, *b;
+  void *y, *sum;
+  float *mean, *rstd;
+  int rows, H, rms;
+  float eps;
+};
+
+// A group of G threads per row, VPT vectors of VEC elements a thread; every tensor is read or
+// written once, in 16-byte accesses where H allows. The row waits in registers (fp32) for its
+// mean and then its variance. Blocks stay and walk the rows.
+template <typename T, int VEC, int VPT, int G>
+__global__ void __launch_bounds__(kFwdThreads<G>) k_norm_fwd(const FwdArgs a) {
+  using V = Vec<T, VEC>;
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  constexpr int GROUPS = kFwdThreads<G> / G;
+  __shared__ float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 1];
+  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  int turn = 0;
+  const int nv = a.H / VEC;
+  const float inv_h = 1.0f / (float)a.H;
+  const V* w = reinterpret_cast<const V*>(a.w);
+  const V* bias = reinterpret_cast<const V*>(a.b);
+  for (int t = blockIdx.x * GROUPS + grp; t < a.rows; t += gridDim.x * GROUPS) {
+    const int64_t o = (int64_t)t * nv;
+    const V* x = reinterpret_cast<const V*>(a.x) + o;
+    const V* res = reinterpret_cast<const V*>(a.res) + o;
+    float h[VPT][VEC];
+    {
+      V xv[VPT], rv[VPT];
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+        if (j + p * G < nv) xv[p] = x[j + p * G];
+      if (a.res) {
+#pragma unroll
+        for (int p = 0; p < VPT; ++p)
+          if (j + p * G < nv) rv[p] = res[j + p * G];
+      }
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[p][i] = 0.0f;
+        if (j + p * G < nv) {
+          unpack<T, VEC>(xv[p], h[p]);
+          if (a.res) {
+            float r[VEC];
+            unpack<T, VEC>(rv[p], r);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) h[p][i] += r[i];
+          }
+        }
+      }
+    }
+    float mu = 0.0f;
+    if (!a.rms) {
+      float s = 0.0f;
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s += h[p][i];
+      mu = group_sum2<G>(s, 0.0f, slots[grp], &turn, 1 + grp).x * inv_h;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float d = h[p][i] - mu;
+          q = fmaf(d, d, q);
+        }
+    const float rs = 1.0f / sqrtf(group_sum2<G>(q, 0.0f, slots[grp], &turn, 1 + grp).x * inv_h + a.eps);
+    V* y = reinterpret_cast<V*>(a.y) + o;
+    V* sum = reinterpret_cast<V*>(a.sum) + o;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        float wf[VEC], v[VEC];
+        unpack<T, VEC>(w[j + p * G], wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = (h[p][i] - mu) * rs * wf[i];
+        if (bias) {
+          float bf[VEC];
+          unpack<T, VEC>(bias[j + p * G], bf);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[i] += bf[i];
+        }
+        if (a.sum) sum[j + p * G] = pack<T, VEC>(h[p]);
+        y[j + p * G] = pack<T, VEC>(v);
+      }
+    if (j == 0) {
+      if (a.mean) a.mean[t] = mu;
+      if (a.rstd) a.rstd[t] = rs;
+    }
+  }
+}
+
+struct BwdArgs {
+  const void *dy, *dsum, *x, *w;
+  const float *mean, *rstd;
+  void* dx;
+  float* part;
+  int rows, H, dbias;
+};
+
+// The groups' column sums are added in order through shared memory ([element][thread], free of bank
+// conflicts) and written as one row of partial sums a block.
+template <int VEC, int VPT, int G>
+__device__ __forceinline__ void write_part(const BwdArgs& a, float (&aw)[VPT][VEC], float (&ab)[VPT][VEC],
+                                           float* smem) {
+  constexpr int GROUPS = 512 / G, COLS = G * VPT * VEC;
+  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  for (int k = 1; k < GROUPS; ++k) {  // group 0 collects the others', one group at a time
+    __syncthreads();
+    if (grp == k) {
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          smem[(p * VEC + i) * G + j] = aw[p][i];
+          smem[COLS + (p * VEC + i) * G + j] = ab[p][i];
+        }
+    }
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          aw[p][i] += smem[(p * VEC + i) * G + j];
+          ab[p][i] += smem[COLS + (p * VEC + i) * G + j];
+        }
+    }
+  }
+  if (grp == 0) {
+    Vec<float, VEC>* pw = reinterpret_cast<Vec<float, VEC>*>(a.part + (int64_t)blockIdx.x * 2 * a.H);
+    Vec<float, VEC>* pb = reinterpret_cast<Vec<float, VEC>*>(a.part + ((int64_t)blockIdx.x * 2 + 1) * a.H);
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < a.H / VEC) {
+        pw[j + p * G] = pack<float, VEC>(aw[p]);
+        if (a.dbias) pb[j + p * G] = pack<float, VEC>(ab[p]);
+      }
+  }
+}
+
+// One pass over dy, x (and dsum): dx, and the block's share of the weight gradients. A group of G
+// threads per row; a thread keeps its columns for every row, so dweight and dbias add up in its
+// registers. Rows come through a ring of STAGES slots in shared memory filled by 16-byte
+// asynchronous copies. A thread copies exactly the vectors it reads, so the ring needs no barrier,
+// the loads run a row or more ahead of the sums, and the values can be read again after the row's
+// sums instead of being held in registers.
+template <typename T, int VPT, int G, int STAGES>
+__global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
+  constexpr int VEC = 16 / sizeof(T);
+  using V = Vec<T, VEC>;
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  constexpr int GROUPS = 512 / G;
+  __shared__ float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 1];
+  extern __shared__ __align__(16) uint8_t ring[];  // [STAGES][3 tensors][VPT][512 threads] vectors
+  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  int turn = 0;
+  const int nv = a.H / VEC;
+  const float inv_h = 1.0f / (float)a.H;
+  const V* dy = reinterpret_cast<const V*>(a.dy);
+  const V* ds = reinterpret_cast<const V*>(a.dsum);
+  const V* x = reinterpret_cast<const V*>(a.x);
+  V* dx = reinterpret_cast<V*>(a.dx);
+  V wv[VPT];
+  float aw[VPT][VEC], ab[VPT][VEC];
+#pragma unroll
+  for (int p = 0; p < VPT; ++p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) aw[p][i] = ab[p][i] = 0.0f;
+    if (j + p * G < nv) wv[p] = reinterpret_cast<const V*>(a.w)[j + p * G];
+  }
+  const uint32_t base = smem_u32(ring) + threadIdx.x * 16;
+  auto slot = [&](int st, int tensor, int p) { return base + (uint32_t)(((st * 3 + tensor) * VPT + p) * 512 * 16); };
+  auto fetch = [&](int t, int st) {
+    if (t < a.rows) {
+      const int64_t o = (int64_t)t * nv + j;
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+        if (j + p * G < nv) {
+          cp_async16(slot(st, 0, p), dy + o + p * G);
+          cp_async16(slot(st, 1, p), x + o + p * G);
+          if (ds) cp_async16(slot(st, 2, p), ds + o + p * G);
+        }
+    }
+    cp_async_commit();
+  };
+  auto read = [&](int st, int tensor, int p, float (&f)[VEC]) {
+    const uint4 u = ld_shared_v4(slot(st, tensor, p));
+    unpack<T, VEC>(*reinterpret_cast<const V*>(&u), f);
+  };
+  const int step = gridDim.x * GROUPS;
+  int t = blockIdx.x * GROUPS + grp;
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
+  int st = 0;
+  float nmu = 0.0f, nrs = 0.0f;  // the next row's statistics
+  auto stats = [&](int r) {
+    if (r < a.rows) {
+      nmu = a.mean ? a.mean[r] : 0.0f;
+      nrs = a.rstd[r];
+    }
+  };
+  stats(t);
+  for (; t < a.rows; t += step) {
+    const float rs = nrs, off = -nmu * nrs;  // xh = x rs + off
+    stats(t + step);
+    cp_async_wait<STAGES - 1>();
+    float s = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        float d[VEC], xv[VEC], wf[VEC];
+        read(st, 0, p, d);
+        read(st, 1, p, xv);
+        unpack<T, VEC>(wv[p], wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float xh = fmaf(xv[i], rs, off);
+          aw[p][i] = fmaf(d[i], xh, aw[p][i]);
+          ab[p][i] += d[i];
+          const float g = d[i] * wf[i];
+          s += g;
+          q = fmaf(g, xh, q);
+        }
+      }
+    const float2 r = group_sum2<G>(s, q, slots[grp], &turn, 1 + grp);
+    // dx = rs g - rs (mean g) - xh rs (mean g xh)
+    const float ms = a.mean ? rs * r.x * inv_h : 0.0f, mq = rs * r.y * inv_h;
+    V* o = dx + (int64_t)t * nv + j;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        float d[VEC], xv[VEC], wf[VEC];
+        read(st, 0, p, d);
+        read(st, 1, p, xv);
+        unpack<T, VEC>(wv[p], wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float xh = fmaf(xv[i], rs, off);
+          d[i] = fmaf(-xh, mq, fmaf(d[i] * wf[i], rs, -ms));
+        }
+        if (ds) {
+          read(st, 2, p, xv);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) d[i] += xv[i];
+        }
+        o[p * G] = pack<T, VEC>(d);
+      }
+    fetch(t + STAGES * step, st);
+    st = st + 1 == STAGES ? 0 : st + 1;
+  }
+  cp_async_wait<0>();
+  write_part<VEC, VPT, G>(a, aw, ab, reinterpret_cast<float*>(ring));
+}
+
+// The same for rows without 16-byte alignment, element by element: the next row's loads travel in
+// registers while this row's sums meet.
+template <typename T, int VPT, int G>
+__global__ void __launch_bounds__(512) k_norm_bwd_odd(const BwdArgs a) {
+  constexpr int VEC = 1;
+  using V = Vec<T, VEC>;
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  constexpr int GROUPS = 512 / G;
+  __shared__ float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 1];
+  extern __shared__ float acc_smem[];  // [2][columns of a group], only with several groups
+  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  int turn = 0;
+  const int nv = a.H / VEC;
+  const float inv_h = 1.0f / (float)a.H;
+  const V* dy = reinterpret_cast<const V*>(a.dy);
+  const V* ds = reinterpret_cast<const V*>(a.dsum);
+  const V* x = reinterpret_cast<const V*>(a.x);
+  V* dx = reinterpret_cast<V*>(a.dx);
+  V wv[VPT];
+  float aw[VPT][VEC], ab[VPT][VEC];
+#pragma unroll
+  for (int p = 0; p < VPT; ++p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) aw[p][i] = ab[p][i] = 0.0f;
+    if (j + p * G < nv) wv[p] = reinterpret_cast<const V*>(a.w)[j + p * G];
+  }
+  V ndy[VPT], nx[VPT], nds[VPT];
+  float nmu = 0.0f, nrs = 0.0f;
+  auto fetch = [&](int t) {
+    if (t >= a.rows) return;
+    const int64_t o = (int64_t)t * nv;
+    nmu = a.mean ? a.mean[t] : 0.0f;
+    nrs = a.rstd[t];
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        ndy[p] = dy[o + j + p * G];
+        nx[p] = x[o + j + p * G];
+        if (ds) nds[p] = ds[o + j + p * G];
+      }
+  };
+  const int step = gridDim.x * GROUPS;
+  fetch(blockIdx.x * GROUPS + grp);
+  for (int t = blockIdx.x * GROUPS + grp; t < a.rows; t += step) {
+    const float mu = nmu, rs = nrs;
+    V cdy[VPT], cx[VPT], cds[VPT];
+    float s = 0.0f, q = 0.0f;
+    // g = dy w and xh of one vector, from the values as loaded (kept that way: they are converted
+    // again after the sums, which costs less than the registers of their fp32 forms)
+    auto expand = [&](int p, float (&d)[VEC], float (&xh)[VEC], float (&wf)[VEC]) {
+      unpack<T, VEC>(cdy[p], d);
+      unpack<T, VEC>(cx[p], xh);
+      unpack<T, VEC>(wv[p], wf);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) xh[i] = (xh[i] - mu) * rs;
+    };
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      if (j + p * G < nv) {
+        cdy[p] = ndy[p];
+        cx[p] = nx[p];
+        if (ds) cds[p] = nds[p];
+        float d[VEC], xh[VEC], wf[VEC];
+        expand(p, d, xh, wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          aw[p][i] = fmaf(d[i], xh[i], aw[p][i]);
+          ab[p][i] += d[i];
+          const float g = d[i] * wf[i];
+          s += g;
+          q = fmaf(g, xh[i], q);
+        }
+      }
+    }
+    fetch(t + step);
+    const float2 r = group_sum2<G>(s, q, slots[grp], &turn, 1 + grp);
+    const float ms = a.mean ? r.x * inv_h : 0.0f, mq = r.y * inv_h;
+    const int64_t o = (int64_t)t * nv;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        float d[VEC], xh[VEC], wf[VEC], v[VEC];
+        expand(p, d, xh, wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = rs * (d[i] * wf[i] - ms - xh[i] * mq);
+        if (ds) {
+          unpack<T, VEC>(cds[p], d);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[i] += d[i];
+        }
+        dx[o + j + p * G] = pack<T, VEC>(v);
+      }
+  }
+  write_part<VEC, VPT, G>(a, aw, ab, acc_smem);
+}
+
+// ---------------------------------------------------------------- choice of the variant
+constexpr int kMaxParts = 512;  // rows of partial sums the workspace holds
+
+// Blocks of a persistent kernel: as many as fit on the GPU at once, or as the rows need.
+template <typename K>
+int resident_blocks(K kern, int threads, size_t smem, int64_t need, int sms, int cap) {
+  int per = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem) != cudaSuccess || per < 1) per = 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({need, (int64_t)per * sms, (int64_t)cap}));
+}
+
+template <typename T, int VEC, int VPT, int G>
+cudaError_t fwd_regs(const FwdArgs& a, int sms, cudaStream_t st) {
+  constexpr int threads = kFwdThreads<G>, groups = threads / G;
+  auto kern = k_norm_fwd<T, VEC, VPT, G>;
+  const int grid = resident_blocks(kern, threads, 0, ((int64_t)a.rows + groups - 1) / groups, sms, 1 << 30);
+  MOE_LAUNCH(kern, grid, threads, 0, st, a);
+  return cudaSuccess;
+}
+
+// Thirty-two elements a thread at most (they stay in registers) and the smallest group that covers
+// the row. With few rows the latency of one row counts instead: the whole block takes the row,
+// eight elements a thread where that covers it.
+template <typename T, int VEC>
+cudaError_t fwd_vec(const FwdArgs& a, int sms, cudaStream_t st, bool* taken) {
+  constexpr int P = 8 / VEC;  // vectors of eight elements
+  const int h = a.H;
+  *taken = true;
+  if (h <= 256) return fwd_regs<T, VEC, P, 32>(a, sms, st);
+  if (a.rows < sms * 2) {
+    if (h <= 2048) return fwd_regs<T, VEC, P, 256>(a, sms, st);
+    if (h <= 4096) return fwd_regs<T, VEC, P, 512>(a, sms, st);
+  }
+  if (h <= 512) return fwd_regs<T, VEC, 2 * P, 32>(a, sms, st);
+  if (h <= 1024) return fwd_regs<T, VEC, 4 * P, 32>(a, sms, st);
+  if (h <= 2048) return fwd_regs<T, VEC, 2 * P, 128>(a, sms, st);
+  if (h <= 4096) return fwd_regs<T, VEC, 4 * P, 128>(a, sms, st);
+  if (h <= 8192) return fwd_regs<T, VEC, 2 * P, 512>(a, sms, st);
+  if (h <= 16384) return fwd_regs<T, VEC, 4 * P, 512>(a, sms, st);
+  *taken = false;
+  return cudaSuccess;
 }
 
 template <typename T>
 cudaError_t fwd(const moe_norm_dims& d, const void* x, const void* res, const void* w, const void* b, void* y,
                 void* sum, float* mean, float* rstd, int sms, cudaStream_t st, int* launches) {
-  const int grid = (int)(d.T < (int64_t)sms * 8 ? d.T : (int64_t)sms * 8);
+  FwdArgs a = {x, res, w, b, y, sum, mean, rstd, (int)d.T, (int)d.H, d.kind == MOE_NORM_RMS, d.eps};
   *launches += 1;
-  MOE_LAUNCH(k_norm_fwd<T>, grid, 256, 0, st, (const T*)x, (const T*)res, (const T*)w, (const T*)b, (T*)y, (T*)sum,
-             mean, rstd, (int)d.T, (int)d.H, d.kind == MOE_NORM_RMS ? 1 : 0, d.eps);
+  constexpr int V = 16 / sizeof(T);
+  bool taken;
+  const cudaError_t e = d.H % V ? fwd_vec<T, 1>(a, sms, st, &taken) : fwd_vec<T, V>(a, sms, st, &taken);
+  if (taken) return e;
+  const int grid = (int)std::min<int64_t>(d.T, (int64_t)sms * 8);
+  MOE_LAUNCH(k_norm_fwd_long<T>, grid, 256, 0, st, (const T*)x, (const T*)res, (const T*)w, (const T*)b, (T*)y,
+             (T*)sum, mean, rstd, a.rows, a.H, a.rms, a.eps);
+  return cudaSuccess;
+}
+
+template <typename T, int EPT, int G>
+cudaError_t bwd_ring(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
+  constexpr int VPT = EPT * (int)sizeof(T) / 16, stage = 3 * VPT * 512 * 16, groups = 512 / G;
+  constexpr int stages = 196608 / stage < 4 ? 196608 / stage : 4;
+  static_assert(stages >= 2 && stages * stage >= (int)sizeof(float) * 2 * G * EPT, "ring too small");
+  auto kern = k_norm_bwd_ring<T, VPT, G, stages>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, stages * stage);
+  if (e != cudaSuccess) return e;
+  *chunks = resident_blocks(kern, 512, stages * stage, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  MOE_LAUNCH(kern, *chunks, 512, stages * stage, st, a);
+  return cudaSuccess;
+}
+
+template <typename T, int VPT, int G>
+cudaError_t bwd_odd(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
+  constexpr int groups = 512 / G;
+  constexpr size_t smem = groups > 1 ? sizeof(float) * 2 * G * VPT : 0;
+  auto kern = k_norm_bwd_odd<T, VPT, G>;
+  *chunks = resident_blocks(kern, 512, smem, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  MOE_LAUNCH(kern, *chunks, 512, smem, st, a);
+  return cudaSuccess;
+}
+
+// The smallest group that covers the row with the columns a thread can keep sums for: 32 elements
+// in bf16, 16 in fp32 and in rows without 16-byte alignment. chunks stays 0 for longer rows.
+template <typename T>
+cudaError_t bwd_regs(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
+  const int h = a.H;
+  *chunks = 0;
+  if (h % (16 / (int)sizeof(T))) {
+    if (h <= 256) return bwd_odd<T, 8, 32>(a, sms, st, chunks);
+    if (h <= 1024) return bwd_odd<T, 8, 128>(a, sms, st, chunks);
+    if (h <= 4096) return bwd_odd<T, 8, 512>(a, sms, st, chunks);
+    if (h <= 8192) return bwd_odd<T, 16, 512>(a, sms, st, chunks);
+    return cudaSuccess;
+  }
+  if (h <= 256) return bwd_ring<T, 8, 32>(a, sms, st, chunks);
+  if (h <= 512) return bwd_ring<T, 16, 32>(a, sms, st, chunks);
+  if constexpr (sizeof(T) == 2) {
+    if (h <= 1024) return bwd_ring<T, 32, 32>(a, sms, st, chunks);
+    if (h <= 2048) return bwd_ring<T, 16, 128>(a, sms, st, chunks);
+    if (h <= 4096) return bwd_ring<T, 32, 128>(a, sms, st, chunks);
+    if (h <= 8192) return bwd_ring<T, 32, 256>(a, sms, st, chunks);
+    if (h <= 16384) return bwd_ring<T, 32, 512>(a, sms, st, chunks);
+  } else {
+    if (h <= 2048) return bwd_ring<T, 16, 128>(a, sms, st, chunks);
+    if (h <= 4096) return bwd_ring<T, 16, 256>(a, sms, st, chunks);
+    if (h <= 8192) return bwd_ring<T, 16, 512>(a, sms, st, chunks);
+  }
   return cudaSuccess;
 }
 
@@ -132,23 +649,35 @@ cudaError_t bwd(const moe_norm_dims& d, void* ws, const void* dy, const void* ds
                 int* launches) {
   float* part = static_cast<float*>(ws);
   const int rows = (int)d.T, H = (int)d.H;
+  const BwdArgs a = {dy, dsum, x, w, mean, rstd, dx, part, rows, H, db != nullptr};
+  int chunks;
+  cudaError_t e = bwd_regs<T>(a, sms, st, &chunks);
+  if (e != cudaSuccess) return e;
+  const int cb = (H + 31) / 32;
+  if (chunks) {
+    *launches += 2;
+    MOE_LAUNCH(k_norm_dw_sum<T>, cb, 256, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);
+    return cudaSuccess;
+  }
   const int per = (rows + kNormChunks - 1) / kNormChunks;
-  const int chunks = (rows + per - 1) / per;
-  const int cb = (H + 255) / 256;
-  *launches += 1;  // before dx, which may be written over dy
-  MOE_LAUNCH(k_norm_dw<T>, dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)x, mean, rstd, part, rows, H, per);
-  *launches += 1;
+  chunks = (rows + per - 1) / per;
+  *launches += 3;  // the weight gradients before dx, which may be written over dy
+  MOE_LAUNCH(k_norm_dw_long<T>, dim3((H + 255) / 256, chunks), 256, 0, st, (const T*)dy, (const T*)x, mean, rstd, part,
+             rows, H, per);
   MOE_LAUNCH(k_norm_dw_sum<T>, cb, 256, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);
-  *launches += 1;
-  const int grid = (int)(d.T < (int64_t)sms * 8 ? d.T : (int64_t)sms * 8);
-  MOE_LAUNCH(k_norm_dx<T>, grid, 256, 0, st, (const T*)dy, (const T*)dsum, (const T*)x, (const T*)w, mean, rstd,
+  const int grid = (int)std::min<int64_t>(d.T, (int64_t)sms * 8);
+  MOE_LAUNCH(k_norm_dx_long<T>, grid, 256, 0, st, (const T*)dy, (const T*)dsum, (const T*)x, (const T*)w, mean, rstd,
              (T*)dx, rows, H);
   return cudaSuccess;
 }
 
 }  // namespace
 
-size_t norm_workspace_bytes(const moe_norm_dims& d) { return (size_t)kNormChunks * 2 * d.H * sizeof(float); }
+size_t norm_workspace_bytes(const moe_norm_dims& d) {
+  // rows of partial sums: one a block (at least one row each), or the row chunks of the long rows
+  const int64_t parts = std::min<int64_t>(d.T, kMaxParts);
+  return (size_t)(parts * 2 * d.H) * sizeof(float) + 256;
+}
 
 cudaError_t launch_norm_fwd(const moe_norm_dims& d, const void* x, const void* residual, const void* weight,
                             const void* bias, void* y, void* sum, float* mean, float* rstd, int sms, cudaStream_t st,
