@@ -1,15 +1,19 @@
 // gate.cu -- routing from router logits, forward and backward.
 //
-// A warp per token; lane l holds the experts e = l + 32 i (i < EPL) in registers. A choice
-// score becomes an order-preserving 32-bit key, so the largest score of the warp is one
-// integer reduction and, among equal scores, the lowest expert another: ties need no care
-// and a token's selection is the same on every run. Key 1 is a masked expert (logit -inf or
-// NaN, or a choice score that is -inf or NaN), key 0 one that cannot be chosen (already
-// taken, in a group that was not kept, or past E).
+// A warp per token. The experts of a group lie on L = 2^n consecutive lanes, R consecutive
+// experts a lane, so everything a group needs is a butterfly over its lanes and the lowest lane
+// with a value holds the lowest expert with it. A choice score becomes an order-preserving
+// 32-bit key: the largest of the warp is one integer reduction, and ties fall to the lower expert
+// by the lane order. Key 1 is a masked expert (logit -inf or NaN, or a choice score that is -inf
+// or NaN), key 0 one that cannot be chosen (taken, in a group that was not kept, or absent).
 //
-// The softmax sums run over a fixed tree: lane l adds its experts by halves (i with
-// i + EPL/2), then the lanes by butterflies, i.e. element j of the padded row with element
-// j + n/2 at each step.
+// Without a bias the scores are ordered as the logits are, so the logits themselves are compared
+// and only the chosen experts' scores are computed; a group's sum of two scores and a bias need
+// every score. The kernels are bound by latency: the logits are read once (T = 8192, E = 256 is
+// 8.4 MB, 1.2 us of HBM time), the rest is a chain of k warp reductions.
+#include <algorithm>
+#include <type_traits>
+
 #include "block.h"
 #include "common.cuh"
 
@@ -17,12 +21,17 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kKeyNone = 0, kKeyMasked = 1;
+template <int EPL>
+constexpr int one_block_tokens = EPL <= 4 ? 32 : EPL <= 16 ? 16 : 8;  // tokens one block may take by itself
 
 __device__ __forceinline__ uint32_t order_key(float c) {
   const uint32_t u = __float_as_uint(c + 0.0f);  // -0 and +0 are one value
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-constexpr uint32_t kKeyNone = 0, kKeyMasked = 1;
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
 
 struct GateArgs {
   const void* logits;
@@ -34,153 +43,184 @@ struct GateArgs {
   const float* dw;
   void* dlogits;
   int T, E, k, G, Kg, take, renorm;
+  int per;     // experts of a group
+  int L, R;    // lanes of a group, experts of a lane
+  int vec;     // the lanes' experts can be read (and written) 16 bytes at a time
+  int direct;  // the logits decide the order
   float scale;
 };
 
-// Scores of one token: s[i] for expert lane + 32 i (0 where masked or past E).
-template <int EPL, bool SOFTMAX, typename TL>
-__device__ __forceinline__ void scores(const TL* row, int E, int lane, float (&l)[EPL], float (&s)[EPL]) {
+// The lane's n logits (of at most EPL) at p; NaN masks its expert as -inf does.
+template <int EPL, typename TL>
+__device__ __forceinline__ void load_logits(const TL* p, int n, bool vec, float (&l)[EPL]) {
+  constexpr int V = 16 / (int)sizeof(TL);
+  if constexpr (EPL % V == 0) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += V) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < n) u = *reinterpret_cast<const uint4*>(p + i);
+        const TL* e = reinterpret_cast<const TL*>(&u);
+#pragma unroll
+        for (int q = 0; q < V; ++q) l[i + q] = i < n ? io<TL>::to_f(e[q]) : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] = l[i] != l[i] ? -INFINITY : l[i];
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    const float v = e < E ? io<TL>::to_f(row[e]) : -INFINITY;
-    l[i] = v != v ? -INFINITY : v;  // NaN masks its expert as -inf does
-  }
-  if constexpr (SOFTMAX) {
-    float m = l[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    // l == m covers +inf (where l - m is NaN); a row without any expert left has m = -inf
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = l[i] == -INFINITY ? 0.0f : (l[i] == m ? 1.0f : expf(l[i] - m));
-    float t[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) t[i] = s[i];
-#pragma unroll
-    for (int h = EPL / 2; h > 0; h >>= 1)
-#pragma unroll
-      for (int i = 0; i < h; ++i) t[i] += t[i + h];
-    const float z = warp_sum(t[0]);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = z > 0.0f ? s[i] / z : 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s[i] = l[i] == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-l[i]));
+    const float v = i < n ? io<TL>::to_f(p[i]) : -INFINITY;
+    l[i] = v != v ? -INFINITY : v;
   }
 }
 
-// Largest key of the warp and the lowest expert that has it; the owner's copy is cleared.
+// e^{l - m} of a softmax with maximum m: 0 for masked experts, 1 at the maximum (which may be +inf)
+__device__ __forceinline__ float soft(float l, float m) {
+  return l == -INFINITY ? 0.0f : (l == m ? 1.0f : expf(l - m));
+}
+__device__ __forceinline__ float logistic(float l) { return l == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-l)); }
+
+// Maximum over the warp (one reduction of order-preserving keys).
+__device__ __forceinline__ float warp_max(float v) { return key_value(__reduce_max_sync(kFull, order_key(v))); }
+
+// Maximum and sum of e^{l - m} over a token's logits.
 template <int EPL>
-__device__ __forceinline__ int take_best(uint32_t (&key)[EPL], int lane, uint32_t* best) {
-  uint32_t b = key[0];
-  int be = lane;
+__device__ __forceinline__ void soft_stats(const float (&l)[EPL], float* m, float* z) {
+  float v = l[0];
 #pragma unroll
-  for (int i = 1; i < EPL; ++i)
-    if (key[i] > b) {
-      b = key[i];
-      be = lane + 32 * i;
-    }
-  const uint32_t m = __reduce_max_sync(kFull, b);
-  const uint32_t e = __reduce_min_sync(kFull, b == m ? (uint32_t)be : 0xffffffffu);
+  for (int i = 1; i < EPL; ++i) v = fmaxf(v, l[i]);
+  *m = warp_max(v);
+  float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    if ((int)e == lane + 32 * i) key[i] = kKeyNone;
-  *best = m;
-  return (int)e;
+  for (int i = 0; i < EPL; ++i) s += soft(l[i], *m);
+  *z = warp_sum(s);
 }
 
 template <int EPL, bool SOFTMAX, typename TL>
-__global__ void __launch_bounds__(256) k_gate_fwd(const GateArgs a) {
+__global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const GateArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ int hist[1024];  // one block only: the counts, written without an atomic on global memory
+  const bool one = gridDim.x == 1 && a.count;
+  if (one) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  float l[EPL], s[EPL];
-  scores<EPL, SOFTMAX>(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E, a.E, lane, l, s);
-  uint32_t key[EPL];
-  float c[EPL];
+  if (t < a.T) {
+    const int grp = lane / a.L;
+    const int e0 = grp * a.per + (lane & (a.L - 1)) * a.R;  // this lane's first expert
+    const int n = grp < a.G ? max(0, min(a.R, (grp + 1) * a.per - e0)) : 0;
+    const TL* row = reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E;
+    uint32_t key[EPL];
+    float m = 0.0f, z = 1.0f;
+    {
+      float l[EPL];
+      load_logits<EPL, TL>(row + e0, n, a.vec, l);
+      if (SOFTMAX && (!a.direct || !a.renorm)) soft_stats<EPL>(l, &m, &z);
+      if (a.direct) {
+        if constexpr (SOFTMAX) {  // beside a +inf logit every other score is zero, and they tie
+          bool inf = false;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    c[i] = s[i] + (a.bias && e < a.E ? a.bias[e] : 0.0f);
-    const bool masked = l[i] == -INFINITY || !(c[i] > -INFINITY);
-    key[i] = e >= a.E ? kKeyNone : masked ? kKeyMasked : order_key(c[i]);
-  }
-  if (a.Kg < a.G) {
-    const int per = a.E / a.G;
-    // lane g keeps group g's score
-    uint32_t gkey = lane < a.G ? kKeyMasked : kKeyNone;
-    for (int g = 0; g < a.G; ++g) {
-      uint32_t gk[EPL];
+          for (int i = 0; i < EPL; ++i) inf |= l[i] == INFINITY;
+          if (__any_sync(kFull, inf)) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (l[i] > -INFINITY) l[i] = l[i] == INFINITY ? 1.0f : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = i >= n ? kKeyNone : l[i] == -INFINITY ? kKeyMasked : order_key(l[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const float s = SOFTMAX ? (z > 0.0f ? soft(l[i], m) / z : 0.0f) : logistic(l[i]);
+          const float c = s + (a.bias && i < n ? a.bias[e0 + i] : 0.0f);
+          key[i] = i >= n ? kKeyNone : (l[i] == -INFINITY || !(c > -INFINITY)) ? kKeyMasked : order_key(c);
+        }
+      }
+    }
+    if (a.Kg < a.G) {
+      uint32_t m1 = kKeyNone, m2 = kKeyNone;  // the group's two largest
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 32 * i;
-        gk[i] = e >= g * per && e < (g + 1) * per ? key[i] : kKeyNone;
+        m2 = max(m2, min(m1, key[i]));
+        m1 = max(m1, key[i]);
       }
-      float score = 0.0f;
-      bool any = false;
-      for (int r = 0; r < a.take; ++r) {
-        uint32_t b;
-        const int e = take_best<EPL>(gk, lane, &b);
-        if (b <= kKeyMasked) break;
-        float ce = 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if ((e >> 5) == i) ce = c[i];
-        ce = __shfl_sync(kFull, ce, e & 31);
-        score = any ? score + ce : ce;
-        any = true;
+      for (int o = 1; o < a.L; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+        m2 = max(max(m2, o2), min(m1, o1));
+        m1 = max(m1, o1);
       }
-      if (lane == g && any) gkey = order_key(score);
-    }
-    uint32_t kept = 0;
-    uint32_t gk1[1] = {gkey};
-    for (int r = 0; r < a.Kg; ++r) {
-      uint32_t b;
-      kept |= 1u << take_best<1>(gk1, lane, &b);
-    }
+      uint32_t gk = m1;
+      if (a.take == 2 && m2 > kKeyMasked) gk = order_key(key_value(m1) + key_value(m2));
+      int rank = 0;  // groups in front of this one
+      for (int g = 0; g < a.G; ++g) {
+        const uint32_t o = __shfl_sync(kFull, gk, g * a.L);
+        rank += o > gk || (o == gk && g < grp);
+      }
+      if (rank >= a.Kg) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 32 * i;
-      if (e < a.E && !((kept >> (e / per)) & 1u)) key[i] = kKeyNone;
+        for (int i = 0; i < EPL; ++i) key[i] = kKeyNone;
+      }
+    }
+    uint32_t best = key[0];  // this lane's largest key, the first expert that has it
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        bi = i;
+      }
+    int my_e = 0;
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
+      const int e = __shfl_sync(kFull, e0 + bi, who);
+      if (lane == j) my_e = e;
+      if (lane == who) {
+        uint32_t b = kKeyNone;
+        int nb = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (i == bi) key[i] = kKeyNone;
+          if (key[i] > b) {
+            b = key[i];
+            nb = i;
+          }
+        }
+        best = b;
+        bi = nb;
+      }
+    }
+    // weights: lane j reads its chosen logit again (a line that is still in L1)
+    float lj = lane < a.k ? io<TL>::to_f(row[my_e]) : -INFINITY;
+    if (lj != lj) lj = -INFINITY;
+    float s;
+    if (SOFTMAX) {
+      // s / S over the chosen is the softmax of the chosen logits: it cannot become 0 / 0
+      if (a.renorm) m = warp_max(lj);
+      s = soft(lj, m);
+      if (!a.renorm) s = z > 0.0f ? s / z : 0.0f;
+    } else {
+      s = logistic(lj);
+    }
+    if (a.renorm) {
+      const float S = warp_sum(s);
+      s = S > 0.0f ? s / S : 0.0f;
+    }
+    if (lane < a.k) {
+      a.idx[(int64_t)t * a.k + lane] = my_e;
+      a.w[(int64_t)t * a.k + lane] = s * a.scale;
+      // whole numbers: the order of the additions does not matter
+      if (a.count) atomicAdd(one ? &hist[my_e] : a.count + my_e, 1);
     }
   }
-  int my_e = 0;
-  float my_s = 0.0f, my_l = -INFINITY;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t b;
-    const int e = take_best<EPL>(key, lane, &b);
-    float se = 0.0f, le = 0.0f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if ((e >> 5) == i) {
-        se = s[i];
-        le = l[i];
-      }
-    se = __shfl_sync(kFull, se, e & 31);
-    le = __shfl_sync(kFull, le, e & 31);
-    if (lane == j) {
-      my_e = e;
-      my_s = se;
-      my_l = le;
-    }
-  }
-  if (a.renorm) {
-    if constexpr (SOFTMAX) {  // s / S over the chosen is the softmax of the chosen logits: it cannot underflow to 0 / 0
-      float m = my_l;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      my_s = my_l == -INFINITY ? 0.0f : (my_l == m ? 1.0f : expf(my_l - m));
-    }
-    const float S = warp_sum(my_s);
-    my_s = S > 0.0f ? my_s / S : 0.0f;
-  }
-  if (lane < a.k) {
-    a.idx[(int64_t)t * a.k + lane] = my_e;
-    a.w[(int64_t)t * a.k + lane] = my_s * a.scale;
-    if (a.count) atomicAdd(a.count + my_e, 1);  // whole numbers: the order of the additions does not matter
+  if (one) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.count[e] = hist[e];
   }
 }
 
@@ -190,71 +230,77 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
-  float l[EPL], s[EPL], ds[EPL];
-  scores<EPL, SOFTMAX>(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E, a.E, lane, l, s);
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) ds[i] = 0.0f;
+  const int e0 = lane * a.R, n = max(0, min(a.R, a.E - e0));
+  const TL* row = reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E;
+  // slot j in lane j; a skipped or masked slot takes no part
   int my_e = -1;
-  float my_dw = 0.0f;
+  float dw = 0.0f;
   if (lane < a.k) {
     my_e = a.idx_in[(int64_t)t * a.k + lane];
-    my_dw = a.dw[(int64_t)t * a.k + lane] * a.scale;
+    dw = a.dw[(int64_t)t * a.k + lane] * a.scale;
     if (my_e < 0 || my_e >= a.E) my_e = -1;
   }
-  // the chosen score (and logit) in its slot's lane
-  float my_s = 0.0f, my_l = -INFINITY;
+  const bool dense = SOFTMAX && !a.renorm;
+  float l[EPL], m = 0.0f, z = 1.0f;
+  if (dense) {
+    load_logits<EPL, TL>(row + e0, n, a.vec, l);
+    soft_stats<EPL>(l, &m, &z);
+  }
+  float lj = my_e >= 0 ? io<TL>::to_f(row[my_e]) : -INFINITY;
+  if (lj != lj) lj = -INFINITY;
+  if (lj == -INFINITY) dw = 0.0f;
+  float d;          // what slot j adds to its expert's gradient
+  float dot = 0.0f; // dense: sum of ds s over the chosen
+  if (dense) {
+    d = dw;
+    dot = warp_sum(dw * (z > 0.0f ? soft(lj, m) / z : 0.0f));
+  } else if (SOFTMAX) {
+    // the weights are the softmax of the chosen logits: dl_j = w_j (dw_j - sum_i w_i dw_i)
+    const float s = soft(lj, warp_max(lj));
+    const float S = warp_sum(s);
+    const float w = S > 0.0f ? s / S : 0.0f;
+    d = w * (dw - warp_sum(w * dw));
+  } else {
+    const float s = logistic(lj);
+    if (a.renorm) {
+      const float S = warp_sum(s), q = warp_sum(dw * s);
+      dw = S > 0.0f ? (dw - q / S) / S : 0.0f;
+    }
+    d = dw * s * (1.0f - s);
+  }
+  float out[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kFull, my_e, j);
-    if (e < 0) continue;
-    float se = 0.0f, le = 0.0f;
+    const int e = __shfl_sync(kFull, my_e, j) - e0;  // < 0 or >= R where another lane has it (or none)
+    const float dj = __shfl_sync(kFull, d, j);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if ((e >> 5) == i) {
-        se = s[i];
-        le = l[i];
-      }
-    se = __shfl_sync(kFull, se, e & 31);
-    le = __shfl_sync(kFull, le, e & 31);
-    if (lane == j) {
-      my_s = se;
-      my_l = le;
+      if (e == i && i < n) out[i] += dj;
+  }
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) out[i] = z > 0.0f ? soft(l[i], m) / z * (out[i] - dot) : 0.0f;
+  }
+  TG* o = reinterpret_cast<TG*>(a.dlogits) + (int64_t)t * a.E + e0;
+  constexpr int V = 16 / (int)sizeof(TG);
+  if constexpr (EPL % V == 0) {
+    if (a.vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += V)
+        if (i < n) {
+          uint4 u;
+          TG* e = reinterpret_cast<TG*>(&u);
+#pragma unroll
+          for (int q = 0; q < V; ++q) e[q] = io<TG>::cvt(out[i + q]);
+          *reinterpret_cast<uint4*>(o + i) = u;
+        }
+      return;
     }
   }
-  if (my_l == -INFINITY) my_dw = 0.0f;  // a masked or skipped slot takes no part
-  if (SOFTMAX && a.renorm) {
-    // the weights are the softmax of the chosen logits: dl_j = w_j (dw_j - sum_i w_i dw_i)
-    float m = my_l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    const float ex = my_l == -INFINITY ? 0.0f : (my_l == m ? 1.0f : expf(my_l - m));
-    const float S = warp_sum(ex);
-    const float wj = S > 0.0f ? ex / S : 0.0f;
-    my_dw = wj * (my_dw - warp_sum(wj * my_dw));
-  } else if (a.renorm) {
-    const float S = warp_sum(my_s);
-    const float dot = warp_sum(my_dw * my_s);
-    my_dw = S > 0.0f ? (my_dw - dot / S) / S * my_s * (1.0f - my_s) : 0.0f;
-  } else if (!SOFTMAX) {
-    my_dw = my_dw * my_s * (1.0f - my_s);
-  }
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kFull, my_e, j);
-    const float d = __shfl_sync(kFull, my_dw, j);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (e == lane + 32 * i) ds[i] += d;
-  }
-  if (SOFTMAX && !a.renorm) {
-    const float dot = warp_sum(my_dw * my_s);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) ds[i] = s[i] * (ds[i] - dot);
-  }
-  TG* out = reinterpret_cast<TG*>(a.dlogits) + (int64_t)t * a.E;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    if (e < a.E) out[e] = io<TG>::cvt(ds[i]);
-  }
+  for (int i = 0; i < EPL; ++i)
+    if (i < n) o[i] = io<TG>::cvt(out[i]);
 }
 
 GateArgs args_of(const moe_gate_dims& d) {
@@ -267,23 +313,26 @@ GateArgs args_of(const moe_gate_dims& d) {
   a.take = d.group_take;
   a.renorm = d.renorm != 0;
   a.scale = d.scale;
+  a.per = a.E / a.G;
   return a;
 }
 
-// f(std::integral_constant<int, EPL>) for the smallest supported number of experts per lane
+// f(integral_constant<EPL>) for the smallest number of experts per lane that holds R. Numbers that
+// are multiples of 8 are read 16 bytes at a time in either type; 4 in fp32.
 template <typename F>
-cudaError_t with_epl(int64_t E, F&& f) {
-  const int epl = (int)((E + 31) / 32);
-  if (epl <= 1) return f(std::integral_constant<int, 1>());
-  if (epl <= 2) return f(std::integral_constant<int, 2>());
-  if (epl <= 4) return f(std::integral_constant<int, 4>());
-  if (epl <= 8) return f(std::integral_constant<int, 8>());
-  if (epl <= 16) return f(std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 32>());
+cudaError_t with_epl(int R, F&& f) {
+  if (R <= 1) return f(std::integral_constant<int, 1>());
+  if (R <= 2) return f(std::integral_constant<int, 2>());
+  if (R <= 4) return f(std::integral_constant<int, 4>());
+  if (R <= 8) return f(std::integral_constant<int, 8>());
+  if (R <= 16) return f(std::integral_constant<int, 16>());
+  if (R <= 32) return f(std::integral_constant<int, 32>());
+  return f(std::integral_constant<int, 64>());  // groups that are no power of two leave lanes empty
 }
 
 template <int EPL, bool SOFTMAX>
-cudaError_t bwd_typed(const moe_gate_dims& d, const GateArgs& a, int grid, cudaStream_t st) {
+cudaError_t bwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st) {
+  const int grid = (int)((d.T + 7) / 8);
   if (d.dtype == MOE_BF16) {
     if (d.grad_dtype == MOE_BF16) MOE_LAUNCH(k_gate_bwd<EPL, SOFTMAX, __nv_bfloat16, __nv_bfloat16>, grid, 256, 0, st, a);
     else MOE_LAUNCH(k_gate_bwd<EPL, SOFTMAX, __nv_bfloat16, float>, grid, 256, 0, st, a);
@@ -294,10 +343,16 @@ cudaError_t bwd_typed(const moe_gate_dims& d, const GateArgs& a, int grid, cudaS
   return cudaSuccess;
 }
 
-template <int EPL, bool SOFTMAX>
-cudaError_t fwd_typed(const moe_gate_dims& d, const GateArgs& a, int grid, cudaStream_t st) {
-  if (d.dtype == MOE_BF16) MOE_LAUNCH(k_gate_fwd<EPL, SOFTMAX, __nv_bfloat16>, grid, 256, 0, st, a);
-  else MOE_LAUNCH(k_gate_fwd<EPL, SOFTMAX, float>, grid, 256, 0, st, a);
+template <int EPL, bool SOFTMAX, typename TL>
+cudaError_t fwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st) {
+  // a few tokens in one block, which then owns the counts; else eight a block
+  const int warps = d.T <= one_block_tokens<EPL> ? (int)d.T : 8;
+  const int grid = (int)((d.T + warps - 1) / warps);
+  if (a.count && grid > 1) {
+    const cudaError_t e = cudaMemsetAsync(a.count, 0, (size_t)d.E * sizeof(int), st);
+    if (e != cudaSuccess) return e;
+  }
+  MOE_LAUNCH(k_gate_fwd<EPL, SOFTMAX, TL>, grid, warps * 32, 0, st, a);
   return cudaSuccess;
 }
 
@@ -311,15 +366,19 @@ cudaError_t launch_gate_fwd(const moe_gate_dims& d, const void* logits, const fl
   a.idx = topk_idx;
   a.w = topk_w;
   a.count = count;
-  if (count) {
-    const cudaError_t e = cudaMemsetAsync(count, 0, (size_t)d.E * sizeof(int), st);
-    if (e != cudaSuccess) return e;
-  }
+  a.L = 1;
+  while (a.L * 2 * a.G <= 32) a.L *= 2;
+  a.R = (a.per + a.L - 1) / a.L;
+  const int V = d.dtype == MOE_BF16 ? 8 : 4;
+  a.vec = a.E % V == 0 && a.per % V == 0 && a.R % V == 0;
+  a.direct = !bias && (a.Kg == a.G || a.take == 1);
   *launches += 1;
-  const int grid = (int)((d.T + 7) / 8);
-  return with_epl(d.E, [&](auto epl) {
-    return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<epl.value, true>(d, a, grid, st)
-                                        : fwd_typed<epl.value, false>(d, a, grid, st);
+  return with_epl(a.R, [&](auto epl) {
+    constexpr int EPL = decltype(epl)::value;
+    if (d.dtype == MOE_BF16)
+      return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true, __nv_bfloat16>(d, a, st)
+                                          : fwd_typed<EPL, false, __nv_bfloat16>(d, a, st);
+    return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true, float>(d, a, st) : fwd_typed<EPL, false, float>(d, a, st);
   });
 }
 
@@ -330,11 +389,15 @@ cudaError_t launch_gate_bwd(const moe_gate_dims& d, const void* logits, const in
   a.idx_in = topk_idx;
   a.dw = dw;
   a.dlogits = dlogits;
+  // groups play no part here: R consecutive experts a lane, in whole 16-byte pieces where E allows
+  a.R = (a.E + 31) / 32;
+  const int V = d.dtype == MOE_BF16 || d.grad_dtype == MOE_BF16 ? 8 : 4;
+  a.vec = a.E % V == 0;
+  if (a.vec) a.R = (a.R + V - 1) / V * V;
   *launches += 1;
-  const int grid = (int)((d.T + 7) / 8);
-  return with_epl(d.E, [&](auto epl) {
-    return d.score == MOE_SCORE_SOFTMAX ? bwd_typed<epl.value, true>(d, a, grid, st)
-                                        : bwd_typed<epl.value, false>(d, a, grid, st);
+  return with_epl(a.R, [&](auto epl) {
+    constexpr int EPL = decltype(epl)::value <= 32 ? decltype(epl)::value : 32;  // E <= 1024
+    return d.score == MOE_SCORE_SOFTMAX ? bwd_typed<EPL, true>(d, a, st) : bwd_typed<EPL, false>(d, a, st);
   });
 }
 
