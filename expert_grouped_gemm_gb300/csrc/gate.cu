@@ -85,23 +85,58 @@ __device__ __forceinline__ float logistic(float l) { return l == -INFINITY ? 0.0
 // Maximum over the warp (one reduction of order-preserving keys).
 __device__ __forceinline__ float warp_max(float v) { return key_value(__reduce_max_sync(kFull, order_key(v))); }
 
-// Maximum and sum of e^{l - m} over a token's logits.
+// Softmax over a token's logits: l becomes the scores, *m the largest logit and *inv the factor of
+// e^{l - m} (0 when every expert is masked).
 template <int EPL>
-__device__ __forceinline__ void soft_stats(const float (&l)[EPL], float* m, float* z) {
+__device__ __forceinline__ void softmax_row(float (&l)[EPL], float* m, float* inv) {
   float v = l[0];
 #pragma unroll
   for (int i = 1; i < EPL; ++i) v = fmaxf(v, l[i]);
   *m = warp_max(v);
-  float s = 0.0f;
+  float z = 0.0f;
+  if (fabsf(*m) < INFINITY) {  // the usual row: e^{-inf - m} = 0 needs no care
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) s += soft(l[i], *m);
-  *z = warp_sum(s);
+    for (int i = 0; i < EPL; ++i) {
+      l[i] = expf(l[i] - *m);
+      z += l[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      l[i] = soft(l[i], *m);
+      z += l[i];
+    }
+  }
+  z = warp_sum(z);
+  *inv = z > 0.0f ? 1.0f / z : 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] *= *inv;
+}
+
+// Keys of a lane in descending order (equal ones in ascending expert order), with their places.
+// An odd-even transposition network: neighbours change places only when the later one is larger.
+template <int EPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[EPL], int (&at)[EPL]) {
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) at[i] = i;
+#pragma unroll
+  for (int r = 0; r < EPL; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < EPL; i += 2) {
+      const bool sw = key[i + 1] > key[i];
+      const uint32_t hi = sw ? key[i + 1] : key[i], lo = sw ? key[i] : key[i + 1];
+      const int ah = sw ? at[i + 1] : at[i], al = sw ? at[i] : at[i + 1];
+      key[i] = hi;
+      key[i + 1] = lo;
+      at[i] = ah;
+      at[i + 1] = al;
+    }
 }
 
 template <int EPL, bool SOFTMAX, typename TL>
 __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const GateArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ int hist[1024];  // one block only: the counts, written without an atomic on global memory
+  __shared__ int hist[1024];  // one block only: it has every token and writes the counts itself
   const bool one = gridDim.x == 1 && a.count;
   if (one) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
@@ -115,11 +150,10 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
     const int n = grp < a.G ? max(0, min(a.R, (grp + 1) * a.per - e0)) : 0;
     const TL* row = reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E;
     uint32_t key[EPL];
-    float m = 0.0f, z = 1.0f;
+    float m = 0.0f, inv = 0.0f;
     {
       float l[EPL];
       load_logits<EPL, TL>(row + e0, n, a.vec, l);
-      if (SOFTMAX && (!a.direct || !a.renorm)) soft_stats<EPL>(l, &m, &z);
       if (a.direct) {
         if constexpr (SOFTMAX) {  // beside a +inf logit every other score is zero, and they tie
           bool inf = false;
@@ -135,10 +169,17 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
         for (int i = 0; i < EPL; ++i) key[i] = i >= n ? kKeyNone : l[i] == -INFINITY ? kKeyMasked : order_key(l[i]);
       } else {
 #pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = l[i] == -INFINITY;
+        if constexpr (SOFTMAX) {
+          softmax_row<EPL>(l, &m, &inv);
+        } else {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) l[i] = sigmoidf_(l[i]);  // within 4 ulp; the weights are taken in full precision below
+        }
+#pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          const float s = SOFTMAX ? (z > 0.0f ? soft(l[i], m) / z : 0.0f) : logistic(l[i]);
-          const float c = s + (a.bias && i < n ? a.bias[e0 + i] : 0.0f);
-          key[i] = i >= n ? kKeyNone : (l[i] == -INFINITY || !(c > -INFINITY)) ? kKeyMasked : order_key(c);
+          const float c = l[i] + (a.bias && i < n ? a.bias[e0 + i] : 0.0f);
+          key[i] = i >= n ? kKeyNone : (key[i] || !(c > -INFINITY)) ? kKeyMasked : order_key(c);
         }
       }
     }
@@ -166,33 +207,53 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
         for (int i = 0; i < EPL; ++i) key[i] = kKeyNone;
       }
     }
-    uint32_t best = key[0];  // this lane's largest key, the first expert that has it
-    int bi = 0;
-#pragma unroll
-    for (int i = 1; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
-      }
+    // k rounds: the largest key of the warp, in its lowest lane. Lanes with few experts sort them
+    // once and then drop the first; longer lists are searched again by the lane that gave one.
     int my_e = 0;
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t top = __reduce_max_sync(kFull, best);
-      const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
-      const int e = __shfl_sync(kFull, e0 + bi, who);
-      if (lane == j) my_e = e;
-      if (lane == who) {
-        uint32_t b = kKeyNone;
+    if constexpr (EPL <= 8) {
+      int at[EPL];
+      sort_keys<EPL>(key, at);
+      for (int j = 0; j < a.k; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, key[0]);
+        const int who = __ffs(__ballot_sync(kFull, key[0] == top)) - 1;
+        const int e = __shfl_sync(kFull, e0 + at[0], who);
+        if (lane == j) my_e = e;
+        if (lane == who) {
+#pragma unroll
+          for (int i = 0; i + 1 < EPL; ++i) {
+            key[i] = key[i + 1];
+            at[i] = at[i + 1];
+          }
+          key[EPL - 1] = kKeyNone;
+        }
+      }
+    } else {
+      uint32_t best = kKeyNone;  // this lane's largest key, the first expert that has it
+      int bi = 0;
+      auto search = [&]() {
+        uint32_t b = key[0];
         int nb = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          if (i == bi) key[i] = kKeyNone;
+        for (int i = 1; i < EPL; ++i)
           if (key[i] > b) {
             b = key[i];
             nb = i;
           }
-        }
         best = b;
         bi = nb;
+      };
+      search();
+      for (int j = 0; j < a.k; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
+        const int e = __shfl_sync(kFull, e0 + bi, who);
+        if (lane == j) my_e = e;
+        if (lane == who) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (i == bi) key[i] = kKeyNone;
+          search();
+        }
       }
     }
     // weights: lane j reads its chosen logit again (a line that is still in L1)
@@ -201,9 +262,15 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
     float s;
     if (SOFTMAX) {
       // s / S over the chosen is the softmax of the chosen logits: it cannot become 0 / 0
-      if (a.renorm) m = warp_max(lj);
+      if (a.renorm) {
+        m = warp_max(lj);
+      } else if (a.direct) {  // the row's sum has not been needed so far
+        float l[EPL];
+        load_logits<EPL, TL>(row + e0, n, a.vec, l);
+        softmax_row<EPL>(l, &m, &inv);
+      }
       s = soft(lj, m);
-      if (!a.renorm) s = z > 0.0f ? s / z : 0.0f;
+      if (!a.renorm) s *= inv;
     } else {
       s = logistic(lj);
     }
@@ -214,14 +281,51 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
     if (lane < a.k) {
       a.idx[(int64_t)t * a.k + lane] = my_e;
       a.w[(int64_t)t * a.k + lane] = s * a.scale;
-      // whole numbers: the order of the additions does not matter
-      if (a.count) atomicAdd(one ? &hist[my_e] : a.count + my_e, 1);
+      if (one) atomicAdd(&hist[my_e], 1);  // whole numbers: the order does not matter
     }
   }
   if (one) {
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.count[e] = hist[e];
   }
+}
+
+// How often each expert stands in idx[n]: histograms in shared memory, one a block, added over a
+// cluster of kCountBlocks. (Counting with atomics on global memory as the tokens are routed took
+// as long again as the routing: the counters of all experts share a few L2 lines.)
+constexpr int kCountBlocks = 8;
+__global__ void __launch_bounds__(1024) __cluster_dims__(kCountBlocks) k_gate_count(const int* idx, int64_t n, int E,
+                                                                                    int* count) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ int hist[1024];
+  const int rank = (int)cluster_ctarank();
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  constexpr int U = 8;
+  for (int64_t i = (int64_t)rank * 1024 + threadIdx.x; i < n; i += (int64_t)kCountBlocks * 1024 * U) {
+    int e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = i + (int64_t)u * kCountBlocks * 1024;
+      e[u] = at < n ? idx[at] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e[u] >= 0) atomicAdd(&hist[e[u]], 1);
+  }
+  cluster_sync_all();
+  const int c = rank * (1024 / kCountBlocks) + (int)threadIdx.x;  // this block's share of the experts
+  if (threadIdx.x < 1024 / kCountBlocks && c < E) {
+    int s = 0;
+#pragma unroll
+    for (int r = 0; r < kCountBlocks; ++r) {
+      int v;
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(&hist[c]), r)) : "memory");
+      s += v;
+    }
+    count[c] = s;
+  }
+  cluster_sync_all();  // no block leaves while another still reads its histogram
 }
 
 template <int EPL, bool SOFTMAX, typename TL, typename TG>
@@ -241,10 +345,10 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
     if (my_e < 0 || my_e >= a.E) my_e = -1;
   }
   const bool dense = SOFTMAX && !a.renorm;
-  float l[EPL], m = 0.0f, z = 1.0f;
+  float l[EPL], m = 0.0f, inv = 0.0f;
   if (dense) {
     load_logits<EPL, TL>(row + e0, n, a.vec, l);
-    soft_stats<EPL>(l, &m, &z);
+    softmax_row<EPL>(l, &m, &inv);
   }
   float lj = my_e >= 0 ? io<TL>::to_f(row[my_e]) : -INFINITY;
   if (lj != lj) lj = -INFINITY;
@@ -253,7 +357,7 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
   float dot = 0.0f; // dense: sum of ds s over the chosen
   if (dense) {
     d = dw;
-    dot = warp_sum(dw * (z > 0.0f ? soft(lj, m) / z : 0.0f));
+    dot = warp_sum(dw * soft(lj, m) * inv);
   } else if (SOFTMAX) {
     // the weights are the softmax of the chosen logits: dl_j = w_j (dw_j - sum_i w_i dw_i)
     const float s = soft(lj, warp_max(lj));
@@ -272,15 +376,15 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
 #pragma unroll
   for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
   for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kFull, my_e, j) - e0;  // < 0 or >= R where another lane has it (or none)
+    const int e = __shfl_sync(kFull, my_e, j) - e0;  // outside [0, R) where another lane has it (or none)
     const float dj = __shfl_sync(kFull, d, j);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (e == i && i < n) out[i] += dj;
+      if (e == i) out[i] += dj;
   }
   if (dense) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) out[i] = z > 0.0f ? soft(l[i], m) / z * (out[i] - dot) : 0.0f;
+    for (int i = 0; i < EPL; ++i) out[i] = l[i] * (out[i] - dot);
   }
   TG* o = reinterpret_cast<TG*>(a.dlogits) + (int64_t)t * a.E + e0;
   constexpr int V = 16 / (int)sizeof(TG);
@@ -344,15 +448,16 @@ cudaError_t bwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st
 }
 
 template <int EPL, bool SOFTMAX, typename TL>
-cudaError_t fwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st) {
+cudaError_t fwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st, int* launches) {
   // a few tokens in one block, which then owns the counts; else eight a block
   const int warps = d.T <= one_block_tokens<EPL> ? (int)d.T : 8;
   const int grid = (int)((d.T + warps - 1) / warps);
-  if (a.count && grid > 1) {
-    const cudaError_t e = cudaMemsetAsync(a.count, 0, (size_t)d.E * sizeof(int), st);
-    if (e != cudaSuccess) return e;
-  }
+  *launches += 1;
   MOE_LAUNCH(k_gate_fwd<EPL, SOFTMAX, TL>, grid, warps * 32, 0, st, a);
+  if (a.count && grid > 1) {
+    *launches += 1;
+    MOE_LAUNCH(k_gate_count, kCountBlocks, 1024, 0, st, (const int*)a.idx, (int64_t)a.T * a.k, a.E, a.count);
+  }
   return cudaSuccess;
 }
 
@@ -372,13 +477,12 @@ cudaError_t launch_gate_fwd(const moe_gate_dims& d, const void* logits, const fl
   const int V = d.dtype == MOE_BF16 ? 8 : 4;
   a.vec = a.E % V == 0 && a.per % V == 0 && a.R % V == 0;
   a.direct = !bias && (a.Kg == a.G || a.take == 1);
-  *launches += 1;
   return with_epl(a.R, [&](auto epl) {
     constexpr int EPL = decltype(epl)::value;
     if (d.dtype == MOE_BF16)
-      return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true, __nv_bfloat16>(d, a, st)
-                                          : fwd_typed<EPL, false, __nv_bfloat16>(d, a, st);
-    return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true, float>(d, a, st) : fwd_typed<EPL, false, float>(d, a, st);
+      return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true, __nv_bfloat16>(d, a, st, launches)
+                                          : fwd_typed<EPL, false, __nv_bfloat16>(d, a, st, launches);
+    return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true, float>(d, a, st, launches) : fwd_typed<EPL, false, float>(d, a, st, launches);
   });
 }
 
