@@ -153,10 +153,17 @@ def _ptr(t, name, dtype=None, required=True):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle as a number, without a Stream object made for every call (3 us on a Grace
+# core against 0.4); PyTorch versions without the function take the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def moe_workspace_size(dims: Dims) -> int:
@@ -283,15 +290,15 @@ def _tensor(t, name, dtype, shape, required=True):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def make_norm_dims(T, H, dtype="bf16", kind="layer", eps=1e-5) -> NormDims:
@@ -307,7 +314,8 @@ def alloc_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
 def moe_norm_fwd(dims: NormDims, x, residual, weight, bias, y, sum=None, mean=None, rstd=None, stream=None):
     """y = norm(x + residual) * weight + bias; sum receives x + residual, mean and rstd the statistics."""
     io, f32 = _io_dtype(dims), torch.float32
-    th, h, t = (dims.T, dims.H), (dims.H,), (dims.T,)
+    T, H = dims.T, dims.H
+    th, h, t = (T, H), (H,), (T,)
     args = (
         _tensor(x, "x", io, th), _tensor(residual, "residual", io, th, False),
         _tensor(weight, "weight", io, h), _tensor(bias, "bias", io, h, False), _tensor(y, "y", io, th),
@@ -318,7 +326,8 @@ def moe_norm_fwd(dims: NormDims, x, residual, weight, bias, y, sum=None, mean=No
 def moe_norm_bwd(dims: NormDims, ws, dy, dsum, x, weight, mean, rstd, dx, dweight, dbias=None, stream=None):
     """Gradients of moe_norm_fwd; x is the tensor that was normalised, dsum what reaches it past the norm."""
     io, f32 = _io_dtype(dims), torch.float32
-    th, h, t = (dims.T, dims.H), (dims.H,), (dims.T,)
+    T, H = dims.T, dims.H
+    th, h, t = (T, H), (H,), (T,)
     _check(load().moe_norm_bwd(
         dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, th),
         _tensor(dsum, "dsum", io, th, False), _tensor(x, "x", io, th), _tensor(weight, "weight", io, h),
@@ -370,10 +379,11 @@ def alloc_linear_workspace(dims: LinearDims, device="cuda") -> torch.Tensor:
 def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stream=None):
     """y = act(x w + bias) + residual; pre receives x w + bias."""
     io = _io_dtype(dims)
-    mn = (dims.M, dims.N)
+    M, K, N = dims.M, dims.K, dims.N
+    mn = (M, N)
     _check(load().moe_linear_fwd(
-        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(x, "x", io, (dims.M, dims.K)),
-        _tensor(w, "w", io, (dims.K, dims.N)), _tensor(bias, "bias", io, (dims.N,), False),
+        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(x, "x", io, (M, K)),
+        _tensor(w, "w", io, (K, N)), _tensor(bias, "bias", io, (N,), False),
         _tensor(residual, "residual", io, mn, False), _tensor(y, "y", torch.float32 if dims.out_f32 else io, mn),
         _tensor(pre, "pre", io, mn, False)))
 
@@ -381,12 +391,13 @@ def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stre
 def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=None, stream=None):
     """Gradients of moe_linear_fwd; pre is needed when the activation is not 'none'."""
     io = _io_dtype(dims)
-    mn, mk, kn = (dims.M, dims.N), (dims.M, dims.K), (dims.K, dims.N)
+    M, K, N = dims.M, dims.K, dims.N
+    mn, mk, kn = (M, N), (M, K), (K, N)
     _check(load().moe_linear_bwd(
         dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, mn),
         _tensor(x, "x", io, mk), _tensor(w, "w", io, kn), _tensor(pre, "pre", io, mn, False),
         _tensor(dx, "dx", io, mk, False), _tensor(dw, "dw", io, kn, False),
-        _tensor(dbias, "dbias", io, (dims.N,), False)))
+        _tensor(dbias, "dbias", io, (N,), False)))
 
 
 def moe_read_status(ws: torch.Tensor, stream=None) -> int:

@@ -388,29 +388,106 @@ struct SplitCfg {
   static_assert(NB * 128 * 4 <= BAR_OFF, "the partial sums reuse the ring");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// z -> y and pre for four neighbouring features of one token (n0 a multiple of 4). VEC: the rows of
+// the outputs are multiples of 16 bytes, so the four values are one access.
+template <bool VEC>
+__device__ __forceinline__ void emit4(const LinearGemm& g, int64_t t, int n0, float (&z)[4], const float (&res)[4]) {
+  const int64_t o = t * g.N + n0;
+  float y[4];
+  act_fwd<true, 4>(g.act, z, y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] += res[i];
+  __nv_bfloat16* pre = reinterpret_cast<__nv_bfloat16*>(g.pre) + o;
+  if constexpr (VEC) {
+    auto two = [](float a, float b) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    if (g.pre) *reinterpret_cast<uint2*>(pre) = make_uint2(two(z[0], z[1]), two(z[2], z[3]));
+    if (g.out_f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + o) = make_float4(y[0], y[1], y[2], y[3]);
+    else *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(g.y) + o) = make_uint2(two(y[0], y[1]), two(y[2], y[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n0 + i >= g.N) break;
+      if (g.pre) pre[i] = __float2bfloat16_rn(z[i]);
+      if (g.out_f32) reinterpret_cast<float*>(g.y)[o + i] = y[i];
+      else reinterpret_cast<__nv_bfloat16*>(g.y)[o + i] = __float2bfloat16_rn(y[i]);
+    }
+  }
 }
 
-// z -> y, pre of one element
-__device__ __forceinline__ void emit(const LinearGemm& g, int64_t t, int n, float z) {
-  const int64_t o = t * g.N + n;
-  const float zz[1] = {z};
-  float y[1];
-  act_fwd<true, 1>(g.act, zz, y);
-  if (g.residual) y[0] += __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g.residual)[o]);
-  if (g.pre) reinterpret_cast<__nv_bfloat16*>(g.pre)[o] = __float2bfloat16_rn(z);
-  if (g.out_f32) reinterpret_cast<float*>(g.y)[o] = y[0];
-  else reinterpret_cast<__nv_bfloat16*>(g.y)[o] = __float2bfloat16_rn(y[0]);
+// four bf16 at p (as many as exist), VEC as above
+template <bool VEC>
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, int left, float (&f)[4]) {
+  if constexpr (VEC) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+    const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < left ? __bfloat162float(p[i]) : 0.0f;
+  }
+}
+
+// Tokens [a, e) of the tile from the parts' sums in the CTAs of the cluster: a warp a token, four
+// features a lane, two tokens' loads in flight. The parts are added in rank order.
+template <bool VEC, int S>
+__device__ __forceinline__ void finish_tokens(const LinearGemm& g, const float* sums, int t0, int f0, int a, int e) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int n0 = f0 + 4 * lane;
+  if (n0 >= g.N) return;
+  const uint32_t base = smem_u32(sums) + lane * 16;
+  uint32_t peer[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) peer[r] = S > 1 ? mapa_shared(base, r) : base;
+  float b[4] = {0, 0, 0, 0};
+  if (g.bias) load4<VEC>(reinterpret_cast<const __nv_bfloat16*>(g.bias) + n0, g.N - n0, b);
+  for (int t = a + warp; t < e; t += 2 * warps) {
+    float4 v[2][S];
+    float res[2][4] = {};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int tt = t + u * warps;
+      if (tt < e) {
+#pragma unroll
+        for (int r = 0; r < S; ++r)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[u][r].x), "=f"(v[u][r].y), "=f"(v[u][r].z), "=f"(v[u][r].w)
+                       : "r"(peer[r] + tt * 512));
+        if (g.residual)
+          load4<VEC>(reinterpret_cast<const __nv_bfloat16*>(g.residual) + (int64_t)(t0 + tt) * g.N + n0, g.N - n0, res[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int tt = t + u * warps;
+      if (tt < e) {
+        float z[4] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w};
+#pragma unroll
+        for (int r = 1; r < S; ++r) {
+          z[0] += v[u][r].x;
+          z[1] += v[u][r].y;
+          z[2] += v[u][r].z;
+          z[3] += v[u][r].w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] += b[i];
+        emit4<VEC>(g, t0 + tt, n0, z, res[u]);
+      }
+    }
+  }
 }
 
 // Block (feature tile of 128, token tile of NB, part of K); the cluster holds the parts of one tile.
-template <int NB>
+template <int NB, int S, bool VEC>
 __global__ void __launch_bounds__(SplitCfg<NB>::THREADS)
     k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const TcArgs args, int S) {
+                   const TcArgs args) {
   using C = SplitCfg<NB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -502,50 +579,23 @@ __global__ void __launch_bounds__(SplitCfg<NB>::THREADS)
 
   // ------------------------------------------------------------ epilogue
   const int ntok = min(NB, g.M - t0);
-  const int f = (warp & 3) * 32 + lane;  // this thread's feature of the tile
-  const int n = f0 + f;
   float* sums = reinterpret_cast<float*>(smem);  // [token][128], over the ring once every MMA has read it
-  bool ok = true;
-  if (warp >= 2) {
-    ok = mbar_wait_bounded(done, 0, abort_flag);
+  if (warp >= 2 && mbar_wait_bounded(done, 0, abort_flag)) {
     tc_fence_after();
-    const float b = ok && g.bias && n < g.N ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g.bias)[n]) : 0.0f;
-    if (ok) {
-#pragma unroll 1
-      for (int c = 0; c < (NB + 31) / 32; ++c) {
-        if (c * 32 >= ntok) break;
-        float v[32];
-        tmem_ld32(tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(c * 32), v);
+    const int f = (warp & 3) * 32 + lane;  // this thread's feature of the tile
+    for (int c = 0; c * 32 < ntok; ++c) {
+      float v[32];
+      tmem_ld32(tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(c * 32), v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int t = c * 32 + i;
-          if (t < ntok) {
-            if (S > 1) sums[t * 128 + f] = v[i];
-            else if (n < g.N) emit(g, t0 + t, n, v[i] + b);
-          }
-        }
-      }
+      for (int i = 0; i < 32; ++i)
+        if (c * 32 + i < ntok) sums[(c * 32 + i) * 128 + f] = v[i];
     }
   }
-  if (S > 1) {
-    cluster_sync_all();  // every part is in its CTA's shared memory
-    if (warp >= 2 && ok && n < g.N) {
-      const int a = ntok * part / S, e = ntok * (part + 1) / S;  // the tokens this CTA finishes
-      const float b = g.bias ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g.bias)[n]) : 0.0f;
-      for (int t = a; t < e; ++t) {
-        const uint32_t addr = smem_u32(sums + t * 128 + f);
-        float v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = r < S ? ld_cluster_f32(mapa_shared(addr, r)) : 0.0f;
-        float z = v[0];
-#pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < S) z += v[r];
-        emit(g, t0 + t, n, z + b);
-      }
-    }
-    cluster_sync_all();  // no CTA leaves while another still reads its sums
-  }
+  // every part is in its CTA's shared memory; each CTA finishes its share of the tokens
+  if constexpr (S > 1) cluster_sync_all();
+  else __syncthreads();
+  if (!*abort_flag) finish_tokens<VEC, S>(g, sums, t0, f0, ntok * part / S, ntok * (part + 1) / S);
+  if constexpr (S > 1) cluster_sync_all();  // no CTA leaves while another still reads its sums
 
   tc_fence_before();
   __syncthreads();
@@ -632,12 +682,11 @@ cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&l.cfg, kern, mA, mB, mY, mP, a);
 }
 
-template <int NB>
-cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
+template <int NB, int S, bool VEC>
+cudaError_t launch_split_as(const LinearGemm& g, cudaStream_t st) {
   using C = SplitCfg<NB>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
-  if (g.a_mn && NB < 64) return cudaErrorInvalidValue;
-  auto kern = k_linear_split<NB>;
+  auto kern = k_linear_split<NB, S, VEC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   CUtensorMap mW, mX;
@@ -652,7 +701,19 @@ cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
   const int64_t total = (int64_t)a.mt * a.nt * S;
   if (total >= (1ll << 31)) return cudaErrorInvalidValue;
   LaunchCfg l(dim3((unsigned)total), C::THREADS, C::SMEM, st, S);
-  return cudaLaunchKernelEx(&l.cfg, kern, mW, mX, a, S);
+  return cudaLaunchKernelEx(&l.cfg, kern, mW, mX, a);
+}
+
+template <int NB>
+cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
+  if (g.a_mn && NB < 64) return cudaErrorInvalidValue;
+  const bool vec = g.N % 8 == 0;
+  switch (S) {
+    case 1: return vec ? launch_split_as<NB, 1, true>(g, st) : launch_split_as<NB, 1, false>(g, st);
+    case 2: return vec ? launch_split_as<NB, 2, true>(g, st) : launch_split_as<NB, 2, false>(g, st);
+    case 4: return vec ? launch_split_as<NB, 4, true>(g, st) : launch_split_as<NB, 4, false>(g, st);
+    default: return vec ? launch_split_as<NB, 8, true>(g, st) : launch_split_as<NB, 8, false>(g, st);
+  }
 }
 
 cudaError_t launch_split(const LinearGemm& g, int nb, int S, cudaStream_t st) {
