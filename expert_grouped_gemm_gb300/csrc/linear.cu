@@ -11,89 +11,184 @@
 namespace moe {
 namespace {
 
+// ---------------------------------------------------------------- fp32 products
 // One product C = op(A) op(B) with element strides, and the epilogue of the forward.
 struct SimtGemm {
-  const void* A;
-  const void* B;
+  const float* A;
+  const float* B;
   int64_t sam, sak, sbk, sbn;  // element strides of A[m, k] and B[k, n]
   int M, K, N;
-  const void* bias;
-  const void* residual;
-  void* out;
-  void* pre;
-  int act, out_f32;
+  const float* bias;
+  const float* residual;
+  float* out;
+  float* pre;
+  int act;
 };
 
-constexpr int kSBM = 64, kSBN = 64, kSBK = 16;
+// fp32 operands need fp32 products (tf32 keeps 10 bits of a factor), so these run on the CUDA
+// cores: a 64 x 64 tile per block of 128 threads, 8 x 4 outputs a thread (three 16-byte shared
+// loads for 32 FMAs), k in slabs of 16, the next slab's global loads in registers while this one is
+// multiplied. Bound by FMA issue. Where the tiles alone leave SMs idle, a cluster of S blocks
+// shares a tile, each with a part of K, and adds the parts in rank order.
+constexpr int kSB = 64, kSK = 16, kSThreads = 128;
 
-// 64 x 64 tile per block of 256 threads, 4 x 4 outputs a thread, fp32 FMAs in ascending k.
-template <typename T>
-__global__ void __launch_bounds__(256) k_linear_simt(const SimtGemm g) {
+// A thread's eight elements of the 64 x 16 slab of an operand X[r, k] (r: the 64 rows of A or columns
+// of B): two 16-byte loads along the contiguous index where the rows allow, else eight loads with
+// neighbouring threads on the contiguous index.
+struct Slab {
+  const float* p;      // element of the first load in slab 0
+  int64_t dr, dslab;   // from one load to the next, from one slab to the next
+  int r, k, rstep, kstep, R, K;
+  bool vec, kc;        // 16-byte loads; k is the contiguous index
+  float v[8];
+  __device__ __forceinline__ void init(const float* X, int64_t sr, int64_t sk, int r0, int R_, int K_, int tid) {
+    R = R_;
+    K = K_;
+    kc = sk == 1;
+    vec = (kc ? sr % 4 == 0 && K % 4 == 0 : sk % 4 == 0 && R % 4 == 0);
+    if (vec) {
+      r = kc ? tid >> 2 : (tid & 15) * 4;
+      k = kc ? (tid & 3) * 4 : tid >> 4;
+      rstep = kc ? 32 : 0;
+      kstep = kc ? 0 : 8;
+    } else {
+      r = kc ? tid >> 4 : tid & 63;
+      k = kc ? tid & 15 : tid >> 6;
+      rstep = kc ? 8 : 0;
+      kstep = kc ? 0 : 2;
+    }
+    p = X + (int64_t)(r0 + r) * sr + (int64_t)k * sk;
+    dr = rstep * sr + kstep * sk;
+    dslab = kSK * sk;
+    R -= r0;
+  }
+  __device__ __forceinline__ void fetch(int s) {
+    const float* q = p + s * dslab;
+    const int ks = s * kSK + k;
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r + i * rstep < R && ks + i * kstep < K) t = *reinterpret_cast<const float4*>(q + i * dr);
+        v[4 * i] = t.x;
+        v[4 * i + 1] = t.y;
+        v[4 * i + 2] = t.z;
+        v[4 * i + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = r + i * rstep < R && ks + i * kstep < K ? q[i * dr] : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void stash(float (*t)[kSB + 4]) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (kc) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[k + j][r + i * rstep] = v[4 * i + j];
+        } else {
+          *reinterpret_cast<float4*>(&t[k + i * kstep][r]) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[k + i * kstep][r + i * rstep] = v[i];
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtGemm g, int S) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float sa[kSBK][kSBM + 4];
-  __shared__ float sb[kSBK][kSBN + 4];
-  const T* A = reinterpret_cast<const T*>(g.A);
-  const T* B = reinterpret_cast<const T*>(g.B);
+  __shared__ __align__(16) float sa[2][kSK][kSB + 4];
+  __shared__ __align__(16) float sb[2][kSK][kSB + 4];
+  __shared__ __align__(16) float sums[kSB][kSB];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int nt = (g.N + kSBN - 1) / kSBN;
-  const int m0 = (blockIdx.x / nt) * kSBM, n0 = (blockIdx.x % nt) * kSBN;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < g.K; k0 += kSBK) {
+  const int part = (int)(blockIdx.x % S), tile = (int)(blockIdx.x / S);
+  const int nt = (g.N + kSB - 1) / kSB;
+  const int m0 = tile / nt * kSB, n0 = tile % nt * kSB;
+  const int slabs = (g.K + kSK - 1) / kSK;
+  const int s0 = (int)((int64_t)slabs * part / S), s1 = (int)((int64_t)slabs * (part + 1) / S);
+  Slab A, B;
+  A.init(g.A, g.sam, g.sak, m0, g.M, g.K, tid);
+  B.init(g.B, g.sbn, g.sbk, n0, g.N, g.K, tid);
+  auto fetch = [&](int s) {
+    A.fetch(s);
+    B.fetch(s);
+  };
+  auto stash = [&](int buf) {
+    A.stash(sa[buf]);
+    B.stash(sb[buf]);
+  };
+  float acc[8][4] = {};
+  fetch(s0);
+  stash(0);
+  __syncthreads();
+  int buf = 0;
+  for (int s = s0; s < s1; ++s) {
+    if (s + 1 < s1) fetch(s + 1);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = tid + 256 * r;  // neighbouring threads on the contiguous index
-      int m, k;
-      if (g.sak == 1) {
-        k = i & 15;
-        m = i >> 4;
-      } else {
-        m = i & 63;
-        k = i >> 6;
-      }
-      sa[k][m] = m0 + m < g.M && k0 + k < g.K ? io<T>::to_f(A[(int64_t)(m0 + m) * g.sam + (int64_t)(k0 + k) * g.sak]) : 0.0f;
-      int n, kb;
-      if (g.sbk == 1) {
-        kb = i & 15;
-        n = i >> 4;
-      } else {
-        n = i & 63;
-        kb = i >> 6;
-      }
-      sb[kb][n] = n0 + n < g.N && k0 + kb < g.K ? io<T>::to_f(B[(int64_t)(k0 + kb) * g.sbk + (int64_t)(n0 + n) * g.sbn]) : 0.0f;
+    for (int k = 0; k < kSK; ++k) {
+      const float4 a0 = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8]);
+      const float4 a1 = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8 + 4]);
+      const float4 b = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
+      const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
     }
+    if (s + 1 < s1) stash(buf ^ 1);
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kSBK; ++k) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = sa[k][ty * 4 + i];
-        b[i] = sb[k][tx * 4 + i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
+    buf ^= 1;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= g.M || n >= g.N) continue;
-      const int64_t o = (int64_t)m * g.N + n;
-      const float z = acc[i][j] + (g.bias ? io<T>::to_f(reinterpret_cast<const T*>(g.bias)[n]) : 0.0f);
-      const float zz[1] = {z};
-      float yy[1];
-      act_fwd<sizeof(T) == 2, 1>(g.act, zz, yy);
-      float y = yy[0];
-      if (g.residual) y += io<T>::to_f(reinterpret_cast<const T*>(g.residual)[o]);
-      if (g.pre) reinterpret_cast<T*>(g.pre)[o] = io<T>::cvt(z);
-      if (g.out_f32) reinterpret_cast<float*>(g.out)[o] = y;
-      else reinterpret_cast<T*>(g.out)[o] = io<T>::cvt(y);
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(&sums[ty * 8 + i][tx * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
+  // this block's share of the tile's rows, four columns a thread
+  const bool vec = g.N % 4 == 0;
+  const int n = n0 + tx * 4;
+  for (int r = kSB * part / S + ty; r < kSB * (part + 1) / S; r += kSThreads / 16) {
+    const int m = m0 + r;
+    if (m >= g.M || n >= g.N) break;
+    float z[4] = {0, 0, 0, 0}, y[4];
+    for (int p = 0; p < S; ++p) {
+      float4 v;
+      const uint32_t at = smem_u32(&sums[r][tx * 4]);
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                   : "r"(S > 1 ? mapa_shared(at, p) : at));
+      z[0] += v.x;
+      z[1] += v.y;
+      z[2] += v.z;
+      z[3] += v.w;
     }
+    const int64_t o = (int64_t)m * g.N + n;
+    if (g.bias)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) z[j] += g.bias[n + j];
+    act_fwd<false, 4>(g.act, z, y);
+    if (g.residual)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) y[j] += g.residual[o + j];
+    if (vec) {
+      if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
+      *reinterpret_cast<float4*>(g.out + o) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) {
+          if (g.pre) g.pre[o + j] = z[j];
+          g.out[o + j] = y[j];
+        }
+    }
+  }
+  if (S > 1) cluster_sync_all();  // no block leaves while another still reads its sums
 }
 
 // ---------------------------------------------------------------- dz and the bias gradient
@@ -222,13 +317,33 @@ __global__ void __launch_bounds__(256) k_pack_rows(const __nv_bfloat16* src, __n
   }
 }
 
-template <typename T>
-cudaError_t run_simt(const SimtGemm& g, cudaStream_t st, int* launches) {
-  const int64_t tiles = (((int64_t)g.M + kSBM - 1) / kSBM) * ((g.N + kSBN - 1) / kSBN);
-  if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+cudaError_t run_f32(const SimtGemm& g, int sms, cudaStream_t st, int* launches) {
+  const int64_t tiles = (((int64_t)g.M + kSB - 1) / kSB) * ((g.N + kSB - 1) / kSB);
+  const int slabs = (g.K + kSK - 1) / kSK;
+  // four blocks fit an SM; a part keeps at least four slabs
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= (int64_t)sms * 4 && slabs >= 8 * S) S *= 2;
+  if (tiles * S >= (1ll << 31)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (MOE_PDL) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (S > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)S;
+    at[n].val.clusterDim.y = 1;
+    at[n++].val.clusterDim.z = 1;
+  }
+  cfg.gridDim = dim3((unsigned)(tiles * S));
+  cfg.blockDim = dim3(kSThreads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = n;
   *launches += 1;
-  MOE_LAUNCH(k_linear_simt<T>, (unsigned)tiles, 256, 0, st, g);
-  return cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, k_linear_f32, g, S);
 }
 
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
@@ -335,8 +450,10 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
   return e;
 }
 
+const float* f(const void* p) { return static_cast<const float*>(p); }
+
 cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const void* x, const void* w, const void* pre,
-                    void* dx, void* dw, void* dbias, cudaStream_t st, int* launches) {
+                    void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
   const LinearWs L = layout(d);
   const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
   float* part = reinterpret_cast<float*>(ws + L.part);
@@ -346,12 +463,12 @@ cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const vo
   if (store || dbias) e = run_dz<float>(d, dy, pre, store ? ws + L.dz : nullptr, N, dbias ? part : nullptr, st, launches);
   if (e == cudaSuccess && dbias) e = run_dbias<float>(d, part, dbias, st, launches);
   if (e == cudaSuccess && dx) {
-    SimtGemm g = {dz, w, N, 1, 1, N, M, N, K, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0};
-    e = run_simt<float>(g, st, launches);
+    SimtGemm g = {f(dz), f(w), N, 1, 1, N, M, N, K, nullptr, nullptr, (float*)dx, nullptr, MOE_ACT_NONE};
+    e = run_f32(g, sms, st, launches);
   }
   if (e == cudaSuccess && dw) {
-    SimtGemm g = {x, dz, 1, K, N, 1, K, M, N, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0};
-    e = run_simt<float>(g, st, launches);
+    SimtGemm g = {f(x), f(dz), 1, K, N, 1, K, M, N, nullptr, nullptr, (float*)dw, nullptr, MOE_ACT_NONE};
+    e = run_f32(g, sms, st, launches);
   }
   return e;
 }
@@ -364,15 +481,16 @@ cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x,
                               const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
   if (d.dtype == MOE_BF16)
     return fwd_bf16(d, static_cast<char*>(ws), x, w, bias, residual, y, pre, sms, st, launches);
-  SimtGemm g = {x, w, d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, bias, residual, y, pre, d.act, d.out_f32};
-  return run_simt<float>(g, st, launches);
+  SimtGemm g = {f(x), f(w), d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, f(bias), f(residual), (float*)y, (float*)pre,
+                d.act};
+  return run_f32(g, sms, st, launches);
 }
 
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,
                               const void* pre, void* dx, void* dw, void* dbias, int sms, cudaStream_t st,
                               int* launches) {
   return d.dtype == MOE_BF16 ? bwd_bf16(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, sms, st, launches)
-                             : bwd_f32(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, st, launches);
+                             : bwd_f32(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, sms, st, launches);
 }
 
 }  // namespace moe
