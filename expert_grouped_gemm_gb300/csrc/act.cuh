@@ -1,16 +1,30 @@
 // act.cuh -- activations of the linear operator and their derivatives.
 //
-// The bf16 operator evaluates them with the hardware exponential and the approximate divide
-// (errors of a few 1e-7 next to a rounding of 2e-3); the fp32 one with the full-precision
-// functions, so that its results keep fp32 accuracy.
+// The bf16 operator evaluates them with the hardware's approximate base-2 exponential and
+// reciprocal (errors of a few 1e-7 next to a rounding of 4e-3; one instruction each, where the
+// intrinsics add range handling that tripled the epilogue's instructions); the fp32 one with the
+// full-precision functions, so that its results keep fp32 accuracy.
 #pragma once
 #include "common.cuh"
 
 namespace moe {
 
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^{-z}); the limits 0 and 1 come out exactly (2^128 and beyond are infinite, 1 / inf = 0)
 template <bool FAST>
 __device__ __forceinline__ float sigmoid_of(float z) {
-  if constexpr (FAST) return sigmoidf_(z);
+  if constexpr (FAST) return rcp_approx(1.0f + ex2_approx(-kLog2e * z));
   return 1.0f / (1.0f + expf(-z));
 }
 
@@ -19,39 +33,31 @@ constexpr float kGeluA = 0.044715f;
 constexpr float kRsqrt2 = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;  // 1 / sqrt(2 pi)
 
-// Q(x) = erfc(|x|) e^{x^2} for the error function, by formula 7.1.26 of Abramowitz and Stegun,
-// Handbook of Mathematical Functions: erf(|x|) = 1 - Q e^{-x^2} with an error of at most 1.5e-7.
-__device__ __forceinline__ float erfc_scaled(float ax) {
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, ax, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  return p * t;
-}
-
-// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and, through g, e^{-z^2 / 2}
-template <bool FAST>
-__device__ __forceinline__ float normal_cdf(float z, float* g) {
-  if constexpr (FAST) {
-    *g = __expf(-0.5f * z * z);
-    const float tail = 0.5f * erfc_scaled(fabsf(z) * kRsqrt2) * *g;  // 1 - Phi(|z|)
-    return z < 0.0f ? tail : 1.0f - tail;
-  } else {
-    *g = expf(-0.5f * z * z);
-    return 0.5f * (1.0f + erff(z * kRsqrt2));
-  }
+// 1 - Phi(|z|) = erfc(|z| / sqrt 2) / 2 for the bf16 operator, by formula 7.1.26 of Abramowitz and
+// Stegun, Handbook of Mathematical Functions (error of erf at most 1.5e-7), its coefficients halved;
+// g receives e^{-z^2 / 2}.
+__device__ __forceinline__ float normal_tail(float z, float* g) {
+  *g = ex2_approx((-0.5f * kLog2e * z) * z);
+  const float t = rcp_approx(fmaf(0.3275911f * kRsqrt2, fabsf(z), 1.0f));
+  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  p = fmaf(p, t, 0.5f * 1.421413741f);
+  p = fmaf(p, t, 0.5f * -0.284496736f);
+  p = fmaf(p, t, 0.5f * 0.254829592f);
+  return p * t * *g;
 }
 
 template <bool FAST, int ACT>
 __device__ __forceinline__ float act_one(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
   if constexpr (ACT == MOE_ACT_GELU) {
+    if constexpr (!FAST) return 0.5f * z * (1.0f + erff(z * kRsqrt2));
+    // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the second term is zero past 100, where inf 0 would be NaN
     float g;
-    return z * normal_cdf<FAST>(z, &g);
+    const float h = 0.5f * z;
+    return fmaf(-fminf(fabsf(z), 100.0f), normal_tail(z, &g), h + fabsf(h));
   }
   // 0.5 (1 + tanh u) = sigmoid(2 u)
-  if constexpr (ACT == MOE_ACT_GELU_TANH) return z * sigmoid_of<FAST>(2.0f * kGeluC * (z + kGeluA * z * z * z));
+  if constexpr (ACT == MOE_ACT_GELU_TANH) return z * sigmoid_of<FAST>(z * fmaf(2.0f * kGeluC * kGeluA * z, z, 2.0f * kGeluC));
   if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid_of<FAST>(z);
   return z;
 }
@@ -60,12 +66,13 @@ template <bool FAST, int ACT>
 __device__ __forceinline__ float act_grad_one(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if constexpr (ACT == MOE_ACT_GELU) {
+    if constexpr (!FAST) return fmaf(z * kRsqrt2Pi, expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * kRsqrt2)));
     float g;
-    const float phi = normal_cdf<FAST>(z, &g);
-    return fmaf(z * kRsqrt2Pi, g, phi);
+    const float tail = normal_tail(z, &g);
+    return fmaf(z * kRsqrt2Pi, g, z < 0.0f ? tail : 1.0f - tail);
   }
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
-    const float s = sigmoid_of<FAST>(2.0f * kGeluC * (z + kGeluA * z * z * z));
+    const float s = sigmoid_of<FAST>(z * fmaf(2.0f * kGeluC * kGeluA * z, z, 2.0f * kGeluC));
     return s + z * (2.0f * s * (1.0f - s)) * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
   }
   if constexpr (ACT == MOE_ACT_SILU) {
@@ -78,7 +85,7 @@ __device__ __forceinline__ float act_grad_one(float z) {
 // One branch for the whole vector: the values of a vector are independent chains, which a
 // branch inside the loop would run one after the other.
 template <bool FAST, int N>
-__device__ __forceinline__ void act_fwd(int act, const float (&z)[N], float (&y)[N]) {
+__device__ __forceinline__ void act_fwd(int act, const float (&z)[N], float (&y)[N]) {  // y may be z
   switch (act) {
 #define MOE_ACT_CASE(A)                                                    \
   case A: {                                                                \
@@ -90,8 +97,9 @@ __device__ __forceinline__ void act_fwd(int act, const float (&z)[N], float (&y)
     MOE_ACT_CASE(MOE_ACT_GELU_TANH)
     MOE_ACT_CASE(MOE_ACT_SILU)
     default:
+      if (y != z)
 #pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = z[i];
+        for (int i = 0; i < N; ++i) y[i] = z[i];
 #undef MOE_ACT_CASE
   }
 }

@@ -195,34 +195,20 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtGemm g, i
 // dz = dy act'(pre), row stride ldz (stored when dz is given), and the column sums of dz (when
 // part is given). Bound by HBM: dy and pre are read once, dz written once. A block of 64 x 4
 // threads owns 64 vectors of VEC columns and a chunk of rows, four rows of it at a time, with
-// the loads of eight steps in flight; it adds its columns in registers, then over its four
+// the loads of four steps in flight; it adds its columns in registers, then over its four
 // row lanes in order.
 constexpr int kDzCols = 64, kDzRows = 4;
 constexpr int kDzSlots = 1216;  // blocks to aim for: 8 for each of 152 SMs
 
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[VEC]) {
-  struct alignas(sizeof(T) * VEC) A {
-    T v[VEC];
-  };
-  const A a = *reinterpret_cast<const A*>(p);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) f[i] = io<T>::to_f(a.v[i]);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
-  struct alignas(sizeof(T) * VEC) A {
-    T v[VEC];
-  };
-  A a;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) a.v[i] = io<T>::cvt(f[i]);
-  *reinterpret_cast<A*>(p) = a;
-}
+struct alignas(sizeof(T) * VEC) Vec {
+  T v[VEC];
+};
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T* dz, float* part, int M, int N,
                                                    int64_t ldz, int act, int per) {
+  using V = Vec<T, VEC>;
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ float red[kDzRows][kDzCols * VEC];
   const int cx = threadIdx.x % kDzCols, ry = threadIdx.x / kDzCols;
@@ -234,21 +220,34 @@ __global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T*
   if (n < N) {
     constexpr int U = 4;  // rows in flight
     for (int m = blockIdx.y * per + ry; m < m1; m += U * kDzRows) {
-      float d[U][VEC], z[U][VEC];
+      V d[U], z[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (m + u * kDzRows < m1) {
           const int64_t o = (int64_t)(m + u * kDzRows) * N + n;
-          load_vec<T, VEC>(dy + o, d[u]);
-          if (pre) load_vec<T, VEC>(pre + o, z[u]);
+          d[u] = *reinterpret_cast<const V*>(dy + o);
+          if (pre) z[u] = *reinterpret_cast<const V*>(pre + o);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (m + u * kDzRows < m1) {
-          if (pre) act_grad_mul<sizeof(T) == 2, VEC>(act, z[u], d[u]);
-          if (dz) store_vec<T, VEC>(dz + (int64_t)(m + u * kDzRows) * ldz + n, d[u]);
+          float f[VEC];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) sum[i] += d[u][i];
+          for (int i = 0; i < VEC; ++i) f[i] = io<T>::to_f(d[u].v[i]);
+          if (pre) {
+            float zf[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) zf[i] = io<T>::to_f(z[u].v[i]);
+            act_grad_mul<sizeof(T) == 2, VEC>(act, zf, f);
+          }
+          if (dz) {
+            V out;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) out.v[i] = io<T>::cvt(f[i]);
+            *reinterpret_cast<V*>(dz + (int64_t)(m + u * kDzRows) * ldz + n) = out;
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) sum[i] += f[i];
         }
     }
   }

@@ -53,6 +53,7 @@ struct Cfg {
 struct TcArgs {
   LinearGemm g;
   int kblocks, mt, nt;
+  int items, whole;  // work items; the first `whole` are tiles, the others halves (BN / 2 columns) of one
 };
 
 // byte offset of 16-byte piece j of row r in a 128-byte-swizzled staging tile
@@ -80,14 +81,26 @@ __device__ __forceinline__ void rows_out(__nv_bfloat16* dst, int64_t ld, uint32_
     }
 }
 
-// Tiles run down eight row blocks before they move to the next columns, so the tiles in
-// flight share a few row and column blocks in L2.
-__device__ __forceinline__ void tile_at(const TcArgs& a, int t, int* m, int* n) {
+// Tiles run down eight row blocks before they move to the next columns, so the tiles in flight
+// share a few row and column blocks in L2. The tiles of a last round that would leave half of the
+// units idle are given out as two halves each: 4096 x 4096 outputs are 256 tiles for 76 CTA pairs,
+// 3.5 rounds in place of 4.
+struct Item {
+  int m, n0, half;  // row block, first column, whether BN / 2 columns
+};
+template <int BN>
+__device__ __forceinline__ Item item_at(const TcArgs& a, int t) {
   constexpr int G = 8;
+  Item it;
+  it.half = t >= a.whole;
+  const int h = t - a.whole;
+  if (it.half) t = a.whole + (h >> 1);
   const int grp = t / (G * a.nt), r = t - grp * (G * a.nt);
   const int rows = min(G, a.mt - grp * G);
-  *n = r / rows;
-  *m = grp * G + (r - *n * rows);
+  const int n = r / rows;
+  it.m = grp * G + (r - n * rows);
+  it.n0 = n * BN + (it.half ? (h & 1) * (BN / 2) : 0);
+  return it;
 }
 
 // VEC: the rows of y, pre and the residual are multiples of 16 bytes (N % 8 == 0); else they are
@@ -140,7 +153,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
   const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
-  const int total = args.mt * args.nt;
+  const int total = args.items;
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
@@ -153,10 +166,11 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     for (int s = 0; s < C::STAGES; ++s) issued[s] = -1;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
-      int mt, nt;
-      tile_at(args, t, &mt, &nt);
-      const int m0 = mt * C::TILE_M + (int)rank * 128;
-      const int n0 = nt * BN + (int)rank * C::BCOLS;
+      const Item it = item_at<BN>(args, t);
+      const int m0 = it.m * C::TILE_M + (int)rank * 128;
+      const int bcols = it.half ? C::BCOLS / 2 : C::BCOLS;
+      const int n0 = it.n0 + (int)rank * bcols;
+      const uint32_t bytes = C::A_BYTES + bcols * kBK * 2;
       for (int kb = 0; kb < args.kblocks; ++kb) {
         if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
           ok = false;
@@ -164,7 +178,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         }
         const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES), sb = sa + C::A_BYTES;
         const uint32_t fb = full0 + stage * 8;
-        if (leader) mbar_arrive_expect_tx(&full[stage], CTAS * C::STAGE_BYTES);
+        if (leader) mbar_arrive_expect_tx(&full[stage], CTAS * bytes);
         issued[stage] = (int)phase;
         auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
           if constexpr (PAIR) tma_load_2d_pair(dst, map, fb, c0, c1);
@@ -178,9 +192,11 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         }
         if (g.b_mn) {
 #pragma unroll
-          for (int c = 0; c < C::BCOLS / 64; ++c) load(sb + c * kChunkBytes, &tmB, n0 + c * 64, kb * kBK);
-        } else {
+          for (int c = 0; c < C::BCOLS / 64; ++c)
+            if (c * 64 < bcols) load(sb + c * kChunkBytes, &tmB, n0 + c * 64, kb * kBK);
+        } else {  // boxes of BCOLS / 2 rows
           load(sb, &tmB, kb * kBK, n0);
+          if (!it.half) load(sb + C::B_BYTES / 2, &tmB, kb * kBK, n0 + C::BCOLS / 2);
         }
         if (++stage == C::STAGES) {
           stage = 0;
@@ -194,7 +210,9 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         if (issued[s] >= 0) mbar_wait_timed(&full[s], (uint32_t)issued[s], 200000000ull);
   } else if (warp == 1 && lane == 0 && leader) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = idesc_bf16(C::TILE_M, BN, g.a_mn, g.b_mn);
+    const uint32_t idesc_whole = idesc_bf16(C::TILE_M, BN, g.a_mn, g.b_mn);
+    const uint32_t idesc_half = idesc_bf16(C::TILE_M, BN / 2, g.a_mn, g.b_mn);
+    uint32_t idesc = idesc_whole;
     const uint32_t sa0 = smem_u32(smem);
     const uint64_t ad0 = g.a_mn ? sdesc_sw128(sa0, kChunkBytes, 1024) : sdesc_sw128(sa0, 16, 1024);
     const uint64_t bd0 =
@@ -215,6 +233,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       if (!free_acc) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+      idesc = t >= args.whole ? idesc_half : idesc_whole;
       for (int kb = 0; kb < args.kblocks; ++kb) {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag)) {
           ok = false;
@@ -247,23 +266,22 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     const int q = warp & 3;    // the tensor-memory lane quarter this warp may read
     const int ew = warp - 2;
     const uint32_t tile = smem_u32(smem + C::EPI_OFF + ew * 2 * kStage);
-    constexpr int CW = BN / 64 / 2;  // 64-column chunks of this warp
-    const int c0 = (ew / 4) * CW;
     const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
     const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
     int acc_i = 0;
     int sc = 0;  // chunks stored so far
     for (int t = unit; t < total; t += units) {
-      int mt, nt;
-      tile_at(args, t, &mt, &nt);
-      const int64_t row0 = (int64_t)mt * C::TILE_M + (int)rank * 128 + q * 32;  // this warp's first row
+      const Item it = item_at<BN>(args, t);
+      const int cw = BN / 64 / (it.half ? 4 : 2);  // 64-column chunks of this warp
+      const int c0 = (ew / 4) * cw;
+      const int64_t row0 = (int64_t)it.m * C::TILE_M + (int)rank * 128 + q * 32;  // this warp's first row
       const int rows = (int)min((int64_t)32, (int64_t)g.M - row0);              // rows of it that exist
       const int acc = acc_i & 1;
       if (!mbar_wait_bounded(&tfull[acc], (uint32_t)((acc_i >> 1) & 1), abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      for (int c = c0; c < c0 + CW; ++c) {
-        const int n0 = nt * BN + c * 64;
+      for (int c = c0; c < c0 + cw; ++c) {
+        const int n0 = it.n0 + c * 64;
         if (rows <= 0 || n0 >= g.N) continue;  // the same for the whole warp
         const int cols = min(64, g.N - n0);    // with VEC a multiple of 8
         // With a second output z takes one tile and y the other; else y alternates between the
@@ -290,48 +308,62 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         uint32_t v[2][32];
         tmem_ld32_async(taddr + c * 64, v[0]);
         tmem_ld32_async(taddr + c * 64 + 32, v[1]);
+        // the bias travels beside the accumulator; every lane needs the same 64 values
+        uint4 bv[8];
+        if (VEC && bias) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            bv[j] = 8 * j < cols ? __ldg(reinterpret_cast<const uint4*>(bias + n0 + 8 * j)) : make_uint4(0, 0, 0, 0);
+        }
         tmem_ld_wait(v[0]);
         tmem_ld_order(v[1]);
-        if (res) {
-          if constexpr (VEC) cp_async_wait<0>();
-          __syncwarp();
-        }
+        float z[64];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float z[8], y[8];
+        for (int i = 0; i < 64; ++i) z[i] = __uint_as_float(v[i >> 5][i & 31]);
+        if (bias) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[j >> 2][(j & 3) * 8 + i]);
-          if (bias && 8 * j < cols) {
+          for (int j = 0; j < 8; ++j) {
             float b[8];
             if constexpr (VEC) {
-              bf16x8_to_f(__ldg(reinterpret_cast<const uint4*>(bias + n0 + 8 * j)), b);
+              bf16x8_to_f(bv[j], b);
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i) b[i] = 8 * j + i < cols ? __bfloat162float(bias[n0 + 8 * j + i]) : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] += b[i];
+            for (int i = 0; i < 8; ++i) z[8 * j + i] += b[i];
           }
-          act_fwd<true, 8>(g.act, z, y);
-          if (res) {
+        }
+        if (g.pre) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z + 8 * j));
+        }
+        act_fwd<true, 64>(g.act, z, z);  // 64 independent chains: two warps a scheduler have little else to hide latency
+        if (res) {
+          if constexpr (VEC) cp_async_wait<0>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
             float b[8];
             bf16x8_to_f(ld_shared_v4(ty + piece(lane, j)), b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += b[i];
+            for (int i = 0; i < 8; ++i) z[8 * j + i] += b[i];
           }
-          if (g.pre) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z));
-          if (!g.out_f32) {  // over the residual piece this lane has just read
-            st_shared_v4(ty + piece(lane, j), f_to_bf16x8(y));
-          } else if (lane < rows && 8 * j < cols) {
-            float* of = reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0 + 8 * j;
+        }
+        if (!g.out_f32) {  // over the residual pieces this lane has just read
+#pragma unroll
+          for (int j = 0; j < 8; ++j) st_shared_v4(ty + piece(lane, j), f_to_bf16x8(z + 8 * j));
+        } else if (lane < rows) {
+          float* o = reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
             if constexpr (VEC) {
-              float4* o = reinterpret_cast<float4*>(of);
-              o[0] = make_float4(y[0], y[1], y[2], y[3]);
-              o[1] = make_float4(y[4], y[5], y[6], y[7]);
+              if (4 * j < cols)
+                *reinterpret_cast<float4*>(o + 4 * j) = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
             } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (8 * j + i < cols) of[i] = y[i];
+              for (int i = 0; i < 4; ++i)
+                if (4 * j + i < cols) o[4 * j + i] = z[4 * j + i];
             }
           }
         }
@@ -666,7 +698,7 @@ cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   CUtensorMap mA, mB, mY, mP;
   bool ok = g.a_mn ? make_map(&mA, g.A, g.K, g.M, g.lda, kBK) : make_map(&mA, g.A, g.M, g.K, g.lda, 128);
-  ok = ok && (g.b_mn ? make_map(&mB, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mB, g.B, g.N, g.K, g.ldb, C::BCOLS));
+  ok = ok && (g.b_mn ? make_map(&mB, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mB, g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
   mY = mP = mA;  // where unused
   if (VEC && !g.out_f32) ok = ok && make_map(&mY, g.y, g.M, g.N, g.N, 32);
   if (VEC && g.pre) ok = ok && make_map(&mP, g.pre, g.M, g.N, g.N, 32);
@@ -676,9 +708,11 @@ cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   a.kblocks = (g.K + kBK - 1) / kBK;
   a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
   a.nt = (g.N + BN - 1) / BN;
-  const int64_t total = (int64_t)a.mt * a.nt;
+  const int64_t total = (int64_t)a.mt * a.nt, units = sms / CTAS, last = total % units;
   if (total >= (1ll << 30)) return cudaErrorInvalidValue;
-  LaunchCfg l(dim3((unsigned)(CTAS * std::min<int64_t>(total, sms / CTAS))), C::THREADS, C::SMEM, st, CTAS);
+  a.whole = (int)(2 * last <= units ? total - last : total);
+  a.items = (int)(total + (total - a.whole));
+  LaunchCfg l(dim3((unsigned)(CTAS * std::min<int64_t>(a.items, units))), C::THREADS, C::SMEM, st, CTAS);
   return cudaLaunchKernelEx(&l.cfg, kern, mA, mB, mY, mP, a);
 }
 
