@@ -412,8 +412,7 @@ struct SplitCfg {
   static constexpr int THREADS = 192;  // producer, MMA issuer, four epilogue warps
   static constexpr int A_BYTES = 128 * kBK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + NB * kBK * 2;
-  // up to 64 tokens two CTAs share an SM
-  static constexpr int STAGES = (NB <= 64 ? 110592 : 196608) / STAGE_BYTES;
+  static constexpr int STAGES = 110592 / STAGE_BYTES;  // two CTAs share an SM
   static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
   static constexpr uint32_t TMEM_COLS = NB < 32 ? 32 : NB;
@@ -693,6 +692,7 @@ template <int CTAS, int BN, bool VEC>
 cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   using C = Cfg<CTAS, BN>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
+  static_assert(CTAS == 1 || BN == 256, "the epilogue's warps need four chunks to share a half tile");
   auto kern = k_linear_tc<CTAS, BN, VEC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -710,7 +710,7 @@ cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
   a.nt = (g.N + BN - 1) / BN;
   const int64_t total = (int64_t)a.mt * a.nt, units = sms / CTAS, last = total % units;
   if (total >= (1ll << 30)) return cudaErrorInvalidValue;
-  a.whole = (int)(2 * last <= units ? total - last : total);
+  a.whole = (int)(CTAS == 2 && 2 * last <= units ? total - last : total);
   a.items = (int)(total + (total - a.whole));
   LaunchCfg l(dim3((unsigned)(CTAS * std::min<int64_t>(a.items, units))), C::THREADS, C::SMEM, st, CTAS);
   return cudaLaunchKernelEx(&l.cfg, kern, mA, mB, mY, mP, a);
@@ -750,34 +750,63 @@ cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
   }
 }
 
-cudaError_t launch_split(const LinearGemm& g, int nb, int S, cudaStream_t st) {
-  switch (nb) {
-    case 16: return launch_split_nb<16>(g, S, st);
-    case 32: return launch_split_nb<32>(g, S, st);
-    case 64: return launch_split_nb<64>(g, S, st);
-    case 128: return launch_split_nb<128>(g, S, st);
-    default: return launch_split_nb<256>(g, S, st);
+// ---------------------------------------------------------------- choice of the variant
+// Estimated time (us) of each variant, from its rounds over the GPU and its k-blocks per round. The
+// constants are a least-squares fit to 114 products (forward, dx and dw for M = 1 .. 8192 and
+// weights 256x256 .. 4096x4096 and 1024x8192, every variant timed on each, caches cold); the
+// variant with the least estimate is 1.8% slower than the best of all on average, 34% at worst.
+// Measured examples (us), pair / single / split with its best cluster:
+//   M = 16,   K = 4096, N = 4096:   23.4 / 21.9 / 9.4 (16 tokens, 4 CTAs)
+//   M = 512,  K = 512,  N = 512:     7.2 /  6.0 / 4.9 (64 tokens, 4 CTAs)
+//   M = 4096, K = 2048, N = 128:    14.9 / 13.5 / 9.3 (64 tokens, 4 CTAs)
+//   M = 2048, K = 4096, N = 4096:   46.3 / 78.3 / 92.7
+// A k-block costs 0.3 us in a tile (its load's latency over the ring) and 0.26 us in a split part;
+// a round of tiles costs its epilogue; a split part costs its share of the tokens, and more where
+// two CTAs share an SM.
+struct Choice {
+  int nb, S;  // nb 0: tiles, of 128 x 128 (S = 1) or 256 x 256 on CTA pairs (S = 2)
+};
+
+double tile_estimate(const LinearGemm& g, int b, int64_t units, int kb, double c0, double ck, double cr) {
+  const int64_t t = (int64_t)((g.M + b - 1) / b) * ((g.N + b - 1) / b), last = t % units;
+  const double rounds = (double)(t / units) + (last == 0 ? 0.0 : t > units && 2 * last <= units ? 0.5 : 1.0);
+  return c0 + rounds * (ck * kb + cr);
+}
+
+Choice choose(const LinearGemm& g, int kb, int sms) {
+  Choice best = {0, 1};
+  double t = tile_estimate(g, 128, sms, kb, 1.56, 0.302, 1.25);
+  const double pair = tile_estimate(g, 256, sms / 2, kb, 2.23, 0.300, 3.05);
+  if (pair < t) {
+    t = pair;
+    best = {0, 2};
   }
+  // an MN-major token matrix is read in chunks of 64 tokens
+  for (int nb = g.a_mn ? 64 : 16; nb <= 64 && (nb < 2 * g.M || nb == 16 || g.a_mn); nb *= 2) {
+    const int64_t tiles = (int64_t)((g.M + nb - 1) / nb) * ((g.N + 127) / 128);
+    for (int S = 1; S <= 8 && S <= kb; S *= 2) {
+      const double rounds = (double)((tiles * S + 2 * sms - 1) / (2 * sms));
+      const double kbs = (double)((kb + S - 1) / S), shared = tiles * S > sms ? 1.0 : 0.0;
+      const double e = 1.82 + (S > 1 ? 1.87 : 0.0) + rounds * (kbs * (0.26 + 0.048 * nb / 64) + 0.034 * nb / S) +
+                       shared * (1.81 * rounds + 0.073 * S);
+      if (e < t) {
+        t = e;
+        best = {nb, S};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
-  const int kblocks = (g.K + kBK - 1) / kBK;
-  const int64_t t256 = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
-  const int64_t t128 = (int64_t)((g.M + 127) / 128) * ((g.N + 127) / 128);
+  const Choice c = choose(g, (g.K + kBK - 1) / kBK, sms);
   const bool vec = g.N % 8 == 0;
-  if (t128 * 2 <= sms || g.M <= 64) {
-    int nb = 16;
-    while (nb < 256 && nb < g.M) nb *= 2;
-    if (g.a_mn && nb < 64) nb = 64;
-    const int64_t tiles = (int64_t)((g.M + nb - 1) / nb) * ((g.N + 127) / 128);
-    const int slots = sms * (nb <= 64 ? 2 : 1);
-    int S = 1;
-    while (S < 8 && 2 * S <= kblocks && tiles * 2 * S <= slots) S *= 2;
-    return launch_split(g, nb, S, st);
-  }
-  if (g.M > 128 && t256 * 2 >= sms) return vec ? launch_tile<2, 256, true>(g, sms, st) : launch_tile<2, 256, false>(g, sms, st);
+  if (c.nb == 16) return launch_split_nb<16>(g, c.S, st);
+  if (c.nb == 32) return launch_split_nb<32>(g, c.S, st);
+  if (c.nb == 64) return launch_split_nb<64>(g, c.S, st);
+  if (c.S == 2) return vec ? launch_tile<2, 256, true>(g, sms, st) : launch_tile<2, 256, false>(g, sms, st);
   return vec ? launch_tile<1, 128, true>(g, sms, st) : launch_tile<1, 128, false>(g, sms, st);
 }
 
