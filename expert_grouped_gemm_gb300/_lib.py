@@ -36,7 +36,8 @@ EXPORTED = ["moe_workspace_size", "moe_fwd", "moe_select_retained", "moe_bwd", "
             "moe_last_error", "moe_workspace_entry", "moe_kernel_launches", "moe_timing_enable",
             "moe_timing_read", "moe_route_noalloc", "moe_plan_quota", "moe_selftest_wait", "moe_fwd_decode",
             "moe_selftest_decode_wait", "moe_norm_workspace_size", "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd",
-            "moe_gate_bwd", "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd"]
+            "moe_gate_bwd", "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd",
+            "moe_fwd_routed", "moe_bwd_routed"]
 
 
 class MoeError(RuntimeError):
@@ -111,9 +112,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moe_gate_bwd.argtypes = [GD] + [vp] * 5
     lib.moe_linear_workspace_size.argtypes = [LD, ctypes.POINTER(sz)]
     lib.moe_linear_fwd.argtypes = [LD, vp, sz] + [vp] * 7
-    lib.moe_linear_bwd.argtypes = [LD, vp, sz] + [vp] * 8
+    lib.moe_linear_bwd.argtypes = [LD, vp, sz] + [vp] * 9
+    lib.moe_fwd_routed.argtypes = [D, vp, sz] + [vp] * 13
+    lib.moe_bwd_routed.argtypes = [D, vp, sz] + [vp] * 3 + [ctypes.c_int] + [vp] * 8
     for name in ["moe_norm_workspace_size", "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd",
-                 "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd"]:
+                 "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd", "moe_fwd_routed", "moe_bwd_routed"]:
         getattr(lib, name).restype = ctypes.c_int
     for name in ["moe_workspace_size", "moe_fwd", "moe_fwd_decode", "moe_selftest_decode_wait", "moe_select_retained",
                  "moe_bwd", "moe_read_status",
@@ -239,6 +242,33 @@ def moe_bwd(dims: Dims, ws: torch.Tensor, dy, x, use_retained, dx, dw_router=Non
         _ptr(dw_router, "dw_router", io, False), _ptr(dw_gate, "dw_gate", io, False), _ptr(dw_up, "dw_up", io, False),
         _ptr(dw_down, "dw_down", io, False), _ptr(dws_gate, "dws_gate", io, False),
         _ptr(dws_up, "dws_up", io, False), _ptr(dws_down, "dws_down", io, False))
+    _check(rc)
+
+
+def moe_fwd_routed(dims: Dims, ws: torch.Tensor, x, topk_idx, topk_w, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, y,
+                   expert_offsets=None, row_of_pair=None, stream=None):
+    """moe_fwd with the caller's experts and weights of every token in place of the router."""
+    io = _io_dtype(dims)
+    rc = load().moe_fwd_routed(
+        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _ptr(x, "x", io),
+        _ptr(topk_idx, "topk_idx", torch.int32), _ptr(topk_w, "topk_w", torch.float32),
+        _ptr(w_gate, "w_gate", io), _ptr(w_up, "w_up", io), _ptr(w_down, "w_down", io),
+        _ptr(ws_gate, "ws_gate", io, False), _ptr(ws_up, "ws_up", io, False), _ptr(ws_down, "ws_down", io, False),
+        _ptr(y, "y", io), _ptr(expert_offsets, "expert_offsets", torch.int32, False),
+        _ptr(row_of_pair, "row_of_pair", torch.int32, False))
+    _check(rc)
+
+
+def moe_bwd_routed(dims: Dims, ws: torch.Tensor, dy, x, use_retained, dx, dtopk_w, dw_gate=None, dw_up=None, dw_down=None,
+                   dws_gate=None, dws_up=None, dws_down=None, stream=None):
+    """moe_bwd after moe_fwd_routed: dtopk_w receives the gradient of the routing weights."""
+    io = _io_dtype(dims)
+    rc = load().moe_bwd_routed(
+        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
+        _ptr(x, "x", io), 1 if use_retained else 0, _ptr(dx, "dx", io), _ptr(dtopk_w, "dtopk_w", torch.float32),
+        _ptr(dw_gate, "dw_gate", io, False), _ptr(dw_up, "dw_up", io, False), _ptr(dw_down, "dw_down", io, False),
+        _ptr(dws_gate, "dws_gate", io, False), _ptr(dws_up, "dws_up", io, False),
+        _ptr(dws_down, "dws_down", io, False))
     _check(rc)
 
 
@@ -388,15 +418,15 @@ def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stre
         _tensor(pre, "pre", io, mn, False)))
 
 
-def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=None, stream=None):
-    """Gradients of moe_linear_fwd; pre is needed when the activation is not 'none'."""
+def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=None, dx_add=None, stream=None):
+    """Gradients of moe_linear_fwd; pre is needed when the activation is not 'none'. dx_add is added to dx."""
     io = _io_dtype(dims)
     M, K, N = dims.M, dims.K, dims.N
     mn, mk, kn = (M, N), (M, K), (K, N)
     _check(load().moe_linear_bwd(
         dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, mn),
         _tensor(x, "x", io, mk), _tensor(w, "w", io, kn), _tensor(pre, "pre", io, mn, False),
-        _tensor(dx, "dx", io, mk, False), _tensor(dw, "dw", io, kn, False),
+        _tensor(dx_add, "dx_add", io, mk, False), _tensor(dx, "dx", io, mk, False), _tensor(dw, "dw", io, kn, False),
         _tensor(dbias, "dbias", io, (N,), False)))
 
 

@@ -354,6 +354,13 @@ __global__ void __launch_bounds__(256) k_router_bwd(const float* g, const int* r
   }
 }
 
+// dtopk_w of pair p = <dY_t, y_pair> (the pair score kernel's g), pair order
+__global__ void __launch_bounds__(256) k_pair_dw(const float* g, const int* rowp_of_pair, int64_t P, float* dtopk_w) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  for (int64_t p = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; p < P; p += (int64_t)gridDim.x * blockDim.x)
+    dtopk_w[p] = g[rowp_of_pair[p]];
+}
+
 // 32x32 tiled transpose: out[c][r] = in[r][c], in is [R, Cc].
 template <typename TIO>
 __global__ void k_transpose(const TIO* in, int R, int Cc, TIO* out) {
@@ -381,6 +388,7 @@ __global__ void __launch_bounds__(256) k_dx_reduce(const TIO* __restrict__ dx_pa
                                                    const TIO* __restrict__ wrT, const TIO* __restrict__ sh_dx, int T,
                                                    int H, int k, TIO* __restrict__ dx) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
+  const int kr = wrT ? k : 0;  // slots with a router term
   if constexpr (sizeof(TIO) == 2) {
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
       const int64_t p0 = (int64_t)t * k;
@@ -403,14 +411,14 @@ __global__ void __launch_bounds__(256) k_dx_reduce(const TIO* __restrict__ dx_pa
             }
           }
         }
-        for (int j0 = 0; j0 < k; j0 += 8) {
+        for (int j0 = 0; j0 < kr; j0 += 8) {
           uint4 u[8];
 #pragma unroll
           for (int jj = 0; jj < 8; ++jj)
-            if (j0 + jj < k) u[jj] = reinterpret_cast<const uint4*>(wrT + (int64_t)topk_idx[p0 + j0 + jj] * H)[i];
+            if (j0 + jj < kr) u[jj] = reinterpret_cast<const uint4*>(wrT + (int64_t)topk_idx[p0 + j0 + jj] * H)[i];
 #pragma unroll
           for (int jj = 0; jj < 8; ++jj) {
-            if (j0 + jj < k) {
+            if (j0 + jj < kr) {
               const float d = dl_sel[p0 + j0 + jj];
               bf16x8_to_f(u[jj], f);
 #pragma unroll
@@ -436,7 +444,7 @@ __global__ void __launch_bounds__(256) k_dx_reduce(const TIO* __restrict__ dx_pa
           const int cr = crow_of_pair[p0 + j];
           if (cr >= 0) acc += io<TIO>::to_f(dx_pair[(int64_t)cr * H + i]);
         }
-        for (int j = 0; j < k; ++j)
+        for (int j = 0; j < kr; ++j)
           acc = fmaf(dl_sel[p0 + j], io<TIO>::to_f(wrT[(int64_t)topk_idx[p0 + j] * H + i]), acc);
         if (sh_dx) acc += io<TIO>::to_f(sh_dx[(int64_t)t * H + i]);
         dx[(int64_t)t * H + i] = io<TIO>::cvt(acc);
@@ -524,6 +532,13 @@ cudaError_t launch_router_bwd(const float* g, const int* rowp_of_pair, const int
   return cudaGetLastError();
 }
 
+cudaError_t launch_pair_dw(const float* g, const int* rowp_of_pair, int64_t P, float* dtopk_w, int num_sms,
+                           cudaStream_t st) {
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>((P + 255) / 256, (int64_t)num_sms * 8));
+  MOE_LAUNCH(k_pair_dw, grid, 256, 0, st, g, rowp_of_pair, P, dtopk_w);
+  return cudaGetLastError();
+}
+
 template <typename TIO>
 cudaError_t launch_transpose(const void* in, int R, int Cc, void* out, cudaStream_t st) {
   dim3 grid((Cc + 31) / 32, (R + 31) / 32), block(32, 8);
@@ -546,13 +561,14 @@ __global__ void __launch_bounds__(256) k_dx_reduce_k8(const __nv_bfloat16* __res
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int lane = threadIdx.x & 31, wpb = blockDim.x >> 5;
   const int nv = H / 8;
+  const int kr = wrT ? k : 0;  // slots with a router term
   for (int t = blockIdx.x * wpb + (threadIdx.x >> 5); t < T; t += gridDim.x * wpb) {
     int c = -1, ex = 0;
     float d = 0.0f;
     if (lane < k) {
       c = crow_of_pair[(int64_t)t * k + lane];
       ex = topk_idx[(int64_t)t * k + lane];
-      d = dl_sel[(int64_t)t * k + lane];
+      if (kr) d = dl_sel[(int64_t)t * k + lane];
     }
     int cj[8], ej[8];
     float dj[8];
@@ -567,7 +583,7 @@ __global__ void __launch_bounds__(256) k_dx_reduce_k8(const __nv_bfloat16* __res
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         u[j] = cj[j] >= 0 ? reinterpret_cast<const uint4*>(dx_pair + (int64_t)cj[j] * H)[i] : make_uint4(0, 0, 0, 0);
-        v[j] = j < k ? reinterpret_cast<const uint4*>(wrT + (int64_t)ej[j] * H)[i] : make_uint4(0, 0, 0, 0);
+        v[j] = j < kr ? reinterpret_cast<const uint4*>(wrT + (int64_t)ej[j] * H)[i] : make_uint4(0, 0, 0, 0);
       }
       float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0}, f[8];
 #pragma unroll
@@ -580,7 +596,7 @@ __global__ void __launch_bounds__(256) k_dx_reduce_k8(const __nv_bfloat16* __res
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j < k) {
+        if (j < kr) {
           bf16x8_to_f(v[j], f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) acc[q] = fmaf(dj[j], f[q], acc[q]);

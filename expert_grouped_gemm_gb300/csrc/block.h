@@ -32,7 +32,7 @@ size_t linear_workspace_bytes(const moe_linear_dims& d);
 cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x, const void* w, const void* bias,
                               const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches);
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,
-                              const void* pre, void* dx, void* dw, void* dbias, int sms, cudaStream_t st,
-                              int* launches);
+                              const void* pre, const void* dx_add, void* dx, void* dw, void* dbias, int sms,
+                              cudaStream_t st, int* launches);
 
 }  // namespace moe

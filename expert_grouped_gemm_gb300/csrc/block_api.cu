@@ -195,17 +195,19 @@ int moe_linear_fwd(const moe_linear_dims* dims, void* ws, size_t ws_bytes, void*
 }
 
 int moe_linear_bwd(const moe_linear_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy, const void* x,
-                   const void* w, const void* pre, void* dx, void* dw, void* dbias) {
+                   const void* w, const void* pre, const void* dx_add, void* dx, void* dw, void* dbias) {
   int rc;
   if ((rc = check_linear(dims)) || (rc = check_workspace(ws, ws_bytes, linear_workspace_bytes(*dims))) ||
       (rc = check_ptr(dy, "dy", true)) || (rc = check_ptr(x, "x", dw != nullptr)) ||
       (rc = check_ptr(w, "w", dx != nullptr)) || (rc = check_ptr(pre, "pre", dims->act != MOE_ACT_NONE)) ||
-      (rc = check_ptr(dx, "dx", false)) || (rc = check_ptr(dw, "dw", false)) ||
+      (rc = check_ptr(dx_add, "dx_add", false)) || (rc = check_ptr(dx, "dx", false)) ||
+      (rc = check_ptr(dw, "dw", false)) ||
       (rc = check_ptr(dbias, "dbias", false)))
     return rc;
+  if (dx_add && !dx) return bad(MOE_ERR_INVALID_ARG, "dx_add given without dx");
   if (dims->act == MOE_ACT_NONE && pre) return bad(MOE_ERR_INVALID_ARG, "pre must be null for MOE_ACT_NONE");
   int n = 0;
-  const cudaError_t e = launch_linear_bwd(*dims, ws, dy, x, w, pre, dx, dw, dbias, sm_count(),
+  const cudaError_t e = launch_linear_bwd(*dims, ws, dy, x, w, pre, dx_add, dx, dw, dbias, sm_count(),
                                           static_cast<cudaStream_t>(stream), &n);
   return finish(e, "moe_linear_bwd", n);
 }

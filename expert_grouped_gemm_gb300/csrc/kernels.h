@@ -16,6 +16,9 @@ cudaError_t launch_route_topk(float* logits, const float* bias, int T, int E, in
                               uint64_t* masks, cudaStream_t st, const float* part = nullptr, int nsplit = 1,
                               int64_t part_stride = 0, bool masks_clear = false, float* logits_out = nullptr,
                               int* topk_idx_out = nullptr, float* topk_w_out = nullptr);
+// The caller's routing in place of the top-k kernel's; the chunk masks must be zero.
+cudaError_t launch_route_given(const int* idx, const float* w, int T, int E, int k, int* topk_idx, float* topk_w,
+                               uint64_t* masks, int* status, cudaStream_t st);
 cudaError_t launch_route_scan(const uint64_t* masks, int C, int E, int* count, int* offset, int* pad_off,
                               int* tile_off, int* chunk_base, int* pair_of_row, int* user_offsets, cudaStream_t st,
                               int* order = nullptr, int* tile_off2 = nullptr, int4* tile_rec = nullptr,
@@ -61,8 +64,12 @@ template <typename TIO>
 cudaError_t launch_router_bwd(const float* g, const int* rowp_of_pair, const int* topk_idx, const float* topk_w,
                               int T, int Tpad, int E, int k, float* dl_sel, void* dl_dense, int num_sms,
                               cudaStream_t st);
+// dtopk_w[t, j] = g of the pair's row: the gradient of a caller's routing weights.
+cudaError_t launch_pair_dw(const float* g, const int* rowp_of_pair, int64_t P, float* dtopk_w, int num_sms,
+                           cudaStream_t st);
 template <typename TIO>
 cudaError_t launch_transpose(const void* in, int R, int Cc, void* out, cudaStream_t st);
+// wrT null: no router term.
 template <typename TIO>
 cudaError_t launch_dx_reduce(const void* dx_pair, const int* crow_of_pair, const int* topk_idx, const float* dl_sel,
                              const void* wrT, const void* sh_dx, int T, int H, int k, void* dx, int num_sms,

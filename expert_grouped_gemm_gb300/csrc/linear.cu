@@ -422,7 +422,7 @@ cudaError_t fwd_bf16(const moe_linear_dims& d, char* ws, const void* x, const vo
 }
 
 cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const void* x, const void* w, const void* pre,
-                     void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
+                     const void* dx_add, void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
   const LinearWs L = layout(d);
   const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
   float* part = reinterpret_cast<float*>(ws + L.part);
@@ -436,7 +436,7 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
   if (e == cudaSuccess && dbias) e = run_dbias<__nv_bfloat16>(d, part, dbias, st, launches);
   if (e == cudaSuccess && dx) {
     if ((e = packed(&w, ws + L.wp, K, N, sms, st, launches)) != cudaSuccess) return e;
-    LinearGemm g = {M, K, N, dz, w, up8(N), up8(N), 0, 0, nullptr, nullptr, dx, nullptr, MOE_ACT_NONE, 0, status};
+    LinearGemm g = {M, K, N, dz, w, up8(N), up8(N), 0, 0, nullptr, dx_add, dx, nullptr, MOE_ACT_NONE, 0, status};
     *launches += 1;
     e = launch_linear_tc(g, sms, st);
   }
@@ -452,7 +452,7 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
 const float* f(const void* p) { return static_cast<const float*>(p); }
 
 cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const void* x, const void* w, const void* pre,
-                    void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
+                    const void* dx_add, void* dx, void* dw, void* dbias, int sms, cudaStream_t st, int* launches) {
   const LinearWs L = layout(d);
   const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
   float* part = reinterpret_cast<float*>(ws + L.part);
@@ -462,7 +462,7 @@ cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const vo
   if (store || dbias) e = run_dz<float>(d, dy, pre, store ? ws + L.dz : nullptr, N, dbias ? part : nullptr, st, launches);
   if (e == cudaSuccess && dbias) e = run_dbias<float>(d, part, dbias, st, launches);
   if (e == cudaSuccess && dx) {
-    SimtGemm g = {f(dz), f(w), N, 1, 1, N, M, N, K, nullptr, nullptr, (float*)dx, nullptr, MOE_ACT_NONE};
+    SimtGemm g = {f(dz), f(w), N, 1, 1, N, M, N, K, nullptr, f(dx_add), (float*)dx, nullptr, MOE_ACT_NONE};
     e = run_f32(g, sms, st, launches);
   }
   if (e == cudaSuccess && dw) {
@@ -486,10 +486,10 @@ cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x,
 }
 
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,
-                              const void* pre, void* dx, void* dw, void* dbias, int sms, cudaStream_t st,
-                              int* launches) {
-  return d.dtype == MOE_BF16 ? bwd_bf16(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, sms, st, launches)
-                             : bwd_f32(d, static_cast<char*>(ws), dy, x, w, pre, dx, dw, dbias, sms, st, launches);
+                              const void* pre, const void* dx_add, void* dx, void* dw, void* dbias, int sms,
+                              cudaStream_t st, int* launches) {
+  return d.dtype == MOE_BF16 ? bwd_bf16(d, static_cast<char*>(ws), dy, x, w, pre, dx_add, dx, dw, dbias, sms, st, launches)
+                             : bwd_f32(d, static_cast<char*>(ws), dy, x, w, pre, dx_add, dx, dw, dbias, sms, st, launches);
 }
 
 }  // namespace moe

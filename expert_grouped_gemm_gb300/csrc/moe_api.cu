@@ -215,6 +215,7 @@ struct State {
   bool fwd_done = false;
   const void *x = nullptr, *w_router = nullptr, *w_gate = nullptr, *w_up = nullptr, *w_down = nullptr;
   const void *ws_gate = nullptr, *ws_up = nullptr, *ws_down = nullptr;
+  bool routed = false;  // the routing was the caller's (moe_fwd_routed)
   bool sel_done = false;
   const void* sel_dy = nullptr;
 };
@@ -612,15 +613,18 @@ int moe_read_status(void* ws, void* stream) {
   return v;
 }
 
-int moe_fwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x, const void* w_router,
-            const float* router_bias, const void* w_gate, const void* w_up, const void* w_down, const void* ws_gate,
-            const void* ws_up, const void* ws_down, void* y, int32_t* topk_idx, float* topk_w,
-            int32_t* expert_offsets, int32_t* row_of_pair, float* logits) {
+// moe_fwd (given_idx null) and moe_fwd_routed (given_idx, given_w in place of the router).
+static int fwd_impl(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x, const void* w_router,
+                    const float* router_bias, const int32_t* given_idx, const float* given_w, bool routed,
+                    const void* w_gate, const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
+                    const void* ws_down, void* y, int32_t* topk_idx, float* topk_w, int32_t* expert_offsets,
+                    int32_t* row_of_pair, float* logits) {
   WsLayout L;
   int rc = check_ws(dims, ws, ws_bytes, &L);
   if (rc) return rc;
   const bool shared = dims->F_shared > 0;
-  if ((rc = check_ptr(x, "x", true)) || (rc = check_ptr(w_router, "w_router", true)) ||
+  if ((rc = check_ptr(x, "x", true)) || (rc = check_ptr(w_router, "w_router", !routed)) ||
+      (rc = check_ptr(given_idx, "topk_idx", routed, 4)) || (rc = check_ptr(given_w, "topk_w", routed, 4)) ||
       (rc = check_ptr(router_bias, "router_bias", false, 4)) || (rc = check_ptr(w_gate, "w_gate", true)) ||
       (rc = check_ptr(w_up, "w_up", true)) || (rc = check_ptr(w_down, "w_down", true)) ||
       (rc = check_ptr(y, "y", true)) || (rc = check_ptr(topk_idx, "topk_idx", false, 4)) ||
@@ -645,8 +649,8 @@ int moe_fwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
   CK(cudaMemsetAsync(p.status, 0, L.off[2] - L.off[0], st));
 
   // router logits = x W_r  (fp32 out; bias added by the top-k kernel)
-  const int rks = moe::internal_router_ksplit(dims, sms);
-  {
+  const int rks = routed ? 1 : moe::internal_router_ksplit(dims, sms);
+  if (!routed) {
     GemmArgs a = base_args(p.status);
     a.var_k = 0;
     a.G = 1;
@@ -671,7 +675,10 @@ int moe_fwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
   }
   {
     Span sp(st, FAM_BW);
-    CKL(launch_route_topk(p.logits, router_bias, T, E, k, p.topk_idx, p.topk_w, p.masks, st,
+    if (routed)
+      CKL(launch_route_given(given_idx, given_w, T, E, k, p.topk_idx, p.topk_w, p.masks, p.status, st));
+    else
+      CKL(launch_route_topk(p.logits, router_bias, T, E, k, p.topk_idx, p.topk_w, p.masks, st,
                           rks > 1 ? p.part : nullptr, rks, (int64_t)T * E, /*masks_clear=*/true, logits, topk_idx,
                           topk_w));
     CKL(launch_route_scan(p.masks, (int)L.C, E, p.count, p.offset, p.pad_off, p.tile_off, p.chunk_base, p.pair_of_row,
@@ -698,6 +705,7 @@ int moe_fwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
   s = State();
   s.d = *dims;
   s.fwd_done = true;
+  s.routed = routed;
   s.x = x;
   s.w_router = w_router;
   s.w_gate = w_gate;
@@ -707,6 +715,22 @@ int moe_fwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
   s.ws_up = ws_up;
   s.ws_down = ws_down;
   return MOE_OK;
+}
+
+int moe_fwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x, const void* w_router,
+            const float* router_bias, const void* w_gate, const void* w_up, const void* w_down, const void* ws_gate,
+            const void* ws_up, const void* ws_down, void* y, int32_t* topk_idx, float* topk_w,
+            int32_t* expert_offsets, int32_t* row_of_pair, float* logits) {
+  return fwd_impl(dims, ws, ws_bytes, stream, x, w_router, router_bias, nullptr, nullptr, false, w_gate, w_up, w_down,
+                  ws_gate, ws_up, ws_down, y, topk_idx, topk_w, expert_offsets, row_of_pair, logits);
+}
+
+int moe_fwd_routed(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x,
+                   const int32_t* topk_idx, const float* topk_w, const void* w_gate, const void* w_up,
+                   const void* w_down, const void* ws_gate, const void* ws_up, const void* ws_down, void* y,
+                   int32_t* expert_offsets, int32_t* row_of_pair) {
+  return fwd_impl(dims, ws, ws_bytes, stream, x, nullptr, nullptr, topk_idx, topk_w, true, w_gate, w_up, w_down,
+                  ws_gate, ws_up, ws_down, y, nullptr, nullptr, expert_offsets, row_of_pair, nullptr);
 }
 
 // moe_fwd_decode and its self-test: stall (1..4) makes that grid barrier of the kernel
@@ -825,21 +849,23 @@ int moe_select_retained(const moe_dims* dims, void* ws, size_t ws_bytes, void* s
   return MOE_OK;
 }
 
-int moe_bwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy, const void* x,
-            int use_retained, void* dx, void* dw_router, void* dw_gate, void* dw_up, void* dw_down, void* dws_gate,
-            void* dws_up, void* dws_down) {
+// moe_bwd and moe_bwd_routed (routed: dtopk_w in place of the router's gradients).
+static int bwd_impl(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy, const void* x,
+                    int use_retained, void* dx, void* dw_router, bool routed, float* dtopk_w, void* dw_gate,
+                    void* dw_up, void* dw_down, void* dws_gate, void* dws_up, void* dws_down) {
   WsLayout L;
   int rc = check_ws(dims, ws, ws_bytes, &L);
   if (rc) return rc;
   const bool frozen = dims->flags & MOE_FROZEN;
   const bool shared = dims->F_shared > 0;
-  if ((rc = check_ptr(dy, "dy", true)) || (rc = check_ptr(x, "x", true)) || (rc = check_ptr(dx, "dx", true)))
+  if ((rc = check_ptr(dy, "dy", true)) || (rc = check_ptr(x, "x", true)) || (rc = check_ptr(dx, "dx", true)) ||
+      (rc = check_ptr(dtopk_w, "dtopk_w", routed, 4)))
     return rc;
   if (frozen) {
     if (dw_router || dw_gate || dw_up || dw_down || dws_gate || dws_up || dws_down)
       return fail(MOE_ERR_INVALID_ARG, "dW pointers must be null with MOE_FROZEN");
   } else {
-    if ((rc = check_ptr(dw_router, "dw_router", true)) || (rc = check_ptr(dw_gate, "dw_gate", true)) ||
+    if ((rc = check_ptr(dw_router, "dw_router", !routed)) || (rc = check_ptr(dw_gate, "dw_gate", true)) ||
         (rc = check_ptr(dw_up, "dw_up", true)) || (rc = check_ptr(dw_down, "dw_down", true)))
       return rc;
     if (shared) {
@@ -856,6 +882,8 @@ int moe_bwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
     auto it = g_state.find(ws);
     if (it == g_state.end() || !it->second.fwd_done) return fail(MOE_ERR_STATE, "moe_bwd before moe_fwd on this workspace");
     if (!same_dims(it->second.d, *dims)) return fail(MOE_ERR_STATE, "dims differ from moe_fwd's");
+    if (it->second.routed != routed)
+      return fail(MOE_ERR_STATE, routed ? "moe_bwd_routed after moe_fwd" : "moe_bwd after moe_fwd_routed");
     if (it->second.x != x) return fail(MOE_ERR_STATE, "x differs from the tensor moe_fwd saw");
     if (use_retained && (!it->second.sel_done || it->second.sel_dy != dy))
       return fail(MOE_ERR_STATE, "use_retained needs moe_select_retained on the same dy first");
@@ -1037,18 +1065,25 @@ int moe_bwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
   }
   {
     Span sp(bs, FAM_BW);
+    const void* wrT = routed ? nullptr : p.wrT;
+    if (routed)
+      CKL(launch_pair_dw(p.g, p.rowp_of_pair, L.P, dtopk_w, sms, bs));
     if (bf) {
-      CKL(launch_router_bwd<__nv_bfloat16>(p.g, p.rowp_of_pair, p.topk_idx, p.topk_w, T, (int)L.Tpad, E, k, p.dl_sel,
-                                          frozen ? nullptr : p.dl, sms, bs));
-      CKL(launch_transpose<__nv_bfloat16>(s.w_router, H, E, p.wrT, bs));
-      CKL(launch_dx_reduce<__nv_bfloat16>(p.dx_pair, crow, p.topk_idx, p.dl_sel, p.wrT, shared ? p.sh_dx : nullptr, T,
-                                         H, k, dx, sms, bs));
+      if (!routed) {
+        CKL(launch_router_bwd<__nv_bfloat16>(p.g, p.rowp_of_pair, p.topk_idx, p.topk_w, T, (int)L.Tpad, E, k, p.dl_sel,
+                                            frozen ? nullptr : p.dl, sms, bs));
+        CKL(launch_transpose<__nv_bfloat16>(s.w_router, H, E, p.wrT, bs));
+      }
+      CKL(launch_dx_reduce<__nv_bfloat16>(p.dx_pair, crow, p.topk_idx, p.dl_sel, wrT, shared ? p.sh_dx : nullptr, T, H,
+                                         k, dx, sms, bs));
     } else {
-      CKL(launch_router_bwd<float>(p.g, p.rowp_of_pair, p.topk_idx, p.topk_w, T, (int)L.Tpad, E, k, p.dl_sel,
-                                  frozen ? nullptr : p.dl, sms, bs));
-      CKL(launch_transpose<float>(s.w_router, H, E, p.wrT, bs));
-      CKL(launch_dx_reduce<float>(p.dx_pair, crow, p.topk_idx, p.dl_sel, p.wrT, shared ? p.sh_dx : nullptr, T, H, k,
-                                 dx, sms, bs));
+      if (!routed) {
+        CKL(launch_router_bwd<float>(p.g, p.rowp_of_pair, p.topk_idx, p.topk_w, T, (int)L.Tpad, E, k, p.dl_sel,
+                                    frozen ? nullptr : p.dl, sms, bs));
+        CKL(launch_transpose<float>(s.w_router, H, E, p.wrT, bs));
+      }
+      CKL(launch_dx_reduce<float>(p.dx_pair, crow, p.topk_idx, p.dl_sel, wrT, shared ? p.sh_dx : nullptr, T, H, k, dx,
+                                 sms, bs));
     }
   }
   if (overlap) CK(cudaEventRecord(side.join, bs));
@@ -1105,7 +1140,7 @@ int moe_bwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
     }
     // dW_router = x^T dl (dl from the router gradient: the side stream joins here)
     if (overlap) CK(cudaStreamWaitEvent(st, side.join, 0));
-    {
+    if (!routed) {
       GemmArgs a = base_args(p.status);
       a.var_k = 1;
       a.G = 1;
@@ -1176,6 +1211,20 @@ int moe_bwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const
     }
   }
   return MOE_OK;
+}
+
+int moe_bwd(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy, const void* x,
+            int use_retained, void* dx, void* dw_router, void* dw_gate, void* dw_up, void* dw_down, void* dws_gate,
+            void* dws_up, void* dws_down) {
+  return bwd_impl(dims, ws, ws_bytes, stream, dy, x, use_retained, dx, dw_router, false, nullptr, dw_gate, dw_up,
+                  dw_down, dws_gate, dws_up, dws_down);
+}
+
+int moe_bwd_routed(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy, const void* x,
+                   int use_retained, void* dx, float* dtopk_w, void* dw_gate, void* dw_up, void* dw_down,
+                   void* dws_gate, void* dws_up, void* dws_down) {
+  return bwd_impl(dims, ws, ws_bytes, stream, dy, x, use_retained, dx, nullptr, true, dtopk_w, dw_gate, dw_up, dw_down,
+                  dws_gate, dws_up, dws_down);
 }
 
 }  // extern "C"

@@ -169,6 +169,58 @@ __global__ void __launch_bounds__(256) k_route_topk(float* logits, const float* 
   }
 }
 
+// ------------------------------------------------------------------ given routing
+// Warp per token (8 per block): the caller's experts and weights into the workspace, and the chunk
+// masks. A token's experts must be k different ones in [0, E). One that is not sets
+// MOE_ERR_DEVICE_ARG and is replaced by the lowest expert the token does not use, with weight 0, so
+// that every pair still has a row of its own (of equal ones the first slot keeps the expert).
+__global__ void __launch_bounds__(256) k_route_given(const int* idx, const float* w, int T, int E, int k,
+                                                     int* topk_idx, float* topk_w, uint64_t* masks, int* status) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ uint32_t s_used[8][32], s_bad[8][32];  // experts taken, slots to replace: one bit each
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * 8 + warp;
+  if (t >= T) return;
+  uint32_t* used = s_used[warp];
+  uint32_t* bad = s_bad[warp];
+  used[lane] = 0;
+  bad[lane] = 0;
+  __syncwarp();
+  const int64_t p0 = (int64_t)t * k;
+  uint64_t* cmask = masks + (int64_t)(t / kChunk) * E;
+  const unsigned long long bit = 1ull << (t % kChunk);
+  bool any_bad = false;
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const int j = j0 + lane;
+    const int e = j < k ? idx[p0 + j] : -1;
+    const bool in = e >= 0 && e < E;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);  // lanes with this expert: the first keeps it
+    const bool ok = in && (__ffs(same) - 1) == lane && !((used[e >> 5] >> (e & 31)) & 1u);
+    __syncwarp();
+    if (ok) {
+      atomicOr(&used[e >> 5], 1u << (e & 31));
+      topk_idx[p0 + j] = e;
+      topk_w[p0 + j] = w[p0 + j];
+      atomicOr(reinterpret_cast<unsigned long long*>(&cmask[e]), bit);
+    }
+    const uint32_t wrong = __ballot_sync(0xffffffffu, j < k && !ok);
+    if (lane == 0) bad[j0 >> 5] = wrong;
+    any_bad |= wrong != 0;
+    __syncwarp();
+  }
+  if (!any_bad || lane != 0) return;
+  set_status(status, MOE_ERR_DEVICE_ARG);
+  int e = 0;
+  for (int j = 0; j < k; ++j) {
+    if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
+    while ((used[e >> 5] >> (e & 31)) & 1u) ++e;  // k <= E: one is free
+    used[e >> 5] |= 1u << (e & 31);
+    topk_idx[p0 + j] = e;
+    topk_w[p0 + j] = 0.0f;
+    atomicOr(reinterpret_cast<unsigned long long*>(&cmask[e]), bit);
+  }
+}
+
 // ------------------------------------------------------------------ scan
 // One block of 1024 threads: expert e is handled by `parts` threads, each owning
 // a contiguous range of chunks (parts = 1024 / E rounded down to a power of two).
@@ -473,6 +525,12 @@ cudaError_t launch_route_topk(float* logits, const float* bias, int T, int E, in
                                  logits_out, topk_idx_out, topk_w_out);
   else MOE_LAUNCH(k_route_topk<32>, grid, 256, 0, st, logits, bias, T, E, k, topk_idx, topk_w, masks, part, nsplit, part_stride,
                                  logits_out, topk_idx_out, topk_w_out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_route_given(const int* idx, const float* w, int T, int E, int k, int* topk_idx, float* topk_w,
+                               uint64_t* masks, int* status, cudaStream_t st) {
+  MOE_LAUNCH(k_route_given, (T + 7) / 8, 256, 0, st, idx, w, T, E, k, topk_idx, topk_w, masks, status);
   return cudaGetLastError();
 }
 

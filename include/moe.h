@@ -352,6 +352,29 @@ MOE_API int moe_gate_fwd(const moe_gate_dims* dims, void* stream, const void* lo
 MOE_API int moe_gate_bwd(const moe_gate_dims* dims, void* stream, const void* logits, const int32_t* topk_idx,
                          const float* dtopk_w, void* dlogits);
 
+/*
+ * moe_fwd_routed -- moe_fwd with the caller's routing (moe_gate_fwd's, say) in place of the
+ * router: pair (t, j) goes to expert topk_idx[t,j] with weight topk_w[t,j]; the rest is moe_fwd's.
+ * Inputs: topk_idx[T,k] int32, a token's k experts different and in [0, E) (one that is not sets
+ * MOE_ERR_DEVICE_ARG in the status word and counts as weight 0), topk_w[T,k] float; the others and
+ * the outputs as in moe_fwd. moe_select_retained and moe_plan_quota follow it as they follow
+ * moe_fwd; the backward is moe_bwd_routed.
+ */
+MOE_API int moe_fwd_routed(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x,
+                           const int32_t* topk_idx, const float* topk_w, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* ws_gate, const void* ws_up, const void* ws_down, void* y,
+                           int32_t* expert_offsets, int32_t* row_of_pair);
+
+/*
+ * moe_bwd_routed -- moe_bwd after moe_fwd_routed: the expert and shared parts of dx and the dW of
+ * the experts, and in place of the router's gradients dtopk_w[t,j] = <dy_t, y_pair(t,j)> (float,
+ * every pair, whatever was retained; what moe_gate_bwd takes). moe_bwd after moe_fwd_routed, or
+ * this call after moe_fwd, is MOE_ERR_STATE. With MOE_FROZEN the dW pointers are null.
+ */
+MOE_API int moe_bwd_routed(const moe_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy,
+                           const void* x, int use_retained, void* dx, float* dtopk_w, void* dw_gate, void* dw_up,
+                           void* dw_down, void* dws_gate, void* dws_up, void* dws_down);
+
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,
@@ -390,13 +413,15 @@ MOE_API int moe_linear_fwd(const moe_linear_dims* dims, void* ws, size_t ws_byte
 
 /*
  * moe_linear_bwd -- gradients of moe_linear_fwd (the residual's is dy itself):
- *   dz = dy act'(pre);  dx = dz w^T;  dw = x^T dz;  dbias_n = sum_m dz.
+ *   dz = dy act'(pre);  dx = dz w^T + dx_add;  dw = x^T dz;  dbias_n = sum_m dz.
  * In bf16 dz is rounded to bf16 for the two products; dbias sums the unrounded dz.
- * Inputs:  dy[M,N] (dims.dtype), x[M,K], w[K,N], pre[M,N] (null when act is MOE_ACT_NONE).
+ * Inputs:  dy[M,N] (dims.dtype), x[M,K], w[K,N], pre[M,N] (null when act is MOE_ACT_NONE),
+ *          dx_add[M,K] (nullable: the gradient that reaches x by another path; may be dx's buffer).
  * Outputs: dx[M,K], dw[K,N], dbias[N], each nullable; overwritten, summed in a fixed order.
  */
 MOE_API int moe_linear_bwd(const moe_linear_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy,
-                           const void* x, const void* w, const void* pre, void* dx, void* dw, void* dbias);
+                           const void* x, const void* w, const void* pre, const void* dx_add, void* dx, void* dw,
+                           void* dbias);
 
 /*
  * moe_selftest_wait -- checks, on the GPU, the bounded barrier wait that every

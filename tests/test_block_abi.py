@@ -109,8 +109,8 @@ def test_linear_arguments(lib):
     def fwd(d, ws=FAKE, size=1 << 30, x=FAKE, w=FAKE, b=None, r=None, y=0x20000, pre=None):
         return lib.moe_linear_fwd(ctypes.byref(d), ws, size, None, x, w, b, r, y, pre)
 
-    def bwd(d, ws=FAKE, size=1 << 30, dy=FAKE, x=FAKE, w=FAKE, pre=None, dx=FAKE, dw=FAKE, db=None):
-        return lib.moe_linear_bwd(ctypes.byref(d), ws, size, None, dy, x, w, pre, dx, dw, db)
+    def bwd(d, ws=FAKE, size=1 << 30, dy=FAKE, x=FAKE, w=FAKE, pre=None, add=None, dx=FAKE, dw=FAKE, db=None):
+        return lib.moe_linear_bwd(ctypes.byref(d), ws, size, None, dy, x, w, pre, add, dx, dw, db)
 
     assert fwd(d, ws=None) == WSP and fwd(d, size=4095) == WSP and fwd(d, ws=0x10080) == WSP
     for k in ("x", "w", "y"):
@@ -122,6 +122,7 @@ def test_linear_arguments(lib):
     assert bwd(linear(act=2)) == INV            # the activation's input is missing
     assert bwd(linear(), pre=FAKE) == INV       # and here there is no activation
     assert bwd(linear(), dy=None) == INV
+    assert bwd(linear(), add=FAKE, dx=None) == INV and bwd(linear(), add=ODD) == INV
     assert bwd(linear(), x=None) == INV and bwd(linear(), w=None) == INV
 
 

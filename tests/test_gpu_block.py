@@ -214,6 +214,23 @@ def test_linear_result_over_the_residual(M, K, N):
     C.check_linear_fwd(c, (y, None), res=res)
 
 
+@pytest.mark.parametrize("M,K,N,dtype", [(3, 512, 384, "bf16"), (1, 129, 64, "bf16"), (600, 520, 264, "bf16"),
+                                         (500, 2048, 1000, "bf16"), (50, 60, 70, "f32")])
+def test_linear_gradient_of_another_path(M, K, N, dtype):
+    """dx_add joins dx before its one rounding, also where it is dx's own buffer."""
+    c = C.linear_case(M, K, N, dtype, seed=15)
+    add = C.rand(16)(M, K, dtype=C.DT[dtype])
+    d, ws = C.linear_ws(c)
+    dx = torch.full_like(add, float("nan"))
+    _lib.moe_linear_bwd(d, ws, c["dy"], c["x"], c["w"], None, dx, dx_add=add)
+    x, w, dy = (C.f64(c[n]) for n in ("x", "w", "dy"))
+    want = dy @ w.T + C.f64(add)
+    tol = C.U[dtype] * np.abs(want) + (N + 32) * 2 * C.E32 * (np.abs(dy) @ np.abs(w).T) + 2 * C.E32 * np.abs(C.f64(add))
+    C.close(dx, want, tol, "dx")
+    _lib.moe_linear_bwd(d, ws, c["dy"], c["x"], c["w"], None, add, dx_add=add)
+    assert torch.equal(add, dx)
+
+
 @pytest.mark.parametrize("M,K,N,dtype", [(3, 512, 384, "bf16"), (600, 520, 264, "bf16"), (300, 200, 100, "f32")])
 def test_linear_gradient_is_the_difference_quotient(M, K, N, dtype):
     """<dy, y> moved along a direction, taken in 64 bits from the products of the inputs, against the gradients."""
