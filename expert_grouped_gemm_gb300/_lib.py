@@ -318,10 +318,11 @@ def _tensor(t, name, dtype, shape, required=True):
         if required:
             raise ValueError(f"{name} is required")
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:

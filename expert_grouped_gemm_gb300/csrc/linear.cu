@@ -265,23 +265,23 @@ __global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T*
   }
 }
 
-// The chunks' column sums added: eight lanes of chunks per column, then those in order.
+// The chunks' column sums added: 32 chunk lanes a column, each in chunk order, then the lanes in order.
 template <typename T>
-__global__ void __launch_bounds__(256) k_linear_dbias(const float* part, int chunks, int N, T* db) {
+__global__ void __launch_bounds__(1024) k_linear_dbias(const float* part, int chunks, int N, T* db) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float red[8][33];
+  __shared__ float red[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int n = blockIdx.x * 32 + cx;
   float s = 0.0f;
   if (n < N) {
-#pragma unroll 8
-    for (int c = ry; c < chunks; c += 8) s += part[(int64_t)c * N + n];
+#pragma unroll 5
+    for (int c = ry; c < chunks; c += 32) s += part[(int64_t)c * N + n];
   }
   red[ry][cx] = s;
   __syncthreads();
   if (ry == 0 && n < N) {
 #pragma unroll
-    for (int r = 1; r < 8; ++r) s += red[r][cx];
+    for (int r = 1; r < 32; ++r) s += red[r][cx];
     db[n] = io<T>::cvt(s);
   }
 }
@@ -293,24 +293,46 @@ int dz_chunks(int64_t M, int64_t N, int vec) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(want, (M + 15) / 16));
 }
 
-// A matrix with odd rows copied to rows of a multiple of 16 bytes, for the tensor-core products
-// (TMA reads rows at 16-byte strides). The columns past C of dst are never read.
-__global__ void __launch_bounds__(256) k_pack_rows(const __nv_bfloat16* src, __nv_bfloat16* dst, int64_t R, int C,
-                                                   int64_t ld) {
+// Matrices with odd rows copied to rows of a multiple of 16 bytes, for the tensor-core products
+// (TMA reads rows at 16-byte strides). The columns past C of dst are never read. Up to two matrices
+// a launch: blocks [0, split) take the first.
+struct PackArgs {
+  const __nv_bfloat16* src[2];
+  __nv_bfloat16* dst[2];
+  int64_t n[2], ld[2];  // elements, row stride of dst
+  int C[2];
+  int split;
+};
+constexpr int kPackPer = 2048;  // elements of a block's step
+
+__global__ void __launch_bounds__(256) k_pack_rows(const PackArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  constexpr int U = 8;
-  const int64_t total = R * C;
-  for (int64_t base = (int64_t)blockIdx.x * 256 * U + threadIdx.x; base < total; base += (int64_t)gridDim.x * 256 * U) {
+  constexpr int U = kPackPer / 256;
+  const int w = (int)blockIdx.x >= a.split;
+  const int b = (int)blockIdx.x - (w ? a.split : 0), blocks = w ? (int)gridDim.x - a.split : a.split;
+  const __nv_bfloat16* src = a.src[w];
+  __nv_bfloat16* dst = a.dst[w];
+  const int64_t n = a.n[w], ld = a.ld[w];
+  const int C = a.C[w];
+  for (int64_t base = (int64_t)b * kPackPer + threadIdx.x; base < n; base += (int64_t)blocks * kPackPer) {
     __nv_bfloat16 v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (base + u * 256 < total) v[u] = src[base + u * 256];
+      if (base + u * 256 < n) v[u] = src[base + u * 256];
+    int64_t r = base / C;
+    int c = (int)(base - r * C);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = base + u * 256;
-      if (i < total) {
-        const int64_t r = i / C;
-        dst[r * ld + (i - r * C)] = v[u];
+      if (base + u * 256 < n) dst[r * ld + c] = v[u];
+      c += 256;
+      if (C >= 256) {
+        if (c >= C) {
+          c -= C;
+          ++r;
+        }
+      } else {
+        r += c / C;
+        c %= C;
       }
     }
   }
@@ -370,16 +392,31 @@ LinearWs layout(const moe_linear_dims& d) {
   return L;
 }
 
-// p itself when its rows are multiples of 16 bytes, else a packed copy at `copy`
-cudaError_t packed(const void** p, void* copy, int64_t R, int64_t C, int sms, cudaStream_t st, int* launches) {
-  if (C % 8 == 0) return cudaSuccess;
-  const int64_t blocks = (R * C + 2047) / 2048;
-  *launches += 1;
-  MOE_LAUNCH(k_pack_rows, (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8), 256, 0, st,
-             static_cast<const __nv_bfloat16*>(*p), static_cast<__nv_bfloat16*>(copy), R, (int)C, up8(C));
-  *p = copy;
-  return cudaSuccess;
-}
+// Each matrix given (p, R rows of C) is replaced by a packed copy where its rows are no multiple of
+// 16 bytes; one launch for both.
+struct Packed {
+  PackArgs a = {};
+  int count = 0;
+  void add(const void** p, void* copy, int64_t R, int64_t C) {
+    if (C % 8 == 0) return;
+    a.src[count] = static_cast<const __nv_bfloat16*>(*p);
+    a.dst[count] = static_cast<__nv_bfloat16*>(copy);
+    a.n[count] = R * C;
+    a.ld[count] = up8(C);
+    a.C[count++] = (int)C;
+    *p = copy;
+  }
+  cudaError_t run(int sms, cudaStream_t st, int* launches) {
+    if (!count) return cudaSuccess;
+    int blocks[2] = {0, 0};
+    for (int i = 0; i < count; ++i)
+      blocks[i] = (int)std::min<int64_t>((a.n[i] + kPackPer - 1) / kPackPer, (int64_t)sms * 8);
+    a.split = blocks[0];
+    *launches += 1;
+    MOE_LAUNCH(k_pack_rows, blocks[0] + blocks[1], 256, 0, st, a);
+    return cudaSuccess;
+  }
+};
 
 template <typename T>
 cudaError_t run_dz(const moe_linear_dims& d, const void* dy, const void* pre, void* dz, int64_t ldz, float* part,
@@ -405,7 +442,7 @@ cudaError_t run_dbias(const moe_linear_dims& d, const float* part, void* db, cud
   const int M = (int)d.M, N = (int)d.N;
   const int want = dz_chunks(M, N, N % V ? 1 : V), per = (M + want - 1) / want, chunks = (M + per - 1) / per;
   *launches += 1;
-  MOE_LAUNCH(k_linear_dbias<T>, (N + 31) / 32, 256, 0, st, part, chunks, N, (T*)db);
+  MOE_LAUNCH(k_linear_dbias<T>, (N + 31) / 32, 1024, 0, st, part, chunks, N, (T*)db);
   return cudaSuccess;
 }
 
@@ -413,8 +450,10 @@ cudaError_t fwd_bf16(const moe_linear_dims& d, char* ws, const void* x, const vo
                      const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches) {
   const LinearWs L = layout(d);
   cudaError_t e;
-  if ((e = packed(&x, ws + L.xp, d.M, d.K, sms, st, launches)) != cudaSuccess) return e;
-  if ((e = packed(&w, ws + L.wp, d.K, d.N, sms, st, launches)) != cudaSuccess) return e;
+  Packed pk;
+  pk.add(&x, ws + L.xp, d.M, d.K);
+  pk.add(&w, ws + L.wp, d.K, d.N);
+  if ((e = pk.run(sms, st, launches)) != cudaSuccess) return e;
   LinearGemm g = {(int)d.M, (int)d.N, (int)d.K, x,   w,     up8(d.K),  up8(d.N), 0, 1, bias, residual,
                   y,        pre,      d.act,    d.out_f32, reinterpret_cast<int*>(ws)};
   *launches += 1;
@@ -434,14 +473,18 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
   if (store || dbias)
     e = run_dz<__nv_bfloat16>(d, dy, pre, store ? ws + L.dz : nullptr, up8(N), dbias ? part : nullptr, st, launches);
   if (e == cudaSuccess && dbias) e = run_dbias<__nv_bfloat16>(d, part, dbias, st, launches);
+  if (e == cudaSuccess) {
+    Packed pk;
+    if (dx) pk.add(&w, ws + L.wp, K, N);
+    if (dw) pk.add(&x, ws + L.xp, M, K);
+    e = pk.run(sms, st, launches);
+  }
   if (e == cudaSuccess && dx) {
-    if ((e = packed(&w, ws + L.wp, K, N, sms, st, launches)) != cudaSuccess) return e;
     LinearGemm g = {M, K, N, dz, w, up8(N), up8(N), 0, 0, nullptr, dx_add, dx, nullptr, MOE_ACT_NONE, 0, status};
     *launches += 1;
     e = launch_linear_tc(g, sms, st);
   }
   if (e == cudaSuccess && dw) {
-    if ((e = packed(&x, ws + L.xp, M, K, sms, st, launches)) != cudaSuccess) return e;
     LinearGemm g = {K, N, M, x, dz, up8(K), up8(N), 1, 1, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0, status};
     *launches += 1;
     e = launch_linear_tc(g, sms, st);

@@ -5,6 +5,7 @@
 // form sum(h^2) - mean^2 loses every digit when the mean is large against the spread).
 // Both directions are bound by HBM: each tensor is read or written once.
 #include <algorithm>
+#include <atomic>
 
 #include "block.h"
 #include "common.cuh"
@@ -143,17 +144,18 @@ __global__ void __launch_bounds__(256) k_norm_dw_long(const T* dy, const T* x, c
   part[((int64_t)blockIdx.y * 2 + 1) * H + i] = ab;
 }
 
-// The chunks' partial sums added: eight chunk lanes a column, each in chunk order, then the lanes.
+// The chunks' partial sums added: 32 chunk lanes a column, each in chunk order, then the lanes in
+// order. A lane has few chunks (five of 152), whose loads travel together.
 template <typename T>
-__global__ void __launch_bounds__(256) k_norm_dw_sum(const float* part, int chunks, int H, T* dw, T* db) {
+__global__ void __launch_bounds__(1024) k_norm_dw_sum(const float* part, int chunks, int H, T* dw, T* db) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float red[2][8][33];
+  __shared__ float red[2][32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + cx;
   float aw = 0.0f, ab = 0.0f;
   if (i < H) {
-#pragma unroll 8
-    for (int c = ry; c < chunks; c += 8) {
+#pragma unroll 5
+    for (int c = ry; c < chunks; c += 32) {
       aw += part[((int64_t)c * 2) * H + i];
       if (db) ab += part[((int64_t)c * 2 + 1) * H + i];
     }
@@ -161,14 +163,12 @@ __global__ void __launch_bounds__(256) k_norm_dw_sum(const float* part, int chun
   red[0][ry][cx] = aw;
   red[1][ry][cx] = ab;
   __syncthreads();
-  if (ry == 0 && i < H) {
+  // warp 0 adds the weight sums, warp 1 the bias sums
+  if (ry < 2 && i < H && (ry == 0 || db)) {
+    float v = red[ry][0][cx];
 #pragma unroll
-    for (int r = 1; r < 8; ++r) {
-      aw += red[0][r][cx];
-      ab += red[1][r][cx];
-    }
-    dw[i] = io<T>::cvt(aw);
-    if (db) db[i] = io<T>::cvt(ab);
+    for (int r = 1; r < 32; ++r) v += red[ry][r][cx];
+    (ry ? db : dw)[i] = io<T>::cvt(v);
   }
 }
 
@@ -537,18 +537,23 @@ __global__ void __launch_bounds__(512) k_norm_bwd_odd(const BwdArgs a) {
 constexpr int kMaxParts = 512;  // rows of partial sums the workspace holds
 
 // Blocks of a persistent kernel: as many as fit on the GPU at once, or as the rows need.
+// The occupancy is asked once per kernel (`cache`): it only sets the grid.
 template <typename K>
-int resident_blocks(K kern, int threads, size_t smem, int64_t need, int sms, int cap) {
-  int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem) != cudaSuccess || per < 1) per = 1;
+int resident_blocks(K kern, std::atomic<int>* cache, int threads, size_t smem, int64_t need, int sms, int cap) {
+  int per = cache->load(std::memory_order_relaxed);
+  if (per < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem) != cudaSuccess || per < 1) per = 1;
+    cache->store(per, std::memory_order_relaxed);
+  }
   return (int)std::max<int64_t>(1, std::min<int64_t>({need, (int64_t)per * sms, (int64_t)cap}));
 }
 
 template <typename T, int VEC, int VPT, int G>
 cudaError_t fwd_regs(const FwdArgs& a, int sms, cudaStream_t st) {
   constexpr int threads = kFwdThreads<G>, groups = threads / G;
+  static std::atomic<int> cache{0};
   auto kern = k_norm_fwd<T, VEC, VPT, G>;
-  const int grid = resident_blocks(kern, threads, 0, ((int64_t)a.rows + groups - 1) / groups, sms, 1 << 30);
+  const int grid = resident_blocks(kern, &cache, threads, 0, ((int64_t)a.rows + groups - 1) / groups, sms, 1 << 30);
   MOE_LAUNCH(kern, grid, threads, 0, st, a);
   return cudaSuccess;
 }
@@ -596,10 +601,11 @@ cudaError_t bwd_ring(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
   constexpr int VPT = EPT * (int)sizeof(T) / 16, stage = 3 * VPT * 512 * 16, groups = 512 / G;
   constexpr int stages = 196608 / stage < 4 ? 196608 / stage : 4;
   static_assert(stages >= 2 && stages * stage >= (int)sizeof(float) * 2 * G * EPT, "ring too small");
+  static std::atomic<int> cache{0};
   auto kern = k_norm_bwd_ring<T, VPT, G, stages>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, stages * stage);
   if (e != cudaSuccess) return e;
-  *chunks = resident_blocks(kern, 512, stages * stage, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  *chunks = resident_blocks(kern, &cache, 512, stages * stage, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
   MOE_LAUNCH(kern, *chunks, 512, stages * stage, st, a);
   return cudaSuccess;
 }
@@ -608,8 +614,9 @@ template <typename T, int VPT, int G>
 cudaError_t bwd_odd(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
   constexpr int groups = 512 / G;
   constexpr size_t smem = groups > 1 ? sizeof(float) * 2 * G * VPT : 0;
+  static std::atomic<int> cache{0};
   auto kern = k_norm_bwd_odd<T, VPT, G>;
-  *chunks = resident_blocks(kern, 512, smem, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  *chunks = resident_blocks(kern, &cache, 512, smem, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
   MOE_LAUNCH(kern, *chunks, 512, smem, st, a);
   return cudaSuccess;
 }
@@ -656,7 +663,7 @@ cudaError_t bwd(const moe_norm_dims& d, void* ws, const void* dy, const void* ds
   const int cb = (H + 31) / 32;
   if (chunks) {
     *launches += 2;
-    MOE_LAUNCH(k_norm_dw_sum<T>, cb, 256, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);
+    MOE_LAUNCH(k_norm_dw_sum<T>, cb, 1024, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);
     return cudaSuccess;
   }
   const int per = (rows + kNormChunks - 1) / kNormChunks;
@@ -664,7 +671,7 @@ cudaError_t bwd(const moe_norm_dims& d, void* ws, const void* dy, const void* ds
   *launches += 3;  // the weight gradients before dx, which may be written over dy
   MOE_LAUNCH(k_norm_dw_long<T>, dim3((H + 255) / 256, chunks), 256, 0, st, (const T*)dy, (const T*)x, mean, rstd, part,
              rows, H, per);
-  MOE_LAUNCH(k_norm_dw_sum<T>, cb, 256, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);
+  MOE_LAUNCH(k_norm_dw_sum<T>, cb, 1024, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);
   const int grid = (int)std::min<int64_t>(d.T, (int64_t)sms * 8);
   MOE_LAUNCH(k_norm_dx_long<T>, grid, 256, 0, st, (const T*)dy, (const T*)dsum, (const T*)x, (const T*)w, mean, rstd,
              (T*)dx, rows, H);
