@@ -59,26 +59,46 @@ struct TcArgs {
 // byte offset of 16-byte piece j of row r in a 128-byte-swizzled staging tile
 __device__ __forceinline__ uint32_t piece(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-// A warp's 32 x 64 piece of a row-major bf16 matrix into a staging tile and back, two columns a lane.
+// A warp's 32 x 64 piece of a row-major bf16 matrix into a staging tile and back, two columns a
+// lane, the loads of eight rows in flight.
 __device__ __forceinline__ void rows_in(uint32_t tile, const __nv_bfloat16* src, int64_t ld, int rows, int cols,
                                         int lane) {
-  for (int r = 0; r < rows; ++r)
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    uint16_t v[8][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = lane + 32 * h;
-      const uint16_t v = c < cols ? *reinterpret_cast<const uint16_t*>(src + r * ld + c) : (uint16_t)0;
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + piece(r, c >> 3) + (c & 7) * 2), "h"(v) : "memory");
-    }
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        v[r][h] = r0 + r < rows && c < cols ? *reinterpret_cast<const uint16_t*>(src + (r0 + r) * ld + c) : (uint16_t)0;
+      }
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + piece(r0 + r, c >> 3) + (c & 7) * 2), "h"(v[r][h]) : "memory");
+      }
+  }
 }
 __device__ __forceinline__ void rows_out(__nv_bfloat16* dst, int64_t ld, uint32_t tile, int rows, int cols, int lane) {
-  for (int r = 0; r < rows; ++r)
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    uint16_t v[8][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = lane + 32 * h;
-      uint16_t v;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(tile + piece(r, c >> 3) + (c & 7) * 2) : "memory");
-      if (c < cols) *reinterpret_cast<uint16_t*>(dst + r * ld + c) = v;
-    }
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[r][h]) : "r"(tile + piece(r0 + r, c >> 3) + (c & 7) * 2) : "memory");
+      }
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lane + 32 * h;
+        if (r0 + r < rows && c < cols) *reinterpret_cast<uint16_t*>(dst + (r0 + r) * ld + c) = v[r][h];
+      }
+  }
 }
 
 // Tiles run down eight row blocks before they move to the next columns, so the tiles in flight
@@ -276,35 +296,42 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       const int c0 = (ew / 4) * cw;
       const int64_t row0 = (int64_t)it.m * C::TILE_M + (int)rank * 128 + q * 32;  // this warp's first row
       const int rows = (int)min((int64_t)32, (int64_t)g.M - row0);              // rows of it that exist
+      // With a second output z takes one staging tile and y the other; else y alternates between
+      // the two. ready(c) waits until the stores that last used chunk c's tile have read it and
+      // sends for its residual: for the first chunk while the products still run.
+      auto ready = [&](int c) {
+        const int n0 = it.n0 + c * 64;
+        if (rows <= 0 || n0 >= g.N) return;
+        const uint32_t ty = tile + (g.pre ? kStage : (sc & 1) * kStage);
+        if (lane == 0) {
+          if (g.pre) bulk_wait_read_all();
+          else bulk_wait_read_but1();
+        }
+        __syncwarp();
+        if (!res) return;
+        const int cols = min(64, g.N - n0);
+        if constexpr (VEC) {  // eight lanes a row, 16 bytes each
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (lane >> 3) + 4 * i, j = lane & 7;
+            if (r < rows && 8 * j < cols) cp_async16(ty + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
+          }
+          cp_async_commit();
+        } else {
+          rows_in(ty, res + row0 * g.N + n0, g.N, rows, cols, lane);
+        }
+      };
+      ready(c0);
       const int acc = acc_i & 1;
       if (!mbar_wait_bounded(&tfull[acc], (uint32_t)((acc_i >> 1) & 1), abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       for (int c = c0; c < c0 + cw; ++c) {
         const int n0 = it.n0 + c * 64;
-        if (rows <= 0 || n0 >= g.N) continue;  // the same for the whole warp
-        const int cols = min(64, g.N - n0);    // with VEC a multiple of 8
-        // With a second output z takes one tile and y the other; else y alternates between the
-        // two, and the stores of the chunk before may still be reading.
+        if (rows <= 0 || n0 >= g.N) break;   // the same for the whole warp
+        const int cols = min(64, g.N - n0);  // with VEC a multiple of 8
         const uint32_t ty = tile + (g.pre ? kStage : (sc & 1) * kStage);
         ++sc;
-        if (lane == 0) {
-          if (g.pre) bulk_wait_read_all();
-          else bulk_wait_read_but1();
-        }
-        __syncwarp();
-        if (res) {
-          if constexpr (VEC) {  // eight lanes a row, 16 bytes each
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = (lane >> 3) + 4 * i, j = lane & 7;
-              if (r < rows && 8 * j < cols) cp_async16(ty + piece(r, j), res + (row0 + r) * g.N + n0 + 8 * j);
-            }
-            cp_async_commit();
-          } else {
-            rows_in(ty, res + row0 * g.N + n0, g.N, rows, cols, lane);
-          }
-        }
         uint32_t v[2][32];
         tmem_ld32_async(taddr + c * 64, v[0]);
         tmem_ld32_async(taddr + c * 64 + 32, v[1]);
@@ -373,6 +400,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           if (!g.out_f32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + o, g.N, ty, rows, cols, lane);
           if (g.pre) rows_out(reinterpret_cast<__nv_bfloat16*>(g.pre) + o, g.N, tile, rows, cols, lane);
           __syncwarp();
+          if (c + 1 < c0 + cw) ready(c + 1);
           continue;
         }
         fence_async_smem();
@@ -382,6 +410,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           if (g.pre) tma_store_2d(&tmP, tile, n0, (int)row0);
           bulk_commit();
         }
+        if (c + 1 < c0 + cw) ready(c + 1);
       }
       tc_fence_before();
       __syncwarp();
