@@ -54,10 +54,13 @@ int sm_count() {
   return cache[dev] = n;
 }
 
+// Row indices are 32-bit and run ahead of the last row by a few grid strides.
+constexpr int64_t kMaxRows = (1ll << 31) - (1 << 20);
+
 int check_norm(const moe_norm_dims* d) {
   if (!d) return bad(MOE_ERR_INVALID_ARG, "dims is null");
   if (d->T < 1 || d->H < 1) return bad(MOE_ERR_INVALID_ARG, "T and H must be >= 1");
-  if (d->T >= (1ll << 31) - 1) return bad(MOE_ERR_UNSUPPORTED, "T >= 2^31 - 1");
+  if (d->T > kMaxRows) return bad(MOE_ERR_UNSUPPORTED, "T > 2^31 - 2^20");
   if (d->H > 65536) return bad(MOE_ERR_UNSUPPORTED, "H (%lld) > 65536", (long long)d->H);
   if (d->kind != MOE_NORM_LAYER && d->kind != MOE_NORM_RMS)
     return bad(MOE_ERR_INVALID_ARG, "unknown norm kind %d", d->kind);
@@ -89,8 +92,8 @@ int check_gate(const moe_gate_dims* d) {
 int check_linear(const moe_linear_dims* d) {
   if (!d) return bad(MOE_ERR_INVALID_ARG, "dims is null");
   if (d->M < 1 || d->K < 1 || d->N < 1) return bad(MOE_ERR_INVALID_ARG, "M, K, N must be >= 1");
-  if (d->M >= (1ll << 31) - 1 || d->K >= (1 << 24) || d->N >= (1 << 24))
-    return bad(MOE_ERR_UNSUPPORTED, "needs M < 2^31 - 1 and K, N < 2^24");
+  if (d->M > kMaxRows || d->K >= (1 << 24) || d->N >= (1 << 24))
+    return bad(MOE_ERR_UNSUPPORTED, "needs M <= 2^31 - 2^20 and K, N < 2^24");
   if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_SILU) return bad(MOE_ERR_INVALID_ARG, "unknown act %d", d->act);
   if (d->out_f32 != 0 && d->out_f32 != 1) return bad(MOE_ERR_INVALID_ARG, "out_f32 must be 0 or 1");
   return check_dtype(d->dtype, "dtype");

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       }
       ++acc_i;
     }
+    cp_async_wait<0>();
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }

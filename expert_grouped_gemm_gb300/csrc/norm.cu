@@ -31,9 +31,28 @@ __device__ __forceinline__ Vec<T, VEC> pack(const float (&f)[VEC]) {
   return a;
 }
 
-// Sums of two values over a group of G threads (a warp, or G / 32 warps that meet at barrier
-// `id`); every thread gets both. `slots` is the group's own, two sets of G / 32 entries used in
-// turn, so one barrier a call is enough. Fixed tree: the same result on every run.
+// Sums over a group of G threads (a warp, or G / 32 warps that meet at barrier `id`) of one value or
+// two; every thread gets them. `slots` is the group's own, two sets of G / 32 entries used in turn,
+// so one barrier a call is enough; behind it every thread adds the warps' sums in order (a few
+// 16-byte shared loads, where a second butterfly costs ten shuffles and additions).
+template <int G>
+__device__ __forceinline__ float group_sum(float a, float2* slots, int* turn, int id) {
+  a = warp_sum(a);
+  if constexpr (G > 32) {
+    constexpr int W = G / 32;
+    float* s = reinterpret_cast<float*>(slots + *turn * W);
+    *turn ^= 1;
+    if ((threadIdx.x & 31) == 0) s[(threadIdx.x % G) >> 5] = a;
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(G) : "memory");
+    a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(s + i);
+      a += (v.x + v.y) + (v.z + v.w);
+    }
+  }
+  return a;
+}
 template <int G>
 __device__ __forceinline__ float2 group_sum2(float a, float b, float2* slots, int* turn, int id) {
   a = warp_sum(a);
@@ -42,12 +61,15 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, float2* slots, in
     constexpr int W = G / 32;
     float2* s = slots + *turn * W;
     *turn ^= 1;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x % G) >> 5;
-    if (lane == 0) s[w] = make_float2(a, b);
+    if ((threadIdx.x & 31) == 0) s[(threadIdx.x % G) >> 5] = make_float2(a, b);
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(G) : "memory");
-    const float2 v = lane < W ? s[lane] : make_float2(0.0f, 0.0f);
-    a = warp_sum(v.x);
-    b = warp_sum(v.y);
+    a = b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(s + i);
+      a += v.x + v.z;
+      b += v.y + v.w;
+    }
   }
   return make_float2(a, b);
 }
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(kFwdThreads<G>) k_norm_fwd(const FwdArgs a) {
   using V = Vec<T, VEC>;
   pdl_wait();  // the previous kernel has completed and its writes are visible
   constexpr int GROUPS = kFwdThreads<G> / G;
-  __shared__ float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 1];
+  __shared__ __align__(16) float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 2];
   const int grp = threadIdx.x / G, j = threadIdx.x % G;
   int turn = 0;
   const int nv = a.H / VEC;
@@ -237,34 +259,35 @@ __global__ void __launch_bounds__(kFwdThreads<G>) k_norm_fwd(const FwdArgs a) {
       for (int p = 0; p < VPT; ++p)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) s += h[p][i];
-      mu = group_sum2<G>(s, 0.0f, slots[grp], &turn, 1 + grp).x * inv_h;
+      mu = group_sum<G>(s, slots[grp], &turn, 1 + grp) * inv_h;
     }
+    V* y = reinterpret_cast<V*>(a.y) + o;
+    V* sum = reinterpret_cast<V*>(a.sum) + o;
     float q = 0.0f;
 #pragma unroll
     for (int p = 0; p < VPT; ++p)
-      if (j + p * G < nv)
+      if (j + p * G < nv) {
+        if (a.sum) sum[j + p * G] = pack<T, VEC>(h[p]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const float d = h[p][i] - mu;
-          q = fmaf(d, d, q);
+          h[p][i] -= mu;
+          q = fmaf(h[p][i], h[p][i], q);
         }
-    const float rs = 1.0f / sqrtf(group_sum2<G>(q, 0.0f, slots[grp], &turn, 1 + grp).x * inv_h + a.eps);
-    V* y = reinterpret_cast<V*>(a.y) + o;
-    V* sum = reinterpret_cast<V*>(a.sum) + o;
+      }
+    const float rs = 1.0f / sqrtf(group_sum<G>(q, slots[grp], &turn, 1 + grp) * inv_h + a.eps);
 #pragma unroll
     for (int p = 0; p < VPT; ++p)
       if (j + p * G < nv) {
         float wf[VEC], v[VEC];
         unpack<T, VEC>(w[j + p * G], wf);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = (h[p][i] - mu) * rs * wf[i];
+        for (int i = 0; i < VEC; ++i) v[i] = h[p][i] * rs * wf[i];
         if (bias) {
           float bf[VEC];
           unpack<T, VEC>(bias[j + p * G], bf);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) v[i] += bf[i];
         }
-        if (a.sum) sum[j + p * G] = pack<T, VEC>(h[p]);
         y[j + p * G] = pack<T, VEC>(v);
       }
     if (j == 0) {
@@ -272,6 +295,112 @@ __global__ void __launch_bounds__(kFwdThreads<G>) k_norm_fwd(const FwdArgs a) {
       if (a.rstd) a.rstd[t] = rs;
     }
   }
+}
+
+// The same for many aligned rows: the rows come through a ring of STAGES slots in shared memory
+// filled by 16-byte asynchronous copies, a row or more ahead of the sums. A thread copies exactly
+// the vectors it reads, so the ring needs no barrier.
+template <typename T, int VPT, int G, int STAGES>
+__global__ void __launch_bounds__(512) k_norm_fwd_ring(const FwdArgs a) {
+  constexpr int VEC = 16 / sizeof(T);
+  using V = Vec<T, VEC>;
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  constexpr int GROUPS = 512 / G;
+  __shared__ __align__(16) float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 2];
+  extern __shared__ __align__(16) uint8_t ring[];  // [STAGES][2 tensors][VPT][512 threads] vectors
+  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  int turn = 0;
+  const int nv = a.H / VEC;
+  const float inv_h = 1.0f / (float)a.H;
+  const V* x = reinterpret_cast<const V*>(a.x);
+  const V* res = reinterpret_cast<const V*>(a.res);
+  V wv[VPT], bv[VPT];
+#pragma unroll
+  for (int p = 0; p < VPT; ++p)
+    if (j + p * G < nv) {
+      wv[p] = reinterpret_cast<const V*>(a.w)[j + p * G];
+      if (a.b) bv[p] = reinterpret_cast<const V*>(a.b)[j + p * G];
+    }
+  const uint32_t base = smem_u32(ring) + threadIdx.x * 16;
+  auto slot = [&](int st, int tensor, int p) { return base + (uint32_t)(((st * 2 + tensor) * VPT + p) * 512 * 16); };
+  auto fetch = [&](int t, int st) {
+    if (t < a.rows) {
+      const int64_t o = (int64_t)t * nv + j;
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
+        if (j + p * G < nv) {
+          cp_async16(slot(st, 0, p), x + o + p * G);
+          if (res) cp_async16(slot(st, 1, p), res + o + p * G);
+        }
+    }
+    cp_async_commit();
+  };
+  auto read = [&](int st, int tensor, int p, float (&f)[VEC]) {
+    const uint4 u = ld_shared_v4(slot(st, tensor, p));
+    unpack<T, VEC>(*reinterpret_cast<const V*>(&u), f);
+  };
+  const int step = gridDim.x * GROUPS;
+  int t = blockIdx.x * GROUPS + grp, st = 0;
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(t + s * step, s);
+  for (; t < a.rows; t += step) {
+    cp_async_wait<STAGES - 1>();
+    float h[VPT][VEC];
+    float s = 0.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) h[p][i] = 0.0f;
+      if (j + p * G < nv) {
+        read(st, 0, p, h[p]);
+        if (res) {
+          float r[VEC];
+          read(st, 1, p, r);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) h[p][i] += r[i];
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s += h[p][i];
+      }
+    }
+    fetch(t + STAGES * step, st);
+    st = st + 1 == STAGES ? 0 : st + 1;
+    const float mu = a.rms ? 0.0f : group_sum<G>(s, slots[grp], &turn, 1 + grp) * inv_h;
+    V* y = reinterpret_cast<V*>(a.y) + (int64_t)t * nv + j;
+    V* sum = reinterpret_cast<V*>(a.sum) + (int64_t)t * nv + j;
+    float q = 0.0f;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        if (a.sum) sum[p * G] = pack<T, VEC>(h[p]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          h[p][i] -= mu;
+          q = fmaf(h[p][i], h[p][i], q);
+        }
+      }
+    const float rs = 1.0f / sqrtf(group_sum<G>(q, slots[grp], &turn, 1 + grp) * inv_h + a.eps);
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < nv) {
+        float wf[VEC], v[VEC];
+        unpack<T, VEC>(wv[p], wf);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = h[p][i] * rs * wf[i];
+        if (a.b) {
+          float bf[VEC];
+          unpack<T, VEC>(bv[p], bf);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[i] += bf[i];
+        }
+        y[p * G] = pack<T, VEC>(v);
+      }
+    if (j == 0) {
+      if (a.mean) a.mean[t] = mu;
+      if (a.rstd) a.rstd[t] = rs;
+    }
+  }
+  cp_async_wait<0>();
 }
 
 struct BwdArgs {
@@ -335,7 +464,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
   using V = Vec<T, VEC>;
   pdl_wait();  // the previous kernel has completed and its writes are visible
   constexpr int GROUPS = 512 / G;
-  __shared__ float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 1];
+  __shared__ __align__(16) float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 2];
   extern __shared__ __align__(16) uint8_t ring[];  // [STAGES][3 tensors][VPT][512 threads] vectors
   const int grp = threadIdx.x / G, j = threadIdx.x % G;
   int turn = 0;
@@ -445,7 +574,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_odd(const BwdArgs a) {
   using V = Vec<T, VEC>;
   pdl_wait();  // the previous kernel has completed and its writes are visible
   constexpr int GROUPS = 512 / G;
-  __shared__ float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 1];
+  __shared__ __align__(16) float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 2];
   extern __shared__ float acc_smem[];  // [2][columns of a group], only with several groups
   const int grp = threadIdx.x / G, j = threadIdx.x % G;
   int turn = 0;
@@ -558,6 +687,20 @@ cudaError_t fwd_regs(const FwdArgs& a, int sms, cudaStream_t st) {
   return cudaSuccess;
 }
 
+template <typename T, int EPT, int G>
+cudaError_t fwd_ring(const FwdArgs& a, int sms, cudaStream_t st) {
+  constexpr int VPT = EPT * (int)sizeof(T) / 16, stage = 2 * VPT * 512 * 16, groups = 512 / G;
+  constexpr int stages = 131072 / stage < 4 ? 131072 / stage : 4;
+  static_assert(stages >= 2, "ring too small");
+  static std::atomic<int> cache{0};
+  auto kern = k_norm_fwd_ring<T, VPT, G, stages>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, stages * stage);
+  if (e != cudaSuccess) return e;
+  const int grid = resident_blocks(kern, &cache, 512, stages * stage, ((int64_t)a.rows + groups - 1) / groups, sms, 1 << 30);
+  MOE_LAUNCH(kern, grid, 512, stages * stage, st, a);
+  return cudaSuccess;
+}
+
 // Thirty-two elements a thread at most (they stay in registers) and the smallest group that covers
 // the row. With few rows the latency of one row counts instead: the whole block takes the row,
 // eight elements a thread where that covers it.
@@ -570,6 +713,14 @@ cudaError_t fwd_vec(const FwdArgs& a, int sms, cudaStream_t st, bool* taken) {
   if (a.rows < sms * 2) {
     if (h <= 2048) return fwd_regs<T, VEC, P, 256>(a, sms, st);
     if (h <= 4096) return fwd_regs<T, VEC, P, 512>(a, sms, st);
+  }
+  if constexpr (VEC > 1) {
+    // enough rows for several a group: the ring hides the loads behind the sums
+    if (a.rows >= sms * 16 && h > 1024 && h <= 8192) {
+      if (h <= 2048) return fwd_ring<T, 16, 128>(a, sms, st);
+      if (h <= 4096) return fwd_ring<T, 16, 256>(a, sms, st);
+      return fwd_ring<T, 16, 512>(a, sms, st);
+    }
   }
   if (h <= 512) return fwd_regs<T, VEC, 2 * P, 32>(a, sms, st);
   if (h <= 1024) return fwd_regs<T, VEC, 4 * P, 32>(a, sms, st);

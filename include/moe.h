@@ -265,7 +265,7 @@ MOE_API int moe_plan_quota(const moe_dims* dims, void* ws, size_t ws_bytes, void
 typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
 
 typedef struct moe_norm_dims {
-  int64_t T;      /* rows (tokens), >= 1 */
+  int64_t T;      /* rows (tokens), 1 <= T <= 2^31 - 2^20 */
   int64_t H;      /* row length, 1 <= H <= 65536; any value */
   int32_t dtype;  /* moe_dtype of x, residual, weight, bias, y, sum and every gradient */
   int32_t kind;   /* moe_norm_kind */
@@ -384,7 +384,7 @@ typedef enum {
 } moe_act;
 
 typedef struct moe_linear_dims {
-  int64_t M;        /* rows (tokens), 1 <= M < 2^31 */
+  int64_t M;        /* rows (tokens), 1 <= M <= 2^31 - 2^20 */
   int64_t K;        /* input features, 1 <= K < 2^24; any value */
   int64_t N;        /* output features, 1 <= N < 2^24; any value */
   int32_t dtype;    /* moe_dtype of x, w, bias, residual, pre and every gradient */
