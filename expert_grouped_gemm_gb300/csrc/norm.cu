@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kFwdThreads<G>) k_norm_fwd(const FwdArgs a) {
 // filled by 16-byte asynchronous copies, a row or more ahead of the sums. A thread copies exactly
 // the vectors it reads, so the ring needs no barrier.
 template <typename T, int VPT, int G, int STAGES>
-__global__ void __launch_bounds__(512) k_norm_fwd_ring(const FwdArgs a) {
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) k_norm_fwd_ring(const FwdArgs a) {
   constexpr int VEC = 16 / sizeof(T);
   using V = Vec<T, VEC>;
   pdl_wait();  // the previous kernel has completed and its writes are visible
@@ -690,7 +690,8 @@ cudaError_t fwd_regs(const FwdArgs& a, int sms, cudaStream_t st) {
 template <typename T, int EPT, int G>
 cudaError_t fwd_ring(const FwdArgs& a, int sms, cudaStream_t st) {
   constexpr int VPT = EPT * (int)sizeof(T) / 16, stage = 2 * VPT * 512 * 16, groups = 512 / G;
-  constexpr int stages = 131072 / stage < 4 ? 131072 / stage : 4;
+  constexpr int room = sizeof(T) == 2 ? 98304 : 131072;  // two blocks an SM in bf16, one in fp32
+  constexpr int stages = room / stage < 4 ? room / stage : 4;
   static_assert(stages >= 2, "ring too small");
   static std::atomic<int> cache{0};
   auto kern = k_norm_fwd_ring<T, VPT, G, stages>;
