@@ -702,26 +702,30 @@ cudaError_t fwd_ring(const FwdArgs& a, int sms, cudaStream_t st) {
   return cudaSuccess;
 }
 
-// Thirty-two elements a thread at most (they stay in registers) and the smallest group that covers
-// the row. With few rows the latency of one row counts instead: the whole block takes the row,
-// eight elements a thread where that covers it.
+// Many aligned rows go through the ring (16 rows an SM and more: 6000 rows of 1024 in bf16 take
+// 10.4 us, 14.2 in registers; 3000 rows of 2048 and fewer leave a group about a row, where the
+// registers are as fast). Else thirty-two elements a thread at most (they stay in registers) and
+// the smallest group that covers the row; with few rows the latency of one row counts, and the
+// whole block takes the row, eight elements a thread where that covers it.
 template <typename T, int VEC>
 cudaError_t fwd_vec(const FwdArgs& a, int sms, cudaStream_t st, bool* taken) {
   constexpr int P = 8 / VEC;  // vectors of eight elements
   const int h = a.H;
   *taken = true;
+  if constexpr (VEC > 1) {
+    if (a.rows >= sms * 16) {
+      if (h <= 256) return fwd_ring<T, 8, 32>(a, sms, st);
+      if (h <= 512) return fwd_ring<T, 16, 32>(a, sms, st);
+      if (h <= 1024) return fwd_ring<T, 8, 128>(a, sms, st);
+      if (h <= 2048) return fwd_ring<T, 16, 128>(a, sms, st);
+      if (h <= 4096) return fwd_ring<T, 16, 256>(a, sms, st);
+      if (h <= 8192) return fwd_ring<T, 16, 512>(a, sms, st);
+    }
+  }
   if (h <= 256) return fwd_regs<T, VEC, P, 32>(a, sms, st);
   if (a.rows < sms * 2) {
     if (h <= 2048) return fwd_regs<T, VEC, P, 256>(a, sms, st);
     if (h <= 4096) return fwd_regs<T, VEC, P, 512>(a, sms, st);
-  }
-  if constexpr (VEC > 1) {
-    // enough rows for several a group: the ring hides the loads behind the sums
-    if (a.rows >= sms * 16 && h > 1024 && h <= 8192) {
-      if (h <= 2048) return fwd_ring<T, 16, 128>(a, sms, st);
-      if (h <= 4096) return fwd_ring<T, 16, 256>(a, sms, st);
-      return fwd_ring<T, 16, 512>(a, sms, st);
-    }
   }
   if (h <= 512) return fwd_regs<T, VEC, 2 * P, 32>(a, sms, st);
   if (h <= 1024) return fwd_regs<T, VEC, 4 * P, 32>(a, sms, st);
