@@ -46,6 +46,7 @@ struct GateArgs {
   int per;     // experts of a group
   int L, R;    // lanes of a group, experts of a lane
   int vec;     // the lanes' experts can be read (and written) 16 bytes at a time
+  int vec_bias;  // and their biases
   int direct;  // the logits decide the order
   float scale;
 };
@@ -74,6 +75,25 @@ __device__ __forceinline__ void load_logits(const TL* p, int n, bool vec, float 
     const float v = i < n ? io<TL>::to_f(p[i]) : -INFINITY;
     l[i] = v != v ? -INFINITY : v;
   }
+}
+
+template <int EPL>
+__device__ __forceinline__ void load_bias(const float* p, int n, bool vec, float (&b)[EPL]) {
+  if constexpr (EPL % 4 == 0) {
+    if (p && vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 4) {
+        const float4 u = i < n ? *reinterpret_cast<const float4*>(p + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        b[i] = u.x;
+        b[i + 1] = u.y;
+        b[i + 2] = u.z;
+        b[i + 3] = u.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) b[i] = p && i < n ? p[i] : 0.0f;
 }
 
 // e^{l - m} of a softmax with maximum m: 0 for masked experts, 1 at the maximum (which may be +inf)
@@ -176,9 +196,11 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
 #pragma unroll
           for (int i = 0; i < EPL; ++i) l[i] = sigmoidf_(l[i]);  // within 4 ulp; the weights are taken in full precision below
         }
+        float bias[EPL];
+        load_bias<EPL>(a.bias ? a.bias + e0 : nullptr, n, a.vec_bias, bias);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          const float c = l[i] + (a.bias && i < n ? a.bias[e0 + i] : 0.0f);
+          const float c = l[i] + bias[i];
           key[i] = i >= n ? kKeyNone : (key[i] || !(c > -INFINITY)) ? kKeyMasked : order_key(c);
         }
       }
@@ -208,7 +230,7 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
       }
     }
     // k rounds: the largest key of the warp, in its lowest lane. Lanes with few experts sort them
-    // once and then drop the first; longer lists are searched again by the lane that gave one.
+    // once and then drop the first; longer lists are searched again, in part, by the lane that gave one.
     int my_e = 0;
     if constexpr (EPL <= 8) {
       int at[EPL];
@@ -228,21 +250,36 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
         }
       }
     } else {
-      uint32_t best = kKeyNone;  // this lane's largest key, the first expert that has it
-      int bi = 0;
-      auto search = [&]() {
-        uint32_t b = key[0];
-        int nb = 0;
+      // eights of the list keep their largest key and its place: only the eighth that lost a key is
+      // searched again
+      constexpr int N = 8, NG = EPL / N;
+      uint32_t gb[NG];
+      int gi[NG];
+      auto search = [&](int g) {
+        gb[g] = key[g * N];
+        gi[g] = g * N;
 #pragma unroll
-        for (int i = 1; i < EPL; ++i)
-          if (key[i] > b) {
-            b = key[i];
-            nb = i;
+        for (int i = 1; i < N; ++i)
+          if (key[g * N + i] > gb[g]) {
+            gb[g] = key[g * N + i];
+            gi[g] = g * N + i;
           }
-        best = b;
-        bi = nb;
       };
-      search();
+      uint32_t best;
+      int bi;
+      auto pick = [&]() {
+        best = gb[0];
+        bi = gi[0];
+#pragma unroll
+        for (int g = 1; g < NG; ++g)
+          if (gb[g] > best) {
+            best = gb[g];
+            bi = gi[g];
+          }
+      };
+#pragma unroll
+      for (int g = 0; g < NG; ++g) search(g);
+      pick();
       for (int j = 0; j < a.k; ++j) {
         const uint32_t top = __reduce_max_sync(kFull, best);
         const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
@@ -250,9 +287,14 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
         if (lane == j) my_e = e;
         if (lane == who) {
 #pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (i == bi) key[i] = kKeyNone;
-          search();
+          for (int g = 0; g < NG; ++g)
+            if (bi / N == g) {
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                if (g * N + i == bi) key[g * N + i] = kKeyNone;
+              search(g);
+            }
+          pick();
         }
       }
     }
@@ -476,6 +518,7 @@ cudaError_t launch_gate_fwd(const moe_gate_dims& d, const void* logits, const fl
   a.R = (a.per + a.L - 1) / a.L;
   const int V = d.dtype == MOE_BF16 ? 8 : 4;
   a.vec = a.E % V == 0 && a.per % V == 0 && a.R % V == 0;
+  a.vec_bias = a.E % 4 == 0 && a.per % 4 == 0 && a.R % 4 == 0 && reinterpret_cast<uintptr_t>(bias) % 16 == 0;
   a.direct = !bias && (a.Kg == a.G || a.take == 1);
   return with_epl(a.R, [&](auto epl) {
     constexpr int EPL = decltype(epl)::value;

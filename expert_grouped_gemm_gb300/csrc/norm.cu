@@ -413,10 +413,10 @@ struct BwdArgs {
 
 // The groups' column sums are added in order through shared memory ([element][thread], free of bank
 // conflicts) and written as one row of partial sums a block.
-template <int VEC, int VPT, int G>
+template <int VEC, int VPT, int G, int THREADS>
 __device__ __forceinline__ void write_part(const BwdArgs& a, float (&aw)[VPT][VEC], float (&ab)[VPT][VEC],
                                            float* smem) {
-  constexpr int GROUPS = 512 / G, COLS = G * VPT * VEC;
+  constexpr int GROUPS = THREADS / G, COLS = G * VPT * VEC;
   const int grp = threadIdx.x / G, j = threadIdx.x % G;
   for (int k = 1; k < GROUPS; ++k) {  // group 0 collects the others', one group at a time
     __syncthreads();
@@ -563,103 +563,83 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
     st = st + 1 == STAGES ? 0 : st + 1;
   }
   cp_async_wait<0>();
-  write_part<VEC, VPT, G>(a, aw, ab, reinterpret_cast<float*>(ring));
+  write_part<VEC, VPT, G, 512>(a, aw, ab, reinterpret_cast<float*>(ring));
 }
 
-// The same for rows without 16-byte alignment, element by element: the next row's loads travel in
-// registers while this row's sums meet.
+// The same for rows without 16-byte alignment, element by element: thread j keeps the columns
+// j + p G, and the next row's loads travel in registers while this row's sums meet. Slots past the
+// row are skipped by the whole group.
+template <int G>
+constexpr int odd_threads = G < 256 ? 256 : G;
+
 template <typename T, int VPT, int G>
-__global__ void __launch_bounds__(512) k_norm_bwd_odd(const BwdArgs a) {
-  constexpr int VEC = 1;
-  using V = Vec<T, VEC>;
+__global__ void __launch_bounds__(odd_threads<G>) k_norm_bwd_odd(const BwdArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  constexpr int GROUPS = 512 / G;
+  constexpr int GROUPS = odd_threads<G> / G;
   __shared__ __align__(16) float2 slots[GROUPS][G > 32 ? 2 * (G / 32) : 2];
   extern __shared__ float acc_smem[];  // [2][columns of a group], only with several groups
   const int grp = threadIdx.x / G, j = threadIdx.x % G;
   int turn = 0;
-  const int nv = a.H / VEC;
-  const float inv_h = 1.0f / (float)a.H;
-  const V* dy = reinterpret_cast<const V*>(a.dy);
-  const V* ds = reinterpret_cast<const V*>(a.dsum);
-  const V* x = reinterpret_cast<const V*>(a.x);
-  V* dx = reinterpret_cast<V*>(a.dx);
-  V wv[VPT];
-  float aw[VPT][VEC], ab[VPT][VEC];
+  const int H = a.H;
+  const float inv_h = 1.0f / (float)H;
+  const T* dy = reinterpret_cast<const T*>(a.dy);
+  const T* ds = reinterpret_cast<const T*>(a.dsum);
+  const T* x = reinterpret_cast<const T*>(a.x);
+  T* dx = reinterpret_cast<T*>(a.dx);
+  float w[VPT], aw[VPT][1], ab[VPT][1];
 #pragma unroll
   for (int p = 0; p < VPT; ++p) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) aw[p][i] = ab[p][i] = 0.0f;
-    if (j + p * G < nv) wv[p] = reinterpret_cast<const V*>(a.w)[j + p * G];
+    aw[p][0] = ab[p][0] = 0.0f;
+    w[p] = j + p * G < H ? io<T>::to_f(reinterpret_cast<const T*>(a.w)[j + p * G]) : 0.0f;
   }
-  V ndy[VPT], nx[VPT], nds[VPT];
+  T ndy[VPT], nx[VPT], nds[VPT];
   float nmu = 0.0f, nrs = 0.0f;
   auto fetch = [&](int t) {
     if (t >= a.rows) return;
-    const int64_t o = (int64_t)t * nv;
+    const int64_t o = (int64_t)t * H + j;
     nmu = a.mean ? a.mean[t] : 0.0f;
     nrs = a.rstd[t];
 #pragma unroll
-    for (int p = 0; p < VPT; ++p)
-      if (j + p * G < nv) {
-        ndy[p] = dy[o + j + p * G];
-        nx[p] = x[o + j + p * G];
-        if (ds) nds[p] = ds[o + j + p * G];
+    for (int p = 0; p < VPT; ++p) {
+      if (p * G >= H) break;
+      if (j + p * G < H) {
+        ndy[p] = dy[o + p * G];
+        nx[p] = x[o + p * G];
+        if (ds) nds[p] = ds[o + p * G];
       }
+    }
   };
   const int step = gridDim.x * GROUPS;
-  fetch(blockIdx.x * GROUPS + grp);
-  for (int t = blockIdx.x * GROUPS + grp; t < a.rows; t += step) {
-    const float mu = nmu, rs = nrs;
-    V cdy[VPT], cx[VPT], cds[VPT];
+  int t = blockIdx.x * GROUPS + grp;
+  fetch(t);
+  for (; t < a.rows; t += step) {
+    const float rs = nrs, off = -nmu * nrs;  // xh = x rs + off
+    float d[VPT], xh[VPT], e[VPT];
     float s = 0.0f, q = 0.0f;
-    // g = dy w and xh of one vector, from the values as loaded (kept that way: they are converted
-    // again after the sums, which costs less than the registers of their fp32 forms)
-    auto expand = [&](int p, float (&d)[VEC], float (&xh)[VEC], float (&wf)[VEC]) {
-      unpack<T, VEC>(cdy[p], d);
-      unpack<T, VEC>(cx[p], xh);
-      unpack<T, VEC>(wv[p], wf);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) xh[i] = (xh[i] - mu) * rs;
-    };
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      if (j + p * G < nv) {
-        cdy[p] = ndy[p];
-        cx[p] = nx[p];
-        if (ds) cds[p] = nds[p];
-        float d[VEC], xh[VEC], wf[VEC];
-        expand(p, d, xh, wf);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          aw[p][i] = fmaf(d[i], xh[i], aw[p][i]);
-          ab[p][i] += d[i];
-          const float g = d[i] * wf[i];
-          s += g;
-          q = fmaf(g, xh[i], q);
-        }
-      }
+      if (p * G >= H) break;
+      const bool in = j + p * G < H;
+      d[p] = in ? io<T>::to_f(ndy[p]) : 0.0f;
+      xh[p] = in ? fmaf(io<T>::to_f(nx[p]), rs, off) : 0.0f;
+      e[p] = in && ds ? io<T>::to_f(nds[p]) : 0.0f;
+      aw[p][0] = fmaf(d[p], xh[p], aw[p][0]);
+      ab[p][0] += d[p];
+      d[p] *= w[p];
+      s += d[p];
+      q = fmaf(d[p], xh[p], q);
     }
     fetch(t + step);
     const float2 r = group_sum2<G>(s, q, slots[grp], &turn, 1 + grp);
-    const float ms = a.mean ? r.x * inv_h : 0.0f, mq = r.y * inv_h;
-    const int64_t o = (int64_t)t * nv;
+    const float ms = a.mean ? rs * r.x * inv_h : 0.0f, mq = rs * r.y * inv_h;
+    T* o = dx + (int64_t)t * H + j;
 #pragma unroll
-    for (int p = 0; p < VPT; ++p)
-      if (j + p * G < nv) {
-        float d[VEC], xh[VEC], wf[VEC], v[VEC];
-        expand(p, d, xh, wf);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = rs * (d[i] * wf[i] - ms - xh[i] * mq);
-        if (ds) {
-          unpack<T, VEC>(cds[p], d);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) v[i] += d[i];
-        }
-        dx[o + j + p * G] = pack<T, VEC>(v);
-      }
+    for (int p = 0; p < VPT; ++p) {
+      if (p * G >= H) break;
+      if (j + p * G < H) o[p * G] = io<T>::cvt(fmaf(-xh[p], mq, fmaf(d[p], rs, -ms)) + e[p]);
+    }
   }
-  write_part<VEC, VPT, G>(a, aw, ab, acc_smem);
+  write_part<1, VPT, G, odd_threads<G>>(a, aw, ab, acc_smem);
 }
 
 // ---------------------------------------------------------------- choice of the variant
@@ -768,12 +748,12 @@ cudaError_t bwd_ring(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
 
 template <typename T, int VPT, int G>
 cudaError_t bwd_odd(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
-  constexpr int groups = 512 / G;
+  constexpr int threads = odd_threads<G>, groups = threads / G;
   constexpr size_t smem = groups > 1 ? sizeof(float) * 2 * G * VPT : 0;
   static std::atomic<int> cache{0};
   auto kern = k_norm_bwd_odd<T, VPT, G>;
-  *chunks = resident_blocks(kern, &cache, 512, smem, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
-  MOE_LAUNCH(kern, *chunks, 512, smem, st, a);
+  *chunks = resident_blocks(kern, &cache, threads, smem, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  MOE_LAUNCH(kern, *chunks, threads, smem, st, a);
   return cudaSuccess;
 }
 
@@ -786,6 +766,7 @@ cudaError_t bwd_regs(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
   if (h % (16 / (int)sizeof(T))) {
     if (h <= 256) return bwd_odd<T, 8, 32>(a, sms, st, chunks);
     if (h <= 1024) return bwd_odd<T, 8, 128>(a, sms, st, chunks);
+    if (h <= 2048) return bwd_odd<T, 16, 128>(a, sms, st, chunks);
     if (h <= 4096) return bwd_odd<T, 8, 512>(a, sms, st, chunks);
     if (h <= 8192) return bwd_odd<T, 16, 512>(a, sms, st, chunks);
     return cudaSuccess;
