@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "act.cuh"
 #include "block.h"
 #include "common.cuh"
 
@@ -153,9 +154,40 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[EPL], int (&at)[EPL]) 
     }
 }
 
+// Bitonic sort of one (key, expert) a lane: keys descending, equal keys by ascending expert.
+__device__ __forceinline__ void warp_sort(uint32_t& key, int& e, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int o = size >> 1; o > 0; o >>= 1) {
+      const uint32_t ok = __shfl_xor_sync(kFull, key, o);
+      const int oe = __shfl_xor_sync(kFull, e, o);
+      const bool mine_first = key > ok || (key == ok && e < oe);
+      // the lower lane of the pair keeps the first in a descending run, the last in an ascending one
+      const bool keep_first = ((lane & o) == 0) == ((lane & size) == 0);
+      if (mine_first != keep_first) {
+        key = ok;
+        e = oe;
+      }
+    }
+}
+// The same for keys alone.
+__device__ __forceinline__ uint32_t warp_sort(uint32_t key, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int o = size >> 1; o > 0; o >>= 1) {
+      const uint32_t ok = __shfl_xor_sync(kFull, key, o);
+      const bool larger = ((lane & o) == 0) == ((lane & size) == 0);
+      key = larger ? max(key, ok) : min(key, ok);
+    }
+  return key;
+}
+
 template <int EPL, bool SOFTMAX, typename TL>
 __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const GateArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ uint2 candidates[EPL <= 8 ? 1 : one_block_tokens<EPL>][32];
   __shared__ int hist[1024];  // one block only: it has every token and writes the counts itself
   const bool one = gridDim.x == 1 && a.count;
   if (one) {
@@ -194,7 +226,7 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
           softmax_row<EPL>(l, &m, &inv);
         } else {
 #pragma unroll
-          for (int i = 0; i < EPL; ++i) l[i] = sigmoidf_(l[i]);  // within 4 ulp; the weights are taken in full precision below
+          for (int i = 0; i < EPL; ++i) l[i] = sigmoid_of<true>(l[i]);  // within a few ulp; the weights are taken in full precision below
         }
         float bias[EPL];
         load_bias<EPL>(a.bias ? a.bias + e0 : nullptr, n, a.vec_bias, bias);
@@ -229,10 +261,11 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
         for (int i = 0; i < EPL; ++i) key[i] = kKeyNone;
       }
     }
-    // k rounds: the largest key of the warp, in its lowest lane. Lanes with few experts sort them
-    // once and then drop the first; longer lists are searched again, in part, by the lane that gave one.
     int my_e = 0;
     if constexpr (EPL <= 8) {
+      // Lanes with few experts sort them once; k rounds take the largest key of the warp, in its
+      // lowest lane, and that lane drops its first. (Gathering as below: E = 128, k = 8 at 8192
+      // tokens 7.2 us, so 5.2; E = 1024 at 2000 tokens 9.9, so 13.)
       int at[EPL];
       sort_keys<EPL>(key, at);
       for (int j = 0; j < a.k; ++j) {
@@ -250,51 +283,55 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
         }
       }
     } else {
-      // eights of the list keep their largest key and its place: only the eighth that lost a key is
-      // searched again
-      constexpr int N = 8, NG = EPL / N;
-      uint32_t gb[NG];
-      int gi[NG];
-      auto search = [&](int g) {
-        gb[g] = key[g * N];
-        gi[g] = g * N;
+      // The k-th largest of the lanes' maxima bounds the k-th largest key from below, so the keys at or
+      // above it hold the k chosen ones and, as a rule, few others: they are gathered, one a lane, and
+      // sorted. More than 32 of them (many equal keys, few lanes with any) are taken one by one.
+      uint32_t lane_max = key[0];
 #pragma unroll
-        for (int i = 1; i < N; ++i)
-          if (key[g * N + i] > gb[g]) {
-            gb[g] = key[g * N + i];
-            gi[g] = g * N + i;
-          }
-      };
-      uint32_t best;
-      int bi;
-      auto pick = [&]() {
-        best = gb[0];
-        bi = gi[0];
+      for (int i = 1; i < EPL; ++i) lane_max = max(lane_max, key[i]);
+      const uint32_t bound = max(__shfl_sync(kFull, warp_sort(lane_max, lane), a.k - 1), kKeyMasked);
+      uint2* cand = candidates[threadIdx.x >> 5];
+      int count = 0;
 #pragma unroll
-        for (int g = 1; g < NG; ++g)
-          if (gb[g] > best) {
-            best = gb[g];
-            bi = gi[g];
-          }
-      };
+      for (int i = 0; i < EPL; ++i) {
+        const uint32_t m = __ballot_sync(kFull, key[i] >= bound);
+        if (m) {
+          const int pos = count + __popc(m & ((1u << lane) - 1u));
+          if (key[i] >= bound && pos < 32) cand[pos] = make_uint2(key[i], (uint32_t)(e0 + i));
+          count += __popc(m);
+        }
+      }
+      if (count <= 32) {
+        __syncwarp();
+        const uint2 c = lane < count ? cand[lane] : make_uint2(kKeyNone, 0x7fffffffu);
+        uint32_t ck = c.x;
+        my_e = (int)c.y;
+        warp_sort(ck, my_e, lane);
+      } else {
+        uint32_t best;  // this lane's largest key, the first expert that has it
+        int bi;
+        auto search = [&]() {
+          best = key[0];
+          bi = 0;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) search(g);
-      pick();
-      for (int j = 0; j < a.k; ++j) {
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
-        const int e = __shfl_sync(kFull, e0 + bi, who);
-        if (lane == j) my_e = e;
-        if (lane == who) {
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            if (bi / N == g) {
-#pragma unroll
-              for (int i = 0; i < N; ++i)
-                if (g * N + i == bi) key[g * N + i] = kKeyNone;
-              search(g);
+          for (int i = 1; i < EPL; ++i)
+            if (key[i] > best) {
+              best = key[i];
+              bi = i;
             }
-          pick();
+        };
+        search();
+        for (int j = 0; j < a.k; ++j) {
+          const uint32_t top = __reduce_max_sync(kFull, best);
+          const int who = __ffs(__ballot_sync(kFull, best == top)) - 1;
+          const int e = __shfl_sync(kFull, e0 + bi, who);
+          if (lane == j) my_e = e;
+          if (lane == who) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (i == bi) key[i] = kKeyNone;
+            search();
+          }
         }
       }
     }
@@ -377,6 +414,11 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const int e0 = lane * a.R, n = max(0, min(a.R, a.E - e0));
+  // what the slots add to each expert's gradient, in the lanes' order
+  __shared__ __align__(16) float sums[8][32 * EPL];
+  float* sum = sums[threadIdx.x >> 5];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) sum[lane + 32 * i] = 0.0f;
   const TL* row = reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E;
   // slot j in lane j; a skipped or masked slot takes no part
   int my_e = -1;
@@ -414,16 +456,21 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
     }
     d = dw * s * (1.0f - s);
   }
+  // expert e is lane e / R's element e % R; its sum stands at [e % R][lane], free of bank conflicts
+  const int at = my_e >= 0 ? (my_e % a.R) * 32 + my_e / a.R : -1;
+  const bool first = (__ffs(__match_any_sync(kFull, my_e)) - 1) == lane;
+  __syncwarp();
+  if (at >= 0 && first) sum[at] = d;
+  if (__any_sync(kFull, at >= 0 && !first)) {  // an expert listed twice: the others add to it in slot order
+    for (int j = 0; j < a.k; ++j) {
+      __syncwarp();
+      if (lane == j && at >= 0 && !first) sum[at] += d;
+    }
+  }
+  __syncwarp();
   float out[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kFull, my_e, j) - e0;  // outside [0, R) where another lane has it (or none)
-    const float dj = __shfl_sync(kFull, d, j);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (e == i) out[i] += dj;
-  }
+  for (int i = 0; i < EPL; ++i) out[i] = sum[i * 32 + lane];
   if (dense) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) out[i] = l[i] * (out[i] - dot);
