@@ -286,10 +286,17 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
       // The k-th largest of the lanes' maxima bounds the k-th largest key from below, so the keys at or
       // above it hold the k chosen ones and, as a rule, few others: they are gathered, one a lane, and
       // sorted. More than 32 of them (many equal keys, few lanes with any) are taken one by one.
-      uint32_t lane_max = key[0];
+      uint32_t half[2] = {kKeyNone, kKeyNone};  // the maxima of the lane's two halves
 #pragma unroll
-      for (int i = 1; i < EPL; ++i) lane_max = max(lane_max, key[i]);
-      const uint32_t bound = max(__shfl_sync(kFull, warp_sort(lane_max, lane), a.k - 1), kKeyMasked);
+      for (int i = 0; i < EPL; ++i) half[2 * i / EPL] = max(half[2 * i / EPL], key[i]);
+      uint32_t top = warp_sort(max(half[0], half[1]), lane);
+      if (a.Kg < a.G) {
+        // lanes of dropped groups hold nothing: the 32 largest of both halves' maxima bound more
+        // tightly (one list against the other reversed; 16 of 2 x 128 experts at 16384 tokens: 30 us, 51 without)
+        const uint32_t low = warp_sort(min(half[0], half[1]), lane);
+        top = warp_sort(max(top, __shfl_sync(kFull, low, 31 - lane)), lane);
+      }
+      const uint32_t bound = max(__shfl_sync(kFull, top, a.k - 1), kKeyMasked);
       uint2* cand = candidates[threadIdx.x >> 5];
       int count = 0;
 #pragma unroll

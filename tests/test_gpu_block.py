@@ -31,6 +31,18 @@ def test_norm(T, H, dtype, kind, residual):
     C.check_norm_bwd(c, mean, rstd, C.run_norm_bwd(c, mean=mean, rstd=rstd, dbias=kind == "layer"))
 
 
+@pytest.mark.parametrize("T,H", [(2440, 64), (2500, 256), (2433, 504), (3000, 1000), (2432, 2048), (2600, 1544), (2450, 4096),
+                                 (2435, 8192), (2441, 1023)])
+@pytest.mark.parametrize("dtype,kind,residual", [("bf16", "layer", True), ("bf16", "rms", False), ("f32", "layer", False),
+                                                 ("f32", "rms", True)])
+def test_norm_several_rows_a_group(T, H, dtype, kind, residual):
+    """Enough rows that every group of threads walks several, loads of later rows running ahead."""
+    c = C.norm_case(T, H, dtype, kind, residual, bias=kind == "layer", seed=H)
+    C.check_norm_fwd(c, C.run_norm_fwd(c))
+    mean, rstd = C.norm_stats(c)
+    C.check_norm_bwd(c, mean, rstd, C.run_norm_bwd(c, mean=mean, rstd=rstd, dbias=kind == "layer"))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_many_rows(dtype):
     """More rows than any grid has blocks, narrow rows and the weight gradients over all of them."""
@@ -94,7 +106,7 @@ GATES = [
     (1, 1, 1, 1, 1, 1), (1, 128, 8, 1, 1, 1), (8, 128, 8, 1, 1, 1), (77, 8, 2, 1, 1, 1), (300, 160, 6, 8, 3, 1),
     (200, 256, 8, 8, 4, 2), (33, 33, 33 - 1, 1, 1, 1), (64, 512, 16, 4, 2, 2), (50, 60, 10, 4, 1, 2),
     (19, 1024, 32, 32, 5, 2), (100, 40, 5, 8, 1, 2), (40, 24, 7, 8, 4, 2), (513, 64, 4, 2, 2, 1), (9, 16, 16, 1, 1, 1),
-    (21, 96, 3, 32, 2, 2),
+    (21, 96, 3, 32, 2, 2), (30, 990, 9, 3, 2, 2), (40, 35, 4, 5, 2, 2), (70, 700, 12, 7, 3, 1), (25, 512, 16, 8, 1, 2),
 ]
 
 
@@ -176,6 +188,16 @@ LINEAR_SIZES = [(1, 1, 1), (3, 1, 5), (1, 64, 64), (1, 2048, 768), (2, 100, 36),
 @pytest.mark.parametrize("act,bias,residual", [("none", True, True), ("gelu", True, False), ("silu", False, True)])
 def test_linear(M, K, N, dtype, act, bias, residual):
     c = C.linear_case(M, K, N, dtype, act, bias, residual, seed=M + K + N)
+    C.check_linear_fwd(c, C.run_linear_fwd(c, save=act != "none"))
+    pre = C.linear_pre(c)
+    C.check_linear_bwd(c, pre, C.run_linear_bwd(c, pre, db=bias))
+
+
+@pytest.mark.parametrize("M,K,N", [(2048, 512, 2048), (2560, 256, 2048), (2300, 200, 4104), (1030, 520, 3001), (2100, 131, 2049)])
+@pytest.mark.parametrize("act,bias,residual", [("gelu", True, True), ("none", False, False)])
+def test_linear_many_tiles(M, K, N, act, bias, residual):
+    """Outputs of several rounds of 256 x 256 tiles, ragged ones and a last round in half tiles among them."""
+    c = C.linear_case(M, K, N, "bf16", act, bias, residual, seed=3)
     C.check_linear_fwd(c, C.run_linear_fwd(c, save=act != "none"))
     pre = C.linear_pre(c)
     C.check_linear_bwd(c, pre, C.run_linear_bwd(c, pre, db=bias))
@@ -263,6 +285,66 @@ def test_linear_infinities_and_nan_pass_through(M, K, N):
     assert torch.isnan(y[1]).all()
     keep = torch.arange(M, device="cuda") != 1
     assert torch.isfinite(y[keep]).all()
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+def _tail(t, n=3):
+    return t[-n:].contiguous()
+
+
+def test_norm_offsets_past_32_bits():
+    T, H = 2_200_003, 1000  # 2.2e9 elements
+    d = _lib.make_norm_dims(T, H)
+    x = torch.randn(T, H, device="cuda", dtype=torch.bfloat16)
+    w, b = C.rand(40)(H, dtype=torch.bfloat16), C.rand(41)(H, dtype=torch.bfloat16)
+    y, m, r = torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    _lib.moe_norm_fwd(d, x, None, w, b, y, None, m, r)
+    c = dict(x=_tail(x), res=None, w=w, b=b, dtype="bf16", kind="layer", eps=1e-5)
+    C.check_norm_fwd(c, (_tail(y), None, m[-3:], r[-3:]))
+    dy = torch.zeros_like(x)
+    dy[-3:] = C.rand(42)(3, H, dtype=torch.bfloat16)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    _lib.moe_norm_bwd(d, _lib.alloc_norm_workspace(d), dy, None, x, w, m, r, dx, dw, db)
+    c.update(T=3, H=H, dy=_tail(dy), dsum=None)
+    C.check_norm_bwd(c, m[-3:], r[-3:], (_tail(dx), dw, db))
+    assert float(dx[:-3].abs().max()) == 0.0
+
+
+def test_gate_offsets_past_32_bits():
+    T, E, k = 9_000_001, 248, 2  # 2.2e9 logits
+    d = _lib.make_gate_dims(T, E, k, "softmax", True, grad_dtype="bf16")
+    logits = torch.randn(T, E, device="cuda")
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w, cnt = torch.empty(T, k, device="cuda"), torch.empty(E, dtype=torch.int32, device="cuda")
+    _lib.moe_gate_fwd(d, logits, None, idx, w, cnt)
+    assert int(cnt.sum()) == T * k and torch.equal(cnt, torch.bincount(idx.flatten(), minlength=E).int())
+    t, i = _tail(logits, 50), _tail(idx, 50)
+    C.check_gate(t, None, k, "softmax", True, 1.0, (i, _tail(w, 50), torch.bincount(i.flatten(), minlength=E).int()))
+    dw = torch.randn(T, k, device="cuda")
+    dl = torch.empty(T, E, dtype=torch.bfloat16, device="cuda")
+    _lib.moe_gate_bwd(d, logits, idx, dw, dl)
+    C.check_gate_bwd(t, i, _tail(dw, 50), "softmax", True, 1.0, _tail(dl, 50))
+
+
+@pytest.mark.parametrize("N", [2048, 2050])
+def test_linear_offsets_past_32_bits(N):
+    M, K = 1_100_001, 64  # 2.25e9 outputs
+    c = dict(M=3, K=K, N=N, dtype="bf16", act="relu", out_f32=False, x=torch.randn(M, K, device="cuda").bfloat16(),
+             w=C.rand(43)(K, N, scale=0.1, dtype=torch.bfloat16), bias=C.rand(44)(N, dtype=torch.bfloat16),
+             res=torch.randn(M, N, device="cuda", dtype=torch.bfloat16))
+    d = _lib.make_linear_dims(M, K, N, "bf16", "relu")
+    ws = _lib.alloc_linear_workspace(d)
+    y, pre = torch.empty_like(c["res"]), torch.empty_like(c["res"])
+    _lib.moe_linear_fwd(d, ws, c["x"], c["w"], c["bias"], c["res"], y, pre)
+    assert _lib.moe_read_status(ws) == _lib.MOE_OK
+    t = dict(c, x=_tail(c["x"]), res=_tail(c["res"]))
+    C.check_linear_fwd(t, (_tail(y), _tail(pre)))
+    dy = torch.zeros_like(y)
+    dy[-3:] = C.rand(45)(3, N, dtype=torch.bfloat16)
+    dx, dw, db = torch.empty_like(c["x"]), torch.empty_like(c["w"]), torch.empty_like(c["bias"])
+    _lib.moe_linear_bwd(d, ws, dy, c["x"], c["w"], pre, dx, dw, db)
+    assert _lib.moe_read_status(ws) == _lib.MOE_OK
+    C.check_linear_bwd(dict(t, dy=_tail(dy)), _tail(pre), (_tail(dx), dw, db))
 
 
 # ---------------------------------------------------------------- all of them
