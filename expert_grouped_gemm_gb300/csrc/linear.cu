@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtGemm g, i
     A.stash(sa[buf]);
     B.stash(sb[buf]);
   };
-  float acc[8][4] = {};
+  // two rows of an output column share one packed FMA (fma.rn.f32x2: the same roundings, half the
+  // instructions)
+  uint64_t acc[4][4] = {};
   fetch(s0);
   stash(0);
   __syncthreads();
@@ -129,23 +131,31 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtGemm g, i
     if (s + 1 < s1) fetch(s + 1);
 #pragma unroll
     for (int k = 0; k < kSK; ++k) {
-      const float4 a0 = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8]);
-      const float4 a1 = *reinterpret_cast<const float4*>(&sa[buf][k][ty * 8 + 4]);
+      const ulonglong2 a0 = *reinterpret_cast<const ulonglong2*>(&sa[buf][k][ty * 8]);
+      const ulonglong2 a1 = *reinterpret_cast<const ulonglong2*>(&sa[buf][k][ty * 8 + 4]);
       const float4 b = *reinterpret_cast<const float4*>(&sb[buf][k][tx * 4]);
-      const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const uint64_t av[4] = {a0.x, a0.y, a1.x, a1.y};
       const float bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int j = 0; j < 4; ++j) {
+        uint64_t bb;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(bv[j]));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        for (int i = 0; i < 4; ++i) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i][j]) : "l"(av[i]), "l"(bb));
+      }
     }
     if (s + 1 < s1) stash(buf ^ 1);
     __syncthreads();
     buf ^= 1;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<float4*>(&sums[ty * 8 + i][tx * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  for (int i = 0; i < 4; ++i) {
+    float lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("mov.b64 {%0, %1}, %2;" : "=f"(lo[j]), "=f"(hi[j]) : "l"(acc[i][j]));
+    *reinterpret_cast<float4*>(&sums[ty * 8 + 2 * i][tx * 4]) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<float4*>(&sums[ty * 8 + 2 * i + 1][tx * 4]) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+  }
   if (S > 1) cluster_sync_all();
   else __syncthreads();
   // this block's share of the tile's rows, four columns a thread
