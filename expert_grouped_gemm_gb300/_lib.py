@@ -157,14 +157,15 @@ def _ptr(t, name, dtype=None, required=True):
 
 
 # The current stream's handle as a number, without a Stream object made for every call (3 us on a Grace
-# core against 0.4); PyTorch versions without the function take the public way.
+# core against 0.2); PyTorch versions without the functions take the public way.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

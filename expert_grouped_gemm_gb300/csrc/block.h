@@ -27,7 +27,9 @@ cudaError_t launch_gate_bwd(const moe_gate_dims& d, const void* logits, const in
                             void* dlogits, int sms, cudaStream_t st, int* launches);
 
 // ---------------------------------------------------------------- linear.cu
-constexpr size_t kLinearHeader = 4096;  // status word and counters, zero between calls
+constexpr size_t kLinearHeader = 4096;   // status word; counters, zero between calls
+constexpr size_t kLinearCounters = 64;   // where they begin
+constexpr int kLinearMaxCounters = (int)(kLinearHeader - kLinearCounters) / 4;
 size_t linear_workspace_bytes(const moe_linear_dims& d);
 cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x, const void* w, const void* bias,
                               const void* residual, void* y, void* pre, int sms, cudaStream_t st, int* launches);

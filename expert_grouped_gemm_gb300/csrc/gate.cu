@@ -10,7 +10,9 @@
 // Without a bias the scores are ordered as the logits are, so the logits themselves are compared
 // and only the chosen experts' scores are computed; a group's sum of two scores and a bias need
 // every score. The kernels are bound by latency: the logits are read once (T = 8192, E = 256 is
-// 8.4 MB, 1.2 us of HBM time), the rest is a chain of k warp reductions.
+// 8.4 MB, 1.2 us of HBM time), the rest is a chain of k warp reductions and, with many tokens, the
+// issue of its instructions: 9.5 us there with 8 groups and a bias, 2.5 more for the counts; 8 tokens
+// of 128 experts 2.5 us; backward of 4097 x 160 3.0 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -28,7 +28,8 @@ struct SimtGemm {
 // fp32 operands need fp32 products (tf32 keeps 10 bits of a factor), so these run on the CUDA
 // cores: a 64 x 64 tile per block of 128 threads, 8 x 4 outputs a thread (three 16-byte shared
 // loads for 32 FMAs), k in slabs of 16, the next slab's global loads in registers while this one is
-// multiplied. Bound by FMA issue. Where the tiles alone leave SMs idle, a cluster of S blocks
+// multiplied. Bound by FMA issue (2000 x 2000 x 2000 364 us, 44 of 80 TFLOP/s: half of the
+// instructions are shared loads, packs and copies). Where the tiles alone leave SMs idle, a cluster of S blocks
 // shares a tile, each with a part of K, and adds the parts in rank order.
 constexpr int kSB = 64, kSK = 16, kSThreads = 128;
 
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtGemm g, i
 
 // ---------------------------------------------------------------- dz and the bias gradient
 // dz = dy act'(pre), row stride ldz (stored when dz is given), and the column sums of dz (when
-// part is given). Bound by HBM: dy and pre are read once, dz written once. A block of 64 x 4
+// part is given). Bound by HBM: dy and pre are read once, dz written once (8192 x 4096 bf16 38 us,
+// 5.3 TB/s). A block of 64 x 4
 // threads owns 64 vectors of VEC columns and a chunk of rows, four rows of it at a time, with
 // the loads of four steps in flight; it adds its columns in registers, then over its four
 // row lanes in order.
@@ -215,12 +217,17 @@ struct alignas(sizeof(T) * VEC) Vec {
   T v[VEC];
 };
 
+//
+// The last block of a group of `wide` column blocks to finish (a counter in the workspace's header,
+// left at zero) adds the chunks' sums into the bias gradient: a few lanes a column, each in chunk
+// order, then the lanes, so the result does not depend on which block that was. With db null the
+// sums stay in part.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T* dz, float* part, int M, int N,
-                                                   int64_t ldz, int act, int per) {
+__global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T* dz, float* part, unsigned* done,
+                                                   T* db, int M, int N, int64_t ldz, int act, int per, int wide) {
   using V = Vec<T, VEC>;
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float red[kDzRows][kDzCols * VEC];
+  __shared__ __align__(16) float red[kDzRows][kDzCols * VEC];
   const int cx = threadIdx.x % kDzCols, ry = threadIdx.x / kDzCols;
   const int n = (blockIdx.x * kDzCols + cx) * VEC;
   const int m1 = min(M, ((int)blockIdx.y + 1) * per);
@@ -272,6 +279,54 @@ __global__ void __launch_bounds__(256) k_linear_dz(const T* dy, const T* pre, T*
 #pragma unroll
     for (int r = 1; r < kDzRows; ++r) s += red[r][c];
     part[(int64_t)blockIdx.y * N + col] = s;
+  }
+  if (!db) return;
+  __shared__ bool last;
+  const int first = blockIdx.x / wide * wide, blocks = min(wide, (int)gridDim.x - first);
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned* count = done + blockIdx.x / wide;
+    last = atomicAdd(count, 1u) == gridDim.y * blocks - 1;
+    if (last) *count = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  constexpr int W = VEC >= 4 ? 4 : 1;               // columns a thread adds, in one load
+  constexpr int TC = kDzCols * VEC / W;             // threads across a block's columns
+  constexpr int LANES = 256 / TC;
+  using F = Vec<float, W>;
+  F* lanes = reinterpret_cast<F*>(&red[0][0]);      // [LANES][TC]
+  const int chunks = (int)gridDim.y, tc = threadIdx.x % TC, lr = threadIdx.x / TC;
+  for (int blk = first; blk < first + blocks; ++blk) {
+    const int col = blk * kDzCols * VEC + tc * W;
+    F s = {};
+    if (col < N) {
+#pragma unroll 16
+      for (int c = lr; c < chunks; c += LANES) {
+        F v;
+        if constexpr (W == 4) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)c * N + col));
+          v = {u.x, u.y, u.z, u.w};
+        } else {
+          v = {__ldcg(part + (int64_t)c * N + col)};
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) s.v[i] += v.v[i];
+      }
+    }
+    __syncthreads();
+    lanes[lr * TC + tc] = s;
+    __syncthreads();
+    if (lr == 0 && col < N) {
+#pragma unroll
+      for (int r = 1; r < LANES; ++r)
+#pragma unroll
+        for (int i = 0; i < W; ++i) s.v[i] += lanes[r * TC + tc].v[i];
+#pragma unroll
+      for (int i = 0; i < W; ++i) db[col + i] = io<T>::cvt(s.v[i]);
+    }
   }
 }
 
@@ -429,30 +484,32 @@ struct Packed {
 };
 
 template <typename T>
-cudaError_t run_dz(const moe_linear_dims& d, const void* dy, const void* pre, void* dz, int64_t ldz, float* part,
-                   cudaStream_t st, int* launches) {
+cudaError_t run_dz(const moe_linear_dims& d, char* ws, float* part, const void* dy, const void* pre, void* dz,
+                   int64_t ldz, void* db, cudaStream_t st, int* launches) {
   constexpr int V = 16 / sizeof(T);
   const int M = (int)d.M, N = (int)d.N;
   const int vec = N % V ? 1 : V;
   const int cb = (N + kDzCols * vec - 1) / (kDzCols * vec);
   const int want = dz_chunks(M, N, vec), per = (M + want - 1) / want, chunks = (M + per - 1) / per;
+  unsigned* done = reinterpret_cast<unsigned*>(ws + kLinearCounters);
+  const int wide = (cb + kLinearMaxCounters - 1) / kLinearMaxCounters;
+  if (!db) part = nullptr;
+  // Few chunks are added by the last block (a launch and 3 us saved at M = 300); many would keep it
+  // for longer than a kernel over all columns takes (152 chunks of 4096 columns: 51 us with dz, 43
+  // in two kernels).
+  void* later = chunks > 32 ? db : nullptr;
+  if (later) db = nullptr;
   *launches += 1;
   if (vec == V)
-    MOE_LAUNCH((k_linear_dz<T, V>), dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)pre, (T*)dz, part, M, N, ldz,
-               d.act, per);
+    MOE_LAUNCH((k_linear_dz<T, V>), dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)pre, (T*)dz, part, done,
+               (T*)db, M, N, ldz, d.act, per, wide);
   else
-    MOE_LAUNCH((k_linear_dz<T, 1>), dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)pre, (T*)dz, part, M, N, ldz,
-               d.act, per);
-  return cudaSuccess;
-}
-
-template <typename T>
-cudaError_t run_dbias(const moe_linear_dims& d, const float* part, void* db, cudaStream_t st, int* launches) {
-  constexpr int V = 16 / sizeof(T);
-  const int M = (int)d.M, N = (int)d.N;
-  const int want = dz_chunks(M, N, N % V ? 1 : V), per = (M + want - 1) / want, chunks = (M + per - 1) / per;
-  *launches += 1;
-  MOE_LAUNCH(k_linear_dbias<T>, (N + 31) / 32, 1024, 0, st, part, chunks, N, (T*)db);
+    MOE_LAUNCH((k_linear_dz<T, 1>), dim3(cb, chunks), 256, 0, st, (const T*)dy, (const T*)pre, (T*)dz, part, done,
+               (T*)db, M, N, ldz, d.act, per, wide);
+  if (later) {
+    *launches += 1;
+    MOE_LAUNCH(k_linear_dbias<T>, (N + 31) / 32, 1024, 0, st, (const float*)part, chunks, N, (T*)later);
+  }
   return cudaSuccess;
 }
 
@@ -481,8 +538,7 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
   const void* dz = store ? ws + L.dz : dy;
   cudaError_t e = cudaSuccess;
   if (store || dbias)
-    e = run_dz<__nv_bfloat16>(d, dy, pre, store ? ws + L.dz : nullptr, up8(N), dbias ? part : nullptr, st, launches);
-  if (e == cudaSuccess && dbias) e = run_dbias<__nv_bfloat16>(d, part, dbias, st, launches);
+    e = run_dz<__nv_bfloat16>(d, ws, part, dy, pre, store ? ws + L.dz : nullptr, up8(N), dbias, st, launches);
   if (e == cudaSuccess) {
     Packed pk;
     if (dx) pk.add(&w, ws + L.wp, K, N);
@@ -512,8 +568,7 @@ cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const vo
   const bool store = (dx || dw) && d.act != MOE_ACT_NONE;
   const void* dz = store ? ws + L.dz : dy;
   cudaError_t e = cudaSuccess;
-  if (store || dbias) e = run_dz<float>(d, dy, pre, store ? ws + L.dz : nullptr, N, dbias ? part : nullptr, st, launches);
-  if (e == cudaSuccess && dbias) e = run_dbias<float>(d, part, dbias, st, launches);
+  if (store || dbias) e = run_dz<float>(d, ws, part, dy, pre, store ? ws + L.dz : nullptr, N, dbias, st, launches);
   if (e == cudaSuccess && dx) {
     SimtGemm g = {f(dz), f(w), N, 1, 1, N, M, N, K, nullptr, f(dx_add), (float*)dx, nullptr, MOE_ACT_NONE};
     e = run_f32(g, sms, st, launches);

