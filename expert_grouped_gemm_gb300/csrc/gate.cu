@@ -186,12 +186,41 @@ __device__ __forceinline__ uint32_t warp_sort(uint32_t key, int lane) {
   return key;
 }
 
+constexpr int kCountBlocks = 8;  // largest cluster that counts
+
+// The blocks' histograms added over the cluster that is the grid, each block a share of the experts
+// (a grid of one block has them all).
+__device__ __forceinline__ void cluster_counts(const int* hist, int E, int* count) {
+  if (gridDim.x == 1) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = hist[e];
+    return;
+  }
+  cluster_sync_all();
+  const int blocks = (int)gridDim.x, share = (E + blocks - 1) / blocks;
+  const int end = min(E, ((int)blockIdx.x + 1) * share);
+  for (int e = (int)blockIdx.x * share + (int)threadIdx.x; e < end; e += blockDim.x) {
+    const uint32_t at = smem_u32(hist + e);
+    int v[kCountBlocks], s = 0;
+#pragma unroll
+    for (int r = 0; r < kCountBlocks; ++r) {
+      v[r] = 0;
+      if (r < blocks)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(mapa_shared(at, r)) : "memory");
+    }
+#pragma unroll
+    for (int r = 0; r < kCountBlocks; ++r) s += v[r];
+    count[e] = s;
+  }
+  cluster_sync_all();  // no block leaves while another still reads its histogram
+}
+
 template <int EPL, bool SOFTMAX, typename TL>
 __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const GateArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ uint2 candidates[EPL <= 8 ? 1 : one_block_tokens<EPL>][32];
-  __shared__ int hist[1024];  // one block only: it has every token and writes the counts itself
-  const bool one = gridDim.x == 1 && a.count;
+  __shared__ int hist[1024];  // the grid is one cluster: it has every token and writes the counts itself
+  const bool one = gridDim.x <= kCountBlocks && a.count;
   if (one) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
@@ -372,25 +401,20 @@ __global__ void __launch_bounds__(32 * one_block_tokens<EPL>) k_gate_fwd(const G
       if (one) atomicAdd(&hist[my_e], 1);  // whole numbers: the order does not matter
     }
   }
-  if (one) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.count[e] = hist[e];
-  }
+  if (one) cluster_counts(hist, a.E, a.count);
 }
 
-// How often each expert stands in idx[n]: histograms in shared memory, one a block, added over a
-// cluster of kCountBlocks. (Counting with atomics on global memory as the tokens are routed took
-// as long again as the routing: the counters of all experts share a few L2 lines.)
-constexpr int kCountBlocks = 8;
+// How often each expert stands in idx[n], for grids of more than one cluster. (Counting with atomics
+// on global memory as the tokens are routed took as long again as the routing: the counters of all
+// experts share a few L2 lines.)
 __global__ void __launch_bounds__(1024) __cluster_dims__(kCountBlocks) k_gate_count(const int* idx, int64_t n, int E,
                                                                                     int* count) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ int hist[1024];
-  const int rank = (int)cluster_ctarank();
   hist[threadIdx.x] = 0;
   __syncthreads();
   constexpr int U = 8;
-  for (int64_t i = (int64_t)rank * 1024 + threadIdx.x; i < n; i += (int64_t)kCountBlocks * 1024 * U) {
+  for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)kCountBlocks * 1024 * U) {
     int e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -401,19 +425,7 @@ __global__ void __launch_bounds__(1024) __cluster_dims__(kCountBlocks) k_gate_co
     for (int u = 0; u < U; ++u)
       if (e[u] >= 0) atomicAdd(&hist[e[u]], 1);
   }
-  cluster_sync_all();
-  const int c = rank * (1024 / kCountBlocks) + (int)threadIdx.x;  // this block's share of the experts
-  if (threadIdx.x < 1024 / kCountBlocks && c < E) {
-    int s = 0;
-#pragma unroll
-    for (int r = 0; r < kCountBlocks; ++r) {
-      int v;
-      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(&hist[c]), r)) : "memory");
-      s += v;
-    }
-    count[c] = s;
-  }
-  cluster_sync_all();  // no block leaves while another still reads its histogram
+  cluster_counts(hist, E, count);
 }
 
 template <int EPL, bool SOFTMAX, typename TL, typename TG>
@@ -547,12 +559,38 @@ cudaError_t bwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st
 
 template <int EPL, bool SOFTMAX, typename TL>
 cudaError_t fwd_typed(const moe_gate_dims& d, const GateArgs& a, cudaStream_t st, int* launches) {
-  // a few tokens in one block, which then owns the counts; else eight a block
-  const int warps = d.T <= one_block_tokens<EPL> ? (int)d.T : 8;
-  const int grid = (int)((d.T + warps - 1) / warps);
+  // As many tokens as one cluster of full blocks holds are routed and counted by it; more by blocks
+  // of eight and a second kernel for the counts. (Without counts: eight a block.)
+  constexpr int kTokens = one_block_tokens<EPL>;
+  const bool one = a.count && d.T <= kTokens * kCountBlocks;
+  const int warps = one ? (int)std::min<int64_t>(d.T, kTokens) : 8;
+  unsigned grid = (unsigned)((d.T + warps - 1) / warps);
   *launches += 1;
+  if (one) {
+    while (grid & (grid - 1)) ++grid;  // clusters of 1, 2, 4 or 8 blocks (one may have no token)
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    unsigned n = 0;
+    if (MOE_PDL) {
+      at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (grid > 1) {
+      at[n].id = cudaLaunchAttributeClusterDimension;
+      at[n].val.clusterDim.x = grid;
+      at[n].val.clusterDim.y = 1;
+      at[n++].val.clusterDim.z = 1;
+    }
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)warps * 32);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, k_gate_fwd<EPL, SOFTMAX, TL>, a);
+  }
+  // (a small grid without counts must not take itself for the counting cluster: a.count is null)
   MOE_LAUNCH(k_gate_fwd<EPL, SOFTMAX, TL>, grid, warps * 32, 0, st, a);
-  if (a.count && grid > 1) {
+  if (a.count) {
     *launches += 1;
     MOE_LAUNCH(k_gate_count, kCountBlocks, 1024, 0, st, (const int*)a.idx, (int64_t)a.T * a.k, a.E, a.count);
   }

@@ -790,7 +790,7 @@ cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
 // Estimated time (us) of each variant, from its rounds over the GPU and its k-blocks per round. The
 // constants are a least-squares fit to 114 products (forward, dx and dw for M = 1 .. 8192 and
 // weights 256x256 .. 4096x4096 and 1024x8192, every variant timed on each, caches cold); the
-// variant with the least estimate is 1.8% slower than the best of all on average, 34% at worst.
+// variant with the least estimate is 1.6% slower than the best of all on average, 34% at worst.
 // Measured examples (us), pair / single / split with its best cluster:
 //   M = 16,   K = 4096, N = 4096:   23.4 / 21.9 / 9.4 (16 tokens, 4 CTAs)
 //   M = 512,  K = 512,  N = 512:     7.2 /  6.0 / 4.9 (64 tokens, 4 CTAs)
@@ -805,7 +805,7 @@ struct Choice {
 
 double tile_estimate(const LinearGemm& g, int b, int64_t units, int kb, double c0, double ck, double cr) {
   const int64_t t = (int64_t)((g.M + b - 1) / b) * ((g.N + b - 1) / b), last = t % units;
-  const double rounds = (double)(t / units) + (last == 0 ? 0.0 : t > units && 2 * last <= units ? 0.5 : 1.0);
+  const double rounds = (double)(t / units) + (last == 0 ? 0.0 : b == 256 && t > units && 2 * last <= units ? 0.5 : 1.0);
   return c0 + rounds * (ck * kb + cr);
 }
 

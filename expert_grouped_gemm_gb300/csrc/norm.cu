@@ -409,14 +409,15 @@ __global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) k_norm_fwd_ring(c
 struct BwdArgs {
   const void *dy, *dsum, *x, *w;
   const float *mean, *rstd;
-  void* dx;
+  void *dx, *dweight, *dbias;
   float* part;
-  int rows, H, dbias;
+  int rows, H;
 };
 
 // The groups' column sums are added in order through shared memory ([element][thread], free of bank
-// conflicts) and written as one row of partial sums a block.
-template <int VEC, int VPT, int G, int THREADS>
+// conflicts) and written as one row of partial sums a block; a grid of one block writes the
+// gradients themselves.
+template <typename T, int VEC, int VPT, int G, int THREADS>
 __device__ __forceinline__ void write_part(const BwdArgs& a, float (&aw)[VPT][VEC], float (&ab)[VPT][VEC],
                                            float* smem) {
   constexpr int GROUPS = THREADS / G, COLS = G * VPT * VEC;
@@ -443,7 +444,16 @@ __device__ __forceinline__ void write_part(const BwdArgs& a, float (&aw)[VPT][VE
         }
     }
   }
-  if (grp == 0) {
+  if (grp == 0 && gridDim.x == 1) {
+    Vec<T, VEC>* dw = reinterpret_cast<Vec<T, VEC>*>(a.dweight);
+    Vec<T, VEC>* db = reinterpret_cast<Vec<T, VEC>*>(a.dbias);
+#pragma unroll
+    for (int p = 0; p < VPT; ++p)
+      if (j + p * G < a.H / VEC) {
+        dw[j + p * G] = pack<T, VEC>(aw[p]);
+        if (db) db[j + p * G] = pack<T, VEC>(ab[p]);
+      }
+  } else if (grp == 0) {
     Vec<float, VEC>* pw = reinterpret_cast<Vec<float, VEC>*>(a.part + (int64_t)blockIdx.x * 2 * a.H);
     Vec<float, VEC>* pb = reinterpret_cast<Vec<float, VEC>*>(a.part + ((int64_t)blockIdx.x * 2 + 1) * a.H);
 #pragma unroll
@@ -566,7 +576,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
     st = st + 1 == STAGES ? 0 : st + 1;
   }
   cp_async_wait<0>();
-  write_part<VEC, VPT, G, 512>(a, aw, ab, reinterpret_cast<float*>(ring));
+  write_part<T, VEC, VPT, G, 512>(a, aw, ab, reinterpret_cast<float*>(ring));
 }
 
 // The same for rows without 16-byte alignment, element by element: thread j keeps the columns
@@ -642,7 +652,7 @@ __global__ void __launch_bounds__(odd_threads<G>) k_norm_bwd_odd(const BwdArgs a
       if (j + p * G < H) o[p * G] = io<T>::cvt(fmaf(-xh[p], mq, fmaf(d[p], rs, -ms)) + e[p]);
     }
   }
-  write_part<1, VPT, G, odd_threads<G>>(a, aw, ab, acc_smem);
+  write_part<T, 1, VPT, G, odd_threads<G>>(a, aw, ab, acc_smem);
 }
 
 // ---------------------------------------------------------------- choice of the variant
@@ -735,6 +745,10 @@ cudaError_t fwd(const moe_norm_dims& d, const void* x, const void* res, const vo
   return cudaSuccess;
 }
 
+// Blocks of the backward: as many as fit at once or the rows need; two rows a group and fewer stay in
+// one block, which needs no second kernel.
+int bwd_blocks_needed(int rows, int groups) { return rows <= 2 * groups ? 1 : (int)(((int64_t)rows + groups - 1) / groups); }
+
 template <typename T, int EPT, int G>
 cudaError_t bwd_ring(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
   constexpr int VPT = EPT * (int)sizeof(T) / 16, stage = 3 * VPT * 512 * 16, groups = 512 / G;
@@ -744,7 +758,7 @@ cudaError_t bwd_ring(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
   auto kern = k_norm_bwd_ring<T, VPT, G, stages>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, stages * stage);
   if (e != cudaSuccess) return e;
-  *chunks = resident_blocks(kern, &cache, 512, stages * stage, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  *chunks = resident_blocks(kern, &cache, 512, stages * stage, bwd_blocks_needed(a.rows, groups), sms, kMaxParts);
   MOE_LAUNCH(kern, *chunks, 512, stages * stage, st, a);
   return cudaSuccess;
 }
@@ -755,7 +769,7 @@ cudaError_t bwd_odd(const BwdArgs& a, int sms, cudaStream_t st, int* chunks) {
   constexpr size_t smem = groups > 1 ? sizeof(float) * 2 * G * VPT : 0;
   static std::atomic<int> cache{0};
   auto kern = k_norm_bwd_odd<T, VPT, G>;
-  *chunks = resident_blocks(kern, &cache, threads, smem, ((int64_t)a.rows + groups - 1) / groups, sms, kMaxParts);
+  *chunks = resident_blocks(kern, &cache, threads, smem, bwd_blocks_needed(a.rows, groups), sms, kMaxParts);
   MOE_LAUNCH(kern, *chunks, threads, smem, st, a);
   return cudaSuccess;
 }
@@ -796,11 +810,15 @@ cudaError_t bwd(const moe_norm_dims& d, void* ws, const void* dy, const void* ds
                 int* launches) {
   float* part = static_cast<float*>(ws);
   const int rows = (int)d.T, H = (int)d.H;
-  const BwdArgs a = {dy, dsum, x, w, mean, rstd, dx, part, rows, H, db != nullptr};
+  const BwdArgs a = {dy, dsum, x, w, mean, rstd, dx, dw, db, part, rows, H};
   int chunks;
   cudaError_t e = bwd_regs<T>(a, sms, st, &chunks);
   if (e != cudaSuccess) return e;
   const int cb = (H + 31) / 32;
+  if (chunks == 1) {
+    *launches += 1;
+    return cudaSuccess;
+  }
   if (chunks) {
     *launches += 2;
     MOE_LAUNCH(k_norm_dw_sum<T>, cb, 1024, 0, st, (const float*)part, chunks, H, (T*)dw, (T*)db);

@@ -102,7 +102,9 @@ def test_norm_gradient_is_the_difference_quotient():
 
 # ---------------------------------------------------------------- gate
 GATES = [
-    # T, E, k, groups, kept, take
+    # T, E, k, groups, kept, take (tokens beside what one block and one cluster of blocks count: 32 x 8, 16 x 8, 8 x 8)
+    (32, 128, 4, 1, 1, 1), (33, 128, 4, 1, 1, 1), (256, 64, 4, 1, 1, 1), (257, 64, 4, 1, 1, 1), (128, 256, 8, 8, 4, 2),
+    (129, 256, 8, 8, 4, 2), (64, 1000, 8, 1, 1, 1), (65, 1000, 8, 1, 1, 1),
     (1, 1, 1, 1, 1, 1), (1, 128, 8, 1, 1, 1), (8, 128, 8, 1, 1, 1), (77, 8, 2, 1, 1, 1), (300, 160, 6, 8, 3, 1),
     (200, 256, 8, 8, 4, 2), (33, 33, 33 - 1, 1, 1, 1), (64, 512, 16, 4, 2, 2), (50, 60, 10, 4, 1, 2),
     (19, 1024, 32, 32, 5, 2), (100, 40, 5, 8, 1, 2), (40, 24, 7, 8, 4, 2), (513, 64, 4, 2, 2, 1), (9, 16, 16, 1, 1, 1),
