@@ -19,6 +19,12 @@ cudaError_t launch_route_topk(float* logits, const float* bias, int T, int E, in
 // The caller's routing in place of the top-k kernel's; the chunk masks must be zero.
 cudaError_t launch_route_given(const int* idx, const float* w, int T, int E, int k, int* topk_idx, float* topk_w,
                                uint64_t* masks, int* status, cudaStream_t st);
+// The same, the scan and the index for up to 64 tokens (one chunk) in one launch, which also zeroes the 256-byte status entry.
+cudaError_t launch_route_given_small(const int* idx, const float* w, int T, int E, int k, int* topk_idx, float* topk_w,
+                                     uint64_t* masks, int* status, int* count, int* offset, int* pad_off,
+                                     int* tile_off, int* chunk_base, int* pair_of_row, int* user_offsets, int* order,
+                                     int* tile_off2, int4* tile_rec, int4* ord_rec, int4* tile_rec2,
+                                     int* rowp_of_pair, int* row_of_pair, int* user_rows, cudaStream_t st);
 cudaError_t launch_route_scan(const uint64_t* masks, int C, int E, int* count, int* offset, int* pad_off,
                               int* tile_off, int* chunk_base, int* pair_of_row, int* user_offsets, cudaStream_t st,
                               int* order = nullptr, int* tile_off2 = nullptr, int4* tile_rec = nullptr,

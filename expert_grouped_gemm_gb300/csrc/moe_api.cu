@@ -645,8 +645,10 @@ static int fwd_impl(const moe_dims* dims, void* ws, size_t ws_bytes, void* strea
   const int sms = num_sms_current();
   const int T = (int)L.T, H = (int)L.H, F = (int)L.F, E = (int)L.E, k = (int)L.k, Fs = (int)L.Fs;
 
+  // a given routing of one chunk is placed by one kernel, which clears the status word itself
+  const bool small = routed && L.C == 1;
   // the status word and the routing chunk masks (the next entry) start at zero
-  CK(cudaMemsetAsync(p.status, 0, L.off[2] - L.off[0], st));
+  if (!small) CK(cudaMemsetAsync(p.status, 0, L.off[2] - L.off[0], st));
 
   // router logits = x W_r  (fp32 out; bias added by the top-k kernel)
   const int rks = routed ? 1 : moe::internal_router_ksplit(dims, sms);
@@ -675,16 +677,23 @@ static int fwd_impl(const moe_dims* dims, void* ws, size_t ws_bytes, void* strea
   }
   {
     Span sp(st, FAM_BW);
-    if (routed)
+    if (small)
+      CKL(launch_route_given_small(given_idx, given_w, T, E, k, p.topk_idx, p.topk_w, p.masks, p.status, p.count,
+                                   p.offset, p.pad_off, p.tile_off, p.chunk_base, p.pair_of_row, expert_offsets,
+                                   p.order, p.tile_off2, p.tile_rec, p.ord_rec, p.tile_rec2, p.rowp_of_pair,
+                                   p.row_of_pair, row_of_pair, st));
+    else if (routed)
       CKL(launch_route_given(given_idx, given_w, T, E, k, p.topk_idx, p.topk_w, p.masks, p.status, st));
     else
       CKL(launch_route_topk(p.logits, router_bias, T, E, k, p.topk_idx, p.topk_w, p.masks, st,
                           rks > 1 ? p.part : nullptr, rks, (int64_t)T * E, /*masks_clear=*/true, logits, topk_idx,
                           topk_w));
-    CKL(launch_route_scan(p.masks, (int)L.C, E, p.count, p.offset, p.pad_off, p.tile_off, p.chunk_base, p.pair_of_row,
-                         expert_offsets, st, p.order, p.tile_off2, p.tile_rec, p.ord_rec, p.tile_rec2));
-    CKL(launch_route_index(p.masks, p.chunk_base, p.topk_idx, p.offset, p.pad_off, T, E, k, p.rowp_of_pair,
-                          p.row_of_pair, p.pair_of_row, st, row_of_pair));
+    if (!small) {
+      CKL(launch_route_scan(p.masks, (int)L.C, E, p.count, p.offset, p.pad_off, p.tile_off, p.chunk_base, p.pair_of_row,
+                           expert_offsets, st, p.order, p.tile_off2, p.tile_rec, p.ord_rec, p.tile_rec2));
+      CKL(launch_route_index(p.masks, p.chunk_base, p.topk_idx, p.offset, p.pad_off, T, E, k, p.rowp_of_pair,
+                            p.row_of_pair, p.pair_of_row, st, row_of_pair));
+    }
     if (bf)
       CKL(launch_gather_rows<__nv_bfloat16>(x, p.pair_of_row, p.pad_off + E, L.Rmax, H, k, p.x_perm, p.xnorm, sms, st));
     else

@@ -170,37 +170,30 @@ __global__ void __launch_bounds__(256) k_route_topk(float* logits, const float* 
 }
 
 // ------------------------------------------------------------------ given routing
-// Warp per token (8 per block): the caller's experts and weights into the workspace, and the chunk
-// masks. A token's experts must be k different ones in [0, E). One that is not sets
+// A token's experts and weights from the caller (idx, w) into the workspace, by one warp, and its bit in
+// the chunk masks. A token's experts must be k different ones in [0, E). One that is not sets
 // MOE_ERR_DEVICE_ARG and is replaced by the lowest expert the token does not use, with weight 0, so
 // that every pair still has a row of its own (of equal ones the first slot keeps the expert).
-__global__ void __launch_bounds__(256) k_route_given(const int* idx, const float* w, int T, int E, int k,
-                                                     int* topk_idx, float* topk_w, uint64_t* masks, int* status) {
-  pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ uint32_t s_used[8][32], s_bad[8][32];  // experts taken, slots to replace: one bit each
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + warp;
-  if (t >= T) return;
-  uint32_t* used = s_used[warp];
-  uint32_t* bad = s_bad[warp];
+// used, bad: the warp's, one bit per expert taken and per slot to replace.
+__device__ __forceinline__ void given_token(const int* idx, const float* w, int E, int k, int* topk_idx, float* topk_w,
+                                            uint64_t* cmask, unsigned long long bit, int* status, uint32_t* used,
+                                            uint32_t* bad) {
+  const int lane = threadIdx.x & 31;
   used[lane] = 0;
   bad[lane] = 0;
   __syncwarp();
-  const int64_t p0 = (int64_t)t * k;
-  uint64_t* cmask = masks + (int64_t)(t / kChunk) * E;
-  const unsigned long long bit = 1ull << (t % kChunk);
   bool any_bad = false;
   for (int j0 = 0; j0 < k; j0 += 32) {
     const int j = j0 + lane;
-    const int e = j < k ? idx[p0 + j] : -1;
+    const int e = j < k ? idx[j] : -1;
     const bool in = e >= 0 && e < E;
     const uint32_t same = __match_any_sync(0xffffffffu, e);  // lanes with this expert: the first keeps it
     const bool ok = in && (__ffs(same) - 1) == lane && !((used[e >> 5] >> (e & 31)) & 1u);
     __syncwarp();
     if (ok) {
       atomicOr(&used[e >> 5], 1u << (e & 31));
-      topk_idx[p0 + j] = e;
-      topk_w[p0 + j] = w[p0 + j];
+      topk_idx[j] = e;
+      topk_w[j] = w[j];
       atomicOr(reinterpret_cast<unsigned long long*>(&cmask[e]), bit);
     }
     const uint32_t wrong = __ballot_sync(0xffffffffu, j < k && !ok);
@@ -208,27 +201,41 @@ __global__ void __launch_bounds__(256) k_route_given(const int* idx, const float
     any_bad |= wrong != 0;
     __syncwarp();
   }
-  if (!any_bad || lane != 0) return;
-  set_status(status, MOE_ERR_DEVICE_ARG);
-  int e = 0;
-  for (int j = 0; j < k; ++j) {
-    if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
-    while ((used[e >> 5] >> (e & 31)) & 1u) ++e;  // k <= E: one is free
-    used[e >> 5] |= 1u << (e & 31);
-    topk_idx[p0 + j] = e;
-    topk_w[p0 + j] = 0.0f;
-    atomicOr(reinterpret_cast<unsigned long long*>(&cmask[e]), bit);
+  if (any_bad && lane == 0) {
+    set_status(status, MOE_ERR_DEVICE_ARG);
+    int e = 0;
+    for (int j = 0; j < k; ++j) {
+      if (!((bad[j >> 5] >> (j & 31)) & 1u)) continue;
+      while ((used[e >> 5] >> (e & 31)) & 1u) ++e;  // k <= E: one is free
+      used[e >> 5] |= 1u << (e & 31);
+      topk_idx[j] = e;
+      topk_w[j] = 0.0f;
+      atomicOr(reinterpret_cast<unsigned long long*>(&cmask[e]), bit);
+    }
   }
+  __syncwarp();
+}
+
+// Warp per token, 8 per block. status and masks are zero before.
+__global__ void __launch_bounds__(256) k_route_given(const int* idx, const float* w, int T, int E, int k,
+                                                     int* topk_idx, float* topk_w, uint64_t* masks, int* status) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ uint32_t s_used[8][32], s_bad[8][32];
+  const int warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * 8 + warp;
+  if (t >= T) return;
+  const int64_t p0 = (int64_t)t * k;
+  given_token(idx + p0, w + p0, E, k, topk_idx + p0, topk_w + p0, masks + (int64_t)(t / kChunk) * E,
+              1ull << (t % kChunk), status, s_used[warp], s_bad[warp]);
 }
 
 // ------------------------------------------------------------------ scan
 // One block of 1024 threads: expert e is handled by `parts` threads, each owning
 // a contiguous range of chunks (parts = 1024 / E rounded down to a power of two).
-__global__ void __launch_bounds__(1024) k_route_scan(const uint64_t* masks, int C, int E, int* count, int* offset,
-                                                     int* pad_off, int* tile_off, int* chunk_base, int* pair_of_row,
-                                                     int* user_offsets, int* order, int* tile_off2,
-                                                     int4* tile_rec, int4* ord_rec, int4* tile_rec2) {
-  pdl_wait();  // the previous kernel has completed and its writes are visible
+__device__ __forceinline__ void route_scan_block(const uint64_t* masks, int C, int E, int* count, int* offset,
+                                                 int* pad_off, int* tile_off, int* chunk_base, int* pair_of_row,
+                                                 int* user_offsets, int* order, int* tile_off2, int4* tile_rec,
+                                                 int4* ord_rec, int4* tile_rec2) {
   __shared__ int part_cnt[1024];
   int parts = 1;
   while (parts * 2 * E <= 1024) parts *= 2;
@@ -301,6 +308,15 @@ __global__ void __launch_bounds__(1024) k_route_scan(const uint64_t* masks, int 
   }
 }
 
+__global__ void __launch_bounds__(1024) k_route_scan(const uint64_t* masks, int C, int E, int* count, int* offset,
+                                                     int* pad_off, int* tile_off, int* chunk_base, int* pair_of_row,
+                                                     int* user_offsets, int* order, int* tile_off2,
+                                                     int4* tile_rec, int4* ord_rec, int4* tile_rec2) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  route_scan_block(masks, C, E, count, offset, pad_off, tile_off, chunk_base, pair_of_row, user_offsets, order, tile_off2,
+                   tile_rec, ord_rec, tile_rec2);
+}
+
 // ------------------------------------------------------------------ pair -> row
 // grid = C chunks, block = 256.
 __global__ void __launch_bounds__(256) k_route_index(const uint64_t* masks, const int* chunk_base, const int* topk_idx,
@@ -329,6 +345,50 @@ __global__ void __launch_bounds__(256) k_route_index(const uint64_t* masks, cons
     row_of_pair[p] = r;
     if (urow) urow[p] = r;  // the caller's copy, when asked for
     pair_of_row[prow] = (int)p;
+  }
+}
+
+// ------------------------------------------------------------------ given routing, few tokens
+// Up to one chunk of tokens (64): one block takes the caller's routing, scans it and places the pairs, and
+// clears the status word before: bound by launches, so the memset and three of them become one, and no memset
+// breaks the chain of early launches. The routed forward (H 2048, F 768, E 128, k 8; a graph of calls): 1 token
+// 46.1 -> 39.8 us, 4 tokens 81.5 -> 75.8, 16 tokens 154 -> 144.
+struct RouteSmall {
+  const int* idx;
+  const float* w;
+  int T, E, k;
+  int* topk_idx;
+  float* topk_w;
+  uint64_t* masks;
+  int* status;
+  int *count, *offset, *pad_off, *tile_off, *chunk_base, *pair_of_row, *user_offsets, *order, *tile_off2;
+  int4 *tile_rec, *ord_rec, *tile_rec2;
+  int *rowp_of_pair, *row_of_pair, *user_rows;
+};
+__global__ void __launch_bounds__(1024) k_route_given_small(const RouteSmall a) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ uint64_t s_mask[1024];
+  __shared__ uint32_t s_used[32][32], s_bad[32][32];
+  const int tid = threadIdx.x, warp = tid >> 5, E = a.E, k = a.k;
+  s_mask[tid] = 0;
+  if (tid < 64) a.status[tid] = 0;
+  __syncthreads();
+  for (int t = warp; t < a.T; t += 32)
+    given_token(a.idx + t * k, a.w + t * k, E, k, a.topk_idx + t * k, a.topk_w + t * k, s_mask, 1ull << t, a.status,
+                s_used[warp], s_bad[warp]);
+  __syncthreads();
+  if (tid < E) a.masks[tid] = s_mask[tid];
+  route_scan_block(s_mask, 1, E, a.count, a.offset, a.pad_off, a.tile_off, a.chunk_base, a.pair_of_row, a.user_offsets,
+                   a.order, a.tile_off2, a.tile_rec, a.ord_rec, a.tile_rec2);
+  __syncthreads();
+  for (int p = tid; p < a.T * k; p += 1024) {
+    const int e = a.topk_idx[p];
+    const int prow = a.chunk_base[e] + __popcll(s_mask[e] & ((1ull << (p / k)) - 1ull));
+    const int r = a.offset[e] + (prow - a.pad_off[e]);
+    a.rowp_of_pair[p] = prow;
+    a.row_of_pair[p] = r;
+    if (a.user_rows) a.user_rows[p] = r;
+    a.pair_of_row[prow] = p;
   }
 }
 
@@ -531,6 +591,18 @@ cudaError_t launch_route_topk(float* logits, const float* bias, int T, int E, in
 cudaError_t launch_route_given(const int* idx, const float* w, int T, int E, int k, int* topk_idx, float* topk_w,
                                uint64_t* masks, int* status, cudaStream_t st) {
   MOE_LAUNCH(k_route_given, (T + 7) / 8, 256, 0, st, idx, w, T, E, k, topk_idx, topk_w, masks, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_route_given_small(const int* idx, const float* w, int T, int E, int k, int* topk_idx, float* topk_w,
+                                     uint64_t* masks, int* status, int* count, int* offset, int* pad_off,
+                                     int* tile_off, int* chunk_base, int* pair_of_row, int* user_offsets, int* order,
+                                     int* tile_off2, int4* tile_rec, int4* ord_rec, int4* tile_rec2,
+                                     int* rowp_of_pair, int* row_of_pair, int* user_rows, cudaStream_t st) {
+  const RouteSmall a{idx, w, T, E, k, topk_idx, topk_w, masks, status, count, offset, pad_off, tile_off, chunk_base,
+                     pair_of_row, user_offsets, order, tile_off2, tile_rec, ord_rec, tile_rec2, rowp_of_pair,
+                     row_of_pair, user_rows};
+  MOE_LAUNCH(k_route_given_small, 1, 1024, 0, st, a);
   return cudaGetLastError();
 }
 

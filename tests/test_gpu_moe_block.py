@@ -112,8 +112,9 @@ def test_routed_with_the_routers_choice_is_moe_fwd(dtype):
         assert rel_fro(ref.grads["dw_router"].double().cpu().numpy(), dwr.numpy()) < TOL[dtype]
 
 
-def test_routed_call_order_and_bad_indices():
-    w = custom("order", T=40, H=128, F=128, E=16, k=3)
+@pytest.mark.parametrize("T", [40, 100])
+def test_routed_call_order_and_bad_indices(T):
+    w = custom("order", T=T, H=128, F=128, E=16, k=3)
     inp = make_inputs(w, seed=4)
     idx, tw = routing(w, 5)
     layer, _, _, g, _ = run_routed(w, inp, idx, tw)
