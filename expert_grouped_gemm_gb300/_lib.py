@@ -70,11 +70,12 @@ class LinearDims(ctypes.Structure):
 
 
 _lib = None
+_bind = None
 
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the library once (raises if it is missing)."""
-    global _lib
+    global _lib, _bind
     if _lib is not None:
         return _lib
     p = path or LIB_PATH
@@ -122,8 +123,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  "moe_bwd", "moe_read_status",
                  "moe_workspace_entry", "moe_timing_enable", "moe_timing_read"]:
         getattr(lib, name).restype = ctypes.c_int
-    _lib = lib
+    try:
+        from . import _bind as bind
+    except ImportError as e:
+        raise RuntimeError("_bind.so not found or built for another PyTorch: build it first (python -c "
+                           "'import __graft_entry__ as g; g.build()')") from e
+    bind.init(*(ctypes.cast(getattr(lib, f), vp).value for f in (
+        "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd")))
+    _lib, _bind = lib, bind
     return lib
+
+
+def _fast():
+    """The module that checks the tensors and calls the library in one step (loaded with the library)."""
+    if _bind is None:
+        load()
+    return _bind
 
 
 def _check(rc: int) -> None:
@@ -345,6 +360,11 @@ def alloc_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
 
 def moe_norm_fwd(dims: NormDims, x, residual, weight, bias, y, sum=None, mean=None, rstd=None, stream=None):
     """y = norm(x + residual) * weight + bias; sum receives x + residual, mean and rstd the statistics."""
+    rc = _fast().norm_fwd(dims, stream if stream is None else _stream(stream), x, residual, weight, bias, y, sum, mean,
+                          rstd)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     io, f32 = _io_dtype(dims), torch.float32
     T, H = dims.T, dims.H
     th, h, t = (T, H), (H,), (T,)
@@ -357,6 +377,11 @@ def moe_norm_fwd(dims: NormDims, x, residual, weight, bias, y, sum=None, mean=No
 
 def moe_norm_bwd(dims: NormDims, ws, dy, dsum, x, weight, mean, rstd, dx, dweight, dbias=None, stream=None):
     """Gradients of moe_norm_fwd; x is the tensor that was normalised, dsum what reaches it past the norm."""
+    rc = _fast().norm_bwd(dims, stream if stream is None else _stream(stream), ws, dy, dsum, x, weight, mean, rstd, dx,
+                          dweight, dbias)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     io, f32 = _io_dtype(dims), torch.float32
     T, H = dims.T, dims.H
     th, h, t = (T, H), (H,), (T,)
@@ -375,6 +400,11 @@ def make_gate_dims(T, E, k, score="softmax", renorm=True, scale=1.0, n_group=1, 
 
 def moe_gate_fwd(dims: GateDims, logits, bias, topk_idx, topk_w, expert_count=None, stream=None):
     """Experts and weights of every token from its router logits; bias takes part in the selection only."""
+    rc = _fast().gate_fwd(dims, stream if stream is None else _stream(stream), logits, bias, topk_idx, topk_w,
+                          expert_count)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     tk = (dims.T, dims.k)
     args = (
         _tensor(logits, "logits", _io_dtype(dims), (dims.T, dims.E)),
@@ -386,6 +416,10 @@ def moe_gate_fwd(dims: GateDims, logits, bias, topk_idx, topk_w, expert_count=No
 
 def moe_gate_bwd(dims: GateDims, logits, topk_idx, dtopk_w, dlogits, stream=None):
     """Gradient of the weights of moe_gate_fwd to the logits, the selection held fixed."""
+    rc = _fast().gate_bwd(dims, stream if stream is None else _stream(stream), logits, topk_idx, dtopk_w, dlogits)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     tk, te = (dims.T, dims.k), (dims.T, dims.E)
     grad = torch.bfloat16 if dims.grad_dtype == MOE_BF16 else torch.float32
     args = (
@@ -410,6 +444,10 @@ def alloc_linear_workspace(dims: LinearDims, device="cuda") -> torch.Tensor:
 
 def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stream=None):
     """y = act(x w + bias) + residual; pre receives x w + bias."""
+    rc = _fast().linear_fwd(dims, stream if stream is None else _stream(stream), ws, x, w, bias, residual, y, pre)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     io = _io_dtype(dims)
     M, K, N = dims.M, dims.K, dims.N
     mn = (M, N)
@@ -422,6 +460,11 @@ def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stre
 
 def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=None, dx_add=None, stream=None):
     """Gradients of moe_linear_fwd; pre is needed when the activation is not 'none'. dx_add is added to dx."""
+    rc = _fast().linear_bwd(dims, stream if stream is None else _stream(stream), ws, dy, x, w, pre, dx_add, dx, dw,
+                            dbias)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     io = _io_dtype(dims)
     M, K, N = dims.M, dims.K, dims.N
     mn, mk, kn = (M, N), (M, K), (K, N)

@@ -3,7 +3,8 @@
 Each .cu file under csrc/ is compiled in parallel to an object in _build/,
 then all objects are linked into expert_grouped_gemm_gb300/libmoe_gb300.so
 (CUDA runtime linked statically; the CUDA driver's tensor-map encoder is looked up
-at run time, so no libcuda link is needed).
+at run time, so no libcuda link is needed). csrc/bind.cpp, the Python module that checks
+tensors and calls the library, becomes _bind.so (g++, against PyTorch's headers).
 """
 from __future__ import annotations
 
@@ -12,11 +13,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(PKG, "_bind.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -33,15 +37,31 @@ def _sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [
+    return _sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(PKG, "..", "include", "moe.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _compile_bind() -> None:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(home, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in inc), BIND_SRC,
+           "-o", tmp, "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stderr}")
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -62,7 +82,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(compile_one, _sources()))
+        bind.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
