@@ -545,17 +545,12 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
     if (dw) pk.add(&x, ws + L.xp, M, K);
     e = pk.run(sms, st, launches);
   }
-  if (e == cudaSuccess && dx) {
-    LinearGemm g = {M, K, N, dz, w, up8(N), up8(N), 0, 0, nullptr, dx_add, dx, nullptr, MOE_ACT_NONE, 0, status};
-    *launches += 1;
-    e = launch_linear_tc(g, sms, st);
-  }
-  if (e == cudaSuccess && dw) {
-    LinearGemm g = {K, N, M, x, dz, up8(K), up8(N), 1, 1, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0, status};
-    *launches += 1;
-    e = launch_linear_tc(g, sms, st);
-  }
-  return e;
+  if (e != cudaSuccess || !(dx || dw)) return e;
+  const LinearGemm gx = {M, K, N, dz, w, up8(N), up8(N), 0, 0, nullptr, dx_add, dx, nullptr, MOE_ACT_NONE, 0, status};
+  const LinearGemm gw = {K, N, M, x, dz, up8(K), up8(N), 1, 1, nullptr, nullptr, dw, nullptr, MOE_ACT_NONE, 0, status};
+  if (dx && dw) return launch_linear_tc2(gx, gw, sms, st, launches);
+  *launches += 1;
+  return launch_linear_tc(dx ? gx : gw, sms, st);
 }
 
 const float* f(const void* p) { return static_cast<const float*>(p); }

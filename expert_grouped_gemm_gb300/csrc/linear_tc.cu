@@ -14,8 +14,11 @@
 // returns.
 //
 // Measured: 4096 x 2048 x 8192 85 us (1.6 PFLOP/s; 99 with bias, gelu and the kept z), 8192 x 4096 x
-// 4096 154 us (1.8). A k-block takes 655 cycles where its MMAs take 512: operand reads and TMA writes
-// together want 125 of shared memory's 128 bytes a clock. Start, end and launch gap are 9 us.
+// 4096 152 us (1.8). Over 16 full rounds (9728 x 4096 x 8192) a k-block takes 0.30 us where its MMAs
+// alone take 0.265 (512 cycles), and 0.28 with half of its loads left out: operand reads and TMA writes
+// together want 125 of shared memory's 128 bytes a clock. Orders of the tiles that read 0.3 to 1 GB of
+// DRAM take the same time. That is with zeros; random data meets the power limit and takes 0.33 us, and
+// there fewer reads help. Start, end and launch gap are 9 us.
 //
 // k_linear_split: for products with too few 128-row tiles to fill the GPU (decoding batches, a
 // narrow output). The wide matrix (the weight) takes the MMA's 128 rows and the tokens its
@@ -60,6 +63,47 @@ struct TcArgs {
   LinearGemm g;
   int kblocks, mt, nt;
   int items, whole;  // work items; the first `whole` are tiles, the others halves (BN / 2 columns) of one
+};
+
+// What a launch of k_linear_tc works on: one product or two.
+template <int N>
+struct TcWork {
+  CUtensorMap A[N], B[N], Y[N], P;
+  TcArgs p[N];
+  int rem, extra;  // N = 2: see Walk
+};
+
+// The items of one unit (a CTA or a pair), in order. One product: every units-th item. Two: the one with
+// more k-blocks first; where its last round is not full, the units from rem on take the first `extra`
+// items of the second product meanwhile; the others of it are dealt out to all units. One launch in
+// place of two saves a start, an end and a launch gap (9 us), and one of the two ragged last rounds.
+template <int N>
+struct Walk {
+  const TcWork<N>& w;
+  const int unit, units;
+  int phase = 0, t, step, end;
+  __device__ __forceinline__ Walk(const TcWork<N>& w_, int unit_, int units_) : w(w_), unit(unit_), units(units_) {
+    t = unit;
+    step = units;
+    end = w.p[0].items;
+  }
+  // the next item: its product and its index there
+  __device__ __forceinline__ bool next(int* prod, int* item) {
+    if constexpr (N == 2) {
+      while (t >= end) {
+        if (++phase > 2) return false;
+        t = phase == 1 ? (unit < w.rem ? w.extra : unit - w.rem) : w.extra + unit;
+        step = phase == 1 ? units - w.rem : units;
+        end = phase == 1 ? w.extra : w.p[1].items;
+      }
+    } else if (t >= end) {
+      return false;
+    }
+    *prod = N == 2 && phase > 0 ? 1 : 0;
+    *item = t;
+    t += step;
+    return true;
+  }
 };
 
 // byte offset of 16-byte piece j of row r in a 128-byte-swizzled staging tile
@@ -131,10 +175,9 @@ __device__ __forceinline__ Item item_at(const TcArgs& a, int t) {
 
 // VEC: the rows of y, pre and the residual are multiples of 16 bytes (N % 8 == 0); else they are
 // read and written element by element, still a whole row of the tile per instruction.
-template <int CTAS, int BN, bool VEC>
+template <int CTAS, int BN, bool VEC, int NP>
 __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
-    k_linear_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmP, const TcArgs args) {
+    k_linear_tc(const __grid_constant__ TcWork<NP> work) {
   using C = Cfg<CTAS, BN>;
   constexpr bool PAIR = CTAS == 2;
   extern __shared__ uint8_t smem_raw[];
@@ -146,7 +189,6 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const LinearGemm& g = args.g;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -179,19 +221,25 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
   const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
-  const int total = args.items;
+  Walk<NP> walk(work, unit, units);
+  int prod, t;
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ producer
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    for (int i = 0; i < NP; ++i) {
+      tma_prefetch_desc(&work.A[i]);
+      tma_prefetch_desc(&work.B[i]);
+    }
     int stage = 0;
     uint32_t phase = 0;
     int issued[C::STAGES];
 #pragma unroll
     for (int s = 0; s < C::STAGES; ++s) issued[s] = -1;
     bool ok = true;
-    for (int t = unit; t < total && ok; t += units) {
+    while (ok && walk.next(&prod, &t)) {
+      const TcArgs& args = work.p[prod];
+      const LinearGemm& g = args.g;
+      const CUtensorMap *tmA = &work.A[prod], *tmB = &work.B[prod];
       const Item it = item_at<BN>(args, t);
       const int m0 = it.m * C::TILE_M + (int)rank * 128;
       const int bcols = it.half ? C::BCOLS / 2 : C::BCOLS;
@@ -211,18 +259,18 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           else tma_load_2d(dst, map, fb, c0, c1);
         };
         if (g.a_mn) {
-          load(sa, &tmA, m0, kb * kBK);
-          load(sa + kChunkBytes, &tmA, m0 + 64, kb * kBK);
+          load(sa, tmA, m0, kb * kBK);
+          load(sa + kChunkBytes, tmA, m0 + 64, kb * kBK);
         } else {
-          load(sa, &tmA, kb * kBK, m0);
+          load(sa, tmA, kb * kBK, m0);
         }
         if (g.b_mn) {
 #pragma unroll
           for (int c = 0; c < C::BCOLS / 64; ++c)
-            if (c * 64 < bcols) load(sb + c * kChunkBytes, &tmB, n0 + c * 64, kb * kBK);
+            if (c * 64 < bcols) load(sb + c * kChunkBytes, tmB, n0 + c * 64, kb * kBK);
         } else {  // boxes of BCOLS / 2 rows
-          load(sb, &tmB, kb * kBK, n0);
-          if (!it.half) load(sb + C::B_BYTES / 2, &tmB, kb * kBK, n0 + C::BCOLS / 2);
+          load(sb, tmB, kb * kBK, n0);
+          if (!it.half) load(sb + C::B_BYTES / 2, tmB, kb * kBK, n0 + C::BCOLS / 2);
         }
         if (++stage == C::STAGES) {
           stage = 0;
@@ -236,14 +284,8 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         if (issued[s] >= 0) mbar_wait_timed(&full[s], (uint32_t)issued[s], 200000000ull);
   } else if (warp == 1 && lane == 0 && leader) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc_whole = idesc_bf16(C::TILE_M, BN, g.a_mn, g.b_mn);
-    const uint32_t idesc_half = idesc_bf16(C::TILE_M, BN / 2, g.a_mn, g.b_mn);
-    uint32_t idesc = idesc_whole;
+    uint32_t idesc = 0;
     const uint32_t sa0 = smem_u32(smem);
-    const uint64_t ad0 = g.a_mn ? sdesc_sw128(sa0, kChunkBytes, 1024) : sdesc_sw128(sa0, 16, 1024);
-    const uint64_t bd0 =
-        g.b_mn ? sdesc_sw128(sa0 + C::A_BYTES, kChunkBytes, 1024) : sdesc_sw128(sa0 + C::A_BYTES, 16, 1024);
-    const uint64_t as = g.a_mn ? 2048 >> 4 : 32 >> 4, bs = g.b_mn ? 2048 >> 4 : 32 >> 4;
     auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
       if constexpr (PAIR) tc_mma_bf16_pair(d, a, b, idesc, acc);
       else tc_mma_bf16(d, a, b, idesc, acc);
@@ -251,7 +293,13 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     int stage = 0, acc_i = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = unit; t < total && ok; t += units) {
+    while (ok && walk.next(&prod, &t)) {
+      const TcArgs& args = work.p[prod];
+      const LinearGemm& g = args.g;
+      const uint64_t ad0 = g.a_mn ? sdesc_sw128(sa0, kChunkBytes, 1024) : sdesc_sw128(sa0, 16, 1024);
+      const uint64_t bd0 =
+          g.b_mn ? sdesc_sw128(sa0 + C::A_BYTES, kChunkBytes, 1024) : sdesc_sw128(sa0 + C::A_BYTES, 16, 1024);
+      const uint64_t as = g.a_mn ? 2048 >> 4 : 32 >> 4, bs = g.b_mn ? 2048 >> 4 : 32 >> 4;
       const int acc = acc_i & 1;
       const uint32_t par = (uint32_t)((acc_i >> 1) & 1);
       const bool free_acc = PAIR ? mbar_wait_bounded_cluster(&tempty[acc], par ^ 1u, abort_flag)
@@ -259,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       if (!free_acc) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * BN);
-      idesc = t >= args.whole ? idesc_half : idesc_whole;
+      idesc = idesc_bf16(C::TILE_M, t >= args.whole ? BN / 2 : BN, g.a_mn, g.b_mn);
       for (int kb = 0; kb < args.kblocks; ++kb) {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag)) {
           ok = false;
@@ -292,11 +340,13 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     const int q = warp & 3;    // the tensor-memory lane quarter this warp may read
     const int ew = warp - 2;
     const uint32_t tile = smem_u32(smem + C::EPI_OFF + ew * 2 * kStage);
-    const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
-    const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
     int acc_i = 0;
     int sc = 0;  // chunks stored so far
-    for (int t = unit; t < total; t += units) {
+    while (walk.next(&prod, &t)) {
+      const TcArgs& args = work.p[prod];
+      const LinearGemm& g = args.g;
+      const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
+      const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
       const Item it = item_at<BN>(args, t);
       const int cw = BN / 64 / (it.half ? 4 : 2);  // 64-column chunks of this warp
       const int c0 = (ew / 4) * cw;
@@ -412,8 +462,8 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (!g.out_f32) tma_store_2d(&tmY, ty, n0, (int)row0);
-          if (g.pre) tma_store_2d(&tmP, tile, n0, (int)row0);
+          if (!g.out_f32) tma_store_2d(&work.Y[prod], ty, n0, (int)row0);
+          if (g.pre) tma_store_2d(&work.P, tile, n0, (int)row0);
           bulk_commit();
         }
         if (c + 1 < c0 + cw) ready(c + 1);
@@ -435,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();  // no CTA of the pair leaves while the other still uses it
   tc_fence_after();
-  if (threadIdx.x == 0 && *abort_flag) set_status(g.status, MOE_ERR_TIMEOUT);
+  if (threadIdx.x == 0 && *abort_flag) set_status(work.p[0].g.status, MOE_ERR_TIMEOUT);
   if (warp == 2) {
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     else tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -724,32 +774,70 @@ bool make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CTAS, int BN, bool VEC>
-cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
+// product g as number i of w: its maps and its tiles
+template <int CTAS, int BN, bool VEC, int N>
+bool fill(TcWork<N>* w, int i, const LinearGemm& g) {
   using C = Cfg<CTAS, BN>;
-  static_assert(C::SMEM <= 232448, "shared memory budget");
-  static_assert(CTAS == 1 || BN == 256, "the epilogue's warps need four chunks to share a half tile");
-  auto kern = k_linear_tc<CTAS, BN, VEC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  CUtensorMap mA, mB, mY, mP;
-  bool ok = g.a_mn ? make_map(&mA, g.A, g.K, g.M, g.lda, kBK) : make_map(&mA, g.A, g.M, g.K, g.lda, 128);
-  ok = ok && (g.b_mn ? make_map(&mB, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mB, g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
-  mY = mP = mA;  // where unused
-  if (VEC && !g.out_f32) ok = ok && make_map(&mY, g.y, g.M, g.N, g.N, 32);
-  if (VEC && g.pre) ok = ok && make_map(&mP, g.pre, g.M, g.N, g.N, 32);
-  if (!ok) return cudaErrorInvalidValue;
-  TcArgs a;
+  bool ok = g.a_mn ? make_map(&w->A[i], g.A, g.K, g.M, g.lda, kBK) : make_map(&w->A[i], g.A, g.M, g.K, g.lda, 128);
+  ok = ok && (g.b_mn ? make_map(&w->B[i], g.B, g.K, g.N, g.ldb, kBK)
+                     : make_map(&w->B[i], g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
+  w->Y[i] = w->A[i];  // where unused
+  if (i == 0) w->P = w->A[i];
+  if (VEC && !g.out_f32) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.N, 32);
+  if (VEC && g.pre) ok = ok && make_map(&w->P, g.pre, g.M, g.N, g.N, 32);
+  TcArgs& a = w->p[i];
   a.g = g;
   a.kblocks = (g.K + kBK - 1) / kBK;
   a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
   a.nt = (g.N + BN - 1) / BN;
-  const int64_t total = (int64_t)a.mt * a.nt, units = sms / CTAS, last = total % units;
-  if (total >= (1ll << 30)) return cudaErrorInvalidValue;
-  a.whole = (int)(CTAS == 2 && 2 * last <= units ? total - last : total);
-  a.items = (int)(total + (total - a.whole));
-  LaunchCfg l(dim3((unsigned)(CTAS * std::min<int64_t>(a.items, units))), C::THREADS, C::SMEM, st, CTAS);
-  return cudaLaunchKernelEx(&l.cfg, kern, mA, mB, mY, mP, a);
+  const int64_t total = (int64_t)a.mt * a.nt;
+  if (!ok || total >= (1ll << 30)) return false;
+  a.items = a.whole = (int)total;
+  return true;
+}
+
+// the tiles of a last round of `round` tiles over `units` as halves, where that leaves none waiting
+void halve(TcArgs* a, int64_t round, int64_t units) {
+  const int64_t last = round % units;
+  if (2 * last > units) return;
+  a->whole -= (int)last;
+  a->items += (int)last;
+}
+
+template <int CTAS, int BN, bool VEC, int N>
+cudaError_t launch_work(const TcWork<N>& w, int64_t units, cudaStream_t st) {
+  using C = Cfg<CTAS, BN>;
+  static_assert(C::SMEM <= 232448, "shared memory budget");
+  static_assert(CTAS == 1 || BN == 256, "the epilogue's warps need four chunks to share a half tile");
+  auto kern = k_linear_tc<CTAS, BN, VEC, N>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  LaunchCfg l(dim3((unsigned)(CTAS * units)), C::THREADS, C::SMEM, st, CTAS);
+  return cudaLaunchKernelEx(&l.cfg, kern, w);
+}
+
+template <int CTAS, int BN, bool VEC>
+cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
+  TcWork<1> w;
+  if (!fill<CTAS, BN, VEC>(&w, 0, g)) return cudaErrorInvalidValue;
+  const int64_t units = sms / CTAS;
+  if (CTAS == 2) halve(&w.p[0], w.p[0].items, units);
+  w.rem = w.extra = 0;
+  return launch_work<CTAS, BN, VEC>(w, std::min<int64_t>(w.p[0].items, units), st);
+}
+
+// Two products in one launch of CTA pairs, the longer k axis first (Walk).
+cudaError_t launch_two(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st) {
+  const LinearGemm &l = g0.K >= g1.K ? g0 : g1, &s = g0.K >= g1.K ? g1 : g0;
+  TcWork<2> w;
+  if (!fill<2, 256, true>(&w, 0, l) || !fill<2, 256, true>(&w, 1, s)) return cudaErrorInvalidValue;
+  const int64_t units = sms / 2;
+  w.rem = (int)(w.p[0].items % units);
+  // a unit without a tile of the last round has time for `fit` tiles of the second product
+  const int64_t fit = (2 * (int64_t)w.p[0].kblocks + w.p[1].kblocks) / (2 * (int64_t)w.p[1].kblocks);
+  w.extra = w.rem ? (int)std::min<int64_t>((units - w.rem) * fit, w.p[1].items) : 0;
+  halve(&w.p[1], w.p[1].items - w.extra, units);
+  return launch_work<2, 256, true>(w, units, st);
 }
 
 template <int NB, int S, bool VEC>
@@ -844,6 +932,28 @@ cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
   if (c.nb == 64) return launch_split_nb<64>(g, c.S, st);
   if (c.S == 2) return vec ? launch_tile<2, 256, true>(g, sms, st) : launch_tile<2, 256, false>(g, sms, st);
   return vec ? launch_tile<1, 128, true>(g, sms, st) : launch_tile<1, 128, false>(g, sms, st);
+}
+
+cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches) {
+  const Choice c0 = choose(g0, (g0.K + kBK - 1) / kBK, sms), c1 = choose(g1, (g1.K + kBK - 1) / kBK, sms);
+  const auto pair = [](const Choice& c) { return c.nb == 0 && c.S == 2; };
+  // k-blocks a unit walks through in both products. Together, in us (dx and dw, separate / in one launch):
+  //   44: 2080 x 1096 x 2312 37.4 / 32.4;  54: 2048 x 2048 x 2048 32.9 / 31.1;
+  //   88: 1500 x 2880 x 2880 43.2 / 42.3;  108: 1024 x 4096 x 4096 55.9 / 50.6, 4096 x 2048 x 2048 53.4 / 53.5;
+  //   216: 8192 x 1024 x 4096 91.8 / 101, 8192 x 2048 x 2048 92.9 / 90.2;  862: 8192 x 4096 x 4096 328 / 341.
+  // After the first product's ragged round the units no longer walk k in step, and what one reads is less
+  // often in L2 for the others: longer walks lose more by that than a launch costs.
+  const auto kblocks = [](const LinearGemm& g) {
+    return (double)((g.M + 255) / 256) * ((g.N + 255) / 256) * ((g.K + kBK - 1) / kBK);
+  };
+  const double walk = (kblocks(g0) + kblocks(g1)) / (sms / 2);
+  if (pair(c0) && pair(c1) && g0.N % 8 == 0 && g1.N % 8 == 0 && walk <= 128.0) {
+    *launches += 1;
+    return launch_two(g0, g1, sms, st);
+  }
+  *launches += 2;
+  const cudaError_t e = launch_linear_tc(g0, sms, st);
+  return e != cudaSuccess ? e : launch_linear_tc(g1, sms, st);
 }
 
 }  // namespace moe

@@ -23,5 +23,7 @@ struct LinearGemm {
 };
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st);
+// Two independent products (neither reads what the other writes), in one launch where both are large.
+cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches);
 
 }  // namespace moe

@@ -218,6 +218,30 @@ def test_linear_many_tiles(M, K, N, act, bias, residual):
     C.check_linear_bwd(c, pre, C.run_linear_bwd(c, pre, db=bias))
 
 
+@pytest.mark.parametrize("M,K,N,one", [(2080, 1096, 2312, True), (2048, 2048, 2048, True), (1024, 4096, 4096, True),
+                                       (3000, 1800, 1032, False), (1288, 3400, 1600, True), (4096, 2048, 4096, False),
+                                       (4096, 2048, 2048, True)])
+def test_linear_both_products_in_one_launch(M, K, N, one):
+    """dx and dw of middling products share a launch, the longer sum first whichever it is: the bits of two calls."""
+    c = C.linear_case(M, K, N, "bf16", seed=5)
+    add = C.rand(6)(M, K, dtype=torch.bfloat16)
+    d, ws = C.linear_ws(c)
+    new = lambda *shape: torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    dx, dw, dx1, dw1 = new(M, K), new(K, N), new(M, K), new(K, N)
+    n = _lib.moe_kernel_launches()
+    _lib.moe_linear_bwd(d, ws, c["dy"], c["x"], c["w"], None, dx, dw, dx_add=add)
+    assert _lib.moe_kernel_launches() - n == (1 if one else 2)
+    _lib.moe_linear_bwd(d, ws, c["dy"], c["x"], c["w"], None, dx1, dx_add=add)
+    _lib.moe_linear_bwd(d, ws, c["dy"], c["x"], c["w"], None, None, dw1)
+    assert torch.equal(dx, dx1) and torch.equal(dw, dw1)
+    assert _lib.moe_read_status(ws) == _lib.MOE_OK
+    x, w, dy, r = (t.double() for t in (c["x"], c["w"], c["dy"], add))
+    for got, want, mag, k in ((dx, dy @ w.T + r, dy.abs() @ w.abs().T + r.abs(), N),
+                              (dw, x.T @ dy, x.abs().T @ dy.abs(), M)):
+        tol = C.U["bf16"] * want.abs() + (k + 32) * 2 * C.E32 * mag
+        assert bool(((got.double() - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ["relu", "gelu_tanh"])
 @pytest.mark.parametrize("M,K,N", [(2, 256, 320), (200, 96, 260), (384, 512, 256)])
