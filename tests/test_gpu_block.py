@@ -242,6 +242,17 @@ def test_linear_both_products_in_one_launch(M, K, N, one):
         assert bool(((got.double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("M,K,N", [(300, 768, 1000), (17, 256, 700), (333, 500, 257), (64, 1300, 70), (70, 65, 1300),
+                                   (1, 512, 512), (1000, 64, 40)])
+def test_linear_f32_gradients_of_unlike_products(M, K, N):
+    """dx and dw in one launch, their tiles in different numbers of parts, the last cluster not full."""
+    c = C.linear_case(M, K, N, "f32", "none", False, seed=9)
+    n = _lib.moe_kernel_launches()
+    out = C.run_linear_bwd(c, None, db=False)
+    assert _lib.moe_kernel_launches() - n == 1
+    C.check_linear_bwd(c, None, out)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ["relu", "gelu_tanh"])
 @pytest.mark.parametrize("M,K,N", [(2, 256, 320), (200, 96, 260), (384, 512, 256)])
