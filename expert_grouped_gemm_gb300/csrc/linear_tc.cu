@@ -13,8 +13,8 @@
 // status word, and the CTA lets its own copies and MMAs finish, frees its tensor memory and
 // returns.
 //
-// Measured: 4096 x 2048 x 8192 85 us (1.6 PFLOP/s; 99 with bias, gelu and the kept z), 8192 x 4096 x
-// 4096 152 us (1.8). Over 16 full rounds (9728 x 4096 x 8192) a k-block takes 0.30 us where its MMAs
+// Measured: 4096 x 2048 x 8192 81 us (1.7 PFLOP/s; 91 with bias, gelu and the kept z), 8192 x 4096 x
+// 4096 148 us (1.86). Over 16 full rounds (9728 x 4096 x 8192) a k-block takes 0.30 us where its MMAs
 // alone take 0.265 (512 cycles), and 0.28 with half of its loads left out: operand reads and TMA writes
 // together want 125 of shared memory's 128 bytes a clock. Orders of the tiles that read 0.3 to 1 GB of
 // DRAM take the same time. That is with zeros; random data meets the power limit and takes 0.33 us, and
@@ -68,7 +68,7 @@ struct TcArgs {
 // What a launch of k_linear_tc works on: one product or two.
 template <int N>
 struct TcWork {
-  CUtensorMap A[N], B[N], Y[N], P;
+  CUtensorMap A[N], B[N], Y[N];
   TcArgs p[N];
   int rem, extra;  // N = 2: see Walk
 };
@@ -171,6 +171,20 @@ __device__ __forceinline__ Item item_at(const TcArgs& a, int t) {
   it.m = grp * G + (r - n * rows);
   it.n0 = n * BN + (it.half ? (h & 1) * (BN / 2) : 0);
   return it;
+}
+
+// Sixteen z of a row as bf16: one 32-byte store where `wide`, else a 16-byte store for each half that exists.
+__device__ __forceinline__ void store_z16(__nv_bfloat16* p, const float* z, int left, bool wide) {
+  if (left <= 0) return;
+  const uint4 a = f_to_bf16x8(z), b = f_to_bf16x8(z + 8);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = a;
+    if (left > 8) *reinterpret_cast<uint4*>(p + 8) = b;
+  }
 }
 
 // VEC: the rows of y, pre and the residual are multiples of 16 bytes (N % 8 == 0); else they are
@@ -352,17 +366,19 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       const int c0 = (ew / 4) * cw;
       const int64_t row0 = (int64_t)it.m * C::TILE_M + (int)rank * 128 + q * 32;  // this warp's first row
       const int rows = (int)min((int64_t)32, (int64_t)g.M - row0);              // rows of it that exist
-      // With a second output z takes one staging tile and y the other; else y alternates between
-      // the two. ready(c) waits until the stores that last used chunk c's tile have read it and
-      // sends for its residual: for the first chunk while the products still run.
+      // y alternates between the two staging tiles and leaves by TMA. z goes out of the registers, 32 bytes
+      // a lane: it spares shared memory, which the products need, a write and a read (4096 x 2048 x 8192
+      // with gelu 96.6 -> 91.3 us; y that way too 92.9, since 32 rows an instruction take longer than one
+      // bulk store). Without VEC z takes the first tile and y the second. ready(c) waits until the store
+      // that last used chunk c's tile has read it and sends for its residual: for the first chunk while
+      // the products still run.
+      const bool wide = VEC && g.N % 16 == 0 && (reinterpret_cast<uintptr_t>(g.pre) & 31) == 0;
+      auto tile_of_y = [&] { return tile + (!VEC && g.pre ? kStage : (sc & 1) * kStage); };
       auto ready = [&](int c) {
         const int n0 = it.n0 + c * 64;
         if (rows <= 0 || n0 >= g.N) return;
-        const uint32_t ty = tile + (g.pre ? kStage : (sc & 1) * kStage);
-        if (lane == 0) {
-          if (g.pre) bulk_wait_read_all();
-          else bulk_wait_read_but1();
-        }
+        const uint32_t ty = tile_of_y();
+        if (lane == 0) bulk_wait_read_but1();
         __syncwarp();
         if (!res) return;
         const int cols = min(64, g.N - n0);
@@ -386,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         const int n0 = it.n0 + c * 64;
         if (rows <= 0 || n0 >= g.N) break;   // the same for the whole warp
         const int cols = min(64, g.N - n0);  // with VEC a multiple of 8
-        const uint32_t ty = tile + (g.pre ? kStage : (sc & 1) * kStage);
+        const uint32_t ty = tile_of_y();
         ++sc;
         uint32_t v[2][32];
         tmem_ld32_async(taddr + c * 64, v[0]);
@@ -418,8 +434,14 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           }
         }
         if (g.pre) {
+          if constexpr (VEC) {
+            __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(g.pre) + (row0 + lane) * g.N + n0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z + 8 * j));
+            for (int j = 0; j < 4; ++j) store_z16(p + 16 * j, z + 16 * j, lane < rows ? cols - 16 * j : 0, wide);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z + 8 * j));
+          }
         }
         act_fwd<true, 64>(g.act, z, z);  // 64 independent chains: two warps a scheduler have little else to hide latency
         if (res) {
@@ -463,7 +485,6 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         __syncwarp();
         if (lane == 0) {
           if (!g.out_f32) tma_store_2d(&work.Y[prod], ty, n0, (int)row0);
-          if (g.pre) tma_store_2d(&work.P, tile, n0, (int)row0);
           bulk_commit();
         }
         if (c + 1 < c0 + cw) ready(c + 1);
@@ -782,9 +803,7 @@ bool fill(TcWork<N>* w, int i, const LinearGemm& g) {
   ok = ok && (g.b_mn ? make_map(&w->B[i], g.B, g.K, g.N, g.ldb, kBK)
                      : make_map(&w->B[i], g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
   w->Y[i] = w->A[i];  // where unused
-  if (i == 0) w->P = w->A[i];
   if (VEC && !g.out_f32) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.N, 32);
-  if (VEC && g.pre) ok = ok && make_map(&w->P, g.pre, g.M, g.N, g.N, 32);
   TcArgs& a = w->p[i];
   a.g = g;
   a.kblocks = (g.K + kBK - 1) / kBK;
