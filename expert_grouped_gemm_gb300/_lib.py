@@ -3,8 +3,10 @@
 Argument marshalling only: each function checks that tensors are contiguous,
 on the GPU and of the expected dtype, passes their pointers and the current
 CUDA stream, and raises MoeError on a non-OK status. Every step of the layer
-runs in the library's kernels. There is no fallback: if the library is
-missing or fails to load, every call raises.
+runs in the library's kernels. The norm, gate and linear operators, whose
+calls can be as short as a launch, do the same in one step of _bind
+(csrc/bind.cpp). There is no fallback: if the library is missing or fails to
+load, every call raises.
 """
 from __future__ import annotations
 
