@@ -472,10 +472,13 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
   } else {
     const float s = logistic(lj);
     if (a.renorm) {
-      const float S = warp_sum(s), q = warp_sum(dw * s);
-      dw = S > 0.0f ? (dw - q / S) / S : 0.0f;
+      // ds_j s_j with s_j / S taken first: 1 / S of denormal scores would be infinite
+      const float S = warp_sum(s);
+      const float w = S > 0.0f ? s / S : 0.0f;
+      d = w * (dw - warp_sum(w * dw)) * (1.0f - s);
+    } else {
+      d = dw * s * (1.0f - s);
     }
-    d = dw * s * (1.0f - s);
   }
   // expert e is lane e / R's element e % R; its sum stands at [e % R][lane], free of bank conflicts
   const int at = my_e >= 0 ? (my_e % a.R) * 32 + my_e / a.R : -1;
