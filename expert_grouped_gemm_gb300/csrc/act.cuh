@@ -50,7 +50,7 @@ template <bool FAST, int ACT>
 __device__ __forceinline__ float act_one(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
   if constexpr (ACT == MOE_ACT_GELU) {
-    if constexpr (!FAST) return 0.5f * z * (1.0f + erff(z * kRsqrt2));
+    if constexpr (!FAST) return z * (0.5f * erfcf(-z * kRsqrt2));  // 1 + erf would cancel for negative z
     // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the second term is zero past 100, where inf 0 would be NaN
     float g;
     const float h = 0.5f * z;
@@ -66,7 +66,7 @@ template <bool FAST, int ACT>
 __device__ __forceinline__ float act_grad_one(float z) {
   if constexpr (ACT == MOE_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if constexpr (ACT == MOE_ACT_GELU) {
-    if constexpr (!FAST) return fmaf(z * kRsqrt2Pi, expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * kRsqrt2)));
+    if constexpr (!FAST) return fmaf(z * kRsqrt2Pi, expf(-0.5f * z * z), 0.5f * erfcf(-z * kRsqrt2));
     float g;
     const float tail = normal_tail(z, &g);
     return fmaf(z * kRsqrt2Pi, g, z < 0.0f ? tail : 1.0f - tail);

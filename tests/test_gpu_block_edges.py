@@ -43,3 +43,96 @@ def test_gate_gradient_of_denormal_sigmoid_scores(k):
     dense = np.zeros((T, E))
     np.put_along_axis(dense, i, W / 2.5, 1)
     C.close(dl, want, 4 * e * dense * mag, "dlogits")
+
+
+# ---------------------------------------------------------------- activations
+E24 = 2.0 ** -24
+TINY = 2.0 ** -126  # below it neither type has normal numbers: a factor that small may be flushed to zero
+CT, AT = np.sqrt(2 / np.pi), 0.044715
+EXACT_SIGMOID = lambda v: np.where(v >= 0, 1 / (1 + np.exp(-np.abs(v))), np.exp(-np.abs(v)) / (1 + np.exp(-np.abs(v))))
+
+
+def phi_cap(z):
+    """The normal distribution function, its lower tail to full relative accuracy."""
+    return 0.5 * torch.special.erfc(torch.tensor(-z) / np.sqrt(2.0)).numpy()
+
+
+def act64(name, z):
+    """(act, act', the sum of the magnitudes of the terms act' is added up from)."""
+    if name == "relu":
+        return np.maximum(z, 0.0), (z > 0).astype(float), (z > 0).astype(float)
+    if name == "gelu":
+        p, q = phi_cap(z), z * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+        return z * p, p + q, p + np.abs(q)
+    u, du = (2 * CT * z * (1 + AT * z * z), 2 * CT * (1 + 3 * AT * z * z)) if name == "gelu_tanh" else (z, 1.0)
+    s, t = EXACT_SIGMOID(u), EXACT_SIGMOID(-u)
+    q = z * s * t * du
+    return z * s, s + q, s + np.abs(q)
+
+
+def rel64(name, z, fast):
+    """Relative error of the distribution function or sigmoid that an activation is made of, in units of 2^-24.
+
+    fp32: exp 2 ulp, erfc 4 ulp, an addition, a division and a product; the rounding of the argument counts as often as
+    it grows through the function: z^2 + 1 times for erfc (twice), |u| times for the exponential (6 roundings for the
+    tanh form). bf16: approximate exponential and reciprocal (2^-22 and 2^-23), two roundings of the exponent."""
+    u = np.abs(2 * CT * z * (1 + AT * z * z)) if name == "gelu_tanh" else np.abs(z)
+    if name == "relu":
+        return 0 * z
+    if name == "gelu":
+        return 16 + 2 * z * z if not fast else 4e-6 / E24 + 40 + 2 * z * z
+    n = 6 if name == "gelu_tanh" else 0
+    return 10 + n * u if not fast else 32 + (n + 4) * u
+
+
+def run_act(name, z, dtype, out_f32, M):
+    """act(z) by a product that gives z exactly."""
+    dt, N, K = C.DT[dtype], z.numel(), 8
+    x = torch.zeros(M, K, dtype=dt, device="cuda")
+    w = torch.zeros(K, N, dtype=dt, device="cuda")
+    x[:, 0], w[0] = 1.0, z
+    c = dict(M=M, K=K, N=N, dtype=dtype, act=name, out_f32=out_f32, x=x, w=w, bias=None, res=None)
+    y, pre = C.run_linear_fwd(c, save=True)
+    assert torch.equal(pre, z.expand(M, N)) and torch.equal(y, y[:1].expand(M, N))
+    return y[0]
+
+
+def run_act_grad(name, z, dtype):
+    """act'(z): the bias gradient of one row with dy = 1."""
+    d, ws = C.linear_ws(dict(M=1, K=8, N=z.numel(), dtype=dtype, act=name, out_f32=False))
+    one = lambda *s: torch.ones(*s, dtype=z.dtype, device="cuda")
+    db = torch.full_like(z, float("nan"))
+    _lib.moe_linear_bwd(d, ws, one(1, z.numel()), one(1, 8), one(8, z.numel()), z[None], None, None, db)
+    return db
+
+
+def grid(dtype, lo=-12.0, hi=12.0):
+    return torch.unique(torch.linspace(lo, hi, 4003).to(C.DT[dtype]))[:4000].contiguous().cuda()
+
+
+ACTS = ["relu", "gelu", "gelu_tanh", "silu"]
+
+
+def act_tol(name, z, Y, fast, unit):
+    return (rel64(name, z, fast) * E24 + unit) * np.abs(Y) + TINY * np.abs(z)
+
+
+def check_act_grad(name, dtype):
+    z = grid(dtype)
+    got, zf, fast = run_act_grad(name, z, dtype), C.f64(z), dtype == "bf16"
+    _, G, terms = act64(name, zf)
+    du = 2 * CT * (1 + 3 * AT * zf * zf) if name == "gelu_tanh" else 1.0
+    tol = (rel64(name, zf, fast) + 4) * E24 * terms + C.U[dtype] * np.abs(G) + TINY * (1 + np.abs(zf) * du)
+    if name in ("gelu_tanh", "silu"):  # 1 - s is off by the rounding of an s near 1, times what multiplies it
+        tol = tol + 8 * E24 * np.abs(zf) * du * EXACT_SIGMOID(zf)
+    C.close(got, G, tol, name)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_f32_activation_is_accurate_in_its_tails(act):
+    z = grid("f32")
+    zf = C.f64(z)
+    Y = act64(act, zf)[0]
+    for M in (1, 700):
+        C.close(run_act(act, z, "f32", False, M), Y, act_tol(act, zf, Y, False, E24), act)
+    check_act_grad(act, "f32")
