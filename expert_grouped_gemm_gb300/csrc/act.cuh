@@ -1,9 +1,9 @@
 // act.cuh -- activations of the linear operator and their derivatives.
 //
-// The bf16 operator evaluates them with the hardware's approximate base-2 exponential and
-// reciprocal (errors of a few 1e-7 next to a rounding of 4e-3; one instruction each, where the
-// intrinsics add range handling that tripled the epilogue's instructions); the fp32 one with the
-// full-precision functions, so that its results keep fp32 accuracy.
+// FAST, where the result is rounded to bf16 (2^-9 of it): the hardware's approximate base-2 exponential and
+// reciprocal (2^-22 and 2^-23; one instruction each, where the intrinsics add range handling that tripled
+// the epilogue's instructions). Else, in the fp32 operator and where the bf16 one returns fp32, the
+// full-precision functions.
 #pragma once
 #include "common.cuh"
 

@@ -188,8 +188,9 @@ __device__ __forceinline__ void store_z16(__nv_bfloat16* p, const float* z, int 
 }
 
 // VEC: the rows of y, pre and the residual are multiples of 16 bytes (N % 8 == 0); else they are
-// read and written element by element, still a whole row of the tile per instruction.
-template <int CTAS, int BN, bool VEC, int NP>
+// read and written element by element, still a whole row of the tile per instruction. F32: y is float, and
+// the activation is evaluated in full precision, since no rounding to bf16 covers the fast forms' errors.
+template <int CTAS, int BN, bool VEC, bool F32, int NP>
 __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     k_linear_tc(const __grid_constant__ TcWork<NP> work) {
   using C = Cfg<CTAS, BN>;
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
             for (int j = 0; j < 8; ++j) st_shared_v4(tile + piece(lane, j), f_to_bf16x8(z + 8 * j));
           }
         }
-        act_fwd<true, 64>(g.act, z, z);  // 64 independent chains: two warps a scheduler have little else to hide latency
+        act_fwd<!F32, 64>(g.act, z, z);  // 64 independent chains: two warps a scheduler have little else to hide latency
         if (res) {
           if constexpr (VEC) cp_async_wait<0>();
           __syncwarp();
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
             for (int i = 0; i < 8; ++i) z[8 * j + i] += b[i];
           }
         }
-        if (!g.out_f32) {  // over the residual pieces this lane has just read
+        if constexpr (!F32) {  // over the residual pieces this lane has just read
 #pragma unroll
           for (int j = 0; j < 8; ++j) st_shared_v4(ty + piece(lane, j), f_to_bf16x8(z + 8 * j));
         } else if (lane < rows) {
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         if constexpr (!VEC) {
           __syncwarp();
           const int64_t o = row0 * g.N + n0;
-          if (!g.out_f32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + o, g.N, ty, rows, cols, lane);
+          if constexpr (!F32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + o, g.N, ty, rows, cols, lane);
           if (g.pre) rows_out(reinterpret_cast<__nv_bfloat16*>(g.pre) + o, g.N, tile, rows, cols, lane);
           __syncwarp();
           if (c + 1 < c0 + cw) ready(c + 1);
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (!g.out_f32) tma_store_2d(&work.Y[prod], ty, n0, (int)row0);
+          if constexpr (!F32) tma_store_2d(&work.Y[prod], ty, n0, (int)row0);
           bulk_commit();
         }
         if (c + 1 < c0 + cw) ready(c + 1);
@@ -532,7 +533,8 @@ template <bool VEC>
 __device__ __forceinline__ void emit4(const LinearGemm& g, int64_t t, int n0, float (&z)[4], const float (&res)[4]) {
   const int64_t o = t * g.N + n0;
   float y[4];
-  act_fwd<true, 4>(g.act, z, y);
+  if (g.out_f32) act_fwd<false, 4>(g.act, z, y);  // no rounding to bf16 covers the fast forms' errors
+  else act_fwd<true, 4>(g.act, z, y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] += res[i];
   __nv_bfloat16* pre = reinterpret_cast<__nv_bfloat16*>(g.pre) + o;
@@ -796,14 +798,14 @@ bool make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
 }
 
 // product g as number i of w: its maps and its tiles
-template <int CTAS, int BN, bool VEC, int N>
+template <int CTAS, int BN, bool VEC, bool F32, int N>
 bool fill(TcWork<N>* w, int i, const LinearGemm& g) {
   using C = Cfg<CTAS, BN>;
   bool ok = g.a_mn ? make_map(&w->A[i], g.A, g.K, g.M, g.lda, kBK) : make_map(&w->A[i], g.A, g.M, g.K, g.lda, 128);
   ok = ok && (g.b_mn ? make_map(&w->B[i], g.B, g.K, g.N, g.ldb, kBK)
                      : make_map(&w->B[i], g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
   w->Y[i] = w->A[i];  // where unused
-  if (VEC && !g.out_f32) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.N, 32);
+  if (VEC && !F32) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.N, 32);
   TcArgs& a = w->p[i];
   a.g = g;
   a.kblocks = (g.K + kBK - 1) / kBK;
@@ -823,40 +825,47 @@ void halve(TcArgs* a, int64_t round, int64_t units) {
   a->items += (int)last;
 }
 
-template <int CTAS, int BN, bool VEC, int N>
+template <int CTAS, int BN, bool VEC, bool F32, int N>
 cudaError_t launch_work(const TcWork<N>& w, int64_t units, cudaStream_t st) {
   using C = Cfg<CTAS, BN>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
   static_assert(CTAS == 1 || BN == 256, "the epilogue's warps need four chunks to share a half tile");
-  auto kern = k_linear_tc<CTAS, BN, VEC, N>;
+  auto kern = k_linear_tc<CTAS, BN, VEC, F32, N>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   LaunchCfg l(dim3((unsigned)(CTAS * units)), C::THREADS, C::SMEM, st, CTAS);
   return cudaLaunchKernelEx(&l.cfg, kern, w);
 }
 
-template <int CTAS, int BN, bool VEC>
-cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
+template <int CTAS, int BN, bool VEC, bool F32>
+cudaError_t launch_tile_as(const LinearGemm& g, int sms, cudaStream_t st) {
   TcWork<1> w;
-  if (!fill<CTAS, BN, VEC>(&w, 0, g)) return cudaErrorInvalidValue;
+  if (!fill<CTAS, BN, VEC, F32>(&w, 0, g)) return cudaErrorInvalidValue;
   const int64_t units = sms / CTAS;
   if (CTAS == 2) halve(&w.p[0], w.p[0].items, units);
   w.rem = w.extra = 0;
-  return launch_work<CTAS, BN, VEC>(w, std::min<int64_t>(w.p[0].items, units), st);
+  return launch_work<CTAS, BN, VEC, F32>(w, std::min<int64_t>(w.p[0].items, units), st);
+}
+
+template <int CTAS, int BN>
+cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
+  if (g.N % 8 == 0)
+    return g.out_f32 ? launch_tile_as<CTAS, BN, true, true>(g, sms, st) : launch_tile_as<CTAS, BN, true, false>(g, sms, st);
+  return g.out_f32 ? launch_tile_as<CTAS, BN, false, true>(g, sms, st) : launch_tile_as<CTAS, BN, false, false>(g, sms, st);
 }
 
 // Two products in one launch of CTA pairs, the longer k axis first (Walk).
 cudaError_t launch_two(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st) {
   const LinearGemm &l = g0.K >= g1.K ? g0 : g1, &s = g0.K >= g1.K ? g1 : g0;
   TcWork<2> w;
-  if (!fill<2, 256, true>(&w, 0, l) || !fill<2, 256, true>(&w, 1, s)) return cudaErrorInvalidValue;
+  if (!fill<2, 256, true, false>(&w, 0, l) || !fill<2, 256, true, false>(&w, 1, s)) return cudaErrorInvalidValue;
   const int64_t units = sms / 2;
   w.rem = (int)(w.p[0].items % units);
   // a unit without a tile of the last round has time for `fit` tiles of the second product
   const int64_t fit = (2 * (int64_t)w.p[0].kblocks + w.p[1].kblocks) / (2 * (int64_t)w.p[1].kblocks);
   w.extra = w.rem ? (int)std::min<int64_t>((units - w.rem) * fit, w.p[1].items) : 0;
   halve(&w.p[1], w.p[1].items - w.extra, units);
-  return launch_work<2, 256, true>(w, units, st);
+  return launch_work<2, 256, true, false>(w, units, st);
 }
 
 template <int NB, int S, bool VEC>
@@ -945,12 +954,10 @@ Choice choose(const LinearGemm& g, int kb, int sms) {
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
   const Choice c = choose(g, (g.K + kBK - 1) / kBK, sms);
-  const bool vec = g.N % 8 == 0;
   if (c.nb == 16) return launch_split_nb<16>(g, c.S, st);
   if (c.nb == 32) return launch_split_nb<32>(g, c.S, st);
   if (c.nb == 64) return launch_split_nb<64>(g, c.S, st);
-  if (c.S == 2) return vec ? launch_tile<2, 256, true>(g, sms, st) : launch_tile<2, 256, false>(g, sms, st);
-  return vec ? launch_tile<1, 128, true>(g, sms, st) : launch_tile<1, 128, false>(g, sms, st);
+  return c.S == 2 ? launch_tile<2, 256>(g, sms, st) : launch_tile<1, 128>(g, sms, st);
 }
 
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches) {

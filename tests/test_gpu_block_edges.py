@@ -85,9 +85,9 @@ def rel64(name, z, fast):
     return 10 + n * u if not fast else 32 + (n + 4) * u
 
 
-def run_act(name, z, dtype, out_f32, M):
+def run_act(name, z, dtype, out_f32, M, K=8):
     """act(z) by a product that gives z exactly."""
-    dt, N, K = C.DT[dtype], z.numel(), 8
+    dt, N = C.DT[dtype], z.numel()
     x = torch.zeros(M, K, dtype=dt, device="cuda")
     w = torch.zeros(K, N, dtype=dt, device="cuda")
     x[:, 0], w[0] = 1.0, z
@@ -136,3 +136,14 @@ def test_f32_activation_is_accurate_in_its_tails(act):
     for M in (1, 700):
         C.close(run_act(act, z, "f32", False, M), Y, act_tol(act, zf, Y, False, E24), act)
     check_act_grad(act, "f32")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,K,odd", [(1, 8, 0), (1, 8, 1), (300, 8, 1), (2100, 8, 0), (2100, 8, 1), (4096, 512, 0), (4096, 512, 1)])
+def test_f32_output_of_bf16_products_has_f32_activations(act, M, K, odd):
+    """Split products, tiles and tiles of CTA pairs, rows that are and are not multiples of 16 bytes."""
+    z = grid("bf16")
+    z = z[:len(z) // 8 * 8 - odd].contiguous()
+    zf = C.f64(z)
+    Y = act64(act, zf)[0]
+    C.close(run_act(act, z, "bf16", True, M, K), Y, act_tol(act, zf, Y, False, E24), act)
