@@ -147,3 +147,15 @@ def test_f32_output_of_bf16_products_has_f32_activations(act, M, K, odd):
     zf = C.f64(z)
     Y = act64(act, zf)[0]
     C.close(run_act(act, z, "bf16", True, M, K), Y, act_tol(act, zf, Y, False, E24), act)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,K,odd", [(1, 8, 0), (2100, 8, 1), (4096, 512, 0)])
+def test_bf16_activation_is_within_its_rounding(act, M, K, odd):
+    """One rounding to bf16 (2^-8 of the value) and the fast forms' own small errors, in the tails as well."""
+    z = grid("bf16")
+    z = z[:len(z) // 8 * 8 - odd].contiguous()
+    zf = C.f64(z)
+    Y = act64(act, zf)[0]
+    C.close(run_act(act, z, "bf16", False, M, K), Y, act_tol(act, zf, Y, True, C.U["bf16"] * (1 + 2.0 ** -10)), act)
+    check_act_grad(act, "bf16")
