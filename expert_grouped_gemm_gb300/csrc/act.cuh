@@ -75,7 +75,8 @@ __device__ __forceinline__ float act_grad_one(float z) {
   }
   if constexpr (ACT == MOE_ACT_GELU_TANH) {
     const float s = sigmoid_of<FAST>(z * fmaf(2.0f * kGeluC * kGeluA * z, z, 2.0f * kGeluC));
-    return s + z * (2.0f * s * (1.0f - s)) * kGeluC * (1.0f + 3.0f * kGeluA * z * z);
+    const float c = fminf(fmaxf(z, -100.0f), 100.0f);  // s (1 - s) is zero past it, where z^2 may be infinite
+    return s + c * (2.0f * s * (1.0f - s)) * kGeluC * (1.0f + 3.0f * kGeluA * c * c);
   }
   if constexpr (ACT == MOE_ACT_SILU) {
     const float s = sigmoid_of<FAST>(z);

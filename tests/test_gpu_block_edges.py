@@ -159,3 +159,12 @@ def test_bf16_activation_is_within_its_rounding(act, M, K, odd):
     Y = act64(act, zf)[0]
     C.close(run_act(act, z, "bf16", False, M, K), Y, act_tol(act, zf, Y, True, C.U["bf16"] * (1 + 2.0 ** -10)), act)
     check_act_grad(act, "bf16")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_activation_of_huge_finite_values(act, dtype):
+    """Past the square root of fp32's range the activations are 0 and z, their derivatives 0 and 1."""
+    z = torch.tensor([-3e38, -1e30, -1e20, -1e19, 1e19, 1e20, 1e30, 3e38], device="cuda").to(C.DT[dtype])
+    assert torch.equal(run_act(act, z, dtype, False, 1), z.clamp_min(0))
+    assert torch.equal(run_act_grad(act, z, dtype), (z > 0).to(z.dtype))
