@@ -34,6 +34,32 @@ __device__ __forceinline__ Vec<T, VEC> pack(const float (&f)[VEC]) {
   return a;
 }
 
+// v += s and out = v s, two elements an instruction (packed fp32, each rounded as the single one would be).
+template <int VEC>
+__device__ __forceinline__ void add_all(float (&v)[VEC], float s) {
+  uint64_t ss;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+#pragma unroll
+  for (int i = 0; i < VEC; i += 2) {
+    uint64_t t;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(v[i]), "f"(v[i + 1]));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(ss));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(t));
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void scale_all(const float (&v)[VEC], float s, float (&out)[VEC]) {
+  uint64_t ss;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+#pragma unroll
+  for (int i = 0; i < VEC; i += 2) {
+    uint64_t t;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(v[i]), "f"(v[i + 1]));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(ss));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(out[i]), "=f"(out[i + 1]) : "l"(t));
+  }
+}
+
 // Sums over a group of G threads (a warp, or G / 32 warps that meet at barrier `id`) of one value or
 // two; every thread gets them. `slots` is the group's own, two sets of G / 32 entries used in turn,
 // so one barrier a call is enough; behind it every thread adds the warps' sums in order (a few
@@ -471,6 +497,8 @@ __device__ __forceinline__ void write_part(const BwdArgs& a, float (&aw)[VPT][VE
 // asynchronous copies. A thread copies exactly the vectors it reads, so the ring needs no barrier,
 // the loads run a row or more ahead of the sums, and the values can be read again after the row's
 // sums instead of being held in registers.
+// xh is (x - mean) rstd: the subtraction of near values is exact, where x rstd - mean rstd would carry the
+// rounding of a large mean into every element of the row.
 template <typename T, int VPT, int G, int STAGES>
 __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
   constexpr int VEC = 16 / sizeof(T);
@@ -528,7 +556,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
   };
   stats(t);
   for (; t < a.rows; t += step) {
-    const float rs = nrs, off = -nmu * nrs;  // xh = x rs + off
+    const float rs = nrs, mu = nmu;
     stats(t + step);
     cp_async_wait<STAGES - 1>();
     float s = 0.0f, q = 0.0f;
@@ -539,18 +567,19 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
         read(st, 0, p, d);
         read(st, 1, p, xv);
         unpack<T, VEC>(wv[p], wf);
+        add_all<VEC>(xv, -mu);
+        scale_all<VEC>(xv, rs, xv);  // xh
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const float xh = fmaf(xv[i], rs, off);
-          aw[p][i] = fmaf(d[i], xh, aw[p][i]);
+          aw[p][i] = fmaf(d[i], xv[i], aw[p][i]);
           ab[p][i] += d[i];
           const float g = d[i] * wf[i];
           s += g;
-          q = fmaf(g, xh, q);
+          q = fmaf(g, xv[i], q);
         }
       }
     const float2 r = group_sum2<G>(s, q, slots[grp], &turn, 1 + grp);
-    // dx = rs g - rs (mean g) - xh rs (mean g xh)
+    // dx = rs (g - (x - mean) rs (mean g xh)) - rs (mean g)
     const float ms = a.mean ? rs * r.x * inv_h : 0.0f, mq = rs * r.y * inv_h;
     V* o = dx + (int64_t)t * nv + j;
 #pragma unroll
@@ -560,11 +589,9 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
         read(st, 0, p, d);
         read(st, 1, p, xv);
         unpack<T, VEC>(wv[p], wf);
+        add_all<VEC>(xv, -mu);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float xh = fmaf(xv[i], rs, off);
-          d[i] = fmaf(-xh, mq, fmaf(d[i] * wf[i], rs, -ms));
-        }
+        for (int i = 0; i < VEC; ++i) d[i] = fmaf(fmaf(-xv[i], mq, d[i] * wf[i]), rs, -ms);
         if (ds) {
           read(st, 2, p, xv);
 #pragma unroll
@@ -626,7 +653,7 @@ __global__ void __launch_bounds__(odd_threads<G>) k_norm_bwd_odd(const BwdArgs a
   int t = blockIdx.x * GROUPS + grp;
   fetch(t);
   for (; t < a.rows; t += step) {
-    const float rs = nrs, off = -nmu * nrs;  // xh = x rs + off
+    const float rs = nrs, mu = nmu;
     float d[VPT], xh[VPT], e[VPT];
     float s = 0.0f, q = 0.0f;
 #pragma unroll
@@ -634,7 +661,7 @@ __global__ void __launch_bounds__(odd_threads<G>) k_norm_bwd_odd(const BwdArgs a
       if (p * G >= H) break;
       const bool in = j + p * G < H;
       d[p] = in ? io<T>::to_f(ndy[p]) : 0.0f;
-      xh[p] = in ? fmaf(io<T>::to_f(nx[p]), rs, off) : 0.0f;
+      xh[p] = in ? (io<T>::to_f(nx[p]) - mu) * rs : 0.0f;
       e[p] = in && ds ? io<T>::to_f(nds[p]) : 0.0f;
       aw[p][0] = fmaf(d[p], xh[p], aw[p][0]);
       ab[p][0] += d[p];

@@ -168,3 +168,40 @@ def test_activation_of_huge_finite_values(act, dtype):
     z = torch.tensor([-3e38, -1e30, -1e20, -1e19, 1e19, 1e20, 1e30, 3e38], device="cuda").to(C.DT[dtype])
     assert torch.equal(run_act(act, z, dtype, False, 1), z.clamp_min(0))
     assert torch.equal(run_act_grad(act, z, dtype), (z > 0).to(z.dtype))
+
+
+# ---------------------------------------------------------------- norm
+@pytest.mark.parametrize("T,H", [(4, 512), (5, 1024), (4, 1111), (3, 2048), (4, 4100), (3, 20000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_gradient_at_a_large_mean(T, H, dtype):
+    """Rows whose mean is 1000 times their spread, and rows of one value: x - mean is exact there (the two are within a
+    factor of two), so xh is off by one rounding, however large the mean is."""
+    c = C.norm_case(T, H, dtype, "layer", False, seed=H, shift=1000.0)
+    c["x"][0], c["x"][1] = 1000.0, 3.0
+    mean, rstd = C.norm_stats(c)
+    mean[0], mean[1] = 1000.0, 3.0
+    dx, dw, db = C.run_norm_bwd(c, mean=mean, rstd=rstd)
+    x, w, dy, m, r = C.f64(c["x"]), C.f64(c["w"]), C.f64(c["dy"]), C.f64(mean), C.f64(rstd)
+    DX, DW, DB = B.norm_bwd(dy, None, x, w, m, r, "layer")
+    X = np.abs((x - m[:, None]) * r[:, None])
+    # a column of dweight: xh's rounding and at most T products and sums; bf16 rounds the result
+    u = C.U[dtype]
+    C.close(dw, DW, u * np.abs(DW) + (T + 8) * E24 * (np.abs(dy) * X).sum(0), "dweight")
+    C.close(db, DB, u * np.abs(DB) + (T + 8) * E24 * np.abs(dy).sum(0), "dbias")
+    # a row's two means: sums over 32 elements a thread at most (80 in the longest rows), 5 steps in a warp, 16 warps
+    g, n = np.abs(dy * w), 128 * E24
+    C.close(dx, DX, u * np.abs(DX) + n * r[:, None] * (g + g.mean(1, keepdims=True) + X * (g * X).mean(1, keepdims=True)),
+            "dx")
+
+
+@pytest.mark.parametrize("T,H", [(4, 512), (4, 1111), (40, 2048), (2440, 512), (2433, 4096), (3, 20000)])
+def test_norm_statistics_at_a_large_mean(T, H):
+    """The variance is taken of h - mean, which is exact here: an error of the mean enters it squared, nothing else grows
+    with the mean (a one-pass variance would be off by 2^-24 of the mean's square)."""
+    c = C.norm_case(T, H, "f32", "layer", False, seed=H, shift=1000.0)
+    _, _, mean, rstd = C.run_norm_fwd(c)
+    _, h, M, R = B.norm_fwd(C.f64(c["x"]), None, C.f64(c["w"]), C.f64(c["b"]), "layer", c["eps"])
+    n = 128 * E24
+    d = n * np.abs(h).max(1)
+    C.close(mean, M, d, "mean")
+    C.close(rstd, R, (n + 0.5 * (d * R) ** 2) * R, "rstd")
