@@ -436,11 +436,16 @@ def make_linear_dims(M, K, N, dtype="bf16", act="none", out_f32=False) -> Linear
 
 
 def alloc_linear_workspace(dims: LinearDims, device="cuda") -> torch.Tensor:
-    """A workspace of moe_linear_workspace_size bytes, its first 4096 bytes zero as the library wants them."""
+    """A workspace of moe_linear_workspace_size bytes, its first 4096 bytes zero as the library wants them.
+
+    They are zero on return (it waits for the current stream), so that the first call may run on any stream. In a
+    graph that is being captured the zeroing is a part of the graph instead, ordered as the capture orders it."""
     n = ctypes.c_size_t(0)
     _check(load().moe_linear_workspace_size(ctypes.byref(dims), ctypes.byref(n)))
     ws = torch.empty(n.value, dtype=torch.uint8, device=device)
     ws[:4096].zero_()
+    if ws.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
     return ws
 
 

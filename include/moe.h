@@ -396,7 +396,8 @@ typedef struct moe_linear_dims {
  * moe_linear_workspace_size -- bytes of workspace of moe_linear_fwd and moe_linear_bwd for
  * these dims (256-byte aligned). The caller sets its first 4096 bytes to zero once, when it
  * allocates the workspace; they hold the status word (moe_read_status) and counters that every
- * call leaves at zero. Host-only; validates dims.
+ * call leaves at zero. The first call has to be ordered behind that zeroing, by its stream or by a
+ * synchronisation. Host-only; validates dims.
  */
 MOE_API int moe_linear_workspace_size(const moe_linear_dims* dims, size_t* bytes);
 

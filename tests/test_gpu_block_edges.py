@@ -205,3 +205,23 @@ def test_norm_statistics_at_a_large_mean(T, H):
     d = n * np.abs(h).max(1)
     C.close(mean, M, d, "mean")
     C.close(rstd, R, (n + 0.5 * (d * R) ** 2) * R, "rstd")
+
+
+# ---------------------------------------------------------------- workspaces
+def test_linear_workspace_is_ready_for_any_stream():
+    """The header is zero when the allocation returns, also behind work that the allocating stream still has to do, so
+    that a first call on another stream finds its counters at zero."""
+    d = _lib.make_linear_dims(256, 64, 512, "bf16", "silu")
+    _lib.alloc_linear_workspace(d).fill_(0xFF)  # what the next allocation of this size gets back
+    c = C.linear_case(256, 64, 512, "bf16", "silu", seed=50)
+    pre = C.linear_pre(c)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    ws = _lib.alloc_linear_workspace(d)
+    with torch.cuda.stream(side):
+        head = ws[:4096].clone()
+        out = C.run_linear_bwd(c, pre, stream=side, dws=(d, ws))
+    side.synchronize()
+    assert int(head.sum()) == 0
+    C.check_linear_bwd(c, pre, out)
