@@ -6,7 +6,7 @@ CUDA stream, and raises MoeError on a non-OK status. Every step of the layer
 runs in the library's kernels. The norm, gate and linear operators, whose
 calls can be as short as a launch, do the same in one step of _bind
 (csrc/bind.cpp). There is no fallback: if the library is missing or fails to
-load, every call raises.
+load, every call raises, and if _bind is, those operators' calls do.
 """
 from __future__ import annotations
 
@@ -77,7 +77,7 @@ _bind = None
 
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the library once (raises if it is missing)."""
-    global _lib, _bind
+    global _lib
     if _lib is not None:
         return _lib
     p = path or LIB_PATH
@@ -125,21 +125,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
                  "moe_bwd", "moe_read_status",
                  "moe_workspace_entry", "moe_timing_enable", "moe_timing_read"]:
         getattr(lib, name).restype = ctypes.c_int
-    try:
-        from . import _bind as bind
-    except ImportError as e:
-        raise RuntimeError("_bind.so not found or built for another PyTorch: build it first (python -c "
-                           "'import __graft_entry__ as g; g.build()')") from e
-    bind.init(*(ctypes.cast(getattr(lib, f), vp).value for f in (
-        "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd")))
-    _lib, _bind = lib, bind
+    _lib = lib
     return lib
 
 
 def _fast():
-    """The module that checks the tensors and calls the library in one step (loaded with the library)."""
+    """The module that checks the tensors and calls the library in one step, for the norm, gate and linear operators."""
+    global _bind
     if _bind is None:
-        load()
+        lib = load()
+        try:
+            from . import _bind as bind
+        except ImportError as e:
+            raise RuntimeError("_bind.so not found or built for another PyTorch: build it first (python -c "
+                               "'import __graft_entry__ as g; g.build()')") from e
+        bind.init(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+            "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd")))
+        _bind = bind
     return _bind
 
 
