@@ -139,6 +139,11 @@ def _fast():
         except ImportError as e:
             raise RuntimeError("_bind.so not found or built for another PyTorch: build it first (python -c "
                                "'import __graft_entry__ as g; g.build()')") from e
+        from .build import bind_target
+        built_for = getattr(bind, "built_for", "another PyTorch")
+        if built_for != bind_target():
+            raise RuntimeError(f"_bind.so was built for {built_for}, this is {bind_target()}: build it again "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
         bind.init(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
             "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd")))
         _bind = bind

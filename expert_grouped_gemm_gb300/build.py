@@ -13,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_STAMP = os.path.join(BUILD, "bind.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -45,23 +47,42 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return all(os.path.getmtime(d) <= t for d in _deps()) and _stamp() == bind_target()
+
+
+def bind_target() -> str:
+    """What _bind.so is built against: the module reads PyTorch's own structures."""
+    import torch
+
+    return f"torch {torch.__version__} python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _stamp() -> str | None:
+    try:
+        with open(BIND_STAMP) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _compile_bind() -> None:
     import torch
 
+    target = bind_target()
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(home, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     tmp = BIND + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in inc), BIND_SRC,
-           "-o", tmp, "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DMOE_BUILT_FOR="{target}"',
+           *(f"-I{d}" for d in inc), BIND_SRC, "-o", tmp, "-L" + os.path.join(home, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stderr}")
     os.replace(tmp, BIND)
+    with open(BIND_STAMP, "w") as f:
+        f.write(target)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

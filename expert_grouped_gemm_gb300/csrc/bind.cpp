@@ -252,4 +252,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind() { return PyModule_Create(&module); }
+// built_for: the PyTorch and Python this was compiled against, whose structures it reads
+PyMODINIT_FUNC PyInit__bind() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", MOE_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -33,3 +33,17 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_a_module_of_another_pytorch_is_not_current(monkeypatch):
+    """It reads PyTorch's structures: after a change of PyTorch it counts as stale, and is not called if it loads."""
+    import torch
+
+    from expert_grouped_gemm_gb300 import _lib
+
+    assert build.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0+other")
+    assert not build.up_to_date()
+    monkeypatch.setattr(_lib, "_bind", None)
+    with pytest.raises(RuntimeError, match="0.0.other"):
+        _lib._fast()
