@@ -1,7 +1,7 @@
 """ctypes binding of libmoe_gb300.so: the C ABI of include/moe.h, same names.
 
 Argument marshalling only: each function checks that tensors are contiguous,
-on the GPU and of the expected dtype, passes their pointers and the current
+on the current device and of the expected dtype, passes their pointers and the current
 CUDA stream, and raises MoeError on a non-OK status. Every step of the layer
 runs in the library's kernels. The norm, gate and linear operators, whose
 calls can be as short as a launch, do the same in one step of _bind
@@ -186,6 +186,26 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+_device = _raw_device or torch.cuda.current_device  # asked only once a CUDA tensor is at hand
+
+
+def _here(t, name):
+    """The library launches on the current device: a tensor of another one is refused."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{_device()}")
+
+
+def _ws(ws):
+    """The workspace's pointer. It stands for its call's device: the experts' calls pass up to twenty tensors, and a look
+    at each one's device was 4 us of host time beside 30."""
+    p = _ptr(ws, "ws", torch.uint8)
+    if ws.get_device() != _device():
+        _here(ws, "ws")
+    return p
+
+
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
@@ -209,7 +229,7 @@ def moe_fwd(dims: Dims, ws: torch.Tensor, x, w_router, router_bias, w_gate, w_up
             y, topk_idx=None, topk_w=None, expert_offsets=None, row_of_pair=None, logits=None, stream=None):
     io = _io_dtype(dims)
     rc = load().moe_fwd(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream),
         _ptr(x, "x", io), _ptr(w_router, "w_router", io), _ptr(router_bias, "router_bias", torch.float32, False),
         _ptr(w_gate, "w_gate", io), _ptr(w_up, "w_up", io), _ptr(w_down, "w_down", io),
         _ptr(ws_gate, "ws_gate", io, False), _ptr(ws_up, "ws_up", io, False), _ptr(ws_down, "ws_down", io, False),
@@ -225,7 +245,7 @@ def moe_fwd_decode(dims: Dims, ws: torch.Tensor, x, w_router, router_bias, w_gat
     """Fused inference forward for 1 <= T <= 16 tokens (bf16); keeps nothing for a backward."""
     io = _io_dtype(dims)
     rc = load().moe_fwd_decode(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream),
         _ptr(x, "x", io), _ptr(w_router, "w_router", io), _ptr(router_bias, "router_bias", torch.float32, False),
         _ptr(w_gate, "w_gate", io), _ptr(w_up, "w_up", io), _ptr(w_down, "w_down", io),
         _ptr(ws_gate, "ws_gate", io, False), _ptr(ws_up, "ws_up", io, False), _ptr(ws_down, "ws_down", io, False),
@@ -240,7 +260,7 @@ def moe_selftest_decode_wait(dims: Dims, ws: torch.Tensor, x, w_router, router_b
     by limit_us: the workspace status word becomes MOE_ERR_TIMEOUT."""
     io = _io_dtype(dims)
     rc = load().moe_selftest_decode_wait(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream),
         _ptr(x, "x", io), _ptr(w_router, "w_router", io), _ptr(router_bias, "router_bias", torch.float32, False),
         _ptr(w_gate, "w_gate", io), _ptr(w_up, "w_up", io), _ptr(w_down, "w_down", io),
         _ptr(ws_gate, "ws_gate", io, False), _ptr(ws_up, "ws_up", io, False), _ptr(ws_down, "ws_down", io, False),
@@ -252,7 +272,7 @@ def moe_select_retained(dims: Dims, ws: torch.Tensor, dy, quota=None, retained_o
                         scores=None, stream=None):
     io = _io_dtype(dims)
     rc = load().moe_select_retained(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
         _ptr(quota, "quota", torch.int32, False), _ptr(retained_offsets, "retained_offsets", torch.int32, False),
         _ptr(retained_rows, "retained_rows", torch.int32, False), _ptr(scores, "scores", torch.float32, False))
     _check(rc)
@@ -262,7 +282,7 @@ def moe_bwd(dims: Dims, ws: torch.Tensor, dy, x, use_retained, dx, dw_router=Non
             dw_down=None, dws_gate=None, dws_up=None, dws_down=None, stream=None):
     io = _io_dtype(dims)
     rc = load().moe_bwd(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
         _ptr(x, "x", io), 1 if use_retained else 0, _ptr(dx, "dx", io),
         _ptr(dw_router, "dw_router", io, False), _ptr(dw_gate, "dw_gate", io, False), _ptr(dw_up, "dw_up", io, False),
         _ptr(dw_down, "dw_down", io, False), _ptr(dws_gate, "dws_gate", io, False),
@@ -275,7 +295,7 @@ def moe_fwd_routed(dims: Dims, ws: torch.Tensor, x, topk_idx, topk_w, w_gate, w_
     """moe_fwd with the caller's experts and weights of every token in place of the router."""
     io = _io_dtype(dims)
     rc = load().moe_fwd_routed(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _ptr(x, "x", io),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream), _ptr(x, "x", io),
         _ptr(topk_idx, "topk_idx", torch.int32), _ptr(topk_w, "topk_w", torch.float32),
         _ptr(w_gate, "w_gate", io), _ptr(w_up, "w_up", io), _ptr(w_down, "w_down", io),
         _ptr(ws_gate, "ws_gate", io, False), _ptr(ws_up, "ws_up", io, False), _ptr(ws_down, "ws_down", io, False),
@@ -289,7 +309,7 @@ def moe_bwd_routed(dims: Dims, ws: torch.Tensor, dy, x, use_retained, dx, dtopk_
     """moe_bwd after moe_fwd_routed: dtopk_w receives the gradient of the routing weights."""
     io = _io_dtype(dims)
     rc = load().moe_bwd_routed(
-        ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
+        ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream), _ptr(dy, "dy", io),
         _ptr(x, "x", io), 1 if use_retained else 0, _ptr(dx, "dx", io), _ptr(dtopk_w, "dtopk_w", torch.float32),
         _ptr(dw_gate, "dw_gate", io, False), _ptr(dw_up, "dw_up", io, False), _ptr(dw_down, "dw_down", io, False),
         _ptr(dws_gate, "dws_gate", io, False), _ptr(dws_up, "dws_up", io, False),
@@ -311,7 +331,7 @@ def moe_route_noalloc(dims: Dims, x, w_router, router_bias, topk_idx, topk_w, ex
 
 def moe_plan_quota(dims: Dims, ws: torch.Tensor, rho_num: int, rho_den: int, quota, budget=None, stream=None):
     """Device-side retention quotas from the last forward's per-expert counts."""
-    rc = load().moe_plan_quota(ctypes.byref(dims), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream),
+    rc = load().moe_plan_quota(ctypes.byref(dims), _ws(ws), ws.numel(), _stream(stream),
                                int(rho_num), int(rho_den), _ptr(budget, "budget", torch.int32, False),
                                _ptr(quota, "quota", torch.int32))
     _check(rc)
@@ -344,12 +364,11 @@ def _tensor(t, name, dtype, shape, required=True):
             raise ValueError(f"{name} is required")
         return None
     try:
-        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        if t.is_cuda and t.get_device() == _device() and t.dtype is dtype and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    _here(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -395,7 +414,7 @@ def moe_norm_bwd(dims: NormDims, ws, dy, dsum, x, weight, mean, rstd, dx, dweigh
     T, H = dims.T, dims.H
     th, h, t = (T, H), (H,), (T,)
     _check(load().moe_norm_bwd(
-        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, th),
+        dims, _ws(ws), ws.numel(), _stream(stream), _tensor(dy, "dy", io, th),
         _tensor(dsum, "dsum", io, th, False), _tensor(x, "x", io, th), _tensor(weight, "weight", io, h),
         _tensor(mean, "mean", f32, t, False), _tensor(rstd, "rstd", f32, t), _tensor(dx, "dx", io, th),
         _tensor(dweight, "dweight", io, h), _tensor(dbias, "dbias", io, h, False)))
@@ -466,7 +485,7 @@ def moe_linear_fwd(dims: LinearDims, ws, x, w, bias, residual, y, pre=None, stre
     M, K, N = dims.M, dims.K, dims.N
     mn = (M, N)
     _check(load().moe_linear_fwd(
-        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(x, "x", io, (M, K)),
+        dims, _ws(ws), ws.numel(), _stream(stream), _tensor(x, "x", io, (M, K)),
         _tensor(w, "w", io, (K, N)), _tensor(bias, "bias", io, (N,), False),
         _tensor(residual, "residual", io, mn, False), _tensor(y, "y", torch.float32 if dims.out_f32 else io, mn),
         _tensor(pre, "pre", io, mn, False)))
@@ -483,7 +502,7 @@ def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=
     M, K, N = dims.M, dims.K, dims.N
     mn, mk, kn = (M, N), (M, K), (K, N)
     _check(load().moe_linear_bwd(
-        dims, _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream), _tensor(dy, "dy", io, mn),
+        dims, _ws(ws), ws.numel(), _stream(stream), _tensor(dy, "dy", io, mn),
         _tensor(x, "x", io, mk), _tensor(w, "w", io, kn), _tensor(pre, "pre", io, mn, False),
         _tensor(dx_add, "dx_add", io, mk, False), _tensor(dx, "dx", io, mk, False), _tensor(dw, "dw", io, kn, False),
         _tensor(dbias, "dbias", io, (N,), False)))
@@ -491,7 +510,7 @@ def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=
 
 def moe_read_status(ws: torch.Tensor, stream=None) -> int:
     """Device status word (MOE_OK, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_ARG); syncs the stream and clears it."""
-    return load().moe_read_status(_ptr(ws, "ws", torch.uint8), _stream(stream))
+    return load().moe_read_status(_ws(ws), _stream(stream))
 
 
 def moe_workspace_entries(dims: Dims) -> dict:

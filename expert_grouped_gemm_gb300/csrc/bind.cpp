@@ -1,5 +1,5 @@
 // bind.cpp -- the Python side of the operators around the experts (norm, gate, linear) as a CPython
-// module: one call checks every tensor (device, type, shape, contiguity), takes the current stream and
+// module: one call checks every tensor (on the current device, type, shape, contiguity), takes the current stream and
 // calls the C ABI. A call of a few microseconds on the GPU is bound by what the host does for it: on a Grace
 // core moe_norm_fwd with four tensors took 4.7 us with the checks in Python (0.38 a tensor) and the call
 // through ctypes (0.6), 2.25 here, 1.7 of them the launch.
@@ -14,6 +14,7 @@
 #include <cstring>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -36,6 +37,7 @@ class Call {
   Call(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, void* dims, Py_ssize_t dims_bytes) : args_(args) {
     ok_ = n == want;
     if (!ok_) return;
+    device_ = c10::cuda::current_device();
     Py_buffer b;
     if (PyObject_GetBuffer(args[0], &b, PyBUF_SIMPLE) != 0) {
       PyErr_Clear();
@@ -46,20 +48,20 @@ class Call {
     if (ok_) memcpy(dims, b.buf, (size_t)dims_bytes);
     PyBuffer_Release(&b);
   }
-  // argument i: a contiguous CUDA tensor of type st and shape [d0] or [d0, d1]
+  // argument i: a contiguous tensor of the current device, of type st and shape [d0] or [d0, d1]
   template <typename P = void>
   P* tensor(int i, bool needed, at::ScalarType st, int64_t d0, int64_t d1 = -1) {
     const at::Tensor* t = get(i, needed);
     if (!t) return nullptr;
     const auto s = t->sizes();
-    ok_ = t->is_cuda() && t->scalar_type() == st && t->is_contiguous() &&
+    ok_ = here(*t) && t->scalar_type() == st && t->is_contiguous() &&
           (d1 < 0 ? s.size() == 1 && s[0] == d0 : s.size() == 2 && s[0] == d0 && s[1] == d1);
     return ok_ ? static_cast<P*>(t->data_ptr()) : nullptr;
   }
   void* workspace(int i, size_t* bytes) {
     const at::Tensor* t = get(i, kNeeded);
     if (!t) return nullptr;
-    ok_ = t->is_cuda() && t->scalar_type() == at::kByte && t->is_contiguous();
+    ok_ = here(*t) && t->scalar_type() == at::kByte && t->is_contiguous();
     *bytes = (size_t)t->numel();
     return ok_ ? t->data_ptr() : nullptr;
   }
@@ -69,7 +71,7 @@ class Call {
   PyObject* run(F f) {
     void* st;
     if (args_[1] == Py_None) {
-      st = c10::cuda::getCurrentCUDAStream().stream();
+      st = c10::cuda::getCurrentCUDAStream(device_).stream();
     } else {
       st = PyLong_AsVoidPtr(args_[1]);
       if (PyErr_Occurred()) {
@@ -95,8 +97,11 @@ class Call {
     ok_ = THPVariable_Check(o);
     return ok_ ? &THPVariable_Unpack(o) : nullptr;
   }
+  // the kernels run on the current device
+  bool here(const at::Tensor& t) const { return t.is_cuda() && t.get_device() == device_; }
   PyObject* const* args_;
   bool ok_;
+  c10::DeviceIndex device_ = -1;
 };
 
 at::ScalarType io_type(int32_t dtype) { return dtype == MOE_BF16 ? at::kBFloat16 : at::kFloat; }

@@ -47,3 +47,30 @@ def test_a_module_of_another_pytorch_is_not_current(monkeypatch):
     monkeypatch.setattr(_lib, "_bind", None)
     with pytest.raises(RuntimeError, match="0.0.other"):
         _lib._fast()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Kernels run on the current device, with its stream: a tensor that lies on another one is named, in every call."""
+    import torch
+
+    from expert_grouped_gemm_gb300 import _lib
+
+    class Other(torch.Tensor):  # a host tensor that says it is on the second GPU
+        is_cuda = property(lambda self: True)
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(_lib, "_device", lambda: 0, raising=False)
+    monkeypatch.setattr(_lib, "_stream", lambda s: 0)
+    bf = torch.bfloat16
+    t = lambda *s, dtype=bf: torch.zeros(*s, dtype=dtype).as_subclass(Other)
+    x, w = t(4, 64), t(64, 64)
+    ws = t(1 << 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x is on cuda:1, the current device is cuda:0"):
+        _lib.moe_norm_fwd(_lib.make_norm_dims(4, 64), x, None, w[0], None, x)
+    with pytest.raises(ValueError, match="ws is on cuda:1"):
+        _lib.moe_linear_fwd(_lib.make_linear_dims(4, 64, 64), ws, x, w, None, None, x)
+    with pytest.raises(ValueError, match="ws is on cuda:1"):
+        _lib.moe_fwd_routed(_lib.make_dims(4, 64, 64, 16, 2), ws, x, t(4, 2, dtype=torch.int32),
+                            t(4, 2, dtype=torch.float32), w, w, w, None, None, None, x)
