@@ -23,9 +23,9 @@ WEIGHTS = ["w_o", "b_o", "norm_w", "norm_b", "w_router", "w_gate", "w_up", "w_do
 class MoEBlock:
     def __init__(self, w: Workload, params: dict, device="cuda", norm: str = "rms", eps: float = 1e-5,
                  score: str = "softmax", renorm: bool = True, scale: float = 1.0, n_group: int = 1,
-                 topk_group: int = 1, group_take: int = 1):
+                 topk_group: int = 1, group_take: int = 1, recompute: bool = False):
         """params: tensors named as in WEIGHTS (b_o, norm_b and, without a shared expert, ws_* may be missing)
-        and the optional fp32 balance_bias[E]."""
+        and the optional fp32 balance_bias[E]. recompute: as in MoELayer."""
         self.w = w
         dev = torch.device(device)
         io = torch.bfloat16 if w.dtype == "bf16" else torch.float32
@@ -36,8 +36,9 @@ class MoEBlock:
         self.proj = _lib.make_linear_dims(T, A, H, w.dtype)
         self.norm = _lib.make_norm_dims(T, H, w.dtype, norm, eps)
         self.router = _lib.make_linear_dims(T, H, E, w.dtype, out_f32=True)
+        # dlogits in the io type: the router's products read it as a tensor-core operand
         self.gate = _lib.make_gate_dims(T, E, k, score, renorm, scale, n_group, topk_group, group_take, "f32", w.dtype)
-        self.moe = _lib.make_dims(T, H, F, E, k, Fs, w.dtype, w.frozen)
+        self.moe = _lib.make_dims(T, H, F, E, k, Fs, w.dtype, w.frozen, recompute)
         self.ws_proj = _lib.alloc_linear_workspace(self.proj, dev)
         self.ws_norm = _lib.alloc_norm_workspace(self.norm, dev)
         self.ws_router = _lib.alloc_linear_workspace(self.router, dev)
@@ -74,10 +75,17 @@ class MoEBlock:
                             p["w_down"], p["ws_gate"], p["ws_up"], p["ws_down"], self.y, stream=stream)
         return self.y, self.h
 
-    def backward(self, attn: torch.Tensor, dy: torch.Tensor, dh: torch.Tensor, stream=None):
-        """Gradients of <dy, y> + <dh, h> for the attn of the last forward: (dattn, dresidual, weight gradients)."""
+    def select(self, dy: torch.Tensor, quota: torch.Tensor | None, stream=None) -> None:
+        """The token-expert pairs of the last forward that backward(use_retained=True) on this dy keeps."""
+        _lib.moe_select_retained(self.moe, self.ws_moe, dy, quota, stream=stream)
+
+    def backward(self, attn: torch.Tensor, dy: torch.Tensor, dh: torch.Tensor, stream=None, use_retained: bool = False):
+        """Gradients of <dy, y> + <dh, h> for the attn of the last forward: (dattn, dresidual, weight gradients).
+
+        use_retained (after select): the experts' part over the kept pairs only; the routing weights' gradient is
+        that of every pair."""
         p, g = self.p, self.grads
-        _lib.moe_bwd_routed(self.moe, self.ws_moe, dy, self.n, False, self.dn, self.dtopk_w, g.get("w_gate"),
+        _lib.moe_bwd_routed(self.moe, self.ws_moe, dy, self.n, use_retained, self.dn, self.dtopk_w, g.get("w_gate"),
                             g.get("w_up"), g.get("w_down"), g.get("ws_gate"), g.get("ws_up"), g.get("ws_down"),
                             stream=stream)
         _lib.moe_gate_bwd(self.gate, self.logits, self.topk_idx, self.dtopk_w, self.dlogits, stream=stream)
