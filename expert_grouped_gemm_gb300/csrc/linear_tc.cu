@@ -34,6 +34,7 @@
 
 #include "act.cuh"
 #include "common.cuh"
+#include "linear_choice.h"
 #include "linear_tc.h"
 
 namespace moe {
@@ -902,58 +903,10 @@ cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
   }
 }
 
-// ---------------------------------------------------------------- choice of the variant
-// Estimated time (us) of each variant, from its rounds over the GPU and its k-blocks per round. The
-// constants are a least-squares fit to 114 products (forward, dx and dw for M = 1 .. 8192 and
-// weights 256x256 .. 4096x4096 and 1024x8192, every variant timed on each, caches cold); the
-// variant with the least estimate is 1.6% slower than the best of all on average, 34% at worst.
-// Measured examples (us), pair / single / split with its best cluster:
-//   M = 16,   K = 4096, N = 4096:   23.4 / 21.9 / 9.4 (16 tokens, 4 CTAs)
-//   M = 512,  K = 512,  N = 512:     7.2 /  6.0 / 4.9 (64 tokens, 4 CTAs)
-//   M = 4096, K = 2048, N = 128:    14.9 / 13.5 / 9.3 (64 tokens, 4 CTAs)
-//   M = 2048, K = 4096, N = 4096:   46.3 / 78.3 / 92.7
-// A k-block costs 0.3 us in a tile (its load's latency over the ring) and 0.26 us in a split part;
-// a round of tiles costs its epilogue; a split part costs its share of the tokens, and more where
-// two CTAs share an SM.
-struct Choice {
-  int nb, S;  // nb 0: tiles, of 128 x 128 (S = 1) or 256 x 256 on CTA pairs (S = 2)
-};
-
-double tile_estimate(const LinearGemm& g, int b, int64_t units, int kb, double c0, double ck, double cr) {
-  const int64_t t = (int64_t)((g.M + b - 1) / b) * ((g.N + b - 1) / b), last = t % units;
-  const double rounds = (double)(t / units) + (last == 0 ? 0.0 : b == 256 && t > units && 2 * last <= units ? 0.5 : 1.0);
-  return c0 + rounds * (ck * kb + cr);
-}
-
-Choice choose(const LinearGemm& g, int kb, int sms) {
-  Choice best = {0, 1};
-  double t = tile_estimate(g, 128, sms, kb, 1.56, 0.302, 1.25);
-  const double pair = tile_estimate(g, 256, sms / 2, kb, 2.23, 0.300, 3.05);
-  if (pair < t) {
-    t = pair;
-    best = {0, 2};
-  }
-  // an MN-major token matrix is read in chunks of 64 tokens
-  for (int nb = g.a_mn ? 64 : 16; nb <= 64 && (nb < 2 * g.M || nb == 16 || g.a_mn); nb *= 2) {
-    const int64_t tiles = (int64_t)((g.M + nb - 1) / nb) * ((g.N + 127) / 128);
-    for (int S = 1; S <= 8 && S <= kb; S *= 2) {
-      const double rounds = (double)((tiles * S + 2 * sms - 1) / (2 * sms));
-      const double kbs = (double)((kb + S - 1) / S), shared = tiles * S > sms ? 1.0 : 0.0;
-      const double e = 1.82 + (S > 1 ? 1.87 : 0.0) + rounds * (kbs * (0.26 + 0.048 * nb / 64) + 0.034 * nb / S) +
-                       shared * (1.81 * rounds + 0.073 * S);
-      if (e < t) {
-        t = e;
-        best = {nb, S};
-      }
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
-  const Choice c = choose(g, (g.K + kBK - 1) / kBK, sms);
+  const LinearChoice c = choose_linear(g.M, g.N, g.K, g.a_mn, sms);
   if (c.nb == 16) return launch_split_nb<16>(g, c.S, st);
   if (c.nb == 32) return launch_split_nb<32>(g, c.S, st);
   if (c.nb == 64) return launch_split_nb<64>(g, c.S, st);
@@ -961,8 +914,9 @@ cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
 }
 
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches) {
-  const Choice c0 = choose(g0, (g0.K + kBK - 1) / kBK, sms), c1 = choose(g1, (g1.K + kBK - 1) / kBK, sms);
-  const auto pair = [](const Choice& c) { return c.nb == 0 && c.S == 2; };
+  const LinearChoice c0 = choose_linear(g0.M, g0.N, g0.K, g0.a_mn, sms);
+  const LinearChoice c1 = choose_linear(g1.M, g1.N, g1.K, g1.a_mn, sms);
+  const auto pair = [](const LinearChoice& c) { return c.nb == 0 && c.S == 2; };
   // k-blocks a unit walks through in both products. Together, in us (dx and dw, separate / in one launch):
   //   44: 2080 x 1096 x 2312 37.4 / 32.4;  54: 2048 x 2048 x 2048 32.9 / 31.1;
   //   88: 1500 x 2880 x 2880 43.2 / 42.3;  108: 1024 x 4096 x 4096 55.9 / 50.6, 4096 x 2048 x 2048 53.4 / 53.5;
