@@ -333,7 +333,8 @@ typedef struct moe_gate_dims {
  * unmasked expert is kept last, and group scores sum unmasked experts only. When all k
  * chosen s are zero the weights are zero. A +inf logit is the limit: softmax shares 1 among
  * the +inf logits.
- * Scores are fp32. Inputs: logits[T,E] (dims.dtype), bias[E] float (nullable).
+ * Scores are fp32 (a sigmoid score below 2^-126 counts as zero in the selection).
+ * Inputs: logits[T,E] (dims.dtype), bias[E] float (nullable).
  * Outputs: topk_idx[T,k] int32, topk_w[T,k] float, expert_count[E] int32 (nullable: tokens
  * that chose each expert, what a balance-bias update reads).
  */

@@ -225,3 +225,27 @@ def test_linear_workspace_is_ready_for_any_stream():
     side.synchronize()
     assert int(head.sum()) == 0
     C.check_linear_bwd(c, pre, out)
+
+
+@pytest.mark.parametrize("shift,spread,steps", [(0.0, 4.0, 100), (-30.0, 0.5, 0), (-60.0, 0.1, 0)])
+def test_gate_selects_on_fp32_scores(shift, spread, steps):
+    """Sigmoid scores with a bias order the experts as 64 bits do wherever two choice scores differ by more than fp32's
+    own roundings: exp 2 ulp (2^-22 of e^-l, which moves s by s (1 - s) times that), an addition and a reciprocal of
+    one ulp (2^-24 and 2^-23 of s), and the sum with the bias (2^-24). Scores of e^-30 and e^-60 among them, which a
+    bias of zero leaves as they are."""
+    T, E, k = 100_000, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = shift + spread * torch.randn(T, E, generator=g, device="cuda")
+    bias = torch.randint(-steps, steps + 1, (E,), generator=g, device="cuda").float() * 1e-3
+    idx, _, _ = C.run_gate(logits, bias, k, "sigmoid", True)
+    s = torch.sigmoid(logits.double())
+    c = s + bias.double()
+    err = s * (1 - s) * 2.0 ** -22 + s * (2.0 ** -23 + E24) + c.abs() * E24
+    want = torch.sort(c, dim=1, descending=True, stable=True).indices[:, :k + 1]
+    cw, ew = c.gather(1, want), err.gather(1, want)
+    # equal scores go to the lower expert, which the stable sort keeps
+    gap = cw[:, :-1] - cw[:, 1:]
+    decided = ((gap > ew[:, :-1] + ew[:, 1:]) | (gap == 0)).all(1)
+    assert float(decided.float().mean()) > 0.9
+    wrong = (idx.long() != want[:, :k]).any(1) & decided
+    assert int(wrong.sum()) == 0
