@@ -28,8 +28,10 @@ struct SimtGemm {
 // fp32 operands need fp32 products (tf32 keeps 10 bits of a factor), so these run on the CUDA
 // cores: a 64 x 64 tile per block of 128 threads, 8 x 4 outputs a thread (three 16-byte shared
 // loads for 32 FMAs), k in slabs of 16, the next slab's global loads in registers while this one is
-// multiplied. Bound by FMA issue (2000 x 2000 x 2000 364 us, 44 of 80 TFLOP/s: half of the
-// instructions are shared loads, packs and copies). Where the tiles alone leave SMs idle, S blocks of a
+// multiplied. Bound by FMA issue (2000 x 2000 x 2000 357 us, 45 of 80 TFLOP/s: half of the
+// instructions are shared loads, packs and copies). As six bf16 products of exact three-way splits on the tensor cores
+// they would lose accuracy: those truncate as they accumulate, and products of positive operands over k = 4096 came out
+// 1.4e-5 low, where fp32 sums are within 1e-6. Where the tiles alone leave SMs idle, S blocks of a
 // cluster share a tile, each with a part of K, and add the parts in rank order. A launch does one product
 // or two (dx and dw), each with its own S: a cluster of the larger S holds several tiles of the other.
 // Together they fill the SMs that either leaves idle: 300 x 768 x 1000 with dz 41.8 -> 33.9 us, 17 x 256 x 700
@@ -574,7 +576,10 @@ cudaError_t bwd_bf16(const moe_linear_dims& d, char* ws, const void* dy, const v
   const int M = (int)d.M, K = (int)d.K, N = (int)d.N;
   float* part = reinterpret_cast<float*>(ws + L.part);
   int* status = reinterpret_cast<int*>(ws);
-  // dz is dy itself without an activation, unless the products need it with wider rows
+  // dz is dy itself without an activation, unless the products need it with wider rows. It is rounded to bf16 because
+  // both products read it as a tensor-core operand, which has the type of the other (the error against 64 bits is 0.0023
+  // of the gradients' size for 0.0017 of their own rounding alone; two more products of what the rounding drops
+  // would double the time). The bias gradient sums the unrounded values.
   const bool store = (dx || dw) && (d.act != MOE_ACT_NONE || N % 8);
   const void* dz = store ? ws + L.dz : dy;
   cudaError_t e = cudaSuccess;

@@ -13,20 +13,18 @@
 // status word, and the CTA lets its own copies and MMAs finish, frees its tensor memory and
 // returns.
 //
-// Measured: 4096 x 2048 x 8192 81 us (1.7 PFLOP/s; 91 with bias, gelu and the kept z), 8192 x 4096 x
-// 4096 148 us (1.86). Over 16 full rounds (9728 x 4096 x 8192) a k-block takes 0.30 us where its MMAs
-// alone take 0.265 (512 cycles), and 0.28 with half of its loads left out: operand reads and TMA writes
-// together want 125 of shared memory's 128 bytes a clock. Orders of the tiles that read 0.3 to 1 GB of
-// DRAM take the same time. That is with zeros; random data meets the power limit and takes 0.33 us, and
-// there fewer reads help. Start, end and launch gap are 9 us.
+// Measured on random data, inputs that change from call to call: 4096 x 2048 x 8192 82 us (1.68 PFLOP/s; 90 with bias
+// and gelu, 94 with the kept z as well), 8192 x 4096 x 4096 154 us (1.78), its dx and dw 345 us (1.59). After seconds of
+// such calls the power limit makes that 170 and 355; between calls of other work the case with the kept z takes 102
+// to 104. At the MMAs' full rate (512 cycles a k-block) operand reads and TMA writes together want 125 of shared memory's 128 bytes a clock.
 //
 // k_linear_split: for products with too few 128-row tiles to fill the GPU (decoding batches, a
 // narrow output). The wide matrix (the weight) takes the MMA's 128 rows and the tokens its
 // columns, so a product with a handful of tokens multiplies 16 of them, not 128; a cluster of
 // up to eight CTAs shares one output tile, each with a part of K, and adds the parts in rank
 // order through distributed shared memory, so the result does not depend on timing. Bound by the
-// stream of the weight: 4 x 4096 x 4096 7.9 us (4.2 TB/s), of which 3 us are the first loads and the
-// cluster's sum.
+// stream of the weight and by what stands around it: 4 x 4096 x 4096 9.9 us with weights that change from call to call
+// (3.4 TB/s), 7.9 with one that stays in L2; start, first loads and the cluster's sum are 3 to 4 us of either.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -369,11 +367,10 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       const int64_t row0 = (int64_t)it.m * C::TILE_M + (int)rank * 128 + q * 32;  // this warp's first row
       const int rows = (int)min((int64_t)32, (int64_t)g.M - row0);              // rows of it that exist
       // y alternates between the two staging tiles and leaves by TMA. z goes out of the registers, 32 bytes
-      // a lane: it spares shared memory, which the products need, a write and a read (4096 x 2048 x 8192
-      // with gelu 96.6 -> 91.3 us; y that way too 92.9, since 32 rows an instruction take longer than one
-      // bulk store). Without VEC z takes the first tile and y the second. ready(c) waits until the store
-      // that last used chunk c's tile has read it and sends for its residual: for the first chunk while
-      // the products still run.
+      // a lane: it spares shared memory, which the products need, a write and a read (4096 x 2048 x 8192 with gelu and
+      // inputs that change: 98.3 -> 94.4 us back to back, 103.6 -> 101.9 between other work). Without VEC z takes the
+      // first tile and y the second. ready(c) waits until the store that last used chunk c's tile has read it and sends
+      // for its residual: for the first chunk while the products still run.
       const bool wide = VEC && g.N % 16 == 0 && (reinterpret_cast<uintptr_t>(g.pre) & 31) == 0;
       auto tile_of_y = [&] { return tile + (!VEC && g.pre ? kStage : (sc & 1) * kStage); };
       auto ready = [&](int c) {

@@ -3,10 +3,13 @@
 // h = x + residual, y = (h - mean) rstd w + b. Sums are fp32 throughout; the variance is
 // the mean of the squared deviations, taken in a second pass over the row (the one-pass
 // form sum(h^2) - mean^2 loses every digit when the mean is large against the spread).
-// Both directions are bound by HBM: each tensor is read or written once. Measured in bf16 with a
-// residual, inputs past L2: forward 8192 x 4096 46 us (5.8 TB/s), backward 49 us (5.5 TB/s, the
-// weight gradients included); one row of 2048 forward 1.8 us. Without a residual the forward is held
-// by the sums' instructions instead (8192 x 4096: 32 us, 4.2 TB/s).
+// Both directions are bound by HBM: each tensor is read or written once. Measured with inputs that change from call
+// to call (400 MB in turn), layer norm:
+//   8192 x 4096 with a residual   bf16 forward 46 us (5.8 TB/s), backward 49 (5.5, weight gradients included); fp32
+//                                 forward 87 (6.1); fp32 backward without a residual 66 (6.1)
+//   4096 x 2048 with a residual   bf16 forward 14.2, backward 19.9; fp32 forward 22, backward 27
+// Without a residual the bf16 forward is held by the sums' instructions instead (8192 x 4096: 31.5 us, 4.3 TB/s; RMS
+// 24.7). One row of 2048 forward 1.5 us.
 #include <algorithm>
 #include <atomic>
 
@@ -608,7 +611,9 @@ __global__ void __launch_bounds__(512) k_norm_bwd_ring(const BwdArgs a) {
 
 // The same for rows without 16-byte alignment, element by element: thread j keeps the columns
 // j + p G, and the next row's loads travel in registers while this row's sums meet. Slots past the
-// row are skipped by the whole group.
+// row are skipped by the whole group. Bound by the latency of these 4- and 2-byte loads, one block an SM: 1001 x 1111
+// in fp32 9.9 us with its second kernel (1.4 TB/s). The variant for 4097 to 8192 columns keeps 16 of each array a
+// thread and spills 144 to 168 bytes: 1001 x 5001 61 us in fp32, 53 in bf16.
 template <int G>
 constexpr int odd_threads = G < 256 ? 256 : G;
 
