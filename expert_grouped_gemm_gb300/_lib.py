@@ -3,7 +3,7 @@
 Argument marshalling only: each function checks that tensors are contiguous,
 on the current device and of the expected dtype, passes their pointers and the current
 CUDA stream, and raises MoeError on a non-OK status. Every step of the layer
-runs in the library's kernels. The norm, gate and linear operators, whose
+runs in the library's kernels. The operators around the experts, whose
 calls can be as short as a launch, do the same in one step of _bind
 (csrc/bind.cpp). There is no fallback: if the library is missing or fails to
 load, every call raises, and if _bind is, those operators' calls do.
@@ -39,7 +39,9 @@ EXPORTED = ["moe_workspace_size", "moe_fwd", "moe_select_retained", "moe_bwd", "
             "moe_timing_read", "moe_route_noalloc", "moe_plan_quota", "moe_selftest_wait", "moe_fwd_decode",
             "moe_selftest_decode_wait", "moe_norm_workspace_size", "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd",
             "moe_gate_bwd", "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd",
-            "moe_fwd_routed", "moe_bwd_routed"]
+            "moe_fwd_routed", "moe_bwd_routed", "moe_balance_workspace_size", "moe_balance_fwd", "moe_balance_bwd",
+            "moe_xent_workspace_size", "moe_xent_fwd", "moe_xent_bwd", "moe_grad_norm_workspace_size", "moe_grad_norm",
+            "moe_adamw_step"]
 
 
 class MoeError(RuntimeError):
@@ -69,6 +71,30 @@ class GateDims(ctypes.Structure):
 class LinearDims(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("act", ctypes.c_int32), ("out_f32", ctypes.c_int32)]
+
+
+class BalanceDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("S", ctypes.c_int64),
+                ("score", ctypes.c_int32), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("z_coef", ctypes.c_float)]
+
+
+class XentDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("H", ctypes.c_int64), ("V", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("tied", ctypes.c_int32), ("z_coef", ctypes.c_float)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWDims(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("step", ctypes.c_int64), ("lr", ctypes.c_float),
+                ("eps", ctypes.c_float), ("grad_scale", ctypes.c_float), ("max_norm", ctypes.c_float),
+                ("state_bits", ctypes.c_int32)]
 
 
 _lib = None
@@ -118,6 +144,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moe_linear_bwd.argtypes = [LD, vp, sz] + [vp] * 9
     lib.moe_fwd_routed.argtypes = [D, vp, sz] + [vp] * 13
     lib.moe_bwd_routed.argtypes = [D, vp, sz] + [vp] * 3 + [ctypes.c_int] + [vp] * 8
+    BD, XD, AD, AT = (ctypes.POINTER(t) for t in (BalanceDims, XentDims, AdamWDims, AdamWTensor))
+    lib.moe_balance_workspace_size.argtypes = [BD, ctypes.POINTER(sz)]
+    lib.moe_balance_fwd.argtypes = [BD, vp, sz] + [vp] * 7
+    lib.moe_balance_bwd.argtypes = [BD] + [vp] * 7
+    lib.moe_xent_workspace_size.argtypes = [XD, ctypes.c_int, ctypes.POINTER(sz)]
+    lib.moe_xent_fwd.argtypes = [XD, vp, sz] + [vp] * 7
+    lib.moe_xent_bwd.argtypes = [XD, vp, sz] + [vp] * 9
+    lib.moe_grad_norm_workspace_size.argtypes = [AT, i64, ctypes.POINTER(sz)]
+    lib.moe_grad_norm.argtypes = [AT, i64, vp, sz, vp, ctypes.c_float, vp]
+    lib.moe_adamw_step.argtypes = [AD, AT, i64, vp, vp, vp, vp]
+    for name in ["moe_balance_workspace_size", "moe_balance_fwd", "moe_balance_bwd", "moe_xent_workspace_size",
+                 "moe_xent_fwd", "moe_xent_bwd", "moe_grad_norm_workspace_size", "moe_grad_norm", "moe_adamw_step"]:
+        getattr(lib, name).restype = ctypes.c_int
     for name in ["moe_norm_workspace_size", "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd",
                  "moe_linear_workspace_size", "moe_linear_fwd", "moe_linear_bwd", "moe_fwd_routed", "moe_bwd_routed"]:
         getattr(lib, name).restype = ctypes.c_int
@@ -130,7 +169,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
 
 
 def _fast():
-    """The module that checks the tensors and calls the library in one step, for the norm, gate and linear operators."""
+    """The module that checks the tensors and calls the library in one step, for the operators around the experts."""
     global _bind
     if _bind is None:
         lib = load()
@@ -145,7 +184,8 @@ def _fast():
             raise RuntimeError(f"_bind.so was built for {built_for}, this is {bind_target()}: build it again "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         bind.init(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
-            "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd")))
+            "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd",
+            "moe_balance_fwd", "moe_balance_bwd", "moe_xent_fwd", "moe_xent_bwd")))
         _bind = bind
     return _bind
 
@@ -468,8 +508,13 @@ def alloc_linear_workspace(dims: LinearDims, device="cuda") -> torch.Tensor:
     graph that is being captured the zeroing is a part of the graph instead, ordered as the capture orders it."""
     n = ctypes.c_size_t(0)
     _check(load().moe_linear_workspace_size(ctypes.byref(dims), ctypes.byref(n)))
-    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
-    ws[:4096].zero_()
+    return _workspace(n.value, 4096, device)
+
+
+def _workspace(size: int, header: int, device) -> torch.Tensor:
+    """A workspace whose first `header` bytes are zero on return, as alloc_linear_workspace says."""
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    ws[:header].zero_()
     if ws.is_cuda and not torch.cuda.is_current_stream_capturing():
         torch.cuda.current_stream(ws.device).synchronize()
     return ws
@@ -506,6 +551,212 @@ def moe_linear_bwd(dims: LinearDims, ws, dy, x, w, pre, dx=None, dw=None, dbias=
         _tensor(x, "x", io, mk), _tensor(w, "w", io, kn), _tensor(pre, "pre", io, mn, False),
         _tensor(dx_add, "dx_add", io, mk, False), _tensor(dx, "dx", io, mk, False), _tensor(dw, "dw", io, kn, False),
         _tensor(dbias, "dbias", io, (N,), False)))
+
+
+def make_balance_dims(T, E, k, S=0, score="softmax", alpha=0.01, z_coef=0.0, dtype="f32", grad_dtype="f32") -> BalanceDims:
+    """S: sequences of the call (their offsets are given on the device); 0: all tokens are one."""
+    return BalanceDims(T, E, k, S, _named(MOE_SCORES, score, "score"), _dt(dtype), _dt(grad_dtype), alpha, z_coef)
+
+
+def alloc_balance_workspace(dims: BalanceDims, device="cuda") -> torch.Tensor:
+    """A workspace of moe_balance_fwd, its header zero on return (as alloc_linear_workspace's)."""
+    n = ctypes.c_size_t(0)
+    _check(load().moe_balance_workspace_size(ctypes.byref(dims), ctypes.byref(n)))
+    return _workspace(n.value, 256, device)
+
+
+def _seq(dims: BalanceDims, t):
+    if t is not None and not dims.S:
+        raise ValueError("seq_start given for dims without sequences (S is 0)")
+    return _tensor(t, "seq_start", torch.int32, (dims.S + 1,), dims.S > 0)
+
+
+def moe_balance_fwd(dims: BalanceDims, ws, logits, topk_idx, seq_start, loss, count, prob=None, stream=None):
+    """loss[2]: balance loss and z loss of router logits; count and prob [max(S, 1), E]: choices and mean probabilities."""
+    rc = _fast().balance_fwd(dims, stream if stream is None else _stream(stream), ws, logits, topk_idx, seq_start, loss,
+                             count, prob)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
+    se, f32 = (max(dims.S, 1), dims.E), torch.float32
+    _check(load().moe_balance_fwd(
+        dims, _ws(ws), ws.numel(), _stream(stream), _tensor(logits, "logits", _io_dtype(dims), (dims.T, dims.E)),
+        _tensor(topk_idx, "topk_idx", torch.int32, (dims.T, dims.k)), _seq(dims, seq_start),
+        _tensor(loss, "loss", f32, (2,)), _tensor(count, "count", torch.int32, se), _tensor(prob, "prob", f32, se, False)))
+
+
+def moe_balance_bwd(dims: BalanceDims, logits, count, seq_start, dloss, dlogits_add, dlogits, stream=None):
+    """Gradient of the sum of moe_balance_fwd's losses to the logits, times dloss[1] (None: 1), plus dlogits_add."""
+    rc = _fast().balance_bwd(dims, stream if stream is None else _stream(stream), logits, count, seq_start, dloss,
+                             dlogits_add, dlogits)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
+    te, grad = (dims.T, dims.E), torch.bfloat16 if dims.grad_dtype == MOE_BF16 else torch.float32
+    args = (
+        _tensor(logits, "logits", _io_dtype(dims), te),
+        _tensor(count, "count", torch.int32, (max(dims.S, 1), dims.E)), _seq(dims, seq_start),
+        _tensor(dloss, "dloss", torch.float32, (1,), False), _tensor(dlogits_add, "dlogits_add", grad, te, False),
+        _tensor(dlogits, "dlogits", grad, te))
+    _check(load().moe_balance_bwd(dims, _stream(stream), *args))
+
+
+def make_xent_dims(M, H, V, dtype="bf16", tied=False, z_coef=0.0) -> XentDims:
+    """tied: w is an embedding table [V, H] in place of [H, V]."""
+    return XentDims(M, H, V, _dt(dtype), 1 if tied else 0, z_coef)
+
+
+def alloc_xent_workspace(dims: XentDims, device="cuda", backward=True) -> torch.Tensor:
+    """A workspace of moe_xent_fwd, and of moe_xent_bwd unless backward is False; its header is zero on return."""
+    n = ctypes.c_size_t(0)
+    _check(load().moe_xent_workspace_size(ctypes.byref(dims), 1 if backward else 0, ctypes.byref(n)))
+    return _workspace(n.value, 256, device)
+
+
+def _xent_inputs(dims: XentDims, x, w, target):
+    io = _io_dtype(dims)
+    return (_tensor(x, "x", io, (dims.M, dims.H)),
+            _tensor(w, "w", io, (dims.V, dims.H) if dims.tied else (dims.H, dims.V)),
+            _tensor(target, "target", torch.int32, (dims.M,)))
+
+
+def moe_xent_fwd(dims: XentDims, ws, x, w, target, loss, lse, total=None, stream=None):
+    """Cross entropy of the logits x w: loss[M], lse[M], and total[2] = (sum of the losses, rows counted)."""
+    rc = _fast().xent_fwd(dims, stream if stream is None else _stream(stream), ws, x, w, target, loss, lse, total)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
+    f32, m = torch.float32, (dims.M,)
+    _check(load().moe_xent_fwd(
+        dims, _ws(ws), ws.numel(), _stream(stream), *_xent_inputs(dims, x, w, target), _tensor(loss, "loss", f32, m),
+        _tensor(lse, "lse", f32, m), _tensor(total, "total", f32, (2,), False)))
+
+
+def moe_xent_bwd(dims: XentDims, ws, x, w, target, lse, dloss, total, dx=None, dw=None, stream=None):
+    """Gradients to x and w for the rows' dloss[M], or of the mean loss (dloss None, the forward's total given)."""
+    rc = _fast().xent_bwd(dims, stream if stream is None else _stream(stream), ws, x, w, target, lse, dloss, total, dx, dw)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
+    f32, m, io = torch.float32, (dims.M,), _io_dtype(dims)
+    _check(load().moe_xent_bwd(
+        dims, _ws(ws), ws.numel(), _stream(stream), *_xent_inputs(dims, x, w, target), _tensor(lse, "lse", f32, m),
+        _tensor(dloss, "dloss", f32, m, False), _tensor(total, "total", f32, (2,), False),
+        _tensor(dx, "dx", io, (dims.M, dims.H), False),
+        _tensor(dw, "dw", io, (dims.V, dims.H) if dims.tied else (dims.H, dims.V), False)))
+
+
+# ---------------------------------------------------------------- optimiser
+class TensorList:
+    """The tensors of an optimiser call as the library reads them; keeps them alive. Made once, used every step."""
+
+    def __init__(self, entries, keep, bits, device):
+        self.count, self.bits, self.device, self._keep = len(entries), bits, device, keep
+        self.array = (AdamWTensor * max(1, len(entries)))(*entries)
+        self.head = self.array  # what the calls pass
+
+
+def _flat(t, name, i, dtypes, n=None):
+    """The pointer of a contiguous CUDA tensor of one of these types (any shape, n values)."""
+    what = f"{name}[{i}]"
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    _here(t, what)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{what} must have {n} values, got {t.numel()}")
+    return t.data_ptr() or None
+
+
+_WEIGHT_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _code(t):
+    return MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
+
+
+def make_grad_tensors(grads) -> TensorList:
+    """Gradients alone, as moe_grad_norm takes them (a list of make_adamw_tensors serves as well)."""
+    grads = list(grads)
+    entries = [AdamWTensor(grad=_flat(g, "grads", i, _WEIGHT_TYPES), n=g.numel(), grad_dtype=_code(g))
+               for i, g in enumerate(grads)]
+    return TensorList(entries, grads, None, grads[0].get_device() if grads else None)
+
+
+def make_adamw_tensors(params, grads, m, v, master=None, m_scale=None, v_scale=None, weight_decay=0.0,
+                       lr_scale=1.0) -> TensorList:
+    """The tensors of moe_adamw_step, one list each. m and v: fp32, or torch.float8_e4m3fn with the fp32 scales of their
+    blocks of 256 values (v holds square roots then). master: fp32 copies of bf16 weights (None, or a list that may
+    hold None). weight_decay and lr_scale: one number, or one for each tensor."""
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    n = len(params)
+    each = lambda x, fill: [fill] * n if x is None else list(x) if isinstance(x, (list, tuple)) else [x] * n
+    master, m_scale, v_scale = each(master, None), each(m_scale, None), each(v_scale, None)
+    decay, lrs = each(weight_decay, 0.0), each(lr_scale, 1.0)
+    for name, x in (("grads", grads), ("m", m), ("v", v), ("master", master), ("m_scale", m_scale), ("v_scale", v_scale),
+                    ("weight_decay", decay), ("lr_scale", lrs)):
+        if len(x) != n:
+            raise ValueError(f"{name} must have {n} entries, got {len(x)}")
+    bits = 8 if n and isinstance(m[0], torch.Tensor) and m[0].dtype == torch.float8_e4m3fn else 32
+    state = (torch.float8_e4m3fn,) if bits == 8 else (torch.float32,)
+    entries, written = [], []
+    for i in range(n):
+        p = _flat(params[i], "params", i, _WEIGHT_TYPES)
+        size = params[i].numel()
+        scales = [None, None]
+        if bits == 8:
+            scales = [_flat(t, name, i, (torch.float32,), (size + 255) // 256)
+                      for name, t in (("m_scale", m_scale[i]), ("v_scale", v_scale[i]))]
+        elif m_scale[i] is not None or v_scale[i] is not None:
+            raise ValueError(f"m_scale and v_scale belong to states in 8 bits, m[{i}] is {m[i].dtype}")
+        mp = None if master[i] is None else _flat(master[i], "master", i, (torch.float32,), size)
+        entries.append(AdamWTensor(p, _flat(grads[i], "grads", i, _WEIGHT_TYPES, size), mp,
+                                   _flat(m[i], "m", i, state, size), _flat(v[i], "v", i, state, size), *scales, size,
+                                   _code(params[i]), _code(grads[i]), lrs[i], decay[i]))
+        written += [t for t in (params[i], m[i], v[i], master[i], m_scale[i], v_scale[i]) if t is not None and t.numel()]
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written)
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("weights or states overlap: every tensor may be listed once")
+    return TensorList(entries, (params, grads, m, v, master, m_scale, v_scale), bits,
+                      params[0].get_device() if n else None)
+
+
+def make_adamw_dims(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, state_bits=32, max_norm=0.0, grad_scale=1.0) -> AdamWDims:
+    return AdamWDims(beta1, beta2, step, lr, eps, grad_scale, max_norm, state_bits)
+
+
+def _list_here(tensors: TensorList):
+    if tensors.device is not None and tensors.device != _device():
+        raise ValueError(f"the tensors are on cuda:{tensors.device}, the current device is cuda:{_device()}")
+
+
+def alloc_grad_norm_workspace(tensors: TensorList, device="cuda") -> torch.Tensor:
+    """A workspace of moe_grad_norm for these tensors, its header zero on return."""
+    n = ctypes.c_size_t(0)
+    _check(load().moe_grad_norm_workspace_size(tensors.head, tensors.count, ctypes.byref(n)))
+    return _workspace(n.value, 256, device)
+
+
+def moe_grad_norm(tensors: TensorList, ws, norm, grad_scale=1.0, stream=None):
+    """norm[1] = grad_scale times the 2-norm of all gradients of the list."""
+    _list_here(tensors)
+    _check(load().moe_grad_norm(tensors.head, tensors.count, _ws(ws), ws.numel(), _stream(stream), grad_scale,
+                                _tensor(norm, "norm", torch.float32, (1,))))
+
+
+def moe_adamw_step(dims: AdamWDims, tensors: TensorList, norm=None, lr=None, step=None, stream=None):
+    """One AdamW step over the list, in place. norm[1]: the gradients' norm (clipping; a step on inf or NaN is left out);
+    lr[1] (fp32), step[1] (int32): on the device, in place of dims'."""
+    _list_here(tensors)
+    if tensors.bits != dims.state_bits and tensors.count:
+        raise ValueError(f"the list's states have {tensors.bits} bits, dims say {dims.state_bits}")
+    one = (1,)
+    _check(load().moe_adamw_step(
+        dims, tensors.head, tensors.count, _stream(stream), _tensor(norm, "norm", torch.float32, one, False),
+        _tensor(lr, "lr", torch.float32, one, False), _tensor(step, "step", torch.int32, one, False)))
 
 
 def moe_read_status(ws: torch.Tensor, stream=None) -> int:

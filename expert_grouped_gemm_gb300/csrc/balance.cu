@@ -1,0 +1,440 @@
+// balance.cu -- balance loss and z loss of router logits, forward and backward.
+//
+// With p = softmax(l), or sigmoid(l) over their sum, n_s the tokens of sequence s, N those of all sequences:
+//   count_se = chosen experts, prob_se = mean of p over the sequence,
+//   loss = alpha E / (k N) sum_se count_se prob_se,   z loss = z / N sum_t lse_t^2,
+//   dl = p (1 - sigma) (c - p.c) + 2 z / N lse p   with c_e = alpha E / (k N) count_se / n_s  ((1 - sigma): sigmoid only).
+//
+// Forward: tokens are cut into chunks of equal length, a block each; a block walks the sequences that its chunk
+// meets and writes one row of sums (p, counts, lse^2) for each. Row c + s holds chunk c of sequence s: along the
+// tokens either index only grows, so no two share a row and chunks + S rows are enough. A second kernel adds a
+// sequence's rows in order, so results do not depend on timing.
+#include <algorithm>
+#include <type_traits>
+
+#include "block.h"
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kWarps = 8;
+
+struct BalanceArgs {
+  const void* logits;
+  const int* idx;
+  const int* start;   // [S + 1] or null
+  int T, E, k, S;
+  int R, vec;         // experts of a lane, in 16-byte pieces
+  int chunk, chunks;
+  float alpha, z;
+  float* row_p;       // [chunks + S][E]
+  int* row_n;         // [chunks + S][E]
+  float* row_z;       // [chunks + S]
+  float* part;        // [S][2]: a sequence's part of the losses
+  unsigned* done;
+  int* status;
+  float* loss;
+  int* count;
+  float* prob;
+  // backward
+  const int* count_in;
+  const float* dloss;
+  const void* add;
+  void* dlogits;
+};
+
+__device__ __forceinline__ int seq_at(const BalanceArgs& a, int s) {
+  return a.start ? min(max(a.start[s], 0), a.T) : (s ? a.T : 0);
+}
+// the last sequence that begins at or before token t (0 if none does)
+__device__ __forceinline__ int seq_of(const BalanceArgs& a, int t) {
+  int lo = 0, hi = a.S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_at(a, mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ float tokens_of_all(const BalanceArgs& a) {
+  return fmaxf(1.0f, (float)(seq_at(a, a.S) - seq_at(a, 0)));
+}
+
+// The lane's n logits (of at most EPL) at p; NaN masks its expert as -inf does.
+template <int EPL, typename TL>
+__device__ __forceinline__ void load_row(const TL* p, int n, bool vec, float (&l)[EPL]) {
+  constexpr int V = 16 / (int)sizeof(TL);
+  if constexpr (EPL % V == 0) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += V) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < n) u = *reinterpret_cast<const uint4*>(p + i);
+        const TL* e = reinterpret_cast<const TL*>(&u);
+#pragma unroll
+        for (int q = 0; q < V; ++q) l[i + q] = i < n ? io<TL>::to_f(e[q]) : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] = l[i] != l[i] ? -INFINITY : l[i];
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const float v = i < n ? io<TL>::to_f(p[i]) : -INFINITY;
+    l[i] = v != v ? -INFINITY : v;
+  }
+}
+
+// Whether a row has a z loss: not where every logit is masked, by -inf or by its type's lowest value (the square of
+// such an lse is no float), nor where one is +inf.
+__device__ __forceinline__ bool has_lse(float lse) { return fabsf(lse) < 9.2e18f; }
+
+__device__ __forceinline__ float warp_max(float v) {
+  const uint32_t u = __float_as_uint(v), key = u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t m = __reduce_max_sync(kFull, key);
+  return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+}
+
+// l becomes p. softmax: returns the row's lse (not finite where the row has no finite logit, or a +inf). sigmoid:
+// away (where given) receives 1 - sigma; scores are taken relative to the largest, so that a row of logits far
+// below zero, whose scores are denormal, has a sum that can be divided by. A masked row is all zeros.
+template <int EPL, bool SOFTMAX>
+__device__ __forceinline__ float probs(float (&l)[EPL], float* away) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+  m = warp_max(m);
+  float sum = 0.0f;
+  if constexpr (SOFTMAX) {
+    if (fabsf(m) < INFINITY) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) sum += l[i] = expf(l[i] - m);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) sum += l[i] = l[i] == INFINITY ? 1.0f : 0.0f;
+    }
+  } else {
+    const float low = m > -INFINITY ? fminf(m, 0.0f) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float e = expf(-fabsf(l[i])), r = 1.0f / (1.0f + e);  // sigma(|l|)
+      if (away) away[i] = l[i] > 0.0f ? e * r : r;
+      l[i] = l[i] > 0.0f ? r : expf(l[i] - low) * r;
+      sum += l[i];
+    }
+  }
+  sum = warp_sum(sum);
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] *= inv;
+  return m + logf(sum);
+}
+
+template <int EPL, bool SOFTMAX, typename TL>
+__global__ void __launch_bounds__(kWarps * 32) k_balance_fwd(const BalanceArgs a) {
+  extern __shared__ float shared[];  // [E] sums of p, [E] counts
+  int* hist = reinterpret_cast<int*>(shared + a.E);
+  __shared__ float zsum[kWarps];
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
+  const int c0 = (int)blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.T);
+  for (int s = seq_of(a, c0); s < a.S; ++s) {
+    const int b0 = max(c0, seq_at(a, s)), b1 = min(c1, seq_at(a, s + 1));
+    if (seq_at(a, s) >= c1) break;
+    if (b0 >= b1) continue;
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+      shared[i] = 0.0f;
+      hist[i] = 0;
+    }
+    float acc[EPL], z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
+    for (int t = b0 + warp; t < b1; t += kWarps) {
+      float l[EPL];
+      load_row<EPL>(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E + e0, n, a.vec, l);
+      const float lse = probs<EPL, SOFTMAX>(l, nullptr);
+      if (SOFTMAX && has_lse(lse)) z += lse * lse;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) acc[i] += l[i];
+    }
+    if (lane == 0) zsum[warp] = z;
+    __syncthreads();
+    const int64_t i1 = (int64_t)b1 * a.k;
+    for (int64_t i = (int64_t)b0 * a.k + threadIdx.x; i < i1; i += blockDim.x) {
+      const int e = a.idx[i];
+      if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
+    }
+    for (int w = 0; w < kWarps; ++w) {  // the warps' sums in order
+      if (w == warp)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (i < n) shared[e0 + i] += acc[i];
+      __syncthreads();
+    }
+    const int64_t row = (int64_t)blockIdx.x + s;
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+      a.row_p[row * a.E + i] = shared[i];
+      a.row_n[row * a.E + i] = hist[i];
+    }
+    if (threadIdx.x == 0) {
+      float v = 0.0f;
+      for (int w = 0; w < kWarps; ++w) v += zsum[w];
+      a.row_z[row] = v;
+    }
+    __syncthreads();
+  }
+}
+
+// A block a sequence: its rows added, then its part of the losses; the last block adds the parts in order.
+__global__ void __launch_bounds__(1024) k_balance_sum(const BalanceArgs a) {
+  __shared__ float red[32];
+  __shared__ float sp[32][33];
+  __shared__ int sn[32][33];
+  __shared__ bool last;
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  const int s = (int)blockIdx.x, cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
+  if (a.start && threadIdx.x == 0 && (a.start[s] > a.start[s + 1] || a.start[s] < 0 || a.start[s + 1] > a.T))
+    set_status(a.status, MOE_ERR_DEVICE_ARG);
+  const int r0 = t0 < t1 ? t0 / a.chunk + s : 0, r1 = t0 < t1 ? (t1 - 1) / a.chunk + s + 1 : 0;
+  const float n = (float)max(t1 - t0, 1), N = tokens_of_all(a);
+  float dot = 0.0f;
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + cx;
+    float p = 0.0f;
+    int c = 0;
+    if (e < a.E)
+      for (int r = r0 + ry; r < r1; r += 32) {
+        p += a.row_p[(int64_t)r * a.E + e];
+        c += a.row_n[(int64_t)r * a.E + e];
+      }
+    sp[ry][cx] = p;
+    sn[ry][cx] = c;
+    __syncthreads();
+    if (ry == 0 && e < a.E) {
+#pragma unroll
+      for (int r = 1; r < 32; ++r) {
+        p += sp[r][cx];
+        c += sn[r][cx];
+      }
+      p /= n;
+      a.count[(int64_t)s * a.E + e] = c;
+      if (a.prob) a.prob[(int64_t)s * a.E + e] = p;
+      dot += (float)c * p;
+    }
+    __syncthreads();
+  }
+  float z = 0.0f;
+  for (int r = r0 + (int)threadIdx.x; r < r1; r += blockDim.x) z += a.row_z[r];
+  z = warp_sum(z);
+  if (cx == 0) red[ry] = z;
+  if (ry == 0) dot = warp_sum(dot);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int r = 1; r < 32; ++r) z += red[r];
+    a.part[2 * s] = dot;
+    a.part[2 * s + 1] = z;
+    __threadfence();
+    last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (threadIdx.x < 2) {
+    float v = 0.0f;
+    for (int i = 0; i < a.S; ++i) v += __ldcg(a.part + 2 * i + threadIdx.x);
+    a.loss[threadIdx.x] = v * (threadIdx.x == 0 ? a.alpha * (float)a.E / (float)a.k : a.z) / N;
+  }
+  if (threadIdx.x == 0) *a.done = 0;
+}
+
+// A warp a token.
+template <int EPL, bool SOFTMAX, typename TL, typename TG>
+__global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  const int t = (int)blockIdx.x * kWarps + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
+  const int64_t o = (int64_t)t * a.E + e0;
+  const int s = seq_of(a, t), t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
+  float l[EPL];
+  if (t >= t0 && t < t1) {
+    const float N = tokens_of_all(a), up = a.dloss ? *a.dloss : 1.0f;
+    load_row<EPL>(reinterpret_cast<const TL*>(a.logits) + o, n, a.vec, l);
+    float away[SOFTMAX ? 1 : EPL];
+    const float lse = probs<EPL, SOFTMAX>(l, SOFTMAX ? nullptr : away);
+    const float f = up * a.alpha * ((float)a.E / (float)a.k) / N / (float)(t1 - t0);
+    float c[EPL], dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      c[i] = i < n ? f * (float)a.count_in[(int64_t)s * a.E + e0 + i] : 0.0f;
+      dot += l[i] * c[i];
+    }
+    dot = warp_sum(dot);
+    const float zf = SOFTMAX && has_lse(lse) ? up * 2.0f * a.z / N * lse : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if constexpr (SOFTMAX) l[i] *= c[i] - dot + zf;
+      else l[i] *= away[i] * (c[i] - dot);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = 0.0f;
+  }
+  const TG* add = reinterpret_cast<const TG*>(a.add);
+  TG* out = reinterpret_cast<TG*>(a.dlogits);
+  constexpr int V = 16 / (int)sizeof(TG);
+  if constexpr (EPL % V == 0) {
+    if (a.vec) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += V) {
+        if (i >= n) break;
+        if (add) {
+          const uint4 u = *reinterpret_cast<const uint4*>(add + o + i);
+          const TG* q = reinterpret_cast<const TG*>(&u);
+#pragma unroll
+          for (int j = 0; j < V; ++j) l[i + j] += io<TG>::to_f(q[j]);
+        }
+        uint4 u;
+        TG* q = reinterpret_cast<TG*>(&u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) q[j] = io<TG>::cvt(l[i + j]);
+        *reinterpret_cast<uint4*>(out + o + i) = u;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (i < n) out[o + i] = io<TG>::cvt(l[i] + (add ? io<TG>::to_f(add[o + i]) : 0.0f));
+}
+
+// ---------------------------------------------------------------- host side
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr int kChunkBlocks = 304;  // chunks to aim for: two for each of 152 SMs
+
+// Tokens of a chunk: enough chunks for every SM, at least a token for each warp.
+int chunk_tokens(int64_t T) {
+  return (int)std::max<int64_t>(kWarps, (T + kChunkBlocks - 1) / kChunkBlocks);
+}
+
+struct BalanceWs {
+  size_t p, n, z, part, total;
+};
+BalanceWs layout(const moe_balance_dims& d) {
+  const size_t c = chunk_tokens(d.T), S = (size_t)std::max<int64_t>(d.S, 1), rows = ((size_t)d.T + c - 1) / c + S;
+  BalanceWs L;
+  size_t o = kBalanceHeader;
+  L.p = o;
+  o += up256(rows * d.E * 4);
+  L.n = o;
+  o += up256(rows * d.E * 4);
+  L.z = o;
+  o += up256(rows * 4);
+  L.part = o;
+  o += up256(S * 8);
+  L.total = o;
+  return L;
+}
+
+template <typename F>
+cudaError_t with_epl(int R, F f) {
+  if (R <= 1) return f(std::integral_constant<int, 1>());
+  if (R <= 2) return f(std::integral_constant<int, 2>());
+  if (R <= 4) return f(std::integral_constant<int, 4>());
+  if (R <= 8) return f(std::integral_constant<int, 8>());
+  if (R <= 16) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());  // E <= 1024
+}
+
+BalanceArgs args_of(const moe_balance_dims& d, const void* logits, const int* start, bool half) {
+  BalanceArgs a = {};
+  a.logits = logits;
+  a.start = d.S ? start : nullptr;
+  a.T = (int)d.T;
+  a.E = (int)d.E;
+  a.k = (int)d.k;
+  a.S = (int)std::max<int64_t>(d.S, 1);
+  a.alpha = d.alpha;
+  a.z = d.z_coef;
+  a.R = (a.E + 31) / 32;
+  const int V = half ? 8 : 4;
+  a.vec = a.E % V == 0;
+  if (a.vec) a.R = (a.R + V - 1) / V * V;
+  return a;
+}
+
+template <int EPL, bool SOFTMAX>
+cudaError_t bwd_typed(const moe_balance_dims& d, const BalanceArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)((d.T + kWarps - 1) / kWarps);
+  using bf = __nv_bfloat16;
+  if (d.dtype == MOE_BF16) {
+    if (d.grad_dtype == MOE_BF16) MOE_LAUNCH(k_balance_bwd<EPL, SOFTMAX, bf, bf>, grid, kWarps * 32, 0, st, a);
+    else MOE_LAUNCH(k_balance_bwd<EPL, SOFTMAX, bf, float>, grid, kWarps * 32, 0, st, a);
+  } else {
+    if (d.grad_dtype == MOE_BF16) MOE_LAUNCH(k_balance_bwd<EPL, SOFTMAX, float, bf>, grid, kWarps * 32, 0, st, a);
+    else MOE_LAUNCH(k_balance_bwd<EPL, SOFTMAX, float, float>, grid, kWarps * 32, 0, st, a);
+  }
+  return cudaSuccess;
+}
+
+template <int EPL, bool SOFTMAX>
+cudaError_t fwd_typed(const moe_balance_dims& d, const BalanceArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)a.E * 8;
+  if (d.dtype == MOE_BF16) MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, __nv_bfloat16>, a.chunks, kWarps * 32, smem, st, a);
+  else MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, float>, a.chunks, kWarps * 32, smem, st, a);
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(const moe_balance_dims& d) { return layout(d).total; }
+
+cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* logits, const int* topk_idx,
+                               const int* seq_start, float* loss, int* count, float* prob, cudaStream_t st,
+                               int* launches) {
+  BalanceArgs a = args_of(d, logits, seq_start, d.dtype == MOE_BF16);
+  const BalanceWs L = layout(d);
+  char* w = static_cast<char*>(ws);
+  a.idx = topk_idx;
+  a.chunk = chunk_tokens(d.T);
+  a.chunks = (a.T + a.chunk - 1) / a.chunk;
+  a.row_p = reinterpret_cast<float*>(w + L.p);
+  a.row_n = reinterpret_cast<int*>(w + L.n);
+  a.row_z = reinterpret_cast<float*>(w + L.z);
+  a.part = reinterpret_cast<float*>(w + L.part);
+  a.status = reinterpret_cast<int*>(w);
+  a.done = reinterpret_cast<unsigned*>(w + 64);
+  a.loss = loss;
+  a.count = count;
+  a.prob = prob;
+  *launches += 2;
+  const cudaError_t e = with_epl(a.R, [&](auto epl) {
+    constexpr int EPL = decltype(epl)::value;
+    return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true>(d, a, st) : fwd_typed<EPL, false>(d, a, st);
+  });
+  if (e != cudaSuccess) return e;
+  MOE_LAUNCH(k_balance_sum, a.S, 1024, 0, st, a);
+  return cudaSuccess;
+}
+
+cudaError_t launch_balance_bwd(const moe_balance_dims& d, const void* logits, const int* count, const int* seq_start,
+                               const float* dloss, const void* dlogits_add, void* dlogits, cudaStream_t st,
+                               int* launches) {
+  BalanceArgs a = args_of(d, logits, seq_start, d.dtype == MOE_BF16 || d.grad_dtype == MOE_BF16);
+  a.count_in = count;
+  a.dloss = dloss;
+  a.add = dlogits_add;
+  a.dlogits = dlogits;
+  *launches += 1;
+  return with_epl(a.R, [&](auto epl) {
+    constexpr int EPL = decltype(epl)::value;
+    return d.score == MOE_SCORE_SOFTMAX ? bwd_typed<EPL, true>(d, a, st) : bwd_typed<EPL, false>(d, a, st);
+  });
+}
+
+}  // namespace moe

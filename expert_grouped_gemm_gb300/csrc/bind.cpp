@@ -1,4 +1,4 @@
-// bind.cpp -- the Python side of the operators around the experts (norm, gate, linear) as a CPython
+// bind.cpp -- the Python side of the operators around the experts as a CPython
 // module: one call checks every tensor (on the current device, type, shape, contiguity), takes the current stream and
 // calls the C ABI. A call of a few microseconds on the GPU is bound by what the host does for it: on a Grace
 // core moe_norm_fwd with four tensors took 4.7 us with the checks in Python (0.38 a tensor) and the call
@@ -28,6 +28,10 @@ decltype(&moe_gate_fwd) g_gate_fwd = nullptr;
 decltype(&moe_gate_bwd) g_gate_bwd = nullptr;
 decltype(&moe_linear_fwd) g_linear_fwd = nullptr;
 decltype(&moe_linear_bwd) g_linear_bwd = nullptr;
+decltype(&moe_balance_fwd) g_balance_fwd = nullptr;
+decltype(&moe_balance_bwd) g_balance_bwd = nullptr;
+decltype(&moe_xent_fwd) g_xent_fwd = nullptr;
+decltype(&moe_xent_bwd) g_xent_bwd = nullptr;
 
 constexpr bool kNeeded = true, kMay = false;  // a tensor that has to be there, one that may be None
 
@@ -230,29 +234,117 @@ PyObject* linear_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(norm_fwd, norm_bwd, gate_fwd, gate_bwd, linear_fwd, linear_bwd): addresses of the C ABI's functions
+PyObject* balance_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    moe_balance_dims d;
+    Call c(a, n, 9, &d, sizeof d);
+    if (!c.ok()) Py_RETURN_NONE;
+    const int64_t S = d.S > 1 ? d.S : 1;
+    size_t bytes = 0;
+    void* ws = c.workspace(2, &bytes);
+    const void* logits = c.tensor(3, kNeeded, io_type(d.dtype), d.T, d.E);
+    const int32_t* idx = c.tensor<int32_t>(4, kNeeded, at::kInt, d.T, d.k);
+    const int32_t* start = c.tensor<int32_t>(5, kMay, at::kInt, d.S + 1);
+    float* loss = c.tensor<float>(6, kNeeded, at::kFloat, 2);
+    int32_t* count = c.tensor<int32_t>(7, kNeeded, at::kInt, S, d.E);
+    float* prob = c.tensor<float>(8, kMay, at::kFloat, S, d.E);
+    if (!c.ok() || (start != nullptr) != (d.S > 0)) Py_RETURN_NONE;
+    return c.run([&](void* st) { return g_balance_fwd(&d, ws, bytes, st, logits, idx, start, loss, count, prob); });
+  });
+}
+
+PyObject* balance_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    moe_balance_dims d;
+    Call c(a, n, 8, &d, sizeof d);
+    if (!c.ok()) Py_RETURN_NONE;
+    const at::ScalarType grad = io_type(d.grad_dtype);
+    const void* logits = c.tensor(2, kNeeded, io_type(d.dtype), d.T, d.E);
+    const int32_t* count = c.tensor<int32_t>(3, kNeeded, at::kInt, d.S > 1 ? d.S : 1, d.E);
+    const int32_t* start = c.tensor<int32_t>(4, kMay, at::kInt, d.S + 1);
+    const float* dloss = c.tensor<float>(5, kMay, at::kFloat, 1);
+    const void* add = c.tensor(6, kMay, grad, d.T, d.E);
+    void* dlogits = c.tensor(7, kNeeded, grad, d.T, d.E);
+    if (!c.ok() || (start != nullptr) != (d.S > 0)) Py_RETURN_NONE;
+    return c.run([&](void* st) { return g_balance_bwd(&d, st, logits, count, start, dloss, add, dlogits); });
+  });
+}
+
+PyObject* xent_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    moe_xent_dims d;
+    Call c(a, n, 9, &d, sizeof d);
+    if (!c.ok()) Py_RETURN_NONE;
+    const at::ScalarType io = io_type(d.dtype);
+    size_t bytes = 0;
+    void* ws = c.workspace(2, &bytes);
+    const void* x = c.tensor(3, kNeeded, io, d.M, d.H);
+    const void* w = c.tensor(4, kNeeded, io, d.tied ? d.V : d.H, d.tied ? d.H : d.V);
+    const int32_t* target = c.tensor<int32_t>(5, kNeeded, at::kInt, d.M);
+    float* loss = c.tensor<float>(6, kNeeded, at::kFloat, d.M);
+    float* lse = c.tensor<float>(7, kNeeded, at::kFloat, d.M);
+    float* total = c.tensor<float>(8, kMay, at::kFloat, 2);
+    if (!c.ok()) Py_RETURN_NONE;
+    return c.run([&](void* st) { return g_xent_fwd(&d, ws, bytes, st, x, w, target, loss, lse, total); });
+  });
+}
+
+PyObject* xent_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    moe_xent_dims d;
+    Call c(a, n, 11, &d, sizeof d);
+    if (!c.ok()) Py_RETURN_NONE;
+    const at::ScalarType io = io_type(d.dtype);
+    const int64_t r = d.tied ? d.V : d.H, q = d.tied ? d.H : d.V;
+    size_t bytes = 0;
+    void* ws = c.workspace(2, &bytes);
+    const void* x = c.tensor(3, kNeeded, io, d.M, d.H);
+    const void* w = c.tensor(4, kNeeded, io, r, q);
+    const int32_t* target = c.tensor<int32_t>(5, kNeeded, at::kInt, d.M);
+    const float* lse = c.tensor<float>(6, kNeeded, at::kFloat, d.M);
+    const float* dloss = c.tensor<float>(7, kMay, at::kFloat, d.M);
+    const float* total = c.tensor<float>(8, kMay, at::kFloat, 2);
+    void* dx = c.tensor(9, kMay, io, d.M, d.H);
+    void* dw = c.tensor(10, kMay, io, r, q);
+    if (!c.ok()) Py_RETURN_NONE;
+    return c.run([&](void* st) { return g_xent_bwd(&d, ws, bytes, st, x, w, target, lse, dloss, total, dx, dw); });
+  });
+}
+
+template <typename F>
+void take(F& f, void* p) {
+  f = reinterpret_cast<F>(p);
+}
+
+// init(addresses of the C ABI's functions, in the order below)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "init takes six addresses");
+  constexpr int kCount = 10;
+  if (n != kCount) {
+    PyErr_Format(PyExc_TypeError, "init takes %d addresses", kCount);
     return nullptr;
   }
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  void* p[kCount];
+  for (int i = 0; i < kCount; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  g_norm_fwd = reinterpret_cast<decltype(g_norm_fwd)>(p[0]);
-  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[1]);
-  g_gate_fwd = reinterpret_cast<decltype(g_gate_fwd)>(p[2]);
-  g_gate_bwd = reinterpret_cast<decltype(g_gate_bwd)>(p[3]);
-  g_linear_fwd = reinterpret_cast<decltype(g_linear_fwd)>(p[4]);
-  g_linear_bwd = reinterpret_cast<decltype(g_linear_bwd)>(p[5]);
+  take(g_norm_fwd, p[0]);
+  take(g_norm_bwd, p[1]);
+  take(g_gate_fwd, p[2]);
+  take(g_gate_bwd, p[3]);
+  take(g_linear_fwd, p[4]);
+  take(g_linear_bwd, p[5]);
+  take(g_balance_fwd, p[6]);
+  take(g_balance_bwd, p[7]);
+  take(g_xent_fwd, p[8]);
+  take(g_xent_bwd, p[9]);
   Py_RETURN_NONE;
 }
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(init),     METHOD(norm_fwd),   METHOD(norm_bwd),   METHOD(gate_fwd),
-                         METHOD(gate_bwd), METHOD(linear_fwd), METHOD(linear_bwd), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(init),        METHOD(norm_fwd),    METHOD(norm_bwd),   METHOD(gate_fwd),
+                         METHOD(gate_bwd),    METHOD(linear_fwd),  METHOD(linear_bwd), METHOD(balance_fwd),
+                         METHOD(balance_bwd), METHOD(xent_fwd),    METHOD(xent_bwd),   {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

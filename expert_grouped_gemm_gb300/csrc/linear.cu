@@ -6,25 +6,13 @@
 #include "act.cuh"
 #include "block.h"
 #include "common.cuh"
+#include "linear_f32.h"
 #include "linear_tc.h"
 
 namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- fp32 products
-// One product C = op(A) op(B) with element strides, and the epilogue of the forward.
-struct SimtGemm {
-  const float* A;
-  const float* B;
-  int64_t sam, sak, sbk, sbn;  // element strides of A[m, k] and B[k, n]
-  int M, K, N;
-  const float* bias;
-  const float* residual;
-  float* out;
-  float* pre;
-  int act;
-};
-
 // fp32 operands need fp32 products (tf32 keeps 10 bits of a factor), so these run on the CUDA
 // cores: a 64 x 64 tile per block of 128 threads, 8 x 4 outputs a thread (three 16-byte shared
 // loads for 32 FMAs), k in slabs of 16, the next slab's global loads in registers while this one is
@@ -185,7 +173,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   if (work.cluster > 1) cluster_sync_all();
   else __syncthreads();
   // this block's share of the tile's rows, four columns a thread
-  const bool vec = g.N % 4 == 0;
+  const bool vec = g.N % 4 == 0 && g.ldo % 4 == 0;
   const int n = n0 + tx * 4;
   for (int r = kSB * part / S + ty; r < kSB * (part + 1) / S; r += kSThreads / 16) {
     const int m = m0 + r;
@@ -202,7 +190,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
       z[2] += v.z;
       z[3] += v.w;
     }
-    const int64_t o = (int64_t)m * g.N + n;
+    const int64_t o = (int64_t)m * g.N + n, oy = g.ldo ? (int64_t)m * g.ldo + n : o;
     if (g.bias)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -214,13 +202,13 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
         if (n + j < g.N) y[j] += g.residual[o + j];
     if (vec) {
       if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
-      *reinterpret_cast<float4*>(g.out + o) = make_float4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<float4*>(g.out + oy) = make_float4(y[0], y[1], y[2], y[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (n + j < g.N) {
           if (g.pre) g.pre[o + j] = z[j];
-          g.out[o + j] = y[j];
+          g.out[oy + j] = y[j];
         }
     }
   }
@@ -428,8 +416,10 @@ __global__ void __launch_bounds__(256) k_pack_rows(const PackArgs a) {
   }
 }
 
+}  // namespace
+
 // One product or two (count) in one launch.
-cudaError_t run_f32(const SimtGemm* g, int count, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_linear_f32(const SimtGemm* g, int count, int sms, cudaStream_t st, int* launches) {
   SimtWork w;
   int64_t tiles[2] = {0, 0};
   int slabs[2] = {0, 0};
@@ -474,6 +464,8 @@ cudaError_t run_f32(const SimtGemm* g, int count, int sms, cudaStream_t st, int*
   *launches += 1;
   return cudaLaunchKernelEx(&cfg, k_linear_f32, w);
 }
+
+namespace {
 
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -525,6 +517,16 @@ struct Packed {
     return cudaSuccess;
   }
 };
+
+}  // namespace
+
+cudaError_t launch_pack_rows(const void** p, void* copy, int64_t R, int64_t C, int sms, cudaStream_t st, int* launches) {
+  Packed pk;
+  pk.add(p, copy, R, C);
+  return pk.run(sms, st, launches);
+}
+
+namespace {
 
 template <typename T>
 cudaError_t run_dz(const moe_linear_dims& d, char* ws, float* part, const void* dy, const void* pre, void* dz,
@@ -615,7 +617,7 @@ cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const vo
   int n = 0;
   if (dx) g[n++] = {f(dz), f(w), N, 1, 1, N, M, N, K, nullptr, f(dx_add), (float*)dx, nullptr, MOE_ACT_NONE};
   if (dw) g[n++] = {f(x), f(dz), 1, K, N, 1, K, M, N, nullptr, nullptr, (float*)dw, nullptr, MOE_ACT_NONE};
-  return run_f32(g, n, sms, st, launches);
+  return launch_linear_f32(g, n, sms, st, launches);
 }
 
 }  // namespace
@@ -628,7 +630,7 @@ cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x,
     return fwd_bf16(d, static_cast<char*>(ws), x, w, bias, residual, y, pre, sms, st, launches);
   SimtGemm g = {f(x), f(w), d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, f(bias), f(residual), (float*)y, (float*)pre,
                 d.act};
-  return run_f32(&g, 1, sms, st, launches);
+  return launch_linear_f32(&g, 1, sms, st, launches);
 }
 
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,

@@ -458,7 +458,12 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) st_shared_v4(ty + piece(lane, j), f_to_bf16x8(z + 8 * j));
         } else if (lane < rows) {
-          float* o = reinterpret_cast<float*>(g.y) + (row0 + lane) * g.N + n0;
+          float* o = reinterpret_cast<float*>(g.y) + (row0 + lane) * g.ldy + n0;
+          if (g.add) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i < cols) z[i] += o[i];
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if constexpr (VEC) {
@@ -474,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         if constexpr (!VEC) {
           __syncwarp();
           const int64_t o = row0 * g.N + n0;
-          if constexpr (!F32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + o, g.N, ty, rows, cols, lane);
+          if constexpr (!F32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + row0 * g.ldy + n0, g.ldy, ty, rows, cols, lane);
           if (g.pre) rows_out(reinterpret_cast<__nv_bfloat16*>(g.pre) + o, g.N, tile, rows, cols, lane);
           __syncwarp();
           if (c + 1 < c0 + cw) ready(c + 1);
@@ -529,12 +534,17 @@ struct SplitCfg {
 // the outputs are multiples of 16 bytes, so the four values are one access.
 template <bool VEC>
 __device__ __forceinline__ void emit4(const LinearGemm& g, int64_t t, int n0, float (&z)[4], const float (&res)[4]) {
-  const int64_t o = t * g.N + n0;
+  const int64_t o = t * g.N + n0, oy = t * g.ldy + n0;
   float y[4];
   if (g.out_f32) act_fwd<false, 4>(g.act, z, y);  // no rounding to bf16 covers the fast forms' errors
   else act_fwd<true, 4>(g.act, z, y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] += res[i];
+  if (g.add) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n0 + i < g.N) y[i] += reinterpret_cast<const float*>(g.y)[oy + i];
+  }
   __nv_bfloat16* pre = reinterpret_cast<__nv_bfloat16*>(g.pre) + o;
   if constexpr (VEC) {
     auto two = [](float a, float b) {
@@ -542,15 +552,15 @@ __device__ __forceinline__ void emit4(const LinearGemm& g, int64_t t, int n0, fl
       return *reinterpret_cast<const uint32_t*>(&h);
     };
     if (g.pre) *reinterpret_cast<uint2*>(pre) = make_uint2(two(z[0], z[1]), two(z[2], z[3]));
-    if (g.out_f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + o) = make_float4(y[0], y[1], y[2], y[3]);
-    else *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(g.y) + o) = make_uint2(two(y[0], y[1]), two(y[2], y[3]));
+    if (g.out_f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.y) + oy) = make_float4(y[0], y[1], y[2], y[3]);
+    else *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(g.y) + oy) = make_uint2(two(y[0], y[1]), two(y[2], y[3]));
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (n0 + i >= g.N) break;
       if (g.pre) pre[i] = __float2bfloat16_rn(z[i]);
-      if (g.out_f32) reinterpret_cast<float*>(g.y)[o + i] = y[i];
-      else reinterpret_cast<__nv_bfloat16*>(g.y)[o + i] = __float2bfloat16_rn(y[i]);
+      if (g.out_f32) reinterpret_cast<float*>(g.y)[oy + i] = y[i];
+      else reinterpret_cast<__nv_bfloat16*>(g.y)[oy + i] = __float2bfloat16_rn(y[i]);
     }
   }
 }
@@ -803,9 +813,10 @@ bool fill(TcWork<N>* w, int i, const LinearGemm& g) {
   ok = ok && (g.b_mn ? make_map(&w->B[i], g.B, g.K, g.N, g.ldb, kBK)
                      : make_map(&w->B[i], g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
   w->Y[i] = w->A[i];  // where unused
-  if (VEC && !F32) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.N, 32);
+  if (VEC && !F32) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.ldy ? g.ldy : g.N, 32);
   TcArgs& a = w->p[i];
   a.g = g;
+  if (!g.ldy) a.g.ldy = g.N;
   a.kblocks = (g.K + kBK - 1) / kBK;
   a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
   a.nt = (g.N + BN - 1) / BN;
@@ -847,7 +858,7 @@ cudaError_t launch_tile_as(const LinearGemm& g, int sms, cudaStream_t st) {
 
 template <int CTAS, int BN>
 cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
-  if (g.N % 8 == 0)
+  if (g.N % 8 == 0 && g.ldy % 8 == 0)
     return g.out_f32 ? launch_tile_as<CTAS, BN, true, true>(g, sms, st) : launch_tile_as<CTAS, BN, true, false>(g, sms, st);
   return g.out_f32 ? launch_tile_as<CTAS, BN, false, true>(g, sms, st) : launch_tile_as<CTAS, BN, false, false>(g, sms, st);
 }
@@ -879,6 +890,7 @@ cudaError_t launch_split_as(const LinearGemm& g, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   TcArgs a;
   a.g = g;
+  if (!g.ldy) a.g.ldy = g.N;
   a.kblocks = (g.K + kBK - 1) / kBK;
   a.mt = (g.M + NB - 1) / NB;
   a.nt = (g.N + 127) / 128;
@@ -891,7 +903,7 @@ cudaError_t launch_split_as(const LinearGemm& g, cudaStream_t st) {
 template <int NB>
 cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
   if (g.a_mn && NB < 64) return cudaErrorInvalidValue;
-  const bool vec = g.N % 8 == 0;
+  const bool vec = g.N % 8 == 0 && g.ldy % 8 == 0;
   switch (S) {
     case 1: return vec ? launch_split_as<NB, 1, true>(g, st) : launch_split_as<NB, 1, false>(g, st);
     case 2: return vec ? launch_split_as<NB, 2, true>(g, st) : launch_split_as<NB, 2, false>(g, st);
@@ -924,7 +936,8 @@ cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sm
     return (double)((g.M + 255) / 256) * ((g.N + 255) / 256) * ((g.K + kBK - 1) / kBK);
   };
   const double walk = (kblocks(g0) + kblocks(g1)) / (sms / 2);
-  if (pair(c0) && pair(c1) && g0.N % 8 == 0 && g1.N % 8 == 0 && walk <= 128.0) {
+  const bool rows16 = g0.N % 8 == 0 && g1.N % 8 == 0 && g0.ldy % 8 == 0 && g1.ldy % 8 == 0;
+  if (pair(c0) && pair(c1) && rows16 && !g0.out_f32 && !g1.out_f32 && walk <= 128.0) {
     *launches += 1;
     return launch_two(g0, g1, sms, st);
   }

@@ -20,6 +20,8 @@ struct LinearGemm {
   void* pre;             // [M, N] bf16 or null
   int act, out_f32;
   int* status;           // receives MOE_ERR_TIMEOUT when a wait runs out
+  int64_t ldy = 0;       // row stride of y, 0: N
+  int add = 0;           // with out_f32: added to what y holds
 };
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st);

@@ -353,6 +353,57 @@ MOE_API int moe_gate_fwd(const moe_gate_dims* dims, void* stream, const void* lo
 MOE_API int moe_gate_bwd(const moe_gate_dims* dims, void* stream, const void* logits, const int32_t* topk_idx,
                          const float* dtopk_w, void* dlogits);
 
+typedef struct moe_balance_dims {
+  int64_t T;           /* tokens, 1 <= T < 2^26 */
+  int64_t E;           /* experts, <= 1024 */
+  int64_t k;           /* experts per token, 1 <= k <= 32 */
+  int64_t S;           /* sequences, <= 2^20; 0: all T tokens are one, and seq_start is null */
+  int32_t score;       /* moe_score: p = softmax(l), or sigmoid(l) over their sum */
+  int32_t dtype;       /* moe_dtype of logits */
+  int32_t grad_dtype;  /* moe_dtype of dlogits and dlogits_add */
+  float alpha;         /* factor of the balance loss (finite) */
+  float z_coef;        /* factor of the z loss (finite); 0 with MOE_SCORE_SIGMOID */
+} moe_balance_dims;
+
+/*
+ * moe_balance_workspace_size -- bytes of workspace of moe_balance_fwd. The caller sets its first
+ * 256 bytes to zero once, when it allocates the workspace, ordered before the first call; they hold
+ * the status word (moe_read_status) and a counter that every call leaves at zero. Host-only.
+ */
+MOE_API int moe_balance_workspace_size(const moe_balance_dims* dims, size_t* bytes);
+
+/*
+ * moe_balance_fwd -- how evenly the experts are used, and the losses that training adds for it.
+ * With n_s the tokens of sequence s and N those of all sequences:
+ *   count[s,e] = times that tokens of s chose e;  prob[s,e] = mean of p[t,e] over them;
+ *   loss[0] = alpha sum_s (n_s / N) sum_e (E count[s,e] / (k n_s)) prob[s,e]   (alpha when all are even);
+ *   loss[1] = z_coef / N sum_t lse_t^2 with lse_t the logsumexp of the token's logits.
+ * Sequences may be empty (their counts and means are zero); tokens before the first and behind the
+ * last one take no part. A logit of -inf or NaN masks its expert (p = 0); a token whose logits are
+ * all masked counts with p = 0, and one whose |lse| is not below 9.2e18 (all its logits masked, by -inf
+ * or by the type's lowest value, or one of them +inf) adds nothing to the z loss.
+ * Inputs:  logits[T,E] (dims.dtype), topk_idx[T,k] int32 (an index outside [0, E) is not counted),
+ *          seq_start[S+1] int32 (null iff S == 0; ascending offsets in [0, T]; others set
+ *          MOE_ERR_DEVICE_ARG in the status word and leave the results unspecified).
+ * Outputs: loss[2] float, count[max(S,1),E] int32, prob[max(S,1),E] float (nullable).
+ * Sums run in a fixed order.
+ */
+MOE_API int moe_balance_fwd(const moe_balance_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* logits,
+                            const int32_t* topk_idx, const int32_t* seq_start, float* loss, int32_t* count, float* prob);
+
+/*
+ * moe_balance_bwd -- gradient of loss[0] + loss[1] to the logits, the counts held fixed. With
+ * c_e = alpha E count[s,e] / (k N n_s) and u = *dloss:
+ *   softmax: dlogits_e = u p_e (c_e - sum_j p_j c_j + 2 z_coef lse / N) + dlogits_add_e;
+ *   sigmoid: dlogits_e = u p_e (1 - sigmoid(l_e)) (c_e - sum_j p_j c_j) + dlogits_add_e.
+ * Tokens outside the sequences get dlogits_add alone.
+ * Inputs:  logits, seq_start as in the forward, count[max(S,1),E] of the forward, dloss[1] float
+ *          (nullable = 1), dlogits_add[T,E] (nullable: the gradient that reaches the logits by another
+ *          path, moe_gate_bwd's say; may be dlogits' buffer). Output: dlogits[T,E] (dims.grad_dtype).
+ */
+MOE_API int moe_balance_bwd(const moe_balance_dims* dims, void* stream, const void* logits, const int32_t* count,
+                            const int32_t* seq_start, const float* dloss, const void* dlogits_add, void* dlogits);
+
 /*
  * moe_fwd_routed -- moe_fwd with the caller's routing (moe_gate_fwd's, say) in place of the
  * router: pair (t, j) goes to expert topk_idx[t,j] with weight topk_w[t,j]; the rest is moe_fwd's.
@@ -424,6 +475,105 @@ MOE_API int moe_linear_fwd(const moe_linear_dims* dims, void* ws, size_t ws_byte
 MOE_API int moe_linear_bwd(const moe_linear_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* dy,
                            const void* x, const void* w, const void* pre, const void* dx_add, void* dx, void* dw,
                            void* dbias);
+
+typedef struct moe_xent_dims {
+  int64_t M;      /* rows (tokens), 1 <= M <= 2^31 - 2^20 */
+  int64_t H;      /* features, 1 <= H < 2^24; any value */
+  int64_t V;      /* vocabulary, 1 <= V < 2^24; any value */
+  int32_t dtype;  /* moe_dtype of x, w, dx, dw */
+  int32_t tied;   /* 0: w[H,V], as moe_linear_fwd's; 1: w[V,H], an embedding table */
+  float z_coef;   /* factor of lse^2 in the loss (finite) */
+} moe_xent_dims;
+
+/*
+ * moe_xent_workspace_size -- bytes of workspace of moe_xent_fwd alone (backward == 0) or of both.
+ * The caller sets its first 256 bytes to zero once, when it allocates the workspace, ordered before
+ * the first call; they hold the status word (moe_read_status) and a counter that every call leaves
+ * at zero. Its size does not grow with M V. Host-only.
+ */
+MOE_API int moe_xent_workspace_size(const moe_xent_dims* dims, int backward, size_t* bytes);
+
+/*
+ * moe_xent_fwd -- softmax cross entropy of l = x w over a vocabulary whose logits are never kept:
+ *   lse_t = log sum_v e^{l_tv};  loss_t = lse_t - l_{t,target} + z_coef lse_t^2.
+ * A negative target is not counted: its loss is 0. One of V or more sets MOE_ERR_DEVICE_ARG in the
+ * status word and is not counted either.
+ * Inputs:  x[M,H], w (dims.tied), target[M] int32.
+ * Outputs: loss[M], lse[M] float; total[2] float (nullable): the sum of the losses and how many rows
+ *          were counted. Logits are fp32 sums; all sums run in a fixed order.
+ */
+MOE_API int moe_xent_fwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x, const void* w,
+                         const int32_t* target, float* loss, float* lse, float* total);
+
+/*
+ * moe_xent_bwd -- gradients of sum_t d_t loss_t: d_t = dloss[t], or 1 / total[1] (of the mean over the
+ * counted rows) where dloss is null; 0 for rows that are not counted.
+ *   dl = d_t ((1 + 2 z_coef lse_t) e^{l - lse_t} - onehot(target_t));  dx = dl w^T;  dw = x^T dl.
+ * The logits are computed again, a piece of the vocabulary at a time. In bf16 dl is rounded to bf16
+ * for the two products; dx is summed over the pieces in fp32.
+ * Inputs:  x, w, target as in the forward, lse[M] of the forward, dloss[M] float or total[2] of the
+ *          forward. Outputs: dx[M,H], dw (dims.tied), each nullable; overwritten.
+ */
+MOE_API int moe_xent_bwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x, const void* w,
+                         const int32_t* target, const float* lse, const float* dloss, const float* total, void* dx,
+                         void* dw);
+
+/* One tensor of an optimiser step. All pointers are device pointers, 16-byte aligned (scales: 4). */
+typedef struct moe_adamw_tensor {
+  void* param;          /* [n], dtype */
+  const void* grad;     /* [n], grad_dtype */
+  float* master;        /* [n]: the weight in 32 bits, which the step reads and writes in place of param; param
+                           receives its rounding. null: param itself */
+  void* m;              /* [n]: float, or e4m3 (moe_adamw_dims.state_bits == 8) */
+  void* v;              /* [n]: float, or e4m3 of the square root */
+  float* m_scale;       /* [(n + 255) / 256]: factor of each 256 values of m; null with 32 bits */
+  float* v_scale;
+  int64_t n;            /* 0 <= n <= 2^40 */
+  int32_t dtype;        /* moe_dtype of param */
+  int32_t grad_dtype;   /* moe_dtype of grad */
+  float lr_scale;       /* factor on the step's lr (finite) */
+  float weight_decay;   /* finite */
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_dims {
+  double beta1, beta2;  /* in [0, 1) */
+  int64_t step;         /* t of the bias corrections, >= 1 for the first step */
+  float lr;             /* finite */
+  float eps;            /* >= 2^-126, finite */
+  float grad_scale;     /* factor on every gradient (finite) */
+  float max_norm;       /* gradients are scaled by min(1, max_norm / norm); <= 0: not clipped */
+  int32_t state_bits;   /* 32 or 8 */
+} moe_adamw_dims;
+
+/*
+ * moe_grad_norm_workspace_size -- bytes of workspace of moe_grad_norm for these tensors. The caller sets
+ * its first 256 bytes to zero once, when it allocates the workspace, ordered before the first call;
+ * every call leaves them at zero.
+ */
+MOE_API int moe_grad_norm_workspace_size(const moe_adamw_tensor* tensors, int64_t count, size_t* bytes);
+
+/*
+ * moe_grad_norm -- norm[0] = |grad_scale| sqrt(sum over all tensors of grad^2), in a fixed order. Squares
+ * are taken in fp32: a gradient past 1.8e19 gives inf. Reads grad, n and grad_dtype of each tensor
+ * (host array, copied by the call).
+ */
+MOE_API int moe_grad_norm(const moe_adamw_tensor* tensors, int64_t count, void* ws, size_t ws_bytes, void* stream,
+                          float grad_scale, float* norm);
+
+/*
+ * moe_adamw_step -- one AdamW step over all tensors (host array, copied by the call), in place:
+ *   g' = grad grad_scale (max_norm > 0 and norm given: min(1, max_norm / *norm));
+ *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2;
+ *   w = w - lr lr_scale (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay w).
+ * With state_bits == 8, m and sqrt(v) are rounded to e4m3 (to nearest, ties to even) after the weights have
+ * used them, over the largest magnitude / 448 (at least 2^-126) of each 256 values; a sqrt(v) above zero is stored as at least 2^-9 of its scale.
+ * norm (nullable, device): where it is inf or NaN nothing is written: no weight, no state.
+ * lr, step (nullable, device, one value each): in place of dims.lr and dims.step, so that a captured
+ * step follows a schedule.
+ * Two tensors of one call must not overlap.
+ */
+MOE_API int moe_adamw_step(const moe_adamw_dims* dims, const moe_adamw_tensor* tensors, int64_t count, void* stream,
+                           const float* norm, const float* lr, const int32_t* step);
 
 /*
  * moe_selftest_wait -- checks, on the GPU, the bounded barrier wait that every
