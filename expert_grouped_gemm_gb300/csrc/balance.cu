@@ -8,10 +8,15 @@
 // Forward: tokens are cut into chunks of equal length, a block each; a block walks the sequences that its chunk
 // meets and writes one row of sums (p, counts, lse^2) for each. Row c + s holds chunk c of sequence s: along the
 // tokens either index only grows, so no two share a row and chunks + S rows are enough. A second kernel adds a
-// sequence's rows in order, so results do not depend on timing.
+// sequence's rows in order, so results do not depend on timing; where there are few rows, the last block of the first
+// kernel does it.
+//
+// Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value): bound by what a warp does for a
+// token, not by HBM.
 #include <algorithm>
 #include <type_traits>
 
+#include "act.cuh"
 #include "block.h"
 #include "common.cuh"
 
@@ -19,7 +24,7 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;  // of a block of the backward
 
 struct BalanceArgs {
   const void* logits;
@@ -32,7 +37,8 @@ struct BalanceArgs {
   float* row_p;       // [chunks + S][E]
   int* row_n;         // [chunks + S][E]
   float* row_z;       // [chunks + S]
-  float* part;        // [S][2]: a sequence's part of the losses
+  float* part;        // [S * column blocks][2]: parts of the losses
+  int few;            // the last block of the first kernel adds the rows
   unsigned* done;
   int* status;
   float* loss;
@@ -111,7 +117,7 @@ __device__ __forceinline__ float probs(float (&l)[EPL], float* away) {
   if constexpr (SOFTMAX) {
     if (fabsf(m) < INFINITY) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) sum += l[i] = expf(l[i] - m);
+      for (int i = 0; i < EPL; ++i) sum += l[i] = ex2_approx((l[i] - m) * kLog2e);
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) sum += l[i] = l[i] == INFINITY ? 1.0f : 0.0f;
@@ -120,9 +126,11 @@ __device__ __forceinline__ float probs(float (&l)[EPL], float* away) {
     const float low = m > -INFINITY ? fminf(m, 0.0f) : 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const float e = expf(-fabsf(l[i])), r = 1.0f / (1.0f + e);  // sigma(|l|)
+      float e = ex2_approx(-kLog2e * fabsf(l[i]));
+      const float r = rcp_approx(1.0f + e);  // sigma(|l|)
       if (away) away[i] = l[i] > 0.0f ? e * r : r;
-      l[i] = l[i] > 0.0f ? r : expf(l[i] - low) * r;
+      if (low < 0.0f) e = ex2_approx((l[i] - low) * kLog2e);  // the whole row is below zero
+      l[i] = l[i] > 0.0f ? r : e * r;
       sum += l[i];
     }
   }
@@ -130,126 +138,182 @@ __device__ __forceinline__ float probs(float (&l)[EPL], float* away) {
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) l[i] *= inv;
-  return m + logf(sum);
+  return SOFTMAX ? m + logf(sum) : 0.0f;
 }
 
-template <int EPL, bool SOFTMAX, typename TL>
-__global__ void __launch_bounds__(kWarps * 32) k_balance_fwd(const BalanceArgs a) {
-  extern __shared__ float shared[];  // [E] sums of p, [E] counts
-  int* hist = reinterpret_cast<int*>(shared + a.E);
-  __shared__ float zsum[kWarps];
+// The rows of sequence s added for experts e0 .. e0 + 31, a column a lane and a warp every warps-th row. Returns the
+// columns' sum of count prob (warp 0).
+template <int WARPS>
+__device__ __forceinline__ float sum_columns(const BalanceArgs& a, int s, int e0, float (*sp)[33], int (*sn)[33]) {
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, e = e0 + cx;
+  const int t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
+  const int r0 = t0 < t1 ? t0 / a.chunk + s : 0, r1 = t0 < t1 ? (t1 - 1) / a.chunk + s + 1 : 0;
+  float p = 0.0f, dot = 0.0f;
+  int c = 0;
+  if (e < a.E) {
+#pragma unroll 4
+    for (int r = r0 + ry; r < r1; r += WARPS) {
+      p += __ldcg(a.row_p + (int64_t)r * a.E + e);
+      c += __ldcg(a.row_n + (int64_t)r * a.E + e);
+    }
+  }
+  sp[ry][cx] = p;
+  sn[ry][cx] = c;
+  __syncthreads();
+  if (ry == 0) {
+    if (e < a.E) {
+#pragma unroll
+      for (int r = 1; r < WARPS; ++r) {
+        p += sp[r][cx];
+        c += sn[r][cx];
+      }
+      p /= (float)max(t1 - t0, 1);
+      a.count[(int64_t)s * a.E + e] = c;
+      if (a.prob) a.prob[(int64_t)s * a.E + e] = p;
+      dot = (float)c * p;
+    }
+    dot = warp_sum(dot);
+  }
+  __syncthreads();
+  return dot;
+}
+
+// Warp 0: the sum of lse^2 over the rows of sequence s.
+__device__ __forceinline__ float sum_z(const BalanceArgs& a, int s) {
+  const int t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
+  float z = 0.0f;
+  if (t0 < t1)
+    for (int r = t0 / a.chunk + s + (int)threadIdx.x; r <= (t1 - 1) / a.chunk + s; r += 32) z += __ldcg(a.row_z + r);
+  return warp_sum(z);
+}
+
+__device__ __forceinline__ void check_seq(const BalanceArgs& a, int s) {
+  if (a.start && threadIdx.x == 0 && (a.start[s] > a.start[s + 1] || a.start[s] < 0 || a.start[s + 1] > a.T))
+    set_status(a.status, MOE_ERR_DEVICE_ARG);
+}
+
+__device__ __forceinline__ void store_losses(const BalanceArgs& a, float dot, float z) {
+  const float N = tokens_of_all(a);
+  a.loss[0] = dot * (a.alpha * ((float)a.E / (float)a.k) / N);
+  a.loss[1] = z * (a.z / N);
+}
+
+// Whether this is the last block of the grid; what the others wrote before is visible to it.
+__device__ __forceinline__ bool last_block(unsigned* done) {
+  __shared__ bool last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
+    if (last) *done = 0;
+  }
+  __syncthreads();
+  __threadfence();
+  return last;
+}
+
+template <int EPL, bool SOFTMAX, typename TL, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a) {
+  extern __shared__ float shared[];  // [WARPS][E] sums of p, [E] counts
+  int* hist = reinterpret_cast<int*>(shared + WARPS * a.E);
+  __shared__ float zsum[WARPS];
+  __shared__ float sp[WARPS][33];
+  __shared__ int sn[WARPS][33];
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
   const int c0 = (int)blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.T);
+  const TL* logits = reinterpret_cast<const TL*>(a.logits) + e0;
   for (int s = seq_of(a, c0); s < a.S; ++s) {
     const int b0 = max(c0, seq_at(a, s)), b1 = min(c1, seq_at(a, s + 1));
     if (seq_at(a, s) >= c1) break;
     if (b0 >= b1) continue;
-    for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
-      shared[i] = 0.0f;
-      hist[i] = 0;
-    }
-    float acc[EPL], z = 0.0f;
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
+    float acc[EPL], z = 0.0f, next[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-    for (int t = b0 + warp; t < b1; t += kWarps) {
+    if (b0 + warp < b1) load_row<EPL>(logits + (int64_t)(b0 + warp) * a.E, n, a.vec, next);
+    for (int t = b0 + warp; t < b1; t += WARPS) {
       float l[EPL];
-      load_row<EPL>(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E + e0, n, a.vec, l);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) l[i] = next[i];
+      if (t + WARPS < b1) load_row<EPL>(logits + (int64_t)(t + WARPS) * a.E, n, a.vec, next);
       const float lse = probs<EPL, SOFTMAX>(l, nullptr);
       if (SOFTMAX && has_lse(lse)) z += lse * lse;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) acc[i] += l[i];
     }
     if (lane == 0) zsum[warp] = z;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (i < n) shared[warp * a.E + e0 + i] = acc[i];
     __syncthreads();
     const int64_t i1 = (int64_t)b1 * a.k;
     for (int64_t i = (int64_t)b0 * a.k + threadIdx.x; i < i1; i += blockDim.x) {
       const int e = a.idx[i];
       if ((unsigned)e < (unsigned)a.E) atomicAdd(&hist[e], 1);
     }
-    for (int w = 0; w < kWarps; ++w) {  // the warps' sums in order
-      if (w == warp)
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (i < n) shared[e0 + i] += acc[i];
-      __syncthreads();
-    }
+    __syncthreads();
     const int64_t row = (int64_t)blockIdx.x + s;
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
-      a.row_p[row * a.E + i] = shared[i];
+      float v = shared[i];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) v += shared[w * a.E + i];
+      a.row_p[row * a.E + i] = v;
       a.row_n[row * a.E + i] = hist[i];
     }
     if (threadIdx.x == 0) {
       float v = 0.0f;
-      for (int w = 0; w < kWarps; ++w) v += zsum[w];
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) v += zsum[w];
       a.row_z[row] = v;
     }
     __syncthreads();
   }
+  if (!a.few || !last_block(a.done)) return;
+  float dot = 0.0f, z = 0.0f;
+  for (int s = 0; s < a.S; ++s) {
+    check_seq(a, s);
+    for (int e = 0; e < a.E; e += 32) dot += sum_columns<WARPS>(a, s, e, sp, sn);
+    if (warp == 0) z += sum_z(a, s);
+  }
+  if (threadIdx.x == 0) store_losses(a, dot, z);
 }
 
-// A block a sequence: its rows added, then its part of the losses; the last block adds the parts in order.
-__global__ void __launch_bounds__(1024) k_balance_sum(const BalanceArgs a) {
-  __shared__ float red[32];
-  __shared__ float sp[32][33];
-  __shared__ int sn[32][33];
-  __shared__ bool last;
+// A block 32 experts of a sequence: its rows added; the last block adds the parts of the losses in a fixed order.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) k_balance_sum(const BalanceArgs a) {
+  __shared__ float sp[kSumWarps][33];
+  __shared__ int sn[kSumWarps][33];
+  __shared__ float2 red[kSumWarps];
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  const int s = (int)blockIdx.x, cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
-  if (a.start && threadIdx.x == 0 && (a.start[s] > a.start[s + 1] || a.start[s] < 0 || a.start[s + 1] > a.T))
-    set_status(a.status, MOE_ERR_DEVICE_ARG);
-  const int r0 = t0 < t1 ? t0 / a.chunk + s : 0, r1 = t0 < t1 ? (t1 - 1) / a.chunk + s + 1 : 0;
-  const float n = (float)max(t1 - t0, 1), N = tokens_of_all(a);
-  float dot = 0.0f;
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    const int e = e0 + cx;
-    float p = 0.0f;
-    int c = 0;
-    if (e < a.E)
-      for (int r = r0 + ry; r < r1; r += 32) {
-        p += a.row_p[(int64_t)r * a.E + e];
-        c += a.row_n[(int64_t)r * a.E + e];
-      }
-    sp[ry][cx] = p;
-    sn[ry][cx] = c;
-    __syncthreads();
-    if (ry == 0 && e < a.E) {
-#pragma unroll
-      for (int r = 1; r < 32; ++r) {
-        p += sp[r][cx];
-        c += sn[r][cx];
-      }
-      p /= n;
-      a.count[(int64_t)s * a.E + e] = c;
-      if (a.prob) a.prob[(int64_t)s * a.E + e] = p;
-      dot += (float)c * p;
+  const int s = (int)blockIdx.x, at = s * (int)gridDim.y + (int)blockIdx.y;
+  if (blockIdx.y == 0) check_seq(a, s);
+  const float dot = sum_columns<kSumWarps>(a, s, (int)blockIdx.y * 32, sp, sn);
+  if (threadIdx.x < 32) {
+    const float z = blockIdx.y == 0 ? sum_z(a, s) : 0.0f;
+    if (threadIdx.x == 0) {
+      a.part[2 * at] = dot;
+      a.part[2 * at + 1] = z;
     }
-    __syncthreads();
   }
-  float z = 0.0f;
-  for (int r = r0 + (int)threadIdx.x; r < r1; r += blockDim.x) z += a.row_z[r];
-  z = warp_sum(z);
-  if (cx == 0) red[ry] = z;
-  if (ry == 0) dot = warp_sum(dot);
+  if (!last_block(a.done)) return;
+  float2 v = make_float2(0.0f, 0.0f);
+  for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += kSumWarps * 32) {
+    v.x += __ldcg(a.part + 2 * i);
+    v.y += __ldcg(a.part + 2 * i + 1);
+  }
+  v.x = warp_sum(v.x);
+  v.y = warp_sum(v.y);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int r = 1; r < 32; ++r) z += red[r];
-    a.part[2 * s] = dot;
-    a.part[2 * s + 1] = z;
-    __threadfence();
-    last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+    for (int w = 1; w < kSumWarps; ++w) {
+      v.x += red[w].x;
+      v.y += red[w].y;
+    }
+    store_losses(a, v.x, v.y);
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  if (threadIdx.x < 2) {
-    float v = 0.0f;
-    for (int i = 0; i < a.S; ++i) v += __ldcg(a.part + 2 * i + threadIdx.x);
-    a.loss[threadIdx.x] = v * (threadIdx.x == 0 ? a.alpha * (float)a.E / (float)a.k : a.z) / N;
-  }
-  if (threadIdx.x == 0) *a.done = 0;
 }
 
 // A warp a token.
@@ -315,18 +379,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
 
 // ---------------------------------------------------------------- host side
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-constexpr int kChunkBlocks = 304;  // chunks to aim for: two for each of 152 SMs
+constexpr int kChunkBlocks = 152;  // chunks to aim for: one for each SM
+constexpr int kFewRows = 16;       // as many rows the last block adds by itself
 
-// Tokens of a chunk: enough chunks for every SM, at least a token for each warp.
-int chunk_tokens(int64_t T) {
-  return (int)std::max<int64_t>(kWarps, (T + kChunkBlocks - 1) / kChunkBlocks);
+// Warps of a forward block: as many as hold their sums in 32 KB.
+int fwd_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
+// Tokens of a chunk: a token for each warp, and no more chunks than SMs.
+int chunk_tokens(const moe_balance_dims& d) {
+  return (int)std::max<int64_t>(fwd_warps(d.E), (d.T + kChunkBlocks - 1) / kChunkBlocks);
 }
 
 struct BalanceWs {
   size_t p, n, z, part, total;
 };
 BalanceWs layout(const moe_balance_dims& d) {
-  const size_t c = chunk_tokens(d.T), S = (size_t)std::max<int64_t>(d.S, 1), rows = ((size_t)d.T + c - 1) / c + S;
+  const size_t c = chunk_tokens(d), S = (size_t)std::max<int64_t>(d.S, 1), rows = ((size_t)d.T + c - 1) / c + S;
   BalanceWs L;
   size_t o = kBalanceHeader;
   L.p = o;
@@ -336,7 +403,7 @@ BalanceWs layout(const moe_balance_dims& d) {
   L.z = o;
   o += up256(rows * 4);
   L.part = o;
-  o += up256(S * 8);
+  o += up256(S * ((d.E + 31) / 32) * 8);
   L.total = o;
   return L;
 }
@@ -382,12 +449,15 @@ cudaError_t bwd_typed(const moe_balance_dims& d, const BalanceArgs& a, cudaStrea
   return cudaSuccess;
 }
 
+template <int EPL, bool SOFTMAX, typename TL>
+cudaError_t fwd_launch(const BalanceArgs& a, cudaStream_t st) {
+  constexpr int W = EPL <= 8 ? 32 : EPL <= 16 ? 16 : 8;  // fwd_warps of every E that comes here
+  MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, TL, W>, a.chunks, W * 32, (size_t)a.E * 4 * (W + 1), st, a);
+  return cudaSuccess;
+}
 template <int EPL, bool SOFTMAX>
 cudaError_t fwd_typed(const moe_balance_dims& d, const BalanceArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)a.E * 8;
-  if (d.dtype == MOE_BF16) MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, __nv_bfloat16>, a.chunks, kWarps * 32, smem, st, a);
-  else MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, float>, a.chunks, kWarps * 32, smem, st, a);
-  return cudaSuccess;
+  return d.dtype == MOE_BF16 ? fwd_launch<EPL, SOFTMAX, __nv_bfloat16>(a, st) : fwd_launch<EPL, SOFTMAX, float>(a, st);
 }
 
 }  // namespace
@@ -401,7 +471,7 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
   const BalanceWs L = layout(d);
   char* w = static_cast<char*>(ws);
   a.idx = topk_idx;
-  a.chunk = chunk_tokens(d.T);
+  a.chunk = chunk_tokens(d);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
   a.row_p = reinterpret_cast<float*>(w + L.p);
   a.row_n = reinterpret_cast<int*>(w + L.n);
@@ -412,13 +482,14 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
   a.loss = loss;
   a.count = count;
   a.prob = prob;
-  *launches += 2;
+  a.few = a.chunks + a.S <= kFewRows;
+  *launches += a.few ? 1 : 2;
   const cudaError_t e = with_epl(a.R, [&](auto epl) {
     constexpr int EPL = decltype(epl)::value;
     return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true>(d, a, st) : fwd_typed<EPL, false>(d, a, st);
   });
-  if (e != cudaSuccess) return e;
-  MOE_LAUNCH(k_balance_sum, a.S, 1024, 0, st, a);
+  if (e != cudaSuccess || a.few) return e;
+  MOE_LAUNCH(k_balance_sum, dim3((unsigned)a.S, (unsigned)((a.E + 31) / 32)), kSumWarps * 32, 0, st, a);
   return cudaSuccess;
 }
 

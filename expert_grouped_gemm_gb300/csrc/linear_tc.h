@@ -24,6 +24,22 @@ struct LinearGemm {
   int add = 0;           // with out_f32: added to what y holds
 };
 
+// What the epilogues of the cross entropy read and write beside a product l[M, N] of logits, columns v0 .. v0 + N - 1 of
+// a vocabulary of V.
+struct XentEpi {
+  float2* part;         // statistics: [slots][M]
+  const int* target;    // gradient: as in XentRows of xent.cu
+  const float* lse;
+  const float* dloss;
+  const float* total;
+  float z;
+  int v0, V;
+};
+// The rows' statistics, one slot for *width columns; nothing else is written.
+cudaError_t launch_xent_stats(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width);
+// y[M, N] (bf16, rows of a multiple of 8) = gradient of the loss to the logits.
+cudaError_t launch_xent_grad(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st);
+
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st);
 // Two independent products (neither reads what the other writes), in one launch where both are large.
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches);

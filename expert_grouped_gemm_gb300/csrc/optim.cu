@@ -60,85 +60,67 @@ __device__ __forceinline__ uint32_t tensor_of(const Table<N>& t, uint32_t chunk,
   return lo;
 }
 
-// Four values from element i of an array of n (bf16 or float), zeros past its end.
-__device__ __forceinline__ void load4(const void* a, bool bf, int64_t i, int64_t n, float (&f)[4]) {
-  if (bf) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a) + i;
-    if (i + 4 <= n) {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
-      f[0] = __uint_as_float(u.x << 16);
-      f[1] = __uint_as_float(u.x & 0xffff0000u);
-      f[2] = __uint_as_float(u.y << 16);
-      f[3] = __uint_as_float(u.y & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = i + j < n ? __bfloat162float(p[j]) : 0.0f;
-    }
-  } else {
-    const float* p = static_cast<const float*>(a) + i;
-    if (i + 4 <= n) {
-      const float4 u = __ldcs(reinterpret_cast<const float4*>(p));
-      f[0] = u.x;
-      f[1] = u.y;
-      f[2] = u.z;
-      f[3] = u.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = i + j < n ? p[j] : 0.0f;
-    }
+// Four neighbouring values: as they lie in memory, and as floats.
+template <bool BF>
+struct Four;
+template <>
+struct Four<true> {
+  uint2 u;
+  __device__ __forceinline__ void load(const void* a, int64_t i) {
+    u = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a) + i));
   }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(u.x << 16);
+    f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16);
+    f[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(void* a, int64_t i, const float (&f)[4]) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
+    __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a) + i),
+           make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y)));
+  }
+};
+template <>
+struct Four<false> {
+  float4 u;
+  __device__ __forceinline__ void load(const void* a, int64_t i) {
+    u = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(a) + i));
+  }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = u.x;
+    f[1] = u.y;
+    f[2] = u.z;
+    f[3] = u.w;
+  }
+  static __device__ __forceinline__ void store(void* a, int64_t i, const float (&f)[4]) {
+    __stcs(reinterpret_cast<float4*>(static_cast<float*>(a) + i), make_float4(f[0], f[1], f[2], f[3]));
+  }
+};
+
+// The same at the end of an array of n, value by value; zeros past it.
+__device__ __forceinline__ void load_tail(const void* a, bool bf, int64_t i, int64_t n, float (&f)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    f[j] = i + j >= n ? 0.0f : bf ? __bfloat162float(static_cast<const __nv_bfloat16*>(a)[i + j]) : static_cast<const float*>(a)[i + j];
 }
-__device__ __forceinline__ void store4(void* a, bool bf, int64_t i, int64_t n, const float (&f)[4]) {
-  if (bf) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a) + i;
-    if (i + 4 <= n) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-      __stcs(reinterpret_cast<uint2*>(p),
-             make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y)));
-    } else {
+__device__ __forceinline__ void store_tail(void* a, bool bf, int64_t i, int64_t n, const float (&f)[4]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < n) p[j] = __float2bfloat16_rn(f[j]);
-    }
-  } else {
-    float* p = static_cast<float*>(a) + i;
-    if (i + 4 <= n) {
-      __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < n) p[j] = f[j];
-    }
+  for (int j = 0; j < 4; ++j) {
+    if (i + j >= n) break;
+    if (bf) static_cast<__nv_bfloat16*>(a)[i + j] = __float2bfloat16_rn(f[j]);
+    else static_cast<float*>(a)[i + j] = f[j];
   }
 }
 
-// Four e4m3 codes and their values.
-__device__ __forceinline__ uint32_t load_codes(const void* a, int64_t i, int64_t n) {
-  const uint8_t* p = static_cast<const uint8_t*>(a) + i;
-  if (i + 4 <= n) return __ldcs(reinterpret_cast<const uint32_t*>(p));
-  uint32_t u = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (i + j < n) u |= (uint32_t)p[j] << (8 * j);
-  return u;
-}
-__device__ __forceinline__ void store_codes(void* a, int64_t i, int64_t n, uint32_t u) {
-  uint8_t* p = static_cast<uint8_t*>(a) + i;
-  if (i + 4 <= n) {
-    __stcs(reinterpret_cast<uint32_t*>(p), u);
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (i + j < n) p[j] = (uint8_t)(u >> (8 * j));
-}
-__device__ __forceinline__ void decode4(uint32_t u, float scale, float (&f)[4]) {
+// Four e4m3 codes: their values, and the codes of four values.
+__device__ __forceinline__ void decode4(uint32_t u, float (&f)[4]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u >> (16 * h)), __NV_E4M3);
     const float2 t = __half22float2(__half2(r));
-    f[2 * h] = t.x * scale;
-    f[2 * h + 1] = t.y * scale;
+    f[2 * h] = t.x;
+    f[2 * h + 1] = t.y;
   }
 }
 __device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
@@ -150,31 +132,24 @@ __device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
 // The scale of a block's values: the warp's largest finite magnitude / 448, at least the smallest normal float.
 // A value that is not finite becomes NaN.
 __device__ __forceinline__ float block_scale(float (&x)[2][4]) {
-  uint32_t big = 0;
+  float big = 0.0f;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) big = max(big, __float_as_uint(x[h][j]) & 0x7fffffffu);
-  big = __reduce_max_sync(0xffffffffu, big);
-  if (big >= 0x7f800000u) {
-    big = 0;
+    for (int j = 0; j < 4; ++j) big = fmaxf(big, fabsf(x[h][j]));  // passes over NaN
+  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+  if (most == 0x7f800000u) {
+    big = 0.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t u = __float_as_uint(x[h][j]) & 0x7fffffffu;
-        if (u >= 0x7f800000u) x[h][j] = __uint_as_float(0x7fffffffu);
-        else big = max(big, u);
+        if (fabsf(x[h][j]) < INFINITY) big = fmaxf(big, fabsf(x[h][j]));
+        else x[h][j] = __uint_as_float(0x7fffffffu);
       }
-    big = __reduce_max_sync(0xffffffffu, big);
+    most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
   }
-  return fmaxf(__uint_as_float(big) * (1.0f / 448.0f), 1.17549435e-38f);
-}
-
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  return fmaxf(__uint_as_float(most) * (1.0f / 448.0f), 1.17549435e-38f);
 }
 
 struct AdamWArgs {
@@ -185,6 +160,167 @@ struct AdamWArgs {
   const float* lr_at;
   const int* step_at;
 };
+
+// What the values of a tensor share in a step.
+struct Factors {
+  float b1, c1, b2, c2, bc2, eps;  // c1, c2: times the gradients' factor and its square
+  float keep, move;                // w = keep w - move m / (r bc2 + eps)
+};
+
+// The step of four values of a block; with 8 bits m and v hold codes' values, sm and sv what they are multiples of, and
+// v receives r = sqrt(v). Roots of v below 2^-126 are zero.
+template <int BITS>
+__device__ __forceinline__ void update4(const Factors& k, float sm, float sv, const float (&g)[4], float (&p)[4],
+                                        float (&m)[4], float (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = fmaf(BITS == 8 ? k.b1 * sm : k.b1, m[j], k.c1 * g[j]);
+    const float gg = k.c2 * g[j];
+    const float old = BITS == 8 ? v[j] * sv : 0.0f;
+    const float vn = BITS == 8 ? fmaf(k.b2 * old, old, gg * gg) : fmaf(k.b2, v[j], gg * gg);
+    float r;
+    if constexpr (BITS == 8) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(vn));
+    else asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(vn));
+    v[j] = BITS == 8 ? r : vn;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r, k.bc2, k.eps)));
+    p[j] = fmaf(k.keep, p[j], -(k.move * m[j]) * inv);
+  }
+}
+
+// m and r of a block as codes over new scales.
+__device__ __forceinline__ void pack_block(const Entry& e, int64_t blk, int lane, float (&m)[2][4], float (&r)[2][4],
+                                           uint32_t (&mc)[2], uint32_t (&rc)[2]) {
+  const float ms = block_scale(m), rs = block_scale(r), mi = 1.0f / ms, ri = 1.0f / rs;
+  if (lane == 0) {
+    e.ms[blk] = ms;
+    e.vs[blk] = rs;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[4], y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = m[h][j] * mi;
+      y[j] = r[h][j] * ri;
+      if (r[h][j] > 0.0f) y[j] = fmaxf(y[j], 0.001953125f);  // 2^-9, the smallest e4m3
+    }
+    mc[h] = encode4(x);
+    rc[h] = encode4(y);
+  }
+}
+
+// Whole blocks blk, blk + kWarps, ... (`steps` of them) of a tensor: every load is sent for before the first is used.
+template <int BITS, bool PB, bool GB, bool MASTER>
+__device__ __forceinline__ void whole_blocks(const Entry& e, const Factors& k, int64_t blk, int lane) {
+  Four<GB> g[kSteps][2];
+  Four<MASTER ? false : PB> p[kSteps][2];
+  Four<false> m[BITS == 32 ? kSteps : 1][2], v[BITS == 32 ? kSteps : 1][2];
+  uint32_t mc[BITS == 8 ? kSteps : 1][2], vc[BITS == 8 ? kSteps : 1][2];
+  float sm[kSteps], sv[kSteps];
+  const void* w = MASTER ? e.master : e.p;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t b = blk + s * kWarps, i = b * kBlock + lane * 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      g[s][h].load(e.g, i + h * 128);
+      p[s][h].load(w, i + h * 128);
+      if constexpr (BITS == 32) {
+        m[s][h].load(e.m, i + h * 128);
+        v[s][h].load(e.v, i + h * 128);
+      } else {
+        mc[s][h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.m) + i + h * 128));
+        vc[s][h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.v) + i + h * 128));
+      }
+    }
+    sm[s] = BITS == 8 ? e.ms[b] : 1.0f;
+    sv[s] = BITS == 8 ? e.vs[b] : 1.0f;
+  }
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t b = blk + s * kWarps, i = b * kBlock + lane * 4;
+    float mf[2][4], vf[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float gf[4], pf[4];
+      g[s][h].get(gf);
+      p[s][h].get(pf);
+      if constexpr (BITS == 32) {
+        m[s][h].get(mf[h]);
+        v[s][h].get(vf[h]);
+      } else {
+        decode4(mc[s][h], mf[h]);
+        decode4(vc[s][h], vf[h]);
+      }
+      update4<BITS>(k, sm[s], sv[s], gf, pf, mf[h], vf[h]);
+      if constexpr (MASTER) Four<false>::store(e.master, i + h * 128, pf);
+      Four<PB>::store(e.p, i + h * 128, pf);
+      if constexpr (BITS == 32) {
+        Four<false>::store(e.m, i + h * 128, mf[h]);
+        Four<false>::store(e.v, i + h * 128, vf[h]);
+      }
+    }
+    if constexpr (BITS == 8) {
+      uint32_t mo[2], vo[2];
+      pack_block(e, b, lane, mf, vf, mo, vo);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + i + h * 128), mo[h]);
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + i + h * 128), vo[h]);
+      }
+    }
+  }
+}
+
+// A block that may end inside.
+template <int BITS>
+__device__ __noinline__ void last_block(const Entry& e, const Factors& k, int64_t blk, int lane) {
+  const bool pb = e.types & 1, gb = e.types & 2;
+  const int64_t i = blk * kBlock + lane * 4, n = e.n;
+  float mf[2][4], vf[2][4];
+  for (int h = 0; h < 2; ++h) {
+    const int64_t at = i + h * 128;
+    float gf[4], pf[4];
+    load_tail(e.g, gb, at, n, gf);
+    if (e.master) load_tail(e.master, false, at, n, pf);
+    else load_tail(e.p, pb, at, n, pf);
+    float sm = 1.0f, sv = 1.0f;
+    if constexpr (BITS == 32) {
+      load_tail(e.m, false, at, n, mf[h]);
+      load_tail(e.v, false, at, n, vf[h]);
+    } else {
+      uint32_t mc = 0, vc = 0;
+      for (int j = 0; j < 4; ++j)
+        if (at + j < n) {
+          mc |= (uint32_t)static_cast<const uint8_t*>(e.m)[at + j] << (8 * j);
+          vc |= (uint32_t)static_cast<const uint8_t*>(e.v)[at + j] << (8 * j);
+        }
+      decode4(mc, mf[h]);
+      decode4(vc, vf[h]);
+      sm = e.ms[blk];
+      sv = e.vs[blk];
+    }
+    update4<BITS>(k, sm, sv, gf, pf, mf[h], vf[h]);
+    if (e.master) store_tail(e.master, false, at, n, pf);
+    store_tail(e.p, pb, at, n, pf);
+    if constexpr (BITS == 32) {
+      store_tail(e.m, false, at, n, mf[h]);
+      store_tail(e.v, false, at, n, vf[h]);
+    }
+  }
+  if constexpr (BITS == 8) {
+    uint32_t mo[2], vo[2];
+    __syncwarp();  // every lane has read the block's scales
+    pack_block(e, blk, lane, mf, vf, mo, vo);
+    for (int h = 0; h < 2; ++h)
+      for (int j = 0; j < 4; ++j)
+        if (i + h * 128 + j < n) {
+          static_cast<uint8_t*>(e.m)[i + h * 128 + j] = (uint8_t)(mo[h] >> (8 * j));
+          static_cast<uint8_t*>(e.v)[i + h * 128 + j] = (uint8_t)(vo[h] >> (8 * j));
+        }
+  }
+}
 
 template <int BITS, int N>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Table<N> tab, const AdamWArgs a) {
@@ -197,84 +333,44 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
   }
   if (a.lr_at) lr = *a.lr_at;
   if (a.step_at) {
-    const float t = (float)*a.step_at;
+    const float t = fmaxf((float)*a.step_at, 1.0f);
     bc1 = -1.0f / expm1f(t * a.ln_b1);
     bc2 = rsqrtf(-expm1f(t * a.ln_b2));
   }
+  Factors k = {a.b1, a.c1 * gs, a.b2, sqrtf(a.c2) * gs, bc2, a.eps, 0.0f, 0.0f};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t at = 0;
   for (uint32_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
     at = tensor_of(tab, chunk, at);
     const Entry& e = tab.e[at];
-    const bool pb = e.types & 1, gb = e.types & 2;
-    const float elr = lr * e.lr_scale, wd = e.wd;
-#pragma unroll
-    for (int step = 0; step < kSteps; ++step) {
-      const int64_t blk = (int64_t)(chunk - e.first) * (kWarps * kSteps) + step * kWarps + warp;
-      const int64_t i0 = blk * kBlock + lane * 4, n = e.n;
-      if (blk * kBlock >= n) break;
-      float p[2][4], g[2][4], m[2][4], v[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t i = i0 + h * 128;
-        load4(e.g, gb, i, n, g[h]);
-        if (e.master) load4(e.master, false, i, n, p[h]);
-        else load4(e.p, pb, i, n, p[h]);
-        if constexpr (BITS == 32) {
-          load4(e.m, false, i, n, m[h]);
-          load4(e.v, false, i, n, v[h]);
-        } else {
-          decode4(load_codes(e.m, i, n), e.ms[blk], m[h]);
-          decode4(load_codes(e.v, i, n), e.vs[blk], v[h]);
-        }
+    const float elr = lr * e.lr_scale;
+    k.keep = 1.0f - elr * e.wd;
+    k.move = elr * bc1;
+    const int64_t blk0 = (int64_t)(chunk - e.first) * (kWarps * kSteps), blk = blk0 + warp;
+    if ((blk0 + kWarps * kSteps) * kBlock <= e.n) {
+      if (e.master) {
+        if (e.types & 2) whole_blocks<BITS, true, true, true>(e, k, blk, lane);
+        else whole_blocks<BITS, true, false, true>(e, k, blk, lane);
+      } else if (e.types & 1) {
+        if (e.types & 2) whole_blocks<BITS, true, true, false>(e, k, blk, lane);
+        else whole_blocks<BITS, true, false, false>(e, k, blk, lane);
+      } else {
+        if (e.types & 2) whole_blocks<BITS, false, true, false>(e, k, blk, lane);
+        else whole_blocks<BITS, false, false, false>(e, k, blk, lane);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float gg = g[h][j] * gs;
-          const float vo = BITS == 8 ? v[h][j] * v[h][j] : v[h][j];
-          m[h][j] = a.b1 * m[h][j] + a.c1 * gg;
-          const float vn = a.b2 * vo + a.c2 * (gg * gg);
-          const float r = sqrt_approx(vn);
-          v[h][j] = BITS == 8 ? r : vn;
-          p[h][j] -= elr * (__fdividef(m[h][j] * bc1, r * bc2 + a.eps) + wd * p[h][j]);
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t i = i0 + h * 128;
-        if (e.master) store4(e.master, false, i, n, p[h]);
-        store4(e.p, pb, i, n, p[h]);
-        if constexpr (BITS == 32) {
-          store4(e.m, false, i, n, m[h]);
-          store4(e.v, false, i, n, v[h]);
-        }
-      }
-      if constexpr (BITS == 8) {
-        const float ms = block_scale(m), vs = block_scale(v), mi = 1.0f / ms, vi = 1.0f / vs;
-        if (lane == 0) {
-          e.ms[blk] = ms;
-          e.vs[blk] = vs;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x[4], y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = m[h][j] * mi;
-            y[j] = v[h][j] * vi;
-            if (v[h][j] > 0.0f && y[j] < 0.001953125f) y[j] = 0.001953125f;  // 2^-9, the smallest e4m3
-          }
-          store_codes(e.m, i0 + h * 128, n, encode4(x));
-          store_codes(e.v, i0 + h * 128, n, encode4(y));
-        }
-      }
+    } else {
+      for (int s = 0; s < kSteps; ++s)
+        if ((blk + s * kWarps) * kBlock < e.n) last_block<BITS>(e, k, blk + s * kWarps, lane);
     }
   }
 }
 
 // ---------------------------------------------------------------- norm
-constexpr int kNormChunk = kThreads * 32;  // values: four 16-byte loads a thread in bf16
+constexpr int kNormChunk = kThreads * 32;  // values: four 16-byte loads a thread in bf16, in flight together
+
+__device__ __forceinline__ float squares(const float (&f)[4]) {
+  return (f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3]);
+}
 
 // A block's sum of squares over its chunks; the last block of the last launch adds the blocks' in order.
 template <int N>
@@ -291,12 +387,40 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
     at = tensor_of(tab, chunk, at);
     const Entry& e = tab.e[at];
     const bool gb = e.types & 2;
-    const int64_t i0 = (int64_t)(chunk - e.first) * kNormChunk + threadIdx.x * 4;
-    float f[8][4];
+    const int64_t i0 = (int64_t)(chunk - e.first) * kNormChunk;
+    if (i0 + kNormChunk <= e.n) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(e.g) + i0 * (gb ? 2 : 4)) + threadIdx.x;
+      if (gb) {
+        uint4 u[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) load4(e.g, gb, i0 + u * kThreads * 4, e.n, f[u]);
+        for (int j = 0; j < 4; ++j) u[j] = __ldcs(p + j * kThreads);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) sum += (f[u][0] * f[u][0] + f[u][1] * f[u][1]) + (f[u][2] * f[u][2] + f[u][3] * f[u][3]);
+        for (int j = 0; j < 4; ++j) {
+          float f[8];
+          bf16x8_to_f(u[j], f);
+          sum += ((f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3])) +
+                 ((f[4] * f[4] + f[5] * f[5]) + (f[6] * f[6] + f[7] * f[7]));
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          uint4 u[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = __ldcs(p + (r * 4 + j) * kThreads);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f[4] = {__uint_as_float(u[j].x), __uint_as_float(u[j].y), __uint_as_float(u[j].z), __uint_as_float(u[j].w)};
+            sum += squares(f);
+          }
+        }
+      }
+    } else {
+      for (int64_t i = i0 + threadIdx.x * 4; i < e.n; i += kThreads * 4) {
+        float f[4];
+        load_tail(e.g, gb, i, e.n, f);
+        sum += squares(f);
+      }
+    }
   }
   sum = warp_sum(sum);
   if (lane == 0) red[warp] = sum;
@@ -328,7 +452,6 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 // ---------------------------------------------------------------- host side
 constexpr int kMany = 384, kFew = 24;  // 80 bytes a tensor: kernel arguments hold 32764
 static_assert(sizeof(Table<kMany>) + sizeof(AdamWArgs) <= 32764, "kernel arguments");
-constexpr int kBlocksPerSm = 8;  // of kThreads
 constexpr int kNormBlocks = 2048;  // at most, whatever the device
 
 // Fills a table with tensors [from, ...) as far as it goes; returns how many of the list it took.
@@ -351,7 +474,13 @@ int64_t fill(Table<N>* t, const moe_adamw_tensor* list, int64_t count, int64_t c
   return i;
 }
 
-int grid_of(uint32_t chunks, int sms) { return (int)std::min<int64_t>(chunks, (int64_t)sms * kBlocksPerSm); }
+// As many blocks as are resident at once: one more round of blocks would double the time of a persistent kernel.
+template <typename K>
+int grid_of(K kernel, uint32_t chunks, int sms) {
+  int per = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0) != cudaSuccess || per < 1) per = 1;
+  return (int)std::min<int64_t>(chunks, (int64_t)sms * per);
+}
 
 template <int N>
 cudaError_t adamw_launches(int bits, const AdamWArgs& a, const moe_adamw_tensor* list, int64_t count, int sms,
@@ -363,8 +492,8 @@ cudaError_t adamw_launches(int bits, const AdamWArgs& a, const moe_adamw_tensor*
     count -= took;
     if (!t.count) continue;
     *launches += 1;
-    if (bits == 8) MOE_LAUNCH((k_adamw<8, N>), grid_of(t.chunks, sms), kThreads, 0, st, t, a);
-    else MOE_LAUNCH((k_adamw<32, N>), grid_of(t.chunks, sms), kThreads, 0, st, t, a);
+    if (bits == 8) MOE_LAUNCH((k_adamw<8, N>), grid_of(k_adamw<8, N>, t.chunks, sms), kThreads, 0, st, t, a);
+    else MOE_LAUNCH((k_adamw<32, N>), grid_of(k_adamw<32, N>, t.chunks, sms), kThreads, 0, st, t, a);
   }
   return cudaSuccess;
 }
@@ -381,7 +510,7 @@ cudaError_t norm_launches(char* ws, const moe_adamw_tensor* list, int64_t count,
     list += took;
     count -= took;
     while (count > 0 && list->n == 0) ++list, --count;  // the launch with the last values is the one that finishes
-    const int grid = std::max(1, std::min(kNormBlocks, grid_of(t.chunks, sms)));  // no value at all: one block writes a norm of zero
+    const int grid = std::max(1, std::min(kNormBlocks, grid_of(k_grad_norm<N>, t.chunks, sms)));  // no value at all: one block writes a norm of zero
     *launches += 1;
     MOE_LAUNCH((k_grad_norm<N>), grid, kThreads, 0, st, t, part, part0, part0 + grid, done, scale,
                count > 0 ? nullptr : norm);

@@ -3,8 +3,11 @@
 //   lse = log sum_v e^l;  loss = lse - l_target + z lse^2;  dl = d ((1 + 2 z lse) e^{l - lse} - onehot);
 //   dx = dl w^T;  dw = x^T dl.
 //
-// The logits exist for a piece of the vocabulary at a time: their largest and the sum of exponentials are carried from
-// piece to piece; the backward computes each piece again, turns it into dl and multiplies that by w and x.
+// bf16: the tensor-core products' epilogue turns a tile of logits into the rows' statistics (largest, sum of
+// exponentials), or into dl, before anything is stored; the forward is one product over the whole vocabulary, the
+// backward takes it a piece at a time: dl of the piece, then its two products. fp32: the logits of a piece are stored,
+// then read. The target's logit is summed in fp32 on the CUDA cores: tensor cores truncate as they add, and a target's
+// products are mostly of one sign.
 #include <algorithm>
 
 #include "block.h"
@@ -18,7 +21,7 @@ namespace {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 
-// sum over the warp of e^{m} parts: (m, s) joined with lanes' (m, s)
+// (m, s) joined with (m2, s2): s e^m is the sum of both.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float big = fmaxf(m, m2);
   if (big == -INFINITY) return;  // both empty
@@ -26,10 +29,8 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = big;
 }
 
-// A block a row: the piece's largest logit and sum joined to what earlier pieces left; the target's logit where it
-// lies in the piece.
-__global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, int cols, int v0, const int* target,
-                                                    float2* stat, float* at_target, int first) {
+// A block a row: the piece's largest logit and sum joined to what earlier pieces left.
+__global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, int cols, float2* stat, int first) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ float2 red[8];
   const int64_t t = blockIdx.x;
@@ -55,66 +56,141 @@ __global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, 
     for (int w = 1; w < 8; ++w) join(m, s, red[w].x, red[w].y);
     if (!first) join(m, s, stat[t].x, stat[t].y);
     stat[t] = make_float2(m, s);
-    const int64_t c = (int64_t)target[t] - v0;
-    if (c >= 0 && c < cols) at_target[t] = row[c];
   }
 }
 
-// lse and loss of 256 rows a block; the blocks' totals are added in order by the last one.
-__global__ void __launch_bounds__(256) k_xent_loss(const float2* stat, const float* at_target, const int* target, int M,
-                                                   int V, float z, float* loss, float* lse, float2* part, unsigned* done,
-                                                   float* total, int* status) {
+// Eight rows' slots [first, end) of stat[slot][M] joined by a block of 256 threads, four slots of eight rows a warp;
+// BASE2: a slot is (largest logit times log2 e, sum of powers of two), else of e. Threads 0 .. 7 hold the result.
+constexpr int kLossRows = 8;
+template <bool BASE2>
+__device__ __forceinline__ float2 join_slots(const float2* stat, int first, int end, int M, int64_t t0, float2 (*red)[kLossRows]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane & 7;
+  const auto both = [](float& m, float& s, float m2, float s2) {
+    if constexpr (BASE2) {
+      const float big = fmaxf(m, m2);
+      s = s * exp2f(m - big) + s2 * exp2f(m2 - big);
+      m = big;
+    } else {
+      join(m, s, m2, s2);
+    }
+  };
+  float m = BASE2 ? -3.0e38f : -INFINITY, s = 0.0f;
+  if (t0 + r < M) {
+#pragma unroll 4
+    for (int i = first + warp * 4 + (lane >> 3); i < end; i += 32) {
+      const float2 v = stat[(int64_t)i * M + t0 + r];
+      both(m, s, v.x, v.y);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+    both(m, s, m2, s2);
+  }
+  if (lane < 8) red[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x < kLossRows) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) both(m, s, red[w][threadIdx.x].x, red[w][threadIdx.x].y);
+  }
+  return make_float2(m, s);
+}
+
+// Slots [first, end) joined into slot 0.
+__global__ void __launch_bounds__(256) k_xent_fold(float2* stat, int first, int end, int M) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float2 red[8];
+  __shared__ float2 red[8][kLossRows];
+  const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
+  const float2 v = join_slots<true>(stat, first, end, M, t0, red);
+  if (threadIdx.x < kLossRows && t0 + threadIdx.x < M) stat[t0 + threadIdx.x] = v;
+}
+
+struct LossArgs {
+  const float2* stat;  // [slots][M]
+  int first, end, M, H, V;
+  const void* x;
+  const void* w;
+  int64_t ldx, swh, swv;  // w[h, v] at h * swh + v * swv
+  const int* target;
+  float z;
+  float* loss;
+  float* lse;
+  float2* part;
+  unsigned* done;
+  float* total;
+  int* status;
+};
+
+// lse and loss of eight rows a block, a warp a row for the target's logit. The blocks' totals are added in order by the
+// last one.
+template <typename T, bool BASE2>
+__global__ void __launch_bounds__(256) k_xent_loss(const LossArgs a) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ float2 red[8][kLossRows];
+  __shared__ float dots[kLossRows];
   __shared__ bool last;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
+  if (t0 + warp < a.M) {
+    const int v = a.target[t0 + warp];
+    float dot = 0.0f;
+    if (v >= 0 && v < a.V) {
+      const T* x = static_cast<const T*>(a.x) + (t0 + warp) * a.ldx;
+      const T* w = static_cast<const T*>(a.w) + v * a.swv;
+#pragma unroll 8
+      for (int h = lane; h < a.H; h += 32) dot = fmaf(io<T>::to_f(x[h]), io<T>::to_f(w[h * a.swh]), dot);
+      dot = warp_sum(dot);
+    }
+    if (lane == 0) dots[warp] = dot;
+  }
+  const float2 st = join_slots<BASE2>(a.stat, a.first, a.end, a.M, t0, red);
   float sum = 0.0f, n = 0.0f;
-  if (t < M) {
-    const float2 st = stat[t];
-    const float e = st.x + logf(st.y);
-    lse[t] = e;
-    const int v = target[t];
-    if (v >= V) set_status(status, MOE_ERR_DEVICE_ARG);
-    if (v >= 0 && v < V) {
-      sum = e - at_target[t] + z * e * e;
+  if (threadIdx.x < kLossRows && t0 + threadIdx.x < a.M) {
+    const float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
+    const int v = a.target[t0 + threadIdx.x];
+    a.lse[t0 + threadIdx.x] = e;
+    if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
+    if (v >= 0 && v < a.V) {
+      sum = e - dots[threadIdx.x] + a.z * e * e;
       n = 1.0f;
     }
-    loss[t] = sum;
+    a.loss[t0 + threadIdx.x] = sum;
   }
-  if (!total) return;
-  sum = warp_sum(sum);
-  n = warp_sum(n);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(sum, n);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) {
-      sum += red[w].x;
-      n += red[w].y;
+  if (!a.total) return;
+  if (warp == 0) {
+    sum = warp_sum(sum);
+    n = warp_sum(n);
+    if (lane == 0) {
+      a.part[blockIdx.x] = make_float2(sum, n);
+      __threadfence();
+      last = atomicAdd(a.done, 1u) == gridDim.x - 1;
     }
-    part[blockIdx.x] = make_float2(sum, n);
-    __threadfence();
-    last = atomicAdd(done, 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  __shared__ double2 wide[256];
-  double a = 0.0, b = 0.0;
+  __shared__ double2 wide[8];
+  double x = 0.0, y = 0.0;
   for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) {
-    const float2 p = __ldcg(part + i);
-    a += p.x;
-    b += p.y;
+    const float2 p = __ldcg(a.part + i);
+    x += p.x;
+    y += p.y;
   }
-  wide[threadIdx.x] = make_double2(a, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  if (lane == 0) wide[warp] = make_double2(x, y);
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 256; ++i) {
-      a += wide[i].x;
-      b += wide[i].y;
+    for (int i = 1; i < 8; ++i) {
+      x += wide[i].x;
+      y += wide[i].y;
     }
-    total[0] = (float)a;
-    total[1] = (float)b;
-    *done = 0;
+    a.total[0] = (float)x;
+    a.total[1] = (float)y;
+    *a.done = 0;
   }
 }
 
@@ -133,16 +209,15 @@ __device__ __forceinline__ float row_grad(const XentRows& r, int64_t t) {
   return r.dloss ? r.dloss[t] : 1.0f / r.total[1];
 }
 
-// dl of a piece from its logits, a block 1024 columns of a row.
-template <typename T>
-__global__ void __launch_bounds__(256) k_xent_dl(const float* l, int64_t ld, int cols, int v0, XentRows r, T* dl) {
+// dl of a piece in place of its logits (fp32), a block 1024 columns of a row.
+__global__ void __launch_bounds__(256) k_xent_dl(float* l, int64_t ld, int cols, int v0, XentRows r) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int64_t t = blockIdx.x;
   const float d = row_grad(r, t), lse = r.lse[t], f = d * (1.0f + 2.0f * r.z * lse);
   const int at = r.target[t] - v0;
   for (int i = blockIdx.y * 1024 + threadIdx.x; i < min(cols, ((int)blockIdx.y + 1) * 1024); i += 256) {
     const float p = d == 0.0f ? 0.0f : expf(l[t * ld + i] - lse) * f;
-    dl[t * ld + i] = io<T>::cvt(i == at ? p - d : p);
+    l[t * ld + i] = i == at ? p - d : p;
   }
 }
 
@@ -160,16 +235,21 @@ __global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat1
 }
 
 // ---------------------------------------------------------------- host side
-// Columns of a piece: a multiple of 256, about 2^24 logits.
+// Columns of a piece: a multiple of 256; about 2^26 values of dl in bf16, 2^24 logits in fp32.
 int64_t piece_cols(const moe_xent_dims& d) {
-  const int64_t want = std::max<int64_t>(1024, (1 << 24) / d.M / 256 * 256);
+  const int64_t want = std::max<int64_t>(1024, (1 << (d.dtype == MOE_BF16 ? 26 : 24)) / d.M / 256 * 256);
   return std::min(want, up8(d.V));
 }
+constexpr int kSlotCols = 64;  // the narrowest slot of the statistics
+// Columns of a forward product in bf16: its statistics (with those of the columns before) stay below 256 MB, or 1 KB a row.
+int64_t stat_cols(const moe_xent_dims& d) {
+  return std::min(d.V, std::max<int64_t>(8192, (1ll << 31) / d.M / 256 * 256));
+}
 
-// Workspace: header, the rows' statistics, a piece's logits and dl, dx in fp32, and copies of x and w with rows of a
+// Workspace: header, the rows' statistics, a piece's logits (fp32) or dl, dx in fp32, and copies of x and w with rows of a
 // multiple of 16 bytes where the caller's are not.
 struct XentWs {
-  size_t stat, at, part, logits, dl, dx, xp, wp, total;
+  size_t stat, part, piece, dx, xp, wp, total;
 };
 XentWs layout(const moe_xent_dims& d, bool backward) {
   const bool bf = d.dtype == MOE_BF16;
@@ -181,16 +261,12 @@ XentWs layout(const moe_xent_dims& d, bool backward) {
     o += up256(bytes);
     return at;
   };
-  L.stat = take((size_t)d.M * 8);
-  L.at = take((size_t)d.M * 4);
-  L.part = take((size_t)((d.M + 255) / 256) * 8);
+  L.stat = take((size_t)d.M * 8 * (bf ? 1 + (stat_cols(d) + kSlotCols - 1) / kSlotCols : 1));
+  L.part = take((size_t)((d.M + kLossRows - 1) / kLossRows) * 8);
   L.xp = take(bf && d.H % 8 ? (size_t)d.M * up8(d.H) * 2 : 0);
   L.wp = take(bf && C % 8 ? (size_t)R * up8(C) * 2 : 0);
-  L.logits = take((size_t)d.M * P * 4);
-  if (backward) {
-    L.dl = take(bf ? (size_t)d.M * P * 2 : 0);
-    L.dx = take(bf && d.V > P ? (size_t)d.M * d.H * 4 : 0);
-  }
+  L.piece = take(bf ? (backward ? (size_t)d.M * P * 2 : 0) : (size_t)d.M * P * 4);
+  L.dx = take(backward && bf && d.V > P ? (size_t)d.M * d.H * 4 : 0);
   L.total = o;
   return L;
 }
@@ -220,24 +296,23 @@ struct Xent {
   const void* w_at(int64_t v0) const {
     return static_cast<const char*>(w) + (d.tied ? v0 * ldw : v0) * (d.dtype == MOE_BF16 ? 2 : 4);
   }
-  cudaError_t logits(int64_t v0, int cols) {
-    float* l = reinterpret_cast<float*>(ws + L.logits);
+  // the product of columns v0 .. v0 + cols - 1 of the logits
+  LinearGemm gemm(int64_t v0, int cols, void* out) const {
+    return {(int)d.M, cols, (int)d.H, x, w_at(v0), ldx, ldw, 0, !d.tied, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, 0,
+            reinterpret_cast<int*>(ws), P};
+  }
+  cudaError_t logits_f32(int64_t v0, int cols) {
     const int M = (int)d.M, H = (int)d.H;
-    if (d.dtype == MOE_BF16) {
-      LinearGemm g = {M, cols, H, x, w_at(v0), ldx, ldw, 0, !d.tied, nullptr, nullptr, l, nullptr, MOE_ACT_NONE, 1,
-                      reinterpret_cast<int*>(ws), P};
-      *launches += 1;
-      return launch_linear_tc(g, sms, st);
-    }
     SimtGemm g = {static_cast<const float*>(x), static_cast<const float*>(w_at(v0)), H, 1, d.tied ? 1 : ldw,
-                  d.tied ? ldw : 1, M, H, cols, nullptr, nullptr, l, nullptr, MOE_ACT_NONE, P};
+                  d.tied ? ldw : 1, M, H, cols, nullptr, nullptr, piece(), nullptr, MOE_ACT_NONE, P};
     return launch_linear_f32(&g, 1, sms, st, launches);
   }
+  float* piece() const { return reinterpret_cast<float*>(ws + L.piece); }
   cudaError_t products(int64_t v0, int cols, void* dx, void* dw) {
     const int M = (int)d.M, H = (int)d.H;
     if (d.dtype == MOE_BF16) {
       int* status = reinterpret_cast<int*>(ws);
-      const void* dl = ws + L.dl;
+      const void* dl = ws + L.piece;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dw) + (dw ? (d.tied ? v0 * d.H : v0) : 0);
       const bool whole = P >= d.V;
       LinearGemm gx = {M, H, cols, dl, w_at(v0), P, ldw, 0, d.tied, nullptr, nullptr, whole ? dx : ws + L.dx, nullptr,
@@ -257,7 +332,7 @@ struct Xent {
       }
       return e;
     }
-    const float* dl = reinterpret_cast<const float*>(ws + L.logits);
+    const float* dl = piece();
     const float *fx = static_cast<const float*>(x), *fw = static_cast<const float*>(w_at(v0));
     float* out = static_cast<float*>(dw) + (dw ? (d.tied ? v0 * d.H : v0) : 0);
     SimtGemm g[2];
@@ -279,19 +354,55 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   Xent c = {d, static_cast<char*>(ws), layout(d, false), x, w, sms, st, launches, 0, 0, 0};
   cudaError_t e = c.prepare();
   if (e != cudaSuccess) return e;
+  const bool bf = d.dtype == MOE_BF16;
   float2* stat = reinterpret_cast<float2*>(c.ws + c.L.stat);
-  float* at = reinterpret_cast<float*>(c.ws + c.L.at);
-  for (int64_t v0 = 0; v0 < d.V; v0 += c.P) {
-    const int cols = (int)std::min(c.P, d.V - v0);
-    if ((e = c.logits(v0, cols)) != cudaSuccess) return e;
-    *launches += 1;
-    MOE_LAUNCH(k_xent_piece, (unsigned)d.M, 256, 0, st, (const float*)(c.ws + c.L.logits), c.P, cols, (int)v0, target,
-               stat, at, (int)(v0 == 0));
+  const unsigned grid = (unsigned)((d.M + kLossRows - 1) / kLossRows);
+  int first = 0, end = 1;  // the slots to join
+  if (bf) {
+    const int64_t cols = stat_cols(d);
+    for (int64_t v0 = 0; v0 < d.V; v0 += cols) {
+      if (v0) {  // what came before, into slot 0
+        *launches += 1;
+        MOE_LAUNCH(k_xent_fold, grid, 256, 0, st, stat, first, end, (int)d.M);
+      }
+      const int n = (int)std::min(cols, d.V - v0);
+      int width = 1;
+      *launches += 1;
+      if ((e = launch_xent_stats(c.gemm(v0, n, nullptr), {stat + d.M}, sms, st, &width)) != cudaSuccess) return e;
+      first = v0 ? 0 : 1;
+      end = 1 + (n + width - 1) / width;
+    }
+  } else {
+    for (int64_t v0 = 0; v0 < d.V; v0 += c.P) {
+      const int cols = (int)std::min(c.P, d.V - v0);
+      if ((e = c.logits_f32(v0, cols)) != cudaSuccess) return e;
+      *launches += 1;
+      MOE_LAUNCH(k_xent_piece, (unsigned)d.M, 256, 0, st, (const float*)c.piece(), c.P, cols, stat, (int)(v0 == 0));
+    }
   }
+  LossArgs a = {};
+  a.stat = stat;
+  a.first = first;
+  a.end = end;
+  a.M = (int)d.M;
+  a.H = (int)d.H;
+  a.V = (int)d.V;
+  a.x = c.x;
+  a.w = c.w;
+  a.ldx = c.ldx;
+  a.swh = d.tied ? 1 : c.ldw;
+  a.swv = d.tied ? c.ldw : 1;
+  a.target = target;
+  a.z = d.z_coef;
+  a.loss = loss;
+  a.lse = lse;
+  a.part = reinterpret_cast<float2*>(c.ws + c.L.part);
+  a.done = reinterpret_cast<unsigned*>(c.ws + 64);
+  a.total = total;
+  a.status = reinterpret_cast<int*>(c.ws);
   *launches += 1;
-  MOE_LAUNCH(k_xent_loss, (unsigned)((d.M + 255) / 256), 256, 0, st, (const float2*)stat, (const float*)at, target,
-             (int)d.M, (int)d.V, d.z_coef, loss, lse, reinterpret_cast<float2*>(c.ws + c.L.part),
-             reinterpret_cast<unsigned*>(c.ws + 64), total, reinterpret_cast<int*>(c.ws));
+  if (bf) MOE_LAUNCH((k_xent_loss<__nv_bfloat16, true>), grid, 256, 0, st, a);
+  else MOE_LAUNCH((k_xent_loss<float, false>), grid, 256, 0, st, a);
   return cudaSuccess;
 }
 
@@ -303,15 +414,17 @@ cudaError_t launch_xent_bwd(const moe_xent_dims& d, void* ws, const void* x, con
   if (e != cudaSuccess) return e;
   const XentRows r = {target, lse, dloss, total, (int)d.V, d.z_coef};
   const bool bf = d.dtype == MOE_BF16;
-  float* l = reinterpret_cast<float*>(c.ws + c.L.logits);
+  XentEpi epi = {nullptr, target, lse, dloss, total, d.z_coef, 0, (int)d.V};
   for (int64_t v0 = 0; v0 < d.V; v0 += c.P) {
     const int cols = (int)std::min(c.P, d.V - v0);
-    if ((e = c.logits(v0, cols)) != cudaSuccess) return e;
-    const dim3 grid((unsigned)d.M, (unsigned)((cols + 1023) / 1024));
     *launches += 1;
-    if (bf) MOE_LAUNCH(k_xent_dl<__nv_bfloat16>, grid, 256, 0, st, (const float*)l, c.P, cols, (int)v0, r,
-                       reinterpret_cast<__nv_bfloat16*>(c.ws + c.L.dl));
-    else MOE_LAUNCH(k_xent_dl<float>, grid, 256, 0, st, (const float*)l, c.P, cols, (int)v0, r, l);
+    if (bf) {
+      epi.v0 = (int)v0;
+      if ((e = launch_xent_grad(c.gemm(v0, cols, c.piece()), epi, sms, st)) != cudaSuccess) return e;
+    } else {
+      if ((e = c.logits_f32(v0, cols)) != cudaSuccess) return e;
+      MOE_LAUNCH(k_xent_dl, dim3((unsigned)d.M, (unsigned)((cols + 1023) / 1024)), 256, 0, st, c.piece(), c.P, cols, (int)v0, r);
+    }
     if ((e = c.products(v0, cols, dx, dw)) != cudaSuccess) return e;
   }
   if (bf && dx && c.P < d.V) {

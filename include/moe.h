@@ -489,7 +489,7 @@ typedef struct moe_xent_dims {
  * moe_xent_workspace_size -- bytes of workspace of moe_xent_fwd alone (backward == 0) or of both.
  * The caller sets its first 256 bytes to zero once, when it allocates the workspace, ordered before
  * the first call; they hold the status word (moe_read_status) and a counter that every call leaves
- * at zero. Its size does not grow with M V. Host-only.
+ * at zero. It holds a piece of the vocabulary at a time: its size does not grow with M V. Host-only.
  */
 MOE_API int moe_xent_workspace_size(const moe_xent_dims* dims, int backward, size_t* bytes);
 
@@ -510,7 +510,7 @@ MOE_API int moe_xent_fwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, v
  * counted rows) where dloss is null; 0 for rows that are not counted.
  *   dl = d_t ((1 + 2 z_coef lse_t) e^{l - lse_t} - onehot(target_t));  dx = dl w^T;  dw = x^T dl.
  * The logits are computed again, a piece of the vocabulary at a time. In bf16 dl is rounded to bf16
- * for the two products; dx is summed over the pieces in fp32.
+ * for the two products, and e^{l - lse} below 2^-126 is zero; dx is summed over the pieces in fp32.
  * Inputs:  x, w, target as in the forward, lse[M] of the forward, dloss[M] float or total[2] of the
  *          forward. Outputs: dx[M,H], dw (dims.tied), each nullable; overwritten.
  */

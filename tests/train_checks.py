@@ -183,6 +183,9 @@ def check_xent_bwd(c, d, out):
     err = err + 4 * E32 * dd * hit
     if c["dtype"] == "bf16":
         err = err + u * np.abs(DL)  # dl is rounded for the two products
+        # Exponentials below the smallest normal float are zero there (the hardware's base-2 exponential flushes): p is
+        # off by at most p < 2^-126, so dl = d f p by at most d f 2^-126 whatever p is, and that is multiplied by x and w.
+        err = err + dd * f * 2.0 ** -126
     a = np.abs(DL) + err
     if gx is not None:
         close(gx, DX, u * np.abs(DX) + (c["V"] + 64) * 2 * E32 * (a @ np.abs(w).T) + err @ np.abs(w).T + 1e-37, "dx")
