@@ -54,13 +54,17 @@ struct BalanceArgs {
 __device__ __forceinline__ int seq_at(const BalanceArgs& a, int s) {
   return a.start ? min(max(a.start[s], 0), a.T) : (s ? a.T : 0);
 }
-// the last sequence that begins at or before token t (0 if none does)
+// The last sequence that begins at or before token t (the first if none does), by the whole warp: 32 offsets are looked
+// at together, since each look waits for memory. Offsets that are not ascending give some sequence in [0, S).
 __device__ __forceinline__ int seq_of(const BalanceArgs& a, int t) {
-  int lo = 0, hi = a.S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_at(a, mid) <= t) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.S;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const uint32_t before = __ballot_sync(kFull, at < n && (lane == 0 || seq_at(a, lo + at) <= t));
+    const int skip = (__popc(before) - 1) * step;
+    lo += skip;
+    n = min(step, n - skip);
   }
   return lo;
 }
@@ -217,8 +221,6 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
   extern __shared__ float shared[];  // [WARPS][E] sums of p, [E] counts
   int* hist = reinterpret_cast<int*>(shared + WARPS * a.E);
   __shared__ float zsum[WARPS];
-  __shared__ float sp[WARPS][33];
-  __shared__ int sn[WARPS][33];
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
@@ -270,14 +272,37 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
     }
     __syncthreads();
   }
-  if (!a.few || !last_block(a.done)) return;
-  float dot = 0.0f, z = 0.0f;
+  if (!a.few) return;
+  if (gridDim.x > 1 && !last_block(a.done)) return;
+  // a column a thread, all its rows
+  float dot = 0.0f, z_of_warp = 0.0f;
   for (int s = 0; s < a.S; ++s) {
     check_seq(a, s);
-    for (int e = 0; e < a.E; e += 32) dot += sum_columns<WARPS>(a, s, e, sp, sn);
-    if (warp == 0) z += sum_z(a, s);
+    const int t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
+    const int r0 = t0 < t1 ? t0 / a.chunk + s : 0, r1 = t0 < t1 ? (t1 - 1) / a.chunk + s + 1 : 0;
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+      float p = 0.0f;
+      int c = 0;
+#pragma unroll 4
+      for (int r = r0; r < r1; ++r) {
+        p += __ldcg(a.row_p + (int64_t)r * a.E + e);
+        c += __ldcg(a.row_n + (int64_t)r * a.E + e);
+      }
+      p /= (float)max(t1 - t0, 1);
+      a.count[(int64_t)s * a.E + e] = c;
+      if (a.prob) a.prob[(int64_t)s * a.E + e] = p;
+      dot += (float)c * p;
+    }
+    if (warp == 0) z_of_warp += sum_z(a, s);
   }
-  if (threadIdx.x == 0) store_losses(a, dot, z);
+  dot = warp_sum(dot);
+  if (lane == 0) zsum[warp] = dot;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) dot += zsum[w];
+    store_losses(a, dot, z_of_warp);
+  }
 }
 
 // A block 32 experts of a sequence: its rows added; the last block adds the parts of the losses in a fixed order.
@@ -384,9 +409,9 @@ constexpr int kFewRows = 16;       // as many rows the last block adds by itself
 
 // Warps of a forward block: as many as hold their sums in 32 KB.
 int fwd_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
-// Tokens of a chunk: a token for each warp, and no more chunks than SMs.
+// Tokens of a chunk: two for each warp, and no more chunks than SMs.
 int chunk_tokens(const moe_balance_dims& d) {
-  return (int)std::max<int64_t>(fwd_warps(d.E), (d.T + kChunkBlocks - 1) / kChunkBlocks);
+  return (int)std::max<int64_t>(2 * fwd_warps(d.E), (d.T + kChunkBlocks - 1) / kChunkBlocks);
 }
 
 struct BalanceWs {

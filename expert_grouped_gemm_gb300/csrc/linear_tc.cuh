@@ -454,6 +454,8 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       XentRow row;
       if constexpr (EPI == kEpiGrad) row.load(args.x, row0 + lane, lane < rows);
       float run_m = -kHuge, run_s = 0.0f;
+      int hit = -1;  // statistics: the target's column of the tile
+      if (EPI == kEpiStats && lane < rows) hit = args.x.target[row0 + lane] - args.x.v0 - it.n0;
       const int acc = acc_i & 1;
       if (!mbar_wait_bounded(&tfull[acc], (uint32_t)((acc_i >> 1) & 1), abort_flag)) break;
       tc_fence_after();
@@ -472,6 +474,13 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 64; ++i) z[i] = i < cols ? __uint_as_float(v[i >> 5][i & 31]) : -INFINITY;
           row_stats<64>(z, run_m, run_s);
+          const int at = hit - c * 64;
+          if (__any_sync(0xffffffffu, at >= 0 && at < cols)) {
+            float l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) l = i == at ? z[i] : l;
+            if (at >= 0 && at < cols) args.x.at[row0 + lane] = l;
+          }
           continue;
         }
         const uint32_t ty = tile_of_y();
@@ -617,6 +626,10 @@ __device__ __forceinline__ void emit_xent(const TcArgs& a, int64_t t, int f0, in
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (n0 + i >= g.N) z[i] = -INFINITY;
+    const int at = a.x.target[t] - a.x.v0 - n0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i == at && n0 + i < g.N) a.x.at[t] = z[i];
     row_stats<4>(z, m, s);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {

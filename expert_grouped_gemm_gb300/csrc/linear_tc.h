@@ -28,6 +28,7 @@ struct LinearGemm {
 // a vocabulary of V.
 struct XentEpi {
   float2* part;         // statistics: [slots][M]
+  float* at;            // statistics: [M], receives the logit of a target among these columns
   const int* target;    // gradient: as in XentRows of xent.cu
   const float* lse;
   const float* dloss;

@@ -24,8 +24,12 @@ namespace {
 
 constexpr int kBlock = 256;     // values that share a scale; a warp's step
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kSteps = 2;       // a warp's steps in a chunk
-constexpr int kChunk = kWarps * kSteps * kBlock;
+// A warp's blocks in a chunk: their loads are in flight together. Two where the states have 8 bits and a block is 1.5 KB;
+// with 32 bits one has 3.6 KB, and more of them cost registers that more warps use better.
+template <int BITS>
+constexpr int steps_of = BITS == 8 ? 2 : 1;
+template <int BITS>
+constexpr int chunk_of = kWarps * steps_of<BITS> * kBlock;
 
 struct Entry {
   void* p;
@@ -211,7 +215,7 @@ __device__ __forceinline__ void pack_block(const Entry& e, int64_t blk, int lane
 }
 
 // Whole blocks blk, blk + kWarps, ... (`steps` of them) of a tensor: every load is sent for before the first is used.
-template <int BITS, bool PB, bool GB, bool MASTER>
+template <int BITS, int kSteps, bool PB, bool GB, bool MASTER>
 __device__ __forceinline__ void whole_blocks(const Entry& e, const Factors& k, int64_t blk, int lane) {
   Four<GB> g[kSteps][2];
   Four<MASTER ? false : PB> p[kSteps][2];
@@ -273,24 +277,37 @@ __device__ __forceinline__ void whole_blocks(const Entry& e, const Factors& k, i
   }
 }
 
-// A block that may end inside.
+template <int BITS, int kSteps>
+__device__ __forceinline__ void whole_blocks(const Entry& e, const Factors& k, int64_t blk, int lane) {
+  if (e.master) {
+    if (e.types & 2) whole_blocks<BITS, kSteps, true, true, true>(e, k, blk, lane);
+    else whole_blocks<BITS, kSteps, true, false, true>(e, k, blk, lane);
+  } else if (e.types & 1) {
+    if (e.types & 2) whole_blocks<BITS, kSteps, true, true, false>(e, k, blk, lane);
+    else whole_blocks<BITS, kSteps, true, false, false>(e, k, blk, lane);
+  } else {
+    if (e.types & 2) whole_blocks<BITS, kSteps, false, true, false>(e, k, blk, lane);
+    else whole_blocks<BITS, kSteps, false, false, false>(e, k, blk, lane);
+  }
+}
+
+// The block that a tensor ends in.
 template <int BITS>
-__device__ __noinline__ void last_block(const Entry& e, const Factors& k, int64_t blk, int lane) {
+__device__ __forceinline__ void last_block(const Entry& e, const Factors& k, int64_t blk, int lane) {
   const bool pb = e.types & 1, gb = e.types & 2;
   const int64_t i = blk * kBlock + lane * 4, n = e.n;
-  float mf[2][4], vf[2][4];
+  float gf[2][4], pf[2][4], mf[2][4], vf[2][4], sm = 1.0f, sv = 1.0f;
+#pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t at = i + h * 128;
-    float gf[4], pf[4];
-    load_tail(e.g, gb, at, n, gf);
-    if (e.master) load_tail(e.master, false, at, n, pf);
-    else load_tail(e.p, pb, at, n, pf);
-    float sm = 1.0f, sv = 1.0f;
+    load_tail(e.g, gb, at, n, gf[h]);
+    load_tail(e.master ? e.master : e.p, e.master ? false : pb, at, n, pf[h]);
     if constexpr (BITS == 32) {
       load_tail(e.m, false, at, n, mf[h]);
       load_tail(e.v, false, at, n, vf[h]);
     } else {
       uint32_t mc = 0, vc = 0;
+#pragma unroll
       for (int j = 0; j < 4; ++j)
         if (at + j < n) {
           mc |= (uint32_t)static_cast<const uint8_t*>(e.m)[at + j] << (8 * j);
@@ -298,12 +315,19 @@ __device__ __noinline__ void last_block(const Entry& e, const Factors& k, int64_
         }
       decode4(mc, mf[h]);
       decode4(vc, vf[h]);
-      sm = e.ms[blk];
-      sv = e.vs[blk];
     }
-    update4<BITS>(k, sm, sv, gf, pf, mf[h], vf[h]);
-    if (e.master) store_tail(e.master, false, at, n, pf);
-    store_tail(e.p, pb, at, n, pf);
+  }
+  if constexpr (BITS == 8) {
+    sm = e.ms[blk];
+    sv = e.vs[blk];
+    __syncwarp();  // every lane has read the block's scales before one is written
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t at = i + h * 128;
+    update4<BITS>(k, sm, sv, gf[h], pf[h], mf[h], vf[h]);
+    if (e.master) store_tail(e.master, false, at, n, pf[h]);
+    store_tail(e.p, pb, at, n, pf[h]);
     if constexpr (BITS == 32) {
       store_tail(e.m, false, at, n, mf[h]);
       store_tail(e.v, false, at, n, vf[h]);
@@ -311,7 +335,6 @@ __device__ __noinline__ void last_block(const Entry& e, const Factors& k, int64_
   }
   if constexpr (BITS == 8) {
     uint32_t mo[2], vo[2];
-    __syncwarp();  // every lane has read the block's scales
     pack_block(e, blk, lane, mf, vf, mo, vo);
     for (int h = 0; h < 2; ++h)
       for (int j = 0; j < 4; ++j)
@@ -346,21 +369,16 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
     const float elr = lr * e.lr_scale;
     k.keep = 1.0f - elr * e.wd;
     k.move = elr * bc1;
+    constexpr int kSteps = steps_of<BITS>;
     const int64_t blk0 = (int64_t)(chunk - e.first) * (kWarps * kSteps), blk = blk0 + warp;
-    if ((blk0 + kWarps * kSteps) * kBlock <= e.n) {
-      if (e.master) {
-        if (e.types & 2) whole_blocks<BITS, true, true, true>(e, k, blk, lane);
-        else whole_blocks<BITS, true, false, true>(e, k, blk, lane);
-      } else if (e.types & 1) {
-        if (e.types & 2) whole_blocks<BITS, true, true, false>(e, k, blk, lane);
-        else whole_blocks<BITS, true, false, false>(e, k, blk, lane);
-      } else {
-        if (e.types & 2) whole_blocks<BITS, false, true, false>(e, k, blk, lane);
-        else whole_blocks<BITS, false, false, false>(e, k, blk, lane);
-      }
+    if (kSteps > 1 && (blk0 + kWarps * kSteps) * kBlock <= e.n) {
+      whole_blocks<BITS, kSteps>(e, k, blk, lane);
     } else {
-      for (int s = 0; s < kSteps; ++s)
-        if ((blk + s * kWarps) * kBlock < e.n) last_block<BITS>(e, k, blk + s * kWarps, lane);
+      for (int s = 0; s < kSteps; ++s) {
+        const int64_t b = blk + s * kWarps;
+        if ((b + 1) * kBlock <= e.n) whole_blocks<BITS, 1>(e, k, b, lane);
+        else if (b * kBlock < e.n) last_block<BITS>(e, k, b, lane);
+      }
     }
   }
 }
@@ -368,8 +386,43 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
 // ---------------------------------------------------------------- norm
 constexpr int kNormChunk = kThreads * 32;  // values: four 16-byte loads a thread in bf16, in flight together
 
-__device__ __forceinline__ float squares(const float (&f)[4]) {
-  return (f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3]);
+// This thread's squares of the n values of a chunk, four 16-byte loads in flight.
+template <bool BF>
+__device__ __forceinline__ float squares(const void* g, int n) {
+  constexpr int V = BF ? 8 : 4;
+  const uint4* p = static_cast<const uint4*>(g);
+  const int vecs = n / V;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNormChunk / V; i += 4 * kThreads) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = i + j * kThreads + threadIdx.x;
+      u[j] = at < vecs ? __ldcs(p + at) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[V];
+      if constexpr (BF) {
+        bf16x8_to_f(u[j], f);
+      } else {
+        f[0] = __uint_as_float(u[j].x);
+        f[1] = __uint_as_float(u[j].y);
+        f[2] = __uint_as_float(u[j].z);
+        f[3] = __uint_as_float(u[j].w);
+      }
+      float s = (f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3]);
+      if constexpr (BF) s += (f[4] * f[4] + f[5] * f[5]) + (f[6] * f[6] + f[7] * f[7]);
+      sum += s;
+    }
+  }
+  const int at = vecs * V + threadIdx.x;
+  if (at < n) {
+    const float f = BF ? __bfloat162float(static_cast<const __nv_bfloat16*>(g)[at]) : static_cast<const float*>(g)[at];
+    sum += f * f;
+  }
+  return sum;
 }
 
 // A block's sum of squares over its chunks; the last block of the last launch adds the blocks' in order.
@@ -388,39 +441,9 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
     const Entry& e = tab.e[at];
     const bool gb = e.types & 2;
     const int64_t i0 = (int64_t)(chunk - e.first) * kNormChunk;
-    if (i0 + kNormChunk <= e.n) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(e.g) + i0 * (gb ? 2 : 4)) + threadIdx.x;
-      if (gb) {
-        uint4 u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = __ldcs(p + j * kThreads);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f[8];
-          bf16x8_to_f(u[j], f);
-          sum += ((f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3])) +
-                 ((f[4] * f[4] + f[5] * f[5]) + (f[6] * f[6] + f[7] * f[7]));
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint4 u[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u[j] = __ldcs(p + (r * 4 + j) * kThreads);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float f[4] = {__uint_as_float(u[j].x), __uint_as_float(u[j].y), __uint_as_float(u[j].z), __uint_as_float(u[j].w)};
-            sum += squares(f);
-          }
-        }
-      }
-    } else {
-      for (int64_t i = i0 + threadIdx.x * 4; i < e.n; i += kThreads * 4) {
-        float f[4];
-        load_tail(e.g, gb, i, e.n, f);
-        sum += squares(f);
-      }
-    }
+    const int n = (int)min((int64_t)kNormChunk, e.n - i0);
+    const char* g = static_cast<const char*>(e.g) + i0 * (gb ? 2 : 4);
+    sum += gb ? squares<true>(g, n) : squares<false>(g, n);
   }
   sum = warp_sum(sum);
   if (lane == 0) red[warp] = sum;
@@ -450,7 +473,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kMany = 384, kFew = 24;  // 80 bytes a tensor: kernel arguments hold 32764
+constexpr int kMany = 384, kSome = 128, kFew = 24;  // 80 bytes a tensor: kernel arguments hold 32764
 static_assert(sizeof(Table<kMany>) + sizeof(AdamWArgs) <= 32764, "kernel arguments");
 constexpr int kNormBlocks = 2048;  // at most, whatever the device
 
@@ -487,7 +510,7 @@ cudaError_t adamw_launches(int bits, const AdamWArgs& a, const moe_adamw_tensor*
                            cudaStream_t st, int* launches) {
   Table<N> t;
   while (count > 0) {
-    const int64_t took = fill(&t, list, count, kChunk);
+    const int64_t took = fill(&t, list, count, bits == 8 ? chunk_of<8> : chunk_of<32>);
     list += took;
     count -= took;
     if (!t.count) continue;
@@ -532,8 +555,9 @@ size_t grad_norm_workspace_bytes(const moe_adamw_tensor* list, int64_t count) {
 cudaError_t launch_grad_norm(void* ws, const moe_adamw_tensor* list, int64_t count, float scale, float* norm, int sms,
                              cudaStream_t st, int* launches) {
   // arguments are copied with every launch: a short list takes a short table
-  return count <= kFew ? norm_launches<kFew>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches)
-                       : norm_launches<kMany>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches);
+  return count <= kFew    ? norm_launches<kFew>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches)
+         : count <= kSome ? norm_launches<kSome>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches)
+                          : norm_launches<kMany>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches);
 }
 
 cudaError_t launch_adamw(const moe_adamw_dims& d, const moe_adamw_tensor* list, int64_t count, const float* norm,
@@ -554,8 +578,9 @@ cudaError_t launch_adamw(const moe_adamw_dims& d, const moe_adamw_tensor* list, 
   a.norm = norm;
   a.lr_at = lr;
   a.step_at = step;
-  return count <= kFew ? adamw_launches<kFew>(d.state_bits, a, list, count, sms, st, launches)
-                       : adamw_launches<kMany>(d.state_bits, a, list, count, sms, st, launches);
+  return count <= kFew    ? adamw_launches<kFew>(d.state_bits, a, list, count, sms, st, launches)
+         : count <= kSome ? adamw_launches<kSome>(d.state_bits, a, list, count, sms, st, launches)
+                          : adamw_launches<kMany>(d.state_bits, a, list, count, sms, st, launches);
 }
 
 }  // namespace moe

@@ -59,9 +59,9 @@ __global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, 
   }
 }
 
-// Eight rows' slots [first, end) of stat[slot][M] joined by a block of 256 threads, four slots of eight rows a warp;
-// BASE2: a slot is (largest logit times log2 e, sum of powers of two), else of e. Threads 0 .. 7 hold the result.
-constexpr int kLossRows = 8;
+// Eight rows' slots [first, end) of stat[slot][M] joined by a block, four slots of eight rows a warp; BASE2: a slot is
+// (largest logit times log2 e, sum of powers of two), else of e. Threads 0 .. 7 hold the result.
+constexpr int kLossRows = 8, kLossWarps = 32;
 template <bool BASE2>
 __device__ __forceinline__ float2 join_slots(const float2* stat, int first, int end, int M, int64_t t0, float2 (*red)[kLossRows]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane & 7;
@@ -76,8 +76,8 @@ __device__ __forceinline__ float2 join_slots(const float2* stat, int first, int 
   };
   float m = BASE2 ? -3.0e38f : -INFINITY, s = 0.0f;
   if (t0 + r < M) {
-#pragma unroll 4
-    for (int i = first + warp * 4 + (lane >> 3); i < end; i += 32) {
+#pragma unroll 8
+    for (int i = first + warp * 4 + (lane >> 3); i < end; i += 4 * kLossWarps) {
       const float2 v = stat[(int64_t)i * M + t0 + r];
       both(m, s, v.x, v.y);
     }
@@ -90,16 +90,16 @@ __device__ __forceinline__ float2 join_slots(const float2* stat, int first, int 
   if (lane < 8) red[warp][lane] = make_float2(m, s);
   __syncthreads();
   if (threadIdx.x < kLossRows) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) both(m, s, red[w][threadIdx.x].x, red[w][threadIdx.x].y);
+#pragma unroll 8
+    for (int w = 1; w < kLossWarps; ++w) both(m, s, red[w][threadIdx.x].x, red[w][threadIdx.x].y);
   }
   return make_float2(m, s);
 }
 
 // Slots [first, end) joined into slot 0.
-__global__ void __launch_bounds__(256) k_xent_fold(float2* stat, int first, int end, int M) {
+__global__ void __launch_bounds__(kLossWarps * 32) k_xent_fold(float2* stat, int first, int end, int M) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float2 red[8][kLossRows];
+  __shared__ float2 red[kLossWarps][kLossRows];
   const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
   const float2 v = join_slots<true>(stat, first, end, M, t0, red);
   if (threadIdx.x < kLossRows && t0 + threadIdx.x < M) stat[t0 + threadIdx.x] = v;
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(256) k_xent_fold(float2* stat, int first, int 
 
 struct LossArgs {
   const float2* stat;  // [slots][M]
+  const float* at;     // BASE2: [M], the targets' logits as the product has them
   int first, end, M, H, V;
   const void* x;
   const void* w;
@@ -121,39 +122,45 @@ struct LossArgs {
   int* status;
 };
 
-// lse and loss of eight rows a block, a warp a row for the target's logit. The blocks' totals are added in order by the
-// last one.
+// lse and loss of eight rows a block, four warps a row for the target's logit in fp32; where the product's own is given,
+// the sum of exponentials is put right by the difference. The blocks' totals are added in order by the last one.
 template <typename T, bool BASE2>
-__global__ void __launch_bounds__(256) k_xent_loss(const LossArgs a) {
+__global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  __shared__ float2 red[8][kLossRows];
-  __shared__ float dots[kLossRows];
+  constexpr int kParts = kLossWarps / kLossRows;
+  __shared__ float2 red[kLossWarps][kLossRows];
+  __shared__ float dots[kLossRows][kParts];
   __shared__ bool last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
-  if (t0 + warp < a.M) {
-    const int v = a.target[t0 + warp];
+  const int row = warp / kParts, part = warp % kParts;
+  if (t0 + row < a.M) {
+    const int v = a.target[t0 + row];
     float dot = 0.0f;
     if (v >= 0 && v < a.V) {
-      const T* x = static_cast<const T*>(a.x) + (t0 + warp) * a.ldx;
+      const T* x = static_cast<const T*>(a.x) + (t0 + row) * a.ldx;
       const T* w = static_cast<const T*>(a.w) + v * a.swv;
-#pragma unroll 8
-      for (int h = lane; h < a.H; h += 32) dot = fmaf(io<T>::to_f(x[h]), io<T>::to_f(w[h * a.swh]), dot);
+#pragma unroll 16
+      for (int h = part * 32 + lane; h < a.H; h += 32 * kParts) dot = fmaf(io<T>::to_f(x[h]), io<T>::to_f(w[h * a.swh]), dot);
       dot = warp_sum(dot);
     }
-    if (lane == 0) dots[warp] = dot;
+    if (lane == 0) dots[row][part] = dot;
   }
   const float2 st = join_slots<BASE2>(a.stat, a.first, a.end, a.M, t0, red);
   float sum = 0.0f, n = 0.0f;
   if (threadIdx.x < kLossRows && t0 + threadIdx.x < a.M) {
-    const float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
+    float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
     const int v = a.target[t0 + threadIdx.x];
-    a.lse[t0 + threadIdx.x] = e;
     if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
     if (v >= 0 && v < a.V) {
-      sum = e - dots[threadIdx.x] + a.z * e * e;
+      float at = dots[threadIdx.x][0];
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) at += dots[threadIdx.x][i];
+      if (BASE2) e += log1pf(expf(at - e) - expf(a.at[t0 + threadIdx.x] - e));
+      sum = e - at + a.z * e * e;
       n = 1.0f;
     }
+    a.lse[t0 + threadIdx.x] = e;
     a.loss[t0 + threadIdx.x] = sum;
   }
   if (!a.total) return;
@@ -169,9 +176,9 @@ __global__ void __launch_bounds__(256) k_xent_loss(const LossArgs a) {
   __syncthreads();
   if (!last) return;
   __threadfence();
-  __shared__ double2 wide[8];
+  __shared__ double2 wide[kLossWarps];
   double x = 0.0, y = 0.0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) {
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kLossWarps * 32) {
     const float2 p = __ldcg(a.part + i);
     x += p.x;
     y += p.y;
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(256) k_xent_loss(const LossArgs a) {
   if (lane == 0) wide[warp] = make_double2(x, y);
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 1; i < kLossWarps; ++i) {
       x += wide[i].x;
       y += wide[i].y;
     }
@@ -249,7 +256,7 @@ int64_t stat_cols(const moe_xent_dims& d) {
 // Workspace: header, the rows' statistics, a piece's logits (fp32) or dl, dx in fp32, and copies of x and w with rows of a
 // multiple of 16 bytes where the caller's are not.
 struct XentWs {
-  size_t stat, part, piece, dx, xp, wp, total;
+  size_t stat, at, part, piece, dx, xp, wp, total;
 };
 XentWs layout(const moe_xent_dims& d, bool backward) {
   const bool bf = d.dtype == MOE_BF16;
@@ -262,6 +269,7 @@ XentWs layout(const moe_xent_dims& d, bool backward) {
     return at;
   };
   L.stat = take((size_t)d.M * 8 * (bf ? 1 + (stat_cols(d) + kSlotCols - 1) / kSlotCols : 1));
+  L.at = take(bf ? (size_t)d.M * 4 : 0);
   L.part = take((size_t)((d.M + kLossRows - 1) / kLossRows) * 8);
   L.xp = take(bf && d.H % 8 ? (size_t)d.M * up8(d.H) * 2 : 0);
   L.wp = take(bf && C % 8 ? (size_t)R * up8(C) * 2 : 0);
@@ -356,19 +364,25 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   if (e != cudaSuccess) return e;
   const bool bf = d.dtype == MOE_BF16;
   float2* stat = reinterpret_cast<float2*>(c.ws + c.L.stat);
+  float* at = reinterpret_cast<float*>(c.ws + c.L.at);
   const unsigned grid = (unsigned)((d.M + kLossRows - 1) / kLossRows);
   int first = 0, end = 1;  // the slots to join
   if (bf) {
     const int64_t cols = stat_cols(d);
+    XentEpi epi = {};
+    epi.part = stat + d.M;
+    epi.at = at;
+    epi.target = target;
     for (int64_t v0 = 0; v0 < d.V; v0 += cols) {
       if (v0) {  // what came before, into slot 0
         *launches += 1;
-        MOE_LAUNCH(k_xent_fold, grid, 256, 0, st, stat, first, end, (int)d.M);
+        MOE_LAUNCH(k_xent_fold, grid, kLossWarps * 32, 0, st, stat, first, end, (int)d.M);
       }
       const int n = (int)std::min(cols, d.V - v0);
       int width = 1;
+      epi.v0 = (int)v0;
       *launches += 1;
-      if ((e = launch_xent_stats(c.gemm(v0, n, nullptr), {stat + d.M}, sms, st, &width)) != cudaSuccess) return e;
+      if ((e = launch_xent_stats(c.gemm(v0, n, nullptr), epi, sms, st, &width)) != cudaSuccess) return e;
       first = v0 ? 0 : 1;
       end = 1 + (n + width - 1) / width;
     }
@@ -382,6 +396,7 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   }
   LossArgs a = {};
   a.stat = stat;
+  a.at = at;
   a.first = first;
   a.end = end;
   a.M = (int)d.M;
@@ -401,8 +416,8 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   a.total = total;
   a.status = reinterpret_cast<int*>(c.ws);
   *launches += 1;
-  if (bf) MOE_LAUNCH((k_xent_loss<__nv_bfloat16, true>), grid, 256, 0, st, a);
-  else MOE_LAUNCH((k_xent_loss<float, false>), grid, 256, 0, st, a);
+  if (bf) MOE_LAUNCH((k_xent_loss<__nv_bfloat16, true>), grid, kLossWarps * 32, 0, st, a);
+  else MOE_LAUNCH((k_xent_loss<float, false>), grid, kLossWarps * 32, 0, st, a);
   return cudaSuccess;
 }
 
@@ -414,7 +429,13 @@ cudaError_t launch_xent_bwd(const moe_xent_dims& d, void* ws, const void* x, con
   if (e != cudaSuccess) return e;
   const XentRows r = {target, lse, dloss, total, (int)d.V, d.z_coef};
   const bool bf = d.dtype == MOE_BF16;
-  XentEpi epi = {nullptr, target, lse, dloss, total, d.z_coef, 0, (int)d.V};
+  XentEpi epi = {};
+  epi.target = target;
+  epi.lse = lse;
+  epi.dloss = dloss;
+  epi.total = total;
+  epi.z = d.z_coef;
+  epi.V = (int)d.V;
   for (int64_t v0 = 0; v0 < d.V; v0 += c.P) {
     const int cols = (int)std::min(c.P, d.V - v0);
     *launches += 1;
