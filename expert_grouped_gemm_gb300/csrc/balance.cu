@@ -226,6 +226,12 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
   const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
   const int c0 = (int)blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.T);
   const TL* logits = reinterpret_cast<const TL*>(a.logits) + e0;
+  // towards L2 while the sequences are looked for: a lane 128 bytes of the warp's rows and of the indices
+  for (int t = c0 + warp; t < c1; t += WARPS)
+    if (lane * (128 / (int)sizeof(TL)) < a.E)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E + lane * (128 / sizeof(TL))));
+  for (int64_t i = (int64_t)c0 * a.k + threadIdx.x * 32; i < (int64_t)c1 * a.k; i += WARPS * 32 * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.idx + i));
   for (int s = seq_of(a, c0); s < a.S; ++s) {
     const int b0 = max(c0, seq_at(a, s)), b1 = min(c1, seq_at(a, s + 1));
     if (seq_at(a, s) >= c1) break;
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
 }
 
 // A block 32 experts of a sequence: its rows added; the last block adds the parts of the losses in a fixed order.
-constexpr int kSumWarps = 32;
+template <int kSumWarps>
 __global__ void __launch_bounds__(kSumWarps * 32) k_balance_sum(const BalanceArgs a) {
   __shared__ float sp[kSumWarps][33];
   __shared__ int sn[kSumWarps][33];
@@ -514,7 +520,10 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
     return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true>(d, a, st) : fwd_typed<EPL, false>(d, a, st);
   });
   if (e != cudaSuccess || a.few) return e;
-  MOE_LAUNCH(k_balance_sum, dim3((unsigned)a.S, (unsigned)((a.E + 31) / 32)), kSumWarps * 32, 0, st, a);
+  // a warp for each of a sequence's rows, as far as that goes
+  const dim3 grid((unsigned)a.S, (unsigned)((a.E + 31) / 32));
+  if (a.chunks >= 16 * a.S) MOE_LAUNCH(k_balance_sum<32>, grid, 1024, 0, st, a);
+  else MOE_LAUNCH(k_balance_sum<8>, grid, 256, 0, st, a);
   return cudaSuccess;
 }
 

@@ -100,6 +100,51 @@ struct SimtWork {
   int cluster;    // blocks of a cluster, a multiple of both S
 };
 
+// This block's share of a tile's rows, four columns a thread: the parts' sums (rank0: the tile's first block in its
+// cluster) and the epilogue.
+__device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB], int m0, int n0, int S, int part, int rank0) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const bool vec = g.N % 4 == 0 && g.ldo % 4 == 0;
+  const int n = n0 + tx * 4;
+  for (int r = kSB * part / S + ty; r < kSB * (part + 1) / S; r += kSThreads / 16) {
+    const int m = m0 + r;
+    if (m >= g.M || n >= g.N) break;
+    float z[4] = {0, 0, 0, 0}, y[4];
+    for (int p = 0; p < S; ++p) {
+      float4 v;
+      const uint32_t at = smem_u32(&sums[r][tx * 4]);
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                   : "r"(S > 1 ? mapa_shared(at, rank0 + p) : at));
+      z[0] += v.x;
+      z[1] += v.y;
+      z[2] += v.z;
+      z[3] += v.w;
+    }
+    const int64_t o = (int64_t)m * g.N + n, oy = g.ldo ? (int64_t)m * g.ldo + n : o;
+    if (g.bias)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) z[j] += g.bias[n + j];
+    act_fwd<false, 4>(g.act, z, y);
+    if (g.residual)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) y[j] += g.residual[o + j];
+    if (vec) {
+      if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
+      *reinterpret_cast<float4*>(g.out + oy) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < g.N) {
+          if (g.pre) g.pre[o + j] = z[j];
+          g.out[oy + j] = y[j];
+        }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ __align__(16) float sa[2][kSK][kSB + 4];
@@ -124,8 +169,8 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   const int slabs = (g.K + kSK - 1) / kSK;
   const int s0 = (int)((int64_t)slabs * part / S), s1 = (int)((int64_t)slabs * (part + 1) / S);
   Slab A, B;
-  A.init(g.A, g.sam, g.sak, m0, g.M, g.K, tid);
-  B.init(g.B, g.sbn, g.sbk, n0, g.N, g.K, tid);
+  A.init(g.A, g.sam, g.sak, m0, g.ma, g.ka, tid);
+  B.init(g.B, g.sbn, g.sbk, n0, g.nb, g.kb, tid);
   auto fetch = [&](int s) {
     A.fetch(s);
     B.fetch(s);
@@ -172,46 +217,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   }
   if (work.cluster > 1) cluster_sync_all();
   else __syncthreads();
-  // this block's share of the tile's rows, four columns a thread
-  const bool vec = g.N % 4 == 0 && g.ldo % 4 == 0;
-  const int n = n0 + tx * 4;
-  for (int r = kSB * part / S + ty; r < kSB * (part + 1) / S; r += kSThreads / 16) {
-    const int m = m0 + r;
-    if (m >= g.M || n >= g.N) break;
-    float z[4] = {0, 0, 0, 0}, y[4];
-    for (int p = 0; p < S; ++p) {
-      float4 v;
-      const uint32_t at = smem_u32(&sums[r][tx * 4]);
-      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                   : "r"(S > 1 ? mapa_shared(at, rank0 + p) : at));
-      z[0] += v.x;
-      z[1] += v.y;
-      z[2] += v.z;
-      z[3] += v.w;
-    }
-    const int64_t o = (int64_t)m * g.N + n, oy = g.ldo ? (int64_t)m * g.ldo + n : o;
-    if (g.bias)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n + j < g.N) z[j] += g.bias[n + j];
-    act_fwd<false, 4>(g.act, z, y);
-    if (g.residual)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n + j < g.N) y[j] += g.residual[o + j];
-    if (vec) {
-      if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
-      *reinterpret_cast<float4*>(g.out + oy) = make_float4(y[0], y[1], y[2], y[3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n + j < g.N) {
-          if (g.pre) g.pre[o + j] = z[j];
-          g.out[oy + j] = y[j];
-        }
-    }
-  }
+  finish_rows(g, sums, m0, n0, S, part, rank0);
   if (work.cluster > 1) cluster_sync_all();  // no block leaves while another still reads its sums
 }
 
@@ -419,23 +425,29 @@ __global__ void __launch_bounds__(256) k_pack_rows(const PackArgs a) {
 }  // namespace
 
 // One product or two (count) in one launch.
-cudaError_t launch_linear_f32(const SimtGemm* g, int count, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, cudaStream_t st, int* launches) {
   SimtWork w;
   int64_t tiles[2] = {0, 0};
   int slabs[2] = {0, 0};
   for (int i = 0; i < 2; ++i) {
     w.g[i] = g[i < count ? i : 0];
+    if (!w.g[i].ma) w.g[i].ma = w.g[i].M;
+    if (!w.g[i].nb) w.g[i].nb = w.g[i].N;
+    if (!w.g[i].ka) w.g[i].ka = w.g[i].K;
+    if (!w.g[i].kb) w.g[i].kb = w.g[i].K;
     w.S[i] = 1;
     if (i >= count) continue;
     tiles[i] = (((int64_t)g[i].M + kSB - 1) / kSB) * ((g[i].N + kSB - 1) / kSB);
     slabs[i] = (g[i].K + kSK - 1) / kSK;
   }
   // four blocks fit an SM; the product with the longer parts is split while its blocks still fit beside
-  // the other's; a part keeps at least four slabs
+  // the other's, or (even) while a part of it would outlast the GPU's even share of all slabs; a part keeps at least
+  // four slabs
+  const int64_t slots = (int64_t)sms * 4, share = (tiles[0] * slabs[0] + tiles[1] * slabs[1]) / slots;
   while (true) {
     const int i = count > 1 && (int64_t)slabs[1] * w.S[0] > (int64_t)slabs[0] * w.S[1];
     if (w.S[i] == 8 || slabs[i] < 8 * w.S[i]) break;
-    if (tiles[0] * w.S[0] + tiles[1] * w.S[1] + tiles[i] * w.S[i] > (int64_t)sms * 4) break;
+    if (tiles[0] * w.S[0] + tiles[1] * w.S[1] + tiles[i] * w.S[i] > slots && !(even && slabs[i] / w.S[i] > share)) break;
     w.S[i] *= 2;
   }
   w.cluster = std::max(w.S[0], w.S[1]);
@@ -617,7 +629,7 @@ cudaError_t bwd_f32(const moe_linear_dims& d, char* ws, const void* dy, const vo
   int n = 0;
   if (dx) g[n++] = {f(dz), f(w), N, 1, 1, N, M, N, K, nullptr, f(dx_add), (float*)dx, nullptr, MOE_ACT_NONE};
   if (dw) g[n++] = {f(x), f(dz), 1, K, N, 1, K, M, N, nullptr, nullptr, (float*)dw, nullptr, MOE_ACT_NONE};
-  return launch_linear_f32(g, n, sms, st, launches);
+  return launch_linear_f32(g, n, false, sms, st, launches);
 }
 
 }  // namespace
@@ -630,7 +642,7 @@ cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x,
     return fwd_bf16(d, static_cast<char*>(ws), x, w, bias, residual, y, pre, sms, st, launches);
   SimtGemm g = {f(x), f(w), d.K, 1, d.N, 1, (int)d.M, (int)d.K, (int)d.N, f(bias), f(residual), (float*)y, (float*)pre,
                 d.act};
-  return launch_linear_f32(&g, 1, sms, st, launches);
+  return launch_linear_f32(&g, 1, false, sms, st, launches);
 }
 
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,

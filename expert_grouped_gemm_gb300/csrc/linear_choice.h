@@ -20,6 +20,7 @@ namespace moe {
 // two CTAs share an SM.
 struct LinearChoice {
   int nb, S;  // nb 0: tiles, of 128 x 128 (S = 1) or 256 x 256 on CTA pairs (S = 2)
+  double us;  // the estimate
 };
 
 inline double linear_tile_estimate(int64_t M, int64_t N, int b, int64_t units, int kb, double c0, double ck, double cr) {
@@ -30,12 +31,12 @@ inline double linear_tile_estimate(int64_t M, int64_t N, int b, int64_t units, i
 
 inline LinearChoice choose_linear(int64_t M, int64_t N, int64_t K, bool a_mn, int sms) {
   const int kb = (int)((K + 63) / 64);  // k-blocks of 64
-  LinearChoice best = {0, 1};
+  LinearChoice best = {0, 1, 0.0};
   double t = linear_tile_estimate(M, N, 128, sms, kb, 1.56, 0.302, 1.25);
   const double pair = linear_tile_estimate(M, N, 256, sms / 2, kb, 2.23, 0.300, 3.05);
   if (pair < t) {
     t = pair;
-    best = {0, 2};
+    best = {0, 2, 0.0};
   }
   // an MN-major token matrix is read in chunks of 64 tokens
   for (int nb = a_mn ? 64 : 16; nb <= 64 && (nb < 2 * M || nb == 16 || a_mn); nb *= 2) {
@@ -47,10 +48,11 @@ inline LinearChoice choose_linear(int64_t M, int64_t N, int64_t K, bool a_mn, in
                        shared * (1.81 * rounds + 0.073 * S);
       if (e < t) {
         t = e;
-        best = {nb, S};
+        best = {nb, S, 0.0};
       }
     }
   }
+  best.us = t;
   return best;
 }
 

@@ -17,9 +17,14 @@ struct SimtGemm {
   float* pre;
   int act;
   int64_t ldo = 0;  // row stride of out, 0: N
+  // Where rows are longer in memory: how many of A's rows and B's columns may be read (what lies past M and N is not
+  // used), and how many k of each (zeros in one, numbers in the other). 0: M, N, K. Multiples of 4 are read 16 bytes at
+  // a time.
+  int ma = 0, nb = 0, ka = 0, kb = 0;
 };
 
-// One product or two (count) in one launch.
-cudaError_t launch_linear_f32(const SimtGemm* g, int count, int sms, cudaStream_t st, int* launches);
+// One product or two (count) in one launch. even: a product of few tiles and a long K is split although the other one
+// fills the GPU.
+cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, cudaStream_t st, int* launches);
 
 }  // namespace moe

@@ -10,7 +10,7 @@ cudaError_t launch_tile_as(const LinearGemm& g, int sms, cudaStream_t st) {
   TcWork<1> w;
   if (!fill<CTAS, BN, VEC, F32>(&w, 0, g)) return cudaErrorInvalidValue;
   const int64_t units = sms / CTAS;
-  if (CTAS == 2) halve(&w.p[0], w.p[0].items, units);
+  if (CTAS == 2 && g.parts == 1) halve(&w.p[0], w.p[0].items, units);
   w.rem = w.extra = 0;
   return launch_work<CTAS, BN, VEC, F32>(w, std::min<int64_t>(w.p[0].items, units), st);
 }
@@ -57,6 +57,8 @@ cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
   if (c.nb == 64) return launch_split_nb<64>(g, c.S, st);
   return c.S == 2 ? launch_tile<2, 256>(g, sms, st) : launch_tile<1, 128>(g, sms, st);
 }
+
+cudaError_t launch_linear_parts(const LinearGemm& g, int sms, cudaStream_t st) { return launch_tile<2, 256>(g, sms, st); }
 
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches) {
   const LinearChoice c0 = choose_linear(g0.M, g0.N, g0.K, g0.a_mn, sms);

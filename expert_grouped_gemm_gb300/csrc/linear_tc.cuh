@@ -230,6 +230,18 @@ __device__ __forceinline__ Item item_at(const TcArgs& a, int t) {
   return it;
 }
 
+// The k-blocks of item *t, and *t without its part of K.
+struct Span {
+  int k0, k1, part;
+};
+template <bool PARTS>
+__device__ __forceinline__ Span span_at(const TcArgs& a, int* t) {
+  if (!PARTS || a.g.parts == 1) return {0, a.kblocks, 0};
+  const int tiles = a.mt * a.nt, part = *t / tiles;
+  *t -= part * tiles;
+  return {(int)((int64_t)a.kblocks * part / a.g.parts), (int)((int64_t)a.kblocks * (part + 1) / a.g.parts), part};
+}
+
 // Sixteen z of a row as bf16: one 32-byte store where `wide`, else a 16-byte store for each half that exists.
 __device__ __forceinline__ void store_z16(__nv_bfloat16* p, const float* z, int left, bool wide) {
   if (left <= 0) return;
@@ -312,12 +324,13 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       const TcArgs& args = work.p[prod];
       const LinearGemm& g = args.g;
       const CUtensorMap *tmA = &work.A[prod], *tmB = &work.B[prod];
+      const Span k = span_at<F32>(args, &t);
       const Item it = item_at<BN>(args, t);
       const int m0 = it.m * C::TILE_M + (int)rank * 128;
       const int bcols = it.half ? C::BCOLS / 2 : C::BCOLS;
       const int n0 = it.n0 + (int)rank * bcols;
       const uint32_t bytes = C::A_BYTES + bcols * kBK * 2;
-      for (int kb = 0; kb < args.kblocks; ++kb) {
+      for (int kb = k.k0; kb < k.k1; ++kb) {
         if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) {
           ok = false;
           break;
@@ -379,8 +392,9 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       if (!free_acc) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+      const Span k = span_at<F32>(args, &t);
       idesc = idesc_bf16(C::TILE_M, t >= args.whole ? BN / 2 : BN, g.a_mn, g.b_mn);
-      for (int kb = 0; kb < args.kblocks; ++kb) {
+      for (int kb = k.k0; kb < k.k1; ++kb) {
         if (!mbar_wait_bounded(&full[stage], phase, abort_flag)) {
           ok = false;
           break;
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         tc_fence_after();
         const uint64_t ad = ad0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
         const uint64_t bd = bd0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
-        mma(d, ad, bd, kb != 0 ? 1u : 0u);
+        mma(d, ad, bd, kb != k.k0 ? 1u : 0u);
         mma(d, ad + as, bd + bs, 1u);
         mma(d, ad + 2 * as, bd + 2 * bs, 1u);
         mma(d, ad + 3 * as, bd + 3 * bs, 1u);
@@ -419,6 +433,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       const LinearGemm& g = args.g;
       const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
       const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
+      const int part = span_at<F32>(args, &t).part;
       const Item it = item_at<BN>(args, t);
       const int cw = BN / 64 / (it.half ? 4 : 2);  // 64-column chunks of this warp
       const int c0 = (ew / 4) * cw;
@@ -541,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) st_shared_v4(ty + piece(lane, j), f_to_bf16x8(z + 8 * j));
         } else if (lane < rows) {
-          float* o = reinterpret_cast<float*>(g.y) + (row0 + lane) * g.ldy + n0;
+          float* o = reinterpret_cast<float*>(g.y) + (part * (int64_t)g.M + row0 + lane) * g.ldy + n0;
           if (g.add) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
@@ -940,8 +955,8 @@ bool fill(TcWork<N>* w, int i, const LinearGemm& g) {
   a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
   a.nt = (g.N + BN - 1) / BN;
   const int64_t total = (int64_t)a.mt * a.nt;
-  if (!ok || total >= (1ll << 30)) return false;
-  a.items = a.whole = (int)total;
+  if (!ok || total * g.parts >= (1ll << 30)) return false;
+  a.items = a.whole = (int)total * g.parts;
   return true;
 }
 

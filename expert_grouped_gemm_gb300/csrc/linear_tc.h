@@ -22,6 +22,7 @@ struct LinearGemm {
   int* status;           // receives MOE_ERR_TIMEOUT when a wait runs out
   int64_t ldy = 0;       // row stride of y, 0: N
   int add = 0;           // with out_f32: added to what y holds
+  int parts = 1;         // with out_f32, launch_linear_parts: K in so many parts, whose sums go to y + part * M * ldy
 };
 
 // What the epilogues of the cross entropy read and write beside a product l[M, N] of logits, columns v0 .. v0 + N - 1 of
@@ -42,6 +43,8 @@ cudaError_t launch_xent_stats(const LinearGemm& g, const XentEpi& x, int sms, cu
 cudaError_t launch_xent_grad(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st);
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st);
+// A product of few tiles and a long K on CTA pairs, K in g.parts parts (out_f32).
+cudaError_t launch_linear_parts(const LinearGemm& g, int sms, cudaStream_t st);
 // Two independent products (neither reads what the other writes), in one launch where both are large.
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches);
 

@@ -5,7 +5,9 @@
 //
 // Bound by HBM: every value is read once and written once. The tensors' descriptions travel as kernel arguments, so
 // that a launch needs no table on the device and a captured one keeps its own. The values of all tensors are cut into
-// chunks that never cross a tensor; persistent blocks walk them.
+// chunks that never cross a tensor. With 32 bits a block takes one chunk (604M values in 2.40 ms, 7.1 TB/s; resident
+// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (34 a value), resident blocks walk them
+// (1.00 ms, 6.1 TB/s; a block each 1.03, two blocks' loads in flight against one 1.05).
 //
 // 8 bits: m and r = sqrt(v) are held as e4m3 (3 bits of mantissa, 17 powers of two) over a float for each 256 values,
 // their largest magnitude / 448. The root halves the span of exponents that v has. An r above zero never becomes zero:
@@ -45,15 +47,18 @@ struct Entry {
   float lr_scale, wd;
 };
 
+constexpr int kMap = 1024;
 template <int N>
 struct Table {
   uint32_t count, chunks;
+  uint16_t map[kMap];  // a chunk's tensor, where there are no more chunks: a search would wait for every step
   Entry e[N];
 };
 
 // The tensor of a chunk, from the one that an earlier chunk was in.
 template <int N>
 __device__ __forceinline__ uint32_t tensor_of(const Table<N>& t, uint32_t chunk, uint32_t at) {
+  if (t.chunks <= kMap) return t.map[chunk];
   uint32_t lo = at, hi = t.count;
   if (at + 1 == hi || t.e[at + 1].first > chunk) return at;
   while (hi - lo > 1) {
@@ -71,7 +76,7 @@ template <>
 struct Four<true> {
   uint2 u;
   __device__ __forceinline__ void load(const void* a, int64_t i) {
-    u = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a) + i));
+    u = __ldcg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a) + i));
   }
   __device__ __forceinline__ void get(float (&f)[4]) const {
     f[0] = __uint_as_float(u.x << 16);
@@ -81,7 +86,7 @@ struct Four<true> {
   }
   static __device__ __forceinline__ void store(void* a, int64_t i, const float (&f)[4]) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-    __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a) + i),
+    __stcg(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a) + i),
            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y)));
   }
 };
@@ -89,7 +94,7 @@ template <>
 struct Four<false> {
   float4 u;
   __device__ __forceinline__ void load(const void* a, int64_t i) {
-    u = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(a) + i));
+    u = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(a) + i));
   }
   __device__ __forceinline__ void get(float (&f)[4]) const {
     f[0] = u.x;
@@ -98,7 +103,7 @@ struct Four<false> {
     f[3] = u.w;
   }
   static __device__ __forceinline__ void store(void* a, int64_t i, const float (&f)[4]) {
-    __stcs(reinterpret_cast<float4*>(static_cast<float*>(a) + i), make_float4(f[0], f[1], f[2], f[3]));
+    __stcg(reinterpret_cast<float4*>(static_cast<float*>(a) + i), make_float4(f[0], f[1], f[2], f[3]));
   }
 };
 
@@ -234,8 +239,8 @@ __device__ __forceinline__ void whole_blocks(const Entry& e, const Factors& k, i
         m[s][h].load(e.m, i + h * 128);
         v[s][h].load(e.v, i + h * 128);
       } else {
-        mc[s][h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.m) + i + h * 128));
-        vc[s][h] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.v) + i + h * 128));
+        mc[s][h] = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.m) + i + h * 128));
+        vc[s][h] = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(e.v) + i + h * 128));
       }
     }
     sm[s] = BITS == 8 ? e.ms[b] : 1.0f;
@@ -270,8 +275,8 @@ __device__ __forceinline__ void whole_blocks(const Entry& e, const Factors& k, i
       pack_block(e, b, lane, mf, vf, mo, vo);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + i + h * 128), mo[h]);
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + i + h * 128), vo[h]);
+        __stcg(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.m) + i + h * 128), mo[h]);
+        __stcg(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(e.v) + i + h * 128), vo[h]);
       }
     }
   }
@@ -346,7 +351,7 @@ __device__ __forceinline__ void last_block(const Entry& e, const Factors& k, int
 }
 
 template <int BITS, int N>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Table<N> tab, const AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ Table<N> tab, const AdamWArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   float gs = a.wide, lr = a.lr, bc1 = a.bc1, bc2 = a.bc2;
   if (a.norm) {
@@ -399,7 +404,7 @@ __device__ __forceinline__ float squares(const void* g, int n) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = i + j * kThreads + threadIdx.x;
-      u[j] = at < vecs ? __ldcs(p + at) : make_uint4(0, 0, 0, 0);
+      u[j] = at < vecs ? __ldcg(p + at) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kMany = 384, kSome = 128, kFew = 24;  // 80 bytes a tensor: kernel arguments hold 32764
+constexpr int kMany = 376, kSome = 128, kFew = 24;  // 80 bytes a tensor: kernel arguments hold 32764
 static_assert(sizeof(Table<kMany>) + sizeof(AdamWArgs) <= 32764, "kernel arguments");
 constexpr int kNormBlocks = 2048;  // at most, whatever the device
 
@@ -494,10 +499,14 @@ int64_t fill(Table<N>* t, const moe_adamw_tensor* list, int64_t count, int64_t c
     chunks += c;
   }
   t->chunks = (uint32_t)chunks;
+  if (chunks <= kMap)
+    for (uint32_t j = 0; j < t->count; ++j)
+      for (uint32_t c = t->e[j].first, end = j + 1 < t->count ? t->e[j + 1].first : t->chunks; c < end; ++c) t->map[c] = (uint16_t)j;
   return i;
 }
 
-// As many blocks as are resident at once: one more round of blocks would double the time of a persistent kernel.
+// As many blocks as are resident at once, for kernels whose blocks walk many chunks: one more round of blocks would
+// double their time.
 template <typename K>
 int grid_of(K kernel, uint32_t chunks, int sms) {
   int per = 0;
@@ -516,7 +525,7 @@ cudaError_t adamw_launches(int bits, const AdamWArgs& a, const moe_adamw_tensor*
     if (!t.count) continue;
     *launches += 1;
     if (bits == 8) MOE_LAUNCH((k_adamw<8, N>), grid_of(k_adamw<8, N>, t.chunks, sms), kThreads, 0, st, t, a);
-    else MOE_LAUNCH((k_adamw<32, N>), grid_of(k_adamw<32, N>, t.chunks, sms), kThreads, 0, st, t, a);
+    else MOE_LAUNCH((k_adamw<32, N>), t.chunks, kThreads, 0, st, t, a);
   }
   return cudaSuccess;
 }

@@ -12,6 +12,7 @@
 
 #include "block.h"
 #include "common.cuh"
+#include "linear_choice.h"
 #include "linear_f32.h"
 #include "linear_tc.h"
 
@@ -20,6 +21,8 @@ namespace {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+// a row length up to a multiple of 16 bytes
+int64_t up_row(const moe_xent_dims& d, int64_t n) { return d.dtype == MOE_BF16 ? up8(n) : (n + 3) / 4 * 4; }
 
 // (m, s) joined with (m2, s2): s e^m is the sum of both.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
@@ -108,10 +111,8 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_fold(float2* stat, int
 struct LossArgs {
   const float2* stat;  // [slots][M]
   const float* at;     // BASE2: [M], the targets' logits as the product has them
-  int first, end, M, H, V;
-  const void* x;
-  const void* w;
-  int64_t ldx, swh, swv;  // w[h, v] at h * swh + v * swv
+  const float* dots;   // [M][parts]
+  int first, end, M, V, parts;
   const int* target;
   float z;
   float* loss;
@@ -122,30 +123,45 @@ struct LossArgs {
   int* status;
 };
 
-// lse and loss of eight rows a block, four warps a row for the target's logit in fp32; where the product's own is given,
-// the sum of exponentials is put right by the difference. The blocks' totals are added in order by the last one.
-template <typename T, bool BASE2>
+// The targets' logits in fp32, a warp 256 features of a row; a kernel of its own, so that the columns of w, a line for
+// every feature, are fetched by all SMs (8 rows of 2048 features: 20 us in one block of k_xent_loss, 3 us here).
+constexpr int kDotCols = 256;
+template <typename T>
+__global__ void __launch_bounds__(256) k_xent_dots(const T* x, const T* w, int64_t ldx, int64_t swh, int64_t swv,
+                                                   const int* target, int M, int H, int V, int parts, float* dots) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t t = at / parts;
+  if (t >= M) return;
+  const int v = target[t], h0 = (int)(at - t * parts) * kDotCols;
+  float dot = 0.0f;
+  if (v >= 0 && v < V) {
+    x += t * ldx;
+    w += v * swv;
+    float a[kDotCols / 32], b[kDotCols / 32];
+#pragma unroll
+    for (int i = 0; i < kDotCols / 32; ++i) {
+      const int h = h0 + i * 32 + lane;
+      a[i] = h < H ? io<T>::to_f(x[h]) : 0.0f;
+      b[i] = h < H ? io<T>::to_f(w[h * swh]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kDotCols / 32; ++i) dot = fmaf(a[i], b[i], dot);
+    dot = warp_sum(dot);
+  }
+  if (lane == 0) dots[at] = dot;
+}
+
+// lse and loss of eight rows a block. Where the product's own logit of the target is given, the sum of exponentials is put
+// right by its difference to the fp32 one. The blocks' totals are added in order by the last one.
+template <bool BASE2>
 __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  constexpr int kParts = kLossWarps / kLossRows;
   __shared__ float2 red[kLossWarps][kLossRows];
-  __shared__ float dots[kLossRows][kParts];
   __shared__ bool last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
-  const int row = warp / kParts, part = warp % kParts;
-  if (t0 + row < a.M) {
-    const int v = a.target[t0 + row];
-    float dot = 0.0f;
-    if (v >= 0 && v < a.V) {
-      const T* x = static_cast<const T*>(a.x) + (t0 + row) * a.ldx;
-      const T* w = static_cast<const T*>(a.w) + v * a.swv;
-#pragma unroll 16
-      for (int h = part * 32 + lane; h < a.H; h += 32 * kParts) dot = fmaf(io<T>::to_f(x[h]), io<T>::to_f(w[h * a.swh]), dot);
-      dot = warp_sum(dot);
-    }
-    if (lane == 0) dots[row][part] = dot;
-  }
   const float2 st = join_slots<BASE2>(a.stat, a.first, a.end, a.M, t0, red);
   float sum = 0.0f, n = 0.0f;
   if (threadIdx.x < kLossRows && t0 + threadIdx.x < a.M) {
@@ -153,9 +169,8 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a)
     const int v = a.target[t0 + threadIdx.x];
     if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
     if (v >= 0 && v < a.V) {
-      float at = dots[threadIdx.x][0];
-#pragma unroll
-      for (int i = 1; i < kParts; ++i) at += dots[threadIdx.x][i];
+      float at = 0.0f;
+      for (int i = 0; i < a.parts; ++i) at += a.dots[(t0 + threadIdx.x) * a.parts + i];
       if (BASE2) e += log1pf(expf(at - e) - expf(a.at[t0 + threadIdx.x] - e));
       sum = e - at + a.z * e * e;
       n = 1.0f;
@@ -216,27 +231,40 @@ __device__ __forceinline__ float row_grad(const XentRows& r, int64_t t) {
   return r.dloss ? r.dloss[t] : 1.0f / r.total[1];
 }
 
-// dl of a piece in place of its logits (fp32), a block 1024 columns of a row.
+// dl of a piece in place of its logits (fp32), a block 1024 columns of a row; zeros up to a multiple of four.
 __global__ void __launch_bounds__(256) k_xent_dl(float* l, int64_t ld, int cols, int v0, XentRows r) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int64_t t = blockIdx.x;
   const float d = row_grad(r, t), lse = r.lse[t], f = d * (1.0f + 2.0f * r.z * lse);
   const int at = r.target[t] - v0;
-  for (int i = blockIdx.y * 1024 + threadIdx.x; i < min(cols, ((int)blockIdx.y + 1) * 1024); i += 256) {
-    const float p = d == 0.0f ? 0.0f : expf(l[t * ld + i] - lse) * f;
+  for (int i = blockIdx.y * 1024 + threadIdx.x; i < min((cols + 3) / 4 * 4, ((int)blockIdx.y + 1) * 1024); i += 256) {
+    const float p = d == 0.0f || i >= cols ? 0.0f : expf(l[t * ld + i] - lse) * f;
     l[t * ld + i] = i == at ? p - d : p;
   }
 }
 
-__global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat16* o, int64_t n) {
+// dx from the sums of `parts` parts of K, in order.
+__global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat16* o, int64_t n, int parts) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
-    if (i + 8 <= n) {
-      const float4 x = *reinterpret_cast<const float4*>(a + i), y = *reinterpret_cast<const float4*>(a + i + 4);
-      const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      *reinterpret_cast<uint4*>(o + i) = f_to_bf16x8(f);
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n % 4 == 0) {  // a part begins at a 16-byte boundary
+#pragma unroll 4
+      for (int p = 0; p < parts; ++p) {
+        const float4 v = *reinterpret_cast<const float4*>(a + p * n + i);
+        f[0] += v.x;
+        f[1] += v.y;
+        f[2] += v.z;
+        f[3] += v.w;
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+      *reinterpret_cast<uint2*>(o + i) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     } else {
-      for (int64_t j = i; j < n; ++j) o[j] = __float2bfloat16_rn(a[j]);
+      for (int64_t j = i; j < min(n, i + 4); ++j) {
+        float v = 0.0f;
+        for (int p = 0; p < parts; ++p) v += a[p * n + j];
+        o[j] = __float2bfloat16_rn(v);
+      }
     }
   }
 }
@@ -247,6 +275,29 @@ int64_t piece_cols(const moe_xent_dims& d) {
   const int64_t want = std::max<int64_t>(1024, (1 << (d.dtype == MOE_BF16 ? 26 : 24)) / d.M / 256 * 256);
   return std::min(want, up8(d.V));
 }
+// Parts of K of a piece's dx product in bf16: its K is a piece of the vocabulary and its tiles may be few. 0: as
+// launch_linear_tc does it, which is as good or better; else pairs of CTAs, each with a tile's part, whose fp32 sums are
+// added afterwards (777 x 1000 over 50001 columns: 16 tiles for 76 pairs, 200 -> 70 us in 4 parts). Estimates as in
+// linear_choice.h; a part costs its sums' way to memory and back.
+int dx_parts(const moe_xent_dims& d) {
+  constexpr int kSms = 152, kUnits = kSms / 2;
+  const int64_t P = piece_cols(d);
+  const int kb = (int)((std::min(P, d.V) + 63) / 64);
+  const bool whole = P >= d.V;
+  const double sums = (double)d.M * d.H * (whole ? 8 : 12) / 6.0e6;
+  int best = 0;
+  double t = choose_linear(d.M, d.H, std::min(P, d.V), false, kSms).us + (whole ? 0.0 : sums);
+  const int64_t tiles = ((d.M + 255) / 256) * ((d.H + 255) / 256);
+  for (int p = 1; p <= 16 && kb / p >= 8; ++p) {
+    const double rounds = (double)((tiles * p + kUnits - 1) / kUnits);
+    const double e = 2.23 + rounds * (0.300 * ((kb + p - 1) / p) + 3.05) + p * sums + (whole ? 3.0 : 0.0);
+    if (e < t) {
+      t = e;
+      best = p;
+    }
+  }
+  return best;
+}
 constexpr int kSlotCols = 64;  // the narrowest slot of the statistics
 // Columns of a forward product in bf16: its statistics (with those of the columns before) stay below 256 MB, or 1 KB a row.
 int64_t stat_cols(const moe_xent_dims& d) {
@@ -256,7 +307,7 @@ int64_t stat_cols(const moe_xent_dims& d) {
 // Workspace: header, the rows' statistics, a piece's logits (fp32) or dl, dx in fp32, and copies of x and w with rows of a
 // multiple of 16 bytes where the caller's are not.
 struct XentWs {
-  size_t stat, at, part, piece, dx, xp, wp, total;
+  size_t stat, at, dots, part, piece, dx, xp, wp, total;
 };
 XentWs layout(const moe_xent_dims& d, bool backward) {
   const bool bf = d.dtype == MOE_BF16;
@@ -270,11 +321,14 @@ XentWs layout(const moe_xent_dims& d, bool backward) {
   };
   L.stat = take((size_t)d.M * 8 * (bf ? 1 + (stat_cols(d) + kSlotCols - 1) / kSlotCols : 1));
   L.at = take(bf ? (size_t)d.M * 4 : 0);
+  L.dots = take((size_t)d.M * ((d.H + kDotCols - 1) / kDotCols) * 4);
   L.part = take((size_t)((d.M + kLossRows - 1) / kLossRows) * 8);
-  L.xp = take(bf && d.H % 8 ? (size_t)d.M * up8(d.H) * 2 : 0);
-  L.wp = take(bf && C % 8 ? (size_t)R * up8(C) * 2 : 0);
+  const size_t es = bf ? 2 : 4;
+  L.xp = take(up_row(d, d.H) != d.H ? (size_t)d.M * up_row(d, d.H) * es : 0);
+  L.wp = take(up_row(d, C) != C ? (size_t)R * up_row(d, C) * es : 0);
   L.piece = take(bf ? (backward ? (size_t)d.M * P * 2 : 0) : (size_t)d.M * P * 4);
-  L.dx = take(backward && bf && d.V > P ? (size_t)d.M * d.H * 4 : 0);
+  const int parts = bf ? dx_parts(d) : 0;
+  L.dx = take(backward && bf && (parts || d.V > P) ? (size_t)d.M * d.H * 4 * std::max(parts, 1) : 0);
   L.total = o;
   return L;
 }
@@ -294,12 +348,17 @@ struct Xent {
   cudaError_t prepare() {
     P = piece_cols(d);
     const bool bf = d.dtype == MOE_BF16;
-    ldx = bf ? up8(d.H) : d.H;
-    ldw = d.tied ? ldx : bf ? up8(d.V) : d.V;
-    if (!bf) return cudaSuccess;
-    cudaError_t e = launch_pack_rows(&x, ws + L.xp, d.M, d.H, sms, st, launches);
-    if (e != cudaSuccess) return e;
-    return launch_pack_rows(&w, ws + L.wp, d.tied ? d.V : d.H, d.tied ? d.H : d.V, sms, st, launches);
+    ldx = up_row(d, d.H);
+    ldw = d.tied ? ldx : up_row(d, d.V);
+    const int u = bf ? 1 : 2;  // a float is copied as two halves of itself
+    const int64_t R = d.tied ? d.V : d.H, C = d.tied ? d.H : d.V;
+    cudaError_t e = launch_pack_rows(&x, ws + L.xp, d.M, d.H * u, sms, st, launches);
+    if (e == cudaSuccess) e = launch_pack_rows(&w, ws + L.wp, R, C * u, sms, st, launches);
+    // fp32: the ends of the copies' rows are read beside zeros, and are zeros (TMA does not read them)
+    if (e == cudaSuccess && !bf && ldx != d.H)
+      e = cudaMemset2DAsync(ws + L.xp + d.H * 4, ldx * 4, 0, (ldx - d.H) * 4, d.M, st);
+    if (e == cudaSuccess && !bf && ldw != C) e = cudaMemset2DAsync(ws + L.wp + C * 4, ldw * 4, 0, (ldw - C) * 4, R, st);
+    return e;
   }
   const void* w_at(int64_t v0) const {
     return static_cast<const char*>(w) + (d.tied ? v0 * ldw : v0) * (d.dtype == MOE_BF16 ? 2 : 4);
@@ -311,10 +370,14 @@ struct Xent {
   }
   cudaError_t logits_f32(int64_t v0, int cols) {
     const int M = (int)d.M, H = (int)d.H;
-    SimtGemm g = {static_cast<const float*>(x), static_cast<const float*>(w_at(v0)), H, 1, d.tied ? 1 : ldw,
-                  d.tied ? ldw : 1, M, H, cols, nullptr, nullptr, piece(), nullptr, MOE_ACT_NONE, P};
-    return launch_linear_f32(&g, 1, sms, st, launches);
+    // w[H,V]: with the zeros at the ends of its rows as columns of their own
+    SimtGemm g = {static_cast<const float*>(x), static_cast<const float*>(w_at(v0)), ldx, 1, d.tied ? 1 : ldw,
+                  d.tied ? ldw : 1, M, H, d.tied ? cols : up4(cols), nullptr, nullptr, piece(), nullptr, MOE_ACT_NONE, P};
+    g.ka = (int)ldx;
+    if (d.tied) g.kb = (int)ldw;
+    return launch_linear_f32(&g, 1, true, sms, st, launches);
   }
+  static int up4(int n) { return (n + 3) / 4 * 4; }
   float* piece() const { return reinterpret_cast<float*>(ws + L.piece); }
   cudaError_t products(int64_t v0, int cols, void* dx, void* dw) {
     const int M = (int)d.M, H = (int)d.H;
@@ -322,9 +385,11 @@ struct Xent {
       int* status = reinterpret_cast<int*>(ws);
       const void* dl = ws + L.piece;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dw) + (dw ? (d.tied ? v0 * d.H : v0) : 0);
-      const bool whole = P >= d.V;
-      LinearGemm gx = {M, H, cols, dl, w_at(v0), P, ldw, 0, d.tied, nullptr, nullptr, whole ? dx : ws + L.dx, nullptr,
-                       MOE_ACT_NONE, !whole, status, 0, v0 > 0};
+      const int parts = dx_parts(d);
+      const bool direct = P >= d.V && !parts;
+      LinearGemm gx = {M, H, cols, dl, w_at(v0), P, ldw, 0, d.tied, nullptr, nullptr, direct ? dx : ws + L.dx, nullptr,
+                       MOE_ACT_NONE, !direct, status, H, v0 > 0};
+      if (parts) gx.parts = std::min(parts, (cols + 63) / 64);
       LinearGemm gw = d.tied ? LinearGemm{cols, H, M, dl, x, P, ldx, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE,
                                           0, status}
                              : LinearGemm{H, cols, M, x, dl, ldx, P, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE,
@@ -332,7 +397,7 @@ struct Xent {
       cudaError_t e = cudaSuccess;
       if (dx) {
         *launches += 1;
-        e = launch_linear_tc(gx, sms, st);
+        e = parts ? launch_linear_parts(gx, sms, st) : launch_linear_tc(gx, sms, st);
       }
       if (dw && e == cudaSuccess) {
         *launches += 1;
@@ -345,11 +410,24 @@ struct Xent {
     float* out = static_cast<float*>(dw) + (dw ? (d.tied ? v0 * d.H : v0) : 0);
     SimtGemm g[2];
     int n = 0;
-    if (dx) g[n++] = {dl, fw, P, 1, d.tied ? ldw : 1, d.tied ? 1 : ldw, M, cols, H, nullptr,
-                      v0 ? static_cast<const float*>(dx) : nullptr, static_cast<float*>(dx), nullptr, MOE_ACT_NONE};
-    if (dw && d.tied) g[n++] = {dl, fx, 1, P, ldx, 1, cols, M, H, nullptr, nullptr, out, nullptr, MOE_ACT_NONE};
-    if (dw && !d.tied) g[n++] = {fx, dl, 1, ldx, P, 1, H, M, cols, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, d.V};
-    return launch_linear_f32(g, n, sms, st, launches);
+    if (dx) {
+      g[n] = {dl, fw, P, 1, d.tied ? ldw : 1, d.tied ? 1 : ldw, M, cols, H, nullptr,
+              v0 ? static_cast<const float*>(dx) : nullptr, static_cast<float*>(dx), nullptr, MOE_ACT_NONE};
+      g[n].ka = up4(cols);  // dl ends in zeros
+      if (d.tied) g[n].nb = (int)ldw;
+      else g[n].kb = up4(cols);
+      ++n;
+    }
+    if (dw && d.tied) {
+      g[n] = {dl, fx, 1, P, ldx, 1, cols, M, H, nullptr, nullptr, out, nullptr, MOE_ACT_NONE};
+      g[n].ma = up4(cols);
+      g[n++].nb = (int)ldx;
+    } else if (dw) {
+      g[n] = {fx, dl, 1, ldx, P, 1, H, M, cols, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, d.V};
+      g[n].ma = (int)ldx;
+      g[n++].nb = up4(cols);
+    }
+    return launch_linear_f32(g, n, true, sms, st, launches);
   }
 };
 
@@ -366,6 +444,15 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   float2* stat = reinterpret_cast<float2*>(c.ws + c.L.stat);
   float* at = reinterpret_cast<float*>(c.ws + c.L.at);
   const unsigned grid = (unsigned)((d.M + kLossRows - 1) / kLossRows);
+  float* dots = reinterpret_cast<float*>(c.ws + c.L.dots);
+  const int parts = (int)((d.H + kDotCols - 1) / kDotCols);
+  const int64_t swh = d.tied ? 1 : c.ldw, swv = d.tied ? c.ldw : 1, warps = d.M * parts;
+  if (warps / 8 >= (1ll << 31) - 1) return cudaErrorInvalidValue;
+  *launches += 1;
+  if (bf) MOE_LAUNCH(k_xent_dots<__nv_bfloat16>, (unsigned)((warps + 7) / 8), 256, 0, st, (const __nv_bfloat16*)c.x,
+                     (const __nv_bfloat16*)c.w, c.ldx, swh, swv, target, (int)d.M, (int)d.H, (int)d.V, parts, dots);
+  else MOE_LAUNCH(k_xent_dots<float>, (unsigned)((warps + 7) / 8), 256, 0, st, (const float*)c.x, (const float*)c.w, c.ldx,
+                  swh, swv, target, (int)d.M, (int)d.H, (int)d.V, parts, dots);
   int first = 0, end = 1;  // the slots to join
   if (bf) {
     const int64_t cols = stat_cols(d);
@@ -400,13 +487,9 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   a.first = first;
   a.end = end;
   a.M = (int)d.M;
-  a.H = (int)d.H;
   a.V = (int)d.V;
-  a.x = c.x;
-  a.w = c.w;
-  a.ldx = c.ldx;
-  a.swh = d.tied ? 1 : c.ldw;
-  a.swv = d.tied ? c.ldw : 1;
+  a.dots = dots;
+  a.parts = parts;
   a.target = target;
   a.z = d.z_coef;
   a.loss = loss;
@@ -416,8 +499,8 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   a.total = total;
   a.status = reinterpret_cast<int*>(c.ws);
   *launches += 1;
-  if (bf) MOE_LAUNCH((k_xent_loss<__nv_bfloat16, true>), grid, kLossWarps * 32, 0, st, a);
-  else MOE_LAUNCH((k_xent_loss<float, false>), grid, kLossWarps * 32, 0, st, a);
+  if (bf) MOE_LAUNCH(k_xent_loss<true>, grid, kLossWarps * 32, 0, st, a);
+  else MOE_LAUNCH(k_xent_loss<false>, grid, kLossWarps * 32, 0, st, a);
   return cudaSuccess;
 }
 
@@ -448,11 +531,12 @@ cudaError_t launch_xent_bwd(const moe_xent_dims& d, void* ws, const void* x, con
     }
     if ((e = c.products(v0, cols, dx, dw)) != cudaSuccess) return e;
   }
-  if (bf && dx && c.P < d.V) {
+  const int parts = bf ? dx_parts(d) : 0;
+  if (bf && dx && (parts || c.P < d.V)) {
     *launches += 1;
     const int64_t n = d.M * d.H;
-    MOE_LAUNCH(k_xent_round, (unsigned)std::min<int64_t>((n + 2047) / 2048, (int64_t)sms * 16), 256, 0, st,
-               (const float*)(c.ws + c.L.dx), static_cast<__nv_bfloat16*>(dx), n);
+    MOE_LAUNCH(k_xent_round, (unsigned)std::min<int64_t>((n + 1023) / 1024, (int64_t)sms * 16), 256, 0, st,
+               (const float*)(c.ws + c.L.dx), static_cast<__nv_bfloat16*>(dx), n, std::max(parts, 1));
   }
   return cudaSuccess;
 }
