@@ -717,9 +717,13 @@ def make_adamw_tensors(params, grads, m, v, master=None, m_scale=None, v_scale=N
                                    _flat(m[i], "m", i, state, size), _flat(v[i], "v", i, state, size), *scales, size,
                                    _code(params[i]), _code(grads[i]), lrs[i], decay[i]))
         written += [t for t in (params[i], m[i], v[i], master[i], m_scale[i], v_scale[i]) if t is not None and t.numel()]
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written)
-    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-        raise ValueError("weights or states overlap: every tensor may be listed once")
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w)
+                   for w, ts in ((1, written), (0, grads)) for t in ts if t.numel())
+    last, last_written = 0, 0  # where what came before ends
+    for a, b, w in spans:
+        if a < (last if w else last_written):
+            raise ValueError("weights, states or gradients overlap: every tensor may be listed once")
+        last, last_written = max(last, b), max(last_written, b if w else 0)
     return TensorList(entries, (params, grads, m, v, master, m_scale, v_scale), bits,
                       params[0].get_device() if n else None)
 

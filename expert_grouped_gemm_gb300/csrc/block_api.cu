@@ -331,6 +331,8 @@ int moe_xent_fwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, void* str
       (rc = check_ptr(target, "target", true, 4)) || (rc = check_ptr(loss, "loss", true, 4)) ||
       (rc = check_ptr(lse, "lse", true, 4)) || (rc = check_ptr(total, "total", false, 4)))
     return rc;
+  if (loss == lse || (total && (total == loss || total == lse)))
+    return bad(MOE_ERR_INVALID_ARG, "loss, lse and total must be different buffers");
   int n = 0;
   const cudaError_t e = launch_xent_fwd(*dims, ws, x, w, target, loss, lse, total, sm_count(),
                                         static_cast<cudaStream_t>(stream), &n);
@@ -348,6 +350,8 @@ int moe_xent_bwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, void* str
     return rc;
   if (dloss && total) return bad(MOE_ERR_INVALID_ARG, "give dloss or total, not both");
   if (!dx && !dw) return bad(MOE_ERR_INVALID_ARG, "dx and dw are both null");
+  if ((dx && (dx == x || dx == w || dx == dw)) || (dw && (dw == x || dw == w)))
+    return bad(MOE_ERR_INVALID_ARG, "dx and dw must be buffers of their own");
   int n = 0;
   const cudaError_t e = launch_xent_bwd(*dims, ws, x, w, target, lse, dloss, total, dx, dw, sm_count(),
                                         static_cast<cudaStream_t>(stream), &n);

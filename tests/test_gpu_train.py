@@ -178,8 +178,8 @@ def test_xent(M, H, V, dtype, tied):
 
 @pytest.mark.parametrize("M,V", [(600, 70000), (2100, 20000), (5000, 9000), (16, 140000)])
 @pytest.mark.parametrize("tied", [False, True])
-def test_xent_several_pieces(M, V, tied):
-    """More of the vocabulary than a piece holds: sums carried from piece to piece, a ragged last one."""
+def test_xent_many_columns(M, V, tied):
+    """Many tiles of the vocabulary, ragged last ones, K in parts (pieces of it: test_gpu_train_edges.py)."""
     c = C.xent_case(M, 40, V, "bf16", tied, z=1e-3, seed=M)
     out = C.run_xent_fwd(c)
     C.check_xent_fwd(c, out)
@@ -463,6 +463,14 @@ def test_adamw_refusals():
     with pytest.raises(ValueError, match="overlap"):
         p = f()
         _lib.make_adamw_tensors([p, p], [f(), f()], [f(), f()], [f(), f()])
+    with pytest.raises(ValueError, match="overlap"):  # a state in the gradient's buffer
+        g = f()
+        _lib.make_adamw_tensors([f()], [g], [g], [f()])
+    with pytest.raises(ValueError, match="overlap"):  # part of a buffer
+        b = f(16)
+        _lib.make_adamw_tensors([b[:8], b[4:12]], [f(), f()], [f(), f()], [f(), f()])
+    shared = f()  # two weights with one gradient
+    _lib.make_adamw_tensors([f(), f()], [shared, shared], [f(), f()], [f(), f()])
     with pytest.raises(ValueError, match="m.0. must have 8 values"):
         _lib.make_adamw_tensors([f()], [f()], [f(9)], [f()])
     with pytest.raises(TypeError, match="v.0. must be"):

@@ -78,10 +78,10 @@ def test_xent_arguments(lib):
         sizes.append(n.value)
     assert 256 <= sizes[0] <= sizes[1]
 
-    def fwd(ws=FAKE, size=1 << 40, x=FAKE, w=FAKE, t=FAKE, loss=FAKE, lse=FAKE, total=None):
+    def fwd(ws=FAKE, size=1 << 40, x=FAKE, w=FAKE, t=FAKE, loss=FAKE, lse=0x20000, total=None):
         return lib.moe_xent_fwd(d, ws, size, None, x, w, t, loss, lse, total)
 
-    def bwd(ws=FAKE, size=1 << 40, x=FAKE, w=FAKE, t=FAKE, lse=FAKE, dl=FAKE, total=None, dx=FAKE, dw=FAKE):
+    def bwd(ws=FAKE, size=1 << 40, x=FAKE, w=FAKE, t=FAKE, lse=FAKE, dl=FAKE, total=None, dx=0x30000, dw=0x40000):
         return lib.moe_xent_bwd(d, ws, size, None, x, w, t, lse, dl, total, dx, dw)
 
     assert fwd(ws=None) == WSP and fwd(size=sizes[0] - 1) == WSP and fwd(ws=0x10010) == WSP
@@ -91,6 +91,8 @@ def test_xent_arguments(lib):
     for k in ("x", "w", "t", "lse"):
         assert bwd(**{k: None}) == INV and bwd(**{k: 0x10001}) == INV
     assert fwd(total=ODD) == INV and bwd(dx=ODD) == INV and bwd(dw=ODD) == INV
+    assert fwd(lse=FAKE) == INV and fwd(total=FAKE) == INV and bwd(dx=FAKE) == INV and bwd(dw=FAKE) == INV
+    assert bwd(dx=0x40000) == INV
     assert bwd(dl=None) == INV and bwd(total=FAKE) == INV and bwd(dx=None, dw=None) == INV
 
 
