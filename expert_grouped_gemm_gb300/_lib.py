@@ -185,7 +185,7 @@ def _fast():
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         bind.init(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
             "moe_norm_fwd", "moe_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_linear_fwd", "moe_linear_bwd",
-            "moe_balance_fwd", "moe_balance_bwd", "moe_xent_fwd", "moe_xent_bwd")))
+            "moe_balance_fwd", "moe_balance_bwd", "moe_xent_fwd", "moe_xent_bwd", "moe_grad_norm", "moe_adamw_step")))
         _bind = bind
     return _bind
 
@@ -653,7 +653,7 @@ class TensorList:
     def __init__(self, entries, keep, bits, device):
         self.count, self.bits, self.device, self._keep = len(entries), bits, device, keep
         self.array = (AdamWTensor * max(1, len(entries)))(*entries)
-        self.head = self.array  # what the calls pass
+        self.address = ctypes.addressof(self.array)
 
 
 def _flat(t, name, i, dtypes, n=None):
@@ -740,27 +740,37 @@ def _list_here(tensors: TensorList):
 def alloc_grad_norm_workspace(tensors: TensorList, device="cuda") -> torch.Tensor:
     """A workspace of moe_grad_norm for these tensors, its header zero on return."""
     n = ctypes.c_size_t(0)
-    _check(load().moe_grad_norm_workspace_size(tensors.head, tensors.count, ctypes.byref(n)))
+    _check(load().moe_grad_norm_workspace_size(tensors.array, tensors.count, ctypes.byref(n)))
     return _workspace(n.value, 256, device)
 
 
 def moe_grad_norm(tensors: TensorList, ws, norm, grad_scale=1.0, stream=None):
     """norm[1] = grad_scale times the 2-norm of all gradients of the list."""
+    rc = _fast().grad_norm(grad_scale, stream if stream is None else _stream(stream), ws, tensors.address, tensors.count,
+                           tensors.device, norm)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
     _list_here(tensors)
-    _check(load().moe_grad_norm(tensors.head, tensors.count, _ws(ws), ws.numel(), _stream(stream), grad_scale,
-                                _tensor(norm, "norm", torch.float32, (1,))))
+    norm = _tensor(norm, "norm", torch.float32, (1,))
+    _check(load().moe_grad_norm(tensors.array, tensors.count, _ws(ws), ws.numel(), _stream(stream), grad_scale, norm))
 
 
 def moe_adamw_step(dims: AdamWDims, tensors: TensorList, norm=None, lr=None, step=None, stream=None):
     """One AdamW step over the list, in place. norm[1]: the gradients' norm (clipping; a step on inf or NaN is left out);
     lr[1] (fp32), step[1] (int32): on the device, in place of dims'."""
-    _list_here(tensors)
     if tensors.bits != dims.state_bits and tensors.count:
         raise ValueError(f"the list's states have {tensors.bits} bits, dims say {dims.state_bits}")
+    rc = _fast().adamw_step(dims, stream if stream is None else _stream(stream), tensors.address, tensors.count,
+                            tensors.device, norm, lr, step)
+    if rc is not None:
+        return _check(rc)
+    # something is not what the operator takes: the checks one by one, which name it
+    _list_here(tensors)
     one = (1,)
-    _check(load().moe_adamw_step(
-        dims, tensors.head, tensors.count, _stream(stream), _tensor(norm, "norm", torch.float32, one, False),
-        _tensor(lr, "lr", torch.float32, one, False), _tensor(step, "step", torch.int32, one, False)))
+    args = (_tensor(norm, "norm", torch.float32, one, False), _tensor(lr, "lr", torch.float32, one, False),
+            _tensor(step, "step", torch.int32, one, False))
+    _check(load().moe_adamw_step(dims, tensors.array, tensors.count, _stream(stream), *args))
 
 
 def moe_read_status(ws: torch.Tensor, stream=None) -> int:

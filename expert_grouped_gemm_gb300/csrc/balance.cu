@@ -8,8 +8,8 @@
 // Forward: tokens are cut into chunks of equal length, a block each; a block walks the sequences that its chunk
 // meets and writes one row of sums (p, counts, lse^2) for each. Row c + s holds chunk c of sequence s: along the
 // tokens either index only grows, so no two share a row and chunks + S rows are enough. A second kernel adds a
-// sequence's rows in order, so results do not depend on timing; where there are few rows, the last block of the first
-// kernel does it.
+// sequence's rows in order, so results do not depend on timing. Tokens that one block takes need neither rows nor a
+// second kernel.
 //
 // Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value): bound by what a warp does for a
 // token, not by HBM.
@@ -38,7 +38,6 @@ struct BalanceArgs {
   int* row_n;         // [chunks + S][E]
   float* row_z;       // [chunks + S]
   float* part;        // [S * column blocks][2]: parts of the losses
-  int few;            // the last block of the first kernel adds the rows
   unsigned* done;
   int* status;
   float* loss;
@@ -87,14 +86,13 @@ __device__ __forceinline__ void load_row(const TL* p, int n, bool vec, float (&l
         for (int q = 0; q < V; ++q) l[i + q] = i < n ? io<TL>::to_f(e[q]) : -INFINITY;
       }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) l[i] = l[i] != l[i] ? -INFINITY : l[i];
+      for (int i = 0; i < EPL; ++i) l[i] = fmaxf(l[i], -INFINITY);  // of NaN and a number: the number
       return;
     }
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const float v = i < n ? io<TL>::to_f(p[i]) : -INFINITY;
-    l[i] = v != v ? -INFINITY : v;
+    l[i] = fmaxf(i < n ? io<TL>::to_f(p[i]) : -INFINITY, -INFINITY);
   }
 }
 
@@ -113,12 +111,11 @@ __device__ __forceinline__ float warp_max(float v) {
 // below zero, whose scores are denormal, has a sum that can be divided by. A masked row is all zeros.
 template <int EPL, bool SOFTMAX>
 __device__ __forceinline__ float probs(float (&l)[EPL], float* away) {
-  float m = l[0];
+  float m = l[0], sum = 0.0f;
 #pragma unroll
   for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
-  m = warp_max(m);
-  float sum = 0.0f;
   if constexpr (SOFTMAX) {
+    m = warp_max(m);
     if (fabsf(m) < INFINITY) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) sum += l[i] = ex2_approx((l[i] - m) * kLog2e);
@@ -127,13 +124,17 @@ __device__ __forceinline__ float probs(float (&l)[EPL], float* away) {
       for (int i = 0; i < EPL; ++i) sum += l[i] = l[i] == INFINITY ? 1.0f : 0.0f;
     }
   } else {
-    const float low = m > -INFINITY ? fminf(m, 0.0f) : 0.0f;
+    float low = 0.0f;
+    if (!__any_sync(kFull, m >= 0.0f)) {  // the whole row is below zero
+      m = warp_max(m);
+      if (m > -INFINITY) low = m;
+    }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       float e = ex2_approx(-kLog2e * fabsf(l[i]));
       const float r = rcp_approx(1.0f + e);  // sigma(|l|)
       if (away) away[i] = l[i] > 0.0f ? e * r : r;
-      if (low < 0.0f) e = ex2_approx((l[i] - low) * kLog2e);  // the whole row is below zero
+      if (low < 0.0f) e = ex2_approx((l[i] - low) * kLog2e);
       l[i] = l[i] > 0.0f ? r : e * r;
       sum += l[i];
     }
@@ -202,17 +203,16 @@ __device__ __forceinline__ void store_losses(const BalanceArgs& a, float dot, fl
   a.loss[1] = z * (a.z / N);
 }
 
-// Whether this is the last block of the grid; what the others wrote before is visible to it.
+// Whether this is the last block of the grid; what the others' first threads wrote before is visible to it.
 __device__ __forceinline__ bool last_block(unsigned* done) {
   __shared__ bool last;
-  __threadfence();
-  __syncthreads();
   if (threadIdx.x == 0) {
+    __threadfence();
     last = atomicAdd(done, 1u) == gridDim.x * gridDim.y - 1;
     if (last) *done = 0;
+    __threadfence();
   }
   __syncthreads();
-  __threadfence();
   return last;
 }
 
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
   const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
   const int c0 = (int)blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.T);
   const TL* logits = reinterpret_cast<const TL*>(a.logits) + e0;
+  float dot = 0.0f, z_all = 0.0f;  // of the only block
   // towards L2 while the sequences are looked for: a lane 128 bytes of the warp's rows and of the indices
   for (int t = c0 + warp; t < c1; t += WARPS)
     if (lane * (128 / (int)sizeof(TL)) < a.E)
@@ -267,39 +268,33 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
       float v = shared[i];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) v += shared[w * a.E + i];
-      a.row_p[row * a.E + i] = v;
-      a.row_n[row * a.E + i] = hist[i];
+      if (a.chunks == 1) {  // the only block: these are the sequence's sums
+        v /= (float)(b1 - b0);
+        dot += (float)hist[i] * v;
+        a.count[(int64_t)s * a.E + i] = hist[i];
+        if (a.prob) a.prob[(int64_t)s * a.E + i] = v;
+      } else {
+        a.row_p[row * a.E + i] = v;
+        a.row_n[row * a.E + i] = hist[i];
+      }
     }
     if (threadIdx.x == 0) {
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) v += zsum[w];
-      a.row_z[row] = v;
+      if (a.chunks == 1) z_all += v;
+      else a.row_z[row] = v;
     }
     __syncthreads();
   }
-  if (!a.few) return;
-  if (gridDim.x > 1 && !last_block(a.done)) return;
-  // a column a thread, all its rows
-  float dot = 0.0f, z_of_warp = 0.0f;
+  if (a.chunks > 1) return;
   for (int s = 0; s < a.S; ++s) {
     check_seq(a, s);
-    const int t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
-    const int r0 = t0 < t1 ? t0 / a.chunk + s : 0, r1 = t0 < t1 ? (t1 - 1) / a.chunk + s + 1 : 0;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-      float p = 0.0f;
-      int c = 0;
-#pragma unroll 4
-      for (int r = r0; r < r1; ++r) {
-        p += __ldcg(a.row_p + (int64_t)r * a.E + e);
-        c += __ldcg(a.row_n + (int64_t)r * a.E + e);
-      }
-      p /= (float)max(t1 - t0, 1);
-      a.count[(int64_t)s * a.E + e] = c;
-      if (a.prob) a.prob[(int64_t)s * a.E + e] = p;
-      dot += (float)c * p;
+    if (seq_at(a, s) < seq_at(a, s + 1)) continue;
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+      a.count[(int64_t)s * a.E + i] = 0;
+      if (a.prob) a.prob[(int64_t)s * a.E + i] = 0.0f;
     }
-    if (warp == 0) z_of_warp += sum_z(a, s);
   }
   dot = warp_sum(dot);
   if (lane == 0) zsum[warp] = dot;
@@ -307,7 +302,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 1; w < WARPS; ++w) dot += zsum[w];
-    store_losses(a, dot, z_of_warp);
+    store_losses(a, dot, z_all);
   }
 }
 
@@ -411,13 +406,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
 // ---------------------------------------------------------------- host side
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr int kChunkBlocks = 152;  // chunks to aim for: one for each SM
-constexpr int kFewRows = 16;       // as many rows the last block adds by itself
 
 // Warps of a forward block: as many as hold their sums in 32 KB.
 int fwd_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
-// Tokens of a chunk: two for each warp, and no more chunks than SMs.
+// Tokens of a chunk: four for each warp where that is all, else at least two, and no more chunks than SMs.
 int chunk_tokens(const moe_balance_dims& d) {
-  return (int)std::max<int64_t>(2 * fwd_warps(d.E), (d.T + kChunkBlocks - 1) / kChunkBlocks);
+  const int64_t w = fwd_warps(d.E);
+  return (int)(d.T <= 4 * w ? d.T : std::max<int64_t>(2 * w, (d.T + kChunkBlocks - 1) / kChunkBlocks));
 }
 
 struct BalanceWs {
@@ -513,13 +508,12 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
   a.loss = loss;
   a.count = count;
   a.prob = prob;
-  a.few = a.chunks + a.S <= kFewRows;
-  *launches += a.few ? 1 : 2;
+  *launches += a.chunks == 1 ? 1 : 2;
   const cudaError_t e = with_epl(a.R, [&](auto epl) {
     constexpr int EPL = decltype(epl)::value;
     return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true>(d, a, st) : fwd_typed<EPL, false>(d, a, st);
   });
-  if (e != cudaSuccess || a.few) return e;
+  if (e != cudaSuccess || a.chunks == 1) return e;
   // a warp for each of a sequence's rows, as far as that goes
   const dim3 grid((unsigned)a.S, (unsigned)((a.E + 31) / 32));
   if (a.chunks >= 16 * a.S) MOE_LAUNCH(k_balance_sum<32>, grid, 1024, 0, st, a);

@@ -32,16 +32,20 @@ decltype(&moe_balance_fwd) g_balance_fwd = nullptr;
 decltype(&moe_balance_bwd) g_balance_bwd = nullptr;
 decltype(&moe_xent_fwd) g_xent_fwd = nullptr;
 decltype(&moe_xent_bwd) g_xent_bwd = nullptr;
+decltype(&moe_grad_norm) g_grad_norm = nullptr;
+decltype(&moe_adamw_step) g_adamw_step = nullptr;
 
 constexpr bool kNeeded = true, kMay = false;  // a tensor that has to be there, one that may be None
 
-// The arguments of one call: args[0] the dims structure, args[1] the stream (None: the current one).
+// The arguments of one call: args[0] the dims structure (dims null: something else), args[1] the stream (None: the
+// current one).
 class Call {
  public:
   Call(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, void* dims, Py_ssize_t dims_bytes) : args_(args) {
     ok_ = n == want;
     if (!ok_) return;
     device_ = c10::cuda::current_device();
+    if (!dims) return;
     Py_buffer b;
     if (PyObject_GetBuffer(args[0], &b, PyBUF_SIMPLE) != 0) {
       PyErr_Clear();
@@ -68,6 +72,20 @@ class Call {
     ok_ = here(*t) && t->scalar_type() == at::kByte && t->is_contiguous();
     *bytes = (size_t)t->numel();
     return ok_ ? t->data_ptr() : nullptr;
+  }
+  // argument i: the optimiser's list, as its address, with its length and its device behind it
+  const moe_adamw_tensor* list(int i, int64_t* count) {
+    if (!ok_) return nullptr;
+    void* p = PyLong_AsVoidPtr(args_[i]);
+    *count = PyLong_AsLongLong(args_[i + 1]);
+    const long long device = args_[i + 2] == Py_None ? device_ : PyLong_AsLongLong(args_[i + 2]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      ok_ = false;
+      return nullptr;
+    }
+    ok_ = device == device_;
+    return static_cast<const moe_adamw_tensor*>(p);
   }
   bool ok() const { return ok_; }
   // the call itself, without the interpreter's lock
@@ -311,6 +329,42 @@ PyObject* xent_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (scale, stream, ws, list, count, device, norm)
+PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(a, n, 7, nullptr, 0);
+    if (!c.ok()) Py_RETURN_NONE;
+    const double scale = PyFloat_AsDouble(a[0]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+    size_t bytes = 0;
+    void* ws = c.workspace(2, &bytes);
+    int64_t count = 0;
+    const moe_adamw_tensor* list = c.list(3, &count);
+    float* norm = c.tensor<float>(6, kNeeded, at::kFloat, 1);
+    if (!c.ok()) Py_RETURN_NONE;
+    return c.run([&](void* st) { return g_grad_norm(list, count, ws, bytes, st, (float)scale, norm); });
+  });
+}
+
+// (dims, stream, list, count, device, norm, lr, step)
+PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    moe_adamw_dims d;
+    Call c(a, n, 8, &d, sizeof d);
+    if (!c.ok()) Py_RETURN_NONE;
+    int64_t count = 0;
+    const moe_adamw_tensor* list = c.list(2, &count);
+    const float* norm = c.tensor<float>(5, kMay, at::kFloat, 1);
+    const float* lr = c.tensor<float>(6, kMay, at::kFloat, 1);
+    const int32_t* step = c.tensor<int32_t>(7, kMay, at::kInt, 1);
+    if (!c.ok()) Py_RETURN_NONE;
+    return c.run([&](void* st) { return g_adamw_step(&d, list, count, st, norm, lr, step); });
+  });
+}
+
 template <typename F>
 void take(F& f, void* p) {
   f = reinterpret_cast<F>(p);
@@ -318,7 +372,7 @@ void take(F& f, void* p) {
 
 // init(addresses of the C ABI's functions, in the order below)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kCount = 10;
+  constexpr int kCount = 12;
   if (n != kCount) {
     PyErr_Format(PyExc_TypeError, "init takes %d addresses", kCount);
     return nullptr;
@@ -338,13 +392,16 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   take(g_balance_bwd, p[7]);
   take(g_xent_fwd, p[8]);
   take(g_xent_bwd, p[9]);
+  take(g_grad_norm, p[10]);
+  take(g_adamw_step, p[11]);
   Py_RETURN_NONE;
 }
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(init),        METHOD(norm_fwd),    METHOD(norm_bwd),   METHOD(gate_fwd),
                          METHOD(gate_bwd),    METHOD(linear_fwd),  METHOD(linear_bwd), METHOD(balance_fwd),
-                         METHOD(balance_bwd), METHOD(xent_fwd),    METHOD(xent_bwd),   {nullptr, nullptr, 0, nullptr}};
+                         METHOD(balance_bwd), METHOD(xent_fwd),    METHOD(xent_bwd),   METHOD(grad_norm),
+                         METHOD(adamw_step),  {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -16,6 +16,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "block.h"
@@ -47,17 +48,25 @@ struct Entry {
   float lr_scale, wd;
 };
 
+// The same for the norm.
+struct Grad {
+  const void* g;
+  int64_t n;
+  uint32_t first;
+  uint32_t types;
+};
+
 constexpr int kMap = 1024;
-template <int N>
+template <typename E, int N>
 struct Table {
   uint32_t count, chunks;
   uint16_t map[kMap];  // a chunk's tensor, where there are no more chunks: a search would wait for every step
-  Entry e[N];
+  E e[N];
 };
 
 // The tensor of a chunk, from the one that an earlier chunk was in.
-template <int N>
-__device__ __forceinline__ uint32_t tensor_of(const Table<N>& t, uint32_t chunk, uint32_t at) {
+template <typename E, int N>
+__device__ __forceinline__ uint32_t tensor_of(const Table<E, N>& t, uint32_t chunk, uint32_t at) {
   if (t.chunks <= kMap) return t.map[chunk];
   uint32_t lo = at, hi = t.count;
   if (at + 1 == hi || t.e[at + 1].first > chunk) return at;
@@ -172,32 +181,89 @@ struct AdamWArgs {
 
 // What the values of a tensor share in a step.
 struct Factors {
-  float b1, c1, b2, c2, bc2, eps;  // c1, c2: times the gradients' factor and its square
-  float keep, move;                // w = keep w - move m / (r bc2 + eps)
+  float gs, b1, c1, b2, c2, bc2, eps;  // gs: the gradients' factor
+  float keep, move;                    // w = keep w - move m / (r bc2 + eps)
 };
 
+// Two floats in one 64-bit operand: the same roundings in half the instructions.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 two(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void apart(f2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 both(float a) { return two(a, a); }
+
 // The step of four values of a block; with 8 bits m and v hold codes' values, sm and sv what they are multiples of, and
-// v receives r = sqrt(v). Roots of v below 2^-126 are zero.
+// v receives r = sqrt(v). Roundings are those of m = c1 g + (b1 m), v = c2 (g g) + (b2 v) with fused last steps, whatever
+// the compiler would join otherwise: in 8 bits a last bit can decide between two codes. For the same reason r is the
+// rounded root: an approximate one and one correction by the residual v - r^2 (Markstein).
 template <int BITS>
 __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, const float (&g)[4], float (&p)[4],
                                         float (&m)[4], float (&v)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    m[j] = fmaf(BITS == 8 ? k.b1 * sm : k.b1, m[j], k.c1 * g[j]);
-    const float gg = k.c2 * g[j];
-    const float old = BITS == 8 ? v[j] * sv : 0.0f;
-    const float vn = BITS == 8 ? fmaf(k.b2 * old, old, gg * gg) : fmaf(k.b2, v[j], gg * gg);
-    float r;
-    if constexpr (BITS == 8) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(vn));
-    else asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(vn));
-    v[j] = BITS == 8 ? r : vn;
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(r, k.bc2, k.eps)));
-    p[j] = fmaf(k.keep, p[j], -(k.move * m[j]) * inv);
+  for (int j = 0; j < 4; j += 2) {
+    const f2 gg = mul2(two(g[j], g[j + 1]), both(k.gs));
+    f2 mo = two(m[j], m[j + 1]), vo = two(v[j], v[j + 1]);
+    if constexpr (BITS == 8) {
+      mo = mul2(mo, both(sm));
+      const f2 ro = mul2(vo, both(sv));
+      vo = mul2(ro, ro);
+    }
+    const f2 mn = fma2(both(k.c1), gg, mul2(both(k.b1), mo));
+    const f2 vn = fma2(both(k.c2), mul2(gg, gg), mul2(both(k.b2), vo));
+    apart(mn, m[j], m[j + 1]);
+    apart(vn, v[j], v[j + 1]);
+    float r[2], inv[2];
+    if constexpr (BITS == 8) {
+      float y[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"(fmaxf(v[j + i], 1.17549435e-38f)));
+      const f2 y2 = two(y[0], y[1]), r0 = mul2(vn, y2), half = mul2(y2, both(0.5f));
+      const f2 rest = fma2(mul2(r0, both(-1.0f)), r0, vn);
+      apart(fma2(rest, half, r0), r[0], r[1]);
+      v[j] = r[0];
+      v[j + 1] = r[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) asm("sqrt.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(v[j + i]));
+    }
+    float den[2];
+    apart(fma2(two(r[0], r[1]), both(k.bc2), both(k.eps)), den[0], den[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[i]) : "f"(den[i]));
+    const f2 move = mul2(mul2(mn, both(-k.move)), two(inv[0], inv[1]));
+    apart(fma2(both(k.keep), two(p[j], p[j + 1]), move), p[j], p[j + 1]);
   }
 }
 
-// m and r of a block as codes over new scales.
+// m and r of a block as codes over new scales. x / scale is the rounded quotient: with the rounded reciprocal, one
+// correction of the product by its residual gives it (Markstein).
+__device__ __forceinline__ void codes4(const float (&x)[4], float scale, float inv, bool root, uint32_t& code) {
+  float q[4];
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    const f2 a = two(x[j], x[j + 1]), q0 = mul2(a, both(inv));
+    apart(fma2(fma2(q0, both(-scale), a), both(inv), q0), q[j], q[j + 1]);
+  }
+  if (root) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (x[j] > 0.0f) q[j] = fmaxf(q[j], 0.001953125f);  // 2^-9, the smallest e4m3
+  }
+  code = encode4(q);
+}
 __device__ __forceinline__ void pack_block(const Entry& e, int64_t blk, int lane, float (&m)[2][4], float (&r)[2][4],
                                            uint32_t (&mc)[2], uint32_t (&rc)[2]) {
   const float ms = block_scale(m), rs = block_scale(r), mi = 1.0f / ms, ri = 1.0f / rs;
@@ -207,15 +273,8 @@ __device__ __forceinline__ void pack_block(const Entry& e, int64_t blk, int lane
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float x[4], y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] = m[h][j] * mi;
-      y[j] = r[h][j] * ri;
-      if (r[h][j] > 0.0f) y[j] = fmaxf(y[j], 0.001953125f);  // 2^-9, the smallest e4m3
-    }
-    mc[h] = encode4(x);
-    rc[h] = encode4(y);
+    codes4(m[h], ms, mi, false, mc[h]);
+    codes4(r[h], rs, ri, true, rc[h]);
   }
 }
 
@@ -351,7 +410,7 @@ __device__ __forceinline__ void last_block(const Entry& e, const Factors& k, int
 }
 
 template <int BITS, int N>
-__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ Table<N> tab, const AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ Table<Entry, N> tab, const AdamWArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   float gs = a.wide, lr = a.lr, bc1 = a.bc1, bc2 = a.bc2;
   if (a.norm) {
@@ -365,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ T
     bc1 = -1.0f / expm1f(t * a.ln_b1);
     bc2 = rsqrtf(-expm1f(t * a.ln_b2));
   }
-  Factors k = {a.b1, a.c1 * gs, a.b2, sqrtf(a.c2) * gs, bc2, a.eps, 0.0f, 0.0f};
+  Factors k = {gs, a.b1, a.c1, a.b2, a.c2, bc2, a.eps, 0.0f, 0.0f};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t at = 0;
   for (uint32_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
@@ -432,7 +491,7 @@ __device__ __forceinline__ float squares(const void* g, int n) {
 
 // A block's sum of squares over its chunks; the last block of the last launch adds the blocks' in order.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ Table<N> tab, float* part, int part0,
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ Table<Grad, N> tab, float* part, int part0,
                                                         int parts, unsigned* done, float scale, float* norm) {
   __shared__ float red[kWarps];
   __shared__ double wide[kWarps];
@@ -443,7 +502,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
   float sum = 0.0f;
   for (uint32_t chunk = blockIdx.x; chunk < tab.chunks; chunk += gridDim.x) {
     at = tensor_of(tab, chunk, at);
-    const Entry& e = tab.e[at];
+    const Grad& e = tab.e[at];
     const bool gb = e.types & 2;
     const int64_t i0 = (int64_t)(chunk - e.first) * kNormChunk;
     const int n = (int)min((int64_t)kNormChunk, e.n - i0);
@@ -478,13 +537,22 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kMany = 376, kSome = 128, kFew = 24;  // 80 bytes a tensor: kernel arguments hold 32764
-static_assert(sizeof(Table<kMany>) + sizeof(AdamWArgs) <= 32764, "kernel arguments");
+// Lengths of tables: kernel arguments hold 32764 bytes, and every launch copies its own, so a short list takes a short
+// one.
+constexpr int kMany = 376, kSome = 176, kFew = 48;      // 80 bytes a tensor
+constexpr int kGradMany = 1200, kGradFew = 176;         // 24 bytes
+static_assert(sizeof(Table<Entry, kMany>) + sizeof(AdamWArgs) <= 32764 && sizeof(Table<Grad, kGradMany>) + 64 <= 32764,
+              "kernel arguments");
 constexpr int kNormBlocks = 2048;  // at most, whatever the device
 
-// Fills a table with tensors [from, ...) as far as it goes; returns how many of the list it took.
-template <int N>
-int64_t fill(Table<N>* t, const moe_adamw_tensor* list, int64_t count, int64_t chunk) {
+void set(Entry& e, const moe_adamw_tensor& s, uint32_t first, uint32_t types) {
+  e = {s.param, s.grad, s.master, s.m, s.v, s.m_scale, s.v_scale, s.n, first, types, s.lr_scale, s.weight_decay};
+}
+void set(Grad& e, const moe_adamw_tensor& s, uint32_t first, uint32_t types) { e = {s.grad, s.n, first, types}; }
+
+// Fills a table with the list's first tensors, as many as fit; returns how many of the list it took.
+template <typename E, int N>
+int64_t fill(Table<E, N>* t, const moe_adamw_tensor* list, int64_t count, int64_t chunk) {
   t->count = 0;
   uint64_t chunks = 0;
   int64_t i = 0;
@@ -493,9 +561,7 @@ int64_t fill(Table<N>* t, const moe_adamw_tensor* list, int64_t count, int64_t c
     if (s.n == 0) continue;
     const uint64_t c = (uint64_t)((s.n + chunk - 1) / chunk);
     if (chunks + c >= (1ull << 31)) break;  // the rest in another launch
-    Entry& e = t->e[t->count++];
-    e = {s.param, s.grad, s.master, s.m, s.v, s.m_scale, s.v_scale, s.n, (uint32_t)chunks,
-         (uint32_t)(s.dtype == MOE_BF16) | (uint32_t)(s.grad_dtype == MOE_BF16) << 1, s.lr_scale, s.weight_decay};
+    set(t->e[t->count++], s, (uint32_t)chunks, (uint32_t)(s.dtype == MOE_BF16) | (uint32_t)(s.grad_dtype == MOE_BF16) << 1);
     chunks += c;
   }
   t->chunks = (uint32_t)chunks;
@@ -508,23 +574,27 @@ int64_t fill(Table<N>* t, const moe_adamw_tensor* list, int64_t count, int64_t c
 // As many blocks as are resident at once, for kernels whose blocks walk many chunks: one more round of blocks would
 // double their time.
 template <typename K>
-int grid_of(K kernel, uint32_t chunks, int sms) {
-  int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0) != cudaSuccess || per < 1) per = 1;
-  return (int)std::min<int64_t>(chunks, (int64_t)sms * per);
+int grid_of(K kernel, std::atomic<int>& per, uint32_t chunks, int sms) {
+  int n = per.load(std::memory_order_relaxed);  // asked once: every GPU that runs this code has the same SMs
+  if (n < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != cudaSuccess || n < 1) n = 1;
+    per.store(n, std::memory_order_relaxed);
+  }
+  return (int)std::min<int64_t>(chunks, (int64_t)sms * n);
 }
 
 template <int N>
 cudaError_t adamw_launches(int bits, const AdamWArgs& a, const moe_adamw_tensor* list, int64_t count, int sms,
                            cudaStream_t st, int* launches) {
-  Table<N> t;
+  static std::atomic<int> resident{0};
+  Table<Entry, N> t;
   while (count > 0) {
     const int64_t took = fill(&t, list, count, bits == 8 ? chunk_of<8> : chunk_of<32>);
     list += took;
     count -= took;
     if (!t.count) continue;
     *launches += 1;
-    if (bits == 8) MOE_LAUNCH((k_adamw<8, N>), grid_of(k_adamw<8, N>, t.chunks, sms), kThreads, 0, st, t, a);
+    if (bits == 8) MOE_LAUNCH((k_adamw<8, N>), grid_of(k_adamw<8, N>, resident, t.chunks, sms), kThreads, 0, st, t, a);
     else MOE_LAUNCH((k_adamw<32, N>), t.chunks, kThreads, 0, st, t, a);
   }
   return cudaSuccess;
@@ -533,7 +603,8 @@ cudaError_t adamw_launches(int bits, const AdamWArgs& a, const moe_adamw_tensor*
 template <int N>
 cudaError_t norm_launches(char* ws, const moe_adamw_tensor* list, int64_t count, float scale, float* norm, int sms,
                           cudaStream_t st, int* launches) {
-  Table<N> t;
+  static std::atomic<int> resident{0};
+  Table<Grad, N> t;
   float* part = reinterpret_cast<float*>(ws + kNormHeader);
   unsigned* done = reinterpret_cast<unsigned*>(ws + 64);
   int part0 = 0;
@@ -542,7 +613,7 @@ cudaError_t norm_launches(char* ws, const moe_adamw_tensor* list, int64_t count,
     list += took;
     count -= took;
     while (count > 0 && list->n == 0) ++list, --count;  // the launch with the last values is the one that finishes
-    const int grid = std::max(1, std::min(kNormBlocks, grid_of(k_grad_norm<N>, t.chunks, sms)));  // no value at all: one block writes a norm of zero
+    const int grid = std::max(1, std::min(kNormBlocks, grid_of(k_grad_norm<N>, resident, t.chunks, sms)));  // no value at all: one block writes a norm of zero
     *launches += 1;
     MOE_LAUNCH((k_grad_norm<N>), grid, kThreads, 0, st, t, part, part0, part0 + grid, done, scale,
                count > 0 ? nullptr : norm);
@@ -557,16 +628,14 @@ cudaError_t norm_launches(char* ws, const moe_adamw_tensor* list, int64_t count,
 size_t grad_norm_workspace_bytes(const moe_adamw_tensor* list, int64_t count) {
   uint64_t chunks = 0;
   for (int64_t i = 0; i < count; ++i) chunks += (uint64_t)((list[i].n + kNormChunk - 1) / kNormChunk);
-  const uint64_t launches = (uint64_t)(count + kMany - 1) / kMany + (chunks >> 30) + 1;
+  const uint64_t launches = (uint64_t)(count + kGradFew - 1) / kGradFew + (chunks >> 30) + 1;
   return kNormHeader + (size_t)((launches * kNormBlocks * 4 + 255) / 256 * 256);
 }
 
 cudaError_t launch_grad_norm(void* ws, const moe_adamw_tensor* list, int64_t count, float scale, float* norm, int sms,
                              cudaStream_t st, int* launches) {
-  // arguments are copied with every launch: a short list takes a short table
-  return count <= kFew    ? norm_launches<kFew>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches)
-         : count <= kSome ? norm_launches<kSome>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches)
-                          : norm_launches<kMany>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches);
+  return count <= kGradFew ? norm_launches<kGradFew>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches)
+                           : norm_launches<kGradMany>(static_cast<char*>(ws), list, count, scale, norm, sms, st, launches);
 }
 
 cudaError_t launch_adamw(const moe_adamw_dims& d, const moe_adamw_tensor* list, int64_t count, const float* norm,
