@@ -81,6 +81,11 @@ __device__ __forceinline__ void row_stats(const float (&z)[N], float& m, float& 
   m = big;
 }
 
+__device__ __forceinline__ float reciprocal_or_zero(const float* p) {
+  const float v = *p;
+  return v != 0.0f ? 1.0f / v : 0.0f;
+}
+
 // What a row's gradient dl = f e^{l - lse} - d onehot is made of; at: the target's column, or -1.
 struct XentRow {
   float lse2, d, f;
@@ -93,7 +98,7 @@ struct XentRow {
     if (v < 0 || v >= x.V) return;
     const float lse = x.lse[t];
     at = v;
-    d = x.dloss ? x.dloss[t] : 1.0f / x.total[1];
+    d = x.dloss ? x.dloss[t] : 1.0f;
     lse2 = lse * kLog2e;
     f = d * (1.0f + 2.0f * x.z * lse);
   }
@@ -515,6 +520,11 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         float z[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) z[i] = __uint_as_float(v[i >> 5][i & 31]);
+        if (EPI == kEpiLinear && g.div) {
+          const float f = reciprocal_or_zero(g.div);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) z[i] *= f;
+        }
         if (bias) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -755,6 +765,11 @@ __device__ __forceinline__ void finish_tokens(const TcArgs& args, const float* s
           z[1] += v[u][r].y;
           z[2] += v[u][r].z;
           z[3] += v[u][r].w;
+        }
+        if (EPI == kEpiLinear && g.div) {
+          const float f = reciprocal_or_zero(g.div);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] *= f;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] += b[i];

@@ -22,6 +22,7 @@ struct LinearGemm {
   int* status;           // receives MOE_ERR_TIMEOUT when a wait runs out
   int64_t ldy = 0;       // row stride of y, 0: N
   int add = 0;           // with out_f32: added to what y holds
+  const float* div = nullptr;  // the product is divided by *div (0: becomes 0)
   int parts = 1;         // with out_f32, launch_linear_parts: K in so many parts, whose sums go to y + part * M * ldy
 };
 
@@ -30,10 +31,9 @@ struct LinearGemm {
 struct XentEpi {
   float2* part;         // statistics: [slots][M]
   float* at;            // statistics: [M], receives the logit of a target among these columns
-  const int* target;    // gradient: as in XentRows of xent.cu
+  const int* target;
   const float* lse;
-  const float* dloss;
-  const float* total;
+  const float* dloss;   // null: gradient of the sum of the losses
   float z;
   int v0, V;
 };

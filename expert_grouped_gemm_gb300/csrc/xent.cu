@@ -10,6 +10,7 @@
 // products are mostly of one sign.
 #include <algorithm>
 
+#include "act.cuh"
 #include "block.h"
 #include "common.cuh"
 #include "linear_choice.h"
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, 
 }
 
 // Eight rows' slots [first, end) of stat[slot][M] joined by a block, four slots of eight rows a warp; BASE2: a slot is
-// (largest logit times log2 e, sum of powers of two), else of e. Threads 0 .. 7 hold the result.
+// (largest logit times log2 e, sum of powers of two), else of e. Warp i < 8 holds row i's result.
 constexpr int kLossRows = 8, kLossWarps = 32;
 template <bool BASE2>
 __device__ __forceinline__ float2 join_slots(const float2* stat, int first, int end, int M, int64_t t0, float2 (*red)[kLossRows]) {
@@ -71,7 +72,7 @@ __device__ __forceinline__ float2 join_slots(const float2* stat, int first, int 
   const auto both = [](float& m, float& s, float m2, float s2) {
     if constexpr (BASE2) {
       const float big = fmaxf(m, m2);
-      s = s * exp2f(m - big) + s2 * exp2f(m2 - big);
+      s = s * ex2_approx(m - big) + s2 * ex2_approx(m2 - big);
       m = big;
     } else {
       join(m, s, m2, s2);
@@ -92,9 +93,15 @@ __device__ __forceinline__ float2 join_slots(const float2* stat, int first, int 
   }
   if (lane < 8) red[warp][lane] = make_float2(m, s);
   __syncthreads();
-  if (threadIdx.x < kLossRows) {
-#pragma unroll 8
-    for (int w = 1; w < kLossWarps; ++w) both(m, s, red[w][threadIdx.x].x, red[w][threadIdx.x].y);
+  if (warp < kLossRows) {
+    const float2 v = red[lane][warp];
+    m = v.x;
+    s = v.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      both(m, s, m2, s2);
+    }
   }
   return make_float2(m, s);
 }
@@ -105,7 +112,8 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_fold(float2* stat, int
   __shared__ float2 red[kLossWarps][kLossRows];
   const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
   const float2 v = join_slots<true>(stat, first, end, M, t0, red);
-  if (threadIdx.x < kLossRows && t0 + threadIdx.x < M) stat[t0 + threadIdx.x] = v;
+  const int row = threadIdx.x >> 5;
+  if (row < kLossRows && (threadIdx.x & 31) == 0 && t0 + row < M) stat[t0 + row] = v;
 }
 
 struct LossArgs {
@@ -159,38 +167,57 @@ template <bool BASE2>
 __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ float2 red[kLossWarps][kLossRows];
+  __shared__ float2 rows[kLossRows];
   __shared__ bool last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
+  const int64_t t = t0 + warp;  // of the first eight warps
+  int v = -1;
+  float at = 0.0f, had = 0.0f;
+  if (warp < kLossRows && t < a.M) {
+    v = a.target[t];
+    for (int i = lane; i < a.parts; i += 32) at += a.dots[t * a.parts + i];
+    at = warp_sum(at);
+    if (BASE2 && v >= 0 && v < a.V) had = a.at[t];
+  }
   const float2 st = join_slots<BASE2>(a.stat, a.first, a.end, a.M, t0, red);
-  float sum = 0.0f, n = 0.0f;
-  if (threadIdx.x < kLossRows && t0 + threadIdx.x < a.M) {
-    float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
-    const int v = a.target[t0 + threadIdx.x];
-    if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
-    if (v >= 0 && v < a.V) {
-      float at = 0.0f;
-      for (int i = 0; i < a.parts; ++i) at += a.dots[(t0 + threadIdx.x) * a.parts + i];
-      if (BASE2) e += log1pf(expf(at - e) - expf(a.at[t0 + threadIdx.x] - e));
-      sum = e - at + a.z * e * e;
-      n = 1.0f;
+  if (warp < kLossRows && lane == 0) {
+    float sum = 0.0f, n = 0.0f;
+    if (t < a.M) {
+      float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
+      if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
+      if (v >= 0 && v < a.V) {
+        if (BASE2) e += log1pf(expf(at - e) - expf(had - e));
+        sum = e - at + a.z * e * e;
+        n = 1.0f;
+      }
+      a.lse[t] = e;
+      a.loss[t] = sum;
     }
-    a.lse[t0 + threadIdx.x] = e;
-    a.loss[t0 + threadIdx.x] = sum;
+    rows[warp] = make_float2(sum, n);
   }
   if (!a.total) return;
-  if (warp == 0) {
-    sum = warp_sum(sum);
-    n = warp_sum(n);
-    if (lane == 0) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float sum = 0.0f, n = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLossRows; ++i) {
+      sum += rows[i].x;
+      n += rows[i].y;
+    }
+    if (gridDim.x == 1) {
+      a.total[0] = sum;
+      a.total[1] = n;
+    } else {
       a.part[blockIdx.x] = make_float2(sum, n);
       __threadfence();
       last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+      __threadfence();
     }
   }
+  if (gridDim.x == 1) return;
   __syncthreads();
   if (!last) return;
-  __threadfence();
   __shared__ double2 wide[kLossWarps];
   double x = 0.0, y = 0.0;
   for (int i = threadIdx.x; i < (int)gridDim.x; i += kLossWarps * 32) {
@@ -243,9 +270,10 @@ __global__ void __launch_bounds__(256) k_xent_dl(float* l, int64_t ld, int cols,
   }
 }
 
-// dx from the sums of `parts` parts of K, in order.
-__global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat16* o, int64_t n, int parts) {
+// dx from the sums of `parts` parts of K, in order, over *div where that is given.
+__global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat16* o, int64_t n, int parts, const float* div) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
+  const float by = div ? *div : 1.0f, f0 = by != 0.0f ? 1.0f / by : 0.0f;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
     float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (n % 4 == 0) {  // a part begins at a 16-byte boundary
@@ -257,13 +285,13 @@ __global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat1
         f[2] += v.z;
         f[3] += v.w;
       }
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0] * f0, f[1] * f0), hi = __floats2bfloat162_rn(f[2] * f0, f[3] * f0);
       *reinterpret_cast<uint2*>(o + i) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     } else {
       for (int64_t j = i; j < min(n, i + 4); ++j) {
         float v = 0.0f;
         for (int p = 0; p < parts; ++p) v += a[p * n + j];
-        o[j] = __float2bfloat16_rn(v);
+        o[j] = __float2bfloat16_rn(v * f0);
       }
     }
   }
@@ -379,7 +407,8 @@ struct Xent {
   }
   static int up4(int n) { return (n + 3) / 4 * 4; }
   float* piece() const { return reinterpret_cast<float*>(ws + L.piece); }
-  cudaError_t products(int64_t v0, int cols, void* dx, void* dw) {
+  // div: bf16's dl is that of the sum of the losses, the products are divided by *div
+  cudaError_t products(int64_t v0, int cols, void* dx, void* dw, const float* div) {
     const int M = (int)d.M, H = (int)d.H;
     if (d.dtype == MOE_BF16) {
       int* status = reinterpret_cast<int*>(ws);
@@ -389,11 +418,13 @@ struct Xent {
       const bool direct = P >= d.V && !parts;
       LinearGemm gx = {M, H, cols, dl, w_at(v0), P, ldw, 0, d.tied, nullptr, nullptr, direct ? dx : ws + L.dx, nullptr,
                        MOE_ACT_NONE, !direct, status, H, v0 > 0};
+      if (direct) gx.div = div;
       if (parts) gx.parts = std::min(parts, (cols + 63) / 64);
       LinearGemm gw = d.tied ? LinearGemm{cols, H, M, dl, x, P, ldx, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE,
                                           0, status}
                              : LinearGemm{H, cols, M, x, dl, ldx, P, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE,
                                           0, status, d.V};
+      gw.div = div;
       cudaError_t e = cudaSuccess;
       if (dx) {
         *launches += 1;
@@ -512,11 +543,14 @@ cudaError_t launch_xent_bwd(const moe_xent_dims& d, void* ws, const void* x, con
   if (e != cudaSuccess) return e;
   const XentRows r = {target, lse, dloss, total, (int)d.V, d.z_coef};
   const bool bf = d.dtype == MOE_BF16;
+  // The mean's gradient has one factor for all rows: in bf16 its rounding in dl would be one error of up to 2^-9 of
+  // everything. There dl is that of the sum, at most 1 (and nearly -1 at a target that is not expected), and the products
+  // are divided (4096 rows, dx 0.0029 -> 0.0019 of its size from 64 bits).
+  const float* div = bf && !dloss ? total + 1 : nullptr;
   XentEpi epi = {};
   epi.target = target;
   epi.lse = lse;
   epi.dloss = dloss;
-  epi.total = total;
   epi.z = d.z_coef;
   epi.V = (int)d.V;
   for (int64_t v0 = 0; v0 < d.V; v0 += c.P) {
@@ -529,14 +563,14 @@ cudaError_t launch_xent_bwd(const moe_xent_dims& d, void* ws, const void* x, con
       if ((e = c.logits_f32(v0, cols)) != cudaSuccess) return e;
       MOE_LAUNCH(k_xent_dl, dim3((unsigned)d.M, (unsigned)((cols + 1023) / 1024)), 256, 0, st, c.piece(), c.P, cols, (int)v0, r);
     }
-    if ((e = c.products(v0, cols, dx, dw)) != cudaSuccess) return e;
+    if ((e = c.products(v0, cols, dx, dw, div)) != cudaSuccess) return e;
   }
   const int parts = bf ? dx_parts(d) : 0;
   if (bf && dx && (parts || c.P < d.V)) {
     *launches += 1;
     const int64_t n = d.M * d.H;
     MOE_LAUNCH(k_xent_round, (unsigned)std::min<int64_t>((n + 1023) / 1024, (int64_t)sms * 16), 256, 0, st,
-               (const float*)(c.ws + c.L.dx), static_cast<__nv_bfloat16*>(dx), n, std::max(parts, 1));
+               (const float*)(c.ws + c.L.dx), static_cast<__nv_bfloat16*>(dx), n, std::max(parts, 1), div);
   }
   return cudaSuccess;
 }

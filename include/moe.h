@@ -510,7 +510,8 @@ MOE_API int moe_xent_fwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, v
  * counted rows) where dloss is null; 0 for rows that are not counted.
  *   dl = d_t ((1 + 2 z_coef lse_t) e^{l - lse_t} - onehot(target_t));  dx = dl w^T;  dw = x^T dl.
  * The logits are computed again, a piece of the vocabulary at a time. In bf16 dl is rounded to bf16
- * for the two products, and e^{l - lse} below 2^-126 is zero; dx is summed over the pieces in fp32.
+ * for the two products (without the mean's 1 / total[1], which divides their sums), and e^{l - lse} below
+ * 2^-126 is zero; dx is summed over the pieces in fp32.
  * Inputs:  x, w, target as in the forward, lse[M] of the forward, dloss[M] float or total[2] of the
  *          forward. Outputs: dx[M,H], dw (dims.tied), each nullable; overwritten.
  */
