@@ -405,14 +405,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
 
 // ---------------------------------------------------------------- host side
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-constexpr int kChunkBlocks = 152;  // chunks to aim for: one for each SM
-
-// Warps of a forward block: as many as hold their sums in 32 KB.
-int fwd_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
-// Tokens of a chunk: four for each warp where that is all, else at least two, and no more chunks than SMs.
+// One block takes what its warps get through in four tokens each (64 tokens of 128 experts 4.2 us; in two kernels 6.0);
+// more go in chunks of 8-warp blocks, four an SM (16384 x 256 in 37 sequences 13.2 us; one block of 32 warps an SM 16.9).
+constexpr int kChunkBlocks = 608;
+constexpr int kChunkWarps = 8;
+int one_block_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }  // as many as hold their sums in 32 KB
 int chunk_tokens(const moe_balance_dims& d) {
-  const int64_t w = fwd_warps(d.E);
-  return (int)(d.T <= 4 * w ? d.T : std::max<int64_t>(2 * w, (d.T + kChunkBlocks - 1) / kChunkBlocks));
+  return (int)(d.T <= 4 * one_block_warps(d.E) ? d.T : std::max<int64_t>(2 * kChunkWarps, (d.T + kChunkBlocks - 1) / kChunkBlocks));
 }
 
 struct BalanceWs {
@@ -477,8 +476,11 @@ cudaError_t bwd_typed(const moe_balance_dims& d, const BalanceArgs& a, cudaStrea
 
 template <int EPL, bool SOFTMAX, typename TL>
 cudaError_t fwd_launch(const BalanceArgs& a, cudaStream_t st) {
-  constexpr int W = EPL <= 8 ? 32 : EPL <= 16 ? 16 : 8;  // fwd_warps of every E that comes here
-  MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, TL, W>, a.chunks, W * 32, (size_t)a.E * 4 * (W + 1), st, a);
+  constexpr int W = EPL <= 8 ? 32 : EPL <= 16 ? 16 : 8;  // one_block_warps of every E that comes here
+  if (a.chunks == 1)
+    MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, TL, W>, 1, W * 32, (size_t)a.E * 4 * (W + 1), st, a);
+  else
+    MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, TL, kChunkWarps>, a.chunks, kChunkWarps * 32, (size_t)a.E * 4 * (kChunkWarps + 1), st, a);
   return cudaSuccess;
 }
 template <int EPL, bool SOFTMAX>

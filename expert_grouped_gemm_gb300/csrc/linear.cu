@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   const int s0 = (int)((int64_t)slabs * part / S), s1 = (int)((int64_t)slabs * (part + 1) / S);
   Slab A, B;
   A.init(g.A, g.sam, g.sak, m0, g.ma, g.ka, tid);
-  B.init(g.B, g.sbn, g.sbk, n0, g.nb, g.kb, tid);
+  B.init(g.B, g.sbn, g.sbk, n0, g.nb, g.K, tid);
   auto fetch = [&](int s) {
     A.fetch(s);
     B.fetch(s);
@@ -434,7 +434,6 @@ cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, 
     if (!w.g[i].ma) w.g[i].ma = w.g[i].M;
     if (!w.g[i].nb) w.g[i].nb = w.g[i].N;
     if (!w.g[i].ka) w.g[i].ka = w.g[i].K;
-    if (!w.g[i].kb) w.g[i].kb = w.g[i].K;
     w.S[i] = 1;
     if (i >= count) continue;
     tiles[i] = (((int64_t)g[i].M + kSB - 1) / kSB) * ((g[i].N + kSB - 1) / kSB);

@@ -18,9 +18,8 @@ struct SimtGemm {
   int act;
   int64_t ldo = 0;  // row stride of out, 0: N
   // Where rows are longer in memory: how many of A's rows and B's columns may be read (what lies past M and N is not
-  // used), and how many k of each (zeros in one, numbers in the other). 0: M, N, K. Multiples of 4 are read 16 bytes at
-  // a time.
-  int ma = 0, nb = 0, ka = 0, kb = 0;
+  // used), and how many k of A (zeros past K). 0: M, N, K. Multiples of 4 are read 16 bytes at a time.
+  int ma = 0, nb = 0, ka = 0;
 };
 
 // One product or two (count) in one launch. even: a product of few tiles and a long K is split although the other one
