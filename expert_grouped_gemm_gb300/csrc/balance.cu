@@ -11,8 +11,9 @@
 // sequence's rows in order, so results do not depend on timing. Tokens that one block takes need neither rows nor a
 // second kernel.
 //
-// Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value): bound by what a warp does for a
-// token, not by HBM.
+// Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value). Bound by what a warp does for a
+// token and by latency, not by HBM: 16384 x 256 in 37 sequences 13.4 us (17 MB are 2.6), 64 x 128 4.1, backward of
+// 8192 x 128 4.9.
 #include <algorithm>
 #include <type_traits>
 

@@ -63,7 +63,8 @@ cudaError_t launch_linear_fwd(const moe_linear_dims& d, void* ws, const void* x,
 cudaError_t launch_linear_bwd(const moe_linear_dims& d, void* ws, const void* dy, const void* x, const void* w,
                               const void* pre, const void* dx_add, void* dx, void* dw, void* dbias, int sms,
                               cudaStream_t st, int* launches);
-// A bf16 matrix *p of R rows of C replaced by its copy with rows of a multiple of 16 bytes, where C needs one.
-cudaError_t launch_pack_rows(const void** p, void* copy, int64_t R, int64_t C, int sms, cudaStream_t st, int* launches);
+// A bf16 matrix *p of R rows of C replaced by its copy with rows of ld, where that is not C.
+cudaError_t launch_pack_rows(const void** p, void* copy, int64_t R, int64_t C, int64_t ld, int sms, cudaStream_t st,
+                             int* launches);
 
 }  // namespace moe

@@ -509,11 +509,13 @@ struct Packed {
   PackArgs a = {};
   int count = 0;
   void add(const void** p, void* copy, int64_t R, int64_t C) {
-    if (C % 8 == 0) return;
+    if (C % 8) add(p, copy, R, C, up8(C));
+  }
+  void add(const void** p, void* copy, int64_t R, int64_t C, int64_t ld) {
     a.src[count] = static_cast<const __nv_bfloat16*>(*p);
     a.dst[count] = static_cast<__nv_bfloat16*>(copy);
     a.n[count] = R * C;
-    a.ld[count] = up8(C);
+    a.ld[count] = ld;
     a.C[count++] = (int)C;
     *p = copy;
   }
@@ -531,9 +533,10 @@ struct Packed {
 
 }  // namespace
 
-cudaError_t launch_pack_rows(const void** p, void* copy, int64_t R, int64_t C, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_pack_rows(const void** p, void* copy, int64_t R, int64_t C, int64_t ld, int sms, cudaStream_t st,
+                             int* launches) {
   Packed pk;
-  pk.add(p, copy, R, C);
+  if (ld != C) pk.add(p, copy, R, C, ld);
   return pk.run(sms, st, launches);
 }
 

@@ -6,8 +6,9 @@
 // Bound by HBM: every value is read once and written once. The tensors' descriptions travel as kernel arguments, so
 // that a launch needs no table on the device and a captured one keeps its own. The values of all tensors are cut into
 // chunks that never cross a tensor. With 32 bits a block takes one chunk (604M values in 2.40 ms, 7.1 TB/s; resident
-// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (34 a value), resident blocks walk them
-// (1.00 ms, 6.1 TB/s; a block each 1.03, two blocks' loads in flight against one 1.05).
+// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (35 a value), resident blocks walk them
+// (1.03 ms, 5.9 TB/s; a block each, measured before the last change of the arithmetic, 3% more). The norm of 604M bf16
+// values takes 175 us (7.0 TB/s).
 //
 // 8 bits: m and r = sqrt(v) are held as e4m3 (3 bits of mantissa, 17 powers of two) over a float for each 256 values,
 // their largest magnitude / 448. The root halves the span of exponents that v has. An r above zero never becomes zero:

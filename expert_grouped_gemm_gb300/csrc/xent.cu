@@ -5,8 +5,9 @@
 //
 // bf16: the tensor-core products' epilogue turns a tile of logits into the rows' statistics (largest, sum of
 // exponentials), or into dl, before anything is stored; the forward is one product over the whole vocabulary, the
-// backward takes it a piece at a time: dl of the piece, then its two products. fp32: the logits of a piece are stored,
-// then read. The target's logit is summed in fp32 on the CUDA cores: tensor cores truncate as they add, and a target's
+// backward takes it a piece at a time: dl of the piece, then its two products. Bound by the products: 4096 x 2048 x 131072
+// 5.44 ms (8 M H V flops at 1.62 PFLOP/s); statistics 1.15 ms by themselves, dl of 32768 columns 0.3. A few rows are a
+// stream of w: 8 x 2048 x 65536 50 us, 44 of them at 6.1 TB/s. fp32: the logits of a piece are stored, then read. The target's logit is summed in fp32 on the CUDA cores: tensor cores truncate as they add, and a target's
 // products are mostly of one sign.
 #include <algorithm>
 
@@ -21,9 +22,17 @@ namespace moe {
 namespace {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
-// the row length of a matrix that the products read
-int64_t up_row(const moe_xent_dims& d, int64_t n) { return d.dtype == MOE_BF16 ? up8(n) : n; }
+int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
+// Row lengths of the matrices that the products read. bf16: TMA wants multiples of 16 bytes, so odd rows are copied; a
+// copy's rows are whole 128-byte lines, which a box's rows then do not straddle. x is copied for that alone where it is
+// small beside the products (777 x 1000 x 50001 with an embedding table 331 -> 311 us; a copy of w as well 423).
+int64_t row_of_w(const moe_xent_dims& d) {
+  const int64_t C = d.tied ? d.H : d.V;
+  return d.dtype == MOE_BF16 && C % 8 ? up64(C) : C;
+}
+int64_t row_of_x(const moe_xent_dims& d) {
+  return d.dtype == MOE_BF16 && (d.H % 8 || (d.H % 64 && d.M >= 256 && d.V >= 8192)) ? up64(d.H) : d.H;
+}
 
 // (m, s) joined with (m2, s2): s e^m is the sum of both.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
@@ -318,11 +327,11 @@ __global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat1
 // 5.42 ms; with 2^26 5.60, 2^25 6.02, 2^28 5.38: the products of a piece have ragged last rounds).
 int64_t piece_cols(const moe_xent_dims& d) {
   const int64_t want = std::max<int64_t>(1024, (1ll << (d.dtype == MOE_BF16 ? 27 : 24)) / d.M / 256 * 256);
-  return std::min(want, up8(d.V));
+  return std::min(want, up64(d.V));
 }
 // Parts of K of a piece's dx product in bf16: its K is a piece of the vocabulary and its tiles may be few. 0: as
 // launch_linear_tc does it, which is as good or better; else pairs of CTAs, each with a tile's part, whose fp32 sums are
-// added afterwards (777 x 1000 over 50001 columns: 16 tiles for 76 pairs, 200 -> 70 us in 4 parts). Estimates as in
+// added afterwards (777 x 1000 over 50001 columns: 16 tiles for 76 pairs, 200 -> 93 us in 4 parts). Estimates as in
 // linear_choice.h; a part costs its sums' way to memory and back.
 int dx_parts(const moe_xent_dims& d) {
   constexpr int kSms = 152, kUnits = kSms / 2;
@@ -368,8 +377,8 @@ XentWs layout(const moe_xent_dims& d, bool backward) {
   L.at = take(bf ? (size_t)d.M * 4 : 0);
   L.dots = take((size_t)d.M * ((d.H + kDotCols - 1) / kDotCols) * 4);
   L.part = take((size_t)((d.M + kLossRows - 1) / kLossRows) * 8);
-  L.xp = take(up_row(d, d.H) != d.H ? (size_t)d.M * up_row(d, d.H) * 2 : 0);
-  L.wp = take(up_row(d, C) != C ? (size_t)R * up_row(d, C) * 2 : 0);
+  L.xp = take(row_of_x(d) != d.H ? (size_t)d.M * row_of_x(d) * 2 : 0);
+  L.wp = take(row_of_w(d) != C ? (size_t)R * row_of_w(d) * 2 : 0);
   L.piece = take(bf ? (backward ? (size_t)d.M * P * 2 : 0) : (size_t)d.M * P * 4);
   const int parts = bf ? dx_parts(d) : 0;
   L.dx = take(backward && bf && (parts || d.V > P) ? (size_t)d.M * d.H * 4 * std::max(parts, 1) : 0);
@@ -392,12 +401,11 @@ struct Xent {
   // 500 x 768 x 10007, where a product's odd rows cost 12).
   cudaError_t prepare() {
     P = piece_cols(d);
-    ldx = up_row(d, d.H);
-    ldw = d.tied ? ldx : up_row(d, d.V);
-    if (d.dtype != MOE_BF16) return cudaSuccess;
-    const cudaError_t e = launch_pack_rows(&x, ws + L.xp, d.M, d.H, sms, st, launches);
+    ldx = row_of_x(d);
+    ldw = row_of_w(d);
+    const cudaError_t e = launch_pack_rows(&x, ws + L.xp, d.M, d.H, ldx, sms, st, launches);
     if (e != cudaSuccess) return e;
-    return launch_pack_rows(&w, ws + L.wp, d.tied ? d.V : d.H, d.tied ? d.H : d.V, sms, st, launches);
+    return launch_pack_rows(&w, ws + L.wp, d.tied ? d.V : d.H, d.tied ? d.H : d.V, ldw, sms, st, launches);
   }
   const void* w_at(int64_t v0) const {
     return static_cast<const char*>(w) + (d.tied ? v0 * ldw : v0) * (d.dtype == MOE_BF16 ? 2 : 4);
