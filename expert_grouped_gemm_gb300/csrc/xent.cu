@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a)
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ float2 red[kLossWarps][kLossRows];
   __shared__ float2 rows[kLossRows];
+  __shared__ float sums[kLossWarps];
+  __shared__ int counts[kLossWarps];
   __shared__ bool last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * kLossRows;
@@ -243,28 +245,29 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a)
   if (gridDim.x == 1) return;
   __syncthreads();
   if (!last) return;
-  __shared__ double2 wide[kLossWarps];
-  double x = 0.0, y = 0.0;
+  // a thread's blocks in order, then trees: every sum of losses is of few and equal terms, the rows are counted as integers
+  float sum = 0.0f;
+  int n = 0;
   for (int i = threadIdx.x; i < (int)gridDim.x; i += kLossWarps * 32) {
     const float2 p = __ldcg(a.part + i);
-    x += p.x;
-    y += p.y;
+    sum += p.x;
+    n += (int)p.y;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
+  sum = warp_sum(sum);
+  n = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  if (lane == 0) {
+    sums[warp] = sum;
+    counts[warp] = n;
   }
-  if (lane == 0) wide[warp] = make_double2(x, y);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kLossWarps; ++i) {
-      x += wide[i].x;
-      y += wide[i].y;
+  if (warp == 0) {
+    sum = warp_sum(sums[lane]);
+    n = (int)__reduce_add_sync(0xffffffffu, (unsigned)counts[lane]);
+    if (lane == 0) {
+      a.total[0] = sum;
+      a.total[1] = (float)n;
+      *a.done = 0;
     }
-    a.total[0] = (float)x;
-    a.total[1] = (float)y;
-    *a.done = 0;
   }
 }
 
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat1
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
     float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (n % 4 == 0) {  // a part begins at a 16-byte boundary
-#pragma unroll 4
+#pragma unroll 8
       for (int p = 0; p < parts; ++p) {
         const float4 v = *reinterpret_cast<const float4*>(a + p * n + i);
         f[0] += v.x;
@@ -342,7 +345,7 @@ int dx_parts(const moe_xent_dims& d) {
   int best = 0;
   double t = choose_linear(d.M, d.H, std::min(P, d.V), false, kSms).us + (whole ? 0.0 : sums);
   const int64_t tiles = ((d.M + 255) / 256) * ((d.H + 255) / 256);
-  for (int p = 1; p <= 16 && kb / p >= 8; ++p) {
+  for (int p = 1; p <= kUnits && kb / p >= 8; ++p) {
     const double rounds = (double)((tiles * p + kUnits - 1) / kUnits);
     const double e = 2.23 + rounds * (0.300 * ((kb + p - 1) / p) + 3.05) + p * sums + (whole ? 3.0 : 0.0);
     if (e < t) {
