@@ -303,8 +303,38 @@ def test_xent_graphs_streams_and_bits():
     assert _lib.moe_read_status(ws) == _lib.MOE_OK
 
 
+def test_calls_at_once_on_two_streams():
+    """The same calls on two streams with workspaces of their own, nothing waited for in between."""
+    c = C.xent_case(130, 256, 5000, "bf16", seed=12)
+    b = C.balance_case(3000, 64, 4, [0, 700, 3000], "softmax", 0.1, seed=13)
+    grads = [torch.randn(70001, device="cuda") for _ in range(3)]
+    t = _lib.make_grad_tensors(grads)
+    runs = []
+    for _ in range(2):
+        d, ws = C.xent_setup(c)
+        bd = C.balance_dims(b)
+        runs.append(dict(stream=torch.cuda.Stream(), d=d, ws=ws, bd=bd, bws=_lib.alloc_balance_workspace(bd),
+                         nws=_lib.alloc_grad_norm_workspace(t), x=[C.nan(130), C.nan(130), C.nan(2)],
+                         g=[torch.empty_like(c["x"]), torch.empty_like(c["w"])], norm=C.nan(1),
+                         b=[C.nan(2), torch.zeros(2, 64, dtype=torch.int32, device="cuda"), C.nan(2, 64)]))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for r in runs:
+            st = r["stream"]
+            _lib.moe_balance_fwd(r["bd"], r["bws"], b["logits"], b["idx"], b["start"], *r["b"], stream=st)
+            _lib.moe_xent_fwd(r["d"], r["ws"], c["x"], c["w"], c["target"], *r["x"], stream=st)
+            _lib.moe_xent_bwd(r["d"], r["ws"], c["x"], c["w"], c["target"], r["x"][1], None, r["x"][2], *r["g"], stream=st)
+            _lib.moe_grad_norm(t, r["nws"], r["norm"], stream=st)
+    torch.cuda.synchronize()
+    for x, y in zip(*([*r["x"], *r["g"], *r["b"], r["norm"]] for r in runs)):
+        assert torch.equal(x, y)
+    C.check_xent_fwd(c, runs[0]["x"])
+    C.check_balance_fwd(b, runs[1]["b"])
+
+
 # ---------------------------------------------------------------- gradient norm
-@pytest.mark.parametrize("sizes", [[1], [0, 3], [255, 256, 257], [8192, 1, 40000], [7] * 30, list(range(1, 401)), [300000] * 3])
+@pytest.mark.parametrize("sizes", [[1], [0, 3], [255, 256, 257], [8192, 1, 40000], [7] * 30, list(range(1, 401)), [300000] * 3,
+                                   [5] * 1250 + [0] * 3, [0] * 2 + [9000] * 1300 + [0]])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_grad_norm(sizes, dtype):
     g = torch.Generator().manual_seed(len(sizes))
@@ -336,7 +366,8 @@ def test_grad_norm_of_nothing_and_of_nan():
 
 
 # ---------------------------------------------------------------- AdamW
-TENSORS = [[1], [3, 0, 5], [255, 256, 257, 4095, 4096, 4097], [1000] * 30, [100003], list(range(1, 420))]
+TENSORS = [[1], [3, 0, 5], [255, 256, 257, 4095, 4096, 4097], [1000] * 30, [100003], list(range(1, 420)),
+           [5000] * 400 + [0]]
 
 
 @pytest.mark.parametrize("sizes", TENSORS)
