@@ -104,7 +104,7 @@ struct SimtWork {
 // cluster) and the epilogue.
 __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB], int m0, int n0, int S, int part, int rank0) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const bool vec = g.N % 4 == 0 && g.ldo % 4 == 0;
+  const bool vec = g.pre ? g.N % 4 == 0 && g.ldo % 4 == 0 : (g.ldo ? g.ldo : g.N) % 4 == 0;
   const int n = n0 + tx * 4;
   for (int r = kSB * part / S + ty; r < kSB * (part + 1) / S; r += kSThreads / 16) {
     const int m = m0 + r;
@@ -131,7 +131,7 @@ __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (n + j < g.N) y[j] += g.residual[o + j];
-    if (vec) {
+    if (vec && n + 4 <= g.N) {
       if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
       *reinterpret_cast<float4*>(g.out + oy) = make_float4(y[0], y[1], y[2], y[3]);
     } else {

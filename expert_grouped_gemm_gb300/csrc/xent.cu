@@ -42,8 +42,10 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = big;
 }
 
-// A block a row: the piece's largest logit and sum joined to what earlier pieces left.
-__global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, int cols, float2* stat, int first) {
+// A block a row: the piece's largest logit and sum joined to what earlier pieces left; the target's logit where it is
+// among the piece's.
+__global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, int cols, int v0, const int* target,
+                                                    float2* stat, float* at_target, int first) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ float2 red[8];
   const int64_t t = blockIdx.x;
@@ -85,6 +87,8 @@ __global__ void __launch_bounds__(256) k_xent_piece(const float* l, int64_t ld, 
     for (int w = 1; w < 8; ++w) join(m, s, red[w].x, red[w].y);
     if (!first) join(m, s, stat[t].x, stat[t].y);
     stat[t] = make_float2(m, s);
+    const int64_t c = (int64_t)target[t] - v0;
+    if (c >= 0 && c < cols) at_target[t] = row[c];
   }
 }
 
@@ -143,8 +147,8 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_fold(float2* stat, int
 
 struct LossArgs {
   const float2* stat;  // [slots][M]
-  const float* at;     // BASE2: [M], the targets' logits as the product has them
-  const float* dots;   // [M][parts]
+  const float* at;     // [M], the targets' logits as the product has them
+  const float* dots;   // BASE2: [M][parts], their sums in fp32
   int first, end, M, V, parts;
   const int* target;
   float z;
@@ -156,12 +160,12 @@ struct LossArgs {
   int* status;
 };
 
-// The targets' logits in fp32, a warp 256 features of a row; a kernel of its own, so that the columns of w, a line for
+// The targets' logits of bf16 products in fp32, a warp 256 features of a row; a kernel of its own, so that the columns of w, a line for
 // every feature, are fetched by all SMs (8 rows of 2048 features: 20 us in one block of k_xent_loss, 3 us here).
 constexpr int kDotCols = 256;
-template <typename T>
-__global__ void __launch_bounds__(256) k_xent_dots(const T* x, const T* w, int64_t ldx, int64_t swh, int64_t swv,
-                                                   const int* target, int M, int H, int V, int parts, float* dots) {
+__global__ void __launch_bounds__(256) k_xent_dots(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t ldx, int64_t swh,
+                                                   int64_t swv, const int* target, int M, int H, int V, int parts,
+                                                   float* dots) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -176,8 +180,8 @@ __global__ void __launch_bounds__(256) k_xent_dots(const T* x, const T* w, int64
 #pragma unroll
     for (int i = 0; i < kDotCols / 32; ++i) {
       const int h = h0 + i * 32 + lane;
-      a[i] = h < H ? io<T>::to_f(x[h]) : 0.0f;
-      b[i] = h < H ? io<T>::to_f(w[h * swh]) : 0.0f;
+      a[i] = h < H ? __bfloat162float(x[h]) : 0.0f;
+      b[i] = h < H ? __bfloat162float(w[h * swh]) : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < kDotCols / 32; ++i) dot = fmaf(a[i], b[i], dot);
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(256) k_xent_dots(const T* x, const T* w, int64
 }
 
 // lse and loss of eight rows a block. Where the product's own logit of the target is given, the sum of exponentials is put
-// right by its difference to the fp32 one. The blocks' totals are added in order by the last one.
+// right by its difference to the fp32 one (BASE2). The blocks' totals are added in order by the last one.
 template <bool BASE2>
 __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
@@ -203,9 +207,13 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a)
   float at = 0.0f, had = 0.0f;
   if (warp < kLossRows && t < a.M) {
     v = a.target[t];
-    for (int i = lane; i < a.parts; i += 32) at += a.dots[t * a.parts + i];
-    at = warp_sum(at);
-    if (BASE2 && v >= 0 && v < a.V) had = a.at[t];
+    if (v >= 0 && v < a.V) had = a.at[t];
+    if constexpr (BASE2) {
+      for (int i = lane; i < a.parts; i += 32) at += a.dots[t * a.parts + i];
+      at = warp_sum(at);
+    } else {
+      at = had;
+    }
   }
   const float2 st = join_slots<BASE2>(a.stat, a.first, a.end, a.M, t0, red);
   if (warp < kLossRows && lane == 0) {
@@ -377,8 +385,8 @@ XentWs layout(const moe_xent_dims& d, bool backward) {
     return at;
   };
   L.stat = take((size_t)d.M * 8 * (bf ? 1 + (stat_cols(d) + kSlotCols - 1) / kSlotCols : 1));
-  L.at = take(bf ? (size_t)d.M * 4 : 0);
-  L.dots = take((size_t)d.M * ((d.H + kDotCols - 1) / kDotCols) * 4);
+  L.at = take((size_t)d.M * 4);
+  L.dots = take(bf ? (size_t)d.M * ((d.H + kDotCols - 1) / kDotCols) * 4 : 0);
   L.part = take((size_t)((d.M + kLossRows - 1) / kLossRows) * 8);
   L.xp = take(row_of_x(d) != d.H ? (size_t)d.M * row_of_x(d) * 2 : 0);
   L.wp = take(row_of_w(d) != C ? (size_t)R * row_of_w(d) * 2 : 0);
@@ -493,13 +501,11 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
   const int parts = (int)((d.H + kDotCols - 1) / kDotCols);
   const int64_t swh = d.tied ? 1 : c.ldw, swv = d.tied ? c.ldw : 1, warps = d.M * parts;
   if (warps / 8 >= (1ll << 31) - 1) return cudaErrorInvalidValue;
-  *launches += 1;
-  if (bf) MOE_LAUNCH(k_xent_dots<__nv_bfloat16>, (unsigned)((warps + 7) / 8), 256, 0, st, (const __nv_bfloat16*)c.x,
-                     (const __nv_bfloat16*)c.w, c.ldx, swh, swv, target, (int)d.M, (int)d.H, (int)d.V, parts, dots);
-  else MOE_LAUNCH(k_xent_dots<float>, (unsigned)((warps + 7) / 8), 256, 0, st, (const float*)c.x, (const float*)c.w, c.ldx,
-                  swh, swv, target, (int)d.M, (int)d.H, (int)d.V, parts, dots);
   int first = 0, end = 1;  // the slots to join
   if (bf) {
+    *launches += 1;
+    MOE_LAUNCH(k_xent_dots, (unsigned)((warps + 7) / 8), 256, 0, st, (const __nv_bfloat16*)c.x, (const __nv_bfloat16*)c.w,
+               c.ldx, swh, swv, target, (int)d.M, (int)d.H, (int)d.V, parts, dots);
     const int64_t cols = stat_cols(d);
     XentEpi epi = {};
     epi.part = stat + d.M;
@@ -523,7 +529,8 @@ cudaError_t launch_xent_fwd(const moe_xent_dims& d, void* ws, const void* x, con
       const int cols = (int)std::min(c.P, d.V - v0);
       if ((e = c.logits_f32(v0, cols)) != cudaSuccess) return e;
       *launches += 1;
-      MOE_LAUNCH(k_xent_piece, (unsigned)d.M, 256, 0, st, (const float*)c.piece(), c.P, cols, stat, (int)(v0 == 0));
+      MOE_LAUNCH(k_xent_piece, (unsigned)d.M, 256, 0, st, (const float*)c.piece(), c.P, cols, (int)v0, target,
+                 stat, at, (int)(v0 == 0));
     }
   }
   LossArgs a = {};
