@@ -213,6 +213,8 @@ __device__ __forceinline__ f2 both(float a) { return two(a, a); }
 template <int BITS>
 __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, const float (&g)[4], float (&p)[4],
                                         float (&m)[4], float (&v)[4]) {
+  float r[4];
+  uint32_t far = 0;
 #pragma unroll
   for (int j = 0; j < 4; j += 2) {
     const f2 gg = mul2(two(g[j], g[j + 1]), both(k.gs));
@@ -226,26 +228,38 @@ __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, co
     const f2 vn = fma2(both(k.c2), mul2(gg, gg), mul2(both(k.b2), vo));
     apart(mn, m[j], m[j + 1]);
     apart(vn, v[j], v[j + 1]);
-    float r[2], inv[2];
     if constexpr (BITS == 8) {
       float y[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"(fmaxf(v[j + i], 1.17549435e-38f)));
+      for (int i = 0; i < 2; ++i) {
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"(v[j + i]));
+        far = max(far, __float_as_uint(v[j + i]) - 0x00800000u);
+      }
       const f2 y2 = two(y[0], y[1]), r0 = mul2(vn, y2), half = mul2(y2, both(0.5f));
-      const f2 rest = fma2(mul2(r0, both(-1.0f)), r0, vn);
-      apart(fma2(rest, half, r0), r[0], r[1]);
-      v[j] = r[0];
-      v[j + 1] = r[1];
+      apart(fma2(fma2(mul2(r0, both(-1.0f)), r0, vn), half, r0), r[j], r[j + 1]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) asm("sqrt.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(v[j + i]));
+      for (int i = 0; i < 2; ++i) asm("sqrt.approx.f32 %0, %1;" : "=f"(r[j + i]) : "f"(v[j + i]));
     }
-    float den[2];
-    apart(fma2(two(r[0], r[1]), both(k.bc2), both(k.eps)), den[0], den[1]);
+  }
+  if constexpr (BITS == 8) {
+    if (far >= 0x7f000000u) {  // a v that is zero, denormal or not finite: the correction has no room there
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = __fsqrt_rn(v[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; j += 2) {
+    float den[2], inv[2];
+    apart(fma2(two(r[j], r[j + 1]), both(k.bc2), both(k.eps)), den[0], den[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[i]) : "f"(den[i]));
-    const f2 move = mul2(mul2(mn, both(-k.move)), two(inv[0], inv[1]));
+    const f2 move = mul2(mul2(two(m[j], m[j + 1]), both(-k.move)), two(inv[0], inv[1]));
     apart(fma2(both(k.keep), two(p[j], p[j + 1]), move), p[j], p[j + 1]);
+    if constexpr (BITS == 8) {
+      v[j] = r[j];
+      v[j + 1] = r[j + 1];
+    }
   }
 }
 

@@ -449,6 +449,30 @@ def test_adamw_values_that_are_not_finite_stay_alone(bits):
             assert torch.equal(a[other], b[other]) and torch.isfinite(a[ok]).all() and torch.isnan(a[300:302]).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("size", [1e-21, 3e-20, 2e-19, 1e20])
+def test_adamw_squares_that_leave_fp32(bits, size):
+    """Gradients whose squares are denormal, zero or infinite in fp32 (all of a tensor, so that 8-bit scales are as
+    small): roots and weights are what that arithmetic gives, and nothing is NaN."""
+    c = C.adamw_case([600], bits=bits, seed=9, step=3, eps=1e-30 if size < 1 else 1e-8, wd=0.0)
+    for k in ("m", "v"):
+        (c[k][0].view(torch.uint8) if bits == 8 else c[k][0]).zero_()
+    c["g"][0].copy_(torch.sign(c["g"][0]) * size * (0.5 + torch.rand(600, device="cuda")))
+    p0 = f64(c["p"][0])
+    g = f64(c["g"][0]).astype(np.float32)
+    C.run_adamw(c)
+    with np.errstate(over="ignore", under="ignore"):
+        v = np.float32(1 - 0.99) * (g * g)
+    m = np.float32(1 - 0.9) * g
+    r = np.sqrt(v.astype(np.float64))
+    want = p0 - np.float32(0.01) * (m / (1 - 0.9 ** 3)) / (r / np.sqrt(1 - 0.99 ** 3) + np.float32(c["eps"]))
+    got = f64(c["p"][0])
+    assert np.isfinite(got).all()
+    # v is off by a denormal's last place and half, r by half of that of itself
+    slack = 1e-5 + 2.0 ** -149 / np.maximum(v.astype(np.float64), 2.0 ** -149)
+    assert (np.abs(got - want) <= 2 * E32 * np.abs(p0) + slack * np.abs(want - p0)).all()
+
+
 def test_adamw8_small_roots_stay_above_zero():
     """In a block with one large gradient, states far below it: a root becomes at least the smallest code, so later
     steps do not divide by eps alone."""
