@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ T
   if (a.norm) {
     const float n = *a.norm;
     if (!(fabsf(n) < INFINITY)) return;  // a step on such gradients would destroy the weights: none is made
-    if (a.max_norm > 0.0f) gs *= a.max_norm / fmaxf(n, a.max_norm);
+    if (a.max_norm > 0.0f && n > a.max_norm) gs *= a.max_norm / n;  // no quotient of two infinities
   }
   if (a.lr_at) lr = *a.lr_at;
   if (a.step_at) {

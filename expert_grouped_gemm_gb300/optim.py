@@ -18,8 +18,9 @@ class AdamW:
                  weight_decay=0.01, lr_scale=1.0, state_bits: int = 32, master: bool = True, max_norm: float = 0.0,
                  grad_scale: float = 1.0, capturable: bool = False):
         """params, grads: lists of tensors, pairwise. master: bf16 weights get an fp32 copy, which the steps change.
-        max_norm > 0: gradients are clipped to that norm, and a step whose norm is inf or NaN leaves everything as it
-        is. capturable: lr and the step count live on the device (self.lr, self.t), so that a captured step moves on."""
+        max_norm > 0 (inf too): gradients are clipped to that norm, and a step whose norm is inf or NaN leaves weights and
+        states as they are, but is counted. capturable: lr and the step count live on the device (self.lr, self.t), so
+        that a captured step moves on."""
         params, grads = list(params), list(grads)
         if state_bits not in (32, 8):
             raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")

@@ -542,7 +542,7 @@ typedef struct moe_adamw_dims {
   float lr;             /* finite */
   float eps;            /* >= 2^-126, finite */
   float grad_scale;     /* factor on every gradient (finite) */
-  float max_norm;       /* gradients are scaled by min(1, max_norm / norm); <= 0: not clipped */
+  float max_norm;       /* gradients are scaled by min(1, max_norm / norm); <= 0, inf: not clipped */
   int32_t state_bits;   /* 32 or 8 */
 } moe_adamw_dims;
 

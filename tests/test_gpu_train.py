@@ -414,6 +414,20 @@ def test_adamw_clips_scales_and_skips(bits):
         assert torch.equal(raw(a), raw(b))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_limit_of_infinity_clips_nothing(bits):
+    """A limit that is there for the norm, and for steps that it leaves out."""
+    c = C.adamw_case([700], bits=bits, seed=12)
+    before = C.adamw_before(c)
+    norm = torch.tensor([8.0], device="cuda")
+    C.run_adamw(c, max_norm=INF, norm=norm)
+    C.check_adamw(c, before)
+    kept = c["p"][0].clone()
+    norm.fill_(INF)
+    C.run_adamw(c, max_norm=INF, norm=norm)
+    assert torch.equal(kept, c["p"][0])
+
+
 def test_adamw_factors_of_each_tensor():
     c = C.adamw_case([600, 600, 1], seed=4, wd=[0.0, 0.5, 0.25])
     before = C.adamw_before(c)
