@@ -8,8 +8,8 @@
 // Forward: tokens are cut into chunks of equal length, a block each; a block walks the sequences that its chunk
 // meets and writes one row of sums (p, counts, lse^2) for each. Row c + s holds chunk c of sequence s: along the
 // tokens either index only grows, so no two share a row and chunks + S rows are enough. A second kernel adds a
-// sequence's rows in order, so results do not depend on timing. Tokens that one block takes need neither rows nor a
-// second kernel.
+// sequence's rows in order, so results do not depend on timing. Few tokens of one or two sequences are one block's and
+// need neither rows nor a second kernel.
 //
 // Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value). Bound by what a warp does for a
 // token and by latency, not by HBM: 16384 x 256 in 37 sequences 13.4 us (17 MB are 2.6), 64 x 128 4.1, backward of
@@ -34,6 +34,7 @@ struct BalanceArgs {
   int T, E, k, S;
   int R, vec;         // experts of a lane, in 16-byte pieces
   int chunk, chunks;
+  bool one;           // a single block: its sums are the results
   float alpha, z;
   float* row_p;       // [chunks + S][E]
   int* row_n;         // [chunks + S][E]
@@ -241,10 +242,13 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E + lane * (128 / sizeof(TL))));
   for (int64_t i = (int64_t)c0 * a.k + threadIdx.x * 32; i < (int64_t)c1 * a.k; i += WARPS * 32 * 32)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.idx + i));
-  for (int s = seq_of(a, c0); s < a.S; ++s) {
+  for (int s = seq_of(a, c0); s < a.S;) {
     const int b0 = max(c0, seq_at(a, s)), b1 = min(c1, seq_at(a, s + 1));
     if (seq_at(a, s) >= c1) break;
-    if (b0 >= b1) continue;
+    if (b0 >= b1) {  // past a run of empty sequences at once
+      s = max(s + 1, seq_of(a, b0));
+      continue;
+    }
     for (int i = threadIdx.x; i < a.E; i += blockDim.x) hist[i] = 0;
     float acc[EPL], z = 0.0f, next[EPL];
 #pragma unroll
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
       float v = shared[i];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) v += shared[w * a.E + i];
-      if (a.chunks == 1) {  // the only block: these are the sequence's sums
+      if (a.one) {  // these are the sequence's sums
         v /= (float)(b1 - b0);
         dot += (float)hist[i] * v;
         a.count[(int64_t)s * a.E + i] = hist[i];
@@ -290,12 +294,13 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) v += zsum[w];
-      if (a.chunks == 1) z_all += v;
+      if (a.one) z_all += v;
       else a.row_z[row] = v;
     }
     __syncthreads();
+    ++s;
   }
-  if (a.chunks > 1) return;
+  if (!a.one) return;
   for (int s = 0; s < a.S; ++s) {
     check_seq(a, s);
     if (seq_at(a, s) < seq_at(a, s + 1)) continue;
@@ -413,13 +418,18 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
 
 // ---------------------------------------------------------------- host side
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-// One block takes what its warps get through in four tokens each (64 tokens of 128 experts 4.2 us; in two kernels 6.0);
-// more go in chunks of 8-warp blocks, four an SM (16384 x 256 in 37 sequences 13.2 us; one block of 32 warps an SM 16.9).
+// One block takes what its warps get through in four tokens each, of at most two sequences, which it walks one after the
+// other (64 tokens of 128 experts 4.3 us, 6.1 in two sequences, 30 in 16; in two kernels 6.0, 6.4 and 6.5). More go in chunks of 8-warp
+// blocks, four an SM (16384 x 256 in 37 sequences 13.2 us; one block of 32 warps an SM 16.9), of two tokens a warp, or as
+// many as a sequence has.
 constexpr int kChunkBlocks = 608;
 constexpr int kChunkWarps = 8;
 int one_block_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }  // as many as hold their sums in 32 KB
+bool one_block(const moe_balance_dims& d) { return d.T <= 4 * one_block_warps(d.E) && d.S <= 2; }
 int chunk_tokens(const moe_balance_dims& d) {
-  return (int)(d.T <= 4 * one_block_warps(d.E) ? d.T : std::max<int64_t>(2 * kChunkWarps, (d.T + kChunkBlocks - 1) / kChunkBlocks));
+  if (one_block(d)) return (int)d.T;
+  const int64_t each = std::clamp<int64_t>(d.T / std::max<int64_t>(d.S, 1), 1, 2 * kChunkWarps);
+  return (int)std::max<int64_t>(each, (d.T + kChunkBlocks - 1) / kChunkBlocks);
 }
 
 struct BalanceWs {
@@ -485,7 +495,7 @@ cudaError_t bwd_typed(const moe_balance_dims& d, const BalanceArgs& a, cudaStrea
 template <int EPL, bool SOFTMAX, typename TL>
 cudaError_t fwd_launch(const BalanceArgs& a, cudaStream_t st) {
   constexpr int W = EPL <= 8 ? 32 : EPL <= 16 ? 16 : 8;  // one_block_warps of every E that comes here
-  if (a.chunks == 1)
+  if (a.one)
     MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, TL, W>, 1, W * 32, (size_t)a.E * 4 * (W + 1), st, a);
   else
     MOE_LAUNCH(k_balance_fwd<EPL, SOFTMAX, TL, kChunkWarps>, a.chunks, kChunkWarps * 32, (size_t)a.E * 4 * (kChunkWarps + 1), st, a);
@@ -509,6 +519,7 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
   a.idx = topk_idx;
   a.chunk = chunk_tokens(d);
   a.chunks = (a.T + a.chunk - 1) / a.chunk;
+  a.one = one_block(d);
   a.row_p = reinterpret_cast<float*>(w + L.p);
   a.row_n = reinterpret_cast<int*>(w + L.n);
   a.row_z = reinterpret_cast<float*>(w + L.z);
@@ -518,12 +529,12 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
   a.loss = loss;
   a.count = count;
   a.prob = prob;
-  *launches += a.chunks == 1 ? 1 : 2;
+  *launches += a.one ? 1 : 2;
   const cudaError_t e = with_epl(a.R, [&](auto epl) {
     constexpr int EPL = decltype(epl)::value;
     return d.score == MOE_SCORE_SOFTMAX ? fwd_typed<EPL, true>(d, a, st) : fwd_typed<EPL, false>(d, a, st);
   });
-  if (e != cudaSuccess || a.chunks == 1) return e;
+  if (e != cudaSuccess || a.one) return e;
   // few sequences have many rows each: 128 of them at a time, eight columns a block (8192 x 128 in one sequence 9.0 us
   // with the first kernel; as below 13.0). Many have few (16384 x 256 in 37 sequences 13.4; as above 22.8)
   if (a.chunks >= 64 * a.S) MOE_LAUNCH((k_balance_sum<32, 8>), dim3((unsigned)a.S, (unsigned)((a.E + 7) / 8)), 1024, 0, st, a);

@@ -56,6 +56,18 @@ def test_balance_many_sequences(S):
     C.check_balance_bwd(c, out[1], C.run_balance_bwd(c, out[1]))
 
 
+@pytest.mark.parametrize("T,S", [(1, 1), (1, 2), (1, 3), (2, 3), (1, 5000), (7, 7), (17, 2), (17, 3), (64, 4), (64, 16),
+                                 (64, 5000), (128, 3), (128, 40), (128, 128), (130, 300)])
+def test_balance_few_tokens_in_sequences(T, S):
+    """From one sequence to far more than tokens: runs of empty ones before, between and behind the others."""
+    g = torch.Generator().manual_seed(T * 10007 + S)
+    at = torch.randint(0, min(T, 9) + 1, (S - 1,), generator=g) * T // min(T, 9)
+    c = C.balance_case(T, 40, 3, [0] + torch.sort(at).values.tolist() + [T], "softmax", 0.02, "f32", "f32", seed=S)
+    out = C.run_balance_fwd(c)
+    C.check_balance_fwd(c, out)
+    C.check_balance_bwd(c, out[1], C.run_balance_bwd(c, out[1]))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_balance_masks_and_extremes(score, dtype):
