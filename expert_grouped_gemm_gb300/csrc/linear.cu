@@ -380,43 +380,65 @@ int dz_chunks(int64_t M, int64_t N, int vec) {
 // Matrices with odd rows copied to rows of a multiple of 16 bytes, for the tensor-core products
 // (TMA reads rows at 16-byte strides). The columns past C of dst are never read. Up to two matrices
 // a launch: blocks [0, split) take the first.
+//
+// A thread stores 16 bytes of a row and loads the two aligned pieces of 16 that they lie in (one of
+// them its neighbour's, from L1): bound by HBM, 4096 x 50257 in 139 us, 5.9 TB/s (value by value 247).
 struct PackArgs {
-  const __nv_bfloat16* src[2];
+  const __nv_bfloat16* src[2];  // 16-byte aligned, as dst
   __nv_bfloat16* dst[2];
-  int64_t n[2], ld[2];  // elements, row stride of dst
+  int64_t n[2], ld[2];  // elements, row stride of dst (a multiple of 8)
   int C[2];
   int split;
 };
-constexpr int kPackPer = 2048;  // elements of a block's step
 
-__global__ void __launch_bounds__(256) k_pack_rows(const PackArgs a) {
+// U: stores of a thread's step, their loads in flight together.
+template <int U>
+__global__ void __launch_bounds__(256, 4) k_pack_rows(const __grid_constant__ PackArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  constexpr int U = kPackPer / 256;
   const int w = (int)blockIdx.x >= a.split;
   const int b = (int)blockIdx.x - (w ? a.split : 0), blocks = w ? (int)gridDim.x - a.split : a.split;
   const __nv_bfloat16* src = a.src[w];
   __nv_bfloat16* dst = a.dst[w];
   const int64_t n = a.n[w], ld = a.ld[w];
-  const int C = a.C[w];
-  for (int64_t base = (int64_t)b * kPackPer + threadIdx.x; base < n; base += (int64_t)blocks * kPackPer) {
-    __nv_bfloat16 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (base + u * 256 < n) v[u] = src[base + u * 256];
-    int64_t r = base / C;
-    int c = (int)(base - r * C);
+  const int C = a.C[w], row = (C + 7) / 8;  // stores of a row
+  const int64_t stores = n / C * row;
+  for (int64_t base = (int64_t)b * (256 * U) + threadIdx.x; base < stores; base += (int64_t)blocks * (256 * U)) {
+    int64_t r = base / row, from[U], to[U];
+    int c = (int)(base - r * row);
+    ulonglong2 lo[U], hi[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (base + u * 256 < n) dst[r * ld + c] = v[u];
+      const bool in = base + u * 256 < stores;
+      from[u] = in ? r * C + c * 8 : n;
+      to[u] = r * ld + c * 8;
+      const int64_t f = from[u] & ~7ll;
+      if (f + 16 <= n) {
+        const ulonglong2* p = reinterpret_cast<const ulonglong2*>(src + f);
+        lo[u] = p[0];
+        hi[u] = p[1];
+      }
       c += 256;
-      if (C >= 256) {
-        if (c >= C) {
-          c -= C;
+      if (row >= 256) {
+        if (c >= row) {
+          c -= row;
           ++r;
         }
       } else {
-        r += c / C;
-        c %= C;
+        r += c / row;
+        c %= row;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t f = from[u] & ~7ll;
+      if (f + 16 <= n) {
+        const bool far = from[u] & 4;
+        const int bits = (int)(from[u] & 3) * 16;
+        const uint64_t x = far ? lo[u].y : lo[u].x, y = far ? hi[u].x : lo[u].y, z = far ? hi[u].y : hi[u].x;
+        const auto joined = [&](uint64_t l, uint64_t h) { return l >> bits | h << 1 << (63 - bits); };
+        *reinterpret_cast<ulonglong2*>(dst + to[u]) = make_ulonglong2(joined(x, y), joined(y, z));
+      } else {  // where the matrix ends
+        for (int i = 0; i < 8 && from[u] + i < n; ++i) dst[to[u] + i] = src[from[u] + i];
       }
     }
   }
@@ -521,12 +543,17 @@ struct Packed {
   }
   cudaError_t run(int sms, cudaStream_t st, int* launches) {
     if (!count) return cudaSuccess;
-    int blocks[2] = {0, 0};
-    for (int i = 0; i < count; ++i)
-      blocks[i] = (int)std::min<int64_t>((a.n[i] + kPackPer - 1) / kPackPer, (int64_t)sms * 8);
-    a.split = blocks[0];
+    const int64_t most = (int64_t)sms * 8;
+    int64_t steps[2] = {0, 0};  // of blocks that store 16 bytes a thread
+    for (int i = 0; i < count; ++i) steps[i] = (a.n[i] / a.C[i] * ((a.C[i] + 7) / 8) + 255) / 256;
     *launches += 1;
-    MOE_LAUNCH(k_pack_rows, blocks[0] + blocks[1], 256, 0, st, a);
+    if (steps[0] <= most && steps[1] <= most) {
+      a.split = (int)steps[0];
+      MOE_LAUNCH(k_pack_rows<1>, a.split + (int)steps[1], 256, 0, st, a);
+    } else {
+      a.split = (int)std::min<int64_t>((steps[0] + 1) / 2, most);
+      MOE_LAUNCH(k_pack_rows<2>, a.split + (int)std::min<int64_t>((steps[1] + 1) / 2, most), 256, 0, st, a);
+    }
     return cudaSuccess;
   }
 };
