@@ -419,9 +419,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
 // ---------------------------------------------------------------- host side
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // One block takes what its warps get through in four tokens each, of at most two sequences, which it walks one after the
-// other (64 tokens of 128 experts 4.3 us, 6.1 in two sequences, 30 in 16; in two kernels 6.0, 6.4 and 6.5). More go in chunks of 8-warp
-// blocks, four an SM (16384 x 256 in 37 sequences 13.2 us; one block of 32 warps an SM 16.9), of two tokens a warp, or as
-// many as a sequence has.
+// other (64 tokens of 128 experts 4.3 us, 6.1 in two sequences, 30 in 16; in two kernels 6.0, 6.4 and 6.5). More go in
+// chunks of 8-warp blocks, four an SM (16384 x 256 in 37 sequences 13.2 us; one block of 32 warps an SM 16.9), of two
+// tokens a warp, or as many as a sequence has.
 constexpr int kChunkBlocks = 608;
 constexpr int kChunkWarps = 8;
 int one_block_warps(int64_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }  // as many as hold their sums in 32 KB

@@ -24,7 +24,7 @@ namespace {
 // or two (dx and dw), each with its own S: a cluster of the larger S holds several tiles of the other.
 // Together they fill the SMs that either leaves idle: 300 x 768 x 1000 with dz 41.8 -> 33.9 us, 17 x 256 x 700
 // 16.6 -> 10.7, 2000 x 2000 x 2000 740 -> 708.
-constexpr int kSB = 64, kSK = 16, kSThreads = 128;
+constexpr int kSB = kF32Tile, kSK = kF32Slab, kSThreads = 128;
 
 // A thread's eight elements of the 64 x 16 slab of an operand X[r, k] (r: the 64 rows of A or columns
 // of B): two 16-byte loads along the contiguous index where the rows allow, else eight loads with
@@ -102,7 +102,8 @@ struct SimtWork {
 
 // This block's share of a tile's rows, four columns a thread: the parts' sums (rank0: the tile's first block in its
 // cluster) and the epilogue.
-__device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB], int m0, int n0, int S, int part, int rank0) {
+__device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB], int m0, int n0, int S, int part, int rank0,
+                                            float* out) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const bool vec = g.pre ? g.N % 4 == 0 && g.ldo % 4 == 0 : (g.ldo ? g.ldo : g.N) % 4 == 0;
   const int n = n0 + tx * 4;
@@ -133,13 +134,13 @@ __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB
         if (n + j < g.N) y[j] += g.residual[o + j];
     if (vec && n + 4 <= g.N) {
       if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
-      *reinterpret_cast<float4*>(g.out + oy) = make_float4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<float4*>(out + oy) = make_float4(y[0], y[1], y[2], y[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (n + j < g.N) {
           if (g.pre) g.pre[o + j] = z[j];
-          g.out[oy + j] = y[j];
+          out[oy + j] = y[j];
         }
     }
   }
@@ -155,7 +156,8 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   const SimtGemm& g = work.g[second];
   const int S = work.S[second];
   const int block = (int)blockIdx.x - (second ? work.blocks0 : 0);
-  const int part = block % S, tile = block / S;
+  const int part = block % S;
+  int tile = block / S;
   const int rank0 = (int)(blockIdx.x % work.cluster) - part;  // the tile's first block in the cluster
   if (tile >= work.tiles[second]) {  // fills up the last cluster: nobody reads its sums
     if (work.cluster > 1) {
@@ -165,9 +167,18 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
     return;
   }
   const int nt = (g.N + kSB - 1) / kSB;
-  const int m0 = tile / nt * kSB, n0 = tile % nt * kSB;
   const int slabs = (g.K + kSK - 1) / kSK;
-  const int s0 = (int)((int64_t)slabs * part / S), s1 = (int)((int64_t)slabs * (part + 1) / S);
+  int first = part, all = S;  // this block's part of K, of so many
+  float* out = g.out;
+  if (g.parts > 1) {
+    const int per = (g.M + kSB - 1) / kSB * nt, q = tile / per;
+    tile -= q * per;
+    first += q * S;
+    all *= g.parts;
+    out += (int64_t)q * g.M * g.N;
+  }
+  const int s0 = (int)((int64_t)slabs * first / all), s1 = (int)((int64_t)slabs * (first + 1) / all);
+  const int m0 = tile / nt * kSB, n0 = tile % nt * kSB;
   Slab A, B;
   A.init(g.A, g.sam, g.sak, m0, g.ma, g.ka, tid);
   B.init(g.B, g.sbn, g.sbk, n0, g.nb, g.K, tid);
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   }
   if (work.cluster > 1) cluster_sync_all();
   else __syncthreads();
-  finish_rows(g, sums, m0, n0, S, part, rank0);
+  finish_rows(g, sums, m0, n0, S, part, rank0, out);
   if (work.cluster > 1) cluster_sync_all();  // no block leaves while another still reads its sums
 }
 
@@ -459,7 +470,8 @@ cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, 
     w.S[i] = 1;
     if (i >= count) continue;
     tiles[i] = (((int64_t)g[i].M + kSB - 1) / kSB) * ((g[i].N + kSB - 1) / kSB);
-    slabs[i] = (g[i].K + kSK - 1) / kSK;
+    slabs[i] = (g[i].K + kSK - 1) / kSK / g[i].parts;  // of a part, if K has parts
+    tiles[i] *= g[i].parts;
   }
   // four blocks fit an SM; the product with the longer parts is split while its blocks still fit beside
   // the other's, or (even) while a part of it would outlast the GPU's even share of all slabs; a part keeps at least
@@ -467,7 +479,7 @@ cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, 
   const int64_t slots = (int64_t)sms * 4, share = (tiles[0] * slabs[0] + tiles[1] * slabs[1]) / slots;
   while (true) {
     const int i = count > 1 && (int64_t)slabs[1] * w.S[0] > (int64_t)slabs[0] * w.S[1];
-    if (w.S[i] == 8 || slabs[i] < 8 * w.S[i]) break;
+    if (w.S[i] == kF32Cluster || slabs[i] < 8 * w.S[i]) break;
     if (tiles[0] * w.S[0] + tiles[1] * w.S[1] + tiles[i] * w.S[i] > slots && !(even && slabs[i] / w.S[i] > share)) break;
     w.S[i] *= 2;
   }

@@ -20,7 +20,12 @@ struct SimtGemm {
   // Where rows are longer in memory: how many of A's rows and B's columns may be read (what lies past M and N is not
   // used), and how many k of A (zeros past K). 0: M, N, K. Multiples of 4 are read 16 bytes at a time.
   int ma = 0, nb = 0, ka = 0;
+  // K in so many parts, whose sums lie one after the other, [parts][M, N] in out (no epilogue, no ldo), for the caller
+  // to add: for a product of few tiles whose K is long for the eight parts that a cluster adds.
+  int parts = 1;
 };
+
+constexpr int kF32Tile = 64, kF32Slab = 16, kF32Cluster = 8;  // rows and columns of a tile, k of a step, parts of a tile
 
 // One product or two (count) in one launch. even: a product of few tiles and a long K is split although the other one
 // fills the GPU.

@@ -7,8 +7,9 @@
 // exponentials), or into dl, before anything is stored; the forward is one product over the whole vocabulary, the
 // backward takes it a piece at a time: dl of the piece, then its two products. Bound by the products: 4096 x 2048 x 131072
 // 5.44 ms (8 M H V flops at 1.62 PFLOP/s); statistics 1.15 ms by themselves, dl of 32768 columns 0.3. A few rows are a
-// stream of w: 8 x 2048 x 65536 50 us, 44 of them at 6.1 TB/s. fp32: the logits of a piece are stored, then read. The target's logit is summed in fp32 on the CUDA cores: tensor cores truncate as they add, and a target's
-// products are mostly of one sign.
+// stream of w: 8 x 2048 x 65536 50 us, 44 of them at 6.1 TB/s. The target's logit is summed in fp32 on the CUDA cores:
+// tensor cores truncate as they add, and a target's products are mostly of one sign. fp32: the logits of a piece are
+// stored, then read.
 #include <algorithm>
 
 #include "act.cuh"
@@ -333,6 +334,17 @@ __global__ void __launch_bounds__(256) k_xent_round(const float* a, __nv_bfloat1
   }
 }
 
+// dx from the sums of fp32 parts, in order, added to what earlier pieces left (add).
+__global__ void __launch_bounds__(256) k_xent_add(const float* a, float* o, int64_t n, int parts, int add) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float v = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) v += a[p * n + i];
+    o[i] = add ? o[i] + v : v;
+  }
+}
+
 // ---------------------------------------------------------------- host side
 // Columns of a piece: a multiple of 256; about 2^27 values of dl in bf16, 2^24 logits in fp32 (4096 x 2048 x 131072
 // 5.42 ms; with 2^26 5.60, 2^25 6.02, 2^28 5.38: the products of a piece have ragged last rounds).
@@ -363,6 +375,19 @@ int dx_parts(const moe_xent_dims& d) {
   }
   return best;
 }
+// The same in fp32, 1: none but those that a cluster adds. While a cluster's part would last longer than the GPU's even
+// share of both products, and than 32 steps, which its sums' way to memory and a launch cost (backward of
+// 17 x 768 x 50257 505 -> 383 us, of 8 x 64 x 50257 280 -> 46).
+int dx_parts_f32(const moe_xent_dims& d, int64_t cols) {
+  constexpr int64_t kSlots = 152 * 4;
+  const auto tiles = [](int64_t m, int64_t n) { return ((m + kF32Tile - 1) / kF32Tile) * ((n + kF32Tile - 1) / kF32Tile); };
+  const auto steps = [](int64_t k) { return (k + kF32Slab - 1) / kF32Slab; };
+  const int64_t all = tiles(d.M, d.H) * steps(cols) + tiles(d.H, cols) * steps(d.M);
+  const int64_t most = std::max<int64_t>(all / kSlots, 32) * kF32Cluster;
+  int parts = 1;
+  while (parts < 64 && steps(cols) / parts > most) parts *= 2;
+  return parts;
+}
 constexpr int kSlotCols = 64;  // the narrowest slot of the statistics
 // Columns of a forward product in bf16: its statistics (with those of the columns before) stay below 256 MB, or 1 KB a row.
 int64_t stat_cols(const moe_xent_dims& d) {
@@ -391,8 +416,9 @@ XentWs layout(const moe_xent_dims& d, bool backward) {
   L.xp = take(row_of_x(d) != d.H ? (size_t)d.M * row_of_x(d) * 2 : 0);
   L.wp = take(row_of_w(d) != C ? (size_t)R * row_of_w(d) * 2 : 0);
   L.piece = take(bf ? (backward ? (size_t)d.M * P * 2 : 0) : (size_t)d.M * P * 4);
-  const int parts = bf ? dx_parts(d) : 0;
-  L.dx = take(backward && bf && (parts || d.V > P) ? (size_t)d.M * d.H * 4 * std::max(parts, 1) : 0);
+  const int parts = bf ? dx_parts(d) : dx_parts_f32(d, std::min(P, d.V));
+  const bool sums = bf ? parts || d.V > P : parts > 1;
+  L.dx = take(backward && sums ? (size_t)d.M * d.H * 4 * std::max(parts, 1) : 0);
   L.total = o;
   return L;
 }
@@ -468,9 +494,14 @@ struct Xent {
     float* out = static_cast<float*>(dw) + (dw ? (d.tied ? v0 * d.H : v0) : 0);
     SimtGemm g[2];
     int n = 0;
+    // no more than the workspace has room for: the last piece's share may be smaller
+    const int parts = dx ? std::min(dx_parts_f32(d, cols), dx_parts_f32(d, std::min(P, d.V))) : 1;
+    float* sums = reinterpret_cast<float*>(ws + L.dx);
     if (dx) {
       g[n] = {dl, fw, P, 1, d.tied ? ldw : 1, d.tied ? 1 : ldw, M, cols, H, nullptr,
-              v0 ? static_cast<const float*>(dx) : nullptr, static_cast<float*>(dx), nullptr, MOE_ACT_NONE};
+              v0 && parts == 1 ? static_cast<const float*>(dx) : nullptr, parts == 1 ? static_cast<float*>(dx) : sums, nullptr,
+              MOE_ACT_NONE};
+      g[n].parts = parts;
       g[n++].ka = up4(cols);  // rows of dl end in zeros
     }
     if (dw && d.tied) {
@@ -480,7 +511,13 @@ struct Xent {
       g[n] = {fx, dl, 1, ldx, P, 1, H, M, cols, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, d.V};
       g[n++].nb = up4(cols);
     }
-    return launch_linear_f32(g, n, true, sms, st, launches);
+    const cudaError_t e = launch_linear_f32(g, n, true, sms, st, launches);
+    if (e != cudaSuccess || parts == 1) return e;
+    *launches += 1;
+    const int64_t size = d.M * d.H;
+    MOE_LAUNCH(k_xent_add, (unsigned)std::min<int64_t>((size + 255) / 256, (int64_t)sms * 8), 256, 0, st, sums,
+               static_cast<float*>(dx), size, parts, (int)(v0 > 0));
+    return cudaSuccess;
   }
 };
 

@@ -206,6 +206,17 @@ def test_xent_several_pieces_f32(tied):
     C.check_xent_bwd(c, f64(c["dloss"]), C.run_xent_bwd(c, out[1], c["dloss"]))
 
 
+@pytest.mark.parametrize("M,H,V", [(1, 64, 50257), (17, 100, 30001), (300, 24, 70001), (3, 5, 9000)])
+@pytest.mark.parametrize("tied", [False, True])
+def test_xent_f32_few_tiles_of_a_long_vocabulary(M, H, V, tied):
+    """dx in parts of the vocabulary, in one piece and (300 rows) in two of different lengths."""
+    c = C.xent_case(M, H, V, "f32", tied, seed=11)
+    out = C.run_xent_fwd(c)
+    both = C.run_xent_bwd(c, out[1], c["dloss"])
+    C.check_xent_bwd(c, f64(c["dloss"]), both)
+    assert torch.equal(C.run_xent_bwd(c, out[1], c["dloss"], dw=False)[0], both[0])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_xent_one_output_only(dtype):
     c = C.xent_case(70, 96, 700, dtype, seed=5)
