@@ -7,8 +7,7 @@
 // that a launch needs no table on the device and a captured one keeps its own. The values of all tensors are cut into
 // chunks that never cross a tensor. With 32 bits a block takes one chunk (604M values in 2.40 ms, 7.1 TB/s; resident
 // blocks that walk 2.68); with 8 bits, where instructions count beside bytes (35 a value), resident blocks walk them
-// (1.03 ms, 5.9 TB/s; a block each, measured before the last change of the arithmetic, 3% more). The norm of 604M bf16
-// values takes 175 us (7.0 TB/s).
+// (1.05 ms, 5.8 TB/s; a block each 1.11). The norm of 604M bf16 values takes 175 us (7.0 TB/s).
 //
 // 8 bits: m and r = sqrt(v) are held as e4m3 (3 bits of mantissa, 17 powers of two) over a float for each 256 values,
 // their largest magnitude / 448. The root halves the span of exponents that v has. An r above zero never becomes zero:
@@ -206,6 +205,10 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 }
 __device__ __forceinline__ f2 both(float a) { return two(a, a); }
 
+// The root's correction needs a residual that is a float: below 2^-100 its last bits pass the smallest one, 2^-149.
+// Smaller v, zero and what is not finite take the library's root.
+constexpr uint32_t kRootMin = 0x0d800000u;  // 2^-100
+
 // The step of four values of a block; with 8 bits m and v hold codes' values, sm and sv what they are multiples of, and
 // v receives r = sqrt(v). Roundings are those of m = c1 g + (b1 m), v = c2 (g g) + (b2 v) with fused last steps, whatever
 // the compiler would join otherwise: in 8 bits a last bit can decide between two codes. For the same reason r is the
@@ -233,7 +236,7 @@ __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, co
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"(v[j + i]));
-        far = max(far, __float_as_uint(v[j + i]) - 0x00800000u);
+        far = max(far, __float_as_uint(v[j + i]) - kRootMin);
       }
       const f2 y2 = two(y[0], y[1]), r0 = mul2(vn, y2), half = mul2(y2, both(0.5f));
       apart(fma2(fma2(mul2(r0, both(-1.0f)), r0, vn), half, r0), r[j], r[j + 1]);
@@ -243,7 +246,7 @@ __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, co
     }
   }
   if constexpr (BITS == 8) {
-    if (far >= 0x7f000000u) {  // a v that is zero, denormal or not finite: the correction has no room there
+    if (far >= 0x7f800000u - kRootMin) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[j] = __fsqrt_rn(v[j]);
     }
