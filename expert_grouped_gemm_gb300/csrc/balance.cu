@@ -12,8 +12,8 @@
 // need neither rows nor a second kernel.
 //
 // Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value). Bound by what a warp does for a
-// token and by latency, not by HBM: 16384 x 256 in 37 sequences 13.4 us (17 MB are 2.6), 64 x 128 4.1, backward of
-// 8192 x 128 4.9.
+// token and by latency, not by HBM: 16384 x 256 in 37 sequences 13.1 us (17 MB are 2.6), 64 x 128 4.1, backward of
+// 8192 x 128 3.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -32,7 +32,7 @@ struct BalanceArgs {
   const int* idx;
   const int* start;   // [S + 1] or null
   int T, E, k, S;
-  int R, vec;         // experts of a lane, in 16-byte pieces
+  int R, vec;         // experts of a lane; whether in fours
   int chunk, chunks;
   bool one;           // a single block: its sums are the results
   float alpha, z;
@@ -73,29 +73,44 @@ __device__ __forceinline__ float tokens_of_all(const BalanceArgs& a) {
   return fmaxf(1.0f, (float)(seq_at(a, a.S) - seq_at(a, 0)));
 }
 
-// The lane's n logits (of at most EPL) at p; NaN masks its expert as -inf does.
+// A lane's experts: slot i holds expert first + (i / 4) 128 + (i % 4) step, four neighbours or every 32nd, so that a warp's
+// accesses are of whole lines (backward of 65536 x 1024 100 us, with a lane's experts next to each other 373; of
+// 8192 x 128 3.8 and 4.9).
+struct Lane {
+  int first, step, E;
+  __device__ __forceinline__ Lane(const BalanceArgs& a)
+      : first((threadIdx.x & 31) * (a.vec ? 4 : 1)), step(a.vec ? 1 : 32), E(a.E) {}
+  __device__ __forceinline__ int at(int i) const { return first + (i >> 2) * 128 + (i & 3) * step; }
+  __device__ __forceinline__ bool has(int i) const { return at(i) < E; }
+};
+
+// Four neighbouring values at p, 16 bytes of floats or 8 of bf16.
+template <typename T>
+using Quad = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+
+// The lane's logits of a row; NaN masks its expert as -inf does.
 template <int EPL, typename TL>
-__device__ __forceinline__ void load_row(const TL* p, int n, bool vec, float (&l)[EPL]) {
-  constexpr int V = 16 / (int)sizeof(TL);
-  if constexpr (EPL % V == 0) {
+__device__ __forceinline__ void load_row(const TL* row, const Lane& x, bool vec, float (&l)[EPL]) {
+  bool done = false;
+  if constexpr (EPL % 4 == 0) {
     if (vec) {
 #pragma unroll
-      for (int i = 0; i < EPL; i += V) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (i < n) u = *reinterpret_cast<const uint4*>(p + i);
+      for (int i = 0; i < EPL; i += 4) {
+        Quad<TL> u = {};
+        if (x.has(i)) u = *reinterpret_cast<const Quad<TL>*>(row + x.at(i));
         const TL* e = reinterpret_cast<const TL*>(&u);
 #pragma unroll
-        for (int q = 0; q < V; ++q) l[i + q] = i < n ? io<TL>::to_f(e[q]) : -INFINITY;
+        for (int q = 0; q < 4; ++q) l[i + q] = x.has(i) ? io<TL>::to_f(e[q]) : -INFINITY;
       }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) l[i] = fmaxf(l[i], -INFINITY);  // of NaN and a number: the number
-      return;
+      done = true;
     }
   }
+  if (!done) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    l[i] = fmaxf(i < n ? io<TL>::to_f(p[i]) : -INFINITY, -INFINITY);
+    for (int i = 0; i < EPL; ++i) l[i] = x.has(i) ? io<TL>::to_f(row[x.at(i)]) : -INFINITY;
   }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) l[i] = fmaxf(l[i], -INFINITY);  // of NaN and a number: the number
 }
 
 // Whether a row has a z loss: not where every logit is masked, by -inf or by its type's lowest value (the square of
@@ -232,9 +247,9 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
   __shared__ float zsum[WARPS];
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
+  const Lane x(a);
   const int c0 = (int)blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.T);
-  const TL* logits = reinterpret_cast<const TL*>(a.logits) + e0;
+  const TL* logits = reinterpret_cast<const TL*>(a.logits);
   float dot = 0.0f, z_all = 0.0f;  // of the only block
   // towards L2 while the sequences are looked for: a lane 128 bytes of the warp's rows and of the indices
   for (int t = c0 + warp; t < c1; t += WARPS)
@@ -253,12 +268,12 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
     float acc[EPL], z = 0.0f, next[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-    if (b0 + warp < b1) load_row<EPL>(logits + (int64_t)(b0 + warp) * a.E, n, a.vec, next);
+    if (b0 + warp < b1) load_row<EPL>(logits + (int64_t)(b0 + warp) * a.E, x, a.vec, next);
     for (int t = b0 + warp; t < b1; t += WARPS) {
       float l[EPL];
 #pragma unroll
       for (int i = 0; i < EPL; ++i) l[i] = next[i];
-      if (t + WARPS < b1) load_row<EPL>(logits + (int64_t)(t + WARPS) * a.E, n, a.vec, next);
+      if (t + WARPS < b1) load_row<EPL>(logits + (int64_t)(t + WARPS) * a.E, x, a.vec, next);
       const float lse = probs<EPL, SOFTMAX>(l, nullptr);
       if (SOFTMAX && has_lse(lse)) z += lse * lse;
 #pragma unroll
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
     if (lane == 0) zsum[warp] = z;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (i < n) shared[warp * a.E + e0 + i] = acc[i];
+      if (x.has(i)) shared[warp * a.E + x.at(i)] = acc[i];
     __syncthreads();
     const int64_t i1 = (int64_t)b1 * a.k;
     for (int64_t i = (int64_t)b0 * a.k + threadIdx.x; i < i1; i += blockDim.x) {
@@ -359,22 +374,22 @@ __global__ void __launch_bounds__(kSumWarps * 32) k_balance_sum(const BalanceArg
 template <int EPL, bool SOFTMAX, typename TL, typename TG>
 __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
-  const int t = (int)blockIdx.x * kWarps + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int t = (int)blockIdx.x * kWarps + (int)(threadIdx.x >> 5);
   if (t >= a.T) return;
-  const int e0 = lane * a.R, n = min(max(a.E - e0, 0), a.R);
-  const int64_t o = (int64_t)t * a.E + e0;
+  const Lane x(a);
+  const int64_t o = (int64_t)t * a.E;
   const int s = seq_of(a, t), t0 = seq_at(a, s), t1 = seq_at(a, s + 1);
   float l[EPL];
   if (t >= t0 && t < t1) {
     const float N = tokens_of_all(a), up = a.dloss ? *a.dloss : 1.0f;
-    load_row<EPL>(reinterpret_cast<const TL*>(a.logits) + o, n, a.vec, l);
+    load_row<EPL>(reinterpret_cast<const TL*>(a.logits) + o, x, a.vec, l);
     float away[SOFTMAX ? 1 : EPL];
     const float lse = probs<EPL, SOFTMAX>(l, SOFTMAX ? nullptr : away);
     const float f = up * a.alpha * ((float)a.E / (float)a.k) / N / (float)(t1 - t0);
     float c[EPL], dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      c[i] = i < n ? f * (float)a.count_in[(int64_t)s * a.E + e0 + i] : 0.0f;
+      c[i] = x.has(i) ? f * (float)a.count_in[(int64_t)s * a.E + x.at(i)] : 0.0f;
       dot += l[i] * c[i];
     }
     dot = warp_sum(dot);
@@ -390,30 +405,28 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
   }
   const TG* add = reinterpret_cast<const TG*>(a.add);
   TG* out = reinterpret_cast<TG*>(a.dlogits);
-  constexpr int V = 16 / (int)sizeof(TG);
-  if constexpr (EPL % V == 0) {
+  if constexpr (EPL % 4 == 0) {
     if (a.vec) {
 #pragma unroll
-      for (int i = 0; i < EPL; i += V) {
-        if (i >= n) break;
-        if (add) {
-          const uint4 u = *reinterpret_cast<const uint4*>(add + o + i);
-          const TG* q = reinterpret_cast<const TG*>(&u);
-#pragma unroll
-          for (int j = 0; j < V; ++j) l[i + j] += io<TG>::to_f(q[j]);
-        }
-        uint4 u;
+      for (int i = 0; i < EPL; i += 4) {
+        if (!x.has(i)) break;
+        Quad<TG> u;
         TG* q = reinterpret_cast<TG*>(&u);
+        if (add) {
+          u = *reinterpret_cast<const Quad<TG>*>(add + o + x.at(i));
 #pragma unroll
-        for (int j = 0; j < V; ++j) q[j] = io<TG>::cvt(l[i + j]);
-        *reinterpret_cast<uint4*>(out + o + i) = u;
+          for (int j = 0; j < 4; ++j) l[i + j] += io<TG>::to_f(q[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = io<TG>::cvt(l[i + j]);
+        *reinterpret_cast<Quad<TG>*>(out + o + x.at(i)) = u;
       }
       return;
     }
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
-    if (i < n) out[o + i] = io<TG>::cvt(l[i] + (add ? io<TG>::to_f(add[o + i]) : 0.0f));
+    if (x.has(i)) out[o + x.at(i)] = io<TG>::cvt(l[i] + (add ? io<TG>::to_f(add[o + x.at(i)]) : 0.0f));
 }
 
 // ---------------------------------------------------------------- host side
@@ -461,7 +474,7 @@ cudaError_t with_epl(int R, F f) {
   return f(std::integral_constant<int, 32>());  // E <= 1024
 }
 
-BalanceArgs args_of(const moe_balance_dims& d, const void* logits, const int* start, bool half) {
+BalanceArgs args_of(const moe_balance_dims& d, const void* logits, const int* start) {
   BalanceArgs a = {};
   a.logits = logits;
   a.start = d.S ? start : nullptr;
@@ -471,10 +484,8 @@ BalanceArgs args_of(const moe_balance_dims& d, const void* logits, const int* st
   a.S = (int)std::max<int64_t>(d.S, 1);
   a.alpha = d.alpha;
   a.z = d.z_coef;
-  a.R = (a.E + 31) / 32;
-  const int V = half ? 8 : 4;
-  a.vec = a.E % V == 0;
-  if (a.vec) a.R = (a.R + V - 1) / V * V;
+  a.vec = a.E % 4 == 0 && a.E > 64;  // of up to 64, more lanes at work are better (65536 x 64 backward 20.6 us, in fours 23.1)
+  a.R = a.vec ? (a.E + 127) / 128 * 4 : (a.E + 31) / 32;
   return a;
 }
 
@@ -513,7 +524,7 @@ size_t balance_workspace_bytes(const moe_balance_dims& d) { return layout(d).tot
 cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* logits, const int* topk_idx,
                                const int* seq_start, float* loss, int* count, float* prob, cudaStream_t st,
                                int* launches) {
-  BalanceArgs a = args_of(d, logits, seq_start, d.dtype == MOE_BF16);
+  BalanceArgs a = args_of(d, logits, seq_start);
   const BalanceWs L = layout(d);
   char* w = static_cast<char*>(ws);
   a.idx = topk_idx;
@@ -545,7 +556,7 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
 cudaError_t launch_balance_bwd(const moe_balance_dims& d, const void* logits, const int* count, const int* seq_start,
                                const float* dloss, const void* dlogits_add, void* dlogits, cudaStream_t st,
                                int* launches) {
-  BalanceArgs a = args_of(d, logits, seq_start, d.dtype == MOE_BF16 || d.grad_dtype == MOE_BF16);
+  BalanceArgs a = args_of(d, logits, seq_start);
   a.count_in = count;
   a.dloss = dloss;
   a.add = dlogits_add;
