@@ -6,8 +6,8 @@
 // Bound by HBM: every value is read once and written once. The tensors' descriptions travel as kernel arguments, so
 // that a launch needs no table on the device and a captured one keeps its own. The values of all tensors are cut into
 // chunks that never cross a tensor. With 32 bits a block takes one chunk (604M values in 2.40 ms, 7.1 TB/s; resident
-// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (35 a value), resident blocks walk them
-// (1.05 ms, 5.8 TB/s; a block each 1.11). The norm of 604M bf16 values takes 175 us (7.0 TB/s).
+// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (36 a value), resident blocks walk them
+// (1.06 ms, 5.8 TB/s; a block each 1.11). The norm of 604M bf16 values takes 175 us (7.0 TB/s).
 //
 // 8 bits: m and r = sqrt(v) are held as e4m3 (3 bits of mantissa, 17 powers of two) over a float for each 256 values,
 // their largest magnitude / 448. The root halves the span of exponents that v has. An r above zero never becomes zero:
@@ -182,7 +182,9 @@ struct AdamWArgs {
 // What the values of a tensor share in a step.
 struct Factors {
   float gs, b1, c1, b2, c2, bc2, eps;  // gs: the gradients' factor
-  float keep, move;                    // w = keep w - move m / (r bc2 + eps)
+  // w = w + (-decay w - move m / (r bc2 + eps)). The decay joins the change, not a factor 1 - decay: a float next to one
+  // is off by up to 2^-25, the same way for every value and step (lr 1e-5 with a decay of 0.01: 1.19 times it).
+  float decay, move;
 };
 
 // Two floats in one 64-bit operand: the same roundings in half the instructions.
@@ -196,6 +198,11 @@ __device__ __forceinline__ void apart(f2 x, float& a, float& b) { asm("mov.b64 {
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   f2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
@@ -258,7 +265,8 @@ __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, co
 #pragma unroll
     for (int i = 0; i < 2; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[i]) : "f"(den[i]));
     const f2 move = mul2(mul2(two(m[j], m[j + 1]), both(-k.move)), two(inv[0], inv[1]));
-    apart(fma2(both(k.keep), two(p[j], p[j + 1]), move), p[j], p[j + 1]);
+    const f2 w = two(p[j], p[j + 1]);
+    apart(add2(w, fma2(both(-k.decay), w, move)), p[j], p[j + 1]);
     if constexpr (BITS == 8) {
       v[j] = r[j];
       v[j + 1] = r[j + 1];
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ T
     at = tensor_of(tab, chunk, at);
     const Entry& e = tab.e[at];
     const float elr = lr * e.lr_scale;
-    k.keep = 1.0f - elr * e.wd;
+    k.decay = elr * e.wd;
     k.move = elr * bc1;
     constexpr int kSteps = steps_of<BITS>;
     const int64_t blk0 = (int64_t)(chunk - e.first) * (kWarps * kSteps), blk = blk0 + warp;
