@@ -251,12 +251,17 @@ __global__ void __launch_bounds__(WARPS * 32) k_balance_fwd(const BalanceArgs a)
   const int c0 = (int)blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.T);
   const TL* logits = reinterpret_cast<const TL*>(a.logits);
   float dot = 0.0f, z_all = 0.0f;  // of the only block
-  // towards L2 while the sequences are looked for: a lane 128 bytes of the warp's rows and of the indices
-  for (int t = c0 + warp; t < c1; t += WARPS)
-    if (lane * (128 / (int)sizeof(TL)) < a.E)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E + lane * (128 / sizeof(TL))));
-  for (int64_t i = (int64_t)c0 * a.k + threadIdx.x * 32; i < (int64_t)c1 * a.k; i += WARPS * 32 * 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.idx + i));
+  // Towards L2 while the sequences are looked for: a lane 128 bytes of the warp's rows and of the indices. Of short chunks
+  // alone (rows not in L2: 64 x 128 4.9 us without, 4.6 with; 4096 x 64 in 8 sequences 11.0, 10.0; 16384 x 256 in 37, 27
+  // rows a chunk, 15.0, 14.9). In longer ones the next row's loads, which are always under way, do better than requests for
+  // all of them at once (32768 x 256, 54 rows a chunk, 17.4, 18.8; 65536 x 1024 60, 71; 2^20 x 256 245, 305).
+  if (a.chunk <= 4 * WARPS) {
+    for (int t = c0 + warp; t < c1; t += WARPS)
+      if (lane * (128 / (int)sizeof(TL)) < a.E)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const TL*>(a.logits) + (int64_t)t * a.E + lane * (128 / sizeof(TL))));
+    for (int64_t i = (int64_t)c0 * a.k + threadIdx.x * 32; i < (int64_t)c1 * a.k; i += WARPS * 32 * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.idx + i));
+  }
   for (int s = seq_of(a, c0); s < a.S;) {
     const int b0 = max(c0, seq_at(a, s)), b1 = min(c1, seq_at(a, s + 1));
     if (seq_at(a, s) >= c1) break;
