@@ -102,10 +102,11 @@ struct SimtWork {
 
 // This block's share of a tile's rows, four columns a thread: the parts' sums (rank0: the tile's first block in its
 // cluster) and the epilogue.
+template <bool XENT>
 __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB], int m0, int n0, int S, int part, int rank0,
                                             float* out) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const bool vec = g.pre ? g.N % 4 == 0 && g.ldo % 4 == 0 : (g.ldo ? g.ldo : g.N) % 4 == 0;
+  const bool vec = (XENT && g.ldo ? g.ldo : g.N) % 4 == 0;
   const int n = n0 + tx * 4;
   for (int r = kSB * part / S + ty; r < kSB * (part + 1) / S; r += kSThreads / 16) {
     const int m = m0 + r;
@@ -122,7 +123,7 @@ __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB
       z[2] += v.z;
       z[3] += v.w;
     }
-    const int64_t o = (int64_t)m * g.N + n, oy = g.ldo ? (int64_t)m * g.ldo + n : o;
+    const int64_t o = (int64_t)m * g.N + n, oy = XENT && g.ldo ? (int64_t)m * g.ldo + n : o;
     if (g.bias)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -132,7 +133,7 @@ __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (n + j < g.N) y[j] += g.residual[o + j];
-    if (vec && n + 4 <= g.N) {
+    if (vec && (!XENT || n + 4 <= g.N)) {
       if (g.pre) *reinterpret_cast<float4*>(g.pre + o) = make_float4(z[0], z[1], z[2], z[3]);
       *reinterpret_cast<float4*>(out + oy) = make_float4(y[0], y[1], y[2], y[3]);
     } else {
@@ -146,6 +147,9 @@ __device__ __forceinline__ void finish_rows(const SimtGemm& g, float (*sums)[kSB
   }
 }
 
+// XENT: a product of the cross entropy, whose matrices have rows of their own lengths and whose K may have parts
+// (SimtGemm); the linear operator's kernel does not look for either.
+template <bool XENT>
 __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   __shared__ __align__(16) float sa[2][kSK][kSB + 4];
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   const int slabs = (g.K + kSK - 1) / kSK;
   int first = part, all = S;  // this block's part of K, of so many
   float* out = g.out;
-  if (g.parts > 1) {
+  if (XENT && g.parts > 1) {
     const int per = (g.M + kSB - 1) / kSB * nt, q = tile / per;
     tile -= q * per;
     first += q * S;
@@ -180,8 +184,8 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   const int s0 = (int)((int64_t)slabs * first / all), s1 = (int)((int64_t)slabs * (first + 1) / all);
   const int m0 = tile / nt * kSB, n0 = tile % nt * kSB;
   Slab A, B;
-  A.init(g.A, g.sam, g.sak, m0, g.ma, g.ka, tid);
-  B.init(g.B, g.sbn, g.sbk, n0, g.nb, g.K, tid);
+  A.init(g.A, g.sam, g.sak, m0, XENT ? g.ma : g.M, XENT ? g.ka : g.K, tid);
+  B.init(g.B, g.sbn, g.sbk, n0, XENT ? g.nb : g.N, g.K, tid);
   auto fetch = [&](int s) {
     A.fetch(s);
     B.fetch(s);
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(kSThreads, 4) k_linear_f32(const SimtWork work
   }
   if (work.cluster > 1) cluster_sync_all();
   else __syncthreads();
-  finish_rows(g, sums, m0, n0, S, part, rank0, out);
+  finish_rows<XENT>(g, sums, m0, n0, S, part, rank0, out);
   if (work.cluster > 1) cluster_sync_all();  // no block leaves while another still reads its sums
 }
 
@@ -458,7 +462,7 @@ __global__ void __launch_bounds__(256, 4) k_pack_rows(const __grid_constant__ Pa
 }  // namespace
 
 // One product or two (count) in one launch.
-cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, cudaStream_t st, int* launches) {
+cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool xent, int sms, cudaStream_t st, int* launches) {
   SimtWork w;
   int64_t tiles[2] = {0, 0};
   int slabs[2] = {0, 0};
@@ -474,13 +478,13 @@ cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, 
     tiles[i] *= g[i].parts;
   }
   // four blocks fit an SM; the product with the longer parts is split while its blocks still fit beside
-  // the other's, or (even) while a part of it would outlast the GPU's even share of all slabs; a part keeps at least
+  // the other's, or (xent) while a part of it would outlast the GPU's even share of all slabs; a part keeps at least
   // four slabs
   const int64_t slots = (int64_t)sms * 4, share = (tiles[0] * slabs[0] + tiles[1] * slabs[1]) / slots;
   while (true) {
     const int i = count > 1 && (int64_t)slabs[1] * w.S[0] > (int64_t)slabs[0] * w.S[1];
     if (w.S[i] == kF32Cluster || slabs[i] < 8 * w.S[i]) break;
-    if (tiles[0] * w.S[0] + tiles[1] * w.S[1] + tiles[i] * w.S[i] > slots && !(even && slabs[i] / w.S[i] > share)) break;
+    if (tiles[0] * w.S[0] + tiles[1] * w.S[1] + tiles[i] * w.S[i] > slots && !(xent && slabs[i] / w.S[i] > share)) break;
     w.S[i] *= 2;
   }
   w.cluster = std::max(w.S[0], w.S[1]);
@@ -507,7 +511,7 @@ cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, 
   cfg.attrs = at;
   cfg.numAttrs = n;
   *launches += 1;
-  return cudaLaunchKernelEx(&cfg, k_linear_f32, w);
+  return xent ? cudaLaunchKernelEx(&cfg, k_linear_f32<true>, w) : cudaLaunchKernelEx(&cfg, k_linear_f32<false>, w);
 }
 
 namespace {

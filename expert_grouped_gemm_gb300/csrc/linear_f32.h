@@ -16,6 +16,7 @@ struct SimtGemm {
   float* out;
   float* pre;
   int act;
+  // the cross entropy's alone:
   int64_t ldo = 0;  // row stride of out, 0: N
   // Where rows are longer in memory: how many of A's rows and B's columns may be read (what lies past M and N is not
   // used), and how many k of A (zeros past K). 0: M, N, K. Multiples of 4 are read 16 bytes at a time.
@@ -27,8 +28,8 @@ struct SimtGemm {
 
 constexpr int kF32Tile = 64, kF32Slab = 16, kF32Cluster = 8;  // rows and columns of a tile, k of a step, parts of a tile
 
-// One product or two (count) in one launch. even: a product of few tiles and a long K is split although the other one
-// fills the GPU.
-cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool even, int sms, cudaStream_t st, int* launches);
+// One product or two (count) in one launch. xent: ldo, ma, nb, ka and parts are taken, and a product of few tiles and a
+// long K is split although the other one fills the GPU.
+cudaError_t launch_linear_f32(const SimtGemm* g, int count, bool xent, int sms, cudaStream_t st, int* launches);
 
 }  // namespace moe

@@ -1,64 +1,26 @@
 // linear_tc.cu -- the linear operator's launches of the tensor-core products.
-#include "linear_choice.h"
 #include "linear_tc.cuh"
 
 namespace moe {
 namespace {
 
-template <int CTAS, int BN, bool VEC, bool F32>
-cudaError_t launch_tile_as(const LinearGemm& g, int sms, cudaStream_t st) {
-  TcWork<1> w;
-  if (!fill<CTAS, BN, VEC, F32>(&w, 0, g)) return cudaErrorInvalidValue;
-  const int64_t units = sms / CTAS;
-  if (CTAS == 2 && g.parts == 1) halve(&w.p[0], w.p[0].items, units);
-  w.rem = w.extra = 0;
-  return launch_work<CTAS, BN, VEC, F32>(w, std::min<int64_t>(w.p[0].items, units), st);
-}
-
-template <int CTAS, int BN>
-cudaError_t launch_tile(const LinearGemm& g, int sms, cudaStream_t st) {
-  if (g.N % 8 == 0 && g.ldy % 8 == 0)
-    return g.out_f32 ? launch_tile_as<CTAS, BN, true, true>(g, sms, st) : launch_tile_as<CTAS, BN, true, false>(g, sms, st);
-  return g.out_f32 ? launch_tile_as<CTAS, BN, false, true>(g, sms, st) : launch_tile_as<CTAS, BN, false, false>(g, sms, st);
-}
-
 // Two products in one launch of CTA pairs, the longer k axis first (Walk).
 cudaError_t launch_two(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st) {
   const LinearGemm &l = g0.K >= g1.K ? g0 : g1, &s = g0.K >= g1.K ? g1 : g0;
-  TcWork<2> w;
-  if (!fill<2, 256, true, false>(&w, 0, l) || !fill<2, 256, true, false>(&w, 1, s)) return cudaErrorInvalidValue;
+  TcWork<2, kEpiLinear> w;
+  if (!fill<2, 256, true, false, 2, kEpiLinear>(&w, 0, l) || !fill<2, 256, true, false, 2, kEpiLinear>(&w, 1, s)) return cudaErrorInvalidValue;
   const int64_t units = sms / 2;
   w.rem = (int)(w.p[0].items % units);
   // a unit without a tile of the last round has time for `fit` tiles of the second product
   const int64_t fit = (2 * (int64_t)w.p[0].kblocks + w.p[1].kblocks) / (2 * (int64_t)w.p[1].kblocks);
   w.extra = w.rem ? (int)std::min<int64_t>((units - w.rem) * fit, w.p[1].items) : 0;
   halve(&w.p[1], w.p[1].items - w.extra, units);
-  return launch_work<2, 256, true, false>(w, units, st);
-}
-
-template <int NB>
-cudaError_t launch_split_nb(const LinearGemm& g, int S, cudaStream_t st) {
-  if (g.a_mn && NB < 64) return cudaErrorInvalidValue;
-  const bool vec = g.N % 8 == 0 && g.ldy % 8 == 0;
-  switch (S) {
-    case 1: return vec ? launch_split_as<NB, 1, true>(g, st) : launch_split_as<NB, 1, false>(g, st);
-    case 2: return vec ? launch_split_as<NB, 2, true>(g, st) : launch_split_as<NB, 2, false>(g, st);
-    case 4: return vec ? launch_split_as<NB, 4, true>(g, st) : launch_split_as<NB, 4, false>(g, st);
-    default: return vec ? launch_split_as<NB, 8, true>(g, st) : launch_split_as<NB, 8, false>(g, st);
-  }
+  return launch_work<2, 256, true, false, 2, kEpiLinear>(w, units, st);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) {
-  const LinearChoice c = choose_linear(g.M, g.N, g.K, g.a_mn, sms);
-  if (c.nb == 16) return launch_split_nb<16>(g, c.S, st);
-  if (c.nb == 32) return launch_split_nb<32>(g, c.S, st);
-  if (c.nb == 64) return launch_split_nb<64>(g, c.S, st);
-  return c.S == 2 ? launch_tile<2, 256>(g, sms, st) : launch_tile<1, 128>(g, sms, st);
-}
-
-cudaError_t launch_linear_parts(const LinearGemm& g, int sms, cudaStream_t st) { return launch_tile<2, 256>(g, sms, st); }
+cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st) { return launch_out<kEpiLinear>(g, sms, st); }
 
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches) {
   const LinearChoice c0 = choose_linear(g0.M, g0.N, g0.K, g0.a_mn, sms);
@@ -74,8 +36,7 @@ cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sm
     return (double)((g.M + 255) / 256) * ((g.N + 255) / 256) * ((g.K + kBK - 1) / kBK);
   };
   const double walk = (kblocks(g0) + kblocks(g1)) / (sms / 2);
-  const bool rows16 = g0.N % 8 == 0 && g1.N % 8 == 0 && g0.ldy % 8 == 0 && g1.ldy % 8 == 0;
-  if (pair(c0) && pair(c1) && rows16 && !g0.out_f32 && !g1.out_f32 && walk <= 128.0) {
+  if (pair(c0) && pair(c1) && g0.N % 8 == 0 && g1.N % 8 == 0 && walk <= 128.0) {
     *launches += 1;
     return launch_two(g0, g1, sms, st);
   }

@@ -30,9 +30,11 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "act.cuh"
 #include "common.cuh"
+#include "linear_choice.h"
 #include "linear_tc.h"
 
 namespace moe {
@@ -116,23 +118,32 @@ struct XentRow {
   }
 };
 
-// What the epilogue makes of a product: the linear operator's outputs, the statistics of a softmax over its columns, or
-// that softmax's gradient. Either runs beside the next tile's products without holding them up (1024 x 1024 x 51200
-// 78 us, 76 with the accumulators left unread).
-enum { kEpiLinear = 0, kEpiStats = 1, kEpiGrad = 2 };
+// What the epilogue makes of a product: the linear operator's outputs, the statistics of a softmax over its columns, that
+// softmax's gradient, or one of the products of that gradient (rows of ldy, add, div, parts). The second and third run
+// beside the next tile's products without holding them up (1024 x 1024 x 51200 78 us, 76 with the accumulators left
+// unread). The last is a form of its own: to look for what it asks for, and to receive it, costs the linear operator's
+// short calls up to 6% (350 x 384 x 320 with gelu 5.14 us for 4.81, backward of 19 x 192 x 384 12.13 for 11.95).
+enum { kEpiLinear = 0, kEpiStats = 1, kEpiGrad = 2, kEpiProduct = 3 };
 
+struct NoXent {};
+template <int EPI>
+using GemmOf = std::conditional_t<EPI == kEpiLinear, LinearGemm, XentGemm>;
+template <int EPI>
+using XentOf = std::conditional_t<EPI == kEpiStats || EPI == kEpiGrad, XentEpi, NoXent>;
+
+template <int EPI>
 struct TcArgs {
-  LinearGemm g;
-  XentEpi x;
+  GemmOf<EPI> g;
+  XentOf<EPI> x;
   int kblocks, mt, nt;
   int items, whole;  // work items; the first `whole` are tiles, the others halves (BN / 2 columns) of one
 };
 
 // What a launch of k_linear_tc works on: one product or two.
-template <int N>
+template <int N, int EPI>
 struct TcWork {
   CUtensorMap A[N], B[N], Y[N];
-  TcArgs p[N];
+  TcArgs<EPI> p[N];
   int rem, extra;  // N = 2: see Walk
 };
 
@@ -140,12 +151,12 @@ struct TcWork {
 // more k-blocks first; where its last round is not full, the units from rem on take the first `extra`
 // items of the second product meanwhile; the others of it are dealt out to all units. One launch in
 // place of two saves a start, an end and a launch gap (9 us), and one of the two ragged last rounds.
-template <int N>
+template <int N, int EPI>
 struct Walk {
-  const TcWork<N>& w;
+  const TcWork<N, EPI>& w;
   const int unit, units;
   int phase = 0, t, step, end;
-  __device__ __forceinline__ Walk(const TcWork<N>& w_, int unit_, int units_) : w(w_), unit(unit_), units(units_) {
+  __device__ __forceinline__ Walk(const TcWork<N, EPI>& w_, int unit_, int units_) : w(w_), unit(unit_), units(units_) {
     t = unit;
     step = units;
     end = w.p[0].items;
@@ -221,8 +232,8 @@ __device__ __forceinline__ void rows_out(__nv_bfloat16* dst, int64_t ld, uint32_
 struct Item {
   int m, n0, half;  // row block, first column, whether BN / 2 columns
 };
-template <int BN>
-__device__ __forceinline__ Item item_at(const TcArgs& a, int t) {
+template <int BN, int EPI>
+__device__ __forceinline__ Item item_at(const TcArgs<EPI>& a, int t) {
   constexpr int G = 8;
   Item it;
   it.half = t >= a.whole;
@@ -240,12 +251,22 @@ __device__ __forceinline__ Item item_at(const TcArgs& a, int t) {
 struct Span {
   int k0, k1, part;
 };
-template <bool PARTS>
-__device__ __forceinline__ Span span_at(const TcArgs& a, int* t) {
-  if (!PARTS || a.g.parts == 1) return {0, a.kblocks, 0};
-  const int tiles = a.mt * a.nt, part = *t / tiles;
-  *t -= part * tiles;
-  return {(int)((int64_t)a.kblocks * part / a.g.parts), (int)((int64_t)a.kblocks * (part + 1) / a.g.parts), part};
+template <bool F32, int EPI>
+__device__ __forceinline__ Span span_at(const TcArgs<EPI>& a, int* t) {
+  if constexpr (F32 && EPI == kEpiProduct) {
+    if (a.g.parts > 1) {
+      const int tiles = a.mt * a.nt, part = *t / tiles;
+      *t -= part * tiles;
+      return {(int)((int64_t)a.kblocks * part / a.g.parts), (int)((int64_t)a.kblocks * (part + 1) / a.g.parts), part};
+    }
+  }
+  return {0, a.kblocks, 0};
+}
+// The row stride of a product's output.
+template <int EPI>
+__device__ __forceinline__ int64_t row_of_y(const GemmOf<EPI>& g) {
+  if constexpr (EPI == kEpiLinear) return g.N;
+  else return g.ldy;
 }
 
 // Sixteen z of a row as bf16: one 32-byte store where `wide`, else a 16-byte store for each half that exists.
@@ -267,7 +288,7 @@ __device__ __forceinline__ void store_z16(__nv_bfloat16* p, const float* z, int 
 // the activation is evaluated in full precision, since no rounding to bf16 covers the fast forms' errors.
 template <int CTAS, int BN, bool VEC, bool F32, int NP, int EPI = kEpiLinear>
 __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
-    k_linear_tc(const __grid_constant__ TcWork<NP> work) {
+    k_linear_tc(const __grid_constant__ TcWork<NP, EPI> work) {
   using C = Cfg<CTAS, BN>;
   constexpr bool PAIR = CTAS == 2;
   extern __shared__ uint8_t smem_raw[];
@@ -311,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
   const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
-  Walk<NP> walk(work, unit, units);
+  Walk<NP, EPI> walk(work, unit, units);
   int prod, t;
 
   if (warp == 0 && lane == 0) {
@@ -327,8 +348,8 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     for (int s = 0; s < C::STAGES; ++s) issued[s] = -1;
     bool ok = true;
     while (ok && walk.next(&prod, &t)) {
-      const TcArgs& args = work.p[prod];
-      const LinearGemm& g = args.g;
+      const TcArgs<EPI>& args = work.p[prod];
+      const GemmOf<EPI>& g = args.g;
       const CUtensorMap *tmA = &work.A[prod], *tmB = &work.B[prod];
       const Span k = span_at<F32>(args, &t);
       const Item it = item_at<BN>(args, t);
@@ -385,8 +406,8 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     while (ok && walk.next(&prod, &t)) {
-      const TcArgs& args = work.p[prod];
-      const LinearGemm& g = args.g;
+      const TcArgs<EPI>& args = work.p[prod];
+      const GemmOf<EPI>& g = args.g;
       const uint64_t ad0 = g.a_mn ? sdesc_sw128(sa0, kChunkBytes, 1024) : sdesc_sw128(sa0, 16, 1024);
       const uint64_t bd0 =
           g.b_mn ? sdesc_sw128(sa0 + C::A_BYTES, kChunkBytes, 1024) : sdesc_sw128(sa0 + C::A_BYTES, 16, 1024);
@@ -435,10 +456,11 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
     int acc_i = 0;
     int sc = 0;  // chunks stored so far
     while (walk.next(&prod, &t)) {
-      const TcArgs& args = work.p[prod];
-      const LinearGemm& g = args.g;
+      const TcArgs<EPI>& args = work.p[prod];
+      const GemmOf<EPI>& g = args.g;
       const __nv_bfloat16* bias = reinterpret_cast<const __nv_bfloat16*>(g.bias);
       const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(g.residual);
+      const int64_t ldy = row_of_y<EPI>(g);
       const int part = span_at<F32>(args, &t).part;
       const Item it = item_at<BN>(args, t);
       const int cw = BN / 64 / (it.half ? 4 : 2);  // 64-column chunks of this warp
@@ -476,7 +498,9 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
       if constexpr (EPI == kEpiGrad) row.load(args.x, row0 + lane, lane < rows);
       float run_m = -kHuge, run_s = 0.0f;
       int hit = -1;  // statistics: the target's column of the tile
-      if (EPI == kEpiStats && lane < rows) hit = args.x.target[row0 + lane] - args.x.v0 - it.n0;
+      if constexpr (EPI == kEpiStats) {
+        if (lane < rows) hit = args.x.target[row0 + lane] - args.x.v0 - it.n0;
+      }
       const int acc = acc_i & 1;
       if (!mbar_wait_bounded(&tfull[acc], (uint32_t)((acc_i >> 1) & 1), abort_flag)) break;
       tc_fence_after();
@@ -521,10 +545,12 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         float z[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) z[i] = __uint_as_float(v[i >> 5][i & 31]);
-        if (EPI == kEpiLinear && g.div) {
-          const float f = reciprocal_or_zero(g.div);
+        if constexpr (EPI == kEpiProduct) {
+          if (g.div) {
+            const float f = reciprocal_or_zero(g.div);
 #pragma unroll
-          for (int i = 0; i < 64; ++i) z[i] *= f;
+            for (int i = 0; i < 64; ++i) z[i] *= f;
+          }
         }
         if (bias) {
 #pragma unroll
@@ -551,7 +577,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
           }
         }
         if constexpr (EPI == kEpiGrad) row.grad<64>(z, args.x.v0 + n0);
-        else act_fwd<!F32, 64>(g.act, z, z);  // 64 independent chains: two warps a scheduler have little else to hide latency
+        else if constexpr (EPI == kEpiLinear) act_fwd<!F32, 64>(g.act, z, z);  // 64 independent chains: two warps a scheduler have little else to hide latency
         if (res) {
           if constexpr (VEC) cp_async_wait<0>();
           __syncwarp();
@@ -567,11 +593,13 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) st_shared_v4(ty + piece(lane, j), f_to_bf16x8(z + 8 * j));
         } else if (lane < rows) {
-          float* o = reinterpret_cast<float*>(g.y) + (part * (int64_t)g.M + row0 + lane) * g.ldy + n0;
-          if (g.add) {
+          float* o = reinterpret_cast<float*>(g.y) + (part * (int64_t)g.M + row0 + lane) * ldy + n0;
+          if constexpr (EPI == kEpiProduct) {
+            if (g.add) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i < cols) z[i] += o[i];
+              for (int i = 0; i < 64; ++i)
+                if (i < cols) z[i] += o[i];
+            }
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -588,7 +616,7 @@ __global__ void __launch_bounds__(Cfg<CTAS, BN>::THREADS, 1)
         if constexpr (!VEC) {
           __syncwarp();
           const int64_t o = row0 * g.N + n0;
-          if constexpr (!F32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + row0 * g.ldy + n0, g.ldy, ty, rows, cols, lane);
+          if constexpr (!F32) rows_out(reinterpret_cast<__nv_bfloat16*>(g.y) + row0 * ldy + n0, ldy, ty, rows, cols, lane);
           if (g.pre) rows_out(reinterpret_cast<__nv_bfloat16*>(g.pre) + o, g.N, tile, rows, cols, lane);
           __syncwarp();
           if (c + 1 < c0 + cw) ready(c + 1);
@@ -645,8 +673,8 @@ struct SplitCfg {
 
 // A token's statistics or gradient from four neighbouring features a lane (a whole warp).
 template <int EPI>
-__device__ __forceinline__ void emit_xent(const TcArgs& a, int64_t t, int f0, int n0, float (&z)[4]) {
-  const LinearGemm& g = a.g;
+__device__ __forceinline__ void emit_xent(const TcArgs<EPI>& a, int64_t t, int f0, int n0, float (&z)[4]) {
+  const GemmOf<EPI>& g = a.g;
   if constexpr (EPI == kEpiStats) {
     float m = -kHuge, s = 0.0f;
 #pragma unroll
@@ -675,18 +703,25 @@ __device__ __forceinline__ void emit_xent(const TcArgs& a, int64_t t, int f0, in
 
 // z -> y and pre for four neighbouring features of one token (n0 a multiple of 4). VEC: the rows of
 // the outputs are multiples of 16 bytes, so the four values are one access.
-template <bool VEC>
-__device__ __forceinline__ void emit4(const LinearGemm& g, int64_t t, int n0, float (&z)[4], const float (&res)[4]) {
-  const int64_t o = t * g.N + n0, oy = t * g.ldy + n0;
+template <bool VEC, int EPI>
+__device__ __forceinline__ void emit4(const GemmOf<EPI>& g, int64_t t, int n0, float (&z)[4], const float (&res)[4]) {
+  const int64_t o = t * g.N + n0, oy = t * row_of_y<EPI>(g) + n0;
   float y[4];
-  if (g.out_f32) act_fwd<false, 4>(g.act, z, y);  // no rounding to bf16 covers the fast forms' errors
-  else act_fwd<true, 4>(g.act, z, y);
+  if constexpr (EPI == kEpiLinear) {
+    if (g.out_f32) act_fwd<false, 4>(g.act, z, y);  // no rounding to bf16 covers the fast forms' errors
+    else act_fwd<true, 4>(g.act, z, y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = z[i];
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] += res[i];
-  if (g.add) {
+  if constexpr (EPI == kEpiProduct) {
+    if (g.add) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + i < g.N) y[i] += reinterpret_cast<const float*>(g.y)[oy + i];
+      for (int i = 0; i < 4; ++i)
+        if (n0 + i < g.N) y[i] += reinterpret_cast<const float*>(g.y)[oy + i];
+    }
   }
   __nv_bfloat16* pre = reinterpret_cast<__nv_bfloat16*>(g.pre) + o;
   if constexpr (VEC) {
@@ -728,11 +763,11 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, int left, float (&
 // Tokens [a, e) of the tile from the parts' sums in the CTAs of the cluster: a warp a token, four
 // features a lane, two tokens' loads in flight. The parts are added in rank order.
 template <bool VEC, int S, int EPI>
-__device__ __forceinline__ void finish_tokens(const TcArgs& args, const float* sums, int t0, int f0, int a, int e) {
-  const LinearGemm& g = args.g;
+__device__ __forceinline__ void finish_tokens(const TcArgs<EPI>& args, const float* sums, int t0, int f0, int a, int e) {
+  const GemmOf<EPI>& g = args.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int n0 = f0 + 4 * lane;
-  if (EPI == kEpiLinear && n0 >= g.N) return;  // else the warp works together
+  if ((EPI == kEpiLinear || EPI == kEpiProduct) && n0 >= g.N) return;  // else the warp works together
   const uint32_t base = smem_u32(sums) + lane * 16;
   uint32_t peer[S];
 #pragma unroll
@@ -767,14 +802,16 @@ __device__ __forceinline__ void finish_tokens(const TcArgs& args, const float* s
           z[2] += v[u][r].z;
           z[3] += v[u][r].w;
         }
-        if (EPI == kEpiLinear && g.div) {
-          const float f = reciprocal_or_zero(g.div);
+        if constexpr (EPI == kEpiProduct) {
+          if (g.div) {
+            const float f = reciprocal_or_zero(g.div);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] *= f;
+            for (int i = 0; i < 4; ++i) z[i] *= f;
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] += b[i];
-        if constexpr (EPI == kEpiLinear) emit4<VEC>(g, t0 + tt, n0, z, res[u]);
+        if constexpr (EPI == kEpiLinear || EPI == kEpiProduct) emit4<VEC, EPI>(g, t0 + tt, n0, z, res[u]);
         else emit_xent<EPI>(args, t0 + tt, f0, n0, z);
       }
     }
@@ -785,7 +822,7 @@ __device__ __forceinline__ void finish_tokens(const TcArgs& args, const float* s
 template <int NB, int S, bool VEC, int EPI = kEpiLinear>
 __global__ void __launch_bounds__(SplitCfg<NB>::THREADS)
     k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const TcArgs args) {
+                   const TcArgs<EPI> args) {
   using C = SplitCfg<NB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -794,7 +831,7 @@ __global__ void __launch_bounds__(SplitCfg<NB>::THREADS)
   uint64_t* done = empty + C::STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const LinearGemm& g = args.g;
+  const GemmOf<EPI>& g = args.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = (int)blockIdx.x % S, tile = (int)blockIdx.x / S;
   const int f0 = (tile % args.nt) * 128, t0 = (tile / args.nt) * NB;
@@ -956,36 +993,42 @@ bool make_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
 }
 
 // product g as number i of w: its maps and its tiles
-template <int CTAS, int BN, bool VEC, bool F32, int N, int EPI = kEpiLinear>
-bool fill(TcWork<N>* w, int i, const LinearGemm& g) {
+template <int CTAS, int BN, bool VEC, bool F32, int N, int EPI>
+bool fill(TcWork<N, EPI>* w, int i, const GemmOf<EPI>& g) {
   using C = Cfg<CTAS, BN>;
   bool ok = g.a_mn ? make_map(&w->A[i], g.A, g.K, g.M, g.lda, kBK) : make_map(&w->A[i], g.A, g.M, g.K, g.lda, 128);
   ok = ok && (g.b_mn ? make_map(&w->B[i], g.B, g.K, g.N, g.ldb, kBK)
                      : make_map(&w->B[i], g.B, g.N, g.K, g.ldb, C::BCOLS / 2));
   w->Y[i] = w->A[i];  // where unused
-  if (VEC && !F32 && EPI != kEpiStats) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, g.ldy ? g.ldy : g.N, 32);
-  TcArgs& a = w->p[i];
+  int64_t ldy = g.N, parts = 1;
+  TcArgs<EPI>& a = w->p[i];
   a.g = g;
-  if (!g.ldy) a.g.ldy = g.N;
+  if constexpr (EPI != kEpiLinear) {
+    if (g.ldy) ldy = g.ldy;
+    a.g.ldy = ldy;
+    parts = g.parts;
+  }
+  if (VEC && !F32 && EPI != kEpiStats) ok = ok && make_map(&w->Y[i], g.y, g.M, g.N, ldy, 32);
   a.kblocks = (g.K + kBK - 1) / kBK;
   a.mt = (g.M + C::TILE_M - 1) / C::TILE_M;
   a.nt = (g.N + BN - 1) / BN;
   const int64_t total = (int64_t)a.mt * a.nt;
-  if (!ok || total * g.parts >= (1ll << 30)) return false;
-  a.items = a.whole = (int)total * g.parts;
+  if (!ok || total * parts >= (1ll << 30)) return false;
+  a.items = a.whole = (int)(total * parts);
   return true;
 }
 
 // the tiles of a last round of `round` tiles over `units` as halves, where that leaves none waiting
-void halve(TcArgs* a, int64_t round, int64_t units) {
+template <int EPI>
+void halve(TcArgs<EPI>* a, int64_t round, int64_t units) {
   const int64_t last = round % units;
   if (2 * last > units) return;
   a->whole -= (int)last;
   a->items += (int)last;
 }
 
-template <int CTAS, int BN, bool VEC, bool F32, int N, int EPI = kEpiLinear>
-cudaError_t launch_work(const TcWork<N>& w, int64_t units, cudaStream_t st) {
+template <int CTAS, int BN, bool VEC, bool F32, int N, int EPI>
+cudaError_t launch_work(const TcWork<N, EPI>& w, int64_t units, cudaStream_t st) {
   using C = Cfg<CTAS, BN>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
   static_assert(CTAS == 1 || BN == 256, "the epilogue's warps need four chunks to share a half tile");
@@ -996,8 +1039,8 @@ cudaError_t launch_work(const TcWork<N>& w, int64_t units, cudaStream_t st) {
   return cudaLaunchKernelEx(&l.cfg, kern, w);
 }
 
-template <int NB, int S, bool VEC, int EPI = kEpiLinear>
-cudaError_t launch_split_as(const LinearGemm& g, cudaStream_t st, const XentEpi& x = {}) {
+template <int NB, int S, bool VEC, int EPI>
+cudaError_t launch_split_as(const GemmOf<EPI>& g, cudaStream_t st, const XentOf<EPI>& x = {}) {
   using C = SplitCfg<NB>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
   auto kern = k_linear_split<NB, S, VEC, EPI>;
@@ -1007,10 +1050,12 @@ cudaError_t launch_split_as(const LinearGemm& g, cudaStream_t st, const XentEpi&
   bool ok = g.b_mn ? make_map(&mW, g.B, g.K, g.N, g.ldb, kBK) : make_map(&mW, g.B, g.N, g.K, g.ldb, 128);
   ok = ok && (g.a_mn ? make_map(&mX, g.A, g.K, g.M, g.lda, kBK) : make_map(&mX, g.A, g.M, g.K, g.lda, NB));
   if (!ok) return cudaErrorInvalidValue;
-  TcArgs a;
+  TcArgs<EPI> a;
   a.g = g;
   a.x = x;
-  if (!g.ldy) a.g.ldy = g.N;
+  if constexpr (EPI != kEpiLinear) {
+    if (!g.ldy) a.g.ldy = g.N;
+  }
   a.kblocks = (g.K + kBK - 1) / kBK;
   a.mt = (g.M + NB - 1) / NB;
   a.nt = (g.N + 127) / 128;
@@ -1018,6 +1063,54 @@ cudaError_t launch_split_as(const LinearGemm& g, cudaStream_t st, const XentEpi&
   if (total >= (1ll << 31)) return cudaErrorInvalidValue;
   LaunchCfg l(dim3((unsigned)total), C::THREADS, C::SMEM, st, S);
   return cudaLaunchKernelEx(&l.cfg, kern, mW, mX, a);
+}
+
+// A product with the linear operator's outputs (kEpiLinear) or as one of the cross entropy's (kEpiProduct).
+template <int CTAS, int BN, bool VEC, bool F32, int EPI>
+cudaError_t launch_tile_as(const GemmOf<EPI>& g, int sms, cudaStream_t st) {
+  TcWork<1, EPI> w;
+  if (!fill<CTAS, BN, VEC, F32, 1, EPI>(&w, 0, g)) return cudaErrorInvalidValue;
+  const int64_t units = sms / CTAS;
+  if (CTAS == 2 && w.p[0].items == w.p[0].mt * w.p[0].nt) halve(&w.p[0], w.p[0].items, units);
+  w.rem = w.extra = 0;
+  return launch_work<CTAS, BN, VEC, F32, 1, EPI>(w, std::min<int64_t>(w.p[0].items, units), st);
+}
+
+// Whether y's rows are multiples of 16 bytes.
+template <int EPI>
+bool rows16(const GemmOf<EPI>& g) {
+  if constexpr (EPI == kEpiLinear) return g.N % 8 == 0;
+  else return g.N % 8 == 0 && g.ldy % 8 == 0;
+}
+
+template <int CTAS, int BN, int EPI>
+cudaError_t launch_tile_out(const GemmOf<EPI>& g, int sms, cudaStream_t st) {
+  if (rows16<EPI>(g))
+    return g.out_f32 ? launch_tile_as<CTAS, BN, true, true, EPI>(g, sms, st)
+                     : launch_tile_as<CTAS, BN, true, false, EPI>(g, sms, st);
+  return g.out_f32 ? launch_tile_as<CTAS, BN, false, true, EPI>(g, sms, st)
+                   : launch_tile_as<CTAS, BN, false, false, EPI>(g, sms, st);
+}
+
+template <int NB, int EPI>
+cudaError_t launch_split_out(const GemmOf<EPI>& g, int S, cudaStream_t st) {
+  if (g.a_mn && NB < 64) return cudaErrorInvalidValue;
+  const bool vec = rows16<EPI>(g);
+  switch (S) {
+    case 1: return vec ? launch_split_as<NB, 1, true, EPI>(g, st) : launch_split_as<NB, 1, false, EPI>(g, st);
+    case 2: return vec ? launch_split_as<NB, 2, true, EPI>(g, st) : launch_split_as<NB, 2, false, EPI>(g, st);
+    case 4: return vec ? launch_split_as<NB, 4, true, EPI>(g, st) : launch_split_as<NB, 4, false, EPI>(g, st);
+    default: return vec ? launch_split_as<NB, 8, true, EPI>(g, st) : launch_split_as<NB, 8, false, EPI>(g, st);
+  }
+}
+
+template <int EPI>
+cudaError_t launch_out(const GemmOf<EPI>& g, int sms, cudaStream_t st) {
+  const LinearChoice c = choose_linear(g.M, g.N, g.K, g.a_mn, sms);
+  if (c.nb == 16) return launch_split_out<16, EPI>(g, c.S, st);
+  if (c.nb == 32) return launch_split_out<32, EPI>(g, c.S, st);
+  if (c.nb == 64) return launch_split_out<64, EPI>(g, c.S, st);
+  return c.S == 2 ? launch_tile_out<2, 256, EPI>(g, sms, st) : launch_tile_out<1, 128, EPI>(g, sms, st);
 }
 
 }  // namespace

@@ -20,10 +20,15 @@ struct LinearGemm {
   void* pre;             // [M, N] bf16 or null
   int act, out_f32;
   int* status;           // receives MOE_ERR_TIMEOUT when a wait runs out
+};
+
+// The same for the cross entropy, which asks for more; a type of its own, so that the linear operator's kernels neither
+// receive nor test it.
+struct XentGemm : LinearGemm {
   int64_t ldy = 0;       // row stride of y, 0: N
   int add = 0;           // with out_f32: added to what y holds
   const float* div = nullptr;  // the product is divided by *div (0: becomes 0)
-  int parts = 1;         // with out_f32, launch_linear_parts: K in so many parts, whose sums go to y + part * M * ldy
+  int parts = 1;         // with out_f32, launch_xent_parts: K in so many parts, whose sums go to y + part * M * ldy
 };
 
 // What the epilogues of the cross entropy read and write beside a product l[M, N] of logits, columns v0 .. v0 + N - 1 of
@@ -38,13 +43,15 @@ struct XentEpi {
   int v0, V;
 };
 // The rows' statistics, one slot for *width columns; nothing else is written.
-cudaError_t launch_xent_stats(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width);
+cudaError_t launch_xent_stats(const XentGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width);
 // y[M, N] (bf16, rows of a multiple of 8) = gradient of the loss to the logits.
-cudaError_t launch_xent_grad(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st);
+cudaError_t launch_xent_grad(const XentGemm& g, const XentEpi& x, int sms, cudaStream_t st);
+// A product of that gradient, without bias, residual, pre and activation.
+cudaError_t launch_xent_product(const XentGemm& g, int sms, cudaStream_t st);
+// One of few tiles and a long K on CTA pairs, K in g.parts parts (out_f32).
+cudaError_t launch_xent_parts(const XentGemm& g, int sms, cudaStream_t st);
 
 cudaError_t launch_linear_tc(const LinearGemm& g, int sms, cudaStream_t st);
-// A product of few tiles and a long K on CTA pairs, K in g.parts parts (out_f32).
-cudaError_t launch_linear_parts(const LinearGemm& g, int sms, cudaStream_t st);
 // Two independent products (neither reads what the other writes), in one launch where both are large.
 cudaError_t launch_linear_tc2(const LinearGemm& g0, const LinearGemm& g1, int sms, cudaStream_t st, int* launches);
 

@@ -353,7 +353,7 @@ int64_t piece_cols(const moe_xent_dims& d) {
   return std::min(want, up64(d.V));
 }
 // Parts of K of a piece's dx product in bf16: its K is a piece of the vocabulary and its tiles may be few. 0: as
-// launch_linear_tc does it, which is as good or better; else pairs of CTAs, each with a tile's part, whose fp32 sums are
+// launch_xent_product does it, which is as good or better; else pairs of CTAs, each with a tile's part, whose fp32 sums are
 // added afterwards (777 x 1000 over 50001 columns: 16 tiles for 76 pairs, 200 -> 93 us in 4 parts). Estimates as in
 // linear_choice.h; a part costs its sums' way to memory and back.
 int dx_parts(const moe_xent_dims& d) {
@@ -448,9 +448,9 @@ struct Xent {
     return static_cast<const char*>(w) + (d.tied ? v0 * ldw : v0) * (d.dtype == MOE_BF16 ? 2 : 4);
   }
   // the product of columns v0 .. v0 + cols - 1 of the logits
-  LinearGemm gemm(int64_t v0, int cols, void* out) const {
-    return {(int)d.M, cols, (int)d.H, x, w_at(v0), ldx, ldw, 0, !d.tied, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, 0,
-            reinterpret_cast<int*>(ws), P};
+  XentGemm gemm(int64_t v0, int cols, void* out) const {
+    return {{(int)d.M, cols, (int)d.H, x, w_at(v0), ldx, ldw, 0, !d.tied, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, 0,
+             reinterpret_cast<int*>(ws)}, P};
   }
   cudaError_t logits_f32(int64_t v0, int cols) {
     const int M = (int)d.M, H = (int)d.H;
@@ -469,23 +469,22 @@ struct Xent {
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(dw) + (dw ? (d.tied ? v0 * d.H : v0) : 0);
       const int parts = dx_parts(d);
       const bool direct = P >= d.V && !parts;
-      LinearGemm gx = {M, H, cols, dl, w_at(v0), P, ldw, 0, d.tied, nullptr, nullptr, direct ? dx : ws + L.dx, nullptr,
-                       MOE_ACT_NONE, !direct, status, H, v0 > 0};
+      XentGemm gx = {{M, H, cols, dl, w_at(v0), P, ldw, 0, d.tied, nullptr, nullptr, direct ? dx : ws + L.dx, nullptr,
+                      MOE_ACT_NONE, !direct, status}, H, v0 > 0};
       if (direct) gx.div = div;
       if (parts) gx.parts = std::min(parts, (cols + 63) / 64);
-      LinearGemm gw = d.tied ? LinearGemm{cols, H, M, dl, x, P, ldx, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE,
-                                          0, status}
-                             : LinearGemm{H, cols, M, x, dl, ldx, P, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE,
-                                          0, status, d.V};
+      XentGemm gw = d.tied ? XentGemm{{cols, H, M, dl, x, P, ldx, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, 0, status}}
+                           : XentGemm{{H, cols, M, x, dl, ldx, P, 1, 1, nullptr, nullptr, out, nullptr, MOE_ACT_NONE, 0, status},
+                                      d.V};
       gw.div = div;
       cudaError_t e = cudaSuccess;
       if (dx) {
         *launches += 1;
-        e = parts ? launch_linear_parts(gx, sms, st) : launch_linear_tc(gx, sms, st);
+        e = parts ? launch_xent_parts(gx, sms, st) : launch_xent_product(gx, sms, st);
       }
       if (dw && e == cudaSuccess) {
         *launches += 1;
-        e = launch_linear_tc(gw, sms, st);
+        e = launch_xent_product(gw, sms, st);
       }
       return e;
     }

@@ -1,14 +1,13 @@
 // xent_tc.cu -- the cross entropy's launches of the tensor-core products: logits that leave the epilogue as a row's
-// statistics, or as its gradient.
-#include "linear_choice.h"
+// statistics, or as its gradient, and the products of that gradient.
 #include "linear_tc.cuh"
 
 namespace moe {
 namespace {
 
 template <int CTAS, int BN, int EPI>
-cudaError_t launch_tile(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st) {
-  TcWork<1> w;
+cudaError_t launch_tile(const XentGemm& g, const XentEpi& x, int sms, cudaStream_t st) {
+  TcWork<1, EPI> w;
   if (!fill<CTAS, BN, true, false, 1, EPI>(&w, 0, g)) return cudaErrorInvalidValue;
   w.p[0].x = x;
   const int64_t units = sms / CTAS;
@@ -18,7 +17,7 @@ cudaError_t launch_tile(const LinearGemm& g, const XentEpi& x, int sms, cudaStre
 }
 
 template <int NB, int EPI>
-cudaError_t launch_split(const LinearGemm& g, const XentEpi& x, int S, cudaStream_t st) {
+cudaError_t launch_split(const XentGemm& g, const XentEpi& x, int S, cudaStream_t st) {
   switch (S) {
     case 1: return launch_split_as<NB, 1, true, EPI>(g, st, x);
     case 2: return launch_split_as<NB, 2, true, EPI>(g, st, x);
@@ -28,7 +27,7 @@ cudaError_t launch_split(const LinearGemm& g, const XentEpi& x, int S, cudaStrea
 }
 
 template <int EPI>
-cudaError_t launch(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width) {
+cudaError_t launch(const XentGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width) {
   const LinearChoice c = choose_linear(g.M, g.N, g.K, g.a_mn, sms);
   *width = c.nb || c.S == 2 ? 128 : 64;
   if (c.nb == 16) return launch_split<16, EPI>(g, x, c.S, st);
@@ -39,13 +38,19 @@ cudaError_t launch(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_xent_stats(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width) {
+cudaError_t launch_xent_stats(const XentGemm& g, const XentEpi& x, int sms, cudaStream_t st, int* width) {
   return launch<kEpiStats>(g, x, sms, st, width);
 }
 
-cudaError_t launch_xent_grad(const LinearGemm& g, const XentEpi& x, int sms, cudaStream_t st) {
+cudaError_t launch_xent_grad(const XentGemm& g, const XentEpi& x, int sms, cudaStream_t st) {
   int width;
   return launch<kEpiGrad>(g, x, sms, st, &width);
+}
+
+cudaError_t launch_xent_product(const XentGemm& g, int sms, cudaStream_t st) { return launch_out<kEpiProduct>(g, sms, st); }
+
+cudaError_t launch_xent_parts(const XentGemm& g, int sms, cudaStream_t st) {
+  return launch_tile_out<2, 256, kEpiProduct>(g, sms, st);
 }
 
 }  // namespace moe
