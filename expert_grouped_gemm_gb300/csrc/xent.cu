@@ -191,8 +191,25 @@ __global__ void __launch_bounds__(256) k_xent_dots(const __nv_bfloat16* x, const
   if (lane == 0) dots[at] = dot;
 }
 
-// lse and loss of eight rows a block. Where the product's own logit of the target is given, the sum of exponentials is put
-// right by its difference to the fp32 one (BASE2). The blocks' totals are added in order by the last one.
+// lse and loss of a row from its sum s 2^m of powers of two, with the target's logit `at` in fp32 in place of the product's
+// own, `had`, in that sum:  loss = log(1 + e^y), y = log(e^L - 1) + had - at,  L = log(s 2^m) - had. The difference to had
+// is taken before the logarithm's rounding, so that a likely target's small loss keeps its digits; no exponential here can
+// overflow and no logarithm sees a negative number, whatever had and at are off (lse + log(1 + e^{at - lse} - e^{had - lse})
+// was NaN where a large had rounded lse away from itself).
+__device__ __forceinline__ void corrected(float m, float s, float had, float at, float* lse, float* loss) {
+  constexpr float kLn2 = 0.6931471805599453f;
+  float L = kLn2 * (log2f(s) + fmaf(-had, kLog2e, m));
+  if (L < 0.0f) L = 0.0f;                             // had is in the sum; NaN stays
+  const float others = logf(-expm1f(-L));             // log of the others' share
+  const float y = (L + others) + (had == at ? 0.0f : had - at);  // of two infinities as well
+  const float t = log1pf(expf(-fabsf(y)));
+  *loss = y > 0.0f ? y + t : t;
+  // the larger of the target's and the others' parts, and what the other adds
+  *lse = y > 0.0f ? ((m + log2f(s)) * kLn2 + others) + t : at + t;
+}
+
+// lse and loss of eight rows a block; with BASE2 the targets' logits are exchanged (corrected). The blocks' totals are
+// added in order by the last one.
 template <bool BASE2>
 __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
@@ -223,8 +240,9 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a)
       float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
       if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
       if (v >= 0 && v < a.V) {
-        if (BASE2) e += log1pf(expf(at - e) - expf(had - e));
-        sum = e - at + a.z * e * e;
+        sum = e - at;
+        if (BASE2) corrected(st.x, st.y, had, at, &e, &sum);
+        sum += a.z * e * e;
         n = 1.0f;
       }
       a.lse[t] = e;

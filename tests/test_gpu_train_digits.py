@@ -47,3 +47,25 @@ def test_adamw_small_decay(lr, wd, bits, master):
     # 2^20 roundings of at most half a step h either way: their mean passes 0.0053 h with a chance of
     # 2 e^{-2^20 0.0053^2 / 2} = 8e-7 (Hoeffding's bound). The smallest decay is a sixth of a step and more.
     assert abs(err.mean()) <= 0.5 * ulp.max() * 0.0053 + part.mean()
+
+
+# ---------------------------------------------------------------- cross entropy
+@pytest.mark.parametrize("M", [20, 300])
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e7, 1e9])
+def test_xent_large_logits_of_one_sign(M, size):
+    """Logits of -1e3 to -1e9, and targets that are the largest of their row: losses are finite and not below zero, and
+    within what the logits are off."""
+    H, V = 2048, 900
+    r = C.rand(M)
+    x, w = r(M, H).abs(), -(1 + 0.2 * r(V, H)).abs()
+    s = (size / (0.8 * H)) ** 0.5
+    x, w = (x * s).bfloat16(), (w * s).bfloat16()
+    for sign in (1, -1):
+        l = sign * (x.double() @ w.double().t())
+        c = dict(M=M, H=H, V=V, dtype="bf16", tied=True, z=0.0, x=x, w=sign * w, target=l.argmax(1).int(), dloss=r(M))
+        out = C.run_xent_fwd(c)
+        assert torch.isfinite(out[0]).all() and float(out[0].min()) >= 0.0
+        C.check_xent_fwd(c, out)
+        if size <= 1e7:  # where a float still has the logits' units
+            for t in C.run_xent_bwd(c, out[1], c["dloss"]):
+                assert torch.isfinite(t).all()
