@@ -88,18 +88,20 @@ __device__ __forceinline__ float reciprocal_or_zero(const float* p) {
   return v != 0.0f ? 1.0f / v : 0.0f;
 }
 
-// What a row's gradient dl = f e^{l - lse} - d onehot is made of; at: the target's column, or -1.
+// What a row's gradient dl = f e^{l - lse} - d onehot is made of; at: the target's column, or -1, and own its gradient:
+// a likely target's is a small difference, in which the logit has to be the one that lse was made of.
 struct XentRow {
-  float lse2, d, f;
+  float lse2, d, f, own;
   int at;
   __device__ __forceinline__ void load(const XentEpi& x, int64_t t, bool exists) {
-    d = f = lse2 = 0.0f;
+    d = f = lse2 = own = 0.0f;
     at = -1;
     if (!exists) return;
     const int v = x.target[t];
     if (v < 0 || v >= x.V) return;
     const float lse = x.lse[t];
     at = v;
+    own = x.own[t];
     d = x.dloss ? x.dloss[t] : 1.0f;
     lse2 = lse * kLog2e;
     f = d * (1.0f + 2.0f * x.z * lse);
@@ -113,7 +115,7 @@ struct XentRow {
     const int c = at - v;
     if (__any_sync(__activemask(), at >= 0 && c >= 0 && c < N)) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] -= i == c ? d : 0.0f;
+      for (int i = 0; i < N; ++i) z[i] = i == c ? own : z[i];
     }
   }
 };

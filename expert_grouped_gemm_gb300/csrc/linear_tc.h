@@ -39,6 +39,7 @@ struct XentEpi {
   const int* target;
   const float* lse;
   const float* dloss;   // null: gradient of the sum of the losses
+  const float* own;     // gradient: [M], that of each row's target
   float z;
   int v0, V;
 };

@@ -164,31 +164,29 @@ struct LossArgs {
 // The targets' logits of bf16 products in fp32, a warp 256 features of a row; a kernel of its own, so that the columns of w, a line for
 // every feature, are fetched by all SMs (8 rows of 2048 features: 20 us in one block of k_xent_loss, 3 us here).
 constexpr int kDotCols = 256;
+__device__ __forceinline__ float dot_part(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t swh, int h0, int H) {
+  const int lane = threadIdx.x & 31;
+  float a[kDotCols / 32], b[kDotCols / 32], dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kDotCols / 32; ++i) {
+    const int h = h0 + i * 32 + lane;
+    a[i] = h < H ? __bfloat162float(x[h]) : 0.0f;
+    b[i] = h < H ? __bfloat162float(w[h * swh]) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kDotCols / 32; ++i) dot = fmaf(a[i], b[i], dot);
+  return warp_sum(dot);
+}
 __global__ void __launch_bounds__(256) k_xent_dots(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t ldx, int64_t swh,
                                                    int64_t swv, const int* target, int M, int H, int V, int parts,
                                                    float* dots) {
   pdl_wait();  // the previous kernel has completed and its writes are visible
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
   const int64_t t = at / parts;
   if (t >= M) return;
   const int v = target[t], h0 = (int)(at - t * parts) * kDotCols;
-  float dot = 0.0f;
-  if (v >= 0 && v < V) {
-    x += t * ldx;
-    w += v * swv;
-    float a[kDotCols / 32], b[kDotCols / 32];
-#pragma unroll
-    for (int i = 0; i < kDotCols / 32; ++i) {
-      const int h = h0 + i * 32 + lane;
-      a[i] = h < H ? __bfloat162float(x[h]) : 0.0f;
-      b[i] = h < H ? __bfloat162float(w[h * swh]) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < kDotCols / 32; ++i) dot = fmaf(a[i], b[i], dot);
-    dot = warp_sum(dot);
-  }
-  if (lane == 0) dots[at] = dot;
+  const float dot = v >= 0 && v < V ? dot_part(x + t * ldx, w + v * swv, swh, h0, H) : 0.0f;
+  if ((threadIdx.x & 31) == 0) dots[at] = dot;
 }
 
 // lse and loss of a row from its sum s 2^m of powers of two, with the target's logit `at` in fp32 in place of the product's
@@ -311,6 +309,37 @@ __device__ __forceinline__ float row_grad(const XentRows& r, int64_t t) {
   const int v = r.target[t];
   if (v < 0 || v >= r.V) return 0.0f;
   return r.dloss ? r.dloss[t] : 1.0f / r.total[1];
+}
+
+// bf16: the targets' gradients (without the mean's factor) from the logits that the forward's lse has in it, in every bit:
+// k_xent_dots' parts in k_xent_loss' order. With the products' own logits the errors of the two do not cancel, and p - 1
+// of a target with p = 1 - 1e-4 was off by a quarter. A block a row.
+__global__ void __launch_bounds__(256) k_xent_own(const __nv_bfloat16* x, const __nv_bfloat16* w, int64_t ldx, int64_t swh,
+                                                  int64_t swv, XentRows r, int H, int parts, float* own) {
+  pdl_wait();  // the previous kernel has completed and its writes are visible
+  __shared__ float part[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x;
+  const int v = r.target[t];
+  if (v < 0 || v >= r.V) return;  // nobody reads it
+  x += t * ldx;
+  w += v * swv;
+  float at = 0.0f;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    for (int p = p0 + warp; p < min(parts, p0 + 32); p += 8) {
+      const float dot = dot_part(x, w, swh, p * kDotCols, H);
+      if (lane == 0) part[p - p0] = dot;
+    }
+    __syncthreads();
+    if (warp == 0 && p0 + lane < parts) at += part[lane];
+    __syncthreads();
+  }
+  if (warp) return;
+  at = warp_sum(at);
+  if (lane == 0) {
+    const float d = r.dloss ? r.dloss[t] : 1.0f, lse = r.lse[t], u = at - lse;
+    own[t] = d == 0.0f ? 0.0f : d * (expm1f(u) + 2.0f * r.z * lse * expf(u));  // f e^u - d
+  }
 }
 
 // dl of a piece in place of its logits (fp32), a block 1024 columns of a row; zeros up to a multiple of four.
@@ -628,6 +657,13 @@ cudaError_t launch_xent_bwd(const moe_xent_dims& d, void* ws, const void* x, con
   epi.dloss = dloss;
   epi.z = d.z_coef;
   epi.V = (int)d.V;
+  if (bf) {
+    float* own = reinterpret_cast<float*>(c.ws + c.L.at);
+    epi.own = own;
+    *launches += 1;
+    MOE_LAUNCH(k_xent_own, (unsigned)d.M, 256, 0, st, (const __nv_bfloat16*)c.x, (const __nv_bfloat16*)c.w, c.ldx,
+               d.tied ? 1 : c.ldw, d.tied ? c.ldw : 1, r, (int)d.H, (int)((d.H + kDotCols - 1) / kDotCols), own);
+  }
   for (int64_t v0 = 0; v0 < d.V; v0 += c.P) {
     const int cols = (int)std::min(c.P, d.V - v0);
     *launches += 1;

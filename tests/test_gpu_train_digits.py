@@ -50,6 +50,68 @@ def test_adamw_small_decay(lr, wd, bits, master):
 
 
 # ---------------------------------------------------------------- cross entropy
+def likely_case(M, V, tied, z, seed):
+    """Rows whose one target has a probability of 1 - 1e-2 to 1 - 1e-5: products of one sign make its logit, and the
+    other logits are of about one."""
+    H = 2048
+    r = C.rand(seed)
+    x = r(M, H).abs()
+    w = r(V, H, scale=0.9 * H ** -0.5)
+    t = V // 2 + 3
+    w[t] = r(H).abs()
+    x, w = x.bfloat16(), w.bfloat16()
+    rest = torch.logsumexp((x.double() @ w.double().t())[:, torch.arange(V) != t], 1)
+    want = rest + torch.linspace(4.6, 11.5, M, dtype=torch.float64).cuda()
+    # the other features keep their sums: only the target's row of w is scaled, the rows' x by what is left
+    w[t] = (w[t].double() * float((want / (x.double() @ w[t].double())).mean())).bfloat16()
+    x = (x.double() * (want / (x.double() @ w[t].double()))[:, None]).bfloat16()
+    return dict(M=M, H=H, V=V, dtype="bf16", tied=tied, z=z, x=x, w=w if tied else w.t().contiguous(),
+                target=torch.full((M,), t, dtype=torch.int32, device="cuda"), dloss=0.5 + r(M).abs())
+
+
+@pytest.mark.parametrize("M,V", [(12, 1000), (300, 1000), (300, 999), (700, 9000)])
+@pytest.mark.parametrize("tied,z", [(False, 0.0), (True, 0.0), (False, 1e-4)])
+def test_xent_gradient_of_likely_targets(M, V, tied, z):
+    """dl of a target is the small difference of its probability and one: p - 1 = -(the others' share), in which the
+    target's own logit has to be the one that lse was made of."""
+    c = likely_case(M, V, tied, z, seed=M + V)
+    loss, lse, _ = C.run_xent_fwd(c)
+    x, w, t, l, le, LOSS, LSE, _, _ = C.xent_bounds(c)
+    rows = np.arange(M)
+    d = f64(c["dloss"])
+    DX, DW, DL = C.O.xent_bwd(x, w, t, z, d)
+    p = np.exp(l - LSE[:, None])
+    others = p.copy()
+    others[rows, t] = 0.0
+    # The others' share: their logits' errors and exponentials; the sum that they join holds the target's 1 as well, whose
+    # exponential is off by 2^-22 (4 units) and which up to 16 terms of a chunk, then chunks, lanes and slots are added to
+    # (28). The target's logit is an fp32 sum of products of one sign, 8 a lane and then trees (32 steps).
+    e_other = le + (256 + 8 * np.abs(l - LSE[:, None])) * E32
+    e_at = 32 * E32 * np.abs(l[rows, t])
+    share = (others * e_other).sum(1) + others.sum(1) * e_at + 48 * E32 * p[rows, t]
+    close = C.close
+    close(loss, LOSS, share / p[rows, t] + 2 * abs(z) * LSE * (e_at + share) + 16 * E32 * (LOSS + abs(z) * LSE ** 2), "loss")
+    half = np.spacing(LSE.astype(np.float32)) / 2.0  # lse is handed on as a float
+    f = 1 + 2 * z * np.abs(LSE)
+    err = d[:, None] * f[:, None] * p * (e_other + half[:, None] + (e_at + share)[:, None])
+    own = share + half + 8 * E32 * others.sum(1)  # of p - 1
+    err[rows, t] = d * (own + 2 * abs(z) * (LSE * own + (e_at + share + half) + 16 * E32 * LSE))
+    err = err + U["bf16"] * (np.abs(DL) + err) + d[:, None] * f[:, None] * 2.0 ** -126
+    a = np.abs(DL) + err
+    for mean in (False, True):
+        if mean:  # the same with one factor for all rows
+            c["dloss"] = None
+            total = torch.tensor([0.0, 2.0], device="cuda")
+            DX, DW, DL2 = C.O.xent_bwd(x, w, t, z, np.full(M, 0.5))
+            scale = (0.5 / d)[:, None]
+            err, a = err * scale, a * scale
+        gx, gw = C.run_xent_bwd(c, lse, c["dloss"], total if mean else None)
+        u = U["bf16"]
+        close(gx, DX, u * np.abs(DX) + (V + 64) * 2 * E32 * (a @ np.abs(w).T) + err @ np.abs(w).T + 1e-37, "dx")
+        got = gw.t() if tied else gw
+        close(got, DW, u * np.abs(DW) + (M + 64) * 2 * E32 * (np.abs(x).T @ a) + np.abs(x).T @ err + 1e-37, "dw")
+
+
 @pytest.mark.parametrize("M", [20, 300])
 @pytest.mark.parametrize("size", [1e3, 1e5, 1e7, 1e9])
 def test_xent_large_logits_of_one_sign(M, size):
