@@ -131,3 +131,90 @@ def test_xent_large_logits_of_one_sign(M, size):
         if size <= 1e7:  # where a float still has the logits' units
             for t in C.run_xent_bwd(c, out[1], c["dloss"]):
                 assert torch.isfinite(t).all()
+
+
+# ---------------------------------------------------------------- far elements and odd rows
+@pytest.mark.parametrize("tied", [False, True])
+def test_xent_weight_past_2_31_elements_by_its_values(tied):
+    """Few features are not zero, so sums are short and their bounds tight, and the columns that make the softmax lie past
+    element 2^31 of w in either layout: whatever else is read changes every output by far more than its bound."""
+    M, H, V = 3, 17000, 131072
+    g = torch.Generator().manual_seed(5)
+    x, w = torch.zeros(M, H, device="cuda"), torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+    w.normal_(0.0, 0.05, generator=torch.Generator(device="cuda").manual_seed(6))
+    cols = torch.randint(126400, V, (M, 6), generator=g)  # 126400 * 17000 > 2^31
+    cols[0, 0] = V - 1
+    at = []
+    for t in range(M):  # half of a row's features below row 16384 of [H, V], which begins at element 2^31, half behind
+        h = torch.cat([torch.randperm(16384, generator=g)[:32], 16384 + torch.randperm(H - 16384, generator=g)[:32]])
+        h[0], h[32] = (0, H - 1) if t == 0 else (h[0], h[32])
+        x[t, h.cuda()] = torch.sign(torch.randn(64, generator=g)).cuda()
+        at.append(h)
+    x = x.bfloat16()
+    for t in range(M):  # logits of 12 to 14.5, from either half alike
+        for j, v in enumerate(cols[t].tolist()):
+            w[v, at[t].cuda()] = (x[t, at[t].cuda()].float() * (12 + 0.5 * j) / 64).bfloat16()
+    target = cols[:, 2].int().cuda()
+    target[1] = 7  # one that the softmax does not expect
+    if not tied:
+        w = w.t().contiguous()
+    d = _lib.make_xent_dims(M, H, V, "bf16", tied)
+    ws = _lib.alloc_xent_workspace(d)
+    loss, lse, total = C.nan(M), C.nan(M), C.nan(2)
+    _lib.moe_xent_fwd(d, ws, x, w, target, loss, lse, total)
+    dx, dw = torch.full_like(x, float("nan")), torch.full_like(w, float("nan"))
+    _lib.moe_xent_bwd(d, ws, x, w, target, lse, None, total, dx, dw)
+    assert _lib.moe_read_status(ws) == _lib.MOE_OK
+    l, xa = torch.empty(M, V, dtype=torch.float64, device="cuda"), 0.0
+    xd = x.double()
+    part = lambda i: (w[i:i + 8192].double().t() if tied else w[:, i:i + 8192].double())
+    for i in range(0, V, 8192):
+        l[:, i:i + 8192] = xd @ part(i)
+        xa = max(xa, float((xd.abs() @ part(i).abs()).max()))
+    want = torch.logsumexp(l, 1)
+    le = 96 * 2 * E32 * xa  # 64 products that are not zero
+    e = le + (V / 32 + 512) * E32
+    assert e < 2e-3 and float((lse.double() - want).abs().max()) < e
+    t64 = target.long()
+    assert float((loss.double() - want + l.gather(1, t64[:, None])[:, 0]).abs().max()) < e + le
+    dl = torch.exp(l - want[:, None])
+    dl[torch.arange(M, device="cuda"), t64] -= 1
+    dl /= M
+    err = (2.0 ** -8 + 2 * e) * (dl.abs() + torch.exp(l - want[:, None]) * 2 * e / M) + 2 * e * torch.exp(l - want[:, None]) / M
+    DX, mag, slack = (torch.zeros(M, H, dtype=torch.float64, device="cuda") for _ in range(3))
+    for i in range(0, V, 8192):
+        wi = part(i).t()
+        DX += dl[:, i:i + 8192] @ wi
+        mag += dl[:, i:i + 8192].abs() @ wi.abs()
+        slack += err[:, i:i + 8192] @ wi.abs()
+        # dw of these columns: rows of features that no x has are zero
+        ref, tol = xd.t() @ dl[:, i:i + 8192], xd.abs().t() @ err[:, i:i + 8192]
+        got = dw[i:i + 8192].double().t() if tied else dw[:, i:i + 8192].double()
+        assert float(((got - ref).abs() - 2.0 ** -8 * ref.abs() - 1.01 * tol).max()) < 1e-30
+    tol = 2.0 ** -8 * DX.abs() + slack + (V + 64) * 2 * E32 * mag
+    assert float(((dx.double() - DX).abs() - tol).max()) < 0
+    assert float(DX.abs().max()) > 10 * float(tol.max())
+
+
+@pytest.mark.parametrize("tied", [False, True])
+def test_xent_bf16_odd_rows_in_a_graph(tied):
+    """Copies of odd rows of x and w, forward and backward, within a graph whose workspace is overwritten before its
+    replay."""
+    c = C.xent_case(70, 33, 2051, "bf16", tied, z=1e-3, seed=2)
+    d, ws = dws = C.xent_setup(c)
+    fwd = C.run_xent_fwd(c, dws)
+    ref = fwd + C.run_xent_bwd(c, fwd[1], c["dloss"], dws=dws)
+    C.check_xent_bwd(c, f64(c["dloss"]), ref[3:])
+    outs = [torch.empty_like(t) for t in ref]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _lib.moe_xent_fwd(d, ws, c["x"], c["w"], c["target"], *outs[:3])
+        _lib.moe_xent_bwd(d, ws, c["x"], c["w"], c["target"], outs[1], c["dloss"], None, *outs[3:])
+    for _ in range(2):
+        ws[256:].fill_(0xFF)
+        for t in outs:
+            t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(ref, outs):
+            assert torch.equal(a, b)
