@@ -40,7 +40,7 @@ class AdamW:
         self.norm = zeros(1, torch.float32)
         self.ws = _lib.alloc_grad_norm_workspace(self.tensors, dev) if max_norm > 0 else None
         self.steps = 0
-        self.lr = torch.full((1,), lr, device=dev) if capturable else None
+        self.lr = torch.full((1,), lr, dtype=torch.float32, device=dev) if capturable else None
         self.t = zeros(1, torch.int32) if capturable else None
 
     def step(self, lr: float | None = None) -> None:

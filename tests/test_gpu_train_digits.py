@@ -218,3 +218,18 @@ def test_xent_bf16_odd_rows_in_a_graph(tied):
         torch.cuda.synchronize()
         for a, b in zip(ref, outs):
             assert torch.equal(a, b)
+
+
+def test_optimiser_with_another_default_type():
+    """lr on the device is fp32 whatever torch's default type is."""
+    from expert_grouped_gemm_gb300.optim import AdamW
+
+    old = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float64)
+    try:
+        p, g = (torch.ones(100, dtype=torch.float32, device="cuda") for _ in range(2))
+        opt = AdamW([p], [g], 0.5, weight_decay=0.0, max_norm=100.0, capturable=True)
+        opt.step()
+    finally:
+        torch.set_default_dtype(old)
+    assert torch.equal(p, torch.full_like(p, 0.5)) or float((p - 0.5).abs().max()) < 1e-6
