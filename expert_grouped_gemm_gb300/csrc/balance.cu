@@ -11,9 +11,13 @@
 // sequence's rows in order, so results do not depend on timing. Few tokens of one or two sequences are one block's and
 // need neither rows nor a second kernel.
 //
-// Exponentials and reciprocals are the hardware's (2^-22 and 2^-23 of the value). Bound by what a warp does for a
-// token and by latency, not by HBM: 16384 x 256 in 37 sequences 13.1 us (17 MB are 2.6), 64 x 128 4.1, backward of
-// 8192 x 128 3.8.
+// Exponentials and reciprocals are the hardware's, for fp32 logits too (with expf and divisions 16384 x 256 in 37 sequences
+// 16.2 us for 13.2, backward of 8192 x 128 4.0 for 3.8). A score is off by 2^-22 of itself and, since the exponent's argument is
+// rounded, by 2^-23 for each unit that its logit is below the row's largest: 1e-6 of itself at 8, and where it is off by
+// more it is small beside the others. One below 2^-126 is zero.
+//
+// Bound by what a warp does for a token and by latency, not by HBM: 16384 x 256 in 37 sequences 13 us (17 MB are 2.6),
+// 64 x 128 4.2, backward of 8192 x 128 3.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -437,8 +441,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_balance_bwd(const BalanceArgs a
 // ---------------------------------------------------------------- host side
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // One block takes what its warps get through in four tokens each, of at most two sequences, which it walks one after the
-// other (64 tokens of 128 experts 4.3 us, 6.1 in two sequences, 30 in 16; in two kernels 6.0, 6.4 and 6.5). More go in
-// chunks of 8-warp blocks, four an SM (16384 x 256 in 37 sequences 13.2 us; one block of 32 warps an SM 16.9), of two
+// other (64 tokens of 128 experts 4.2 us, 6.1 in two sequences, 30 in 16; in two kernels 6.0, 6.4 and 6.5). More go in
+// chunks of 8-warp blocks, four an SM (16384 x 256 in 37 sequences 13 us; one block of 32 warps an SM 17), of two
 // tokens a warp, or as many as a sequence has.
 constexpr int kChunkBlocks = 608;
 constexpr int kChunkWarps = 8;
@@ -552,7 +556,7 @@ cudaError_t launch_balance_fwd(const moe_balance_dims& d, void* ws, const void* 
   });
   if (e != cudaSuccess || a.one) return e;
   // few sequences have many rows each: 128 of them at a time, eight columns a block (8192 x 128 in one sequence 9.0 us
-  // with the first kernel; as below 13.0). Many have few (16384 x 256 in 37 sequences 13.4; as above 22.8)
+  // with the first kernel; as below 13). Many have few (16384 x 256 in 37 sequences 13; as above 23)
   if (a.chunks >= 64 * a.S) MOE_LAUNCH((k_balance_sum<32, 8>), dim3((unsigned)a.S, (unsigned)((a.E + 7) / 8)), 1024, 0, st, a);
   else MOE_LAUNCH((k_balance_sum<8, 32>), dim3((unsigned)a.S, (unsigned)((a.E + 31) / 32)), 256, 0, st, a);
   return cudaSuccess;

@@ -219,7 +219,9 @@ constexpr uint32_t kRootMin = 0x0d800000u;  // 2^-100
 // The step of four values of a block; with 8 bits m and v hold codes' values, sm and sv what they are multiples of, and
 // v receives r = sqrt(v). Roundings are those of m = c1 g + (b1 m), v = c2 (g g) + (b2 v) with fused last steps, whatever
 // the compiler would join otherwise: in 8 bits a last bit can decide between two codes. For the same reason r is the
-// rounded root: an approximate one and one correction by the residual v - r^2 (Markstein).
+// rounded root: an approximate one and one correction by the residual v - r^2 (P. Markstein, IBM J. Res. Develop. 34, 1990).
+// That it is the rounded one rests on how far the approximation is off: compared with __fsqrt_rn, all mantissas of every
+// pair of exponents from 2^-100 to 2^126 are equal.
 template <int BITS>
 __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, const float (&g)[4], float (&p)[4],
                                         float (&m)[4], float (&v)[4]) {
@@ -274,8 +276,10 @@ __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, co
   }
 }
 
-// m and r of a block as codes over new scales. x / scale is the rounded quotient: with the rounded reciprocal, one
-// correction of the product by its residual gives it (Markstein).
+// m and r of a block as codes over new scales. x / scale is the rounded quotient, or nearly always: with the rounded
+// reciprocal, one correction of the product by its residual (the same paper). Of 6e10 quotients of x from 2^-101 on, all
+// mantissas over 4096 scales among them, none differs from the division; below, the residual passes the smallest float and
+// one in 2e6 is off by its last bit.
 __device__ __forceinline__ void codes4(const float (&x)[4], float scale, float inv, bool root, uint32_t& code) {
   float q[4];
 #pragma unroll

@@ -386,7 +386,8 @@ MOE_API int moe_balance_workspace_size(const moe_balance_dims* dims, size_t* byt
  *          seq_start[S+1] int32 (null iff S == 0; ascending offsets in [0, T]; others set
  *          MOE_ERR_DEVICE_ARG in the status word and leave the results unspecified).
  * Outputs: loss[2] float, count[max(S,1),E] int32, prob[max(S,1),E] float (nullable).
- * Sums run in a fixed order.
+ * Sums run in a fixed order. p is off by 2^-22 of itself and by 2^-23 for each unit of its exponential's
+ * argument (softmax: how far its logit is below the token's largest); an exponential below 2^-126 is zero.
  */
 MOE_API int moe_balance_fwd(const moe_balance_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* logits,
                             const int32_t* topk_idx, const int32_t* seq_start, float* loss, int32_t* count, float* prob);
@@ -500,7 +501,8 @@ MOE_API int moe_xent_workspace_size(const moe_xent_dims* dims, int backward, siz
  * status word and is not counted either.
  * Inputs:  x[M,H], w (dims.tied), target[M] int32.
  * Outputs: loss[M], lse[M] float; total[2] float (nullable): the sum of the losses and how many rows
- *          were counted. Logits are fp32 sums; all sums run in a fixed order.
+ *          were counted. Logits are fp32 sums; all sums run in a fixed order. A row with a logit of +inf or
+ *          NaN has an lse and a loss of NaN.
  */
 MOE_API int moe_xent_fwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, void* stream, const void* x, const void* w,
                          const int32_t* target, float* loss, float* lse, float* total);
@@ -511,7 +513,8 @@ MOE_API int moe_xent_fwd(const moe_xent_dims* dims, void* ws, size_t ws_bytes, v
  *   dl = d_t ((1 + 2 z_coef lse_t) e^{l - lse_t} - onehot(target_t));  dx = dl w^T;  dw = x^T dl.
  * The logits are computed again, a piece of the vocabulary at a time. In bf16 dl is rounded to bf16
  * for the two products (without the mean's 1 / total[1], which divides their sums), and e^{l - lse} below
- * 2^-126 is zero; dx is summed over the pieces in fp32.
+ * 2^-126 is zero; dx is summed over the pieces in fp32. The target's own logit is the one of the forward's
+ * loss, in every bit, so its p - 1 is off by no more than the others' share and lse's rounding are.
  * Inputs:  x, w, target as in the forward, lse[M] of the forward, dloss[M] float or total[2] of the
  *          forward. Outputs: dx[M,H], dw (dims.tied), each nullable; overwritten.
  */
@@ -555,7 +558,7 @@ MOE_API int moe_grad_norm_workspace_size(const moe_adamw_tensor* tensors, int64_
 
 /*
  * moe_grad_norm -- norm[0] = |grad_scale| sqrt(sum over all tensors of grad^2), in a fixed order. Squares
- * are taken in fp32: a gradient past 1.8e19 gives inf. Reads grad, n and grad_dtype of each tensor
+ * are taken in fp32: a gradient past 1.8e19 gives inf, one below 2^-75 adds nothing. Reads grad, n and grad_dtype of each tensor
  * (host array, copied by the call).
  */
 MOE_API int moe_grad_norm(const moe_adamw_tensor* tensors, int64_t count, void* ws, size_t ws_bytes, void* stream,
@@ -567,7 +570,8 @@ MOE_API int moe_grad_norm(const moe_adamw_tensor* tensors, int64_t count, void* 
  *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2;
  *   w = w - lr lr_scale (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay w).
  * With state_bits == 8, m and sqrt(v) are rounded to e4m3 (to nearest, ties to even) after the weights have
- * used them, over the largest magnitude / 448 (at least 2^-126) of each 256 values; a sqrt(v) above zero is stored as at least 2^-9 of its scale.
+ * used them, over the largest magnitude / 448 (at least 2^-126) of each 256 values; a sqrt(v) above zero is stored as at
+ * least 2^-9 of its scale. The decay is added to the change, not to the weight's factor: it loses no digits where it is small.
  * norm (nullable, device): where it is inf or NaN nothing is written: no weight, no state.
  * lr, step (nullable, device, one value each): in place of dims.lr and dims.step, so that a captured
  * step follows a schedule.

@@ -220,6 +220,29 @@ def test_xent_bf16_odd_rows_in_a_graph(tied):
             assert torch.equal(a, b)
 
 
+# ---------------------------------------------------------------- 8-bit codes
+@pytest.mark.parametrize("first", [2.0 ** -12, 1.0, 2.0 ** 20])
+def test_adamw8_codes_of_rounded_roots_and_quotients(first):
+    """With both betas zero m is the gradient and v its rounded square: the codes are those of the rounded root and of the
+    rounded quotients by the stored scales, for every mantissa, bit for bit."""
+    n = 1 << 24
+    g = (np.arange(n, dtype=np.uint32) & 0x7FFFFF | (np.arange(n, dtype=np.uint32) >> 23) + 127 << 23).view(np.float32)
+    g = g[np.random.default_rng(3).permutation(n)]
+    g *= np.float32(first) * np.exp2(np.random.default_rng(4).integers(-9, 1, n)).astype(np.float32)  # within e4m3's span
+    g[::2] *= -1
+    zeros = lambda k, dt=torch.float32: torch.zeros(k, dtype=dt, device="cuda")
+    f8 = lambda: zeros(n, torch.uint8).view(torch.float8_e4m3fn)
+    p, m, v, ms, vs = zeros(n), f8(), f8(), zeros(n // 256), zeros(n // 256)
+    t = _lib.make_adamw_tensors([p], [torch.from_numpy(g).cuda()], [m], [v], None, [ms], [vs])
+    _lib.moe_adamw_step(_lib.make_adamw_dims(0.1, 0.0, 0.0, 1e-8, 1, 8), t)
+    for name, code, scale, x in (("m", m, ms, g), ("r", v, vs, np.sqrt(g * g))):
+        q = (x.reshape(-1, 256) / scale.cpu().numpy()[:, None]).astype(np.float64)  # fp32 quotients
+        want = C.O.round_e4m3(q)
+        if name == "r":
+            want = np.maximum(want, 2.0 ** -9)
+        assert np.array_equal(f64(code).reshape(-1, 256), want), name
+
+
 def test_optimiser_with_another_default_type():
     """lr on the device is fp32 whatever torch's default type is."""
     from expert_grouped_gemm_gb300.optim import AdamW
