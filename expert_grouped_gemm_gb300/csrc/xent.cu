@@ -189,6 +189,12 @@ __global__ void __launch_bounds__(256) k_xent_dots(const __nv_bfloat16* x, const
   if ((threadIdx.x & 31) == 0) dots[at] = dot;
 }
 
+// log(s 2^m) + more
+__device__ __forceinline__ float lse_of(float m, float s, float more) {
+  constexpr float kLn2 = 0.6931471805599453f;
+  return fmaf(m, kLn2, fmaf(log2f(s), kLn2, more));
+}
+
 // lse and loss of a row from its sum s 2^m of powers of two, with the target's logit `at` in fp32 in place of the product's
 // own, `had`, in that sum:  loss = log(1 + e^y), y = log(e^L - 1) + had - at,  L = log(s 2^m) - had. The difference to had
 // is taken before the logarithm's rounding, so that a likely target's small loss keeps its digits; no exponential here can
@@ -197,13 +203,14 @@ __global__ void __launch_bounds__(256) k_xent_dots(const __nv_bfloat16* x, const
 __device__ __forceinline__ void corrected(float m, float s, float had, float at, float* lse, float* loss) {
   constexpr float kLn2 = 0.6931471805599453f;
   float L = kLn2 * (log2f(s) + fmaf(-had, kLog2e, m));
-  if (L < 0.0f) L = 0.0f;                             // had is in the sum; NaN stays
-  const float others = logf(-expm1f(-L));             // log of the others' share
-  const float y = (L + others) + (had == at ? 0.0f : had - at);  // of two infinities as well
+  if (L < 0.0f) L = 0.0f;                         // had is in the sum; NaN stays
+  const float others = logf(-expm1f(-L));         // log of the others' share
+  const float off = had == at ? 0.0f : had - at;  // of two infinities as well
+  const float y = (L + others) + off;
   const float t = log1pf(expf(-fabsf(y)));
-  *loss = y > 0.0f ? y + t : t;
-  // the larger of the target's and the others' parts, and what the other adds
-  *lse = y > 0.0f ? ((m + log2f(s)) * kLn2 + others) + t : at + t;
+  // the larger of the target's and the others' parts, and what the other adds; the small terms first
+  *loss = y > 0.0f ? L + ((others + t) + off) : t;
+  *lse = y > 0.0f ? lse_of(m, s, others + t) : at + t;
 }
 
 // lse and loss of eight rows a block; with BASE2 the targets' logits are exchanged (corrected). The blocks' totals are
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kLossWarps * 32) k_xent_loss(const LossArgs a)
   if (warp < kLossRows && lane == 0) {
     float sum = 0.0f, n = 0.0f;
     if (t < a.M) {
-      float e = BASE2 ? (st.x + log2f(st.y)) * 0.6931471805599453f : st.x + logf(st.y);
+      float e = BASE2 ? lse_of(st.x, st.y, 0.0f) : st.x + logf(st.y);
       if (v >= a.V) set_status(a.status, MOE_ERR_DEVICE_ARG);
       if (v >= 0 && v < a.V) {
         sum = e - at;
