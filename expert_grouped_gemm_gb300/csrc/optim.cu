@@ -6,8 +6,8 @@
 // Bound by HBM: every value is read once and written once. The tensors' descriptions travel as kernel arguments, so
 // that a launch needs no table on the device and a captured one keeps its own. The values of all tensors are cut into
 // chunks that never cross a tensor. With 32 bits a block takes one chunk (604M values in 2.40 ms, 7.1 TB/s; resident
-// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (36 a value), resident blocks walk them
-// (1.06 ms, 5.8 TB/s; a block each 1.11). The norm of 604M bf16 values takes 175 us (7.0 TB/s).
+// blocks that walk 2.68); with 8 bits, where instructions count beside bytes (37 a value), resident blocks walk them
+// (1.08 ms, 5.6 TB/s; a block each 6% more). The norm of 604M bf16 values takes 175 us (7.0 TB/s).
 //
 // 8 bits: m and r = sqrt(v) are held as e4m3 (3 bits of mantissa, 17 powers of two) over a float for each 256 values,
 // their largest magnitude / 448. The root halves the span of exponents that v has. An r above zero never becomes zero:
@@ -212,6 +212,13 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 }
 __device__ __forceinline__ f2 both(float a) { return two(a, a); }
 
+// An infinite weight is an entry that a program has masked. It keeps its value: what decays is the largest float, since
+// inf against inf, or 0 inf, is NaN.
+__device__ __forceinline__ float finite(float a) {
+  asm("min.xorsign.abs.f32 %0, %0, %1;" : "+f"(a) : "f"(3.40282347e38f));
+  return a;
+}
+
 // The root's correction needs a residual that is a float: below 2^-100 its last bits pass the smallest one, 2^-149.
 // Smaller v, zero and what is not finite take the library's root.
 constexpr uint32_t kRootMin = 0x0d800000u;  // 2^-100
@@ -267,8 +274,8 @@ __device__ __forceinline__ void update4(const Factors& k, float sm, float sv, co
 #pragma unroll
     for (int i = 0; i < 2; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[i]) : "f"(den[i]));
     const f2 move = mul2(mul2(two(m[j], m[j + 1]), both(-k.move)), two(inv[0], inv[1]));
-    const f2 w = two(p[j], p[j + 1]);
-    apart(add2(w, fma2(both(-k.decay), w, move)), p[j], p[j + 1]);
+    const f2 w = two(finite(p[j]), finite(p[j + 1]));
+    apart(add2(two(p[j], p[j + 1]), fma2(both(-k.decay), w, move)), p[j], p[j + 1]);
     if constexpr (BITS == 8) {
       v[j] = r[j];
       v[j + 1] = r[j + 1];

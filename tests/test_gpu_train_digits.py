@@ -49,6 +49,30 @@ def test_adamw_small_decay(lr, wd, bits, master):
     assert abs(err.mean()) <= 0.5 * ulp.max() * 0.0053 + part.mean()
 
 
+@pytest.mark.parametrize("wd", [0.0, 0.1])
+@pytest.mark.parametrize("bits,param,master", [(32, "f32", False), (32, "bf16", True), (32, "bf16", False), (8, "f32", False),
+                                               (8, "bf16", True)])
+def test_adamw_infinite_weights_stay(wd, bits, param, master):
+    """Entries that a program has masked with an infinite weight keep it, with and without a decay, and the weights beside
+    them are those of a step without such entries."""
+    n = 1500
+    c, ref = (C.adamw_case([n], param, "f32", master, bits, seed=24, wd=wd) for _ in range(2))
+    at = torch.tensor([0, 1, 2, 3, 130, 257, 1023, n - 1], device="cuda")
+    value = torch.tensor([-1, 1, -1, -1, 1, -1, -1, 1], device="cuda") * float("inf")
+    for k in ("p", "master"):
+        if c[k][0] is not None:
+            c[k][0][at] = value.to(c[k][0].dtype)
+    C.run_adamw(c)
+    C.run_adamw(ref)
+    others = torch.ones(n, dtype=torch.bool, device="cuda")
+    others[at] = False
+    for k in ("p", "master"):
+        if c[k][0] is not None:
+            assert torch.equal(c[k][0][at].float(), value) and torch.equal(c[k][0][others], ref[k][0][others])
+    raw = lambda x: x.view(torch.uint8) if bits == 8 else x
+    assert torch.equal(raw(c["m"][0]), raw(ref["m"][0])) and torch.equal(raw(c["v"][0]), raw(ref["v"][0]))
+
+
 # ---------------------------------------------------------------- cross entropy
 def likely_case(M, V, tied, z, seed):
     """Rows whose one target has a probability of 1 - 1e-2 to 1 - 1e-5: products of one sign make its logit, and the
