@@ -6,8 +6,8 @@
 // bf16: the tensor-core products' epilogue turns a tile of logits into the rows' statistics (largest, sum of
 // exponentials), or into dl, before anything is stored; the forward is one product over the whole vocabulary, the
 // backward takes it a piece at a time: dl of the piece, then its two products. Bound by the products: 4096 x 2048 x 131072
-// 5.44 ms (8 M H V flops at 1.62 PFLOP/s); statistics 1.15 ms by themselves, dl of 32768 columns 0.3. A few rows are a
-// stream of w: 8 x 2048 x 65536 50 us, 44 of them at 6.1 TB/s. The target's logit is summed in fp32 on the CUDA cores:
+// 5.4 to 5.6 ms (8 M H V flops at 1.6 PFLOP/s); statistics 1.15 ms by themselves, dl of 32768 columns 0.3. A few rows are a
+// stream of w: 8 x 2048 x 65536 51 us, 44 of them at 6.1 TB/s. The target's logit is summed in fp32 on the CUDA cores:
 // tensor cores truncate as they add, and a target's products are mostly of one sign. fp32: the logits of a piece are
 // stored, then read.
 #include <algorithm>
