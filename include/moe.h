@@ -569,6 +569,8 @@ MOE_API int moe_grad_norm(const moe_adamw_tensor* tensors, int64_t count, void* 
  *   g' = grad grad_scale (max_norm > 0 and norm given: min(1, max_norm / *norm));
  *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2;
  *   w = w - lr lr_scale (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay w).
+ * beta1, beta2 and their complements enter m and v as floats (off by up to 2^-25), the bias corrections as doubles (floats
+ * where step is on the device). An infinite weight keeps its value.
  * With state_bits == 8, m and sqrt(v) are rounded to e4m3 (to nearest, ties to even) after the weights have
  * used them, over the largest magnitude / 448 (at least 2^-126) of each 256 values; a sqrt(v) above zero is stored as at
  * least 2^-9 of its scale. The decay is added to the change, not to the weight's factor: it loses no digits where it is small.
